@@ -303,6 +303,120 @@ qlin_status qlin_silu_and_mul_per_block_quant(int64_t M, int64_t K, const uint16
                                               int64_t ldx, void *Q, int64_t ldq, float *scale,
                                               void *stream);
 
+/* Products with 4-bit weights and group scales:
+ *   Y[m,n] = bf16( sum_g s[n,g] * sum_{k in group g} X[m,k] * (q[n,k] - z[n,g]) )
+ * with q in 0..15, groups of `group` (32, 64 or 128) consecutive k starting at
+ * k = 0, and z = 8 when b_zero is NULL.  The products are exact, the sums
+ * fp32, the result is rounded once to bf16.
+ *
+ * X [M][ldx] bf16 bits.  B [N][ldb] bytes, two codes per byte: byte j of a row
+ * holds k = 2j in its low and k = 2j + 1 in its high nibble.  b_scale
+ * [N][K/group] contiguous, of type `st`; b_zero [N][K/group] bytes, or NULL.
+ * Y [M][ldy] bf16 bits.
+ *
+ * Shapes: M >= 0, N >= 0 (0 is a no-op), 0 < K <= 2^20, K % group == 0.
+ * ldx >= K with ldx % 8 == 0 (elements), ldb >= K/2 with ldb % 16 == 0
+ * (bytes), ldy >= N; X, B and Y 16-byte aligned, b_scale 4-byte aligned.  An
+ * infinity or NaN in X reaches the outputs that the formula gives it and no
+ * other row.  The caller owns every buffer; the call is asynchronous on
+ * `stream`, allocates nothing and needs no workspace.  Errors as for
+ * qlin_scaled_mm (a group or scale type not listed: QLIN_ERR_BAD_ARGUMENT). */
+typedef enum qlin_scale_type {
+    QLIN_SCALE_F32 = 0,
+    QLIN_SCALE_BF16 = 1,
+    QLIN_SCALE_F16 = 2
+} qlin_scale_type;
+
+qlin_status qlin_w4_mm(int64_t M, int64_t N, int64_t K, int64_t group, const uint16_t *X,
+                       int64_t ldx, const uint8_t *B, int64_t ldb, qlin_scale_type st,
+                       const void *b_scale, const uint8_t *b_zero, uint16_t *Y, int64_t ldy,
+                       void *stream);
+
+/* The same for `groups` experts in one launch: expert g owns the rows
+ * group_offsets[g] .. group_offsets[g+1]-1 of X and Y and the weights
+ * B + g * b_group_stride bytes with b_scale (and b_zero) [groups][N][K/group]
+ * contiguous.  group_offsets: groups + 1 nondecreasing int32 values in DEVICE
+ * memory, read on the GPU and held to 0..rows there (a table that is not
+ * nondecreasing leaves rows uncomputed but stays inside the buffers).  rows:
+ * the rows of X and Y.  max_rows: a bound on any expert's row count; rows of
+ * an expert beyond it are not computed.  Rows outside every expert keep what Y
+ * holds.  groups <= 65535 (0 is a no-op); b_group_stride >= 0 and % 16 == 0. */
+qlin_status qlin_grouped_w4_mm(int64_t groups, const int32_t *group_offsets, int64_t max_rows,
+                               int64_t rows, int64_t N, int64_t K, int64_t group,
+                               const uint16_t *X, int64_t ldx, const uint8_t *B, int64_t ldb,
+                               int64_t b_group_stride, qlin_scale_type st, const void *b_scale,
+                               const uint8_t *b_zero, uint16_t *Y, int64_t ldy, void *stream);
+
+/* Routing of tokens to experts, around the grouped products: tokens sorted by
+ * expert (moe_sort), their rows copied in that order (moe_permute; both in
+ * one call: moe_dispatch), the experts' rows brought back with the router's
+ * weights (moe_combine), and the gradients of both directions.
+ *
+ * A slot is one (token, choice) pair, index i = token * topk + choice.  Its
+ * expert is topk_ids[i] (int32, or int64 with id_bits = 64); a slot whose id
+ * is outside 0..experts-1 (padding, an expert held elsewhere) is absent.
+ *   group_offsets [experts+1]: group_offsets[e] = slots with an expert < e.
+ *   slot_row [tokens*topk]: the slot's row in the order by (expert, slot
+ *     index), or -1 when absent.  Rows group_offsets[experts] .. tokens*topk-1
+ *     belong to no slot.
+ * Every other call takes slot_row as it is; an entry outside 0..rows-1 counts
+ * as absent, where `rows` is the rows of the sorted buffers.  No two slots
+ * may name the same row.
+ *
+ *   moe_permute            out[slot_row[i]] = X[i / topk], and the same for
+ *                          the scales [tokens][scale_cols] (NULL: none)
+ *   moe_combine            out[t] = sum_j w[t,j] * Y[slot_row[t,j]]
+ *   moe_combine_backward   dY[slot_row[t,j]] = w[t,j] * dOut[t],
+ *                          dW[t,j] = sum_k dOut[t,k] * Y[slot_row[t,j],k]
+ *   moe_permute_backward   dX[t] = sum_j dOut[slot_row[t,j]]
+ * Absent slots are skipped (their weight is not read) and get dW = 0; a token
+ * with no present slot gets a zero row.  Rows that belong to no slot are
+ * neither read nor written.  Sums are fp32, over j in ascending order, and
+ * are rounded once; results do not depend on timing.  dY may not overlap Y,
+ * and no output may overlap an input.
+ *
+ * Shapes: tokens, rows >= 0 (0 tokens: nothing but the offsets is written),
+ * 1 <= topk <= 1024, tokens * topk < 2^30, 1 <= experts <= 2048, rows < 2^30,
+ * 0 < K <= 2^20 (moe_permute: 0 < row_bytes <= 2^22), row strides >= the row's
+ * length.  Every buffer is aligned to its element (moe_permute: any).
+ * topk_ids, slot_row, weights, dW and the scales are contiguous.  Row strides of X, Y and
+ * the outputs are in elements (moe_permute, moe_dispatch: bytes).  moe_dispatch needs rows >= tokens * topk.  The
+ * workspace of moe_sort and moe_dispatch (qlin_moe_sort_workspace_size bytes,
+ * 4-byte aligned, any contents; 0 for few slots) must not be used by two calls
+ * that may overlap in time.  The calls are asynchronous on `stream` and
+ * allocate nothing.  Errors as for qlin_scaled_mm. */
+typedef enum qlin_row_type {
+    QLIN_ROW_F32 = 0,
+    QLIN_ROW_BF16 = 1,
+    QLIN_ROW_F16 = 2
+} qlin_row_type;
+
+size_t qlin_moe_sort_workspace_size(int64_t tokens, int64_t topk, int64_t experts);
+qlin_status qlin_moe_sort(int32_t id_bits, int64_t tokens, int64_t topk, int64_t experts,
+                          const void *topk_ids, int32_t *group_offsets, int32_t *slot_row,
+                          void *workspace, size_t workspace_bytes, void *stream);
+qlin_status qlin_moe_permute(int64_t tokens, int64_t topk, int64_t rows, int64_t row_bytes,
+                             const void *X, int64_t ldx, const int32_t *slot_row, void *Out,
+                             int64_t ldo, const float *scale, int64_t scale_cols,
+                             float *out_scale, void *stream);
+qlin_status qlin_moe_dispatch(int32_t id_bits, int64_t tokens, int64_t topk, int64_t experts,
+                              const void *topk_ids, int64_t rows, int64_t row_bytes, const void *X,
+                              int64_t ldx, void *Out, int64_t ldo, const float *scale,
+                              int64_t scale_cols, float *out_scale, int32_t *group_offsets,
+                              int32_t *slot_row, void *workspace, size_t workspace_bytes,
+                              void *stream);
+qlin_status qlin_moe_combine(qlin_row_type rt, int64_t tokens, int64_t topk, int64_t rows,
+                             int64_t K, const void *Y, int64_t ldy, const int32_t *slot_row,
+                             const float *weights, void *Out, int64_t ldo, void *stream);
+qlin_status qlin_moe_combine_backward(qlin_row_type rt, int64_t tokens, int64_t topk, int64_t rows,
+                                      int64_t K, const void *dOut, int64_t ldo, const void *Y,
+                                      int64_t ldy, const int32_t *slot_row, const float *weights,
+                                      void *dY, int64_t lddy, float *dW, void *stream);
+qlin_status qlin_moe_permute_backward(qlin_row_type rt, int64_t tokens, int64_t topk, int64_t rows,
+                                      int64_t K, const void *dOut, int64_t ldo,
+                                      const int32_t *slot_row, void *dX, int64_t ldx,
+                                      void *stream);
+
 /* The config the table selects for a problem: the entry for (scaling, dt,
  * N, K) at the smallest tuned M >= M (else the largest tuned M); shapes not
  * in the table get the format's default for that M range. */

@@ -9,6 +9,7 @@ and the current stream.
 
     Y = scaled_mm(a_q, a_scale, b_q, b_scale)          # FP8_Dynamic / W8A8_INT8
     Y = block_scaled_mm(a_q, a_scale, b_q, b_scale)    # Block_FP8
+    Y = w4_mm(x, b_q, b_scale, b_zero)                 # 4-bit weights, bf16 activations
 
 ``a_q`` [M,K] and ``b_q`` [N,K] (torch.float8_e4m3fn or torch.int8, rows
 K-contiguous); fp32 scales ``a_scale`` [M] and ``b_scale`` [N], or for the
@@ -156,6 +157,26 @@ def _lib():
     lib.qlin_silu_and_mul_dynamic_per_token_quant.restype = I
     lib.qlin_silu_and_mul_per_block_quant.argtypes = [I64, I64, P, I64, P, I64, P, P]
     lib.qlin_silu_and_mul_per_block_quant.restype = I
+    lib.qlin_w4_mm.argtypes = [I64, I64, I64, I64, P, I64, P, I64, I, P, P, P, I64, P]
+    lib.qlin_w4_mm.restype = I
+    lib.qlin_grouped_w4_mm.argtypes = [I64, P, I64, I64, I64, I64, I64, P, I64, P, I64, I64, I, P, P, P,
+                                       I64, P]
+    lib.qlin_grouped_w4_mm.restype = I
+    lib.qlin_moe_sort_workspace_size.argtypes = [I64, I64, I64]
+    lib.qlin_moe_sort_workspace_size.restype = SZ
+    lib.qlin_moe_sort.argtypes = [ctypes.c_int32, I64, I64, I64, P, P, P, P, SZ, P]
+    lib.qlin_moe_sort.restype = I
+    lib.qlin_moe_permute.argtypes = [I64, I64, I64, I64, P, I64, P, P, I64, P, I64, P, P]
+    lib.qlin_moe_permute.restype = I
+    lib.qlin_moe_dispatch.argtypes = [ctypes.c_int32, I64, I64, I64, P, I64, I64, P, I64, P, I64, P, I64, P, P,
+                                      P, P, SZ, P]
+    lib.qlin_moe_dispatch.restype = I
+    lib.qlin_moe_combine.argtypes = [I, I64, I64, I64, I64, P, I64, P, P, P, I64, P]
+    lib.qlin_moe_combine.restype = I
+    lib.qlin_moe_combine_backward.argtypes = [I, I64, I64, I64, I64, P, I64, P, I64, P, P, P, I64, P, P]
+    lib.qlin_moe_combine_backward.restype = I
+    lib.qlin_moe_permute_backward.argtypes = [I, I64, I64, I64, I64, P, I64, P, P, I64, P]
+    lib.qlin_moe_permute_backward.restype = I
     _LIB = lib
     return lib
 
@@ -555,6 +576,271 @@ def grouped_block_scaled_mm(a_q, a_scale, b_q, b_scale, group_offsets, max_rows:
            a_scale.data_ptr(), b_q.data_ptr(), b_q.stride(1), b_q.stride(0), b_scale.data_ptr(),
            (N // 128) * (K // 128), out.data_ptr(), out.stride(0), stream.cuda_stream,
            ctypes.byref(c) if c else None], "qlin_grouped_block_scaled_mm")
+    return out
+
+
+# ---------------------------------------------------------------------------
+# 4-bit weights
+# ---------------------------------------------------------------------------
+_SCALE_TYPE = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+
+
+def _matrix(t: torch.Tensor, name: str, device=None) -> int:
+    """The row stride of a 2-D device tensor with contiguous rows (on `device`)."""
+    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
+        raise ValueError(f"{name} must be 2-D with contiguous rows")
+    if not t.is_cuda or (device is not None and t.device != device):
+        raise ValueError(f"{name} must be a device tensor, on one device with the others")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]      # a single row's stride says nothing
+
+
+def _flat(t: torch.Tensor, dtype, shape, name: str, device) -> torch.Tensor:
+    """A contiguous tensor of one type and shape on `device`."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous, on one device with the others")
+    return t
+
+
+def _rows_out(out, shape, dtype, device, name="out"):
+    """(`out` or a new tensor of shape and dtype, its row stride)."""
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=device), shape[1]
+    if out.dtype != dtype or tuple(out.shape) != tuple(shape):
+        raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)}")
+    return out, _matrix(out, name, device)
+
+
+def _call_on(device, fn, args, what):
+    """_call with `device`'s current stream as the last argument."""
+    if device.index == torch.cuda.current_device():
+        _call(fn, args + [torch.cuda.current_stream(device).cuda_stream], what)
+    else:
+        with torch.cuda.device(device):
+            _call(fn, args + [torch.cuda.current_stream(device).cuda_stream], what)
+
+
+def _w4_scales(b_scale, b_zero, lead, K, device):
+    """(group, scale type, zero points' address) of 4-bit weights [*lead, K]."""
+    if b_scale.dim() != len(lead) + 1 or b_scale.shape[-1] == 0 or K % b_scale.shape[-1] or \
+            K // b_scale.shape[-1] not in (32, 64, 128):
+        raise ValueError(f"b_scale must be [..., N, K/group] with a group of 32, 64 or 128, "
+                         f"got {tuple(b_scale.shape)} for K = {K}")
+    if b_scale.dtype not in _SCALE_TYPE:
+        raise TypeError(f"b_scale must be float32, bfloat16 or float16, got {b_scale.dtype}")
+    shape = (*lead, b_scale.shape[-1])
+    _flat(b_scale, b_scale.dtype, shape, "b_scale", device)
+    if b_zero is not None:
+        _flat(b_zero, torch.uint8, shape, "b_zero", device)
+    return K // b_scale.shape[-1], _SCALE_TYPE[b_scale.dtype], None if b_zero is None else b_zero.data_ptr()
+
+
+def w4_mm(x, b_q, b_scale, b_zero=None, out=None):
+    """Product with 4-bit weights: bf16 [M,N], y[m,n] = sum_g s[n,g] sum_{k in g}
+    x[m,k] (q[n,k] - z[n,g]).  x bf16 [M,K]; b_q uint8 [N, K/2], k even in the
+    low nibble; b_scale [N, K/group] float32, bfloat16 or float16, its width
+    giving the group (32, 64 or 128); b_zero uint8 of the same shape, 8
+    everywhere when None."""
+    if x.dtype != torch.bfloat16:
+        raise TypeError(f"x must be bfloat16, got {x.dtype}")
+    if b_q.dtype != torch.uint8:
+        raise TypeError(f"b_q must be uint8, got {b_q.dtype}")
+    dev = x.device
+    ldx, ldb = _matrix(x, "x"), _matrix(b_q, "b_q", dev)
+    M, K = x.shape
+    N = b_q.shape[0]
+    if b_q.shape[1] * 2 != K:
+        raise ValueError("x is [M,K] and b_q must be [N,K/2]")
+    group, st, zero = _w4_scales(b_scale, b_zero, (N,), K, dev)
+    out, ldy = _rows_out(out, (M, N), torch.bfloat16, dev)
+    _call_on(dev, _lib().qlin_w4_mm, [M, N, K, group, x.data_ptr(), ldx, b_q.data_ptr(), ldb, st,
+                                      b_scale.data_ptr(), zero, out.data_ptr(), ldy], "qlin_w4_mm")
+    return out
+
+
+def grouped_w4_mm(x, b_q, b_scale, group_offsets, max_rows: int, b_zero=None, out=None):
+    """w4_mm for each expert's rows: expert g computes rows group_offsets[g] ..
+    group_offsets[g+1]-1 of x bf16 [rows,K] against b_q[g] uint8 [N, K/2] with
+    b_scale[g] (and b_zero[g]) [N, K/group]; bf16 out [rows,N].  group_offsets
+    int32 [G+1] on the device; max_rows bounds any expert's row count."""
+    if x.dtype != torch.bfloat16:
+        raise TypeError(f"x must be bfloat16, got {x.dtype}")
+    if b_q.dtype != torch.uint8:
+        raise TypeError(f"b_q must be uint8, got {b_q.dtype}")
+    dev = x.device
+    ldx = _matrix(x, "x")
+    if b_q.dim() != 3 or b_q.stride(2) != 1 or b_q.device != dev:
+        raise ValueError("b_q must be a [G,N,K/2] tensor with contiguous rows, on x's device")
+    rows, K = x.shape
+    G, N = b_q.shape[:2]
+    if b_q.shape[2] * 2 != K:
+        raise ValueError("x is [rows,K] and b_q must be [G,N,K/2]")
+    group, st, zero = _w4_scales(b_scale, b_zero, (G, N), K, dev)
+    _flat(group_offsets, torch.int32, (G + 1,), "group_offsets", dev)
+    out, ldy = _rows_out(out, (rows, N), torch.bfloat16, dev)
+    _call_on(dev, _lib().qlin_grouped_w4_mm,
+             [G, group_offsets.data_ptr(), int(max_rows), rows, N, K, group, x.data_ptr(), ldx, b_q.data_ptr(),
+              b_q.stride(1), b_q.stride(0), st, b_scale.data_ptr(), zero, out.data_ptr(), ldy],
+             "qlin_grouped_w4_mm")
+    return out
+
+
+# ---------------------------------------------------------------------------
+# Routing of tokens to experts.  topk_ids [T, topk] holds each token's
+# experts; an id outside 0..experts-1 makes its slot absent.
+# ---------------------------------------------------------------------------
+_ROW_TYPE = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+
+
+def _ids(topk_ids, experts):
+    if topk_ids.dtype not in (torch.int32, torch.int64):
+        raise TypeError(f"topk_ids must be int32 or int64, got {topk_ids.dtype}")
+    if topk_ids.dim() != 2 or not topk_ids.is_cuda or not topk_ids.is_contiguous():
+        raise ValueError("topk_ids must be a contiguous [T, topk] device tensor")
+    T, topk = topk_ids.shape
+    return 8 * topk_ids.element_size(), T, topk, int(experts)
+
+
+def _slots(slot_row, device):
+    if slot_row.dim() != 2:
+        raise ValueError("slot_row must be [T, topk]")
+    _flat(slot_row, torch.int32, slot_row.shape, "slot_row", device)
+    return slot_row.shape
+
+
+def _sort_buffers(T, topk, experts, device):
+    """(offsets, slot_row, workspace and its bytes) of a sort: the workspace
+    is the call's own, given back to the allocator in stream order (or, under
+    capture, to the graph's pool)."""
+    # (a count the library refuses gets a token buffer: the call launches nothing)
+    offsets = torch.empty((experts + 1 if 1 <= experts <= 2048 else 1,), dtype=torch.int32, device=device)
+    slot_row = torch.empty((T, topk), dtype=torch.int32, device=device)
+    n = _lib().qlin_moe_sort_workspace_size(T, topk, experts)
+    return offsets, slot_row, torch.empty((n,), dtype=torch.uint8, device=device) if n else None, n
+
+
+def moe_sort(topk_ids, experts: int):
+    """Order of the slots by expert: (group_offsets int32 [experts+1], slot_row
+    int32 [T, topk]).  group_offsets are the grouped products'; slot_row is
+    each slot's row in the order by (expert, slot), -1 for an absent slot."""
+    bits, T, topk, experts = _ids(topk_ids, experts)
+    offsets, slot_row, ws, n = _sort_buffers(T, topk, experts, topk_ids.device)
+    _call_on(topk_ids.device, _lib().qlin_moe_sort,
+             [bits, T, topk, experts, topk_ids.data_ptr(), offsets.data_ptr(), slot_row.data_ptr(),
+              None if ws is None else ws.data_ptr(), n], "qlin_moe_sort")
+    return offsets, slot_row
+
+
+def _permute_args(x, T, scale, rows, out, out_scale):
+    """The sorted rows' buffers (out, out_scale) and the call's row arguments."""
+    dev = x.device
+    ldx = _matrix(x, "x")
+    if x.shape[0] != T:
+        raise ValueError(f"x has {x.shape[0]} rows for {T} tokens")
+    K, es = x.shape[1], x.element_size()
+    if out is not None:
+        rows = out.shape[0]
+    out, ldo = _rows_out(out, (rows, K), x.dtype, dev)
+    cols = 0
+    if scale is not None:
+        if scale.dim() not in (1, 2):
+            raise ValueError("scale must be [T] or [T, G]")
+        _flat(scale, torch.float32, (T, *scale.shape[1:]), "scale", dev)
+        cols = scale.shape[1] if scale.dim() == 2 else 1
+        shape = (rows, *scale.shape[1:])
+        if out_scale is None:
+            out_scale = torch.empty(shape, dtype=torch.float32, device=dev)
+        _flat(out_scale, torch.float32, shape, "out_scale", dev)
+    elif out_scale is not None:
+        raise ValueError("out_scale without scale")
+    return out, out_scale, rows, [K * es, x.data_ptr(), ldx * es], [out.data_ptr(), ldo * es], \
+        [None if scale is None else scale.data_ptr(), cols, None if scale is None else out_scale.data_ptr()]
+
+
+def moe_permute(x, slot_row, scale=None, out=None, out_scale=None):
+    """Rows of x [T,K] (any type) copied to each of their slots' rows: (rows
+    [T*topk, K], scales): out[slot_row[t,j]] = x[t].  `scale` (float32 [T] or
+    [T,G], a quantizer's) moves along; None otherwise.  Rows of no slot keep
+    what `out` holds.  A given `out` may have any number of rows; slots
+    beyond it are absent."""
+    T, topk = _slots(slot_row, x.device)
+    out, out_scale, rows, src, dst, sc = _permute_args(x, T, scale, T * topk, out, out_scale)
+    _call_on(x.device, _lib().qlin_moe_permute, [T, topk, rows, *src, slot_row.data_ptr(), *dst, *sc],
+             "qlin_moe_permute")
+    return out, out_scale
+
+
+def moe_dispatch(x, topk_ids, experts: int, scale=None, out=None, out_scale=None):
+    """moe_sort and moe_permute in one call: (rows, scales, group_offsets,
+    slot_row).  A given `out` needs at least T*topk rows."""
+    bits, T, topk, experts = _ids(topk_ids, experts)
+    if topk_ids.device != x.device:
+        raise ValueError("topk_ids must be on x's device")
+    out, out_scale, rows, src, dst, sc = _permute_args(x, T, scale, T * topk, out, out_scale)
+    offsets, slot_row, ws, n = _sort_buffers(T, topk, experts, x.device)
+    _call_on(x.device, _lib().qlin_moe_dispatch,
+             [bits, T, topk, experts, topk_ids.data_ptr(), rows, *src, *dst, *sc, offsets.data_ptr(),
+              slot_row.data_ptr(), None if ws is None else ws.data_ptr(), n], "qlin_moe_dispatch")
+    return out, out_scale, offsets, slot_row
+
+
+def _row_type(t, name):
+    if t.dtype not in _ROW_TYPE:
+        raise TypeError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
+    return _ROW_TYPE[t.dtype]
+
+
+def moe_combine(y, slot_row, weights, out=None):
+    """The experts' rows brought back: out[t] = sum_j weights[t,j] y[slot_row[t,j]],
+    [T,K] of y's type (float32, bfloat16 or float16), fp32 sums in the order of
+    j; weights float32 [T, topk].  Absent slots add nothing."""
+    rt = _row_type(y, "y")
+    ldy = _matrix(y, "y")
+    T, topk = _slots(slot_row, y.device)
+    _flat(weights, torch.float32, (T, topk), "weights", y.device)
+    rows, K = y.shape
+    out, ldo = _rows_out(out, (T, K), y.dtype, y.device)
+    _call_on(y.device, _lib().qlin_moe_combine,
+             [rt, T, topk, rows, K, y.data_ptr(), ldy, slot_row.data_ptr(), weights.data_ptr(), out.data_ptr(),
+              ldo], "qlin_moe_combine")
+    return out
+
+
+def moe_combine_backward(dout, y, slot_row, weights, dy=None):
+    """Gradients of moe_combine: (dy [rows,K], dweights float32 [T, topk]) from
+    dout [T,K] and the call's inputs.  dy's rows of no slot keep what it holds
+    (a new dy: anything); dweights is 0 for absent slots."""
+    rt = _row_type(y, "y")
+    if dout.dtype != y.dtype:
+        raise TypeError("dout and y must have the same dtype")
+    ldy, ldo = _matrix(y, "y"), _matrix(dout, "dout", y.device)
+    T, topk = _slots(slot_row, y.device)
+    _flat(weights, torch.float32, (T, topk), "weights", y.device)
+    rows, K = y.shape
+    if tuple(dout.shape) != (T, K):
+        raise ValueError(f"dout has shape {tuple(dout.shape)}, expected {(T, K)}")
+    dy, lddy = _rows_out(dy, (rows, K), y.dtype, y.device, "dy")
+    dweights = torch.empty((T, topk), dtype=torch.float32, device=y.device)
+    _call_on(y.device, _lib().qlin_moe_combine_backward,
+             [rt, T, topk, rows, K, dout.data_ptr(), ldo, y.data_ptr(), ldy, slot_row.data_ptr(),
+              weights.data_ptr(), dy.data_ptr(), lddy, dweights.data_ptr()], "qlin_moe_combine_backward")
+    return dy, dweights
+
+
+def moe_permute_backward(drows, slot_row, out=None):
+    """Gradient of moe_permute: dx[t] = sum_j drows[slot_row[t,j]], [T,K] of
+    drows' type, fp32 sums."""
+    rt = _row_type(drows, "drows")
+    ld = _matrix(drows, "drows")
+    T, topk = _slots(slot_row, drows.device)
+    rows, K = drows.shape
+    out, ldo = _rows_out(out, (T, K), drows.dtype, drows.device)
+    _call_on(drows.device, _lib().qlin_moe_permute_backward,
+             [rt, T, topk, rows, K, drows.data_ptr(), ld, slot_row.data_ptr(), out.data_ptr(), ldo],
+             "qlin_moe_permute_backward")
     return out
 
 

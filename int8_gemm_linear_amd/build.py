@@ -25,6 +25,8 @@ SOURCES = [
     "qlin_reduce.hip",
     "qlin_quant.hip",
     "qlin_fused.hip",
+    "qlin_w4.hip",
+    "qlin_moe.hip",
     "qlin_stream_fp8.hip",
     "qlin_stream_int8.hip",
     "qlin_stream_block.hip",

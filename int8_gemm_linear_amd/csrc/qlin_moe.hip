@@ -1,0 +1,640 @@
+// Routing of tokens to experts around the grouped products: the sort of
+// (token, choice) slots by expert, the copies of token rows in that order,
+// the weighted return, and the gradients of both directions.
+//
+// Slot i = token * topk + choice has the expert id topk_ids[i].  With
+// c[e] = #{i : id[i] = e},
+//   offsets[e] = sum_{e' < e} c[e'],
+//   row[i]     = offsets[id[i]] + #{i' < i : id[i'] = id[i]},
+// a stable counting sort, so rows do not depend on timing.  Everything else
+// is addressed by row[i]: permute scatters token rows to row[i], combine and
+// the gradients gather from it.  All of it moves bytes once; HBM bounds the
+// long calls and the launch the short ones.
+#include <hip/hip_fp16.h>
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "qlin_device.h"
+#include "qlin_dpp.h"
+#include "qlinear.h"
+
+namespace qlin {
+namespace {
+
+constexpr int64_t kMaxSlots = ((int64_t)1 << 30) - 1;
+constexpr int64_t kMaxTopk = 1024;
+constexpr int kMaxExperts = 2048;
+constexpr int64_t kMaxRowK = (int64_t)1 << 20;
+constexpr int64_t kMaxRowBytes = (int64_t)1 << 22;
+constexpr int64_t kMaxStride = (int64_t)1 << 31;
+
+bool aligned(const void *p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
+
+// ---------------------------------------------------------------------------
+// Sort
+// ---------------------------------------------------------------------------
+constexpr int kSortWaves = 8;                  // x 2048 experts of LDS counters: 64 KB
+constexpr int kSortThreads = 64 * kSortWaves;
+constexpr int64_t kSortOne = 4096;             // slots up to which one workgroup sorts alone
+constexpr int kSortMaxBlocks = 256;
+
+// The expert of slot i, or -1.
+template <typename ID>
+__device__ inline int expert_of(const ID *ids, int i, int experts)
+{
+    const ID id = ids[i];
+    return id >= 0 && id < (ID)experts ? (int)id : -1;
+}
+
+// Lanes of the wave that hold the same expert as this one (all 64 lanes call).
+__device__ inline uint64_t same_expert(int e, int bits)
+{
+    const uint64_t present = __ballot(e >= 0);
+    uint64_t m = e >= 0 ? present : ~present;
+    for (int b = 0; b < bits; ++b) {
+        const uint64_t set = __ballot((e >> b) & 1);
+        m &= (e >> b) & 1 ? set : ~set;
+    }
+    return m;
+}
+
+struct SortArgs {
+    const void *ids;
+    int32_t *offsets;
+    int32_t *slot_row;
+    int32_t *counts;      // [blocks][experts], or NULL for one workgroup
+    int n;                // slots
+    int per_block;        // slots per workgroup, a multiple of kSortThreads
+    int experts;
+    int bits;             // 2^bits >= experts
+};
+
+// Slots per expert of each workgroup's range (integer atomics in LDS: the
+// counts do not depend on their order).
+template <typename ID>
+__global__ void __launch_bounds__(kSortThreads) k_moe_count(SortArgs a)
+{
+    __shared__ int32_t hist[kMaxExperts];
+    for (int e = threadIdx.x; e < a.experts; e += kSortThreads) hist[e] = 0;
+    __syncthreads();
+    const int beg = blockIdx.x * a.per_block, end = min(beg + a.per_block, a.n);
+    for (int i = beg + threadIdx.x; i < end; i += kSortThreads) {
+        const int e = expert_of(static_cast<const ID *>(a.ids), i, a.experts);
+        if (e >= 0)
+            atomicAdd(&hist[e], 1);
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < a.experts; e += kSortThreads)
+        a.counts[(int64_t)blockIdx.x * a.experts + e] = hist[e];
+}
+
+// Rows of each workgroup's slots.  A wave owns a contiguous part of the
+// workgroup's range: it counts that part, the workgroup turns the waves'
+// counts and the counts of the workgroups before it into the wave's first row
+// of each expert, and the wave walks its part again 64 slots at a time, a
+// slot's rank among the 64 being the number of lower lanes with its expert.
+template <typename ID>
+__global__ void __launch_bounds__(kSortThreads) k_moe_place(SortArgs a)
+{
+    __shared__ int32_t hist[kSortWaves * kMaxExperts];
+    __shared__ int32_t wave_total[kSortWaves];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const ID *ids = static_cast<const ID *>(a.ids);
+    for (int i = tid; i < kSortWaves * a.experts; i += kSortThreads) hist[i] = 0;
+    __syncthreads();
+    const int part = a.per_block / kSortWaves;
+    const int beg = min(blockIdx.x * a.per_block + wave * part, a.n), end = min(beg + part, a.n);
+    int32_t *mine = hist + wave * a.experts;
+    for (int i = beg + lane; i < end; i += 64) {
+        const int e = expert_of(ids, i, a.experts);
+        if (e >= 0)
+            atomicAdd(&mine[e], 1);
+    }
+    __syncthreads();
+
+    // exclusive sums over the experts, a thread taking `each` consecutive ones
+    const int each = (a.experts + kSortThreads - 1) / kSortThreads;
+    int total[kMaxExperts / kSortThreads], before[kMaxExperts / kSortThreads], sum = 0;
+#pragma unroll
+    for (int j = 0; j < kMaxExperts / kSortThreads; ++j) {
+        const int e = tid * each + j;
+        total[j] = before[j] = 0;
+        if (j < each && e < a.experts) {
+            if (a.counts) {
+                for (int b = 0; b < (int)gridDim.x; ++b) {
+                    const int c = a.counts[(int64_t)b * a.experts + e];
+                    total[j] += c;
+                    before[j] += b < (int)blockIdx.x ? c : 0;
+                }
+            } else {
+                for (int w = 0; w < kSortWaves; ++w) total[j] += hist[w * a.experts + e];
+            }
+        }
+        sum += total[j];
+    }
+    int scan = sum;
+    for (int d = 1; d < 64; d <<= 1) {
+        const int v = __shfl_up(scan, d);
+        scan += lane >= d ? v : 0;
+    }
+    if (lane == 63)
+        wave_total[wave] = scan;
+    __syncthreads();
+    int first = scan - sum;
+    for (int w = 0; w < wave; ++w) first += wave_total[w];
+#pragma unroll
+    for (int j = 0; j < kMaxExperts / kSortThreads; ++j) {
+        const int e = tid * each + j;
+        if (j < each && e < a.experts) {
+            if (blockIdx.x == 0) {
+                a.offsets[e] = first;
+                if (e == a.experts - 1)
+                    a.offsets[a.experts] = first + total[j];
+            }
+            int at = first + before[j];
+            for (int w = 0; w < kSortWaves; ++w) {
+                const int c = hist[w * a.experts + e];
+                hist[w * a.experts + e] = at;
+                at += c;
+            }
+        }
+        first += total[j];
+    }
+    __syncthreads();
+
+    for (int base = beg; base < end; base += 64) {
+        const int i = base + lane;
+        const int e = i < end ? expert_of(ids, i, a.experts) : -1;
+        const uint64_t same = same_expert(e, a.bits);
+        const int lead = __ffsll((unsigned long long)same) - 1;
+        int at = 0;
+        if (e >= 0 && lane == lead)
+            at = atomicAdd(&mine[e], __popcll(same));
+        at = __shfl(at, lead);
+        if (i < end)
+            a.slot_row[i] = e >= 0 ? at + __popcll(same & (((uint64_t)1 << lane) - 1)) : -1;
+    }
+}
+
+int sort_blocks(int64_t n)
+{
+    return n <= kSortOne ? 1 : (int)min((n + 2047) / 2048, (int64_t)kSortMaxBlocks);
+}
+
+qlin_status check_sort(int32_t id_bits, int64_t tokens, int64_t topk, int64_t experts, const void *ids,
+                       const int32_t *offsets, const int32_t *slot_row, const void *ws, size_t ws_bytes)
+{
+    if (id_bits != 32 && id_bits != 64)
+        return QLIN_ERR_BAD_ARGUMENT;
+    if (tokens < 0 || topk < 1 || topk > kMaxTopk || tokens > kMaxSlots / topk || experts < 1 ||
+        experts > kMaxExperts)
+        return QLIN_ERR_BAD_SHAPE;
+    if (!offsets || (tokens > 0 && (!ids || !slot_row)))
+        return QLIN_ERR_NULL_POINTER;
+    if (!aligned(ids, id_bits / 8) || !aligned(offsets, 4) || !aligned(slot_row, 4) || !aligned(ws, 4))
+        return QLIN_ERR_MISALIGNED;
+    const size_t need = qlin_moe_sort_workspace_size(tokens, topk, experts);
+    if (need && (!ws || ws_bytes < need))
+        return QLIN_ERR_WORKSPACE;
+    return QLIN_OK;
+}
+
+template <typename ID>
+hipError_t launch_sort_id(const SortArgs &a, int blocks, hipStream_t s)
+{
+    if (a.counts) {
+        hipLaunchKernelGGL((k_moe_count<ID>), dim3(blocks), dim3(kSortThreads), 0, s, a);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess)
+            return e;
+    }
+    hipLaunchKernelGGL((k_moe_place<ID>), dim3(blocks), dim3(kSortThreads), 0, s, a);
+    return hipGetLastError();
+}
+
+hipError_t launch_sort(int32_t id_bits, int64_t tokens, int64_t topk, int64_t experts, const void *ids,
+                       int32_t *offsets, int32_t *slot_row, void *ws, hipStream_t s)
+{
+    const int64_t n = tokens * topk;
+    const int blocks = sort_blocks(n);
+    int64_t per = (n + blocks - 1) / blocks;
+    per = (per + kSortThreads - 1) / kSortThreads * kSortThreads;
+    int bits = 0;
+    while (((int64_t)1 << bits) < experts) ++bits;
+    const SortArgs a{ids, offsets, slot_row, blocks > 1 ? static_cast<int32_t *>(ws) : nullptr, (int)n,
+                     (int)per, (int)experts, bits};
+    return id_bits == 64 ? launch_sort_id<int64_t>(a, blocks, s) : launch_sort_id<int32_t>(a, blocks, s);
+}
+
+// ---------------------------------------------------------------------------
+// Rows.  A token belongs to `lanes` consecutive threads (a power of two up
+// to the workgroup's 256), each of which takes 16-byte pieces of the row;
+// what is left of a row after its 16-byte pieces goes element by element.
+// Pieces need only the element's alignment (the hardware loads and stores 16
+// bytes at any address), so odd widths and strides take the same path.
+// ---------------------------------------------------------------------------
+constexpr int kRowThreads = 256;
+
+struct RowArgs {
+    const uint8_t *x;       // permute: X; combine: Y; gradient: dOut
+    const uint8_t *y;       // gradient: Y
+    uint8_t *out;
+    const int32_t *slot_row;
+    const float *weights;   // combine (NULL: all 1) and its gradient
+    const float *scale;     // permute
+    float *out_f;           // permute: the rows' scales; gradient: dW
+    int64_t ldx, ldy, ldo;  // bytes
+    int tokens, topk, rows;
+    int cols;               // permute: bytes of a row; otherwise its elements
+    int scale_cols;
+    int lanes;
+};
+
+__global__ void __launch_bounds__(kRowThreads) k_moe_permute(RowArgs a)
+{
+    const int token = blockIdx.x * (kRowThreads / a.lanes) + threadIdx.x / a.lanes;
+    const int lane = threadIdx.x & (a.lanes - 1);
+    if (token >= a.tokens)
+        return;
+    const uint8_t *x = a.x + (int64_t)token * a.ldx;
+    const int32_t *rows = a.slot_row + (int64_t)token * a.topk;
+    const int pieces = a.cols >> 4, tail = a.cols & 15;
+    for (int p = lane; p < pieces; p += a.lanes) {
+        v4i v;
+        __builtin_memcpy(&v, x + 16 * (int64_t)p, 16);
+        for (int j = 0; j < a.topk; ++j) {
+            const int r = rows[j];
+            if ((unsigned)r < (unsigned)a.rows)
+                __builtin_memcpy(a.out + r * a.ldo + 16 * (int64_t)p, &v, 16);
+        }
+    }
+    for (int i = lane; i < tail; i += a.lanes) {
+        const int at = 16 * pieces + i;
+        for (int j = 0; j < a.topk; ++j) {
+            const int r = rows[j];
+            if ((unsigned)r < (unsigned)a.rows)
+                a.out[r * a.ldo + at] = x[at];
+        }
+    }
+    for (int c = lane; c < a.scale_cols; c += a.lanes) {
+        const float s = a.scale[(int64_t)token * a.scale_cols + c];
+        for (int j = 0; j < a.topk; ++j) {
+            const int r = rows[j];
+            if ((unsigned)r < (unsigned)a.rows)
+                a.out_f[(int64_t)r * a.scale_cols + c] = s;
+        }
+    }
+}
+
+template <typename T> struct Elem;
+template <> struct Elem<float> {
+    static __device__ inline float get(float v) { return v; }
+    static __device__ inline float put(float v) { return v; }
+};
+template <> struct Elem<__half> {
+    static __device__ inline float get(__half v) { return __half2float(v); }
+    static __device__ inline __half put(float v) { return __float2half(v); }
+};
+template <> struct Elem<uint16_t> {                // bf16 bits
+    static __device__ inline float get(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
+    static __device__ inline uint16_t put(float v) { return bf16_bits(v); }
+};
+
+// out[t] = sum_j w[t,j] y[row[t,j]]
+template <typename T>
+__global__ void __launch_bounds__(kRowThreads) k_moe_combine(RowArgs a)
+{
+    constexpr int V = 16 / sizeof(T);
+    const int token = blockIdx.x * (kRowThreads / a.lanes) + threadIdx.x / a.lanes;
+    const int lane = threadIdx.x & (a.lanes - 1);
+    if (token >= a.tokens)
+        return;
+    const int32_t *rows = a.slot_row + (int64_t)token * a.topk;
+    const float *weights = a.weights ? a.weights + (int64_t)token * a.topk : nullptr;
+    uint8_t *out = a.out + (int64_t)token * a.ldo;
+    const int pieces = a.cols / V, tail = a.cols % V;
+    for (int p = lane; p < pieces; p += a.lanes) {
+        float sum[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) sum[i] = 0.0f;
+        for (int j = 0; j < a.topk; ++j) {
+            const int r = rows[j];
+            if ((unsigned)r < (unsigned)a.rows) {
+                T v[V];
+                __builtin_memcpy(v, a.x + r * a.ldx + 16 * (int64_t)p, 16);
+                const float w = weights ? weights[j] : 1.0f;
+#pragma unroll
+                for (int i = 0; i < V; ++i) sum[i] = fmaf(w, Elem<T>::get(v[i]), sum[i]);
+            }
+        }
+        T o[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) o[i] = Elem<T>::put(sum[i]);
+        __builtin_memcpy(out + 16 * (int64_t)p, o, 16);
+    }
+    for (int i = lane; i < tail; i += a.lanes) {
+        const int64_t at = pieces * V + i;
+        float sum = 0.0f;
+        for (int j = 0; j < a.topk; ++j) {
+            const int r = rows[j];
+            if ((unsigned)r < (unsigned)a.rows)
+                sum = fmaf(weights ? weights[j] : 1.0f,
+                           Elem<T>::get(reinterpret_cast<const T *>(a.x + r * a.ldx)[at]), sum);
+        }
+        reinterpret_cast<T *>(out)[at] = Elem<T>::put(sum);
+    }
+}
+
+// dy[row[t,j]] = w[t,j] dout[t],  dw[t,j] = <dout[t], y[row[t,j]]>: one wave
+// per token, the dot products summed over its lanes in a fixed order.
+template <typename T>
+__global__ void __launch_bounds__(kRowThreads) k_moe_combine_backward(RowArgs a)
+{
+    constexpr int V = 16 / sizeof(T);
+    const int token = blockIdx.x * (kRowThreads / 64) + threadIdx.x / 64;
+    const int lane = threadIdx.x & 63;
+    if (token >= a.tokens)
+        return;
+    const uint8_t *dout = a.x + (int64_t)token * a.ldx;
+    const int pieces = a.cols / V, tail = a.cols % V;
+    for (int j = 0; j < a.topk; ++j) {
+        const int64_t slot = (int64_t)token * a.topk + j;
+        const int r = a.slot_row[slot];
+        float dot = 0.0f;
+        if ((unsigned)r < (unsigned)a.rows) {
+            const float w = a.weights[slot];
+            const uint8_t *y = a.y + r * a.ldy;
+            uint8_t *dy = a.out + r * a.ldo;
+            for (int p = lane; p < pieces; p += 64) {
+                T d[V], v[V], o[V];
+                __builtin_memcpy(d, dout + 16 * (int64_t)p, 16);
+                __builtin_memcpy(v, y + 16 * (int64_t)p, 16);
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const float f = Elem<T>::get(d[i]);
+                    dot = fmaf(f, Elem<T>::get(v[i]), dot);
+                    o[i] = Elem<T>::put(w * f);
+                }
+                __builtin_memcpy(dy + 16 * (int64_t)p, o, 16);
+            }
+            if (lane < tail) {
+                const int at = pieces * V + lane;
+                const float f = Elem<T>::get(reinterpret_cast<const T *>(dout)[at]);
+                dot = fmaf(f, Elem<T>::get(reinterpret_cast<const T *>(y)[at]), dot);
+                reinterpret_cast<T *>(dy)[at] = Elem<T>::put(w * f);
+            }
+        }
+        dot = wave_sum(dot);
+        if (lane == 0)
+            a.out_f[slot] = dot;
+    }
+}
+
+// Threads per token: enough for one 16-byte piece each, up to a workgroup.
+int row_lanes(int64_t bytes)
+{
+    int l = 16;
+    while (l < kRowThreads && 16 * (int64_t)l < bytes) l *= 2;
+    return l;
+}
+
+dim3 row_grid(const RowArgs &a)
+{
+    const int per = kRowThreads / a.lanes;
+    return dim3((unsigned)((a.tokens + per - 1) / per));
+}
+
+qlin_status check_rows(int64_t tokens, int64_t topk, int64_t rows)
+{
+    if (tokens < 0 || topk < 1 || topk > kMaxTopk || tokens > kMaxSlots / topk || rows < 0 || rows > kMaxSlots)
+        return QLIN_ERR_BAD_SHAPE;
+    return QLIN_OK;
+}
+
+qlin_status check_permute(int64_t row_bytes, const void *X, int64_t ldx, const void *Out, int64_t ldo,
+                          const float *scale, int64_t scale_cols, const float *out_scale)
+{
+    if (row_bytes <= 0 || row_bytes > kMaxRowBytes || scale_cols < 0 || scale_cols > kMaxRowK)
+        return QLIN_ERR_BAD_SHAPE;
+    if (!X || !Out || (scale_cols > 0 && (!scale || !out_scale)))
+        return QLIN_ERR_NULL_POINTER;
+    if (ldx < row_bytes || ldo < row_bytes || ldx > kMaxStride || ldo > kMaxStride)
+        return QLIN_ERR_BAD_STRIDE;
+    if (scale_cols > 0 && (!aligned(scale, 4) || !aligned(out_scale, 4)))
+        return QLIN_ERR_MISALIGNED;
+    return QLIN_OK;
+}
+
+hipError_t launch_permute(int64_t tokens, int64_t topk, int64_t rows, int64_t row_bytes, const void *X,
+                          int64_t ldx, const int32_t *slot_row, void *Out, int64_t ldo, const float *scale,
+                          int64_t scale_cols, float *out_scale, hipStream_t s)
+{
+    RowArgs a{};
+    a.x = static_cast<const uint8_t *>(X);
+    a.out = static_cast<uint8_t *>(Out);
+    a.slot_row = slot_row;
+    a.scale = scale;
+    a.out_f = out_scale;
+    a.ldx = ldx;
+    a.ldo = ldo;
+    a.tokens = (int)tokens;
+    a.topk = (int)topk;
+    a.rows = (int)rows;
+    a.cols = (int)row_bytes;
+    a.scale_cols = (int)scale_cols;
+    a.lanes = row_lanes(row_bytes);
+    hipLaunchKernelGGL(k_moe_permute, row_grid(a), dim3(kRowThreads), 0, s, a);
+    return hipGetLastError();
+}
+
+// Bytes of an element, 0 for an unknown type.
+int elem_size(qlin_row_type rt)
+{
+    return rt == QLIN_ROW_F32 ? 4 : rt == QLIN_ROW_BF16 || rt == QLIN_ROW_F16 ? 2 : 0;
+}
+
+qlin_status combine(qlin_row_type rt, int64_t tokens, int64_t topk, int64_t rows, int64_t K, const void *Y,
+                    int64_t ldy, const int32_t *slot_row, const float *weights, void *Out, int64_t ldo,
+                    void *stream)
+{
+    const int es = elem_size(rt);
+    if (!es)
+        return QLIN_ERR_BAD_ARGUMENT;
+    const qlin_status st = check_rows(tokens, topk, rows);
+    if (st != QLIN_OK)
+        return st;
+    if (K <= 0 || K > kMaxRowK)
+        return QLIN_ERR_BAD_SHAPE;
+    if (tokens == 0)
+        return QLIN_OK;
+    if ((rows > 0 && !Y) || !slot_row || !Out)
+        return QLIN_ERR_NULL_POINTER;
+    if (ldy < K || ldo < K || ldy > kMaxStride || ldo > kMaxStride)
+        return QLIN_ERR_BAD_STRIDE;
+    if (!aligned(Y, es) || !aligned(Out, es) || !aligned(slot_row, 4) || !aligned(weights, 4))
+        return QLIN_ERR_MISALIGNED;
+    RowArgs a{};
+    a.x = static_cast<const uint8_t *>(Y);
+    a.out = static_cast<uint8_t *>(Out);
+    a.slot_row = slot_row;
+    a.weights = weights;
+    a.ldx = ldy * es;
+    a.ldo = ldo * es;
+    a.tokens = (int)tokens;
+    a.topk = (int)topk;
+    a.rows = (int)rows;
+    a.cols = (int)K;
+    a.lanes = row_lanes(K * es);
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    const dim3 grid = row_grid(a), block(kRowThreads);
+    switch (rt) {
+    case QLIN_ROW_F32: hipLaunchKernelGGL((k_moe_combine<float>), grid, block, 0, s, a); break;
+    case QLIN_ROW_BF16: hipLaunchKernelGGL((k_moe_combine<uint16_t>), grid, block, 0, s, a); break;
+    case QLIN_ROW_F16: hipLaunchKernelGGL((k_moe_combine<__half>), grid, block, 0, s, a); break;
+    }
+    return hipGetLastError() == hipSuccess ? QLIN_OK : QLIN_ERR_HIP;
+}
+
+}  // namespace
+}  // namespace qlin
+
+using namespace qlin;
+
+extern "C" {
+
+size_t qlin_moe_sort_workspace_size(int64_t tokens, int64_t topk, int64_t experts)
+{
+    if (tokens < 0 || topk < 1 || topk > kMaxTopk || tokens > kMaxSlots / topk || experts < 1 ||
+        experts > kMaxExperts)
+        return 0;
+    const int blocks = sort_blocks(tokens * topk);
+    return blocks > 1 ? (size_t)blocks * experts * sizeof(int32_t) : 0;
+}
+
+qlin_status qlin_moe_sort(int32_t id_bits, int64_t tokens, int64_t topk, int64_t experts,
+                          const void *topk_ids, int32_t *group_offsets, int32_t *slot_row,
+                          void *workspace, size_t workspace_bytes, void *stream)
+{
+    const qlin_status st = check_sort(id_bits, tokens, topk, experts, topk_ids, group_offsets, slot_row,
+                                      workspace, workspace_bytes);
+    if (st != QLIN_OK)
+        return st;
+    return launch_sort(id_bits, tokens, topk, experts, topk_ids, group_offsets, slot_row, workspace,
+                       static_cast<hipStream_t>(stream)) == hipSuccess ? QLIN_OK : QLIN_ERR_HIP;
+}
+
+qlin_status qlin_moe_permute(int64_t tokens, int64_t topk, int64_t rows, int64_t row_bytes,
+                             const void *X, int64_t ldx, const int32_t *slot_row, void *Out,
+                             int64_t ldo, const float *scale, int64_t scale_cols, float *out_scale,
+                             void *stream)
+{
+    qlin_status st = check_rows(tokens, topk, rows);
+    if (st != QLIN_OK)
+        return st;
+    if (tokens == 0 || rows == 0)
+        return row_bytes <= 0 || row_bytes > kMaxRowBytes ? QLIN_ERR_BAD_SHAPE : QLIN_OK;
+    st = check_permute(row_bytes, X, ldx, Out, ldo, scale, scale_cols, out_scale);
+    if (st != QLIN_OK)
+        return st;
+    if (!slot_row)
+        return QLIN_ERR_NULL_POINTER;
+    if (!aligned(slot_row, 4))
+        return QLIN_ERR_MISALIGNED;
+    return launch_permute(tokens, topk, rows, row_bytes, X, ldx, slot_row, Out, ldo, scale, scale_cols,
+                          out_scale, static_cast<hipStream_t>(stream)) == hipSuccess ? QLIN_OK
+                                                                                    : QLIN_ERR_HIP;
+}
+
+qlin_status qlin_moe_dispatch(int32_t id_bits, int64_t tokens, int64_t topk, int64_t experts,
+                              const void *topk_ids, int64_t rows, int64_t row_bytes, const void *X,
+                              int64_t ldx, void *Out, int64_t ldo, const float *scale,
+                              int64_t scale_cols, float *out_scale, int32_t *group_offsets,
+                              int32_t *slot_row, void *workspace, size_t workspace_bytes, void *stream)
+{
+    qlin_status st = check_sort(id_bits, tokens, topk, experts, topk_ids, group_offsets, slot_row, workspace,
+                                workspace_bytes);
+    if (st != QLIN_OK)
+        return st;
+    if (rows < tokens * topk || rows > kMaxSlots)
+        return QLIN_ERR_BAD_SHAPE;
+    if (tokens > 0) {
+        st = check_permute(row_bytes, X, ldx, Out, ldo, scale, scale_cols, out_scale);
+        if (st != QLIN_OK)
+            return st;
+    } else if (row_bytes <= 0 || row_bytes > kMaxRowBytes) {
+        return QLIN_ERR_BAD_SHAPE;
+    }
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (launch_sort(id_bits, tokens, topk, experts, topk_ids, group_offsets, slot_row, workspace, s) !=
+        hipSuccess)
+        return QLIN_ERR_HIP;
+    if (tokens == 0)
+        return QLIN_OK;
+    return launch_permute(tokens, topk, rows, row_bytes, X, ldx, slot_row, Out, ldo, scale, scale_cols,
+                          out_scale, s) == hipSuccess ? QLIN_OK : QLIN_ERR_HIP;
+}
+
+qlin_status qlin_moe_combine(qlin_row_type rt, int64_t tokens, int64_t topk, int64_t rows, int64_t K,
+                             const void *Y, int64_t ldy, const int32_t *slot_row, const float *weights,
+                             void *Out, int64_t ldo, void *stream)
+{
+    if (tokens > 0 && !weights)
+        return QLIN_ERR_NULL_POINTER;
+    return combine(rt, tokens, topk, rows, K, Y, ldy, slot_row, weights, Out, ldo, stream);
+}
+
+qlin_status qlin_moe_permute_backward(qlin_row_type rt, int64_t tokens, int64_t topk, int64_t rows,
+                                      int64_t K, const void *dOut, int64_t ldo, const int32_t *slot_row,
+                                      void *dX, int64_t ldx, void *stream)
+{
+    return combine(rt, tokens, topk, rows, K, dOut, ldo, slot_row, nullptr, dX, ldx, stream);
+}
+
+qlin_status qlin_moe_combine_backward(qlin_row_type rt, int64_t tokens, int64_t topk, int64_t rows,
+                                      int64_t K, const void *dOut, int64_t ldo, const void *Y,
+                                      int64_t ldy, const int32_t *slot_row, const float *weights,
+                                      void *dY, int64_t lddy, float *dW, void *stream)
+{
+    const int es = elem_size(rt);
+    if (!es)
+        return QLIN_ERR_BAD_ARGUMENT;
+    const qlin_status st = check_rows(tokens, topk, rows);
+    if (st != QLIN_OK)
+        return st;
+    if (K <= 0 || K > kMaxRowK)
+        return QLIN_ERR_BAD_SHAPE;
+    if (tokens == 0)
+        return QLIN_OK;
+    if (!dOut || !slot_row || !weights || !dW || (rows > 0 && (!Y || !dY)))
+        return QLIN_ERR_NULL_POINTER;
+    if (ldo < K || ldy < K || lddy < K || ldo > kMaxStride || ldy > kMaxStride || lddy > kMaxStride)
+        return QLIN_ERR_BAD_STRIDE;
+    if (!aligned(dOut, es) || !aligned(Y, es) || !aligned(dY, es) || !aligned(slot_row, 4) ||
+        !aligned(weights, 4) || !aligned(dW, 4))
+        return QLIN_ERR_MISALIGNED;
+    RowArgs a{};
+    a.x = static_cast<const uint8_t *>(dOut);
+    a.y = static_cast<const uint8_t *>(Y);
+    a.out = static_cast<uint8_t *>(dY);
+    a.out_f = dW;
+    a.slot_row = slot_row;
+    a.weights = weights;
+    a.ldx = ldo * es;
+    a.ldy = ldy * es;
+    a.ldo = lddy * es;
+    a.tokens = (int)tokens;
+    a.topk = (int)topk;
+    a.rows = (int)rows;
+    a.cols = (int)K;
+    a.lanes = 64;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    const dim3 grid = row_grid(a), block(kRowThreads);
+    switch (rt) {
+    case QLIN_ROW_F32: hipLaunchKernelGGL((k_moe_combine_backward<float>), grid, block, 0, s, a); break;
+    case QLIN_ROW_BF16: hipLaunchKernelGGL((k_moe_combine_backward<uint16_t>), grid, block, 0, s, a); break;
+    case QLIN_ROW_F16: hipLaunchKernelGGL((k_moe_combine_backward<__half>), grid, block, 0, s, a); break;
+    }
+    return hipGetLastError() == hipSuccess ? QLIN_OK : QLIN_ERR_HIP;
+}
+
+}  // extern "C"
