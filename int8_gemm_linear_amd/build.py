@@ -26,6 +26,12 @@ SOURCES = [
     "qlin_quant.hip",
     "qlin_fused.hip",
     "qlin_w4.hip",
+    "qlin_w4_stream_32.hip",
+    "qlin_w4_stream_64.hip",
+    "qlin_w4_stream_128.hip",
+    "qlin_w4_tile_32.hip",
+    "qlin_w4_tile_64.hip",
+    "qlin_w4_tile_128.hip",
     "qlin_moe.hip",
     "qlin_stream_fp8.hip",
     "qlin_stream_int8.hip",

@@ -1,0 +1,235 @@
+// Products with 4-bit weights: what the kernels and the dispatcher share.
+//
+//   Y[m,n] = bf16( sum_g s[n,g] * sum_{k in g} X[m,k] * (q[n,k] - z[n,g]) )
+//
+// Codes become bf16 without a conversion: bf16 holds 7 mantissa bits, so the
+// bit pattern 0x4300 | q is the number 128 + q exactly.  The matrix cores then
+// sum x * (128 + q) over a group in fp32, and
+//   sum x (q - z) = sum x (128 + q) - (128 + z) * sum x
+// takes the rest away, the sum of x over the group being one for all weight
+// rows.  Products are exact; what the larger terms cost is fp32 rounding of
+// sums up to 136/8 times as large, 2^-20 relative beside the 2^-8 of the
+// result's rounding to bf16.
+//
+// Where a row of X is not finite, or so large that 143 x overflows fp32, that
+// difference is NaN although the formula's value may not be: such outputs are
+// computed again from the formula in fp64 (exact_value), one by one.
+#pragma once
+
+#include <hip/hip_fp16.h>
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "qlin_device.h"
+#include "qlinear.h"
+
+namespace qlin {
+namespace w4 {
+
+struct Args {
+    const uint16_t *x;
+    const uint8_t *b;
+    const uint8_t *scale;
+    const uint8_t *zero;          // or NULL: 8
+    uint16_t *y;
+    const int32_t *group_off;     // experts' row offsets, or NULL
+    int64_t b_gstride;            // bytes between experts' weights
+    int64_t ldx, ldb, ldy;        // elements, bytes, elements
+    int M;                        // rows (experts: the bound on an expert's rows)
+    int rows;                     // experts: rows of X and Y
+    int N, K, G;                  // G = K / group
+    int st;                       // qlin_scale_type
+};
+
+typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
+typedef uint32_t v2u __attribute__((ext_vector_type(2)));
+
+// Narrows the arguments to the workgroup's expert (grid.z), its rows held
+// inside the buffers whatever the offsets say; false: no rows.
+__device__ inline bool enter_expert(Args &a)
+{
+    if (!a.group_off)
+        return true;
+    const int e = blockIdx.z;
+    const int beg = min(max(a.group_off[e], 0), a.rows), end = min(a.group_off[e + 1], a.rows);
+    a.M = min(end - beg, a.M);
+    if (a.M <= 0)
+        return false;
+    a.x += (int64_t)beg * a.ldx;
+    a.y += (int64_t)beg * a.ldy;
+    a.b += e * a.b_gstride;
+    const int64_t sb = (int64_t)e * a.N * a.G;
+    a.scale += sb * (a.st == QLIN_SCALE_F32 ? 4 : 2);
+    if (a.zero)
+        a.zero += sb;
+    return true;
+}
+
+// Eight codes of one dword -> 128 + q as eight bf16, the nibbles four apart
+// side by side: 0 4 1 5 2 6 3 7.  Seven instructions; the natural order takes
+// ten.  `magic` holds 0x4300 twice in a vector register, which the compiler
+// is not told: an instruction takes one constant, and that is the mask.
+__device__ inline uint32_t expand_magic()
+{
+    uint32_t v = 0x43004300u;
+    asm volatile("" : "+v"(v));
+    return v;
+}
+
+__device__ inline v4i expand8(uint32_t w, uint32_t magic)
+{
+    const uint32_t mask = 0x000f000fu;
+    v4i r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        r[i] = (int)(((w >> (4 * i)) & mask) | magic);
+    }
+    return r;
+}
+
+// The same in the order of k, for operands that are copied into LDS as they
+// are: a nibble and its upper neighbour are brought 16 bits apart, two pairs
+// at a time.
+__device__ inline v4i expand8_natural(uint32_t w, uint32_t magic)
+{
+    const uint32_t mask = 0x000f000fu;
+    const uint32_t half[2] = {w & 0xffffu, w >> 16};
+    v4i r;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        uint32_t t = half[i] | (half[i] << 12);
+        asm("" : "+v"(t));          // (one instruction; not taken apart to be merged with the masks)
+        r[2 * i] = (int)((t & mask) | magic);
+        r[2 * i + 1] = (int)(((t >> 8) & mask) | magic);
+    }
+    return r;
+}
+
+// Eight tokens' values in the order of expand8.
+__device__ inline v4i operand_order(v4i x)
+{
+    v4i r;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        r[2 * i] = (int)__builtin_amdgcn_perm((uint32_t)x[2 + i], (uint32_t)x[i], 0x05040100u);
+        r[2 * i + 1] = (int)__builtin_amdgcn_perm((uint32_t)x[2 + i], (uint32_t)x[i], 0x07060302u);
+    }
+    return r;
+}
+
+__device__ inline v4f mma(v4i a, v4i b, v4f c)
+{
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, a), __builtin_bit_cast(v8bf, b), c,
+                                                   0, 0, 0);
+}
+
+// A scale from its 16 or 32 bits.
+template <int SB>
+__device__ inline float scale_value(uint32_t bits, int st)
+{
+    if (SB == 4)
+        return __uint_as_float(bits);
+    const float h = __half2float(__ushort_as_half((uint16_t)bits));
+    return st == QLIN_SCALE_BF16 ? __uint_as_float(bits << 16) : h;
+}
+
+// Two 16-byte loads of whole 128-byte lines, rows 0..7 and 8..15 of a block:
+// lane (n, q) of a load has row n mod 8 and the 16 bytes q of the line's
+// first half (n < 8) or second half (n >= 8).  Afterwards `a` holds the first
+// half and `b` the second, lane (n, q) the 16 bytes q of row n.
+__device__ inline void halves(v4i &a, v4i &b)
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int x = a[i], y = b[i];
+        // row_ror:8; banks 2 and 3 are lanes 8..15 of each 16
+        a[i] = __builtin_amdgcn_update_dpp(x, y, 0x128, 0xF, 0xC, false);
+        b[i] = __builtin_amdgcn_update_dpp(y, x, 0x128, 0xF, 0x3, false);
+    }
+}
+
+// A wave's 16-byte load brings lane (n, quarter q) the codes k = 32 q .. 32 q
+// + 31 of row n of a 128-code step: four dwords, one matrix instruction each,
+// an instruction summing over the four quarters.  With groups of 128 that is
+// one group.  With shorter groups the dwords change quarters first, so that
+// an instruction's four quarters hold one group (of 64: two instructions).
+// quarters(): that exchange; k_of(j, q): the k at which the eight codes of
+// instruction j in quarter q then start.
+template <int GROUP>
+__device__ inline void quarters(v4i &w)
+{
+    if (GROUP == 128)
+        return;
+    const v2u a = __builtin_amdgcn_permlane32_swap((uint32_t)w[0], (uint32_t)w[2], false, false);
+    const v2u b = __builtin_amdgcn_permlane32_swap((uint32_t)w[1], (uint32_t)w[3], false, false);
+    if (GROUP == 64) {
+        w = v4i{(int)a[0], (int)b[0], (int)a[1], (int)b[1]};
+    } else {
+        const v2u c = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);
+        const v2u d = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
+        w = v4i{(int)c[0], (int)c[1], (int)d[0], (int)d[1]};
+    }
+}
+
+template <int GROUP>
+__device__ inline int k_of(int j, int q)
+{
+    return GROUP == 128 ? 32 * q + 8 * j
+         : GROUP == 64  ? 32 * (2 * (j >> 1) + (q & 1)) + 8 * ((j & 1) + 2 * (q >> 1))
+                        : 32 * j + 8 * q;
+}
+
+// The other way: the place among a step's 16 operand pieces (4 j + q) of the
+// eight values starting at k = 8 r.
+template <int GROUP>
+__device__ inline int piece_of(int r)
+{
+    r &= 15;
+    return GROUP == 128 ? 4 * (r & 3) + (r >> 2)
+         : GROUP == 64  ? 8 * (r >> 3) + 4 * (r & 1) + 2 * ((r >> 1) & 1) + ((r >> 2) & 1)
+                        : r;
+}
+
+// The formula's value in fp64, for an output whose fast value is not finite.
+__device__ inline float exact_value(const Args &a, int64_t m, int64_t n)
+{
+    const int group = a.K / a.G;
+    double sum = 0.0;
+    for (int g = 0; g < a.G; ++g) {
+        const int64_t at = n * a.G + g;
+        const double s = a.st == QLIN_SCALE_F32
+                             ? reinterpret_cast<const float *>(a.scale)[at]
+                             : scale_value<2>(reinterpret_cast<const uint16_t *>(a.scale)[at], a.st);
+        const int z = a.zero ? a.zero[at] : 8;
+        for (int k = g * group; k < (g + 1) * group; ++k) {
+            const int q = (a.b[n * a.ldb + (k >> 1)] >> (4 * (k & 1))) & 15;
+            const float x = __uint_as_float((uint32_t)a.x[m * a.ldx + k] << 16);
+            sum += s * (double)(q - z) * (double)x;
+        }
+    }
+    return (float)sum;
+}
+
+__device__ inline bool is_finite(float v) { return fabsf(v) <= 3.4028234663852886e38f; }
+
+// One output: rounded to bf16, or computed again where it is not finite.
+__device__ inline void store_value(const Args &a, int64_t m, int64_t n, float v)
+{
+    if (!is_finite(v))
+        v = exact_value(a, m, n);
+    a.y[m * a.ldy + n] = bf16_bits(v);
+}
+
+constexpr int kStreamTokens = 8;
+
+// Launchers, one unit per group length; `experts` is grid.z.
+typedef hipError_t (*Launch)(const Args &a, int experts, hipStream_t s);
+hipError_t launch_stream_32(const Args &a, int experts, hipStream_t s);
+hipError_t launch_stream_64(const Args &a, int experts, hipStream_t s);
+hipError_t launch_stream_128(const Args &a, int experts, hipStream_t s);
+hipError_t launch_tile_32(const Args &a, int experts, hipStream_t s);
+hipError_t launch_tile_64(const Args &a, int experts, hipStream_t s);
+hipError_t launch_tile_128(const Args &a, int experts, hipStream_t s);
+
+}  // namespace w4
+}  // namespace qlin
