@@ -319,7 +319,10 @@ qlin_status qlin_silu_and_mul_per_block_quant(int64_t M, int64_t K, const uint16
  * (bytes), ldy >= N; X, B and Y 16-byte aligned, b_scale 4-byte aligned.  An
  * infinity or NaN in X reaches the outputs that the formula gives it and no
  * other row.  The caller owns every buffer; the call is asynchronous on
- * `stream`, allocates nothing and needs no workspace.  Errors as for
+ * `stream` and allocates nothing.  workspace: qlin_w4_workspace_size bytes,
+ * 16-byte aligned, with any contents, not used by two calls that may overlap
+ * in time (the parts of K where M x N alone is too little work for the GPU;
+ * they are added in order, so results do not depend on timing).  Errors as for
  * qlin_scaled_mm (a group or scale type not listed: QLIN_ERR_BAD_ARGUMENT). */
 typedef enum qlin_scale_type {
     QLIN_SCALE_F32 = 0,
@@ -330,7 +333,9 @@ typedef enum qlin_scale_type {
 qlin_status qlin_w4_mm(int64_t M, int64_t N, int64_t K, int64_t group, const uint16_t *X,
                        int64_t ldx, const uint8_t *B, int64_t ldb, qlin_scale_type st,
                        const void *b_scale, const uint8_t *b_zero, uint16_t *Y, int64_t ldy,
-                       void *stream);
+                       void *workspace, size_t workspace_bytes, void *stream);
+/* Workspace bytes of a qlin_w4_mm of these sizes (0 for most). */
+size_t qlin_w4_workspace_size(int64_t M, int64_t N, int64_t K);
 
 /* The same for `groups` experts in one launch: expert g owns the rows
  * group_offsets[g] .. group_offsets[g+1]-1 of X and Y and the weights
@@ -340,7 +345,8 @@ qlin_status qlin_w4_mm(int64_t M, int64_t N, int64_t K, int64_t group, const uin
  * nondecreasing leaves rows uncomputed but stays inside the buffers).  rows:
  * the rows of X and Y.  max_rows: a bound on any expert's row count; rows of
  * an expert beyond it are not computed.  Rows outside every expert keep what Y
- * holds.  groups <= 65535 (0 is a no-op); b_group_stride >= 0 and % 16 == 0. */
+ * holds.  groups <= 65535 (0 is a no-op); b_group_stride >= 0 and % 16 == 0.
+ * No workspace. */
 qlin_status qlin_grouped_w4_mm(int64_t groups, const int32_t *group_offsets, int64_t max_rows,
                                int64_t rows, int64_t N, int64_t K, int64_t group,
                                const uint16_t *X, int64_t ldx, const uint8_t *B, int64_t ldb,

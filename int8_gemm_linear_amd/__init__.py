@@ -157,8 +157,10 @@ def _lib():
     lib.qlin_silu_and_mul_dynamic_per_token_quant.restype = I
     lib.qlin_silu_and_mul_per_block_quant.argtypes = [I64, I64, P, I64, P, I64, P, P]
     lib.qlin_silu_and_mul_per_block_quant.restype = I
-    lib.qlin_w4_mm.argtypes = [I64, I64, I64, I64, P, I64, P, I64, I, P, P, P, I64, P]
+    lib.qlin_w4_mm.argtypes = [I64, I64, I64, I64, P, I64, P, I64, I, P, P, P, I64, P, SZ, P]
     lib.qlin_w4_mm.restype = I
+    lib.qlin_w4_workspace_size.argtypes = [I64, I64, I64]
+    lib.qlin_w4_workspace_size.restype = SZ
     lib.qlin_grouped_w4_mm.argtypes = [I64, P, I64, I64, I64, I64, I64, P, I64, P, I64, I64, I, P, P, P,
                                        I64, P]
     lib.qlin_grouped_w4_mm.restype = I
@@ -656,8 +658,12 @@ def w4_mm(x, b_q, b_scale, b_zero=None, out=None):
         raise ValueError("x is [M,K] and b_q must be [N,K/2]")
     group, st, zero = _w4_scales(b_scale, b_zero, (N,), K, dev)
     out, ldy = _rows_out(out, (M, N), torch.bfloat16, dev)
+    # the workspace is the call's own: see _sort_buffers
+    n = _lib().qlin_w4_workspace_size(M, N, K)
+    ws = torch.empty((n,), dtype=torch.uint8, device=dev) if n else None
     _call_on(dev, _lib().qlin_w4_mm, [M, N, K, group, x.data_ptr(), ldx, b_q.data_ptr(), ldb, st,
-                                      b_scale.data_ptr(), zero, out.data_ptr(), ldy], "qlin_w4_mm")
+                                      b_scale.data_ptr(), zero, out.data_ptr(), ldy,
+                                      None if ws is None else ws.data_ptr(), n], "qlin_w4_mm")
     return out
 
 

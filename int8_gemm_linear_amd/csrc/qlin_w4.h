@@ -37,32 +37,69 @@ struct Args {
     int64_t ldx, ldb, ldy;        // elements, bytes, elements
     int M;                        // rows (experts: the bound on an expert's rows)
     int rows;                     // experts: rows of X and Y
+    int experts;                  // 0 without experts
     int N, K, G;                  // G = K / group
     int st;                       // qlin_scale_type
+    int splits;                   // parts of K, summed by a second kernel
+    int split_k;                  // codes of a part
+    float *part;                  // [splits][M][N] sums of the parts
 };
 
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 typedef uint32_t v2u __attribute__((ext_vector_type(2)));
 
-// Narrows the arguments to the workgroup's expert (grid.z), its rows held
-// inside the buffers whatever the offsets say; false: no rows.
-__device__ inline bool enter_expert(Args &a)
+// Tiles of TILE rows that cover every expert's rows (or M): at most this many.
+inline int64_t row_tiles(const Args &a, int tile)
 {
-    if (!a.group_off)
-        return true;
-    const int e = blockIdx.z;
-    const int beg = min(max(a.group_off[e], 0), a.rows), end = min(a.group_off[e + 1], a.rows);
-    a.M = min(end - beg, a.M);
-    if (a.M <= 0)
-        return false;
-    a.x += (int64_t)beg * a.ldx;
-    a.y += (int64_t)beg * a.ldy;
-    a.b += e * a.b_gstride;
-    const int64_t sb = (int64_t)e * a.N * a.G;
-    a.scale += sb * (a.st == QLIN_SCALE_F32 ? 4 : 2);
-    if (a.zero)
-        a.zero += sb;
-    return true;
+    return a.group_off ? a.rows / tile + a.experts : ((int64_t)a.M + tile - 1) / tile;
+}
+
+// The first row m0 of the workgroup's tile `y` among those; narrows the
+// arguments to its expert, whose rows are held inside the buffers whatever the
+// offsets say.  Counting the experts' tiles here, 64 experts at a time, keeps
+// the grid near the work: a grid of max_rows for every expert would be mostly
+// workgroups that leave at once (32 tokens, 128 experts: 49152, of which 9 in
+// 10).  False: no such tile.
+template <int TILE>
+__device__ inline bool enter_tile(Args &a, int y, int &m0)
+{
+    if (!a.group_off) {
+        m0 = y * TILE;
+        return m0 < a.M;
+    }
+    const int lane = threadIdx.x & 63;
+    for (int e0 = 0; e0 < a.experts; e0 += 64) {
+        const int e = e0 + lane;
+        int beg = 0, rows = 0;
+        if (e < a.experts) {
+            beg = min(max(a.group_off[e], 0), a.rows);
+            rows = min(max(min(a.group_off[e + 1], a.rows) - beg, 0), a.M);
+        }
+        const int tiles = (rows + TILE - 1) / TILE;
+        int scan = tiles;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int v = __shfl_up(scan, d);
+            scan += lane >= d ? v : 0;
+        }
+        const int all = __builtin_amdgcn_readlane(scan, 63);
+        if (y < all) {
+            const int at = __builtin_ctzll(__ballot(scan > y));
+            beg = __builtin_amdgcn_readlane(beg, at);
+            a.M = __builtin_amdgcn_readlane(rows, at);
+            m0 = (y - __builtin_amdgcn_readlane(scan - tiles, at)) * TILE;
+            a.x += (int64_t)beg * a.ldx;
+            a.y += (int64_t)beg * a.ldy;
+            a.b += (e0 + at) * a.b_gstride;
+            const int64_t sb = (int64_t)(e0 + at) * a.N * a.G;
+            a.scale += sb * (a.st == QLIN_SCALE_F32 ? 4 : 2);
+            if (a.zero)
+                a.zero += sb;
+            return true;
+        }
+        y -= all;
+    }
+    return false;
 }
 
 // Eight codes of one dword -> 128 + q as eight bf16, the nibbles four apart
@@ -222,14 +259,23 @@ __device__ inline void store_value(const Args &a, int64_t m, int64_t n, float v)
 
 constexpr int kStreamTokens = 8;
 
-// Launchers, one unit per group length; `experts` is grid.z.
-typedef hipError_t (*Launch)(const Args &a, int experts, hipStream_t s);
-hipError_t launch_stream_32(const Args &a, int experts, hipStream_t s);
-hipError_t launch_stream_64(const Args &a, int experts, hipStream_t s);
-hipError_t launch_stream_128(const Args &a, int experts, hipStream_t s);
-hipError_t launch_tile_32(const Args &a, int experts, hipStream_t s);
-hipError_t launch_tile_64(const Args &a, int experts, hipStream_t s);
-hipError_t launch_tile_128(const Args &a, int experts, hipStream_t s);
+// Launchers, one unit per group length.
+typedef hipError_t (*Launch)(const Args &a, hipStream_t s);
+hipError_t launch_stream_32(const Args &a, hipStream_t s);
+hipError_t launch_stream_64(const Args &a, hipStream_t s);
+hipError_t launch_stream_128(const Args &a, hipStream_t s);
+hipError_t launch_tile_32(const Args &a, hipStream_t s);
+hipError_t launch_tile_64(const Args &a, hipStream_t s);
+hipError_t launch_tile_128(const Args &a, hipStream_t s);
+
+// The tile kernel's tiles for M tokens (experts: a typical expert's): 16 tb
+// tokens, 64 rb weight rows, ks codes of K at a time.
+struct TilePick {
+    int tb, rb, ks;
+};
+TilePick pick_tile(int64_t tokens, int64_t N);
+// Parts of K for a product without experts (1: none).
+int pick_splits(int64_t M, int64_t N, int64_t K);
 
 }  // namespace w4
 }  // namespace qlin

@@ -1,5 +1,7 @@
 // Entry points of the products with 4-bit weights: checks, and the choice of
 // the kernel.
+#include <algorithm>
+
 #include "qlin_w4.h"
 
 namespace qlin {
@@ -56,18 +58,91 @@ w4::Args make_args(int64_t M, int64_t N, int64_t K, int64_t group, const uint16_
     return a;
 }
 
-qlin_status launch(const w4::Args &a, int64_t experts, void *stream)
+// Sum of the parts of K, in order; four outputs a thread where N allows.
+template <int V>
+__global__ void __launch_bounds__(256) k_reduce(w4::Args a)
 {
-    if (a.M > 65535 * 128)
-        return QLIN_ERR_BAD_SHAPE;
-    const int group = a.K / a.G;
+    const int64_t all = (int64_t)a.M * a.N;
+    const int64_t e = ((int64_t)blockIdx.x * 256 + threadIdx.x) * V;
+    if (e >= all)
+        return;
+    float v[V] = {};
+    for (int s = 0; s < a.splits; ++s) {
+        float p[V];
+        __builtin_memcpy(p, a.part + s * all + e, 4 * V);
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] += p[i];
+    }
+    const int64_t m = e / a.N, n = e % a.N;
+#pragma unroll
+    for (int i = 0; i < V; ++i) w4::store_value(a, m, n + i, v[i]);
+}
+
+size_t part_bytes(int64_t M, int64_t N, int splits) { return splits > 1 ? (size_t)splits * M * N * sizeof(float) : 0; }
+
+qlin_status launch(w4::Args &a, void *ws, size_t ws_bytes, void *stream)
+{
     static const w4::Launch kStream[3] = {w4::launch_stream_32, w4::launch_stream_64, w4::launch_stream_128};
     static const w4::Launch kTile[3] = {w4::launch_tile_32, w4::launch_tile_64, w4::launch_tile_128};
-    const w4::Launch fn = (a.M <= w4::kStreamTokens ? kStream : kTile)[group == 128 ? 2 : group == 64 ? 1 : 0];
-    return fn(a, (int)experts, static_cast<hipStream_t>(stream)) == hipSuccess ? QLIN_OK : QLIN_ERR_HIP;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    const int group = a.K / a.G, which = group == 128 ? 2 : group == 64 ? 1 : 0;
+    a.splits = 1;
+    a.split_k = a.K;
+    // experts: by the rows of a typical one
+    if ((a.experts ? a.rows / a.experts : a.M) <= w4::kStreamTokens)
+        return kStream[which](a, s) == hipSuccess ? QLIN_OK : QLIN_ERR_HIP;
+    if (!a.experts) {
+        a.splits = w4::pick_splits(a.M, a.N, a.K);
+        const size_t need = part_bytes(a.M, a.N, a.splits);
+        if (need && (!ws || ws_bytes < need))
+            return QLIN_ERR_WORKSPACE;
+        if (need && !aligned(ws, 16))
+            return QLIN_ERR_MISALIGNED;
+        a.part = static_cast<float *>(ws);
+        const int ks = w4::pick_tile(a.M, a.N).ks;
+        const int stages = (a.K + ks - 1) / ks;
+        a.split_k = (stages + a.splits - 1) / a.splits * ks;
+    }
+    if (kTile[which](a, s) != hipSuccess)
+        return QLIN_ERR_HIP;
+    if (a.splits > 1) {
+        const int v = a.N % 4 == 0 ? 4 : 1;
+        const dim3 grid((unsigned)(((int64_t)a.M * a.N / v + 255) / 256));
+        if (v == 4)
+            hipLaunchKernelGGL(k_reduce<4>, grid, dim3(256), 0, s, a);
+        else
+            hipLaunchKernelGGL(k_reduce<1>, grid, dim3(256), 0, s, a);
+        if (hipGetLastError() != hipSuccess)
+            return QLIN_ERR_HIP;
+    }
+    return QLIN_OK;
 }
 
 }  // namespace
+
+namespace w4 {
+
+TilePick pick_tile(int64_t tokens, int64_t)
+{
+    return tokens <= 16 ? TilePick{1, 1, 256} : tokens <= 32 ? TilePick{2, 2, 256} : TilePick{4, 4, 128};
+}
+
+int pick_splits(int64_t M, int64_t N, int64_t K)
+{
+    if (M <= kStreamTokens)
+        return 1;
+    const TilePick p = pick_tile(M, N);
+    const int64_t tiles = ((M + 16 * p.tb - 1) / (16 * p.tb)) * ((N + 64 * p.rb - 1) / (64 * p.rb));
+    const int64_t stages = (K + p.ks - 1) / p.ks;
+    // two workgroups of a CU, each at least four stages of K
+    const int64_t splits = std::min((512 + tiles - 1) / tiles, stages / 4);
+    if (splits <= 1 || tiles >= 256)
+        return 1;
+    const int64_t each = (stages + splits - 1) / splits;
+    return (int)((stages + each - 1) / each);        // none of them empty
+}
+
+}  // namespace w4
 }  // namespace qlin
 
 using namespace qlin;
@@ -77,12 +152,20 @@ extern "C" {
 qlin_status qlin_w4_mm(int64_t M, int64_t N, int64_t K, int64_t group, const uint16_t *X,
                        int64_t ldx, const uint8_t *B, int64_t ldb, qlin_scale_type st,
                        const void *b_scale, const uint8_t *b_zero, uint16_t *Y, int64_t ldy,
-                       void *stream)
+                       void *workspace, size_t workspace_bytes, void *stream)
 {
     const qlin_status r = check(M, N, K, group, X, ldx, B, ldb, st, b_scale, Y, ldy);
     if (r != QLIN_OK || M == 0 || N == 0)
         return r;
-    return launch(make_args(M, N, K, group, X, ldx, B, ldb, st, b_scale, b_zero, Y, ldy), 1, stream);
+    w4::Args a = make_args(M, N, K, group, X, ldx, B, ldb, st, b_scale, b_zero, Y, ldy);
+    return launch(a, workspace, workspace_bytes, stream);
+}
+
+size_t qlin_w4_workspace_size(int64_t M, int64_t N, int64_t K)
+{
+    if (M <= 0 || M > kMaxRows || N <= 0 || N > kMaxRows || K <= 0 || K > kMaxW4K)
+        return 0;
+    return part_bytes(M, N, w4::pick_splits(M, N, K));
 }
 
 qlin_status qlin_grouped_w4_mm(int64_t groups, const int32_t *group_offsets, int64_t max_rows,
@@ -107,7 +190,8 @@ qlin_status qlin_grouped_w4_mm(int64_t groups, const int32_t *group_offsets, int
     a.group_off = group_offsets;
     a.b_gstride = b_group_stride;
     a.rows = (int)rows;
-    return launch(a, groups, stream);
+    a.experts = (int)groups;
+    return launch(a, nullptr, 0, stream);
 }
 
 }  // extern "C"

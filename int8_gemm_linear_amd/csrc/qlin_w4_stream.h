@@ -153,16 +153,15 @@ __device__ inline void add_slot(v4f *total, S &slot, const v4i *x, int st, uint3
 template <int U, int AHEAD, int GROUP, int SB, bool ZERO, bool EVEN>
 __global__ void __launch_bounds__(64 * kStreamWaves) k_stream(Args a, int kc)
 {
-    if (!enter_expert(a))
+    const int gx = (a.N + 8 * U - 1) / (8 * U);
+    int m0;
+    if (!enter_tile<kStreamTokens>(a, blockIdx.x / gx, m0))
         return;
     extern __shared__ v4i lds[];
-    const int m0 = blockIdx.y * kStreamTokens;
-    if (m0 >= a.M)
-        return;
     const int lane = threadIdx.x & 63, waves = blockDim.x >> 6;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = lane & 15, q = lane >> 4;
-    const int n0 = blockIdx.x * 8 * U;
+    const int n0 = (int)(blockIdx.x % gx) * 8 * U;
     const int tokens = min(a.M - m0, kStreamTokens);
     const int pitch = token_pitch(min(kc, (a.K + kSlot - 1) / kSlot * kSlot));
     const uint8_t *wrow[U], *srow[U], *zrow[U];
@@ -240,9 +239,11 @@ __global__ void __launch_bounds__(64 * kStreamWaves) k_stream(Args a, int kc)
 }
 
 template <int U, int AHEAD, int GROUP, int SB, bool ZERO, bool EVEN>
-hipError_t launch_stream_as(const Args &a, int experts, int waves, int lds_bytes, hipStream_t s)
+hipError_t launch_stream_as(const Args &a, int waves, int lds_bytes, hipStream_t s)
 {
-    const int gx = (a.N + 8 * U - 1) / (8 * U), gy = (a.M + kStreamTokens - 1) / kStreamTokens;
+    const int64_t grid = (int64_t)((a.N + 8 * U - 1) / (8 * U)) * row_tiles(a, kStreamTokens);
+    if (grid > 0x7fffffff)
+        return hipErrorInvalidValue;
     const int slots = (a.K + kSlot - 1) / kSlot;
     const int tokens = min(a.M, kStreamTokens);
     const int fits = (lds_bytes / (16 * tokens) - 4) * 8;               // codes of K whose tokens fit
@@ -250,37 +251,37 @@ hipError_t launch_stream_as(const Args &a, int experts, int waves, int lds_bytes
     const int round = AHEAD * waves * kSlot;
     const int kc = min(fits / round, (a.K + round - 1) / round) * round;
     const int lds = max(16 * tokens * token_pitch(min(kc, slots * kSlot)), waves * U * 512);
-    hipLaunchKernelGGL((k_stream<U, AHEAD, GROUP, SB, ZERO, EVEN>), dim3(gx, gy, experts), dim3(64 * waves), lds, s,
-                       a, kc);
+    hipLaunchKernelGGL((k_stream<U, AHEAD, GROUP, SB, ZERO, EVEN>), dim3((unsigned)grid), dim3(64 * waves), lds,
+                       s, a, kc);
     return hipGetLastError();
 }
 
 template <int GROUP, int SB, bool ZERO, bool EVEN>
-hipError_t stream_pick(const Args &a, int experts, hipStream_t s)
+hipError_t stream_pick(const Args &a, hipStream_t s)
 {
-    const int64_t rows = (int64_t)a.N * experts;
+    const int64_t rows = (int64_t)a.N * max(a.experts, 1);
     if (rows <= 16 * 256)
-        return launch_stream_as<1, 2, GROUP, SB, ZERO, EVEN>(a, experts, 4, kStreamLds, s);
+        return launch_stream_as<1, 2, GROUP, SB, ZERO, EVEN>(a, 4, kStreamLds, s);
     if (a.M <= 2 || rows <= 32 * 1024)
-        return launch_stream_as<2, 2, GROUP, SB, ZERO, EVEN>(a, experts, 4, kStreamLds, s);
-    return launch_stream_as<4, 2, GROUP, SB, ZERO, EVEN>(a, experts, 4, kStreamLds, s);
+        return launch_stream_as<2, 2, GROUP, SB, ZERO, EVEN>(a, 4, kStreamLds, s);
+    return launch_stream_as<4, 2, GROUP, SB, ZERO, EVEN>(a, 4, kStreamLds, s);
 }
 
 template <int GROUP, int SB, bool ZERO>
-hipError_t stream_even(const Args &a, int experts, hipStream_t s)
+hipError_t stream_even(const Args &a, hipStream_t s)
 {
     // groups of 128 divide K by themselves
     if (GROUP == 128 || a.K % 128 == 0)
-        return stream_pick<GROUP, SB, ZERO, true>(a, experts, s);
-    return stream_pick<GROUP, SB, ZERO, GROUP == 128>(a, experts, s);
+        return stream_pick<GROUP, SB, ZERO, true>(a, s);
+    return stream_pick<GROUP, SB, ZERO, GROUP == 128>(a, s);
 }
 
 template <int GROUP>
-hipError_t stream_any(const Args &a, int experts, hipStream_t s)
+hipError_t stream_any(const Args &a, hipStream_t s)
 {
     if (a.st == QLIN_SCALE_F32)
-        return a.zero ? stream_even<GROUP, 4, true>(a, experts, s) : stream_even<GROUP, 4, false>(a, experts, s);
-    return a.zero ? stream_even<GROUP, 2, true>(a, experts, s) : stream_even<GROUP, 2, false>(a, experts, s);
+        return a.zero ? stream_even<GROUP, 4, true>(a, s) : stream_even<GROUP, 4, false>(a, s);
+    return a.zero ? stream_even<GROUP, 2, true>(a, s) : stream_even<GROUP, 2, false>(a, s);
 }
 
 }  // namespace w4

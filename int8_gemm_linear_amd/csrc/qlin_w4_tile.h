@@ -1,18 +1,25 @@
 // 4-bit products of more than 8 tokens: tiles on the matrix cores.
 //
-// A workgroup owns 16 TB tokens and 16 RB W weight rows, W waves side by side
-// along the rows.  The tokens of KS codes at a time are copied straight into
-// LDS (two buffers) in the order in which the matrix instructions take their
-// operands; each wave loads its own rows' codes and scales into registers,
-// one stage ahead, and expands them there, once for all tokens.  A group's
-// products are summed by themselves, corrected by its sum of x, scaled and
-// added to the totals in registers.
+// A workgroup of four waves owns 16 TB tokens and 64 RB weight rows, 16 RB a
+// wave.  The tokens of KS codes at a time are copied straight into LDS, two
+// stages ahead through three buffers, in the order in which the matrix
+// instructions take their operands; each wave loads its own rows' codes and
+// scales into registers, one stage ahead, and expands them there, once for
+// all tokens.  A group's products are summed by themselves, starting from
+// what its sum of x takes away, then scaled and added to the totals.  That
+// sum of x is the same for all weight rows: a stage ahead, each wave computes
+// it for some of the tokens with products by ones and leaves it in LDS.
+//
+// Where M x N is too few tiles for the 256 CUs, K is split over workgroups
+// whose sums a second kernel adds in order.
 #pragma once
 
 #include "qlin_w4.h"
 
 namespace qlin {
 namespace w4 {
+
+constexpr int kTileWaves = 4;
 
 // The codes, scales and zero points of a wave's rows for a stage.  With KS =
 // 256 two loads take whole 128-byte lines of 8 rows each (see halves()).
@@ -45,19 +52,27 @@ struct Codes {
 };
 
 template <int TB, int RB, int KS, int GROUP, int SB, bool ZERO>
-__global__ void __launch_bounds__(256) k_tile(Args a)
+__global__ void __launch_bounds__(64 * kTileWaves) k_tile(Args a)
 {
-    constexpr int H = KS / 128, PIECES = KS / 8, PER = GROUP / 32;
-    if (!enter_expert(a))
+    constexpr int H = KS / 128, PIECES = KS / 8, PER = GROUP / 32, NG = KS / GROUP;
+    constexpr int COPIES = 16 * TB * PIECES / 64;           // 1 KB each
+    // id = 8 (y + tiles * (nx / 8)) + nx mod 8 (+ the split's share of the
+    // grid): workgroups go to the 8 XCDs in turn, so the token tiles of a
+    // weight tile meet in one L2
+    const int gx = (a.N + 64 * RB - 1) / (64 * RB), gx8 = (gx + 7) & ~7;
+    const int per = gridDim.x / a.splits, tiles = per / gx8;
+    const int split = blockIdx.x / per, id = blockIdx.x % per;
+    const int nx = id / (8 * tiles) * 8 + (id & 7);
+    int m0;
+    if (nx >= gx || !enter_tile<16 * TB>(a, (id >> 3) % tiles, m0))
         return;
-    __shared__ v4i lds[2][16 * TB * PIECES];
-    const int m0 = blockIdx.y * 16 * TB;
-    if (m0 >= a.M)
-        return;
-    const int lane = threadIdx.x & 63, waves = blockDim.x >> 6;
+    __shared__ v4i lds[3][16 * TB * PIECES];
+    __shared__ v4f sums[2][NG][TB * 4];             // [group][token / 4], times -136 without zero points
+    const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = lane & 15, q = lane >> 4;
-    const int n0 = (blockIdx.x * waves + wave) * 16 * RB;
+    const int n0 = (nx * kTileWaves + wave) * 16 * RB;
+    const int kbeg = split * a.split_k, kend = min(a.K, kbeg + a.split_k);
     const uint8_t *wrow[RB][H], *srow[RB], *zrow[RB];
 #pragma unroll
     for (int r = 0; r < RB; ++r) {
@@ -76,79 +91,134 @@ __global__ void __launch_bounds__(256) k_tile(Args a)
         for (int t = 0; t < TB; ++t) total[r][t] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 
     // place p of token t holds the step's piece p with its bits 2 and 3
-    // exchanged by t: a read of 16 tokens x 4 pieces meets every bank equally
+    // exchanged by t: a read of 16 tokens x 4 pieces meets every bank equally.
+    // A wave's copies are 4 KB apart: the lane's place in them is one
+    const int copy_t = (wave * 64 + lane) / PIECES, copy_p = lane % PIECES;
+    const int copy_k = 128 * (copy_p >> 4) + k_of<GROUP>(((copy_p >> 2) & 3) ^ (copy_t & 3), copy_p & 3);
     auto stage = [&](int k0, int buf) {
-        for (int i = wave; i < 16 * TB * PIECES / 64; i += waves) {
-            const int at = i * 64 + lane, t = at / PIECES, p = at % PIECES;
-            const int k = k0 + 128 * (p >> 4) + k_of<GROUP>(((p >> 2) & 3) ^ (t & 3), p & 3);
-            if (k < a.K)
-                lds_dma16(a.x + (int64_t)min(m0 + t, a.M - 1) * a.ldx + k, &lds[buf][i * 64]);
+#pragma unroll
+        for (int i = 0; i < COPIES / kTileWaves; ++i) {
+            const int t = min(m0 + copy_t + i * (256 / PIECES), a.M - 1);
+            v4i *to = &lds[buf][(i * kTileWaves + wave) * 64];
+            if (k0 + copy_k < kend)
+                lds_dma16(a.x + (int64_t)t * a.ldx + k0 + copy_k, to);
             else
-                lds[buf][at] = zero4i();
+                to[lane] = zero4i();
         }
     };
     int place[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) place[j] = n * PIECES + 4 * (j ^ (n & 3)) + q;
 
-    const uint32_t magic = expand_magic();
     const v4i ones = {0x3f803f80, 0x3f803f80, 0x3f803f80, 0x3f803f80};
+    auto sum = [&](int buf, int to) {
+#pragma unroll
+        for (int i = 0; i < (TB * H + kTileWaves - 1) / kTileWaves; ++i) {
+            const int task = i * kTileWaves + wave, t = task / H, h = task % H;
+            if (task >= TB * H)
+                break;
+#pragma unroll
+            for (int g = 0; g < 4 / PER; ++g) {
+                v4f s = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int j = 0; j < PER; ++j) s = mma(lds[buf][place[g * PER + j] + 16 * h + 16 * t * PIECES], ones, s);
+                if (!ZERO)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) s[j] *= -136.0f;
+                if (n == 0)
+                    sums[to][h * (4 / PER) + g][t * 4 + q] = s;
+            }
+        }
+    };
+
+    const uint32_t magic = expand_magic();
     Codes<RB, KS, GROUP, SB, ZERO> cur, next;
-    stage(0, 0);
-    cur.load(a, wrow, srow, zrow, 0, n, q);
-    for (int k0 = 0, buf = 0; k0 < a.K; k0 += KS, buf ^= 1) {
+    stage(kbeg, 0);
+    if (kbeg + KS < kend)
+        stage(kbeg + KS, 1);
+    cur.load(a, wrow, srow, zrow, kbeg, n, q);
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    sum(0, 0);
+    int buf = 0, par = 0;
+    for (int k0 = kbeg; k0 < kend; k0 += KS) {
+        const int buf1 = buf == 2 ? 0 : buf + 1, buf2 = buf1 == 2 ? 0 : buf1 + 1;
+        // the next stage's tokens have landed; this stage's sums are there; the last stage's buffer is free
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
         __syncthreads();
-        if (k0 + KS < a.K) {
-            stage(k0 + KS, buf ^ 1);
-            next.load(a, wrow, srow, zrow, k0 + KS, n, q);
-        }
+        if (k0 + 2 * KS < kend)
+            stage(k0 + 2 * KS, buf2);
+        next.load(a, wrow, srow, zrow, k0 + KS, n, q);
+        if (k0 + KS < kend)
+            sum(buf1, par ^ 1);
+        const v4i *xs = lds[buf];
 #pragma unroll
         for (int h = 0; h < H; ++h) {
             if (H == 2 && h == 0) {
 #pragma unroll
-                for (int r = 0; r < RB; ++r) halves(cur.w[r][0], cur.w[r][1]);
+                for (int r = 0; r < RB; ++r) halves(cur.w[r][0], cur.w[r][H - 1]);
             }
 #pragma unroll
             for (int r = 0; r < RB; ++r) quarters<GROUP>(cur.w[r][h]);
 #pragma unroll
             for (int g = 0; g < 4 / PER; ++g) {
+                const int at = h * (4 / PER) + g;
                 v4i b[RB][PER];
                 float sv[RB], zv[RB];
 #pragma unroll
                 for (int r = 0; r < RB; ++r) {
 #pragma unroll
                     for (int i = 0; i < PER; ++i) b[r][i] = expand8_natural((uint32_t)cur.w[r][h][g * PER + i], magic);
-                    sv[r] = scale_value<SB>(cur.s[r][h * (4 / PER) + g], a.st);
-                    zv[r] = ZERO ? -128.0f - (float)cur.z[r][h * (4 / PER) + g] : -136.0f;
+                    sv[r] = scale_value<SB>(cur.s[r][at], a.st);
+                    zv[r] = -128.0f - (float)cur.z[r][at];
                 }
+                // the products of one token block, while the last one's are scaled
+                v4f acc[2][RB];
 #pragma unroll
-                for (int t = 0; t < TB; ++t) {
-                    v4i x[PER];
-                    v4f sum_x = {0.0f, 0.0f, 0.0f, 0.0f}, acc[RB];
+                for (int t = 0; t <= TB; ++t) {
+                    if (t < TB) {
+                        const v4f s = sums[par][at][t * 4 + q];
 #pragma unroll
-                    for (int i = 0; i < PER; ++i) {
-                        x[i] = lds[buf][place[g * PER + i] + 16 * h + 16 * t * PIECES];
-                        sum_x = mma(x[i], ones, sum_x);
+                        for (int r = 0; r < RB; ++r)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) acc[t & 1][r][i] = ZERO ? zv[r] * s[i] : s[i];
+#pragma unroll
+                        for (int i = 0; i < PER; ++i) {
+                            const v4i x = xs[place[g * PER + i] + 16 * h + 16 * t * PIECES];
+#pragma unroll
+                            for (int r = 0; r < RB; ++r) acc[t & 1][r] = mma(x, b[r][i], acc[t & 1][r]);
+                        }
                     }
+                    if (t > 0) {
 #pragma unroll
-                    for (int r = 0; r < RB; ++r) {
-                        acc[r] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+                        for (int r = 0; r < RB; ++r)
 #pragma unroll
-                        for (int i = 0; i < PER; ++i) acc[r] = mma(x[i], b[r][i], acc[r]);
+                            for (int i = 0; i < 4; ++i)
+                                total[r][t - 1][i] = fmaf(sv[r], acc[(t - 1) & 1][r][i], total[r][t - 1][i]);
                     }
-#pragma unroll
-                    for (int r = 0; r < RB; ++r)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            total[r][t][i] = fmaf(sv[r], fmaf(zv[r], sum_x[i], acc[r][i]), total[r][t][i]);
                 }
             }
         }
         cur = next;
+        buf = buf1;
+        par ^= 1;
     }
 
     // lane (n, q) holds tokens 4 q .. 4 q + 3 of row n
+    if (a.splits > 1) {
+        float *part = a.part + (int64_t)split * a.M * a.N;
+#pragma unroll
+        for (int t = 0; t < TB; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int m = m0 + 16 * t + 4 * q + i;
+#pragma unroll
+                for (int r = 0; r < RB; ++r)
+                    if (m < a.M && n0 + 16 * r + n < a.N)
+                        part[(int64_t)m * a.N + n0 + 16 * r + n] = total[r][t][i];
+            }
+        return;
+    }
     bool fine = true;
 #pragma unroll
     for (int t = 0; t < TB; ++t)
@@ -175,32 +245,32 @@ __global__ void __launch_bounds__(256) k_tile(Args a)
 }
 
 template <int TB, int RB, int KS, int GROUP, int SB, bool ZERO>
-hipError_t launch_tile_as(const Args &a, int experts, hipStream_t s)
+hipError_t launch_tile_as(const Args &a, hipStream_t s)
 {
-    constexpr int W = 4;
-    const dim3 grid((a.N + 16 * RB * W - 1) / (16 * RB * W), (a.M + 16 * TB - 1) / (16 * TB), experts);
-    hipLaunchKernelGGL((k_tile<TB, RB, KS, GROUP, SB, ZERO>), grid, dim3(64 * W), 0, s, a);
+    const int64_t gx8 = ((a.N + 64 * RB - 1) / (64 * RB) + 7) & ~7;
+    const int64_t grid = gx8 * row_tiles(a, 16 * TB) * a.splits;
+    if (grid > 0x7fffffff)
+        return hipErrorInvalidValue;
+    hipLaunchKernelGGL((k_tile<TB, RB, KS, GROUP, SB, ZERO>), dim3((unsigned)grid), dim3(64 * kTileWaves), 0, s, a);
     return hipGetLastError();
 }
 
 template <int GROUP, int SB, bool ZERO>
-hipError_t tile_pick(const Args &a, int experts, hipStream_t s)
+hipError_t tile_pick(const Args &a, hipStream_t s)
 {
-    if (a.M <= 16)
-        return launch_tile_as<1, 1, 256, GROUP, SB, ZERO>(a, experts, s);
-    if (a.M <= 32)
-        return launch_tile_as<2, 1, 256, GROUP, SB, ZERO>(a, experts, s);
-    if (a.M <= 64)
-        return launch_tile_as<4, 2, 256, GROUP, SB, ZERO>(a, experts, s);
-    return launch_tile_as<8, 4, 128, GROUP, SB, ZERO>(a, experts, s);
+    switch (pick_tile(a.experts ? a.rows / a.experts : a.M, a.N).tb) {
+    case 1: return launch_tile_as<1, 1, 256, GROUP, SB, ZERO>(a, s);
+    case 2: return launch_tile_as<2, 2, 256, GROUP, SB, ZERO>(a, s);
+    default: return launch_tile_as<4, 4, 128, GROUP, SB, ZERO>(a, s);
+    }
 }
 
 template <int GROUP>
-hipError_t tile_any(const Args &a, int experts, hipStream_t s)
+hipError_t tile_any(const Args &a, hipStream_t s)
 {
     if (a.st == QLIN_SCALE_F32)
-        return a.zero ? tile_pick<GROUP, 4, true>(a, experts, s) : tile_pick<GROUP, 4, false>(a, experts, s);
-    return a.zero ? tile_pick<GROUP, 2, true>(a, experts, s) : tile_pick<GROUP, 2, false>(a, experts, s);
+        return a.zero ? tile_pick<GROUP, 4, true>(a, s) : tile_pick<GROUP, 4, false>(a, s);
+    return a.zero ? tile_pick<GROUP, 2, true>(a, s) : tile_pick<GROUP, 2, false>(a, s);
 }
 
 }  // namespace w4

@@ -4,7 +4,7 @@
 namespace qlin {
 namespace w4 {
 
-hipError_t launch_tile_128(const Args &a, int experts, hipStream_t s) { return tile_any<128>(a, experts, s); }
+hipError_t launch_tile_128(const Args &a, hipStream_t s) { return tile_any<128>(a, s); }
 
 }  // namespace w4
 }  // namespace qlin

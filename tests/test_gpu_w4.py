@@ -177,7 +177,7 @@ def test_grouped_w4_offsets_stay_inside_the_buffers():
     sizes, N, K, group = [3, 4, 5], 32, 256, 64
     case = grouped_case(sizes, N, K, group, torch.float32, False, 9)
     x, codes, s, z, _ = case
-    off = np.array([-5, 3, 2, 100000], np.int32)
+    off = np.array([-5, 4, 2, 100000], np.int32)     # rows 2 and 3 are two experts': either's
     whole = torch.full((x.shape[0] + 64, N), 3.0, dtype=torch.bfloat16, device="cuda")
     say("bad offsets")
     q.grouped_w4_mm(dev(x), dev(ref.pack4(codes)), dev(s), dev(off), 64, out=whole[:x.shape[0]])
@@ -185,7 +185,7 @@ def test_grouped_w4_offsets_stay_inside_the_buffers():
     assert bool((whole[x.shape[0]:] == 3.0).all())
     y = whole[:x.shape[0]].cpu()
     ref.w4_check(y[0:2], ref.f64(x[0:2]), codes[0], ref.f64(s[0]), None, group, "expert 0")
-    ref.w4_check(y[2:], ref.f64(x[2:]), codes[2], ref.f64(s[2]), None, group, "expert 2")
+    ref.w4_check(y[4:], ref.f64(x[4:]), codes[2], ref.f64(s[2]), None, group, "expert 2")
 
 
 def test_grouped_w4_equals_single_product():

@@ -12,9 +12,9 @@ OK, NULL, SHAPE, STRIDE, ALIGN, WS, ARG = 0, 1, 2, 3, 4, 5, 9
 A, B, S, Z, Y, I, O, R, W = (0x10000 * k for k in range(1, 10))       # never dereferenced
 
 
-def w4(M=4, N=64, K=256, group=128, x=A, ldx=None, b=B, ldb=None, st=0, s=S, z=None, y=Y, ldy=None):
+def w4(M=4, N=64, K=256, group=128, x=A, ldx=None, b=B, ldb=None, st=0, s=S, z=None, y=Y, ldy=None, ws=None, n=0):
     return q.lib().qlin_w4_mm(M, N, K, group, x, K if ldx is None else ldx, b, K // 2 if ldb is None else ldb,
-                              st, s, z, y, N if ldy is None else ldy, None)
+                              st, s, z, y, N if ldy is None else ldy, ws, n, None)
 
 
 def test_w4_refusals():
@@ -25,6 +25,11 @@ def test_w4_refusals():
     assert w4(ldx=248) == STRIDE and w4(ldx=260) == STRIDE and w4(ldb=112) == STRIDE and w4(ldb=136) == STRIDE
     assert w4(ldy=63) == STRIDE
     assert w4(x=A + 8) == ALIGN and w4(b=B + 4) == ALIGN and w4(y=Y + 2) == ALIGN and w4(s=S + 2) == ALIGN
+    need = q.lib().qlin_w4_workspace_size(32, 512, 8192)
+    assert need > 0 and need % (32 * 512 * 4) == 0 and q.lib().qlin_w4_workspace_size(1, 512, 8192) == 0
+    assert q.lib().qlin_w4_workspace_size(-1, 512, 8192) == 0
+    assert w4(M=32, N=512, K=8192) == WS and w4(M=32, N=512, K=8192, ws=W, n=need - 1) == WS
+    assert w4(M=32, N=512, K=8192, ws=W + 8, n=need) == ALIGN
     assert w4(M=0, x=None, y=None) == OK and w4(N=0, b=None, s=None, y=None) == OK
 
 
