@@ -587,31 +587,39 @@ def grouped_block_scaled_mm(a_q, a_scale, b_q, b_scale, group_offsets, max_rows:
 _SCALE_TYPE = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 
 
-def _matrix(t: torch.Tensor, name: str, device=None) -> int:
-    """The row stride of a 2-D device tensor with contiguous rows (on `device`)."""
-    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
+# (the stream object alone takes 2 us to make, half a launch)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _matrix(t: torch.Tensor, name: str, device) -> int:
+    """The row stride of a 2-D tensor on `device` with contiguous rows."""
+    if t.dim() != 2:
         raise ValueError(f"{name} must be 2-D with contiguous rows")
-    if not t.is_cuda or (device is not None and t.device != device):
+    rows, cols = t.shape
+    ld, one = t.stride()
+    if one != 1 and cols > 1:
+        raise ValueError(f"{name} must be 2-D with contiguous rows")
+    if t.device != device or not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor, on one device with the others")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]      # a single row's stride says nothing
+    return ld if rows > 1 else cols                          # a single row's stride says nothing
 
 
-def _flat(t: torch.Tensor, dtype, shape, name: str, device) -> torch.Tensor:
-    """A contiguous tensor of one type and shape on `device`."""
+def _flat(t: torch.Tensor, dtype, shape, name: str, device):
+    """Checks a contiguous tensor of one type and shape on `device`."""
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous, on one device with the others")
-    return t
 
 
 def _rows_out(out, shape, dtype, device, name="out"):
     """(`out` or a new tensor of shape and dtype, its row stride)."""
     if out is None:
         return torch.empty(shape, dtype=dtype, device=device), shape[1]
-    if out.dtype != dtype or tuple(out.shape) != tuple(shape):
+    if out.dtype != dtype or out.shape != shape:
         raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)}")
     return out, _matrix(out, name, device)
 
@@ -619,25 +627,30 @@ def _rows_out(out, shape, dtype, device, name="out"):
 def _call_on(device, fn, args, what):
     """_call with `device`'s current stream as the last argument."""
     if device.index == torch.cuda.current_device():
-        _call(fn, args + [torch.cuda.current_stream(device).cuda_stream], what)
+        st = fn(*args, _raw_stream(device.index))
     else:
         with torch.cuda.device(device):
-            _call(fn, args + [torch.cuda.current_stream(device).cuda_stream], what)
+            st = fn(*args, _raw_stream(device.index))
+    if st != 0:
+        raise QlinError(st, what)
 
 
 def _w4_scales(b_scale, b_zero, lead, K, device):
     """(group, scale type, zero points' address) of 4-bit weights [*lead, K]."""
-    if b_scale.dim() != len(lead) + 1 or b_scale.shape[-1] == 0 or K % b_scale.shape[-1] or \
-            K // b_scale.shape[-1] not in (32, 64, 128):
+    st = _SCALE_TYPE.get(b_scale.dtype)
+    if st is None:
+        raise TypeError(f"b_scale must be float32, bfloat16 or float16, got {b_scale.dtype}")
+    cols = b_scale.shape[-1] if b_scale.dim() else 0
+    group = K // cols if cols else 0
+    if b_scale.dim() != len(lead) + 1 or group * cols != K or group not in (32, 64, 128):
         raise ValueError(f"b_scale must be [..., N, K/group] with a group of 32, 64 or 128, "
                          f"got {tuple(b_scale.shape)} for K = {K}")
-    if b_scale.dtype not in _SCALE_TYPE:
-        raise TypeError(f"b_scale must be float32, bfloat16 or float16, got {b_scale.dtype}")
-    shape = (*lead, b_scale.shape[-1])
+    shape = (*lead, cols)
     _flat(b_scale, b_scale.dtype, shape, "b_scale", device)
-    if b_zero is not None:
-        _flat(b_zero, torch.uint8, shape, "b_zero", device)
-    return K // b_scale.shape[-1], _SCALE_TYPE[b_scale.dtype], None if b_zero is None else b_zero.data_ptr()
+    if b_zero is None:
+        return group, st, None
+    _flat(b_zero, torch.uint8, shape, "b_zero", device)
+    return group, st, b_zero.data_ptr()
 
 
 def w4_mm(x, b_q, b_scale, b_zero=None, out=None):
@@ -651,17 +664,18 @@ def w4_mm(x, b_q, b_scale, b_zero=None, out=None):
     if b_q.dtype != torch.uint8:
         raise TypeError(f"b_q must be uint8, got {b_q.dtype}")
     dev = x.device
-    ldx, ldb = _matrix(x, "x"), _matrix(b_q, "b_q", dev)
+    ldx, ldb = _matrix(x, "x", dev), _matrix(b_q, "b_q", dev)
     M, K = x.shape
-    N = b_q.shape[0]
-    if b_q.shape[1] * 2 != K:
+    N, half = b_q.shape
+    if half * 2 != K:
         raise ValueError("x is [M,K] and b_q must be [N,K/2]")
     group, st, zero = _w4_scales(b_scale, b_zero, (N,), K, dev)
     out, ldy = _rows_out(out, (M, N), torch.bfloat16, dev)
     # the workspace is the call's own: see _sort_buffers
-    n = _lib().qlin_w4_workspace_size(M, N, K)
+    lib = _lib()
+    n = lib.qlin_w4_workspace_size(M, N, K)
     ws = torch.empty((n,), dtype=torch.uint8, device=dev) if n else None
-    _call_on(dev, _lib().qlin_w4_mm, [M, N, K, group, x.data_ptr(), ldx, b_q.data_ptr(), ldb, st,
+    _call_on(dev, lib.qlin_w4_mm, [M, N, K, group, x.data_ptr(), ldx, b_q.data_ptr(), ldb, st,
                                       b_scale.data_ptr(), zero, out.data_ptr(), ldy,
                                       None if ws is None else ws.data_ptr(), n], "qlin_w4_mm")
     return out
@@ -677,7 +691,7 @@ def grouped_w4_mm(x, b_q, b_scale, group_offsets, max_rows: int, b_zero=None, ou
     if b_q.dtype != torch.uint8:
         raise TypeError(f"b_q must be uint8, got {b_q.dtype}")
     dev = x.device
-    ldx = _matrix(x, "x")
+    ldx = _matrix(x, "x", dev)
     if b_q.dim() != 3 or b_q.stride(2) != 1 or b_q.device != dev:
         raise ValueError("b_q must be a [G,N,K/2] tensor with contiguous rows, on x's device")
     rows, K = x.shape
@@ -743,7 +757,7 @@ def moe_sort(topk_ids, experts: int):
 def _permute_args(x, T, scale, rows, out, out_scale):
     """The sorted rows' buffers (out, out_scale) and the call's row arguments."""
     dev = x.device
-    ldx = _matrix(x, "x")
+    ldx = _matrix(x, "x", dev)
     if x.shape[0] != T:
         raise ValueError(f"x has {x.shape[0]} rows for {T} tokens")
     K, es = x.shape[1], x.element_size()
@@ -804,7 +818,7 @@ def moe_combine(y, slot_row, weights, out=None):
     [T,K] of y's type (float32, bfloat16 or float16), fp32 sums in the order of
     j; weights float32 [T, topk].  Absent slots add nothing."""
     rt = _row_type(y, "y")
-    ldy = _matrix(y, "y")
+    ldy = _matrix(y, "y", y.device)
     T, topk = _slots(slot_row, y.device)
     _flat(weights, torch.float32, (T, topk), "weights", y.device)
     rows, K = y.shape
@@ -822,7 +836,7 @@ def moe_combine_backward(dout, y, slot_row, weights, dy=None):
     rt = _row_type(y, "y")
     if dout.dtype != y.dtype:
         raise TypeError("dout and y must have the same dtype")
-    ldy, ldo = _matrix(y, "y"), _matrix(dout, "dout", y.device)
+    ldy, ldo = _matrix(y, "y", y.device), _matrix(dout, "dout", y.device)
     T, topk = _slots(slot_row, y.device)
     _flat(weights, torch.float32, (T, topk), "weights", y.device)
     rows, K = y.shape
@@ -840,7 +854,7 @@ def moe_permute_backward(drows, slot_row, out=None):
     """Gradient of moe_permute: dx[t] = sum_j drows[slot_row[t,j]], [T,K] of
     drows' type, fp32 sums."""
     rt = _row_type(drows, "drows")
-    ld = _matrix(drows, "drows")
+    ld = _matrix(drows, "drows", drows.device)
     T, topk = _slots(slot_row, drows.device)
     rows, K = drows.shape
     out, ldo = _rows_out(out, (T, K), drows.dtype, drows.device)

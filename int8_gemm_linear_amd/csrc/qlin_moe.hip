@@ -212,17 +212,23 @@ hipError_t launch_sort_id(const SortArgs &a, int blocks, hipStream_t s)
     return hipGetLastError();
 }
 
-hipError_t launch_sort(int32_t id_bits, int64_t tokens, int64_t topk, int64_t experts, const void *ids,
-                       int32_t *offsets, int32_t *slot_row, void *ws, hipStream_t s)
+SortArgs sort_args(int64_t tokens, int64_t topk, int64_t experts, const void *ids, int32_t *offsets,
+                   int32_t *slot_row, void *ws, int blocks)
 {
     const int64_t n = tokens * topk;
-    const int blocks = sort_blocks(n);
     int64_t per = (n + blocks - 1) / blocks;
     per = (per + kSortThreads - 1) / kSortThreads * kSortThreads;
     int bits = 0;
     while (((int64_t)1 << bits) < experts) ++bits;
-    const SortArgs a{ids, offsets, slot_row, blocks > 1 ? static_cast<int32_t *>(ws) : nullptr, (int)n,
-                     (int)per, (int)experts, bits};
+    return SortArgs{ids, offsets, slot_row, blocks > 1 ? static_cast<int32_t *>(ws) : nullptr, (int)n,
+                    (int)per, (int)experts, bits};
+}
+
+hipError_t launch_sort(int32_t id_bits, int64_t tokens, int64_t topk, int64_t experts, const void *ids,
+                       int32_t *offsets, int32_t *slot_row, void *ws, hipStream_t s)
+{
+    const int blocks = sort_blocks(tokens * topk);
+    const SortArgs a = sort_args(tokens, topk, experts, ids, offsets, slot_row, ws, blocks);
     return id_bits == 64 ? launch_sort_id<int64_t>(a, blocks, s) : launch_sort_id<int32_t>(a, blocks, s);
 }
 
@@ -250,14 +256,10 @@ struct RowArgs {
     int lanes;
 };
 
-__global__ void __launch_bounds__(kRowThreads) k_moe_permute(RowArgs a)
+// Copies a token's row and scales to its slots' rows, as thread `lane` of its a.lanes.
+__device__ inline void copy_token(const RowArgs &a, int token, const int32_t *rows, int lane)
 {
-    const int token = blockIdx.x * (kRowThreads / a.lanes) + threadIdx.x / a.lanes;
-    const int lane = threadIdx.x & (a.lanes - 1);
-    if (token >= a.tokens)
-        return;
     const uint8_t *x = a.x + (int64_t)token * a.ldx;
-    const int32_t *rows = a.slot_row + (int64_t)token * a.topk;
     const int pieces = a.cols >> 4, tail = a.cols & 15;
     for (int p = lane; p < pieces; p += a.lanes) {
         v4i v;
@@ -284,6 +286,77 @@ __global__ void __launch_bounds__(kRowThreads) k_moe_permute(RowArgs a)
                 a.out_f[(int64_t)r * a.scale_cols + c] = s;
         }
     }
+}
+
+__global__ void __launch_bounds__(kRowThreads) k_moe_permute(RowArgs a)
+{
+    const int token = blockIdx.x * (kRowThreads / a.lanes) + threadIdx.x / a.lanes;
+    if (token < a.tokens)
+        copy_token(a, token, a.slot_row + (int64_t)token * a.topk, threadIdx.x & (a.lanes - 1));
+}
+
+// Sort and copy in one launch, for few slots: each workgroup counts for its
+// own slots who comes before them (the ids fit LDS; a wave takes a slot, its
+// lanes the ids), and then copies its tokens' rows; the last workgroup makes
+// the offsets.  16 tokens, top-8, 2 KB rows: one launch instead of two.
+constexpr int kFusedSlots = 1024;
+
+template <typename ID>
+__global__ void __launch_bounds__(kRowThreads) k_moe_dispatch(SortArgs s, RowArgs a)
+{
+    __shared__ int32_t expert[kFusedSlots], row[kFusedSlots];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    for (int i = tid; i < s.n; i += kRowThreads) expert[i] = expert_of(static_cast<const ID *>(s.ids), i, s.experts);
+    __syncthreads();
+    if (blockIdx.x == gridDim.x - 1) {
+        // offsets[e]: slots with a smaller expert
+        __shared__ int32_t hist[kMaxExperts], total[kRowThreads / 64];
+        for (int e = tid; e < s.experts; e += kRowThreads) hist[e] = 0;
+        __syncthreads();
+        for (int i = tid; i < s.n; i += kRowThreads)
+            if (expert[i] >= 0)
+                atomicAdd(&hist[expert[i]], 1);
+        __syncthreads();
+        const int each = (s.experts + kRowThreads - 1) / kRowThreads;
+        int sum = 0;
+        for (int e = tid * each; e < min((tid + 1) * each, s.experts); ++e) sum += hist[e];
+        int scan = sum;
+        for (int d = 1; d < 64; d <<= 1) {
+            const int v = __shfl_up(scan, d);
+            scan += lane >= d ? v : 0;
+        }
+        if (lane == 63)
+            total[wave] = scan;
+        __syncthreads();
+        int at = scan - sum;
+        for (int w = 0; w < wave; ++w) at += total[w];
+        for (int e = tid * each; e < min((tid + 1) * each, s.experts); ++e) {
+            s.offsets[e] = at;
+            at += hist[e];
+            if (e == s.experts - 1)
+                s.offsets[s.experts] = at;
+        }
+        return;
+    }
+    const int per = kRowThreads / a.lanes;                  // tokens of the workgroup
+    const int t0 = blockIdx.x * per, first = t0 * a.topk, last = min(first + per * a.topk, s.n);
+    for (int i = first + wave; i < last; i += kRowThreads / 64) {
+        const int e = expert[i];
+        int before = 0;
+        for (int j = lane; j < s.n; j += 64) {
+            const int f = expert[j];
+            before += f >= 0 && (f < e || (f == e && j < i)) ? 1 : 0;
+        }
+        before = wave_sum(before);
+        if (lane == 0) {
+            row[i - first] = e >= 0 ? before : -1;
+            s.slot_row[i] = e >= 0 ? before : -1;
+        }
+    }
+    __syncthreads();
+    const int token = t0 + tid / a.lanes;
+    if (token < a.tokens)
+        copy_token(a, token, row + tid / a.lanes * a.topk, tid & (a.lanes - 1));
 }
 
 template <typename T> struct Elem;
@@ -425,9 +498,9 @@ qlin_status check_permute(int64_t row_bytes, const void *X, int64_t ldx, const v
     return QLIN_OK;
 }
 
-hipError_t launch_permute(int64_t tokens, int64_t topk, int64_t rows, int64_t row_bytes, const void *X,
-                          int64_t ldx, const int32_t *slot_row, void *Out, int64_t ldo, const float *scale,
-                          int64_t scale_cols, float *out_scale, hipStream_t s)
+RowArgs permute_args(int64_t tokens, int64_t topk, int64_t rows, int64_t row_bytes, const void *X, int64_t ldx,
+                     const int32_t *slot_row, void *Out, int64_t ldo, const float *scale, int64_t scale_cols,
+                     float *out_scale)
 {
     RowArgs a{};
     a.x = static_cast<const uint8_t *>(X);
@@ -443,6 +516,11 @@ hipError_t launch_permute(int64_t tokens, int64_t topk, int64_t rows, int64_t ro
     a.cols = (int)row_bytes;
     a.scale_cols = (int)scale_cols;
     a.lanes = row_lanes(row_bytes);
+    return a;
+}
+
+hipError_t launch_permute(const RowArgs &a, hipStream_t s)
+{
     hipLaunchKernelGGL(k_moe_permute, row_grid(a), dim3(kRowThreads), 0, s, a);
     return hipGetLastError();
 }
@@ -540,9 +618,9 @@ qlin_status qlin_moe_permute(int64_t tokens, int64_t topk, int64_t rows, int64_t
         return QLIN_ERR_NULL_POINTER;
     if (!aligned(slot_row, 4))
         return QLIN_ERR_MISALIGNED;
-    return launch_permute(tokens, topk, rows, row_bytes, X, ldx, slot_row, Out, ldo, scale, scale_cols,
-                          out_scale, static_cast<hipStream_t>(stream)) == hipSuccess ? QLIN_OK
-                                                                                    : QLIN_ERR_HIP;
+    const RowArgs a = permute_args(tokens, topk, rows, row_bytes, X, ldx, slot_row, Out, ldo, scale, scale_cols,
+                                   out_scale);
+    return launch_permute(a, static_cast<hipStream_t>(stream)) == hipSuccess ? QLIN_OK : QLIN_ERR_HIP;
 }
 
 qlin_status qlin_moe_dispatch(int32_t id_bits, int64_t tokens, int64_t topk, int64_t experts,
@@ -565,13 +643,23 @@ qlin_status qlin_moe_dispatch(int32_t id_bits, int64_t tokens, int64_t topk, int
         return QLIN_ERR_BAD_SHAPE;
     }
     hipStream_t s = static_cast<hipStream_t>(stream);
+    const RowArgs a = permute_args(tokens, topk, rows, row_bytes, X, ldx, slot_row, Out, ldo, scale, scale_cols,
+                                   out_scale);
+    if (tokens > 0 && tokens * topk <= kFusedSlots) {
+        const SortArgs sa = sort_args(tokens, topk, experts, topk_ids, group_offsets, slot_row, nullptr, 1);
+        const dim3 grid(row_grid(a).x + 1);
+        if (id_bits == 64)
+            hipLaunchKernelGGL((k_moe_dispatch<int64_t>), grid, dim3(kRowThreads), 0, s, sa, a);
+        else
+            hipLaunchKernelGGL((k_moe_dispatch<int32_t>), grid, dim3(kRowThreads), 0, s, sa, a);
+        return hipGetLastError() == hipSuccess ? QLIN_OK : QLIN_ERR_HIP;
+    }
     if (launch_sort(id_bits, tokens, topk, experts, topk_ids, group_offsets, slot_row, workspace, s) !=
         hipSuccess)
         return QLIN_ERR_HIP;
     if (tokens == 0)
         return QLIN_OK;
-    return launch_permute(tokens, topk, rows, row_bytes, X, ldx, slot_row, Out, ldo, scale, scale_cols,
-                          out_scale, s) == hipSuccess ? QLIN_OK : QLIN_ERR_HIP;
+    return launch_permute(a, s) == hipSuccess ? QLIN_OK : QLIN_ERR_HIP;
 }
 
 qlin_status qlin_moe_combine(qlin_row_type rt, int64_t tokens, int64_t topk, int64_t rows, int64_t K,

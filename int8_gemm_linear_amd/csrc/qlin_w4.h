@@ -40,6 +40,7 @@ struct Args {
     int experts;                  // 0 without experts
     int N, K, G;                  // G = K / group
     int st;                       // qlin_scale_type
+    int tiles;                    // tile kernel: token tiles of the grid
     int splits;                   // parts of K, summed by a second kernel
     int split_k;                  // codes of a part
     float *part;                  // [splits][M][N] sums of the parts
@@ -158,6 +159,15 @@ __device__ inline v4f mma(v4i a, v4i b, v4f c)
 {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, a), __builtin_bit_cast(v8bf, b), c,
                                                    0, 0, 0);
+}
+
+// All of the wave's loads and LDS copies have arrived (vmcnt 0), in a form
+// that the compiler counts too: its own waits would otherwise still expect
+// the loads before it, and wait for copies issued since.
+__device__ inline void wait_loads()
+{
+    __builtin_amdgcn_s_waitcnt(0x0f70);
+    asm volatile("" ::: "memory");
 }
 
 // A scale from its 16 or 32 bits.

@@ -89,10 +89,10 @@ struct Slot {
     }
 };
 
-// 16-byte pieces from one token's values of k codes to the next's: four more
-// than they take, so that a read of 8 tokens x 8 pieces meets every bank
-// equally often.
-__host__ __device__ inline int token_pitch(int k) { return k / 8 + 4; }
+// 16-byte pieces from one token's values of k codes to the next's: one more
+// than they take, so that the 8 tokens that read one piece meet different
+// banks.
+__host__ __device__ inline int token_pitch(int k) { return k / 8 + 1; }
 
 // Tokens' values of codes c0 .. to LDS, in operand order: piece 4 j + q of a
 // step of 128 holds k_of(j, q).  T x P loads of a thread are in flight at
@@ -246,7 +246,7 @@ hipError_t launch_stream_as(const Args &a, int waves, int lds_bytes, hipStream_t
         return hipErrorInvalidValue;
     const int slots = (a.K + kSlot - 1) / kSlot;
     const int tokens = min(a.M, kStreamTokens);
-    const int fits = (lds_bytes / (16 * tokens) - 4) * 8;               // codes of K whose tokens fit
+    const int fits = (lds_bytes / (16 * tokens) - 1) * 8;               // codes of K whose tokens fit
     waves = min(waves, min(slots, fits / (AHEAD * kSlot)));
     const int round = AHEAD * waves * kSlot;
     const int kc = min(fits / round, (a.K + round - 1) / round) * round;

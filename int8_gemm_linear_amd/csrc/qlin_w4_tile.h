@@ -27,7 +27,7 @@ template <int RB, int KS, int GROUP, int SB, bool ZERO>
 struct Codes {
     static constexpr int H = KS / 128, NG = KS / GROUP;
     v4i w[RB][H];
-    uint32_t s[RB][NG], z[RB][NG];
+    uint32_t s[RB][(SB * NG + 3) / 4], z[RB][(NG + 3) / 4];
 
     __device__ inline void load(const Args &a, const uint8_t *const (*wrow)[H], const uint8_t *const *srow,
                                 const uint8_t *const *zrow, int k0, int n, int q)
@@ -39,32 +39,66 @@ struct Codes {
 #pragma unroll
             for (int h = 0; h < H; ++h) w[r][h] = ld16(wrow[r][h] + at);
         const int g0 = k0 / GROUP;
+        if (k0 + KS <= a.K) {
+#pragma unroll
+            for (int r = 0; r < RB; ++r) {
+                __builtin_memcpy(s[r], srow[r] + SB * g0, SB * NG);
+                if (ZERO)
+                    __builtin_memcpy(z[r], zrow[r] + g0, NG);
+            }
+            return;
+        }
 #pragma unroll
         for (int r = 0; r < RB; ++r)
 #pragma unroll
             for (int i = 0; i < NG; ++i) {
                 const int g = min(g0 + i, a.G - 1);
-                s[r][i] = SB == 4 ? reinterpret_cast<const uint32_t *>(srow[r])[g]
-                                  : reinterpret_cast<const uint16_t *>(srow[r])[g];
-                z[r][i] = ZERO ? zrow[r][g] : 8;
+                __builtin_memcpy(reinterpret_cast<uint8_t *>(s[r]) + SB * i, srow[r] + SB * g, SB);
+                if (ZERO)
+                    reinterpret_cast<uint8_t *>(z[r])[i] = zrow[r][g];
             }
+    }
+
+    __device__ inline float scale(int r, int i, int st) const
+    {
+        return scale_value<SB>(SB == 4 ? s[r][i] : (s[r][i / 2] >> (16 * (i & 1))) & 0xffffu, st);
+    }
+
+    // -(128 + z)
+    __device__ inline float bias(int r, int i) const
+    {
+        return -128.0f - (float)((z[r][i / 4] >> (8 * (i & 3))) & 0xffu);
     }
 };
 
+// A grid of gx weight tiles by `tiles` token tiles: weight tiles per XCD, token
+// tiles per block and blocks.
+struct Blocks {
+    int across, high, blocks;
+};
+__host__ __device__ inline Blocks tile_blocks(int gx, int tiles)
+{
+    const int blocks = (tiles + 7) / 8;
+    return Blocks{(gx + 7) / 8, (tiles + blocks - 1) / blocks, blocks};
+}
+
 template <int TB, int RB, int KS, int GROUP, int SB, bool ZERO>
-__global__ void __launch_bounds__(64 * kTileWaves) k_tile(Args a)
+__global__ void __launch_bounds__(64 * kTileWaves, 2) k_tile(Args a)
 {
     constexpr int H = KS / 128, PIECES = KS / 8, PER = GROUP / 32, NG = KS / GROUP;
     constexpr int COPIES = 16 * TB * PIECES / 64;           // 1 KB each
-    // id = 8 (y + tiles * (nx / 8)) + nx mod 8 (+ the split's share of the
-    // grid): workgroups go to the 8 XCDs in turn, so the token tiles of a
-    // weight tile meet in one L2
-    const int gx = (a.N + 64 * RB - 1) / (64 * RB), gx8 = (gx + 7) & ~7;
-    const int per = gridDim.x / a.splits, tiles = per / gx8;
-    const int split = blockIdx.x / per, id = blockIdx.x % per;
-    const int nx = id / (8 * tiles) * 8 + (id & 7);
+    // Workgroups go to the 8 XCDs in turn, so id mod 8 names the L2: each takes
+    // every 8th weight tile, and walks them in blocks of up to 8 token tiles,
+    // so that what runs at once shares both its weights and its tokens there
+    // (2048 tokens on 10240 x 5120: 287 us against 305 us with all token
+    // tiles of a weight tile in a row).
+    const int gx = (a.N + 64 * RB - 1) / (64 * RB);
+    const int per = gridDim.x / a.splits, split = blockIdx.x / per, id = blockIdx.x % per;
+    const Blocks bl = tile_blocks(gx, a.tiles);
+    const int j = id >> 3, y = j / (bl.across * bl.high) * bl.high + j % bl.high;
+    const int nx = j % (bl.across * bl.high) / bl.high * 8 + (id & 7);
     int m0;
-    if (nx >= gx || !enter_tile<16 * TB>(a, (id >> 3) % tiles, m0))
+    if (nx >= gx || y >= a.tiles || !enter_tile<16 * TB>(a, y, m0))
         return;
     __shared__ v4i lds[3][16 * TB * PIECES];
     __shared__ v4f sums[2][NG][TB * 4];             // [group][token / 4], times -136 without zero points
@@ -90,25 +124,31 @@ __global__ void __launch_bounds__(64 * kTileWaves) k_tile(Args a)
 #pragma unroll
         for (int t = 0; t < TB; ++t) total[r][t] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 
-    // place p of token t holds the step's piece p with its bits 2 and 3
-    // exchanged by t: a read of 16 tokens x 4 pieces meets every bank equally.
-    // A wave's copies are 4 KB apart: the lane's place in them is one
+    // Place p of token t holds the values of codes 8 (p xor t mod 16) .. of its
+    // step: the 16 tokens that read one piece meet 16 different places of the
+    // 256 bytes in which the banks repeat, and four lanes of a copy still read
+    // 64 bytes side by side.  A wave's copies are 4 KB apart: the lane's place in
+    // them is one.
     const int copy_t = (wave * 64 + lane) / PIECES, copy_p = lane % PIECES;
-    const int copy_k = 128 * (copy_p >> 4) + k_of<GROUP>(((copy_p >> 2) & 3) ^ (copy_t & 3), copy_p & 3);
+    const int copy_piece = (copy_p ^ copy_t) & 15;
+    static_assert(256 / PIECES % 16 == 0 || 256 / PIECES == 8, "tokens of a wave's copies");
     auto stage = [&](int k0, int buf) {
 #pragma unroll
         for (int i = 0; i < COPIES / kTileWaves; ++i) {
             const int t = min(m0 + copy_t + i * (256 / PIECES), a.M - 1);
+            // eight tokens on: bit 3 of the exchange alternates
+            const int piece = 256 / PIECES == 8 ? copy_piece ^ (8 * (i & 1)) : copy_piece;
+            const int k = k0 + 128 * (copy_p >> 4) + 8 * piece;
             v4i *to = &lds[buf][(i * kTileWaves + wave) * 64];
-            if (k0 + copy_k < kend)
-                lds_dma16(a.x + (int64_t)t * a.ldx + k0 + copy_k, to);
+            if (k < kend)
+                lds_dma16(a.x + (int64_t)t * a.ldx + k, to);
             else
                 to[lane] = zero4i();
         }
     };
     int place[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) place[j] = n * PIECES + 4 * (j ^ (n & 3)) + q;
+    for (int j = 0; j < 4; ++j) place[j] = n * PIECES + ((k_of<GROUP>(j, q) / 8) ^ n);
 
     const v4i ones = {0x3f803f80, 0x3f803f80, 0x3f803f80, 0x3f803f80};
     auto sum = [&](int buf, int to) {
@@ -137,14 +177,14 @@ __global__ void __launch_bounds__(64 * kTileWaves) k_tile(Args a)
     if (kbeg + KS < kend)
         stage(kbeg + KS, 1);
     cur.load(a, wrow, srow, zrow, kbeg, n, q);
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    wait_loads();
     __syncthreads();
     sum(0, 0);
     int buf = 0, par = 0;
     for (int k0 = kbeg; k0 < kend; k0 += KS) {
         const int buf1 = buf == 2 ? 0 : buf + 1, buf2 = buf1 == 2 ? 0 : buf1 + 1;
         // the next stage's tokens have landed; this stage's sums are there; the last stage's buffer is free
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        wait_loads();
         __syncthreads();
         if (k0 + 2 * KS < kend)
             stage(k0 + 2 * KS, buf2);
@@ -169,25 +209,32 @@ __global__ void __launch_bounds__(64 * kTileWaves) k_tile(Args a)
                 for (int r = 0; r < RB; ++r) {
 #pragma unroll
                     for (int i = 0; i < PER; ++i) b[r][i] = expand8_natural((uint32_t)cur.w[r][h][g * PER + i], magic);
-                    sv[r] = scale_value<SB>(cur.s[r][at], a.st);
-                    zv[r] = -128.0f - (float)cur.z[r][at];
+                    sv[r] = cur.scale(r, at, a.st);
+                    zv[r] = ZERO ? cur.bias(r, at) : 0.0f;
                 }
-                // the products of one token block, while the last one's are scaled
-                v4f acc[2][RB];
+                // The products of a token block, while the operands of the
+                // next come from LDS and the sums of the last are scaled.
+                v4f acc[2][RB], s[2];
+                v4i x[2][PER];
+                auto fetch = [&](int t) {
+                    s[t & 1] = sums[par][at][t * 4 + q];
+#pragma unroll
+                    for (int i = 0; i < PER; ++i) x[t & 1][i] = xs[place[g * PER + i] + 16 * h + 16 * t * PIECES];
+                };
+                fetch(0);
 #pragma unroll
                 for (int t = 0; t <= TB; ++t) {
+                    if (t + 1 < TB)
+                        fetch(t + 1);
                     if (t < TB) {
-                        const v4f s = sums[par][at][t * 4 + q];
 #pragma unroll
                         for (int r = 0; r < RB; ++r)
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) acc[t & 1][r][i] = ZERO ? zv[r] * s[i] : s[i];
+                            for (int i = 0; i < 4; ++i) acc[t & 1][r][i] = ZERO ? zv[r] * s[t & 1][i] : s[t & 1][i];
 #pragma unroll
-                        for (int i = 0; i < PER; ++i) {
-                            const v4i x = xs[place[g * PER + i] + 16 * h + 16 * t * PIECES];
+                        for (int i = 0; i < PER; ++i)
 #pragma unroll
-                            for (int r = 0; r < RB; ++r) acc[t & 1][r] = mma(x, b[r][i], acc[t & 1][r]);
-                        }
+                            for (int r = 0; r < RB; ++r) acc[t & 1][r] = mma(x[t & 1][i], b[r][i], acc[t & 1][r]);
                     }
                     if (t > 0) {
 #pragma unroll
@@ -196,6 +243,7 @@ __global__ void __launch_bounds__(64 * kTileWaves) k_tile(Args a)
                             for (int i = 0; i < 4; ++i)
                                 total[r][t - 1][i] = fmaf(sv[r], acc[(t - 1) & 1][r][i], total[r][t - 1][i]);
                     }
+                    __builtin_amdgcn_sched_barrier(0);
                 }
             }
         }
@@ -245,10 +293,14 @@ __global__ void __launch_bounds__(64 * kTileWaves) k_tile(Args a)
 }
 
 template <int TB, int RB, int KS, int GROUP, int SB, bool ZERO>
-hipError_t launch_tile_as(const Args &a, hipStream_t s)
+hipError_t launch_tile_as(Args a, hipStream_t s)
 {
-    const int64_t gx8 = ((a.N + 64 * RB - 1) / (64 * RB) + 7) & ~7;
-    const int64_t grid = gx8 * row_tiles(a, 16 * TB) * a.splits;
+    const int64_t tiles = row_tiles(a, 16 * TB);
+    if (tiles > 0x7fffffff / 8)
+        return hipErrorInvalidValue;
+    a.tiles = (int)tiles;
+    const Blocks bl = tile_blocks((a.N + 64 * RB - 1) / (64 * RB), a.tiles);
+    const int64_t grid = (int64_t)8 * bl.across * bl.high * bl.blocks * a.splits;
     if (grid > 0x7fffffff)
         return hipErrorInvalidValue;
     hipLaunchKernelGGL((k_tile<TB, RB, KS, GROUP, SB, ZERO>), dim3((unsigned)grid), dim3(64 * kTileWaves), 0, s, a);
