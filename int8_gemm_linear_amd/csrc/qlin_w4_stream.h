@@ -2,23 +2,27 @@
 // registers, and everything else hides behind them.
 //
 // A workgroup owns 8 U weight rows and all tokens; its waves share K in slots
-// of 256 codes (one 128-byte line of each row), slot i going to wave i mod W,
-// so that the workgroup reads whole row segments.  A load takes the whole
-// lines of 8 rows, 16 bytes a lane (reading half lines of 16 rows instead
-// costs a quarter of the bandwidth: 131 MB in 28 us against 21 us), and feeds
-// the matrix cores as it comes: lane (n, q) holds the 16 bytes q of row n mod
-// 8's first half line for n < 8, of its second for n >= 8.  So columns 0..7
-// of a product are 8 rows over the slot's first 128 codes, columns 8..15 the
-// same rows over the other 128; the token operand has the 8 tokens' first
-// 128 values in rows 0..7 and the other 128 in rows 8..15.  The two diagonal
-// 8 x 8 blocks are wanted, the other two are not looked at.
+// of 256 codes (one 128-byte line of each row), slot i going to wave i mod W.
 //
-// A wave keeps the codes and scales of AHEAD slots in flight and nothing
-// else: loads return in order, so a load of tokens issued between them would
-// wait for all of them.  The tokens come from LDS, where the workgroup puts
-// them, in the order of the matrix instructions' operands, for as much of K
-// as fits at once.  The waves' sums meet in LDS and are added in wave order:
-// no second launch, no workspace, and the same bits every time.
+// Loads go by the cache, products by the matrix cores, and a permutation of
+// the lanes lies between.  The L1 takes one access for each 64 bytes that
+// four lanes in a row ask for together, and 64 accesses for lanes that each
+// ask elsewhere; with loads in the order of the matrix operands those accesses
+// alone took 34 us for 131 MB.  So lane l loads 16 bytes l mod 8 of row l / 8
+// (of 8 weight rows, or of 8 tokens), and one scale load covers 32 rows x the
+// slot's two halves.  Afterwards lane (n, q) takes from lane 8 (n mod 8) +
+// 4 (n / 8) + q: the 16 bytes q of row n mod 8's first half line for n < 8,
+// of its second for n >= 8.  Columns 0..7 of a product are then 8 rows over
+// the slot's first 128 codes, columns 8..15 the same rows over the other 128,
+// and the token operand has the 8 tokens' first 128 values in rows 0..7 and
+// the other 128 in rows 8..15.  The two diagonal 8 x 8 blocks are wanted, the
+// other two are not looked at.
+//
+// A wave keeps AHEAD slots in flight, each with its codes, scales and token
+// operands, all in registers: loads return in order, so they arrive together
+// and nothing waits for more than it needs.  The waves' sums meet in LDS and
+// are added in wave order: no second launch, no workspace, and the same bits
+// every time.
 #pragma once
 
 #include "qlin_w4.h"
@@ -28,198 +32,180 @@ namespace w4 {
 
 constexpr int kSlot = 256;
 constexpr int kStreamWaves = 8;
-constexpr int kStreamLds = 64 * 1024;       // tokens in LDS at once: two workgroups of a CU
 
-// The codes, scales and zero points of a slot.  EVEN: K % 128 == 0.
+__device__ inline uint32_t from_lane(int lane, uint32_t v)
+{
+    return (uint32_t)__builtin_amdgcn_ds_bpermute(4 * lane, (int)v);
+}
+
+__device__ inline v4i from_lane(int lane, v4i v)
+{
+    v4i r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = (int)from_lane(lane, (uint32_t)v[i]);
+    return r;
+}
+
+// A slot's codes, scales, zero points and token operands, as loaded.  EVEN: K
+// % 128 == 0.
 template <int U, int GROUP, int SB, bool ZERO, bool EVEN>
 struct Slot {
-    static constexpr int NG = 128 / GROUP;          // a lane's groups
-    static constexpr int SW = (NG * SB + 3) / 4;    // dwords of its scales
-    v4i w[U];
-    uint32_t s[U][SW];
-    uint32_t z[U];
+    static constexpr int NG = 128 / GROUP;          // groups of a half
+    static constexpr int SW = (NG * SB + 3) / 4;    // dwords of their scales
+    static constexpr int SL = (U + 3) / 4;          // scale loads: 32 rows each
+    v4i w[U], x[4];
+    uint32_t s[SL][SW], z[SL];
 
-    // k0: the lane's first code (its row's half line)
     __device__ inline void load(const Args &a, const uint8_t *const *wrow, const uint8_t *const *srow,
-                                const uint8_t *const *zrow, int k0, int q)
+                                const uint8_t *const *zrow, const uint16_t *xrow, int k0, int lane)
     {
-        // past the end of K the tokens are zeros and any codes do
-        const int at = min(k0 + 32 * q, a.K - 32) / 2;
+        const int seg = lane & 7;
+        // past the end of K the tokens are made zeros and any codes do
+        const int at = min(k0 + 32 * seg, a.K - 32) / 2;
 #pragma unroll
         for (int u = 0; u < U; ++u) w[u] = ld_nt(wrow[u] + at);
-        const int g0 = min(k0, EVEN ? a.K - 128 : a.K - 32) / GROUP;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (NG == 1) {
-                s[u][0] = SB == 4 ? reinterpret_cast<const uint32_t *>(srow[u])[g0]
-                                  : reinterpret_cast<const uint16_t *>(srow[u])[g0];
-                z[u] = ZERO ? zrow[u][g0] : 0;
-            } else if (EVEN) {
-                __builtin_memcpy(s[u], srow[u] + SB * g0, NG * SB);
-                z[u] = 0;
+        for (int j = 0; j < 4; ++j)
+            x[j] = ld16(reinterpret_cast<const uint8_t *>(
+                xrow + min(k0 + 128 * (seg >> 2) + 32 * j + 8 * (seg & 3), a.K - 8)));
+        const int g0 = min(k0 + 128 * (lane & 1), EVEN ? a.K - 128 : a.K - 32) / GROUP;
+#pragma unroll
+        for (int l = 0; l < SL; ++l) {
+            z[l] = 0;
+            s[l][0] = 0;
+            if (EVEN) {
+                __builtin_memcpy(s[l], srow[l] + SB * g0, NG * SB);
                 if (ZERO)
-                    __builtin_memcpy(&z[u], zrow[u] + g0, NG);
+                    __builtin_memcpy(&z[l], zrow[l] + g0, NG);
             } else {
 #pragma unroll
-                for (int i = 0; i < SW; ++i) s[u][i] = 0;
-                z[u] = 0;
+                for (int i = 1; i < SW; ++i) s[l][i] = 0;
 #pragma unroll
                 for (int i = 0; i < NG; ++i) {
                     const int g = min(g0 + i, a.G - 1);
                     if (SB == 4)
-                        s[u][i] = reinterpret_cast<const uint32_t *>(srow[u])[g];
+                        s[l][i] = reinterpret_cast<const uint32_t *>(srow[l])[g];
                     else
-                        s[u][i / 2] |= (uint32_t)reinterpret_cast<const uint16_t *>(srow[u])[g] << (16 * (i & 1));
+                        s[l][i / 2] |= (uint32_t)reinterpret_cast<const uint16_t *>(srow[l])[g] << (16 * (i & 1));
                     if (ZERO)
-                        z[u] |= (uint32_t)zrow[u][g] << (8 * i);
+                        z[l] |= (uint32_t)zrow[l][g] << (8 * i);
                 }
             }
         }
     }
-
-    __device__ inline float scale(int u, int i, int st) const
-    {
-        return scale_value<SB>(SB == 4 ? s[u][i] : NG == 1 ? s[u][0] : (s[u][i / 2] >> (16 * (i & 1))) & 0xffffu, st);
-    }
-
-    // -(128 + z)
-    __device__ inline float bias(int u, int i) const
-    {
-        return ZERO ? -128.0f - (float)((z[u] >> (8 * i)) & 0xffu) : -136.0f;
-    }
 };
 
-// 16-byte pieces from one token's values of k codes to the next's: one more
-// than they take, so that the 8 tokens that read one piece meet different
-// banks.
-__host__ __device__ inline int token_pitch(int k) { return k / 8 + 1; }
-
-// Tokens' values of codes c0 .. to LDS, in operand order: piece 4 j + q of a
-// step of 128 holds k_of(j, q).  T x P loads of a thread are in flight at
-// once: a load from L2 takes as long as one of the weights.
-template <int GROUP, int T, int P>
-__device__ inline void stage_tokens(v4i *lds, int pitch, const uint16_t *x, int64_t ldx, int tokens, int c0, int K,
-                                    int pieces)
+// total += the slot's products; `partial` where the slot passes the end of K.
+// An instruction takes 32 codes in a row, which keeps the token loads in whole
+// pieces of 64 bytes, whatever the group.
+template <int U, int GROUP, int SB, bool ZERO, bool EVEN>
+__device__ inline void add_slot(v4f *total, const Slot<U, GROUP, SB, ZERO, EVEN> &slot, int k0, bool partial,
+                                const Args &a, int lane, uint32_t magic)
 {
-    for (int p0 = threadIdx.x; p0 < pieces; p0 += P * blockDim.x) {
-        v4i v[P][T];
-#pragma unroll
-        for (int i = 0; i < P; ++i)
-#pragma unroll
-            for (int t = 0; t < T; ++t) {
-                const int k = c0 + 8 * (p0 + i * (int)blockDim.x);
-                v[i][t] = ld16(reinterpret_cast<const uint8_t *>(x + min(t, tokens - 1) * ldx + min(k, K - 8)));
-            }
-#pragma unroll
-        for (int i = 0; i < P; ++i)
-#pragma unroll
-            for (int t = 0; t < T; ++t) {
-                const int p = p0 + i * (int)blockDim.x;
-                if (t < tokens && p < pieces)
-                    lds[t * pitch + (p & ~15) + piece_of<GROUP>(p)] = c0 + 8 * p < K ? operand_order(v[i][t]) : zero4i();
-            }
-    }
-}
-
-// total += the slot's products with the tokens; x: the lane's token pieces.
-template <int U, int GROUP, typename S>
-__device__ inline void add_slot(v4f *total, S &slot, const v4i *x, int st, uint32_t magic)
-{
+    typedef Slot<U, GROUP, SB, ZERO, EVEN> S;
     constexpr int PER = GROUP / 32;                 // matrix instructions of a group
     const v4i ones = {0x3f803f80, 0x3f803f80, 0x3f803f80, 0x3f803f80};
+    const int n = lane & 15, q = lane >> 4;
+    const int from = 8 * (n & 7) + 4 * (n >> 3) + q, from_s = 2 * (n & 7) + (n >> 3);
+    v4i x[4], w[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) quarters<GROUP>(slot.w[u]);
+    for (int j = 0; j < 4; ++j) {
+        x[j] = from_lane(from, slot.x[j]);
+        if (partial && k0 + 128 * (n >> 3) + 32 * j + 8 * q >= a.K)
+            x[j] = zero4i();
+        x[j] = operand_order(x[j]);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        w[u] = from_lane(from, slot.w[u]);
+        quarters<32>(w[u]);
+    }
+    v4f sum_x[4 / PER];
 #pragma unroll
     for (int g = 0; g < 4 / PER; ++g) {
-        v4i xv[PER];
-        v4f sum_x = {0.0f, 0.0f, 0.0f, 0.0f};
+        sum_x[g] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            xv[i] = x[4 * (g * PER + i)];
-            sum_x = mma(xv[i], ones, sum_x);
-        }
+        for (int i = 0; i < PER; ++i) sum_x[g] = mma(x[g * PER + i], ones, sum_x[g]);
+    }
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
+    for (int u = 0; u < U; ++u) {
+        uint32_t s[S::SW], z = 0;
+#pragma unroll
+        for (int i = 0; i < S::SW; ++i) s[i] = from_lane(from_s + 16 * (u & 3), slot.s[u / 4][i]);
+        if (ZERO)
+            z = from_lane(from_s + 16 * (u & 3), slot.z[u / 4]);
+#pragma unroll
+        for (int g = 0; g < 4 / PER; ++g) {
             v4f acc = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-            for (int i = 0; i < PER; ++i) acc = mma(xv[i], expand8((uint32_t)slot.w[u][g * PER + i], magic), acc);
-            const float sv = slot.scale(u, g, st), zv = slot.bias(u, g);
+            for (int i = 0; i < PER; ++i)
+                acc = mma(x[g * PER + i], expand8((uint32_t)w[u][g * PER + i], magic), acc);
+            const float sv = scale_value<SB>(SB == 4 ? s[g] : S::NG == 1 ? s[0] & 0xffffu
+                                                            : (s[g / 2] >> (16 * (g & 1))) & 0xffffu, a.st);
+            const float zv = ZERO ? -128.0f - (float)((z >> (8 * g)) & 0xffu) : -136.0f;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) total[u][i] = fmaf(sv, fmaf(zv, sum_x[i], acc[i]), total[u][i]);
+            for (int i = 0; i < 4; ++i) total[u][i] = fmaf(sv, fmaf(zv, sum_x[g][i], acc[i]), total[u][i]);
         }
     }
 }
 
 template <int U, int AHEAD, int GROUP, int SB, bool ZERO, bool EVEN>
-__global__ void __launch_bounds__(64 * kStreamWaves) k_stream(Args a, int kc)
+__global__ void __launch_bounds__(64 * kStreamWaves) k_stream(Args a)
 {
     const int gx = (a.N + 8 * U - 1) / (8 * U);
     int m0;
     if (!enter_tile<kStreamTokens>(a, blockIdx.x / gx, m0))
         return;
-    extern __shared__ v4i lds[];
+    extern __shared__ float part[];                 // [wave][half][u][token][row]
     const int lane = threadIdx.x & 63, waves = blockDim.x >> 6;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int n = lane & 15, q = lane >> 4;
     const int n0 = (int)(blockIdx.x % gx) * 8 * U;
     const int tokens = min(a.M - m0, kStreamTokens);
-    const int pitch = token_pitch(min(kc, (a.K + kSlot - 1) / kSlot * kSlot));
-    const uint8_t *wrow[U], *srow[U], *zrow[U];
+    constexpr int SL = (U + 3) / 4;
+    // the rows of absent tokens compute what nobody reads
+    const uint16_t *xrow = a.x + (int64_t)(m0 + min(lane >> 3, tokens - 1)) * a.ldx;
+    const uint8_t *wrow[U], *srow[SL], *zrow[SL];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const int64_t row = min(n0 + 8 * u + (n & 7), a.N - 1);
-        wrow[u] = a.b + row * a.ldb;
-        srow[u] = a.scale + row * a.G * SB;
-        zrow[u] = ZERO ? a.zero + row * a.G : nullptr;
+    for (int u = 0; u < U; ++u) wrow[u] = a.b + (int64_t)min(n0 + 8 * u + (lane >> 3), a.N - 1) * a.ldb;
+#pragma unroll
+    for (int l = 0; l < SL; ++l) {
+        const int64_t row = min(n0 + 32 * l + min(lane >> 1, 8 * U - 1), a.N - 1);
+        srow[l] = a.scale + row * a.G * SB;
+        zrow[l] = ZERO ? a.zero + row * a.G : nullptr;
     }
     v4f total[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) total[u] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 
     const uint32_t magic = expand_magic();
-    const int stride = waves * kSlot, half = 128 * (n >> 3);
+    const int stride = waves * kSlot;
     Slot<U, GROUP, SB, ZERO, EVEN> slot[AHEAD];
     int k0 = wave * kSlot;
 #pragma unroll
-    for (int d = 0; d < AHEAD; ++d) slot[d].load(a, wrow, srow, zrow, k0 + d * stride + half, q);
-
-    // operand row n: token n mod 8, the slot's half n / 8; the rows of absent tokens compute what nobody reads
-    const v4i *mine = lds + min(n & 7, tokens - 1) * pitch + (half >> 3) + q;
-    for (int c0 = 0; c0 < a.K; c0 += kc) {          // kc: a multiple of AHEAD * stride
-        __syncthreads();
-        // piece 4 j + q of a step of 128 holds k_of(j, q)
-        const int pieces = (min(kc, a.K - c0) + kSlot - 1) / kSlot * (kSlot / 8);
-        if (tokens <= 2)
-            stage_tokens<GROUP, 2, 4>(lds, pitch, a.x + (int64_t)m0 * a.ldx, a.ldx, tokens, c0, a.K, pieces);
-        else
-            stage_tokens<GROUP, 8, 1>(lds, pitch, a.x + (int64_t)m0 * a.ldx, a.ldx, tokens, c0, a.K, pieces);
-        __syncthreads();
-        const int end = min(c0 + kc, a.K);
-        const int left = end > k0 ? (end - k0 + stride - 1) / stride : 0;      // the wave's slots of the chunk
-        for (int i = 0; i < left / AHEAD; ++i) {
+    for (int d = 0; d < AHEAD; ++d) slot[d].load(a, wrow, srow, zrow, xrow, k0 + d * stride, lane);
+    __builtin_amdgcn_sched_barrier(0);
+    const int left = a.K > k0 ? (a.K - k0 + stride - 1) / stride : 0;          // the wave's slots
+    for (int i = 0; i < left / AHEAD; ++i) {
 #pragma unroll
-            for (int d = 0; d < AHEAD; ++d) {
-                add_slot<U, GROUP>(total, slot[d], mine + (k0 - c0) / 8, a.st, magic);
-                // unconditional, so that waits stay counted: past the end of K
-                // it reads the row's last line again
-                slot[d].load(a, wrow, srow, zrow, k0 + AHEAD * stride + half, q);
-                k0 += stride;
-                // keeps these loads before the next slot's wait
-                __builtin_amdgcn_sched_barrier(0);
-            }
+        for (int d = 0; d < AHEAD; ++d) {
+            add_slot(total, slot[d], k0, k0 + kSlot > a.K, a, lane, magic);
+            // unconditional, so that waits stay counted: past the end of K it
+            // reads the row's last line again
+            slot[d].load(a, wrow, srow, zrow, xrow, k0 + AHEAD * stride, lane);
+            k0 += stride;
+            // keeps these loads before the next slot's wait
+            __builtin_amdgcn_sched_barrier(0);
         }
-        // a remainder only where K ends
-#pragma unroll
-        for (int d = 0; d < AHEAD - 1; ++d)
-            if (d < left % AHEAD) {
-                add_slot<U, GROUP>(total, slot[d], mine + (k0 - c0) / 8, a.st, magic);
-                k0 += stride;
-            }
     }
+#pragma unroll
+    for (int d = 0; d < AHEAD - 1; ++d)
+        if (d < left % AHEAD) {
+            add_slot(total, slot[d], k0, k0 + kSlot > a.K, a, lane, magic);
+            k0 += stride;
+        }
 
+    const int n = lane & 15, q = lane >> 4;
     // lane (n, q) holds operand rows 4 q .. 4 q + 3 of column n: wanted where both are of the same half
-    __syncthreads();
-    float *part = reinterpret_cast<float *>(lds);           // [wave][half][u][token][row]
     if (n >> 3 == q >> 1) {
 #pragma unroll
         for (int u = 0; u < U; ++u)
@@ -239,20 +225,14 @@ __global__ void __launch_bounds__(64 * kStreamWaves) k_stream(Args a, int kc)
 }
 
 template <int U, int AHEAD, int GROUP, int SB, bool ZERO, bool EVEN>
-hipError_t launch_stream_as(const Args &a, int waves, int lds_bytes, hipStream_t s)
+hipError_t launch_stream_as(const Args &a, int waves, hipStream_t s)
 {
     const int64_t grid = (int64_t)((a.N + 8 * U - 1) / (8 * U)) * row_tiles(a, kStreamTokens);
     if (grid > 0x7fffffff)
         return hipErrorInvalidValue;
-    const int slots = (a.K + kSlot - 1) / kSlot;
-    const int tokens = min(a.M, kStreamTokens);
-    const int fits = (lds_bytes / (16 * tokens) - 1) * 8;               // codes of K whose tokens fit
-    waves = min(waves, min(slots, fits / (AHEAD * kSlot)));
-    const int round = AHEAD * waves * kSlot;
-    const int kc = min(fits / round, (a.K + round - 1) / round) * round;
-    const int lds = max(16 * tokens * token_pitch(min(kc, slots * kSlot)), waves * U * 512);
-    hipLaunchKernelGGL((k_stream<U, AHEAD, GROUP, SB, ZERO, EVEN>), dim3((unsigned)grid), dim3(64 * waves), lds,
-                       s, a, kc);
+    waves = min(waves, (a.K + kSlot - 1) / kSlot);
+    hipLaunchKernelGGL((k_stream<U, AHEAD, GROUP, SB, ZERO, EVEN>), dim3((unsigned)grid), dim3(64 * waves),
+                       waves * U * 512, s, a);
     return hipGetLastError();
 }
 
@@ -261,10 +241,10 @@ hipError_t stream_pick(const Args &a, hipStream_t s)
 {
     const int64_t rows = (int64_t)a.N * max(a.experts, 1);
     if (rows <= 16 * 256)
-        return launch_stream_as<1, 2, GROUP, SB, ZERO, EVEN>(a, 4, kStreamLds, s);
+        return launch_stream_as<1, 2, GROUP, SB, ZERO, EVEN>(a, 4, s);
     if (a.M <= 2 || rows <= 32 * 1024)
-        return launch_stream_as<2, 2, GROUP, SB, ZERO, EVEN>(a, 4, kStreamLds, s);
-    return launch_stream_as<4, 2, GROUP, SB, ZERO, EVEN>(a, 4, kStreamLds, s);
+        return launch_stream_as<2, 2, GROUP, SB, ZERO, EVEN>(a, 4, s);
+    return launch_stream_as<4, 2, GROUP, SB, ZERO, EVEN>(a, 4, s);
 }
 
 template <int GROUP, int SB, bool ZERO>
