@@ -316,7 +316,8 @@ qlin_status qlin_silu_and_mul_per_block_quant(int64_t M, int64_t K, const uint16
  *
  * Shapes: M >= 0, N >= 0 (0 is a no-op), 0 < K <= 2^20, K % group == 0.
  * ldx >= K with ldx % 8 == 0 (elements), ldb >= K/2 with ldb % 16 == 0
- * (bytes), ldy >= N; X, B and Y 16-byte aligned, b_scale 4-byte aligned.  An
+ * (bytes), ldy >= N, rows of X and B at most 2^25 bytes apart; X, B and Y
+ * 16-byte aligned, b_scale 4-byte aligned.  An
  * infinity or NaN in X reaches the outputs that the formula gives it and no
  * other row.  The caller owns every buffer; the call is asynchronous on
  * `stream` and allocates nothing.  workspace: qlin_w4_workspace_size bytes,

@@ -170,7 +170,7 @@ __device__ inline void wait_loads()
     asm volatile("" ::: "memory");
 }
 
-// A scale from its 16 or 32 bits.
+// A scale from its 16 (the rest is anything) or 32 bits.
 template <int SB>
 __device__ inline float scale_value(uint32_t bits, int st)
 {

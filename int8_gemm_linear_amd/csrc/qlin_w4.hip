@@ -10,6 +10,7 @@ namespace {
 constexpr int64_t kMaxRows = (int64_t)1 << 24;
 constexpr int64_t kMaxW4K = (int64_t)1 << 20;
 constexpr int64_t kMaxStride = ((int64_t)1 << 31) - 1;
+constexpr int64_t kMaxRowBytes = (int64_t)1 << 25;        // of X and B: a workgroup's 64 rows lie within 2^31
 
 bool aligned(const void *p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
@@ -29,7 +30,8 @@ qlin_status check(int64_t M, int64_t N, int64_t K, int64_t group, const void *X,
         return QLIN_OK;
     if (!X || !B || !scale || !Y)
         return QLIN_ERR_NULL_POINTER;
-    if (ldx < K || ldx % 8 != 0 || ldx > kMaxStride || ldb < K / 2 || ldb % 16 != 0 || ldb > kMaxStride ||
+    if (ldx < K || ldx % 8 != 0 || 2 * ldx > kMaxRowBytes || ldb < K / 2 || ldb % 16 != 0 ||
+        ldb > kMaxRowBytes ||
         ldy < N || ldy > kMaxStride)
         return QLIN_ERR_BAD_STRIDE;
     if (!aligned(X, 16) || !aligned(B, 16) || !aligned(Y, 16) || !aligned(scale, 4))

@@ -46,9 +46,17 @@ __device__ inline v4i from_lane(int lane, v4i v)
     return r;
 }
 
-// A slot's codes, scales, zero points and token operands, as loaded.  EVEN: K
-// % 128 == 0.
-template <int U, int GROUP, int SB, bool ZERO, bool EVEN>
+// Where a lane's loads go: bases of the workgroup's rows at code 0, and the
+// lane's offsets from them (bytes; of scales, elements).
+template <int U>
+struct Lane {
+    const uint8_t *wbase, *xbase, *sbase, *zbase;
+    uint32_t w[U], x, s[(U + 3) / 4], z[(U + 3) / 4];
+};
+
+// A slot's codes, scales, zero points and token operands, as loaded.  WHOLE: K
+// is whole slots, and a slot past the end reads the last one instead.
+template <int U, int GROUP, int SB, bool ZERO, bool WHOLE>
 struct Slot {
     static constexpr int NG = 128 / GROUP;          // groups of a half
     static constexpr int SW = (NG * SB + 3) / 4;    // dwords of their scales
@@ -56,62 +64,94 @@ struct Slot {
     v4i w[U], x[4];
     uint32_t s[SL][SW], z[SL];
 
-    __device__ inline void load(const Args &a, const uint8_t *const *wrow, const uint8_t *const *srow,
-                                const uint8_t *const *zrow, const uint16_t *xrow, int k0, int lane)
+    // Addresses are a uniform base and the lane's 32-bit offset from it: rows
+    // of the workgroup lie less than 2^31 bytes apart.
+    __device__ inline void load(const Args &a, const Lane<U> &o, int k0, int lane)
     {
-        const int seg = lane & 7;
+        if (WHOLE) {
+            k0 = min(k0, a.K - kSlot);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[j] = ld16(o.xbase + 2 * k0 + 64 * j + o.x);
+#pragma unroll
+            for (int u = 0; u < U; ++u) w[u] = ld_nt(o.wbase + k0 / 2 + o.w[u]);
+            // Whole dwords, where a lane's own would be less, both halves' or
+            // more: a narrower load's value is widened in an operation of its
+            // own, which the compiler puts, with its wait, right behind it.
+            const int g0 = k0 / GROUP, gz = ZERO && NG == 1 ? min(g0, a.G - 4) : g0;
+#pragma unroll
+            for (int l = 0; l < SL; ++l) {
+                __builtin_memcpy(s[l], o.sbase + (int64_t)SB * g0 + o.s[l] * SB, SB * (NG * SB == 2 ? 2 : NG));
+                if (ZERO)
+                    __builtin_memcpy(&z[l], o.zbase + gz + o.z[l], 4);
+            }
+            return;
+        }
         // past the end of K the tokens are made zeros and any codes do
-        const int at = min(k0 + 32 * seg, a.K - 32) / 2;
+        const int seg = lane & 7;
+        const int over = max(k0 + 32 * seg - (a.K - 32), 0);
 #pragma unroll
-        for (int u = 0; u < U; ++u) w[u] = ld_nt(wrow[u] + at);
+        for (int u = 0; u < U; ++u) w[u] = ld_nt(o.wbase + (k0 - over) / 2 + o.w[u]);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            x[j] = ld16(reinterpret_cast<const uint8_t *>(
-                xrow + min(k0 + 128 * (seg >> 2) + 32 * j + 8 * (seg & 3), a.K - 8)));
-        const int g0 = min(k0 + 128 * (lane & 1), EVEN ? a.K - 128 : a.K - 32) / GROUP;
+        for (int j = 0; j < 4; ++j) {
+            const int k = k0 + 128 * (seg >> 2) + 32 * j + 8 * (seg & 3);
+            x[j] = ld16(o.xbase + 2 * (k0 + 32 * j - max(k - (a.K - 8), 0)) + o.x);
+        }
+        const int g0 = k0 / GROUP + (lane & 1) * NG;
 #pragma unroll
         for (int l = 0; l < SL; ++l) {
             z[l] = 0;
-            s[l][0] = 0;
-            if (EVEN) {
-                __builtin_memcpy(s[l], srow[l] + SB * g0, NG * SB);
+#pragma unroll
+            for (int i = 0; i < SW; ++i) s[l][i] = 0;
+#pragma unroll
+            for (int i = 0; i < NG; ++i) {
+                const int64_t at = min(g0 + i, a.G - 1) + (int64_t)o.z[l];
+                if (SB == 4)
+                    s[l][i] = reinterpret_cast<const uint32_t *>(o.sbase)[at];
+                else
+                    s[l][i / 2] |= (uint32_t)reinterpret_cast<const uint16_t *>(o.sbase)[at] << (16 * (i & 1));
                 if (ZERO)
-                    __builtin_memcpy(&z[l], zrow[l] + g0, NG);
-            } else {
-#pragma unroll
-                for (int i = 1; i < SW; ++i) s[l][i] = 0;
-#pragma unroll
-                for (int i = 0; i < NG; ++i) {
-                    const int g = min(g0 + i, a.G - 1);
-                    if (SB == 4)
-                        s[l][i] = reinterpret_cast<const uint32_t *>(srow[l])[g];
-                    else
-                        s[l][i / 2] |= (uint32_t)reinterpret_cast<const uint16_t *>(srow[l])[g] << (16 * (i & 1));
-                    if (ZERO)
-                        z[l] |= (uint32_t)zrow[l][g] << (8 * i);
-                }
+                    z[l] |= (uint32_t)o.zbase[at] << (8 * i);
             }
+        }
+    }
+
+    // Uses of the slot come after this point of the program: the compiler
+    // moves an operation on a scale up to the slot before otherwise, and its
+    // wait with it.
+    __device__ inline void arrive()
+    {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) asm volatile("" : "+v"(x[j]));
+#pragma unroll
+        for (int u = 0; u < U; ++u) asm volatile("" : "+v"(w[u]));
+#pragma unroll
+        for (int l = 0; l < SL; ++l) {
+#pragma unroll
+            for (int i = 0; i < SW; ++i) asm volatile("" : "+v"(s[l][i]));
+            if (ZERO)
+                asm volatile("" : "+v"(z[l]));
         }
     }
 };
 
-// total += the slot's products; `partial` where the slot passes the end of K.
+// total += the slot's products.
 // An instruction takes 32 codes in a row, which keeps the token loads in whole
 // pieces of 64 bytes, whatever the group.
-template <int U, int GROUP, int SB, bool ZERO, bool EVEN>
-__device__ inline void add_slot(v4f *total, const Slot<U, GROUP, SB, ZERO, EVEN> &slot, int k0, bool partial,
-                                const Args &a, int lane, uint32_t magic)
+template <int U, int GROUP, int SB, bool ZERO, bool WHOLE>
+__device__ inline void add_slot(v4f *total, Slot<U, GROUP, SB, ZERO, WHOLE> &slot, int k0, const Args &a,
+                                int lane, uint32_t magic)
 {
-    typedef Slot<U, GROUP, SB, ZERO, EVEN> S;
+    typedef Slot<U, GROUP, SB, ZERO, WHOLE> S;
     constexpr int PER = GROUP / 32;                 // matrix instructions of a group
     const v4i ones = {0x3f803f80, 0x3f803f80, 0x3f803f80, 0x3f803f80};
     const int n = lane & 15, q = lane >> 4;
     const int from = 8 * (n & 7) + 4 * (n >> 3) + q, from_s = 2 * (n & 7) + (n >> 3);
+    slot.arrive();
     v4i x[4], w[U];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         x[j] = from_lane(from, slot.x[j]);
-        if (partial && k0 + 128 * (n >> 3) + 32 * j + 8 * q >= a.K)
+        if (!WHOLE && k0 + 128 * (n >> 3) + 32 * j + 8 * q >= a.K)
             x[j] = zero4i();
         x[j] = operand_order(x[j]);
     }
@@ -129,19 +169,25 @@ __device__ inline void add_slot(v4f *total, const Slot<U, GROUP, SB, ZERO, EVEN>
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
+        // (what the loads took of the other half is shifted out)
+        const int half = n >> 3;
         uint32_t s[S::SW], z = 0;
 #pragma unroll
         for (int i = 0; i < S::SW; ++i) s[i] = from_lane(from_s + 16 * (u & 3), slot.s[u / 4][i]);
-        if (ZERO)
+        if (WHOLE && S::NG * SB == 2)
+            s[0] >>= 16 * half;
+        if (ZERO) {
             z = from_lane(from_s + 16 * (u & 3), slot.z[u / 4]);
+            if (WHOLE && S::NG < 4)
+                z >>= 8 * (S::NG * half + (S::NG == 1 ? max(k0 / GROUP - (a.G - 4), 0) : 0));
+        }
 #pragma unroll
         for (int g = 0; g < 4 / PER; ++g) {
             v4f acc = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int i = 0; i < PER; ++i)
                 acc = mma(x[g * PER + i], expand8((uint32_t)w[u][g * PER + i], magic), acc);
-            const float sv = scale_value<SB>(SB == 4 ? s[g] : S::NG == 1 ? s[0] & 0xffffu
-                                                            : (s[g / 2] >> (16 * (g & 1))) & 0xffffu, a.st);
+            const float sv = scale_value<SB>(SB == 4 ? s[g] : S::NG == 1 ? s[0] : s[g / 2] >> (16 * (g & 1)), a.st);
             const float zv = ZERO ? -128.0f - (float)((z >> (8 * g)) & 0xffu) : -136.0f;
 #pragma unroll
             for (int i = 0; i < 4; ++i) total[u][i] = fmaf(sv, fmaf(zv, sum_x[g][i], acc[i]), total[u][i]);
@@ -149,7 +195,7 @@ __device__ inline void add_slot(v4f *total, const Slot<U, GROUP, SB, ZERO, EVEN>
     }
 }
 
-template <int U, int AHEAD, int GROUP, int SB, bool ZERO, bool EVEN>
+template <int U, int AHEAD, int GROUP, int SB, bool ZERO, bool WHOLE>
 __global__ void __launch_bounds__(64 * kStreamWaves) k_stream(Args a)
 {
     const int gx = (a.N + 8 * U - 1) / (8 * U);
@@ -162,16 +208,22 @@ __global__ void __launch_bounds__(64 * kStreamWaves) k_stream(Args a)
     const int n0 = (int)(blockIdx.x % gx) * 8 * U;
     const int tokens = min(a.M - m0, kStreamTokens);
     constexpr int SL = (U + 3) / 4;
-    // the rows of absent tokens compute what nobody reads
-    const uint16_t *xrow = a.x + (int64_t)(m0 + min(lane >> 3, tokens - 1)) * a.ldx;
-    const uint8_t *wrow[U], *srow[SL], *zrow[SL];
+    Lane<U> o;
+    o.wbase = a.b + (int64_t)n0 * a.ldb;
+    o.xbase = reinterpret_cast<const uint8_t *>(a.x + (int64_t)m0 * a.ldx);
+    o.sbase = a.scale + (int64_t)n0 * a.G * SB;
+    o.zbase = ZERO ? a.zero + (int64_t)n0 * a.G : nullptr;
+    // rows past the end repeat the last; absent tokens' compute what nobody reads
+    o.x = (uint32_t)min(lane >> 3, tokens - 1) * (uint32_t)(2 * a.ldx) + 256 * ((lane >> 2) & 1) + 16 * (lane & 3);
 #pragma unroll
-    for (int u = 0; u < U; ++u) wrow[u] = a.b + (int64_t)min(n0 + 8 * u + (lane >> 3), a.N - 1) * a.ldb;
+    for (int u = 0; u < U; ++u)
+        o.w[u] = (uint32_t)min(8 * u + (lane >> 3), a.N - 1 - n0) * (uint32_t)a.ldb + 16 * (lane & 7);
 #pragma unroll
     for (int l = 0; l < SL; ++l) {
-        const int64_t row = min(n0 + 32 * l + min(lane >> 1, 8 * U - 1), a.N - 1);
-        srow[l] = a.scale + row * a.G * SB;
-        zrow[l] = ZERO ? a.zero + row * a.G : nullptr;
+        o.z[l] = (uint32_t)min(32 * l + min(lane >> 1, 8 * U - 1), a.N - 1 - n0) * (uint32_t)a.G;
+        o.s[l] = o.z[l] + (WHOLE && 128 / GROUP * SB != 2 ? (lane & 1) * (128 / GROUP) : 0);
+        if (WHOLE && GROUP == 32)
+            o.z[l] += (lane & 1) * 4;
     }
     v4f total[U];
 #pragma unroll
@@ -179,19 +231,19 @@ __global__ void __launch_bounds__(64 * kStreamWaves) k_stream(Args a)
 
     const uint32_t magic = expand_magic();
     const int stride = waves * kSlot;
-    Slot<U, GROUP, SB, ZERO, EVEN> slot[AHEAD];
+    Slot<U, GROUP, SB, ZERO, WHOLE> slot[AHEAD];
     int k0 = wave * kSlot;
 #pragma unroll
-    for (int d = 0; d < AHEAD; ++d) slot[d].load(a, wrow, srow, zrow, xrow, k0 + d * stride, lane);
+    for (int d = 0; d < AHEAD; ++d) slot[d].load(a, o, k0 + d * stride, lane);
     __builtin_amdgcn_sched_barrier(0);
     const int left = a.K > k0 ? (a.K - k0 + stride - 1) / stride : 0;          // the wave's slots
     for (int i = 0; i < left / AHEAD; ++i) {
 #pragma unroll
         for (int d = 0; d < AHEAD; ++d) {
-            add_slot(total, slot[d], k0, k0 + kSlot > a.K, a, lane, magic);
+            add_slot(total, slot[d], k0, a, lane, magic);
             // unconditional, so that waits stay counted: past the end of K it
             // reads the row's last line again
-            slot[d].load(a, wrow, srow, zrow, xrow, k0 + AHEAD * stride, lane);
+            slot[d].load(a, o, k0 + AHEAD * stride, lane);
             k0 += stride;
             // keeps these loads before the next slot's wait
             __builtin_amdgcn_sched_barrier(0);
@@ -200,7 +252,7 @@ __global__ void __launch_bounds__(64 * kStreamWaves) k_stream(Args a)
 #pragma unroll
     for (int d = 0; d < AHEAD - 1; ++d)
         if (d < left % AHEAD) {
-            add_slot(total, slot[d], k0, k0 + kSlot > a.K, a, lane, magic);
+            add_slot(total, slot[d], k0, a, lane, magic);
             k0 += stride;
         }
 
@@ -224,44 +276,53 @@ __global__ void __launch_bounds__(64 * kStreamWaves) k_stream(Args a)
     }
 }
 
-template <int U, int AHEAD, int GROUP, int SB, bool ZERO, bool EVEN>
+template <int U, int AHEAD, int GROUP, int SB, bool ZERO, bool WHOLE>
 hipError_t launch_stream_as(const Args &a, int waves, hipStream_t s)
 {
     const int64_t grid = (int64_t)((a.N + 8 * U - 1) / (8 * U)) * row_tiles(a, kStreamTokens);
     if (grid > 0x7fffffff)
         return hipErrorInvalidValue;
     waves = min(waves, (a.K + kSlot - 1) / kSlot);
-    hipLaunchKernelGGL((k_stream<U, AHEAD, GROUP, SB, ZERO, EVEN>), dim3((unsigned)grid), dim3(64 * waves),
+    hipLaunchKernelGGL((k_stream<U, AHEAD, GROUP, SB, ZERO, WHOLE>), dim3((unsigned)grid), dim3(64 * waves),
                        waves * U * 512, s, a);
     return hipGetLastError();
 }
 
-template <int GROUP, int SB, bool ZERO, bool EVEN>
+template <int GROUP, int SB, bool ZERO, bool WHOLE>
 hipError_t stream_pick(const Args &a, hipStream_t s)
 {
-    const int64_t rows = (int64_t)a.N * max(a.experts, 1);
-    if (rows <= 16 * 256)
-        return launch_stream_as<1, 2, GROUP, SB, ZERO, EVEN>(a, 4, s);
-    if (a.M <= 2 || rows <= 32 * 1024)
-        return launch_stream_as<2, 2, GROUP, SB, ZERO, EVEN>(a, 4, s);
-    return launch_stream_as<4, 2, GROUP, SB, ZERO, EVEN>(a, 4, s);
+    // More rows a workgroup share one read of the tokens and one start, fewer
+    // give the 256 CUs more workgroups: 8 rows up to two workgroups a CU, 32
+    // from 16 times that (experts: of those that can have rows).  Measured, us
+    // with 8 / 16 / 32 rows, one token: 3.6 / 3.9 / 4.4 (2048 x 2048),
+    // 10.9 / 9.6 / 10.4 (10240 x 5120), 36 / 31.0 / 30.6 (51200 x 5120);
+    // 32 tokens through 128 experts of 1536 x 2048: - / 39.8 / 35.9.
+    // Waves: as many as K has slots while workgroups are few, one or two when
+    // they fill the GPU by themselves (the experts: 35.9 with two, 40.3 with
+    // four).
+    const int64_t units = (int64_t)((a.N + 7) / 8) * (a.experts ? min(a.experts, a.rows) : 1);
+    const int u = units >= 4096 ? 4 : units > 512 ? 2 : 1;
+    const int waves = (int)min(max((6144 * u + units - 1) / units, (int64_t)1), (int64_t)kStreamWaves);
+    if (u == 1)
+        return launch_stream_as<1, 1, GROUP, SB, ZERO, WHOLE>(a, waves, s);
+    if (u == 2)
+        return launch_stream_as<2, 1, GROUP, SB, ZERO, WHOLE>(a, waves, s);
+    return launch_stream_as<4, 2, GROUP, SB, ZERO, WHOLE>(a, waves, s);
 }
 
 template <int GROUP, int SB, bool ZERO>
-hipError_t stream_even(const Args &a, hipStream_t s)
+hipError_t stream_whole(const Args &a, hipStream_t s)
 {
-    // groups of 128 divide K by themselves
-    if (GROUP == 128 || a.K % 128 == 0)
-        return stream_pick<GROUP, SB, ZERO, true>(a, s);
-    return stream_pick<GROUP, SB, ZERO, GROUP == 128>(a, s);
+    // (a dword of zero points needs four groups)
+    return a.K % kSlot == 0 && a.G >= 4 ? stream_pick<GROUP, SB, ZERO, true>(a, s) : stream_pick<GROUP, SB, ZERO, false>(a, s);
 }
 
 template <int GROUP>
 hipError_t stream_any(const Args &a, hipStream_t s)
 {
     if (a.st == QLIN_SCALE_F32)
-        return a.zero ? stream_even<GROUP, 4, true>(a, s) : stream_even<GROUP, 4, false>(a, s);
-    return a.zero ? stream_even<GROUP, 2, true>(a, s) : stream_even<GROUP, 2, false>(a, s);
+        return a.zero ? stream_whole<GROUP, 4, true>(a, s) : stream_whole<GROUP, 4, false>(a, s);
+    return a.zero ? stream_whole<GROUP, 2, true>(a, s) : stream_whole<GROUP, 2, false>(a, s);
 }
 
 }  // namespace w4
