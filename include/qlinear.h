@@ -311,7 +311,8 @@ qlin_status qlin_silu_and_mul_per_block_quant(int64_t M, int64_t K, const uint16
  *
  * X [M][ldx] bf16 bits.  B [N][ldb] bytes, two codes per byte: byte j of a row
  * holds k = 2j in its low and k = 2j + 1 in its high nibble.  b_scale
- * [N][K/group] contiguous, of type `st`; b_zero [N][K/group] bytes, or NULL.
+ * [N][K/group] contiguous, of type `st`; b_zero [N][K/group] bytes 0..15 (of
+ * which the upper four bits are not read), or NULL.
  * Y [M][ldy] bf16 bits.
  *
  * Shapes: M >= 0, N >= 0 (0 is a no-op), 0 < K <= 2^20, K % group == 0.

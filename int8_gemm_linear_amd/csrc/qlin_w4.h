@@ -170,6 +170,16 @@ __device__ inline void wait_loads()
     asm volatile("" ::: "memory");
 }
 
+// lds_dma16 from a uniform base and the lane's offset.
+__device__ inline void lds_dma16_at(const uint8_t *base, uint32_t offset, const void *lds)
+{
+    const unsigned to = (unsigned)(size_t)lds;
+    asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1"
+                 :
+                 : "v"(offset), "s"(base), "s"(__builtin_amdgcn_readfirstlane(to))
+                 : "memory", "m0");
+}
+
 // A scale from its 16 (the rest is anything) or 32 bits.
 template <int SB>
 __device__ inline float scale_value(uint32_t bits, int st)
@@ -247,7 +257,7 @@ __device__ inline float exact_value(const Args &a, int64_t m, int64_t n)
         const double s = a.st == QLIN_SCALE_F32
                              ? reinterpret_cast<const float *>(a.scale)[at]
                              : scale_value<2>(reinterpret_cast<const uint16_t *>(a.scale)[at], a.st);
-        const int z = a.zero ? a.zero[at] : 8;
+        const int z = a.zero ? a.zero[at] & 15 : 8;
         for (int k = g * group; k < (g + 1) * group; ++k) {
             const int q = (a.b[n * a.ldb + (k >> 1)] >> (4 * (k & 1))) & 15;
             const float x = __uint_as_float((uint32_t)a.x[m * a.ldx + k] << 16);

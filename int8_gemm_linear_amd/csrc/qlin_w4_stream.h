@@ -188,7 +188,7 @@ __device__ inline void add_slot(v4f *total, Slot<U, GROUP, SB, ZERO, WHOLE> &slo
             for (int i = 0; i < PER; ++i)
                 acc = mma(x[g * PER + i], expand8((uint32_t)w[u][g * PER + i], magic), acc);
             const float sv = scale_value<SB>(SB == 4 ? s[g] : S::NG == 1 ? s[0] : s[g / 2] >> (16 * (g & 1)), a.st);
-            const float zv = ZERO ? -128.0f - (float)((z >> (8 * g)) & 0xffu) : -136.0f;
+            const float zv = ZERO ? -128.0f - (float)((z >> (8 * g)) & 15u) : -136.0f;
 #pragma unroll
             for (int i = 0; i < 4; ++i) total[u][i] = fmaf(sv, fmaf(zv, sum_x[g][i], acc[i]), total[u][i]);
         }
@@ -293,14 +293,14 @@ hipError_t stream_pick(const Args &a, hipStream_t s)
 {
     // More rows a workgroup share one read of the tokens and one start, fewer
     // give the 256 CUs more workgroups: 8 rows up to two workgroups a CU, 32
-    // from 16 times that (experts: of those that can have rows).  Measured, us
+    // from 16 times that (experts: of the tiles in the grid).  Measured, us
     // with 8 / 16 / 32 rows, one token: 3.6 / 3.9 / 4.4 (2048 x 2048),
     // 10.9 / 9.6 / 10.4 (10240 x 5120), 36 / 31.0 / 30.6 (51200 x 5120);
     // 32 tokens through 128 experts of 1536 x 2048: - / 39.8 / 35.9.
     // Waves: as many as K has slots while workgroups are few, one or two when
     // they fill the GPU by themselves (the experts: 35.9 with two, 40.3 with
     // four).
-    const int64_t units = (int64_t)((a.N + 7) / 8) * (a.experts ? min(a.experts, a.rows) : 1);
+    const int64_t units = (int64_t)((a.N + 7) / 8) * (a.experts ? row_tiles(a, kStreamTokens) : 1);
     const int u = units >= 4096 ? 4 : units > 512 ? 2 : 1;
     const int waves = (int)min(max((6144 * u + units - 1) / units, (int64_t)1), (int64_t)kStreamWaves);
     if (u == 1)

@@ -21,41 +21,54 @@ namespace w4 {
 
 constexpr int kTileWaves = 4;
 
+// Where a lane's loads go: bytes from the wave's first row (of scales: elements).
+template <int RB, int H>
+struct Lane {
+    const uint8_t *wbase, *sbase, *zbase;
+    uint32_t w[RB][H], s[RB];
+};
+
 // The codes, scales and zero points of a wave's rows for a stage.  With KS =
 // 256 two loads take whole 128-byte lines of 8 rows each (see halves()).
-template <int RB, int KS, int GROUP, int SB, bool ZERO>
+template <int RB, int KS, int GROUP, int SB, bool ZERO, bool WHOLE>
 struct Codes {
     static constexpr int H = KS / 128, NG = KS / GROUP;
     v4i w[RB][H];
     uint32_t s[RB][(SB * NG + 3) / 4], z[RB][(NG + 3) / 4];
 
-    __device__ inline void load(const Args &a, const uint8_t *const (*wrow)[H], const uint8_t *const *srow,
-                                const uint8_t *const *zrow, int k0, int n, int q)
+    // Addresses are a uniform base, the wave's first row at code 0, and the
+    // lane's 32-bit offset from it.
+    __device__ inline void load(const Args &a, const Lane<RB, H> &o, int k0, int n, int q)
     {
-        // past the end of K the tokens are zeros and any codes do
-        const int at = min(k0 + 32 * q + (H == 2 ? 128 * (n >> 3) : 0), a.K - 32) / 2;
+        if (WHOLE) {
+            k0 = min(k0, a.K - KS);
+            const int64_t g0 = k0 / GROUP;
 #pragma unroll
-        for (int r = 0; r < RB; ++r)
+            for (int r = 0; r < RB; ++r)
 #pragma unroll
-            for (int h = 0; h < H; ++h) w[r][h] = ld16(wrow[r][h] + at);
-        const int g0 = k0 / GROUP;
-        if (k0 + KS <= a.K) {
+                for (int h = 0; h < H; ++h) w[r][h] = ld16(o.wbase + k0 / 2 + o.w[r][h]);
 #pragma unroll
             for (int r = 0; r < RB; ++r) {
-                __builtin_memcpy(s[r], srow[r] + SB * g0, SB * NG);
+                __builtin_memcpy(s[r], o.sbase + SB * g0 + SB * o.s[r], SB * NG);
                 if (ZERO)
-                    __builtin_memcpy(z[r], zrow[r] + g0, NG);
+                    __builtin_memcpy(z[r], o.zbase + g0 + o.s[r], NG);
             }
             return;
         }
+        // past the end of K the tokens are zeros and any codes do
+        const int over = max(k0 + 32 * q + (H == 2 ? 128 * (n >> 3) : 0) - (a.K - 32), 0);
+#pragma unroll
+        for (int r = 0; r < RB; ++r)
+#pragma unroll
+            for (int h = 0; h < H; ++h) w[r][h] = ld16(o.wbase + (k0 - over) / 2 + o.w[r][h]);
 #pragma unroll
         for (int r = 0; r < RB; ++r)
 #pragma unroll
             for (int i = 0; i < NG; ++i) {
-                const int g = min(g0 + i, a.G - 1);
-                __builtin_memcpy(reinterpret_cast<uint8_t *>(s[r]) + SB * i, srow[r] + SB * g, SB);
+                const int64_t at = min(k0 / GROUP + i, a.G - 1) + (int64_t)o.s[r];
+                __builtin_memcpy(reinterpret_cast<uint8_t *>(s[r]) + SB * i, o.sbase + SB * at, SB);
                 if (ZERO)
-                    reinterpret_cast<uint8_t *>(z[r])[i] = zrow[r][g];
+                    reinterpret_cast<uint8_t *>(z[r])[i] = o.zbase[at];
             }
     }
 
@@ -64,10 +77,12 @@ struct Codes {
         return scale_value<SB>(SB == 4 ? s[r][i] : (s[r][i / 2] >> (16 * (i & 1))) & 0xffffu, st);
     }
 
-    // -(128 + z)
-    __device__ inline float bias(int r, int i) const
+    // 15 - z in both halves of a dword: added to expanded codes it makes them
+    // 143 + (q - z), and what has to be taken away the same for all rows.
+    __device__ inline uint32_t raise(int r, int i) const
     {
-        return -128.0f - (float)((z[r][i / 4] >> (8 * (i & 3))) & 0xffu);
+        const uint32_t up = 15u - ((z[r][i / 4] >> (8 * (i & 3))) & 15u);
+        return up | (up << 16);
     }
 };
 
@@ -82,10 +97,15 @@ __host__ __device__ inline Blocks tile_blocks(int gx, int tiles)
     return Blocks{(gx + 7) / 8, (tiles + blocks - 1) / blocks, blocks};
 }
 
-template <int TB, int RB, int KS, int GROUP, int SB, bool ZERO>
+template <int TB, int RB, int KS, int GROUP, int SB, bool ZERO, bool WHOLE>
 __global__ void __launch_bounds__(64 * kTileWaves, 2) k_tile(Args a)
 {
-    constexpr int H = KS / 128, PIECES = KS / 8, PER = GROUP / 32, NG = KS / GROUP;
+    // A group of 128 is taken as two of 64 with the same scale: the operands
+    // of 64 codes x 64 rows fit the registers beside everything else, those of
+    // 128 do not (with zero points: 312 us against 218 us at 1000 tokens on
+    // 10240 x 5120).
+    constexpr int SUB = GROUP < 64 ? GROUP : 64;
+    constexpr int H = KS / 128, PIECES = KS / 8, PER = SUB / 32, NS = KS / SUB;
     constexpr int COPIES = 16 * TB * PIECES / 64;           // 1 KB each
     // Workgroups go to the 8 XCDs in turn, so id mod 8 names the L2: each takes
     // every 8th weight tile, and walks them in blocks of up to 8 token tiles,
@@ -101,22 +121,25 @@ __global__ void __launch_bounds__(64 * kTileWaves, 2) k_tile(Args a)
     if (nx >= gx || y >= a.tiles || !enter_tile<16 * TB>(a, y, m0))
         return;
     __shared__ v4i lds[3][16 * TB * PIECES];
-    __shared__ v4f sums[2][NG][TB * 4];             // [group][token / 4], times -136 without zero points
+    __shared__ v4f sums[2][NS][TB * 4];             // [SUB codes][token / 4], times what the codes are too large by
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = lane & 15, q = lane >> 4;
     const int n0 = (nx * kTileWaves + wave) * 16 * RB;
     const int kbeg = split * a.split_k, kend = min(a.K, kbeg + a.split_k);
-    const uint8_t *wrow[RB][H], *srow[RB], *zrow[RB];
+    // (a wave past the last row repeats it)
+    const int first = min(n0, a.N - 1);
+    Lane<RB, H> o;
+    o.wbase = a.b + (int64_t)first * a.ldb;
+    o.sbase = a.scale + (int64_t)first * a.G * SB;
+    o.zbase = ZERO ? a.zero + (int64_t)first * a.G : nullptr;
 #pragma unroll
     for (int r = 0; r < RB; ++r) {
-        const int base = n0 + 16 * r;
 #pragma unroll
         for (int h = 0; h < H; ++h)
-            wrow[r][h] = a.b + (int64_t)min(H == 2 ? base + 8 * h + (n & 7) : base + n, a.N - 1) * a.ldb;
-        const int64_t row = min(base + n, a.N - 1);
-        srow[r] = a.scale + row * a.G * SB;
-        zrow[r] = ZERO ? a.zero + row * a.G : nullptr;
+            o.w[r][h] = (uint32_t)min(H == 2 ? 16 * r + 8 * h + (n & 7) : 16 * r + n, a.N - 1 - first) * (uint32_t)a.ldb +
+                        16 * q + (H == 2 ? 64 * (n >> 3) : 0);
+        o.s[r] = (uint32_t)min(16 * r + n, a.N - 1 - first) * (uint32_t)a.G;
     }
     v4f total[RB][TB];
 #pragma unroll
@@ -132,23 +155,31 @@ __global__ void __launch_bounds__(64 * kTileWaves, 2) k_tile(Args a)
     const int copy_t = (wave * 64 + lane) / PIECES, copy_p = lane % PIECES;
     const int copy_piece = (copy_p ^ copy_t) & 15;
     static_assert(256 / PIECES % 16 == 0 || 256 / PIECES == 8, "tokens of a wave's copies");
+    uint32_t copy_x[COPIES / kTileWaves];                   // bytes from the first token at code 0
+#pragma unroll
+    for (int i = 0; i < COPIES / kTileWaves; ++i) {
+        // eight tokens on, bit 3 of the exchange is the other
+        const int piece = 256 / PIECES == 8 ? copy_piece ^ (8 * (i & 1)) : copy_piece;
+        copy_x[i] = (uint32_t)min(copy_t + i * (256 / PIECES), a.M - 1 - m0) * (uint32_t)(2 * a.ldx) +
+                    256 * (copy_p >> 4) + 16 * piece;
+    }
+    const uint8_t *xbase = reinterpret_cast<const uint8_t *>(a.x + (int64_t)m0 * a.ldx);
     auto stage = [&](int k0, int buf) {
+        if (WHOLE)
+            k0 = min(k0, a.K - KS);
 #pragma unroll
         for (int i = 0; i < COPIES / kTileWaves; ++i) {
-            const int t = min(m0 + copy_t + i * (256 / PIECES), a.M - 1);
-            // eight tokens on: bit 3 of the exchange alternates
-            const int piece = 256 / PIECES == 8 ? copy_piece ^ (8 * (i & 1)) : copy_piece;
-            const int k = k0 + 128 * (copy_p >> 4) + 8 * piece;
             v4i *to = &lds[buf][(i * kTileWaves + wave) * 64];
-            if (k < kend)
-                lds_dma16(a.x + (int64_t)t * a.ldx + k, to);
+            const int piece = 256 / PIECES == 8 ? copy_piece ^ (8 * (i & 1)) : copy_piece;
+            if (WHOLE || k0 + 128 * (copy_p >> 4) + 8 * piece < kend)
+                lds_dma16_at(xbase + 2 * (int64_t)k0, copy_x[i], to);
             else
                 to[lane] = zero4i();
         }
     };
     int place[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) place[j] = n * PIECES + ((k_of<GROUP>(j, q) / 8) ^ n);
+    for (int j = 0; j < 4; ++j) place[j] = n * PIECES + ((k_of<SUB>(j, q) / 8) ^ n);
 
     const v4i ones = {0x3f803f80, 0x3f803f80, 0x3f803f80, 0x3f803f80};
     auto sum = [&](int buf, int to) {
@@ -162,9 +193,8 @@ __global__ void __launch_bounds__(64 * kTileWaves, 2) k_tile(Args a)
                 v4f s = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                 for (int j = 0; j < PER; ++j) s = mma(lds[buf][place[g * PER + j] + 16 * h + 16 * t * PIECES], ones, s);
-                if (!ZERO)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) s[j] *= -136.0f;
+                for (int j = 0; j < 4; ++j) s[j] *= ZERO ? -143.0f : -136.0f;
                 if (n == 0)
                     sums[to][h * (4 / PER) + g][t * 4 + q] = s;
             }
@@ -172,11 +202,10 @@ __global__ void __launch_bounds__(64 * kTileWaves, 2) k_tile(Args a)
     };
 
     const uint32_t magic = expand_magic();
-    Codes<RB, KS, GROUP, SB, ZERO> cur, next;
+    Codes<RB, KS, GROUP, SB, ZERO, WHOLE> cur, next;
     stage(kbeg, 0);
-    if (kbeg + KS < kend)
-        stage(kbeg + KS, 1);
-    cur.load(a, wrow, srow, zrow, kbeg, n, q);
+    stage(kbeg + KS, 1);
+    cur.load(a, o, kbeg, n, q);
     wait_loads();
     __syncthreads();
     sum(0, 0);
@@ -186,11 +215,6 @@ __global__ void __launch_bounds__(64 * kTileWaves, 2) k_tile(Args a)
         // the next stage's tokens have landed; this stage's sums are there; the last stage's buffer is free
         wait_loads();
         __syncthreads();
-        if (k0 + 2 * KS < kend)
-            stage(k0 + 2 * KS, buf2);
-        next.load(a, wrow, srow, zrow, k0 + KS, n, q);
-        if (k0 + KS < kend)
-            sum(buf1, par ^ 1);
         const v4i *xs = lds[buf];
 #pragma unroll
         for (int h = 0; h < H; ++h) {
@@ -199,42 +223,62 @@ __global__ void __launch_bounds__(64 * kTileWaves, 2) k_tile(Args a)
                 for (int r = 0; r < RB; ++r) halves(cur.w[r][0], cur.w[r][H - 1]);
             }
 #pragma unroll
-            for (int r = 0; r < RB; ++r) quarters<GROUP>(cur.w[r][h]);
+            for (int r = 0; r < RB; ++r) quarters<SUB>(cur.w[r][h]);
 #pragma unroll
             for (int g = 0; g < 4 / PER; ++g) {
                 const int at = h * (4 / PER) + g;
                 v4i b[RB][PER];
-                float sv[RB], zv[RB];
+                float sv[RB];
 #pragma unroll
                 for (int r = 0; r < RB; ++r) {
+                    const uint32_t up = ZERO ? cur.raise(r, at * SUB / GROUP) : 0;
 #pragma unroll
-                    for (int i = 0; i < PER; ++i) b[r][i] = expand8_natural((uint32_t)cur.w[r][h][g * PER + i], magic);
-                    sv[r] = cur.scale(r, at, a.st);
-                    zv[r] = ZERO ? cur.bias(r, at) : 0.0f;
+                    for (int i = 0; i < PER; ++i) {
+                        // expanded here and not earlier, where registers are not free yet
+                        uint32_t w = (uint32_t)cur.w[r][h][g * PER + i];
+                        asm volatile("" : "+v"(w));
+                        b[r][i] = expand8_natural(w, magic);
+                        if (ZERO)
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) b[r][i][j] += (int)up;
+                    }
+                    sv[r] = cur.scale(r, at * SUB / GROUP, a.st);
                 }
                 // The products of a token block, while the operands of the
-                // next come from LDS and the sums of the last are scaled.
-                v4f acc[2][RB], s[2];
-                v4i x[2][PER];
-                auto fetch = [&](int t) {
-                    s[t & 1] = sums[par][at][t * 4 + q];
+                // next come from LDS (each into the registers of the one just
+                // used) and the sums of the last are scaled.
+                v4f acc[2][RB], s;
+                v4i x[PER];
+                auto fetch = [&](int t, int i) { x[i] = xs[place[g * PER + i] + 16 * h + 16 * t * PIECES]; };
+                s = sums[par][at][q];
 #pragma unroll
-                    for (int i = 0; i < PER; ++i) x[t & 1][i] = xs[place[g * PER + i] + 16 * h + 16 * t * PIECES];
-                };
-                fetch(0);
+                for (int i = 0; i < PER; ++i) fetch(0, i);
 #pragma unroll
                 for (int t = 0; t <= TB; ++t) {
-                    if (t + 1 < TB)
-                        fetch(t + 1);
+                    // What the stage asks of memory, and the next one's sums,
+                    // go between its products; always, for a branch would
+                    // keep them apart: past the end of K they repeat the last
+                    // stage (or read zeros), and nobody looks.
+                    if (at == 0 && t == 0)
+                        stage(k0 + 2 * KS, buf2);
+                    if (at == 0 && t == (TB > 1 ? 1 : 0))
+                        next.load(a, o, k0 + KS, n, q);
+                    if (at == 0 && t == (TB > 2 ? 2 : TB))
+                        sum(buf1, par ^ 1);
                     if (t < TB) {
 #pragma unroll
                         for (int r = 0; r < RB; ++r)
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) acc[t & 1][r][i] = ZERO ? zv[r] * s[t & 1][i] : s[t & 1][i];
+                            for (int i = 0; i < 4; ++i) acc[t & 1][r][i] = s[i];
+                        if (t + 1 < TB)
+                            s = sums[par][at][(t + 1) * 4 + q];
 #pragma unroll
-                        for (int i = 0; i < PER; ++i)
+                        for (int i = 0; i < PER; ++i) {
 #pragma unroll
-                            for (int r = 0; r < RB; ++r) acc[t & 1][r] = mma(x[t & 1][i], b[r][i], acc[t & 1][r]);
+                            for (int r = 0; r < RB; ++r) acc[t & 1][r] = mma(x[i], b[r][i], acc[t & 1][r]);
+                            if (t + 1 < TB)
+                                fetch(t + 1, i);
+                        }
                     }
                     if (t > 0) {
 #pragma unroll
@@ -292,7 +336,7 @@ __global__ void __launch_bounds__(64 * kTileWaves, 2) k_tile(Args a)
     }
 }
 
-template <int TB, int RB, int KS, int GROUP, int SB, bool ZERO>
+template <int TB, int RB, int KS, int GROUP, int SB, bool ZERO, bool WHOLE>
 hipError_t launch_tile_as(Args a, hipStream_t s)
 {
     const int64_t tiles = row_tiles(a, 16 * TB);
@@ -303,17 +347,24 @@ hipError_t launch_tile_as(Args a, hipStream_t s)
     const int64_t grid = (int64_t)8 * bl.across * bl.high * bl.blocks * a.splits;
     if (grid > 0x7fffffff)
         return hipErrorInvalidValue;
-    hipLaunchKernelGGL((k_tile<TB, RB, KS, GROUP, SB, ZERO>), dim3((unsigned)grid), dim3(64 * kTileWaves), 0, s, a);
+    hipLaunchKernelGGL((k_tile<TB, RB, KS, GROUP, SB, ZERO, WHOLE>), dim3((unsigned)grid), dim3(64 * kTileWaves), 0, s, a);
     return hipGetLastError();
+}
+
+template <int TB, int RB, int KS, int GROUP, int SB, bool ZERO>
+hipError_t tile_whole(const Args &a, hipStream_t s)
+{
+    return a.K % KS == 0 ? launch_tile_as<TB, RB, KS, GROUP, SB, ZERO, true>(a, s)
+                         : launch_tile_as<TB, RB, KS, GROUP, SB, ZERO, false>(a, s);
 }
 
 template <int GROUP, int SB, bool ZERO>
 hipError_t tile_pick(const Args &a, hipStream_t s)
 {
     switch (pick_tile(a.experts ? a.rows / a.experts : a.M, a.N).tb) {
-    case 1: return launch_tile_as<1, 1, 256, GROUP, SB, ZERO>(a, s);
-    case 2: return launch_tile_as<2, 2, 256, GROUP, SB, ZERO>(a, s);
-    default: return launch_tile_as<4, 4, 128, GROUP, SB, ZERO>(a, s);
+    case 1: return tile_whole<1, 1, 256, GROUP, SB, ZERO>(a, s);
+    case 2: return tile_whole<2, 2, 256, GROUP, SB, ZERO>(a, s);
+    default: return tile_whole<4, 4, 128, GROUP, SB, ZERO>(a, s);
     }
 }
 
