@@ -190,6 +190,19 @@ __device__ inline float scale_value(uint32_t bits, int st)
     return st == QLIN_SCALE_BF16 ? __uint_as_float(bits << 16) : h;
 }
 
+__device__ inline uint32_t from_lane(int lane, uint32_t v)
+{
+    return (uint32_t)__builtin_amdgcn_ds_bpermute(4 * lane, (int)v);
+}
+
+__device__ inline v4i from_lane(int lane, v4i v)
+{
+    v4i r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = (int)from_lane(lane, (uint32_t)v[i]);
+    return r;
+}
+
 // Two 16-byte loads of whole 128-byte lines, rows 0..7 and 8..15 of a block:
 // lane (n, q) of a load has row n mod 8 and the 16 bytes q of the line's
 // first half (n < 8) or second half (n >= 8).  Afterwards `a` holds the first

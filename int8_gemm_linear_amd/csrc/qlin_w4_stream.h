@@ -33,19 +33,6 @@ namespace w4 {
 constexpr int kSlot = 256;
 constexpr int kStreamWaves = 8;
 
-__device__ inline uint32_t from_lane(int lane, uint32_t v)
-{
-    return (uint32_t)__builtin_amdgcn_ds_bpermute(4 * lane, (int)v);
-}
-
-__device__ inline v4i from_lane(int lane, v4i v)
-{
-    v4i r;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) r[i] = (int)from_lane(lane, (uint32_t)v[i]);
-    return r;
-}
-
 // Where a lane's loads go: bases of the workgroup's rows at code 0, and the
 // lane's offsets from them (bytes; of scales, elements).
 template <int U>

@@ -25,20 +25,25 @@ constexpr int kTileWaves = 4;
 template <int RB, int H>
 struct Lane {
     const uint8_t *wbase, *sbase, *zbase;
-    uint32_t w[RB][H], s[RB];
+    uint32_t w[RB][H], s;
 };
 
-// The codes, scales and zero points of a wave's rows for a stage.  With KS =
-// 256 two loads take whole 128-byte lines of 8 rows each (see halves()).
+// The codes, scales and zero points of a wave's rows for a stage, as loaded:
+// in an order that is good for the cache (the L1 takes one access for each 64
+// bytes that four lanes in a row ask for together), which a permutation of the
+// lanes turns into the matrix operands'.  Lane l loads 16 bytes l mod 8 of row
+// l / 8 where a stage has whole 128-byte lines (KS = 256, two loads for 16
+// rows), l mod 4 of row l / 4 where it has half lines, and the scales of row l.
+// (With loads in the operands' order: 1000 tokens on 10240 x 5120 171 us.)
 template <int RB, int KS, int GROUP, int SB, bool ZERO, bool WHOLE>
 struct Codes {
     static constexpr int H = KS / 128, NG = KS / GROUP;
     v4i w[RB][H];
-    uint32_t s[RB][(SB * NG + 3) / 4], z[RB][(NG + 3) / 4];
+    uint32_t s[(SB * NG + 3) / 4], z[(NG + 3) / 4];
 
     // Addresses are a uniform base, the wave's first row at code 0, and the
     // lane's 32-bit offset from it.
-    __device__ inline void load(const Args &a, const Lane<RB, H> &o, int k0, int n, int q)
+    __device__ inline void load(const Args &a, const Lane<RB, H> &o, int k0, int lane)
     {
         if (WHOLE) {
             k0 = min(k0, a.K - KS);
@@ -47,41 +52,51 @@ struct Codes {
             for (int r = 0; r < RB; ++r)
 #pragma unroll
                 for (int h = 0; h < H; ++h) w[r][h] = ld16(o.wbase + k0 / 2 + o.w[r][h]);
-#pragma unroll
-            for (int r = 0; r < RB; ++r) {
-                __builtin_memcpy(s[r], o.sbase + SB * g0 + SB * o.s[r], SB * NG);
-                if (ZERO)
-                    __builtin_memcpy(z[r], o.zbase + g0 + o.s[r], NG);
-            }
+            __builtin_memcpy(s, o.sbase + SB * g0 + SB * o.s, SB * NG);
+            if (ZERO)
+                __builtin_memcpy(z, o.zbase + g0 + o.s, NG);
             return;
         }
         // past the end of K the tokens are zeros and any codes do
-        const int over = max(k0 + 32 * q + (H == 2 ? 128 * (n >> 3) : 0) - (a.K - 32), 0);
+        const int over = max(k0 + 32 * (H == 2 ? lane & 7 : lane & 3) - (a.K - 32), 0);
 #pragma unroll
         for (int r = 0; r < RB; ++r)
 #pragma unroll
             for (int h = 0; h < H; ++h) w[r][h] = ld16(o.wbase + (k0 - over) / 2 + o.w[r][h]);
 #pragma unroll
-        for (int r = 0; r < RB; ++r)
-#pragma unroll
-            for (int i = 0; i < NG; ++i) {
-                const int64_t at = min(k0 / GROUP + i, a.G - 1) + (int64_t)o.s[r];
-                __builtin_memcpy(reinterpret_cast<uint8_t *>(s[r]) + SB * i, o.sbase + SB * at, SB);
-                if (ZERO)
-                    reinterpret_cast<uint8_t *>(z[r])[i] = o.zbase[at];
-            }
+        for (int i = 0; i < NG; ++i) {
+            const int64_t at = min(k0 / GROUP + i, a.G - 1) + (int64_t)o.s;
+            __builtin_memcpy(reinterpret_cast<uint8_t *>(s) + SB * i, o.sbase + SB * at, SB);
+            if (ZERO)
+                reinterpret_cast<uint8_t *>(z)[i] = o.zbase[at];
+        }
     }
 
-    __device__ inline float scale(int r, int i, int st) const
+    // The codes in the operands' order: lane (n, q) the 16 bytes q of row n of
+    // each step of 128 codes.
+    __device__ inline void permute(int n, int q)
     {
-        return scale_value<SB>(SB == 4 ? s[r][i] : (s[r][i / 2] >> (16 * (i & 1))) & 0xffffu, st);
+        const int from = H == 2 ? 8 * (n & 7) + 4 * (n >> 3) + q : 4 * n + q;
+#pragma unroll
+        for (int r = 0; r < RB; ++r) {
+#pragma unroll
+            for (int h = 0; h < H; ++h) w[r][h] = from_lane(from, w[r][h]);
+            if (H == 2)
+                halves(w[r][0], w[r][H - 1]);
+        }
+    }
+
+    __device__ inline float scale(int r, int n, int i, int st) const
+    {
+        const uint32_t v = from_lane(16 * r + n, s[SB == 4 ? i : i / 2]);
+        return scale_value<SB>(SB == 4 ? v : v >> (16 * (i & 1)), st);
     }
 
     // 15 - z in both halves of a dword: added to expanded codes it makes them
     // 143 + (q - z), and what has to be taken away the same for all rows.
-    __device__ inline uint32_t raise(int r, int i) const
+    __device__ inline uint32_t raise(int r, int n, int i) const
     {
-        const uint32_t up = 15u - ((z[r][i / 4] >> (8 * (i & 3))) & 15u);
+        const uint32_t up = 15u - ((from_lane(16 * r + n, z[i / 4]) >> (8 * (i & 3))) & 15u);
         return up | (up << 16);
     }
 };
@@ -137,10 +152,10 @@ __global__ void __launch_bounds__(64 * kTileWaves, 2) k_tile(Args a)
     for (int r = 0; r < RB; ++r) {
 #pragma unroll
         for (int h = 0; h < H; ++h)
-            o.w[r][h] = (uint32_t)min(H == 2 ? 16 * r + 8 * h + (n & 7) : 16 * r + n, a.N - 1 - first) * (uint32_t)a.ldb +
-                        16 * q + (H == 2 ? 64 * (n >> 3) : 0);
-        o.s[r] = (uint32_t)min(16 * r + n, a.N - 1 - first) * (uint32_t)a.G;
+            o.w[r][h] = (uint32_t)min(H == 2 ? 16 * r + 8 * h + (lane >> 3) : 16 * r + (lane >> 2), a.N - 1 - first) *
+                            (uint32_t)a.ldb + 16 * (H == 2 ? lane & 7 : lane & 3);
     }
+    o.s = (uint32_t)min(lane & (16 * RB - 1), a.N - 1 - first) * (uint32_t)a.G;
     v4f total[RB][TB];
 #pragma unroll
     for (int r = 0; r < RB; ++r)
@@ -205,7 +220,7 @@ __global__ void __launch_bounds__(64 * kTileWaves, 2) k_tile(Args a)
     Codes<RB, KS, GROUP, SB, ZERO, WHOLE> cur, next;
     stage(kbeg, 0);
     stage(kbeg + KS, 1);
-    cur.load(a, o, kbeg, n, q);
+    cur.load(a, o, kbeg, lane);
     wait_loads();
     __syncthreads();
     sum(0, 0);
@@ -216,12 +231,9 @@ __global__ void __launch_bounds__(64 * kTileWaves, 2) k_tile(Args a)
         wait_loads();
         __syncthreads();
         const v4i *xs = lds[buf];
+        cur.permute(n, q);
 #pragma unroll
         for (int h = 0; h < H; ++h) {
-            if (H == 2 && h == 0) {
-#pragma unroll
-                for (int r = 0; r < RB; ++r) halves(cur.w[r][0], cur.w[r][H - 1]);
-            }
 #pragma unroll
             for (int r = 0; r < RB; ++r) quarters<SUB>(cur.w[r][h]);
 #pragma unroll
@@ -231,7 +243,7 @@ __global__ void __launch_bounds__(64 * kTileWaves, 2) k_tile(Args a)
                 float sv[RB];
 #pragma unroll
                 for (int r = 0; r < RB; ++r) {
-                    const uint32_t up = ZERO ? cur.raise(r, at * SUB / GROUP) : 0;
+                    const uint32_t up = ZERO ? cur.raise(r, n, at * SUB / GROUP) : 0;
 #pragma unroll
                     for (int i = 0; i < PER; ++i) {
                         // expanded here and not earlier, where registers are not free yet
@@ -242,7 +254,7 @@ __global__ void __launch_bounds__(64 * kTileWaves, 2) k_tile(Args a)
 #pragma unroll
                             for (int j = 0; j < 4; ++j) b[r][i][j] += (int)up;
                     }
-                    sv[r] = cur.scale(r, at * SUB / GROUP, a.st);
+                    sv[r] = cur.scale(r, n, at * SUB / GROUP, a.st);
                 }
                 // The products of a token block, while the operands of the
                 // next come from LDS (each into the registers of the one just
@@ -262,7 +274,7 @@ __global__ void __launch_bounds__(64 * kTileWaves, 2) k_tile(Args a)
                     if (at == 0 && t == 0)
                         stage(k0 + 2 * KS, buf2);
                     if (at == 0 && t == (TB > 1 ? 1 : 0))
-                        next.load(a, o, k0 + KS, n, q);
+                        next.load(a, o, k0 + KS, lane);
                     if (at == 0 && t == (TB > 2 ? 2 : TB))
                         sum(buf1, par ^ 1);
                     if (t < TB) {

@@ -32,18 +32,20 @@ def w4_check(y, x, codes, scale, zero, group, what=""):
 
     Bound: each value is rounded to bf16 once (half a step of the result);
     before that the sums are fp32.  Inside a group the kernels add products
-    of x with 128 + q and take (128 + z) times the group's sum of x away:
-    at most group + 4 additions, each off by at most 2^-23 (the matrix cores
-    need not round to nearest) of sum |x| (256 + q + z); then K / group + 40
-    additions (groups, then waves) of the groups' true values times s."""
+    of x with 128 + q and take (128 + z) times the group's sum of x away, or
+    with 143 + q - z and 143 times it: at most group + 4 additions, each off
+    by at most 2^-23 (the matrix cores need not round to nearest) of
+    sum |x| (286 + q), which is at least sum |x| (256 + q + z) and
+    sum |x| (286 + q - z); then K / group + 40 additions (groups, then waves)
+    of the groups' true values times s (groups of 128 may be taken in two)."""
     x, codes = np.asarray(x, np.float64), np.asarray(codes)
     s = np.repeat(np.asarray(scale, np.float64), group, axis=-1)
     z = np.full(codes.shape, 8.0) if zero is None else np.repeat(np.asarray(zero, np.float64), group, axis=-1)
     ref = x @ (s * (codes - z)).T
     ax, K = np.abs(x), x.shape[1]
-    inner = ax @ (np.abs(s) * (256.0 + codes + z)).T
+    inner = ax @ (np.abs(s) * (286.0 + codes)).T
     outer = ax @ (np.abs(s) * np.abs(codes - z)).T
-    tol = BF16_HALF * np.abs(ref) + 1.01 * 2.0 ** -23 * ((group + 4) * inner + (K // group + 40) * outer) + F32_MIN
+    tol = BF16_HALF * np.abs(ref) + 1.01 * 2.0 ** -23 * ((group + 4) * inner + (2 * (K // group) + 40) * outer) + F32_MIN
     got = f64(y)
     assert got.shape == ref.shape, (what, got.shape, ref.shape)
     bad = ~(np.abs(got - ref) <= tol)
