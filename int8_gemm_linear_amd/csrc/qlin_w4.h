@@ -301,14 +301,13 @@ hipError_t launch_tile_32(const Args &a, hipStream_t s);
 hipError_t launch_tile_64(const Args &a, hipStream_t s);
 hipError_t launch_tile_128(const Args &a, hipStream_t s);
 
-// The tile kernel's tiles for M tokens (experts: a typical expert's): 16 tb
-// tokens, 64 rb weight rows, ks codes of K at a time.
+// The tile kernel's tile, 16 tb tokens x 64 rb weight rows with ks codes of K
+// at a time, and the parts of K: for M tokens, or with experts for `rows` rows
+// of them (one part).
 struct TilePick {
-    int tb, rb, ks;
+    int tb, rb, ks, splits;
 };
-TilePick pick_tile(int64_t tokens, int64_t N);
-// Parts of K for a product without experts (1: none).
-int pick_splits(int64_t M, int64_t N, int64_t K);
+TilePick pick_tile(int64_t M, int64_t N, int64_t K, int64_t experts, int64_t rows);
 
 }  // namespace w4
 }  // namespace qlin

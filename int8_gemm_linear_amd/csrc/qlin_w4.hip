@@ -94,16 +94,16 @@ qlin_status launch(w4::Args &a, void *ws, size_t ws_bytes, void *stream)
     if ((a.experts ? a.rows / a.experts : a.M) <= w4::kStreamTokens)
         return kStream[which](a, s) == hipSuccess ? QLIN_OK : QLIN_ERR_HIP;
     if (!a.experts) {
-        a.splits = w4::pick_splits(a.M, a.N, a.K);
-        const size_t need = part_bytes(a.M, a.N, a.splits);
+        const w4::TilePick p = w4::pick_tile(a.M, a.N, a.K, 0, 0);
+        const size_t need = part_bytes(a.M, a.N, p.splits);
         if (need && (!ws || ws_bytes < need))
             return QLIN_ERR_WORKSPACE;
         if (need && !aligned(ws, 16))
             return QLIN_ERR_MISALIGNED;
+        const int stages = (a.K + p.ks - 1) / p.ks;
+        a.splits = p.splits;
+        a.split_k = (stages + p.splits - 1) / p.splits * p.ks;
         a.part = static_cast<float *>(ws);
-        const int ks = w4::pick_tile(a.M, a.N).ks;
-        const int stages = (a.K + ks - 1) / ks;
-        a.split_k = (stages + a.splits - 1) / a.splits * ks;
     }
     if (kTile[which](a, s) != hipSuccess)
         return QLIN_ERR_HIP;
@@ -124,24 +124,44 @@ qlin_status launch(w4::Args &a, void *ws, size_t ws_bytes, void *stream)
 
 namespace w4 {
 
-TilePick pick_tile(int64_t tokens, int64_t)
+// The tile and the parts of K with the least estimated time.  Two workgroups
+// run on a CU, 512 at once; a round of them takes (stages + 2) x `us`, a last
+// round of half as many 0.65 of that; parts of K cost a second kernel and the
+// traffic of their sums.  `us` is what a stage took with 512 workgroups
+// running.  Of the tiles that were tried (tb 1, 2, 4 x rb 1, 2, 4, K split in
+// 1 to 20) on 51200 x 5120, 10240 x 5120, 5120 x 25600, 2048 x 2048 and 1536 x
+// 8192 with 12 to 256 tokens these three and this choice come within 10% of
+// the best: 32 tokens on 5120 x 25600 34 us in ten parts (one: 251), 256 on
+// 10240 x 5120 53 us in three parts (one: 63).
+TilePick pick_tile(int64_t M, int64_t N, int64_t K, int64_t experts, int64_t rows)
 {
-    return tokens <= 16 ? TilePick{1, 1, 256} : tokens <= 32 ? TilePick{2, 2, 256} : TilePick{4, 4, 128};
-}
-
-int pick_splits(int64_t M, int64_t N, int64_t K)
-{
-    if (M <= kStreamTokens)
-        return 1;
-    const TilePick p = pick_tile(M, N);
-    const int64_t tiles = ((M + 16 * p.tb - 1) / (16 * p.tb)) * ((N + 64 * p.rb - 1) / (64 * p.rb));
-    const int64_t stages = (K + p.ks - 1) / p.ks;
-    // two workgroups of a CU, each at least four stages of K
-    const int64_t splits = std::min((512 + tiles - 1) / tiles, stages / 4);
-    if (splits <= 1 || tiles >= 256)
-        return 1;
-    const int64_t each = (stages + splits - 1) / splits;
-    return (int)((stages + each - 1) / each);        // none of them empty
+    static const struct {
+        int tb, rb, ks;
+        double us;
+    } kTiles[] = {{1, 1, 256, 1.6}, {2, 2, 256, 2.4}, {4, 4, 128, 2.7}};
+    TilePick best{4, 4, 128, 1};
+    double least = 1e30;
+    for (const auto &t : kTiles) {
+        const int64_t high = 16 * t.tb, stages = (K + t.ks - 1) / t.ks;
+        // an expert's last tile is half full on average
+        const double tall = experts ? (double)rows / high + 0.5 * std::min(experts, rows) : (double)((M + high - 1) / high);
+        const double tiles = tall * ((N + 64 * t.rb - 1) / (64 * t.rb));
+        const int most = experts ? 1 : (int)std::min<int64_t>(20, std::max<int64_t>(stages / 2, 1));
+        for (int splits = 1; splits <= most; ++splits) {
+            const int64_t each = (stages + splits - 1) / splits;
+            if ((stages + each - 1) / each != splits)
+                continue;                                    // a part would be empty
+            const double rounds = tiles * splits / 512, whole = (double)(int64_t)rounds, rest = rounds - whole;
+            double us = (whole + (rest > 0.5 ? 1.0 : rest > 0.0 ? 0.65 : 0.0)) * (each + 2) * t.us;
+            if (splits > 1)
+                us += 4.0 + splits * (double)M * N * 8 / 5e6;
+            if (us < least) {
+                least = us;
+                best = TilePick{t.tb, t.rb, t.ks, splits};
+            }
+        }
+    }
+    return best;
 }
 
 }  // namespace w4
@@ -167,7 +187,7 @@ size_t qlin_w4_workspace_size(int64_t M, int64_t N, int64_t K)
 {
     if (M <= 0 || M > kMaxRows || N <= 0 || N > kMaxRows || K <= 0 || K > kMaxW4K)
         return 0;
-    return part_bytes(M, N, w4::pick_splits(M, N, K));
+    return M <= w4::kStreamTokens ? 0 : part_bytes(M, N, w4::pick_tile(M, N, K, 0, 0).splits);
 }
 
 qlin_status qlin_grouped_w4_mm(int64_t groups, const int32_t *group_offsets, int64_t max_rows,

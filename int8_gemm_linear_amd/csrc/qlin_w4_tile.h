@@ -373,7 +373,7 @@ hipError_t tile_whole(const Args &a, hipStream_t s)
 template <int GROUP, int SB, bool ZERO>
 hipError_t tile_pick(const Args &a, hipStream_t s)
 {
-    switch (pick_tile(a.experts ? a.rows / a.experts : a.M, a.N).tb) {
+    switch (pick_tile(a.M, a.N, a.K, a.experts, a.rows).tb) {
     case 1: return tile_whole<1, 1, 256, GROUP, SB, ZERO>(a, s);
     case 2: return tile_whole<2, 2, 256, GROUP, SB, ZERO>(a, s);
     default: return tile_whole<4, 4, 128, GROUP, SB, ZERO>(a, s);
