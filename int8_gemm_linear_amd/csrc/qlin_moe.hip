@@ -14,6 +14,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "qlin_device.h"
 #include "qlin_dpp.h"
 #include "qlinear.h"
@@ -36,7 +38,9 @@ bool aligned(const void *p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0;
 constexpr int kSortWaves = 8;                  // x 2048 experts of LDS counters: 64 KB
 constexpr int kSortThreads = 64 * kSortWaves;
 constexpr int64_t kSortOne = 4096;             // slots up to which one workgroup sorts alone
-constexpr int kSortMaxBlocks = 256;
+constexpr int kSortBlock = 2048;               // slots of a workgroup otherwise, until
+constexpr int kSortMaxBlocks = 256;            // there would be more workgroups than this
+constexpr int kSortHold = 4;                   // ids a thread loads at a time
 
 // The expert of slot i, or -1.
 template <typename ID>
@@ -44,6 +48,17 @@ __device__ inline int expert_of(const ID *ids, int i, int experts)
 {
     const ID id = ids[i];
     return id >= 0 && id < (ID)experts ? (int)id : -1;
+}
+
+// The experts of slots i, i + step, ..., -1 from `end` on: all loads, then all uses.
+template <typename ID>
+__device__ inline void load_experts(int (&e)[kSortHold], const ID *ids, int i, int step, int end, int experts)
+{
+    ID id[kSortHold];
+#pragma unroll
+    for (int h = 0; h < kSortHold; ++h) id[h] = i + h * step < end ? ids[i + h * step] : (ID)-1;
+#pragma unroll
+    for (int h = 0; h < kSortHold; ++h) e[h] = id[h] >= 0 && id[h] < (ID)experts ? (int)id[h] : -1;
 }
 
 // Lanes of the wave that hold the same expert as this one (all 64 lanes call).
@@ -78,10 +93,13 @@ __global__ void __launch_bounds__(kSortThreads) k_moe_count(SortArgs a)
     for (int e = threadIdx.x; e < a.experts; e += kSortThreads) hist[e] = 0;
     __syncthreads();
     const int beg = blockIdx.x * a.per_block, end = min(beg + a.per_block, a.n);
-    for (int i = beg + threadIdx.x; i < end; i += kSortThreads) {
-        const int e = expert_of(static_cast<const ID *>(a.ids), i, a.experts);
-        if (e >= 0)
-            atomicAdd(&hist[e], 1);
+    for (int i = beg + threadIdx.x; i < end; i += kSortHold * kSortThreads) {
+        int e[kSortHold];
+        load_experts(e, static_cast<const ID *>(a.ids), i, kSortThreads, end, a.experts);
+#pragma unroll
+        for (int h = 0; h < kSortHold; ++h)
+            if (e[h] >= 0)
+                atomicAdd(&hist[e[h]], 1);
     }
     __syncthreads();
     for (int e = threadIdx.x; e < a.experts; e += kSortThreads)
@@ -93,44 +111,66 @@ __global__ void __launch_bounds__(kSortThreads) k_moe_count(SortArgs a)
 // counts and the counts of the workgroups before it into the wave's first row
 // of each expert, and the wave walks its part again 64 slots at a time, a
 // slot's rank among the 64 being the number of lower lanes with its expert.
+// Latency bounds it: the counts of all workgroups are summed by all threads at
+// once, kSortHold loads of each in flight (a thread per expert that walked the
+// workgroups' counts: 13 us for 65 528 slots and 128 experts, this: 6 us).
 template <typename ID>
 __global__ void __launch_bounds__(kSortThreads) k_moe_place(SortArgs a)
 {
     __shared__ int32_t hist[kSortWaves * kMaxExperts];
+    __shared__ int32_t total[kMaxExperts], before[kMaxExperts];
     __shared__ int32_t wave_total[kSortWaves];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const ID *ids = static_cast<const ID *>(a.ids);
-    for (int i = tid; i < kSortWaves * a.experts; i += kSortThreads) hist[i] = 0;
-    __syncthreads();
     const int part = a.per_block / kSortWaves;
     const int beg = min(blockIdx.x * a.per_block + wave * part, a.n), end = min(beg + part, a.n);
+    int held[kSortHold];                                    // the part's first 64 kSortHold slots
+    load_experts(held, ids, beg + lane, 64, end, a.experts);
+    for (int i = tid; i < kSortWaves * a.experts; i += kSortThreads) hist[i] = 0;
+    for (int i = tid; i < a.experts; i += kSortThreads) total[i] = before[i] = 0;
+    __syncthreads();
     int32_t *mine = hist + wave * a.experts;
-    for (int i = beg + lane; i < end; i += 64) {
-        const int e = expert_of(ids, i, a.experts);
-        if (e >= 0)
-            atomicAdd(&mine[e], 1);
+    for (int i = beg; i < end; i += 64 * kSortHold) {
+        int e[kSortHold];
+        if (i == beg)
+            for (int h = 0; h < kSortHold; ++h) e[h] = held[h];
+        else
+            load_experts(e, ids, i + lane, 64, end, a.experts);
+#pragma unroll
+        for (int h = 0; h < kSortHold; ++h)
+            if (e[h] >= 0)
+                atomicAdd(&mine[e[h]], 1);
+    }
+    if (a.counts) {
+        const int all = gridDim.x * a.experts, earlier = blockIdx.x * a.experts;
+        for (int i = tid; i < all; i += kSortHold * kSortThreads) {
+            int c[kSortHold];
+#pragma unroll
+            for (int h = 0; h < kSortHold; ++h) {
+                const int at = i + h * kSortThreads;
+                c[h] = at < all ? a.counts[at] : 0;
+            }
+#pragma unroll
+            for (int h = 0; h < kSortHold; ++h) {
+                const int at = i + h * kSortThreads;
+                if (c[h]) {
+                    atomicAdd(&total[at % a.experts], c[h]);
+                    if (at < earlier)
+                        atomicAdd(&before[at % a.experts], c[h]);
+                }
+            }
+        }
     }
     __syncthreads();
 
     // exclusive sums over the experts, a thread taking `each` consecutive ones
     const int each = (a.experts + kSortThreads - 1) / kSortThreads;
-    int total[kMaxExperts / kSortThreads], before[kMaxExperts / kSortThreads], sum = 0;
-#pragma unroll
-    for (int j = 0; j < kMaxExperts / kSortThreads; ++j) {
-        const int e = tid * each + j;
-        total[j] = before[j] = 0;
-        if (j < each && e < a.experts) {
-            if (a.counts) {
-                for (int b = 0; b < (int)gridDim.x; ++b) {
-                    const int c = a.counts[(int64_t)b * a.experts + e];
-                    total[j] += c;
-                    before[j] += b < (int)blockIdx.x ? c : 0;
-                }
-            } else {
-                for (int w = 0; w < kSortWaves; ++w) total[j] += hist[w * a.experts + e];
-            }
-        }
-        sum += total[j];
+    const int e0 = min(tid * each, a.experts), e1 = min(e0 + each, a.experts);
+    int sum = 0;
+    for (int e = e0; e < e1; ++e) {
+        if (!a.counts)
+            for (int w = 0; w < kSortWaves; ++w) total[e] += hist[w * a.experts + e];
+        sum += total[e];
     }
     int scan = sum;
     for (int d = 1; d < 64; d <<= 1) {
@@ -142,43 +182,46 @@ __global__ void __launch_bounds__(kSortThreads) k_moe_place(SortArgs a)
     __syncthreads();
     int first = scan - sum;
     for (int w = 0; w < wave; ++w) first += wave_total[w];
-#pragma unroll
-    for (int j = 0; j < kMaxExperts / kSortThreads; ++j) {
-        const int e = tid * each + j;
-        if (j < each && e < a.experts) {
-            if (blockIdx.x == 0) {
-                a.offsets[e] = first;
-                if (e == a.experts - 1)
-                    a.offsets[a.experts] = first + total[j];
-            }
-            int at = first + before[j];
-            for (int w = 0; w < kSortWaves; ++w) {
-                const int c = hist[w * a.experts + e];
-                hist[w * a.experts + e] = at;
-                at += c;
-            }
+    for (int e = e0; e < e1; ++e) {
+        if (blockIdx.x == 0) {
+            a.offsets[e] = first;
+            if (e == a.experts - 1)
+                a.offsets[a.experts] = first + total[e];
         }
-        first += total[j];
+        int at = first + before[e];
+        for (int w = 0; w < kSortWaves; ++w) {
+            const int c = hist[w * a.experts + e];
+            hist[w * a.experts + e] = at;
+            at += c;
+        }
+        first += total[e];
     }
     __syncthreads();
 
-    for (int base = beg; base < end; base += 64) {
-        const int i = base + lane;
-        const int e = i < end ? expert_of(ids, i, a.experts) : -1;
-        const uint64_t same = same_expert(e, a.bits);
-        const int lead = __ffsll((unsigned long long)same) - 1;
-        int at = 0;
-        if (e >= 0 && lane == lead)
-            at = atomicAdd(&mine[e], __popcll(same));
-        at = __shfl(at, lead);
-        if (i < end)
-            a.slot_row[i] = e >= 0 ? at + __popcll(same & (((uint64_t)1 << lane) - 1)) : -1;
+    for (int i = beg; i < end; i += 64 * kSortHold) {
+        int e[kSortHold];
+        if (i == beg)
+            for (int h = 0; h < kSortHold; ++h) e[h] = held[h];
+        else
+            load_experts(e, ids, i + lane, 64, end, a.experts);
+#pragma unroll
+        for (int h = 0; h < kSortHold; ++h) {
+            const int slot = i + h * 64 + lane;
+            const uint64_t same = same_expert(e[h], a.bits);
+            const int lead = __ffsll((unsigned long long)same) - 1;
+            int at = 0;
+            if (e[h] >= 0 && lane == lead)
+                at = atomicAdd(&mine[e[h]], __popcll(same));
+            at = __shfl(at, lead);
+            if (slot < end)
+                a.slot_row[slot] = e[h] >= 0 ? at + __popcll(same & (((uint64_t)1 << lane) - 1)) : -1;
+        }
     }
 }
 
 int sort_blocks(int64_t n)
 {
-    return n <= kSortOne ? 1 : (int)min((n + 2047) / 2048, (int64_t)kSortMaxBlocks);
+    return n <= kSortOne ? 1 : (int)min((n + kSortBlock - 1) / kSortBlock, (int64_t)kSortMaxBlocks);
 }
 
 qlin_status check_sort(int32_t id_bits, int64_t tokens, int64_t topk, int64_t experts, const void *ids,
@@ -373,7 +416,24 @@ template <> struct Elem<uint16_t> {                // bf16 bits
     static __device__ inline uint16_t put(float v) { return bf16_bits(v); }
 };
 
-// out[t] = sum_j w[t,j] y[row[t,j]]
+// Choices whose rows a thread loads together.
+constexpr int kChoices = 4;
+
+// Rows and weights of choices j to j + kChoices of a token; a choice without a
+// row has row -1.
+__device__ inline void load_choices(int (&row)[kChoices], float (&w)[kChoices], const RowArgs &a, int64_t slot,
+                                    int j)
+{
+#pragma unroll
+    for (int c = 0; c < kChoices; ++c) {
+        const int r = j + c < a.topk ? a.slot_row[slot + j + c] : -1;
+        row[c] = (unsigned)r < (unsigned)a.rows ? r : -1;
+        w[c] = a.weights && j + c < a.topk ? a.weights[slot + j + c] : 1.0f;
+    }
+}
+
+// out[t] = sum_j w[t,j] y[row[t,j]], the choices in order.  Bound by the rows'
+// bytes: 8191 tokens of 8 rows of 4 KB 4.6 TB/s.
 template <typename T>
 __global__ void __launch_bounds__(kRowThreads) k_moe_combine(RowArgs a)
 {
@@ -382,23 +442,27 @@ __global__ void __launch_bounds__(kRowThreads) k_moe_combine(RowArgs a)
     const int lane = threadIdx.x & (a.lanes - 1);
     if (token >= a.tokens)
         return;
-    const int32_t *rows = a.slot_row + (int64_t)token * a.topk;
-    const float *weights = a.weights ? a.weights + (int64_t)token * a.topk : nullptr;
+    const int64_t slot = (int64_t)token * a.topk;
     uint8_t *out = a.out + (int64_t)token * a.ldo;
     const int pieces = a.cols / V, tail = a.cols % V;
     for (int p = lane; p < pieces; p += a.lanes) {
         float sum[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) sum[i] = 0.0f;
-        for (int j = 0; j < a.topk; ++j) {
-            const int r = rows[j];
-            if ((unsigned)r < (unsigned)a.rows) {
-                T v[V];
-                __builtin_memcpy(v, a.x + r * a.ldx + 16 * (int64_t)p, 16);
-                const float w = weights ? weights[j] : 1.0f;
+        for (int j = 0; j < a.topk; j += kChoices) {
+            int row[kChoices];
+            float w[kChoices];
+            T v[kChoices][V];
+            load_choices(row, w, a, slot, j);
 #pragma unroll
-                for (int i = 0; i < V; ++i) sum[i] = fmaf(w, Elem<T>::get(v[i]), sum[i]);
-            }
+            for (int c = 0; c < kChoices; ++c)
+                if (row[c] >= 0)
+                    __builtin_memcpy(v[c], a.x + row[c] * a.ldx + 16 * (int64_t)p, 16);
+#pragma unroll
+            for (int c = 0; c < kChoices; ++c)
+                if (row[c] >= 0)
+#pragma unroll
+                    for (int i = 0; i < V; ++i) sum[i] = fmaf(w[c], Elem<T>::get(v[c][i]), sum[i]);
         }
         T o[V];
 #pragma unroll
@@ -409,57 +473,76 @@ __global__ void __launch_bounds__(kRowThreads) k_moe_combine(RowArgs a)
         const int64_t at = pieces * V + i;
         float sum = 0.0f;
         for (int j = 0; j < a.topk; ++j) {
-            const int r = rows[j];
+            const int r = a.slot_row[slot + j];
             if ((unsigned)r < (unsigned)a.rows)
-                sum = fmaf(weights ? weights[j] : 1.0f,
+                sum = fmaf(a.weights ? a.weights[slot + j] : 1.0f,
                            Elem<T>::get(reinterpret_cast<const T *>(a.x + r * a.ldx)[at]), sum);
         }
         reinterpret_cast<T *>(out)[at] = Elem<T>::put(sum);
     }
 }
 
-// dy[row[t,j]] = w[t,j] dout[t],  dw[t,j] = <dout[t], y[row[t,j]]>: one wave
-// per token, the dot products summed over its lanes in a fixed order.
+// dy[row[t,j]] = w[t,j] dout[t],  dw[t,j] = <dout[t], y[row[t,j]]>: a.lanes
+// threads (whole waves) per token, a piece of dout serving kChoices rows, the
+// dot products summed over the lanes and then the waves in a fixed order.
+// Bound by the bytes of the rows read and written.
 template <typename T>
 __global__ void __launch_bounds__(kRowThreads) k_moe_combine_backward(RowArgs a)
 {
     constexpr int V = 16 / sizeof(T);
-    const int token = blockIdx.x * (kRowThreads / 64) + threadIdx.x / 64;
-    const int lane = threadIdx.x & 63;
-    if (token >= a.tokens)
-        return;
+    __shared__ float part[2][kRowThreads / 64][kChoices];
+    const int tid = threadIdx.x, lane = tid & (a.lanes - 1);
+    const int token = blockIdx.x * (kRowThreads / a.lanes) + tid / a.lanes;
+    const bool live = token < a.tokens;
     const uint8_t *dout = a.x + (int64_t)token * a.ldx;
-    const int pieces = a.cols / V, tail = a.cols % V;
-    for (int j = 0; j < a.topk; ++j) {
-        const int64_t slot = (int64_t)token * a.topk + j;
-        const int r = a.slot_row[slot];
-        float dot = 0.0f;
-        if ((unsigned)r < (unsigned)a.rows) {
-            const float w = a.weights[slot];
-            const uint8_t *y = a.y + r * a.ldy;
-            uint8_t *dy = a.out + r * a.ldo;
-            for (int p = lane; p < pieces; p += 64) {
-                T d[V], v[V], o[V];
-                __builtin_memcpy(d, dout + 16 * (int64_t)p, 16);
-                __builtin_memcpy(v, y + 16 * (int64_t)p, 16);
+    const int64_t slot = (int64_t)token * a.topk;
+    const int pieces = live ? a.cols / V : 0, tail = live ? a.cols % V : 0;
+    for (int j = 0, turn = 0; j < a.topk; j += kChoices, turn ^= 1) {
+        int row[kChoices] = {-1, -1, -1, -1};
+        float w[kChoices], dot[kChoices] = {};
+        if (live)
+            load_choices(row, w, a, slot, j);
+        for (int p = lane; p < pieces; p += a.lanes) {
+            T d[V], v[kChoices][V];
+            __builtin_memcpy(d, dout + 16 * (int64_t)p, 16);
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const float f = Elem<T>::get(d[i]);
-                    dot = fmaf(f, Elem<T>::get(v[i]), dot);
-                    o[i] = Elem<T>::put(w * f);
+            for (int c = 0; c < kChoices; ++c)
+                if (row[c] >= 0)
+                    __builtin_memcpy(v[c], a.y + row[c] * a.ldy + 16 * (int64_t)p, 16);
+#pragma unroll
+            for (int c = 0; c < kChoices; ++c)
+                if (row[c] >= 0) {
+                    T o[V];
+#pragma unroll
+                    for (int i = 0; i < V; ++i) {
+                        const float f = Elem<T>::get(d[i]);
+                        dot[c] = fmaf(f, Elem<T>::get(v[c][i]), dot[c]);
+                        o[i] = Elem<T>::put(w[c] * f);
+                    }
+                    __builtin_memcpy(a.out + row[c] * a.ldo + 16 * (int64_t)p, o, 16);
                 }
-                __builtin_memcpy(dy + 16 * (int64_t)p, o, 16);
-            }
-            if (lane < tail) {
-                const int at = pieces * V + lane;
-                const float f = Elem<T>::get(reinterpret_cast<const T *>(dout)[at]);
-                dot = fmaf(f, Elem<T>::get(reinterpret_cast<const T *>(y)[at]), dot);
-                reinterpret_cast<T *>(dy)[at] = Elem<T>::put(w * f);
-            }
         }
-        dot = wave_sum(dot);
-        if (lane == 0)
-            a.out_f[slot] = dot;
+        if (lane < tail) {
+            const int at = pieces * V + lane;
+            const float f = Elem<T>::get(reinterpret_cast<const T *>(dout)[at]);
+#pragma unroll
+            for (int c = 0; c < kChoices; ++c)
+                if (row[c] >= 0) {
+                    dot[c] = fmaf(f, Elem<T>::get(reinterpret_cast<const T *>(a.y + row[c] * a.ldy)[at]), dot[c]);
+                    reinterpret_cast<T *>(a.out + row[c] * a.ldo)[at] = Elem<T>::put(w[c] * f);
+                }
+        }
+#pragma unroll
+        for (int c = 0; c < kChoices; ++c) dot[c] = wave_sum(dot[c]);
+        if ((tid & 63) == 0)
+            for (int c = 0; c < kChoices; ++c) part[turn][tid / 64][c] = dot[c];
+        __syncthreads();
+        // `turn` keeps the next choices' sums apart, so one barrier is enough
+        if (live && lane < kChoices && j + lane < a.topk) {
+            float sum = 0.0f;
+            for (int u = 0; u < a.lanes / 64; ++u) sum += part[turn][tid / 64 + u][lane];
+            a.out_f[slot + j + lane] = sum;
+        }
     }
 }
 
@@ -714,7 +797,7 @@ qlin_status qlin_moe_combine_backward(qlin_row_type rt, int64_t tokens, int64_t 
     a.topk = (int)topk;
     a.rows = (int)rows;
     a.cols = (int)K;
-    a.lanes = 64;
+    a.lanes = std::max(row_lanes(K * es), 64);
     hipStream_t s = static_cast<hipStream_t>(stream);
     const dim3 grid = row_grid(a), block(kRowThreads);
     switch (rt) {
