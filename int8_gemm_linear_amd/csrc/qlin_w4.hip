@@ -1,6 +1,7 @@
 // Entry points of the products with 4-bit weights: checks, and the choice of
 // the kernel.
 #include <algorithm>
+#include <cmath>
 
 #include "qlin_w4.h"
 
@@ -124,37 +125,41 @@ qlin_status launch(w4::Args &a, void *ws, size_t ws_bytes, void *stream)
 
 namespace w4 {
 
-// The tile and the parts of K with the least estimated time.  Two workgroups
-// run on a CU, 512 at once; a round of them takes (stages + 2) x `us`, a last
-// round of half as many 0.65 of that; parts of K cost a second kernel and the
-// traffic of their sums.  `us` is what a stage took with 512 workgroups
-// running.  Of the tiles that were tried (tb 1, 2, 4 x rb 1, 2, 4, K split in
-// 1 to 20) on 51200 x 5120, 10240 x 5120, 5120 x 25600, 2048 x 2048 and 1536 x
-// 8192 with 12 to 256 tokens these three and this choice come within 10% of
-// the best: 32 tokens on 5120 x 25600 34 us in ten parts (one: 251), 256 on
-// 10240 x 5120 53 us in three parts (one: 63).
+// The tile and the parts of K with the least estimated time.  A CU runs `at_once`
+// workgroups of a tile; with so many on every CU a stage takes `us` (`more` where
+// they come in several rounds), with fewer down to 0.4 of that, and starting and
+// ending a workgroup costs four stages.  Parts of K cost another launch and the
+// traffic of their sums.  Of all these tiles with 1 to 20 parts this choice takes
+// 2% longer than the best on average, 13% at most, on eight shapes from 2048 x 2048
+// to 51200 x 5120 and 5120 x 25600 with 12 to 1000 tokens and groups of 64 and
+// 128.  12 tokens on 51200 x 5120: 39 us with rb = 2, 44 us with rb = 1; 32 on
+// 5120 x 25600: 32 us in ten parts, 251 us in one; 500 on 10240 x 5120: 82 us with
+// tb, rb = 4, 2, 89 us with 4, 4; 2048: 277 and 254 us.
 TilePick pick_tile(int64_t M, int64_t N, int64_t K, int64_t experts, int64_t rows)
 {
     static const struct {
-        int tb, rb, ks;
-        double us;
-    } kTiles[] = {{1, 1, 256, 1.6}, {2, 2, 256, 2.4}, {4, 4, 128, 2.7}};
+        int tb, rb, ks, at_once;
+        double us, more;
+    } kTiles[] = {{1, 1, 256, 3, 1.3, 1.3}, {1, 2, 256, 2, 1.5, 1.5}, {2, 1, 256, 3, 1.7, 1.7},
+                  {2, 2, 256, 2, 2.0, 2.0}, {4, 2, 128, 3, 2.0, 2.0}, {4, 4, 128, 2, 2.9, 2.5}};
+    constexpr int kMostParts = 20;
     TilePick best{4, 4, 128, 1};
     double least = 1e30;
     for (const auto &t : kTiles) {
         const int64_t high = 16 * t.tb, stages = (K + t.ks - 1) / t.ks;
         // an expert's last tile is half full on average
         const double tall = experts ? (double)rows / high + 0.5 * std::min(experts, rows) : (double)((M + high - 1) / high);
-        const double tiles = tall * ((N + 64 * t.rb - 1) / (64 * t.rb));
-        const int most = experts ? 1 : (int)std::min<int64_t>(20, std::max<int64_t>(stages / 2, 1));
+        const double each_cu = tall * ((N + 64 * t.rb - 1) / (64 * t.rb)) / 256;
+        const int most = experts ? 1 : (int)std::min<int64_t>(kMostParts, stages);
         for (int splits = 1; splits <= most; ++splits) {
             const int64_t each = (stages + splits - 1) / splits;
             if ((stages + each - 1) / each != splits)
                 continue;                                    // a part would be empty
-            const double rounds = tiles * splits / 512, whole = (double)(int64_t)rounds, rest = rounds - whole;
-            double us = (whole + (rest > 0.5 ? 1.0 : rest > 0.0 ? 0.65 : 0.0)) * (each + 2) * t.us;
+            const double whole = std::floor(each_cu * splits / t.at_once);
+            const double rest = std::ceil(each_cu * splits - whole * t.at_once - 1e-9);
+            double us = (whole + (rest > 0 ? 0.4 + 0.6 * rest / t.at_once : 0)) * (each + 4) * (whole > 0 ? t.more : t.us);
             if (splits > 1)
-                us += 4.0 + splits * (double)M * N * 8 / 5e6;
+                us += 1.0 + splits * (double)M * N * 8 / 5e6;
             if (us < least) {
                 least = us;
                 best = TilePick{t.tb, t.rb, t.ks, splits};

@@ -115,12 +115,7 @@ __host__ __device__ inline Blocks tile_blocks(int gx, int tiles)
 template <int TB, int RB, int KS, int GROUP, int SB, bool ZERO, bool WHOLE>
 __global__ void __launch_bounds__(64 * kTileWaves, 2) k_tile(Args a)
 {
-    // A group of 128 is taken as two of 64 with the same scale: the operands
-    // of 64 codes x 64 rows fit the registers beside everything else, those of
-    // 128 do not (with zero points: 312 us against 218 us at 1000 tokens on
-    // 10240 x 5120).
-    constexpr int SUB = GROUP < 64 ? GROUP : 64;
-    constexpr int H = KS / 128, PIECES = KS / 8, PER = SUB / 32, NS = KS / SUB;
+    constexpr int H = KS / 128, PIECES = KS / 8, PER = GROUP / 32, NS = KS / GROUP;
     constexpr int COPIES = 16 * TB * PIECES / 64;           // 1 KB each
     // Workgroups go to the 8 XCDs in turn, so id mod 8 names the L2: each takes
     // every 8th weight tile, and walks them in blocks of up to 8 token tiles,
@@ -136,7 +131,7 @@ __global__ void __launch_bounds__(64 * kTileWaves, 2) k_tile(Args a)
     if (nx >= gx || y >= a.tiles || !enter_tile<16 * TB>(a, y, m0))
         return;
     __shared__ v4i lds[3][16 * TB * PIECES];
-    __shared__ v4f sums[2][NS][TB * 4];             // [SUB codes][token / 4], times what the codes are too large by
+    __shared__ v4f sums[2][NS][TB * 4];             // [group][token / 4], times what the codes are too large by
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = lane & 15, q = lane >> 4;
@@ -194,7 +189,7 @@ __global__ void __launch_bounds__(64 * kTileWaves, 2) k_tile(Args a)
     };
     int place[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) place[j] = n * PIECES + ((k_of<SUB>(j, q) / 8) ^ n);
+    for (int j = 0; j < 4; ++j) place[j] = n * PIECES + ((k_of<GROUP>(j, q) / 8) ^ n);
 
     const v4i ones = {0x3f803f80, 0x3f803f80, 0x3f803f80, 0x3f803f80};
     auto sum = [&](int buf, int to) {
@@ -235,7 +230,7 @@ __global__ void __launch_bounds__(64 * kTileWaves, 2) k_tile(Args a)
 #pragma unroll
         for (int h = 0; h < H; ++h) {
 #pragma unroll
-            for (int r = 0; r < RB; ++r) quarters<SUB>(cur.w[r][h]);
+            for (int r = 0; r < RB; ++r) quarters<GROUP>(cur.w[r][h]);
 #pragma unroll
             for (int g = 0; g < 4 / PER; ++g) {
                 const int at = h * (4 / PER) + g;
@@ -243,7 +238,7 @@ __global__ void __launch_bounds__(64 * kTileWaves, 2) k_tile(Args a)
                 float sv[RB];
 #pragma unroll
                 for (int r = 0; r < RB; ++r) {
-                    const uint32_t up = ZERO ? cur.raise(r, n, at * SUB / GROUP) : 0;
+                    const uint32_t up = ZERO ? cur.raise(r, n, at) : 0;
 #pragma unroll
                     for (int i = 0; i < PER; ++i) {
                         // expanded here and not earlier, where registers are not free yet
@@ -254,7 +249,7 @@ __global__ void __launch_bounds__(64 * kTileWaves, 2) k_tile(Args a)
 #pragma unroll
                             for (int j = 0; j < 4; ++j) b[r][i][j] += (int)up;
                     }
-                    sv[r] = cur.scale(r, n, at * SUB / GROUP, a.st);
+                    sv[r] = cur.scale(r, n, at, a.st);
                 }
                 // The products of a token block, while the operands of the
                 // next come from LDS (each into the registers of the one just
@@ -373,9 +368,13 @@ hipError_t tile_whole(const Args &a, hipStream_t s)
 template <int GROUP, int SB, bool ZERO>
 hipError_t tile_pick(const Args &a, hipStream_t s)
 {
-    switch (pick_tile(a.M, a.N, a.K, a.experts, a.rows).tb) {
-    case 1: return tile_whole<1, 1, 256, GROUP, SB, ZERO>(a, s);
-    case 2: return tile_whole<2, 2, 256, GROUP, SB, ZERO>(a, s);
+    const TilePick p = pick_tile(a.M, a.N, a.K, a.experts, a.rows);
+    switch (10 * p.tb + p.rb) {
+    case 11: return tile_whole<1, 1, 256, GROUP, SB, ZERO>(a, s);
+    case 12: return tile_whole<1, 2, 256, GROUP, SB, ZERO>(a, s);
+    case 21: return tile_whole<2, 1, 256, GROUP, SB, ZERO>(a, s);
+    case 22: return tile_whole<2, 2, 256, GROUP, SB, ZERO>(a, s);
+    case 42: return tile_whole<4, 2, 128, GROUP, SB, ZERO>(a, s);
     default: return tile_whole<4, 4, 128, GROUP, SB, ZERO>(a, s);
     }
 }
