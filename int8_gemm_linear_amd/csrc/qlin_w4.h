@@ -40,7 +40,8 @@ struct Args {
     int experts;                  // 0 without experts
     int N, K, G;                  // G = K / group
     int st;                       // qlin_scale_type
-    int tiles;                    // tile kernel: token tiles of the grid
+    int tb, rb;                   // tile kernel: the tile,
+    int tiles;                    // token tiles of the grid
     int splits;                   // parts of K, summed by a second kernel
     int split_k;                  // codes of a part
     float *part;                  // [splits][M][N] sums of the parts
@@ -247,17 +248,6 @@ __device__ inline int k_of(int j, int q)
     return GROUP == 128 ? 32 * q + 8 * j
          : GROUP == 64  ? 32 * (2 * (j >> 1) + (q & 1)) + 8 * ((j & 1) + 2 * (q >> 1))
                         : 32 * j + 8 * q;
-}
-
-// The other way: the place among a step's 16 operand pieces (4 j + q) of the
-// eight values starting at k = 8 r.
-template <int GROUP>
-__device__ inline int piece_of(int r)
-{
-    r &= 15;
-    return GROUP == 128 ? 4 * (r & 3) + (r >> 2)
-         : GROUP == 64  ? 8 * (r >> 3) + 4 * (r & 1) + 2 * ((r >> 1) & 1) + ((r >> 2) & 1)
-                        : r;
 }
 
 // The formula's value in fp64, for an output whose fast value is not finite.

@@ -94,18 +94,18 @@ qlin_status launch(w4::Args &a, void *ws, size_t ws_bytes, void *stream)
     // experts: by the rows of a typical one
     if ((a.experts ? a.rows / a.experts : a.M) <= w4::kStreamTokens)
         return kStream[which](a, s) == hipSuccess ? QLIN_OK : QLIN_ERR_HIP;
-    if (!a.experts) {
-        const w4::TilePick p = w4::pick_tile(a.M, a.N, a.K, 0, 0);
-        const size_t need = part_bytes(a.M, a.N, p.splits);
-        if (need && (!ws || ws_bytes < need))
-            return QLIN_ERR_WORKSPACE;
-        if (need && !aligned(ws, 16))
-            return QLIN_ERR_MISALIGNED;
-        const int stages = (a.K + p.ks - 1) / p.ks;
-        a.splits = p.splits;
-        a.split_k = (stages + p.splits - 1) / p.splits * p.ks;
-        a.part = static_cast<float *>(ws);
-    }
+    const w4::TilePick p = w4::pick_tile(a.M, a.N, a.K, a.experts, a.rows);
+    const size_t need = part_bytes(a.M, a.N, p.splits);
+    if (need && (!ws || ws_bytes < need))
+        return QLIN_ERR_WORKSPACE;
+    if (need && !aligned(ws, 16))
+        return QLIN_ERR_MISALIGNED;
+    const int stages = (a.K + p.ks - 1) / p.ks;
+    a.tb = p.tb;
+    a.rb = p.rb;
+    a.splits = p.splits;
+    a.split_k = (stages + p.splits - 1) / p.splits * p.ks;
+    a.part = static_cast<float *>(ws);
     if (kTile[which](a, s) != hipSuccess)
         return QLIN_ERR_HIP;
     if (a.splits > 1) {

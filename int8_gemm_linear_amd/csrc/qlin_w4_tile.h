@@ -368,8 +368,7 @@ hipError_t tile_whole(const Args &a, hipStream_t s)
 template <int GROUP, int SB, bool ZERO>
 hipError_t tile_pick(const Args &a, hipStream_t s)
 {
-    const TilePick p = pick_tile(a.M, a.N, a.K, a.experts, a.rows);
-    switch (10 * p.tb + p.rb) {
+    switch (10 * a.tb + a.rb) {
     case 11: return tile_whole<1, 1, 256, GROUP, SB, ZERO>(a, s);
     case 12: return tile_whole<1, 2, 256, GROUP, SB, ZERO>(a, s);
     case 21: return tile_whole<2, 1, 256, GROUP, SB, ZERO>(a, s);

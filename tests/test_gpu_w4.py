@@ -60,6 +60,87 @@ def test_w4_matches_fp64(M, N, K, group):
         ref.w4_check(y, ref.f64(x), codes, ref.f64(s), z, group, f"{(M, N, K, group, st, zero)}")
 
 
+# the tiles of 16 to 64 tokens and 64 to 256 weight rows, K whole and split,
+# stages of K that end inside a stage and that do not
+TILES = [
+    (9, 700, 640), (9, 700, 768), (40, 16400, 640), (40, 16400, 512), (20, 8200, 96), (20, 8200, 256),
+    (20, 3001, 1152), (20, 3001, 1280), (77, 16400, 640), (77, 16400, 512), (20, 16400, 96), (40, 16400, 256),
+    (96, 3001, 2528), (64, 8200, 2048), (301, 20000, 96), (301, 20000, 256),
+]
+
+
+@pytest.mark.parametrize("M,N,K", TILES)
+def test_w4_every_tile(M, N, K):
+    for i, group in enumerate(g for g in (32, 64, 128) if K % g == 0):
+        st = SCALES[(i + K // 32) % 3]
+        for zero in (False, True):
+            say("tile", M, N, K, group, st, zero)
+            codes, s, z = weights((N,), K, group, st, zero, 31)
+            x = tokens(M, K, 32)
+            a = [dev(t) for t in (x, ref.pack4(codes), s, z)]
+            y = q.w4_mm(*a)
+            assert torch.equal(y, q.w4_mm(*a))
+            # every row of x, a spread of the weights' rows with the first and last ones
+            pick = np.unique(np.concatenate([np.arange(0, N, 97), np.arange(70), np.arange(max(0, N - 140), N)]))
+            ref.w4_check(y[:, torch.from_numpy(pick).cuda()], ref.f64(x), codes[pick], ref.f64(s)[pick],
+                         None if z is None else z[pick], group, f"{(M, N, K, group, st, zero)}")
+
+
+@pytest.mark.parametrize("M", [1, 8, 9, 40, 200])
+def test_w4_values_whose_products_pass_fp32(M):
+    # finite tokens so large that x (128 + q) is not finite in fp32; the formula's value is
+    N, K, group = 96, 512, 128
+    codes, s, z = weights((N,), K, group, torch.float32, True, 41)
+    x = tokens(M, K, 42)
+    x[::2, 5], x[::2, 9] = 2.0 ** 126, -1.5 * 2.0 ** 126
+    say("large", M)
+    y = q.w4_mm(dev(x), dev(ref.pack4(codes)), dev(s), dev(z))
+    ref.w4_check(y, ref.f64(x), codes, ref.f64(s), z, group, f"large {M}")
+
+
+@pytest.mark.parametrize("M", [1, 30, 300])
+def test_w4_upper_bits_of_zero_points_are_not_read(M):
+    N, K, group = 200, 768, 64
+    codes, s, z = weights((N,), K, group, torch.bfloat16, True, 43)
+    x, b, sd = dev(tokens(M, K, 44)), dev(ref.pack4(codes)), dev(s)
+    more = np.random.default_rng(45).integers(0, 16, z.shape, dtype=np.uint8) << 4
+    say("zero points", M)
+    assert torch.equal(q.w4_mm(x, b, sd, dev(z)), q.w4_mm(x, b, sd, dev(z | more)))
+
+
+def test_w4_two_streams_and_two_graphs_with_parts_of_k():
+    # 30 tokens on a long K: every call sums parts in a workspace of its own
+    M, N, K, group = 30, 300, 8192, 128
+    codes, s, z = weights((N,), K, group, torch.bfloat16, False, 46)
+    b, sd = dev(ref.pack4(codes)), dev(s)
+    xs = [dev(tokens(M, K, 47 + i)) for i in range(2)]
+    want = [q.w4_mm(x, b, sd) for x in xs]
+    ref.w4_check(want[0], ref.f64(xs[0]), codes, ref.f64(s), None, group, "parts")
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in range(2)], [[], []]
+    for rep in range(8):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                got[i].append(q.w4_mm(xs[i], b, sd))
+    torch.cuda.synchronize()
+    say("streams")
+    assert all(torch.equal(y, want[i]) for i in range(2) for y in got[i])
+    graphs = []
+    for x in xs:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            y = q.w4_mm(x, b, sd)
+        graphs.append((g, y))
+    for rep in range(3):
+        for (g, _), st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                g.replay()
+        torch.cuda.synchronize()
+        say("graphs", rep)
+        assert all(torch.equal(y, w) for (_, y), w in zip(graphs, want))
+        assert torch.equal(q.w4_mm(xs[0], b, sd), want[0])
+
+
 @pytest.mark.parametrize("M,N,K,group", [(3, 50, 512, 64), (40, 50, 512, 32), (200, 140, 512, 128)])
 def test_w4_strides_and_neighbours(M, N, K, group):
     # rows inside wider buffers, the columns beside them untouched
@@ -153,6 +234,9 @@ GROUPED = [
     ([130, 0, 257, 64, 1], 80, 256, 128),
     ([40, 33, 90], 144, 768, 64),
     ([1] * 40, 33, 256, 32),
+    ([3] * 20 + [60, 0, 200], 1300, 384, 128),
+    ([20, 9, 31, 12] * 12, 700, 512, 64),
+    ([100, 70, 0, 129] * 6, 1030, 160, 32),
 ]
 
 
