@@ -303,6 +303,7 @@ __global__ void __launch_bounds__(64 * kTileWaves, 2) k_tile(Args a)
         par ^= 1;
     }
 
+    wait_loads();                                           // the copies past the end have landed
     // lane (n, q) holds tokens 4 q .. 4 q + 3 of row n
     if (a.splits > 1) {
         float *part = a.part + (int64_t)split * a.M * a.N;
@@ -318,28 +319,48 @@ __global__ void __launch_bounds__(64 * kTileWaves, 2) k_tile(Args a)
             }
         return;
     }
+    // The wave's values change places in LDS, so that lanes store 16 bytes and
+    // 2 RB of them a token's (two bytes each, 16 lanes side by side: 16 000 rows
+    // of 128 experts, N 2048, K 768 118 us).  Rows are 16 bytes longer than
+    // they need to be: the four rows that are written at once are then in
+    // different banks.
+    constexpr int ROW = 16 * RB + 8;
+    static_assert(kTileWaves * 16 * TB * ROW * 2 <= (int)sizeof(lds), "a tile of values");
+    __syncthreads();                                        // the last stage's tokens are read
+    uint16_t *mine = reinterpret_cast<uint16_t *>(lds) + wave * 16 * TB * ROW;
     bool fine = true;
 #pragma unroll
     for (int t = 0; t < TB; ++t)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int m = m0 + 16 * t + 4 * q + i;
-            if (m >= a.M)
-                continue;
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int r = 0; r < RB; ++r) {
-                if (n0 + 16 * r + n < a.N)
-                    a.y[m * a.ldy + n0 + 16 * r + n] = bf16_bits(total[r][t][i]);
+                mine[(16 * t + 4 * q + i) * ROW + 16 * r + n] = bf16_bits(total[r][t][i]);
                 fine = fine && is_finite(total[r][t][i]);
             }
+    if (!fine)
+        // rare: the lane looks its values over again, in a loop that costs no registers above
+        for (int e = 0; e < 4 * TB * RB; ++e) {
+            const int t = 16 * (e / (4 * RB)) + 4 * q + e / RB % 4, c = 16 * (e % RB) + n;
+            uint16_t &v = mine[t * ROW + c];
+            if (m0 + t < a.M && n0 + c < a.N && (v & 0x7f80) == 0x7f80)
+                v = bf16_bits(exact_value(a, m0 + t, n0 + c));
         }
-    if (fine)
-        return;
-    // rare: the lane looks its outputs over again, in a loop that costs no registers above
-    for (int e = 0; e < 4 * TB * RB; ++e) {
-        const int64_t m = m0 + 16 * (e / (4 * RB)) + 4 * q + e / RB % 4, c = n0 + 16 * (e % RB) + n;
-        if (m < a.M && c < a.N && (a.y[m * a.ldy + c] & 0x7f80) == 0x7f80)
-            a.y[m * a.ldy + c] = bf16_bits(exact_value(a, m, c));
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    constexpr int PIECES_OUT = 16 * TB * 2 * RB;
+#pragma unroll
+    for (int i = 0; i < (PIECES_OUT + 63) / 64; ++i) {
+        const int u = 64 * i + lane, t = u / (2 * RB), c = 8 * (u % (2 * RB));
+        if (u >= PIECES_OUT || m0 + t >= a.M || n0 + c >= a.N)
+            continue;
+        const uint16_t *from = mine + t * ROW + c;
+        uint16_t *to = a.y + (m0 + t) * a.ldy + n0 + c;
+        if (n0 + c + 8 <= a.N)
+            __builtin_memcpy(to, from, 16);
+        else
+            for (int k = 0; k < a.N - n0 - c; ++k) to[k] = from[k];
     }
 }
 
