@@ -39,10 +39,16 @@ COPY_BYTES = 256 << 20          # the calibration copy of bench.py --copy-calib
 COPY_TAG = "bitwise_not"        # its kernel is torch's elementwise bitwise_not
 
 
+# sources that no counted workload runs: the 4-bit products and the token routing
+OTHER_SOURCES = ("qlin_w4", "qlin_moe")
+
+
 def fingerprint(table_path: str | None = None) -> str:
-    """sha256 over the kernel sources and the config table in use."""
+    """sha256 over the sources of the 8-bit kernels and the config table in use."""
     h = hashlib.sha256()
     for p in sorted(glob.glob(os.path.join(PKG, "csrc", "*"))):
+        if os.path.basename(p).startswith(OTHER_SOURCES):
+            continue
         h.update(os.path.basename(p).encode())
         with open(p, "rb") as f:
             h.update(f.read())
