@@ -106,11 +106,10 @@ __device__ inline bool enter_tile(Args &a, int y, int &m0)
 
 // Eight codes of one dword -> 128 + q as eight bf16, the nibbles four apart
 // side by side: 0 4 1 5 2 6 3 7.  Seven instructions; the natural order takes
-// ten.  `magic` holds 0x4300 twice in a vector register, which the compiler
+// nine.  `magic` holds 0x4300 twice in a vector register, which the compiler
 // is not told: an instruction takes one constant, and that is the mask.
-__device__ inline uint32_t expand_magic()
+__device__ inline uint32_t expand_magic(uint32_t v)
 {
-    uint32_t v = 0x43004300u;
     asm volatile("" : "+v"(v));
     return v;
 }
@@ -127,21 +126,24 @@ __device__ inline v4i expand8(uint32_t w, uint32_t magic)
 }
 
 // The same in the order of k, for operands that are copied into LDS as they
-// are: a nibble and its upper neighbour are brought 16 bits apart, two pairs
-// at a time.
-__device__ inline v4i expand8_natural(uint32_t w, uint32_t magic)
+// are: nibbles become bytes, `up` (a byte for each, at most 15) is added to
+// them four at a time, and a byte permutation puts pairs beside the upper
+// bytes of 128: nine instructions, eleven with `up`.  `magic` holds 0x43 four
+// times.  (Nibble pairs shifted 16 bits apart, the rest added to each of the
+// four results: ten and fourteen.)
+template <bool UP>
+__device__ inline v4i expand8_natural(uint32_t w, uint32_t magic, uint32_t up)
 {
-    const uint32_t mask = 0x000f000fu;
-    const uint32_t half[2] = {w & 0xffffu, w >> 16};
-    v4i r;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        uint32_t t = half[i] | (half[i] << 12);
-        asm("" : "+v"(t));          // (one instruction; not taken apart to be merged with the masks)
-        r[2 * i] = (int)((t & mask) | magic);
-        r[2 * i + 1] = (int)(((t >> 8) & mask) | magic);
+    uint32_t even = w & 0x0f0f0f0fu, odd = (w >> 4) & 0x0f0f0f0fu;
+    if (UP) {
+        even += up;
+        odd += up;
     }
-    return r;
+    const uint32_t low = __builtin_amdgcn_perm(odd, even, 0x05010400u);
+    const uint32_t high = __builtin_amdgcn_perm(odd, even, 0x07030602u);
+    return v4i{(int)__builtin_amdgcn_perm(low, magic, 0x00050004u), (int)__builtin_amdgcn_perm(low, magic, 0x00070006u),
+               (int)__builtin_amdgcn_perm(high, magic, 0x00050004u),
+               (int)__builtin_amdgcn_perm(high, magic, 0x00070006u)};
 }
 
 // Eight tokens' values in the order of expand8.

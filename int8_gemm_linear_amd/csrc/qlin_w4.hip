@@ -141,7 +141,7 @@ TilePick pick_tile(int64_t M, int64_t N, int64_t K, int64_t experts, int64_t row
         int tb, rb, ks, at_once;
         double us, more;
     } kTiles[] = {{1, 1, 256, 3, 1.3, 1.3}, {1, 2, 256, 2, 1.5, 1.5}, {2, 1, 256, 3, 1.7, 1.7},
-                  {2, 2, 256, 2, 2.0, 2.0}, {4, 2, 128, 3, 2.0, 2.0}, {4, 4, 128, 2, 2.9, 2.5}};
+                  {2, 2, 256, 2, 2.0, 2.0}, {4, 2, 128, 3, 2.0, 2.1}, {4, 4, 128, 2, 2.9, 2.5}};
     constexpr int kMostParts = 20;
     TilePick best{4, 4, 128, 1};
     double least = 1e30;

@@ -92,12 +92,12 @@ struct Codes {
         return scale_value<SB>(SB == 4 ? v : v >> (16 * (i & 1)), st);
     }
 
-    // 15 - z in both halves of a dword: added to expanded codes it makes them
-    // 143 + (q - z), and what has to be taken away the same for all rows.
+    // 15 - z in each byte: added to the codes it makes them 143 + (q - z), and
+    // what has to be taken away the same for all rows.
     __device__ inline uint32_t raise(int r, int n, int i) const
     {
-        const uint32_t up = 15u - ((from_lane(16 * r + n, z[i / 4]) >> (8 * (i & 3))) & 15u);
-        return up | (up << 16);
+        const uint32_t zero = (from_lane(16 * r + n, z[i / 4]) >> (8 * (i & 3))) & 15u;
+        return (15u - zero) * 0x01010101u;
     }
 };
 
@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(64 * kTileWaves, 2) k_tile(Args a)
         }
     };
 
-    const uint32_t magic = expand_magic();
+    const uint32_t magic = expand_magic(0x43434343u);
     Codes<RB, KS, GROUP, SB, ZERO, WHOLE> cur, next;
     stage(kbeg, 0);
     stage(kbeg + KS, 1);
@@ -244,10 +244,7 @@ __global__ void __launch_bounds__(64 * kTileWaves, 2) k_tile(Args a)
                         // expanded here and not earlier, where registers are not free yet
                         uint32_t w = (uint32_t)cur.w[r][h][g * PER + i];
                         asm volatile("" : "+v"(w));
-                        b[r][i] = expand8_natural(w, magic);
-                        if (ZERO)
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) b[r][i][j] += (int)up;
+                        b[r][i] = expand8_natural<ZERO>(w, magic, up);
                     }
                     sv[r] = cur.scale(r, n, at, a.st);
                 }
