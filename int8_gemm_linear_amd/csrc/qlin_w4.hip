@@ -83,6 +83,19 @@ __global__ void __launch_bounds__(256) k_reduce(w4::Args a)
 
 size_t part_bytes(int64_t M, int64_t N, int splits) { return splits > 1 ? (size_t)splits * M * N * sizeof(float) : 0; }
 
+// Whether the streaming kernel takes the call: up to 8 tokens; of experts,
+// which differ in their rows, up to 4 on average, or 8 where a tile of 64
+// weight rows each does not fill the CUs twice.  128 experts on 1536 x 2048
+// with 4 rows each 48 us against 49 us with tiles, with 6 rows 60 and 51 us;
+// 8 experts on 1536 x 4096 with 8 rows each 15 and 16 us.
+bool streams(const w4::Args &a)
+{
+    if (!a.experts)
+        return a.M <= w4::kStreamTokens;
+    const int64_t few = a.experts * (((int64_t)a.N + 63) / 64) <= 512 ? w4::kStreamTokens : w4::kStreamTokens / 2;
+    return a.rows <= few * a.experts;
+}
+
 qlin_status launch(w4::Args &a, void *ws, size_t ws_bytes, void *stream)
 {
     static const w4::Launch kStream[3] = {w4::launch_stream_32, w4::launch_stream_64, w4::launch_stream_128};
@@ -91,8 +104,7 @@ qlin_status launch(w4::Args &a, void *ws, size_t ws_bytes, void *stream)
     const int group = a.K / a.G, which = group == 128 ? 2 : group == 64 ? 1 : 0;
     a.splits = 1;
     a.split_k = a.K;
-    // experts: by the rows of a typical one
-    if ((a.experts ? a.rows / a.experts : a.M) <= w4::kStreamTokens)
+    if (streams(a))
         return kStream[which](a, s) == hipSuccess ? QLIN_OK : QLIN_ERR_HIP;
     const w4::TilePick p = w4::pick_tile(a.M, a.N, a.K, a.experts, a.rows);
     const size_t need = part_bytes(a.M, a.N, p.splits);
@@ -135,20 +147,27 @@ namespace w4 {
 // 128.  12 tokens on 51200 x 5120: 39 us with rb = 2, 44 us with rb = 1; 32 on
 // 5120 x 25600: 32 us in ten parts, 251 us in one; 500 on 10240 x 5120: 82 us with
 // tb, rb = 4, 2, 89 us with 4, 4; 2048: 277 and 254 us.
+// With experts, whose rows differ, no tile is higher than 1.5 times their mean
+// (25 rows each of 128 experts on 1536 x 2048: 88 us with tb = 2, 105 us with 4);
+// this choice is then 1% off the best on average, 8 to 128 experts with 2 to
+// 150 rows each.
 TilePick pick_tile(int64_t M, int64_t N, int64_t K, int64_t experts, int64_t rows)
 {
     static const struct {
         int tb, rb, ks, at_once;
         double us, more;
-    } kTiles[] = {{1, 1, 256, 3, 1.3, 1.3}, {1, 2, 256, 2, 1.5, 1.5}, {2, 1, 256, 3, 1.7, 1.7},
+    } kTiles[] = {{1, 1, 256, 3, 1.3, 1.3}, {1, 2, 256, 2, 1.55, 1.55}, {2, 1, 256, 3, 1.7, 1.7},
                   {2, 2, 256, 2, 2.0, 2.0}, {4, 2, 128, 3, 2.0, 2.1}, {4, 4, 128, 2, 2.9, 2.5}};
     constexpr int kMostParts = 20;
     TilePick best{4, 4, 128, 1};
     double least = 1e30;
     for (const auto &t : kTiles) {
         const int64_t high = 16 * t.tb, stages = (K + t.ks - 1) / t.ks;
-        // an expert's last tile is half full on average
-        const double tall = experts ? (double)rows / high + 0.5 * std::min(experts, rows) : (double)((M + high - 1) / high);
+        // each expert that has rows has a tile, and its last one is half full on average
+        const double mean = experts ? (double)rows / experts : 0;
+        if (t.tb > 1 && experts && high > 1.5 * mean)
+            continue;
+        const double tall = experts ? experts * std::max(std::min(1.0, mean), mean / high + 0.5) : (double)((M + high - 1) / high);
         const double each_cu = tall * ((N + 64 * t.rb - 1) / (64 * t.rb)) / 256;
         const int most = experts ? 1 : (int)std::min<int64_t>(kMostParts, stages);
         for (int splits = 1; splits <= most; ++splits) {

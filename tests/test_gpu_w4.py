@@ -237,6 +237,9 @@ GROUPED = [
     ([3] * 20 + [60, 0, 200], 1300, 384, 128),
     ([20, 9, 31, 12] * 12, 700, 512, 64),
     ([100, 70, 0, 129] * 6, 1030, 160, 32),
+    ([70, 33, 0, 90] * 16, 1300, 320, 64),
+    ([25, 10, 31, 40] * 16, 1300, 256, 128),
+    ([1, 9, 0, 14, 20, 3] * 20, 1100, 192, 32),
 ]
 
 
