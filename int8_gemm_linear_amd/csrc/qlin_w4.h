@@ -206,6 +206,18 @@ __device__ inline v4i from_lane(int lane, v4i v)
     return r;
 }
 
+// Eight lanes load a row's 128-byte line, lane l (of 64) its 16 bytes
+// line_piece(l); lane (n, q) finds the 16 bytes 4 (n / 8) + q of row n mod 8 in
+// lane from_line(n, q).  The upper 32 lanes have their pieces in pairs the other
+// way round (still 64 bytes for four lanes in a row): half a wave then asks 32
+// different banks, not each of 16 twice.
+__device__ inline int line_piece(int lane) { return (lane & 7) ^ ((lane >> 4) & 2); }
+__device__ inline int from_line(int n, int q) { return 8 * (n & 7) + ((4 * (n >> 3) + q) ^ ((n >> 1) & 2)); }
+
+// The same for half lines, four lanes each: 16 bytes q of row n.
+__device__ inline int half_piece(int lane) { return (lane & 3) ^ ((lane >> 4) & 2); }
+__device__ inline int from_half(int n, int q) { return 4 * n + (q ^ ((n >> 2) & 2)); }
+
 // Two 16-byte loads of whole 128-byte lines, rows 0..7 and 8..15 of a block:
 // lane (n, q) of a load has row n mod 8 and the 16 bytes q of the line's
 // first half (n < 8) or second half (n >= 8).  Afterwards `a` holds the first

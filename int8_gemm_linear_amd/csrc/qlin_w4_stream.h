@@ -9,10 +9,10 @@
 // four lanes in a row ask for together, and 64 accesses for lanes that each
 // ask elsewhere; with loads in the order of the matrix operands those accesses
 // alone took 34 us for 131 MB.  So lane l loads 16 bytes l mod 8 of row l / 8
-// (of 8 weight rows, or of 8 tokens), and one scale load covers 32 rows x the
-// slot's two halves.  Afterwards lane (n, q) takes from lane 8 (n mod 8) +
-// 4 (n / 8) + q: the 16 bytes q of row n mod 8's first half line for n < 8,
-// of its second for n >= 8.  Columns 0..7 of a product are then 8 rows over
+// (of 8 weight rows, or of 8 tokens; bytes in the order of line_piece), and one
+// scale load covers 32 rows x the slot's two halves.  Afterwards lane (n, q)
+// takes the 16 bytes q of row n mod 8's first half line for n < 8, of its second
+// for n >= 8.  Columns 0..7 of a product are then 8 rows over
 // the slot's first 128 codes, columns 8..15 the same rows over the other 128,
 // and the token operand has the 8 tokens' first 128 values in rows 0..7 and
 // the other 128 in rows 8..15.  The two diagonal 8 x 8 blocks are wanted, the
@@ -74,7 +74,7 @@ struct Slot {
             return;
         }
         // past the end of K the tokens are made zeros and any codes do
-        const int seg = lane & 7;
+        const int seg = line_piece(lane);
         const int over = max(k0 + 32 * seg - (a.K - 32), 0);
 #pragma unroll
         for (int u = 0; u < U; ++u) w[u] = ld_nt(o.wbase + (k0 - over) / 2 + o.w[u]);
@@ -132,7 +132,7 @@ __device__ inline void add_slot(v4f *total, Slot<U, GROUP, SB, ZERO, WHOLE> &slo
     constexpr int PER = GROUP / 32;                 // matrix instructions of a group
     const v4i ones = {0x3f803f80, 0x3f803f80, 0x3f803f80, 0x3f803f80};
     const int n = lane & 15, q = lane >> 4;
-    const int from = 8 * (n & 7) + 4 * (n >> 3) + q, from_s = 2 * (n & 7) + (n >> 3);
+    const int from = from_line(n, q), from_s = 2 * (n & 7) + (n >> 3);
     slot.arrive();
     v4i x[4], w[U];
 #pragma unroll
@@ -153,6 +153,8 @@ __device__ inline void add_slot(v4f *total, Slot<U, GROUP, SB, ZERO, WHOLE> &slo
         sum_x[g] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int i = 0; i < PER; ++i) sum_x[g] = mma(x[g * PER + i], ones, sum_x[g]);
+        if (!ZERO)
+            sum_x[g] *= -136.0f;
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -170,14 +172,15 @@ __device__ inline void add_slot(v4f *total, Slot<U, GROUP, SB, ZERO, WHOLE> &slo
         }
 #pragma unroll
         for (int g = 0; g < 4 / PER; ++g) {
-            v4f acc = {0.0f, 0.0f, 0.0f, 0.0f};
+            v4f acc = sum_x[g];                     // what the codes are too large by, times x
+            if (ZERO)
+                acc *= -128.0f - (float)((z >> (8 * g)) & 15u);
 #pragma unroll
             for (int i = 0; i < PER; ++i)
                 acc = mma(x[g * PER + i], expand8((uint32_t)w[u][g * PER + i], magic), acc);
             const float sv = scale_value<SB>(SB == 4 ? s[g] : S::NG == 1 ? s[0] : s[g / 2] >> (16 * (g & 1)), a.st);
-            const float zv = ZERO ? -128.0f - (float)((z >> (8 * g)) & 15u) : -136.0f;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) total[u][i] = fmaf(sv, fmaf(zv, sum_x[g][i], acc[i]), total[u][i]);
+            for (int i = 0; i < 4; ++i) total[u][i] = fmaf(sv, acc[i], total[u][i]);
         }
     }
 }
@@ -201,10 +204,10 @@ __global__ void __launch_bounds__(64 * kStreamWaves) k_stream(Args a)
     o.sbase = a.scale + (int64_t)n0 * a.G * SB;
     o.zbase = ZERO ? a.zero + (int64_t)n0 * a.G : nullptr;
     // rows past the end repeat the last; absent tokens' compute what nobody reads
-    o.x = (uint32_t)min(lane >> 3, tokens - 1) * (uint32_t)(2 * a.ldx) + 256 * ((lane >> 2) & 1) + 16 * (lane & 3);
+    o.x = (uint32_t)min(lane >> 3, tokens - 1) * (uint32_t)(2 * a.ldx) + 256 * ((lane >> 2) & 1) + 16 * (line_piece(lane) & 3);
 #pragma unroll
     for (int u = 0; u < U; ++u)
-        o.w[u] = (uint32_t)min(8 * u + (lane >> 3), a.N - 1 - n0) * (uint32_t)a.ldb + 16 * (lane & 7);
+        o.w[u] = (uint32_t)min(8 * u + (lane >> 3), a.N - 1 - n0) * (uint32_t)a.ldb + 16 * line_piece(lane);
 #pragma unroll
     for (int l = 0; l < SL; ++l) {
         o.z[l] = (uint32_t)min(32 * l + min(lane >> 1, 8 * U - 1), a.N - 1 - n0) * (uint32_t)a.G;
@@ -286,14 +289,18 @@ hipError_t stream_pick(const Args &a, hipStream_t s)
     // 32 tokens through 128 experts of 1536 x 2048: - / 39.8 / 35.9.
     // Waves: as many as K has slots while workgroups are few, one or two when
     // they fill the GPU by themselves (the experts: 35.9 with two, 40.3 with
-    // four).
+    // four).  Where K is long and the tokens are several, reading them again is
+    // what costs, and 32 rows share it: 8 tokens on 5120 x 25600 27.7 against
+    // 36 us with 16 rows, on 5120 x 8192 10.4 and 11.5 (one token 10.2 and 9.8).
     const int64_t units = (int64_t)((a.N + 7) / 8) * (a.experts ? row_tiles(a, kStreamTokens) : 1);
+    const bool tokens_cost = a.K >= 8192 && (a.experts ? a.rows / a.experts : a.M) > 2;
     const int u = units >= 4096 ? 4 : units > 512 ? 2 : 1;
     const int waves = (int)min(max((6144 * u + units - 1) / units, (int64_t)1), (int64_t)kStreamWaves);
     if (u == 1)
         return launch_stream_as<1, 1, GROUP, SB, ZERO, WHOLE>(a, waves, s);
     if (u == 2)
-        return launch_stream_as<2, 1, GROUP, SB, ZERO, WHOLE>(a, waves, s);
+        return tokens_cost ? launch_stream_as<4, 1, GROUP, SB, ZERO, WHOLE>(a, kStreamWaves, s)
+                           : launch_stream_as<2, 1, GROUP, SB, ZERO, WHOLE>(a, waves, s);
     return launch_stream_as<4, 2, GROUP, SB, ZERO, WHOLE>(a, waves, s);
 }
 

@@ -31,9 +31,9 @@ struct Lane {
 // The codes, scales and zero points of a wave's rows for a stage, as loaded:
 // in an order that is good for the cache (the L1 takes one access for each 64
 // bytes that four lanes in a row ask for together), which a permutation of the
-// lanes turns into the matrix operands'.  Lane l loads 16 bytes l mod 8 of row
-// l / 8 where a stage has whole 128-byte lines (KS = 256, two loads for 16
-// rows), l mod 4 of row l / 4 where it has half lines, and the scales of row l.
+// lanes turns into the matrix operands'.  Eight lanes load a row where a stage
+// has whole 128-byte lines (KS = 256, two loads for 16 rows), four where it has
+// half lines, and lane l the scales of row l.
 // (With loads in the operands' order: 1000 tokens on 10240 x 5120 171 us.)
 template <int RB, int KS, int GROUP, int SB, bool ZERO, bool WHOLE>
 struct Codes {
@@ -58,7 +58,7 @@ struct Codes {
             return;
         }
         // past the end of K the tokens are zeros and any codes do
-        const int over = max(k0 + 32 * (H == 2 ? lane & 7 : lane & 3) - (a.K - 32), 0);
+        const int over = max(k0 + 32 * (H == 2 ? line_piece(lane) : half_piece(lane)) - (a.K - 32), 0);
 #pragma unroll
         for (int r = 0; r < RB; ++r)
 #pragma unroll
@@ -76,7 +76,7 @@ struct Codes {
     // each step of 128 codes.
     __device__ inline void permute(int n, int q)
     {
-        const int from = H == 2 ? 8 * (n & 7) + 4 * (n >> 3) + q : 4 * n + q;
+        const int from = H == 2 ? from_line(n, q) : from_half(n, q);
 #pragma unroll
         for (int r = 0; r < RB; ++r) {
 #pragma unroll
@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(64 * kTileWaves, 2) k_tile(Args a)
 #pragma unroll
         for (int h = 0; h < H; ++h)
             o.w[r][h] = (uint32_t)min(H == 2 ? 16 * r + 8 * h + (lane >> 3) : 16 * r + (lane >> 2), a.N - 1 - first) *
-                            (uint32_t)a.ldb + 16 * (H == 2 ? lane & 7 : lane & 3);
+                            (uint32_t)a.ldb + 16 * (H == 2 ? line_piece(lane) : half_piece(lane));
     }
     o.s = (uint32_t)min(lane & (16 * RB - 1), a.N - 1 - first) * (uint32_t)a.G;
     v4f total[RB][TB];
