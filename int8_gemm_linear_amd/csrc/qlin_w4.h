@@ -280,6 +280,8 @@ __device__ inline float exact_value(const Args &a, int64_t m, int64_t n)
             const float x = __uint_as_float((uint32_t)a.x[m * a.ldx + k] << 16);
             sum += s * (double)(q - z) * (double)x;
         }
+        if (sum != sum)
+            break;                  // and nothing brings it back
     }
     return (float)sum;
 }

@@ -361,6 +361,29 @@ def test_training_step_in_two_streams_and_a_graph():
         step()
 
 
+def test_rows_past_4_gib():
+    # sorted rows 64 Mi elements apart: permute, combine and both gradients on 8 to 10 GiB of rows
+    T, topk, E, K = 40, 2, 7, 130
+    ids = make_ids(T, topk, E, "absent", 8)
+    _, row = ref.sort_reference(ids, E)
+    g = torch.Generator().manual_seed(70)
+    x = torch.randn((T, K), generator=g).to(torch.bfloat16)
+    w = torch.rand((T, topk), generator=g)
+    ld = (1 << 26) + 2
+    say("far rows")
+    far = torch.empty(T * topk * ld, dtype=torch.bfloat16, device="cuda").as_strided((T * topk, K), (ld, 1))
+    far.zero_()
+    r = torch.from_numpy(row).cuda()
+    q.moe_permute(x.cuda(), r, out=far)
+    near, _ = q.moe_permute(x.cuda(), r, out=torch.zeros((T * topk, K), dtype=torch.bfloat16, device="cuda"))
+    assert torch.equal(far, near)
+    assert torch.equal(q.moe_combine(far, r, w.cuda()), q.moe_combine(near, r, w.cuda()))
+    assert torch.equal(q.moe_permute_backward(far, r), q.moe_permute_backward(near, r))
+    dy, dw = q.moe_combine_backward(x.cuda(), near, r, w.cuda(), dy=torch.zeros_like(near))
+    _, fw = q.moe_combine_backward(x.cuda(), near, r, w.cuda(), dy=far)
+    assert torch.equal(far, dy) and torch.equal(fw, dw)
+
+
 def test_quantized_codes_through_the_router_match_the_unsorted_product():
     # int8 codes and their scales dispatched, the grouped product, and back: each
     # row is the single product's, bit for bit up to the combine's one rounding

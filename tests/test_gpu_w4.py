@@ -99,6 +99,40 @@ def test_w4_values_whose_products_pass_fp32(M):
     ref.w4_check(y, ref.f64(x), codes, ref.f64(s), z, group, f"large {M}")
 
 
+@pytest.mark.parametrize("M", [2, 40])
+def test_w4_rows_and_experts_past_4_gib(M):
+    # rows of y 128 Mi elements apart (of few, 1 Gi: 10 and 12 GiB), experts' weights 2 GiB apart
+    N, K, group = 100, 256, 64
+    codes, s, z = weights((3, N), K, group, torch.bfloat16, True, 48)
+    x = tokens(3 * M, K, 49)
+    packed = ref.pack4(codes)
+    say("far", M)
+    ldy = ((1 << 30) if M < 10 else (1 << 27)) + 8
+    rows = max(M, 6)
+    x = torch.cat([x, x])
+    y = torch.empty(rows * ldy, dtype=torch.bfloat16, device="cuda")
+    out = y.as_strided((rows, N), (ldy, 1))
+    q.w4_mm(dev(x[:rows]), dev(packed[0]), dev(s[0]), dev(z[0]), out=out)
+    ref.w4_check(out, ref.f64(x[:rows]), codes[0], ref.f64(s[0]), z[0], group, "far rows")
+    del y, out
+    apart = (1 << 31) + 64
+    b = torch.empty(3 * apart, dtype=torch.uint8, device="cuda").as_strided((3, N, K // 2), (apart, K // 2, 1))
+    b.copy_(dev(packed))
+    off = torch.tensor([0, M, 2 * M, 3 * M], dtype=torch.int32, device="cuda")
+    got = q.grouped_w4_mm(dev(x[:3 * M]), b, dev(s), off, M, dev(z))
+    for e in range(3):
+        ref.w4_check(got[e * M:(e + 1) * M], ref.f64(x[e * M:(e + 1) * M]), codes[e], ref.f64(s[e]), z[e], group,
+                     f"far expert {e}")
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 5120, 8192), (300, 4096, 4096)])
+def test_w4_nothing_but_nan(M, N, K):
+    x = torch.full((M, K), float("nan"), dtype=torch.bfloat16, device="cuda")
+    b, s = torch.zeros((N, K // 2), dtype=torch.uint8, device="cuda"), torch.ones((N, K // 128), device="cuda")
+    say("nan", M, N, K)
+    assert bool(torch.isnan(q.w4_mm(x, b, s)).all())
+
+
 @pytest.mark.parametrize("M", [1, 30, 300])
 def test_w4_upper_bits_of_zero_points_are_not_read(M):
     N, K, group = 200, 768, 64
