@@ -37,20 +37,15 @@ bool aligned(const void *p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0;
 // ---------------------------------------------------------------------------
 constexpr int kSortWaves = 8;                  // x 2048 experts of LDS counters: 64 KB
 constexpr int kSortThreads = 64 * kSortWaves;
-constexpr int64_t kSortOne = 4096;             // slots up to which one workgroup sorts alone
+// Slots up to which one workgroup sorts alone (4096: 7.2 us in one launch and in
+// two; 2048: 4.7 and 7; 8192: 11.9 and 7.4).
+constexpr int64_t kSortOne = 4096;
 constexpr int kSortBlock = 2048;               // slots of a workgroup otherwise, until
 constexpr int kSortMaxBlocks = 256;            // there would be more workgroups than this
 constexpr int kSortHold = 4;                   // ids a thread loads at a time
 
-// The expert of slot i, or -1.
-template <typename ID>
-__device__ inline int expert_of(const ID *ids, int i, int experts)
-{
-    const ID id = ids[i];
-    return id >= 0 && id < (ID)experts ? (int)id : -1;
-}
-
-// The experts of slots i, i + step, ..., -1 from `end` on: all loads, then all uses.
+// The experts of slots i, i + step, ... (an id outside 0..experts-1: -1), -1
+// from `end` on: all loads, then all uses.
 template <typename ID>
 __device__ inline void load_experts(int (&e)[kSortHold], const ID *ids, int i, int step, int end, int experts)
 {
@@ -299,7 +294,9 @@ struct RowArgs {
     int lanes;
 };
 
-// Copies a token's row and scales to its slots' rows, as thread `lane` of its a.lanes.
+// Copies a token's row and scales to its slots' rows, as thread `lane` of its
+// a.lanes: a row is read once and written topk times.  Bound by those bytes:
+// 8191 tokens of 2 KB and 16 scales to 8 rows each 31 us, 4.8 TB/s.
 __device__ inline void copy_token(const RowArgs &a, int token, const int32_t *rows, int lane)
 {
     const uint8_t *x = a.x + (int64_t)token * a.ldx;
@@ -339,9 +336,11 @@ __global__ void __launch_bounds__(kRowThreads) k_moe_permute(RowArgs a)
 }
 
 // Sort and copy in one launch, for few slots: each workgroup counts for its
-// own slots who comes before them (the ids fit LDS; a wave takes a slot, its
+// own slots who comes before them (the ids fit LDS; a wave takes slots, its
 // lanes the ids), and then copies its tokens' rows; the last workgroup makes
-// the offsets.  16 tokens, top-8, 2 KB rows: one launch instead of two.
+// the offsets.  Latency bounds it.  Top-8, 128 experts, 2 KB rows, this and the
+// two (or three) launches: 128 slots 5.0 and 9 us, 1024 7.5 and 9.4, and more
+// slots are counted faster by the sort (2048 in two launches 9.9 us).
 constexpr int kFusedSlots = 1024;
 
 template <typename ID>
@@ -349,7 +348,14 @@ __global__ void __launch_bounds__(kRowThreads) k_moe_dispatch(SortArgs s, RowArg
 {
     __shared__ int32_t expert[kFusedSlots], row[kFusedSlots];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    for (int i = tid; i < s.n; i += kRowThreads) expert[i] = expert_of(static_cast<const ID *>(s.ids), i, s.experts);
+    for (int i = tid; i < s.n; i += kSortHold * kRowThreads) {
+        int e[kSortHold];
+        load_experts(e, static_cast<const ID *>(s.ids), i, kRowThreads, s.n, s.experts);
+#pragma unroll
+        for (int h = 0; h < kSortHold; ++h)
+            if (i + h * kRowThreads < s.n)
+                expert[i + h * kRowThreads] = e[h];
+    }
     __syncthreads();
     if (blockIdx.x == gridDim.x - 1) {
         // offsets[e]: slots with a smaller expert
@@ -383,17 +389,24 @@ __global__ void __launch_bounds__(kRowThreads) k_moe_dispatch(SortArgs s, RowArg
     }
     const int per = kRowThreads / a.lanes;                  // tokens of the workgroup
     const int t0 = blockIdx.x * per, first = t0 * a.topk, last = min(first + per * a.topk, s.n);
-    for (int i = first + wave; i < last; i += kRowThreads / 64) {
-        const int e = expert[i];
-        int before = 0;
+    // four slots a wave at a time: each id read serves all of them
+    for (int i = first + 4 * wave; i < last; i += 4 * kRowThreads / 64) {
+        int e[4], before[4] = {};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) e[c] = expert[min(i + c, last - 1)];
+#pragma unroll 4
         for (int j = lane; j < s.n; j += 64) {
             const int f = expert[j];
-            before += f >= 0 && (f < e || (f == e && j < i)) ? 1 : 0;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) before[c] += f >= 0 && (f < e[c] || (f == e[c] && j < i + c)) ? 1 : 0;
         }
-        before = wave_sum(before);
-        if (lane == 0) {
-            row[i - first] = e >= 0 ? before : -1;
-            s.slot_row[i] = e >= 0 ? before : -1;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            before[c] = wave_sum(before[c]);
+            if (lane == 0 && i + c < last) {
+                row[i + c - first] = e[c] >= 0 ? before[c] : -1;
+                s.slot_row[i + c] = e[c] >= 0 ? before[c] : -1;
+            }
         }
     }
     __syncthreads();
@@ -433,7 +446,8 @@ __device__ inline void load_choices(int (&row)[kChoices], float (&w)[kChoices], 
 }
 
 // out[t] = sum_j w[t,j] y[row[t,j]], the choices in order.  Bound by the rows'
-// bytes: 8191 tokens of 8 rows of 4 KB 4.6 TB/s.
+// bytes: 8191 tokens of 8 rows of 4 KB 60 us, 4.8 TB/s (a row after another:
+// 65 us; 16 tokens 3.8 and 4.2 us, a launch and two latencies).
 template <typename T>
 __global__ void __launch_bounds__(kRowThreads) k_moe_combine(RowArgs a)
 {
@@ -485,7 +499,8 @@ __global__ void __launch_bounds__(kRowThreads) k_moe_combine(RowArgs a)
 // dy[row[t,j]] = w[t,j] dout[t],  dw[t,j] = <dout[t], y[row[t,j]]>: a.lanes
 // threads (whole waves) per token, a piece of dout serving kChoices rows, the
 // dot products summed over the lanes and then the waves in a fixed order.
-// Bound by the bytes of the rows read and written.
+// Bound by the bytes of the rows read and written: 8192 tokens of 8 rows of
+// 4 KB 104 us, 5.3 TB/s (one wave per token, a row after another: 124 us).
 template <typename T>
 __global__ void __launch_bounds__(kRowThreads) k_moe_combine_backward(RowArgs a)
 {

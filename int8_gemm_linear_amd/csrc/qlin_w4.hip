@@ -83,8 +83,9 @@ __global__ void __launch_bounds__(256) k_reduce(w4::Args a)
 
 size_t part_bytes(int64_t M, int64_t N, int splits) { return splits > 1 ? (size_t)splits * M * N * sizeof(float) : 0; }
 
-// Whether the streaming kernel takes the call: up to 8 tokens; of experts,
-// which differ in their rows, up to 4 on average, or 8 where a tile of 64
+// Whether the streaming kernel takes the call: up to 8 tokens (8 on 51200 x 5120
+// 36 us, where the smallest tiles take 40; 12 would have to be streamed twice); of
+// experts, which differ in their rows, up to 4 on average, or 8 where a tile of 64
 // weight rows each does not fill the CUs twice.  128 experts on 1536 x 2048
 // with 4 rows each 48 us against 49 us with tiles, with 6 rows 60 and 51 us;
 // 8 experts on 1536 x 4096 with 8 rows each 15 and 16 us.
@@ -145,8 +146,8 @@ namespace w4 {
 // 2% longer than the best on average, 13% at most, on eight shapes from 2048 x 2048
 // to 51200 x 5120 and 5120 x 25600 with 12 to 1000 tokens and groups of 64 and
 // 128.  12 tokens on 51200 x 5120: 39 us with rb = 2, 44 us with rb = 1; 32 on
-// 5120 x 25600: 32 us in ten parts, 251 us in one; 500 on 10240 x 5120: 82 us with
-// tb, rb = 4, 2, 89 us with 4, 4; 2048: 277 and 254 us.
+// 5120 x 25600: 32 us in ten parts, 251 us in one; 512 on 10240 x 5120: 80 us with
+// tb, rb = 4, 2, 96 us with 4, 4; 2048: 267 and 247 us.
 // With experts, whose rows differ, no tile is higher than 1.5 times their mean
 // (25 rows each of 128 experts on 1536 x 2048: 88 us with tb = 2, 105 us with 4);
 // this choice is then 1% off the best on average, 8 to 128 experts with 2 to

@@ -12,6 +12,14 @@
 //
 // Where M x N is too few tiles for the 256 CUs, K is split over workgroups
 // whose sums a second kernel adds in order.
+//
+// With many tokens the matrix instructions and the vector instructions that
+// expand codes and scale sums take about as long as each other, and two or three
+// waves on a SIMD overlap them: 1000 tokens on 10240 x 5120 138 us, 760 TFLOP/s;
+// 2048 tokens 238 us, 900 TFLOP/s.  With few, it is the time of a stage, from its
+// loads to its products, over the parts of K: 32 tokens on 5120 x 25600 with zero
+// points 35 us.  16 000 rows of 128 experts on 2048 x 768 115 us, 440 TFLOP/s: six
+// stages a tile, which starting and ending it outweigh.
 #pragma once
 
 #include "qlin_w4.h"
@@ -34,7 +42,7 @@ struct Lane {
 // lanes turns into the matrix operands'.  Eight lanes load a row where a stage
 // has whole 128-byte lines (KS = 256, two loads for 16 rows), four where it has
 // half lines, and lane l the scales of row l.
-// (With loads in the operands' order: 1000 tokens on 10240 x 5120 171 us.)
+// (1000 tokens on 10240 x 5120: 167 us, with loads in the operands' order 171.)
 template <int RB, int KS, int GROUP, int SB, bool ZERO, bool WHOLE>
 struct Codes {
     static constexpr int H = KS / 128, NG = KS / GROUP;
@@ -107,7 +115,7 @@ struct Codes {
 // all quarters' the same four.  So the token's upper two bits count down: 0, 3, 2,
 // 1 keeps both apart (with the token itself, 0 to 3, each place of one quarter met
 // one of the other: half as many again LDS cycles, 1000 tokens on 10240 x 5120
-// 145 us).
+// 148 us, so 138 us).
 __device__ inline int mix(int t) { return (4 * (-(t >> 2) & 3)) | (t & 3); }
 
 // A grid of gx weight tiles by `tiles` token tiles: weight tiles per XCD, token
@@ -129,7 +137,7 @@ __global__ void __launch_bounds__(64 * kTileWaves, 2) k_tile(Args a)
     // Workgroups go to the 8 XCDs in turn, so id mod 8 names the L2: each takes
     // every 8th weight tile, and walks them in blocks of up to 8 token tiles,
     // so that what runs at once shares both its weights and its tokens there
-    // (2048 tokens on 10240 x 5120: 287 us against 305 us with all token
+    // (2048 tokens on 10240 x 5120, as it was then: 287 us against 305 us with all token
     // tiles of a weight tile in a row).
     const int gx = (a.N + 64 * RB - 1) / (64 * RB);
     const int per = gridDim.x / a.splits, split = blockIdx.x / per, id = blockIdx.x % per;
@@ -326,8 +334,8 @@ __global__ void __launch_bounds__(64 * kTileWaves, 2) k_tile(Args a)
         return;
     }
     // The wave's values change places in LDS, so that lanes store 16 bytes and
-    // 2 RB of them a token's (two bytes each, 16 lanes side by side: 16 000 rows
-    // of 128 experts, N 2048, K 768 118 us).  Rows are 16 bytes longer than
+    // 2 RB of them a token's (16 000 rows of 128 experts, N 2048, K 768: 119 us;
+    // two bytes each, 16 lanes side by side: 127 us).  Rows are 16 bytes longer than
     // they need to be: the four rows that are written at once are then in
     // different banks.
     constexpr int ROW = 16 * RB + 8;
