@@ -10,6 +10,8 @@ and the current stream.
     Y = scaled_mm(a_q, a_scale, b_q, b_scale)          # FP8_Dynamic / W8A8_INT8
     Y = block_scaled_mm(a_q, a_scale, b_q, b_scale)    # Block_FP8
     Y = w4_mm(x, b_q, b_scale, b_zero)                 # 4-bit weights, bf16 activations
+    rows, scales, off, slot_row = moe_dispatch(x, topk_ids, experts, scale)
+    Y = moe_combine(expert_rows, slot_row, weights)    # grouped products lie between the two
 
 ``a_q`` [M,K] and ``b_q`` [N,K] (torch.float8_e4m3fn or torch.int8, rows
 K-contiguous); fp32 scales ``a_scale`` [M] and ``b_scale`` [N], or for the
