@@ -589,13 +589,14 @@ def grouped_block_scaled_mm(a_q, a_scale, b_q, b_scale, group_offsets, max_rows:
 _SCALE_TYPE = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 
 
-# (the stream object alone takes 2 us to make, half a launch)
+# (the stream object alone takes 2 us to make, half a launch; the current device 0.1 us more than this)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
-def _matrix(t: torch.Tensor, name: str, device) -> int:
-    """The row stride of a 2-D tensor on `device` with contiguous rows."""
+def _matrix(t: torch.Tensor, name: str, device):
+    """(rows, columns, row stride) of a 2-D tensor on `device` with contiguous rows."""
     if t.dim() != 2:
         raise ValueError(f"{name} must be 2-D with contiguous rows")
     rows, cols = t.shape
@@ -604,7 +605,7 @@ def _matrix(t: torch.Tensor, name: str, device) -> int:
         raise ValueError(f"{name} must be 2-D with contiguous rows")
     if t.device != device or not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor, on one device with the others")
-    return ld if rows > 1 else cols                          # a single row's stride says nothing
+    return rows, cols, ld if rows > 1 else cols              # a single row's stride says nothing
 
 
 def _flat(t: torch.Tensor, dtype, shape, name: str, device):
@@ -623,12 +624,12 @@ def _rows_out(out, shape, like, name="out"):
         return like.new_empty(shape), shape[1]               # (0.25 us less than torch.empty)
     if out.dtype != like.dtype or out.shape != shape:
         raise ValueError(f"{name} must be a {like.dtype} tensor of shape {tuple(shape)}")
-    return out, _matrix(out, name, like.device)
+    return out, _matrix(out, name, like.device)[2]
 
 
 def _call_on(device, fn, args, what):
     """_call with `device`'s current stream as the last argument."""
-    if device.index == torch.cuda.current_device():
+    if device.index == _current_device():
         st = fn(*args, _raw_stream(device.index))
     else:
         with torch.cuda.device(device):
@@ -642,13 +643,14 @@ def _w4_scales(b_scale, b_zero, lead, K, device):
     st = _SCALE_TYPE.get(b_scale.dtype)
     if st is None:
         raise TypeError(f"b_scale must be float32, bfloat16 or float16, got {b_scale.dtype}")
-    cols = b_scale.shape[-1] if b_scale.dim() else 0
+    shape = b_scale.shape
+    cols = shape[-1] if shape else 0
     group = K // cols if cols else 0
-    if b_scale.dim() != len(lead) + 1 or group * cols != K or group not in (32, 64, 128):
+    if group not in (32, 64, 128) or group * cols != K or shape != (*lead, cols):
         raise ValueError(f"b_scale must be [..., N, K/group] with a group of 32, 64 or 128, "
-                         f"got {tuple(b_scale.shape)} for K = {K}")
-    shape = (*lead, cols)
-    _flat(b_scale, b_scale.dtype, shape, "b_scale", device)
+                         f"got {tuple(shape)} for N = {lead[-1]}, K = {K}")
+    if b_scale.device != device or not b_scale.is_contiguous():
+        raise ValueError("b_scale must be contiguous, on one device with the others")
     if b_zero is None:
         return group, st, None
     _flat(b_zero, torch.uint8, shape, "b_zero", device)
@@ -666,9 +668,8 @@ def w4_mm(x, b_q, b_scale, b_zero=None, out=None):
     if b_q.dtype != torch.uint8:
         raise TypeError(f"b_q must be uint8, got {b_q.dtype}")
     dev = x.device
-    ldx, ldb = _matrix(x, "x", dev), _matrix(b_q, "b_q", dev)
-    M, K = x.shape
-    N, half = b_q.shape
+    M, K, ldx = _matrix(x, "x", dev)
+    N, half, ldb = _matrix(b_q, "b_q", dev)
     if half * 2 != K:
         raise ValueError("x is [M,K] and b_q must be [N,K/2]")
     group, st, zero = _w4_scales(b_scale, b_zero, (N,), K, dev)
@@ -677,9 +678,9 @@ def w4_mm(x, b_q, b_scale, b_zero=None, out=None):
     lib = _lib()
     n = lib.qlin_w4_workspace_size(M, N, K)
     ws = b_q.new_empty(n) if n else None
-    _call_on(dev, lib.qlin_w4_mm, [M, N, K, group, x.data_ptr(), ldx, b_q.data_ptr(), ldb, st,
-                                      b_scale.data_ptr(), zero, out.data_ptr(), ldy,
-                                      None if ws is None else ws.data_ptr(), n], "qlin_w4_mm")
+    _call_on(dev, lib.qlin_w4_mm,
+             (M, N, K, group, x.data_ptr(), ldx, b_q.data_ptr(), ldb, st, b_scale.data_ptr(), zero, out.data_ptr(),
+              ldy, None if ws is None else ws.data_ptr(), n), "qlin_w4_mm")
     return out
 
 
@@ -693,12 +694,11 @@ def grouped_w4_mm(x, b_q, b_scale, group_offsets, max_rows: int, b_zero=None, ou
     if b_q.dtype != torch.uint8:
         raise TypeError(f"b_q must be uint8, got {b_q.dtype}")
     dev = x.device
-    ldx = _matrix(x, "x", dev)
+    rows, K, ldx = _matrix(x, "x", dev)
     if b_q.dim() != 3 or b_q.stride(2) != 1 or b_q.device != dev:
         raise ValueError("b_q must be a [G,N,K/2] tensor with contiguous rows, on x's device")
-    rows, K = x.shape
-    G, N = b_q.shape[:2]
-    if b_q.shape[2] * 2 != K:
+    G, N, half = b_q.shape
+    if half * 2 != K:
         raise ValueError("x is [rows,K] and b_q must be [G,N,K/2]")
     group, st, zero = _w4_scales(b_scale, b_zero, (G, N), K, dev)
     _flat(group_offsets, torch.int32, (G + 1,), "group_offsets", dev)
@@ -727,9 +727,10 @@ def _ids(topk_ids, experts):
 
 
 def _slots(slot_row, device):
-    if slot_row.dim() != 2:
-        raise ValueError("slot_row must be [T, topk]")
-    _flat(slot_row, torch.int32, slot_row.shape, "slot_row", device)
+    if slot_row.dtype != torch.int32:
+        raise TypeError(f"slot_row must be int32, got {slot_row.dtype}")
+    if slot_row.dim() != 2 or slot_row.device != device or not slot_row.is_contiguous():
+        raise ValueError("slot_row must be a contiguous [T, topk] tensor, on one device with the others")
     return slot_row.shape
 
 
@@ -763,28 +764,28 @@ def moe_sort(topk_ids, experts: int):
 def _permute_args(x, T, scale, rows, out, out_scale):
     """The sorted rows' buffers (out, out_scale) and the call's row arguments."""
     dev = x.device
-    ldx = _matrix(x, "x", dev)
-    if x.shape[0] != T:
-        raise ValueError(f"x has {x.shape[0]} rows for {T} tokens")
-    K, es = x.shape[1], x.element_size()
+    tokens, K, ldx = _matrix(x, "x", dev)
+    if tokens != T:
+        raise ValueError(f"x has {tokens} rows for {T} tokens")
+    es = x.element_size()
     if out is not None:
         rows = out.shape[0]
     out, ldo = _rows_out(out, (rows, K), x)
-    cols = 0
-    if scale is not None:
+    if scale is None:
+        if out_scale is not None:
+            raise ValueError("out_scale without scale")
+        sc = (None, 0, None)
+    else:
+        rest = scale.shape[1:]
         if scale.dim() not in (1, 2):
             raise ValueError("scale must be [T] or [T, G]")
-        _flat(scale, torch.float32, (T, *scale.shape[1:]), "scale", dev)
-        cols = scale.shape[1] if scale.dim() == 2 else 1
-        shape = (rows, *scale.shape[1:])
+        _flat(scale, torch.float32, (T, *rest), "scale", dev)
         if out_scale is None:
-            out_scale = scale.new_empty(shape)
+            out_scale = scale.new_empty((rows, *rest))
         else:
-            _flat(out_scale, torch.float32, shape, "out_scale", dev)
-    elif out_scale is not None:
-        raise ValueError("out_scale without scale")
-    return out, out_scale, rows, [K * es, x.data_ptr(), ldx * es], [out.data_ptr(), ldo * es], \
-        [None if scale is None else scale.data_ptr(), cols, None if scale is None else out_scale.data_ptr()]
+            _flat(out_scale, torch.float32, (rows, *rest), "out_scale", dev)
+        sc = (scale.data_ptr(), rest[0] if rest else 1, out_scale.data_ptr())
+    return out, out_scale, rows, (K * es, x.data_ptr(), ldx * es), (out.data_ptr(), ldo * es), sc
 
 
 def moe_permute(x, slot_row, scale=None, out=None, out_scale=None):
@@ -824,15 +825,14 @@ def moe_combine(y, slot_row, weights, out=None):
     """The experts' rows brought back: out[t] = sum_j weights[t,j] y[slot_row[t,j]],
     [T,K] of y's type (float32, bfloat16 or float16), fp32 sums in the order of
     j; weights float32 [T, topk].  Absent slots add nothing."""
-    rt = _row_type(y, "y")
-    ldy = _matrix(y, "y", y.device)
-    T, topk = _slots(slot_row, y.device)
-    _flat(weights, torch.float32, (T, topk), "weights", y.device)
-    rows, K = y.shape
+    rt, dev = _row_type(y, "y"), y.device
+    rows, K, ldy = _matrix(y, "y", dev)
+    T, topk = _slots(slot_row, dev)
+    _flat(weights, torch.float32, (T, topk), "weights", dev)
     out, ldo = _rows_out(out, (T, K), y)
-    _call_on(y.device, _lib().qlin_moe_combine,
-             [rt, T, topk, rows, K, y.data_ptr(), ldy, slot_row.data_ptr(), weights.data_ptr(), out.data_ptr(),
-              ldo], "qlin_moe_combine")
+    _call_on(dev, _lib().qlin_moe_combine,
+             (rt, T, topk, rows, K, y.data_ptr(), ldy, slot_row.data_ptr(), weights.data_ptr(), out.data_ptr(),
+              ldo), "qlin_moe_combine")
     return out
 
 
@@ -840,33 +840,32 @@ def moe_combine_backward(dout, y, slot_row, weights, dy=None):
     """Gradients of moe_combine: (dy [rows,K], dweights float32 [T, topk]) from
     dout [T,K] and the call's inputs.  dy's rows of no slot keep what it holds
     (a new dy: anything); dweights is 0 for absent slots."""
-    rt = _row_type(y, "y")
+    rt, dev = _row_type(y, "y"), y.device
     if dout.dtype != y.dtype:
         raise TypeError("dout and y must have the same dtype")
-    ldy, ldo = _matrix(y, "y", y.device), _matrix(dout, "dout", y.device)
-    T, topk = _slots(slot_row, y.device)
-    _flat(weights, torch.float32, (T, topk), "weights", y.device)
-    rows, K = y.shape
-    if tuple(dout.shape) != (T, K):
-        raise ValueError(f"dout has shape {tuple(dout.shape)}, expected {(T, K)}")
+    rows, K, ldy = _matrix(y, "y", dev)
+    tokens, cols, ldo = _matrix(dout, "dout", dev)
+    T, topk = _slots(slot_row, dev)
+    _flat(weights, torch.float32, (T, topk), "weights", dev)
+    if tokens != T or cols != K:
+        raise ValueError(f"dout has shape {(tokens, cols)}, expected {(T, K)}")
     dy, lddy = _rows_out(dy, (rows, K), y, "dy")
     dweights = torch.empty_like(weights)
-    _call_on(y.device, _lib().qlin_moe_combine_backward,
-             [rt, T, topk, rows, K, dout.data_ptr(), ldo, y.data_ptr(), ldy, slot_row.data_ptr(),
-              weights.data_ptr(), dy.data_ptr(), lddy, dweights.data_ptr()], "qlin_moe_combine_backward")
+    _call_on(dev, _lib().qlin_moe_combine_backward,
+             (rt, T, topk, rows, K, dout.data_ptr(), ldo, y.data_ptr(), ldy, slot_row.data_ptr(),
+              weights.data_ptr(), dy.data_ptr(), lddy, dweights.data_ptr()), "qlin_moe_combine_backward")
     return dy, dweights
 
 
 def moe_permute_backward(drows, slot_row, out=None):
     """Gradient of moe_permute: dx[t] = sum_j drows[slot_row[t,j]], [T,K] of
     drows' type, fp32 sums."""
-    rt = _row_type(drows, "drows")
-    ld = _matrix(drows, "drows", drows.device)
-    T, topk = _slots(slot_row, drows.device)
-    rows, K = drows.shape
+    rt, dev = _row_type(drows, "drows"), drows.device
+    rows, K, ld = _matrix(drows, "drows", dev)
+    T, topk = _slots(slot_row, dev)
     out, ldo = _rows_out(out, (T, K), drows)
-    _call_on(drows.device, _lib().qlin_moe_permute_backward,
-             [rt, T, topk, rows, K, drows.data_ptr(), ld, slot_row.data_ptr(), out.data_ptr(), ldo],
+    _call_on(dev, _lib().qlin_moe_permute_backward,
+             (rt, T, topk, rows, K, drows.data_ptr(), ld, slot_row.data_ptr(), out.data_ptr(), ldo),
              "qlin_moe_permute_backward")
     return out
 
