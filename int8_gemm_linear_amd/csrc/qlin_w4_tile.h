@@ -118,15 +118,22 @@ struct Codes {
 // 148 us, so 138 us).
 __device__ inline int mix(int t) { return (4 * (-(t >> 2) & 3)) | (t & 3); }
 
-// A grid of gx weight tiles by `tiles` token tiles: weight tiles per XCD, token
-// tiles per block and blocks.
+// A grid of gx weight tiles by `tiles` token tiles, in chunks of one weight tile
+// by up to 8 token tiles.  Workgroups go to the 8 XCDs in turn, so id mod 8 names
+// the L2: each takes every 8th chunk, so that what runs at once shares both its
+// weights and its tokens there (2048 tokens on 10240 x 5120, as it was then: 287 us
+// against 305 us with all token tiles of a weight tile in a row); the workgroups of
+// the chunks that are left over go to the XCDs one by one (every 8th weight tile to
+// an XCD, and none to some where there are fewer than 8: 9660 rows of 16 experts on
+// 100 x 1152 47 us, so 19 us; 1000 tokens on 5120 x 25600 536 and 435 us).
 struct Blocks {
-    int across, high, blocks;
+    int high, blocks;                   // token tiles of a chunk, such blocks
+    int64_t all;                        // workgroups of a part of K
 };
 __host__ __device__ inline Blocks tile_blocks(int gx, int tiles)
 {
-    const int blocks = (tiles + 7) / 8;
-    return Blocks{(gx + 7) / 8, (tiles + blocks - 1) / blocks, blocks};
+    const int blocks = (tiles + 7) / 8, high = (tiles + blocks - 1) / blocks;
+    return Blocks{high, blocks, ((int64_t)gx * blocks * high + 7) & ~(int64_t)7};
 }
 
 template <int TB, int RB, int KS, int GROUP, int SB, bool ZERO, bool WHOLE>
@@ -134,18 +141,15 @@ __global__ void __launch_bounds__(64 * kTileWaves, 2) k_tile(Args a)
 {
     constexpr int H = KS / 128, PIECES = KS / 8, PER = GROUP / 32, NS = KS / GROUP;
     constexpr int COPIES = 16 * TB * PIECES / 64;           // 1 KB each
-    // Workgroups go to the 8 XCDs in turn, so id mod 8 names the L2: each takes
-    // every 8th weight tile, and walks them in blocks of up to 8 token tiles,
-    // so that what runs at once shares both its weights and its tokens there
-    // (2048 tokens on 10240 x 5120, as it was then: 287 us against 305 us with all token
-    // tiles of a weight tile in a row).
     const int gx = (a.N + 64 * RB - 1) / (64 * RB);
-    const int per = gridDim.x / a.splits, split = blockIdx.x / per, id = blockIdx.x % per;
     const Blocks bl = tile_blocks(gx, a.tiles);
-    const int j = id >> 3, y = j / (bl.across * bl.high) * bl.high + j % bl.high;
-    const int nx = j % (bl.across * bl.high) / bl.high * 8 + (id & 7);
+    const int all = (int)bl.all, split = blockIdx.x / all, id = blockIdx.x % all;
+    const int each = gx * bl.blocks / 8 * bl.high;          // an XCD's workgroups of whole chunks
+    const int j = id >> 3, rest = 8 * each + (j - each) * 8 + (id & 7);
+    const int chunk = j < each ? j / bl.high * 8 + (id & 7) : rest / bl.high;
+    const int nx = chunk % gx, y = chunk / gx * bl.high + (j < each ? j : rest) % bl.high;
     int m0;
-    if (nx >= gx || y >= a.tiles || !enter_tile<16 * TB>(a, y, m0))
+    if (y >= a.tiles || !enter_tile<16 * TB>(a, y, m0))
         return;
     __shared__ v4i lds[3][16 * TB * PIECES];
     __shared__ v4f sums[2][NS][TB * 4];             // [group][token / 4], times what the codes are too large by
@@ -386,7 +390,7 @@ hipError_t launch_tile_as(Args a, hipStream_t s)
         return hipErrorInvalidValue;
     a.tiles = (int)tiles;
     const Blocks bl = tile_blocks((a.N + 64 * RB - 1) / (64 * RB), a.tiles);
-    const int64_t grid = (int64_t)8 * bl.across * bl.high * bl.blocks * a.splits;
+    const int64_t grid = bl.all * a.splits;
     if (grid > 0x7fffffff)
         return hipErrorInvalidValue;
     hipLaunchKernelGGL((k_tile<TB, RB, KS, GROUP, SB, ZERO, WHOLE>), dim3((unsigned)grid), dim3(64 * kTileWaves), 0, s, a);
