@@ -47,6 +47,14 @@ struct Args {
     float *part;                  // [splits][M][N] sums of the parts
 };
 
+// How K ends: with a whole stage (or slot); inside one, which then is the last one's
+// number of codes before the end, those that were had already against zeros; or
+// before one is full, where every load is held inside K by itself.  (K = 6304, 18
+// tokens, N = 40875, groups of 32: 135 us with every load held, so 81 us; a kernel
+// for the first two together costs whole stages 2%, and the streaming kernel with
+// fp32 scales 18%.)
+enum Ends { kWhole, kInside, kShort };
+
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 typedef uint32_t v2u __attribute__((ext_vector_type(2)));
 
@@ -313,6 +321,7 @@ hipError_t launch_tile_128(const Args &a, hipStream_t s);
 struct TilePick {
     int tb, rb, ks, splits;
 };
+constexpr TilePick kShortTile{4, 2, 128, 1};                // for K below a stage of any tile
 TilePick pick_tile(int64_t M, int64_t N, int64_t K, int64_t experts, int64_t rows);
 
 }  // namespace w4

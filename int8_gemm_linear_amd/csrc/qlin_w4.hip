@@ -169,13 +169,13 @@ TilePick pick_tile(int64_t M, int64_t N, int64_t K, int64_t experts, int64_t row
     } kTiles[] = {{1, 1, 256, 3, 1.3, 1.3}, {1, 2, 256, 2, 1.55, 1.55}, {2, 1, 256, 3, 1.7, 1.7},
                   {2, 2, 256, 2, 2.0, 2.0}, {4, 2, 128, 3, 2.0, 2.1}, {4, 4, 128, 2, 2.9, 2.5}};
     constexpr int kMostParts = 20;
-    TilePick best{4, 4, 128, 1};
+    TilePick best = kShortTile;
     double least = 1e30;
     for (const auto &t : kTiles) {
         const int64_t high = 16 * t.tb, stages = (K + t.ks - 1) / t.ks;
         // each expert that has rows has a tile, and its last one is half full on average
         const double mean = experts ? (double)rows / experts : 0;
-        if (t.tb > 1 && experts && high > 1.5 * mean)
+        if ((t.tb > 1 && experts && high > 1.5 * mean && K >= 256) || t.ks > K)
             continue;
         const double tall = experts ? experts * std::max(std::min(1.0, mean), mean / high + 0.5) : (double)((M + high - 1) / high);
         const double each_cu = tall * ((N + 64 * t.rb - 1) / (64 * t.rb)) / 256;

@@ -47,7 +47,7 @@ struct Lane {
 };
 
 // A slot's codes, scales, zero points and token operands, as loaded.  WHOLE: K
-// is whole slots, and a slot past the end reads the last one instead.
+// has 256 codes at least, and a slot that would pass its end is the last 256.
 template <int U, int GROUP, int SB, bool ZERO, bool WHOLE>
 struct Slot {
     static constexpr int NG = 128 / GROUP;          // groups of a half
@@ -129,10 +129,11 @@ struct Slot {
 // total += the slot's products.
 // An instruction takes 32 codes in a row, which keeps the token loads in whole
 // pieces of 64 bytes, whatever the group.
-template <int U, int GROUP, int SB, bool ZERO, bool WHOLE>
-__device__ inline void add_slot(v4f *total, Slot<U, GROUP, SB, ZERO, WHOLE> &slot, int k0, const Args &a,
+template <int U, int GROUP, int SB, bool ZERO, int ENDS>
+__device__ inline void add_slot(v4f *total, Slot<U, GROUP, SB, ZERO, ENDS != kShort> &slot, int k0, const Args &a,
                                 int lane, uint32_t magic)
 {
+    constexpr bool WHOLE = ENDS != kShort;
     typedef Slot<U, GROUP, SB, ZERO, WHOLE> S;
     constexpr int PER = GROUP / 32;                 // matrix instructions of a group
     const v4i ones = {0x3f803f80, 0x3f803f80, 0x3f803f80, 0x3f803f80};
@@ -146,6 +147,15 @@ __device__ inline void add_slot(v4f *total, Slot<U, GROUP, SB, ZERO, WHOLE> &slo
         if (!WHOLE && k0 + 128 * (n >> 3) + 32 * j + 8 * q >= a.K)
             x[j] = zero4i();
         x[j] = operand_order(x[j]);
+    }
+    const int at = ENDS == kInside ? min(k0, a.K - kSlot) : k0;
+    if (ENDS == kInside && at < k0) {
+        // K ends inside the slot, which holds its last 256 codes: the slot
+        // before has had these values already
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (at + 128 * (n >> 3) + 32 * j + 8 * q < k0)
+                x[j] = zero4i();
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -173,7 +183,7 @@ __device__ inline void add_slot(v4f *total, Slot<U, GROUP, SB, ZERO, WHOLE> &slo
         if (ZERO) {
             z = from_lane(from_s + 16 * (u & 3), slot.z[u / 4]);
             if (WHOLE && S::NG < 4)
-                z >>= 8 * (S::NG * half + (S::NG == 1 ? max(k0 / GROUP - (a.G - 4), 0) : 0));
+                z >>= 8 * (S::NG * half + (S::NG == 1 ? max(at / GROUP - (a.G - 4), 0) : 0));
         }
 #pragma unroll
         for (int g = 0; g < 4 / PER; ++g) {
@@ -190,9 +200,10 @@ __device__ inline void add_slot(v4f *total, Slot<U, GROUP, SB, ZERO, WHOLE> &slo
     }
 }
 
-template <int U, int AHEAD, int GROUP, int SB, bool ZERO, bool WHOLE>
+template <int U, int AHEAD, int GROUP, int SB, bool ZERO, int ENDS>
 __global__ void __launch_bounds__(64 * kStreamWaves) k_stream(Args a)
 {
+    constexpr bool WHOLE = ENDS != kShort;
     const int gx = (a.N + 8 * U - 1) / (8 * U);
     int m0;
     if (!enter_tile<kStreamTokens>(a, blockIdx.x / gx, m0))
@@ -235,7 +246,7 @@ __global__ void __launch_bounds__(64 * kStreamWaves) k_stream(Args a)
     for (int i = 0; i < left / AHEAD; ++i) {
 #pragma unroll
         for (int d = 0; d < AHEAD; ++d) {
-            add_slot(total, slot[d], k0, a, lane, magic);
+            add_slot<U, GROUP, SB, ZERO, ENDS>(total, slot[d], k0, a, lane, magic);
             // unconditional, so that waits stay counted: past the end of K it
             // reads the row's last line again
             slot[d].load(a, o, k0 + AHEAD * stride, lane);
@@ -247,7 +258,7 @@ __global__ void __launch_bounds__(64 * kStreamWaves) k_stream(Args a)
 #pragma unroll
     for (int d = 0; d < AHEAD - 1; ++d)
         if (d < left % AHEAD) {
-            add_slot(total, slot[d], k0, a, lane, magic);
+            add_slot<U, GROUP, SB, ZERO, ENDS>(total, slot[d], k0, a, lane, magic);
             k0 += stride;
         }
 
@@ -271,19 +282,19 @@ __global__ void __launch_bounds__(64 * kStreamWaves) k_stream(Args a)
     }
 }
 
-template <int U, int AHEAD, int GROUP, int SB, bool ZERO, bool WHOLE>
+template <int U, int AHEAD, int GROUP, int SB, bool ZERO, int ENDS>
 hipError_t launch_stream_as(const Args &a, int waves, hipStream_t s)
 {
     const int64_t grid = (int64_t)((a.N + 8 * U - 1) / (8 * U)) * row_tiles(a, kStreamTokens);
     if (grid > 0x7fffffff)
         return hipErrorInvalidValue;
     waves = min(waves, (a.K + kSlot - 1) / kSlot);
-    hipLaunchKernelGGL((k_stream<U, AHEAD, GROUP, SB, ZERO, WHOLE>), dim3((unsigned)grid), dim3(64 * waves),
+    hipLaunchKernelGGL((k_stream<U, AHEAD, GROUP, SB, ZERO, ENDS>), dim3((unsigned)grid), dim3(64 * waves),
                        waves * U * 512, s, a);
     return hipGetLastError();
 }
 
-template <int GROUP, int SB, bool ZERO, bool WHOLE>
+template <int GROUP, int SB, bool ZERO, int ENDS>
 hipError_t stream_pick(const Args &a, hipStream_t s)
 {
     // More rows a workgroup share one read of the tokens and one start, fewer
@@ -302,26 +313,28 @@ hipError_t stream_pick(const Args &a, hipStream_t s)
     const int u = units >= 4096 ? 4 : units > 512 ? 2 : 1;
     const int waves = (int)min(max((6144 * u + units - 1) / units, (int64_t)1), (int64_t)kStreamWaves);
     if (u == 1)
-        return launch_stream_as<1, 1, GROUP, SB, ZERO, WHOLE>(a, waves, s);
+        return launch_stream_as<1, 1, GROUP, SB, ZERO, ENDS>(a, waves, s);
     if (u == 2)
-        return tokens_cost ? launch_stream_as<4, 1, GROUP, SB, ZERO, WHOLE>(a, kStreamWaves, s)
-                           : launch_stream_as<2, 1, GROUP, SB, ZERO, WHOLE>(a, waves, s);
-    return launch_stream_as<4, 2, GROUP, SB, ZERO, WHOLE>(a, waves, s);
+        return tokens_cost ? launch_stream_as<4, 1, GROUP, SB, ZERO, ENDS>(a, kStreamWaves, s)
+                           : launch_stream_as<2, 1, GROUP, SB, ZERO, ENDS>(a, waves, s);
+    return launch_stream_as<4, 2, GROUP, SB, ZERO, ENDS>(a, waves, s);
 }
 
 template <int GROUP, int SB, bool ZERO>
-hipError_t stream_whole(const Args &a, hipStream_t s)
+hipError_t stream_ends(const Args &a, hipStream_t s)
 {
     // (a dword of zero points needs four groups)
-    return a.K % kSlot == 0 && a.G >= 4 ? stream_pick<GROUP, SB, ZERO, true>(a, s) : stream_pick<GROUP, SB, ZERO, false>(a, s);
+    if (a.K < kSlot || a.G < 4)
+        return stream_pick<GROUP, SB, ZERO, kShort>(a, s);
+    return a.K % kSlot == 0 ? stream_pick<GROUP, SB, ZERO, kWhole>(a, s) : stream_pick<GROUP, SB, ZERO, kInside>(a, s);
 }
 
 template <int GROUP>
 hipError_t stream_any(const Args &a, hipStream_t s)
 {
     if (a.st == QLIN_SCALE_F32)
-        return a.zero ? stream_whole<GROUP, 4, true>(a, s) : stream_whole<GROUP, 4, false>(a, s);
-    return a.zero ? stream_whole<GROUP, 2, true>(a, s) : stream_whole<GROUP, 2, false>(a, s);
+        return a.zero ? stream_ends<GROUP, 4, true>(a, s) : stream_ends<GROUP, 4, false>(a, s);
+    return a.zero ? stream_ends<GROUP, 2, true>(a, s) : stream_ends<GROUP, 2, false>(a, s);
 }
 
 }  // namespace w4

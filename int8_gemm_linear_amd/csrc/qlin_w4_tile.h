@@ -136,9 +136,10 @@ __host__ __device__ inline Blocks tile_blocks(int gx, int tiles)
     return Blocks{high, blocks, ((int64_t)gx * blocks * high + 7) & ~(int64_t)7};
 }
 
-template <int TB, int RB, int KS, int GROUP, int SB, bool ZERO, bool WHOLE>
+template <int TB, int RB, int KS, int GROUP, int SB, bool ZERO, int ENDS>
 __global__ void __launch_bounds__(64 * kTileWaves, 2) k_tile(Args a)
 {
+    constexpr bool WHOLE = ENDS != kShort;
     constexpr int H = KS / 128, PIECES = KS / 8, PER = GROUP / 32, NS = KS / GROUP;
     constexpr int COPIES = 16 * TB * PIECES / 64;           // 1 KB each
     const int gx = (a.N + 64 * RB - 1) / (64 * RB);
@@ -186,13 +187,13 @@ __global__ void __launch_bounds__(64 * kTileWaves, 2) k_tile(Args a)
     const int copy_t = (wave * 64 + lane) / PIECES, copy_p = lane % PIECES;
     const int copy_piece = (copy_p ^ mix(copy_t)) & 15;
     static_assert(256 / PIECES % 16 == 0 || 256 / PIECES == 8, "tokens of a wave's copies");
+    // (eight tokens on, bit 3 of the exchange is the other)
+    auto piece_at = [&](int i) { return 256 / PIECES == 8 ? copy_piece ^ (8 * (i & 1)) : copy_piece; };
     uint32_t copy_x[COPIES / kTileWaves];                   // bytes from the first token at code 0
 #pragma unroll
     for (int i = 0; i < COPIES / kTileWaves; ++i) {
-        // eight tokens on, bit 3 of the exchange is the other
-        const int piece = 256 / PIECES == 8 ? copy_piece ^ (8 * (i & 1)) : copy_piece;
         copy_x[i] = (uint32_t)min(copy_t + i * (256 / PIECES), a.M - 1 - m0) * (uint32_t)(2 * a.ldx) +
-                    256 * (copy_p >> 4) + 16 * piece;
+                    256 * (copy_p >> 4) + 16 * piece_at(i);
     }
     const uint8_t *xbase = reinterpret_cast<const uint8_t *>(a.x + (int64_t)m0 * a.ldx);
     auto stage = [&](int k0, int buf) {
@@ -201,8 +202,7 @@ __global__ void __launch_bounds__(64 * kTileWaves, 2) k_tile(Args a)
 #pragma unroll
         for (int i = 0; i < COPIES / kTileWaves; ++i) {
             v4i *to = &lds[buf][(i * kTileWaves + wave) * 64];
-            const int piece = 256 / PIECES == 8 ? copy_piece ^ (8 * (i & 1)) : copy_piece;
-            if (WHOLE || k0 + 128 * (copy_p >> 4) + 8 * piece < kend)
+            if (WHOLE || k0 + 128 * (copy_p >> 4) + 8 * piece_at(i) < kend)
                 lds_dma16_at(xbase + 2 * (int64_t)k0, copy_x[i], to);
             else
                 to[lane] = zero4i();
@@ -246,6 +246,17 @@ __global__ void __launch_bounds__(64 * kTileWaves, 2) k_tile(Args a)
         // the next stage's tokens have landed; this stage's sums are there; the last stage's buffer is free
         wait_loads();
         __syncthreads();
+        if (ENDS == kInside && k0 > a.K - KS) {
+            // K ends inside the stage, which holds its last KS codes: the
+            // tokens' values that the stage before had already are made zeros
+#pragma unroll
+            for (int i = 0; i < COPIES / kTileWaves; ++i)
+                if (a.K - KS + 128 * (copy_p >> 4) + 8 * piece_at(i) < k0)
+                    lds[buf][(i * kTileWaves + wave) * 64 + lane] = zero4i();
+            __syncthreads();
+            sum(buf, par);
+            __syncthreads();
+        }
         const v4i *xs = lds[buf];
         cur.permute(n, q);
 #pragma unroll
@@ -382,7 +393,7 @@ __global__ void __launch_bounds__(64 * kTileWaves, 2) k_tile(Args a)
     }
 }
 
-template <int TB, int RB, int KS, int GROUP, int SB, bool ZERO, bool WHOLE>
+template <int TB, int RB, int KS, int GROUP, int SB, bool ZERO, int ENDS>
 hipError_t launch_tile_as(Args a, hipStream_t s)
 {
     const int64_t tiles = row_tiles(a, 16 * TB);
@@ -393,27 +404,30 @@ hipError_t launch_tile_as(Args a, hipStream_t s)
     const int64_t grid = bl.all * a.splits;
     if (grid > 0x7fffffff)
         return hipErrorInvalidValue;
-    hipLaunchKernelGGL((k_tile<TB, RB, KS, GROUP, SB, ZERO, WHOLE>), dim3((unsigned)grid), dim3(64 * kTileWaves), 0, s, a);
+    hipLaunchKernelGGL((k_tile<TB, RB, KS, GROUP, SB, ZERO, ENDS>), dim3((unsigned)grid), dim3(64 * kTileWaves), 0, s, a);
     return hipGetLastError();
 }
 
 template <int TB, int RB, int KS, int GROUP, int SB, bool ZERO>
-hipError_t tile_whole(const Args &a, hipStream_t s)
+hipError_t tile_ends(const Args &a, hipStream_t s)
 {
-    return a.K % KS == 0 ? launch_tile_as<TB, RB, KS, GROUP, SB, ZERO, true>(a, s)
-                         : launch_tile_as<TB, RB, KS, GROUP, SB, ZERO, false>(a, s);
+    if (a.K % KS == 0)
+        return launch_tile_as<TB, RB, KS, GROUP, SB, ZERO, kWhole>(a, s);
+    return launch_tile_as<TB, RB, KS, GROUP, SB, ZERO, kInside>(a, s);
 }
 
 template <int GROUP, int SB, bool ZERO>
 hipError_t tile_pick(const Args &a, hipStream_t s)
 {
+    if (a.K < 128)
+        return launch_tile_as<kShortTile.tb, kShortTile.rb, kShortTile.ks, GROUP, SB, ZERO, kShort>(a, s);
     switch (10 * a.tb + a.rb) {
-    case 11: return tile_whole<1, 1, 256, GROUP, SB, ZERO>(a, s);
-    case 12: return tile_whole<1, 2, 256, GROUP, SB, ZERO>(a, s);
-    case 21: return tile_whole<2, 1, 256, GROUP, SB, ZERO>(a, s);
-    case 22: return tile_whole<2, 2, 256, GROUP, SB, ZERO>(a, s);
-    case 42: return tile_whole<4, 2, 128, GROUP, SB, ZERO>(a, s);
-    default: return tile_whole<4, 4, 128, GROUP, SB, ZERO>(a, s);
+    case 11: return tile_ends<1, 1, 256, GROUP, SB, ZERO>(a, s);
+    case 12: return tile_ends<1, 2, 256, GROUP, SB, ZERO>(a, s);
+    case 21: return tile_ends<2, 1, 256, GROUP, SB, ZERO>(a, s);
+    case 22: return tile_ends<2, 2, 256, GROUP, SB, ZERO>(a, s);
+    case 42: return tile_ends<4, 2, 128, GROUP, SB, ZERO>(a, s);
+    default: return tile_ends<4, 4, 128, GROUP, SB, ZERO>(a, s);
     }
 }
 

@@ -66,7 +66,7 @@ def test_w4_matches_fp64(M, N, K, group):
 TILES = [
     (5, 4500, 8192), (8, 4200, 8288), (3, 33000, 640), (9, 700, 640), (9, 700, 768), (40, 16400, 640), (40, 16400, 512), (20, 8200, 96), (20, 8200, 256),
     (20, 3001, 1152), (20, 3001, 1280), (77, 16400, 640), (77, 16400, 512), (20, 16400, 96), (40, 16400, 256),
-    (700, 100, 256), (1200, 1100, 384), (96, 3001, 2528), (64, 8200, 2048), (301, 20000, 96), (301, 20000, 256),
+    (700, 100, 256), (1200, 1100, 384), (96, 3001, 2528), (64, 8200, 2048), (301, 20000, 96), (301, 20000, 160), (301, 20000, 256), (30, 700, 8352),
 ]
 
 
