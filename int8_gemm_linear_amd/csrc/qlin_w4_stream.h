@@ -18,16 +18,18 @@
 // the other 128 in rows 8..15.  The two diagonal 8 x 8 blocks are wanted, the
 // other two are not looked at.
 //
-// A wave keeps AHEAD slots in flight, each with its codes, scales and token
-// operands, all in registers: loads return in order, so they arrive together
-// and nothing waits for more than it needs.  The waves' sums meet in LDS and
-// are added in wave order: no second launch, no workspace, and the same bits
-// every time.
+// A wave keeps one slot in flight, its codes, scales and token operands all in
+// registers, and four or five waves on a SIMD hide each other's waits.  (Two slots
+// take 160 to 210 registers, two or three waves: with groups of 128 the same time
+// on 51200 x 5120, with groups of 32 and for experts, most of whose workgroups have
+// nothing to do, 10 to 35% more; 27 tokens, top-8, 64 experts of 809 x 1216 23.0
+// against 18.0 us.)  The waves' sums meet in LDS and are added in wave order: no
+// second launch, no workspace, and the same bits every time.
 //
 // The bytes bound it from below and the vector instructions come close behind:
 // 226 for 256 codes of 32 rows, half of which turn codes into bf16, keep the
 // vector units busy for 57% of the time.  One token on 51200 x 5120: 30 us, 4.5
-// TB/s; 32 tokens through 128 experts of 1536 x 2048: 39 us, 4.7 TB/s.
+// TB/s; 32 tokens through 128 experts of 1536 x 2048: 35 us, 5.2 TB/s.
 #pragma once
 
 #include "qlin_w4.h"
@@ -200,7 +202,7 @@ __device__ inline void add_slot(v4f *total, Slot<U, GROUP, SB, ZERO, ENDS != kSh
     }
 }
 
-template <int U, int AHEAD, int GROUP, int SB, bool ZERO, int ENDS>
+template <int U, int GROUP, int SB, bool ZERO, int ENDS>
 __global__ void __launch_bounds__(64 * kStreamWaves) k_stream(Args a)
 {
     constexpr bool WHOLE = ENDS != kShort;
@@ -237,30 +239,15 @@ __global__ void __launch_bounds__(64 * kStreamWaves) k_stream(Args a)
 
     const uint32_t magic = expand_magic(0x43004300u);
     const int stride = waves * kSlot;
-    Slot<U, GROUP, SB, ZERO, WHOLE> slot[AHEAD];
-    int k0 = wave * kSlot;
-#pragma unroll
-    for (int d = 0; d < AHEAD; ++d) slot[d].load(a, o, k0 + d * stride, lane);
-    __builtin_amdgcn_sched_barrier(0);
-    const int left = a.K > k0 ? (a.K - k0 + stride - 1) / stride : 0;          // the wave's slots
-    for (int i = 0; i < left / AHEAD; ++i) {
-#pragma unroll
-        for (int d = 0; d < AHEAD; ++d) {
-            add_slot<U, GROUP, SB, ZERO, ENDS>(total, slot[d], k0, a, lane, magic);
-            // unconditional, so that waits stay counted: past the end of K it
-            // reads the row's last line again
-            slot[d].load(a, o, k0 + AHEAD * stride, lane);
-            k0 += stride;
-            // keeps these loads before the next slot's wait
-            __builtin_amdgcn_sched_barrier(0);
-        }
+    Slot<U, GROUP, SB, ZERO, WHOLE> slot;
+    slot.load(a, o, wave * kSlot, lane);
+    for (int k0 = wave * kSlot; k0 < a.K; k0 += stride) {
+        __builtin_amdgcn_sched_barrier(0);
+        add_slot<U, GROUP, SB, ZERO, ENDS>(total, slot, k0, a, lane, magic);
+        // unconditional, so that waits stay counted: past the end of K it
+        // reads the row's last line again
+        slot.load(a, o, k0 + stride, lane);
     }
-#pragma unroll
-    for (int d = 0; d < AHEAD - 1; ++d)
-        if (d < left % AHEAD) {
-            add_slot<U, GROUP, SB, ZERO, ENDS>(total, slot[d], k0, a, lane, magic);
-            k0 += stride;
-        }
 
     const int n = lane & 15, q = lane >> 4;
     // lane (n, q) holds operand rows 4 q .. 4 q + 3 of column n: wanted where both are of the same half
@@ -282,14 +269,14 @@ __global__ void __launch_bounds__(64 * kStreamWaves) k_stream(Args a)
     }
 }
 
-template <int U, int AHEAD, int GROUP, int SB, bool ZERO, int ENDS>
+template <int U, int GROUP, int SB, bool ZERO, int ENDS>
 hipError_t launch_stream_as(const Args &a, int waves, hipStream_t s)
 {
     const int64_t grid = (int64_t)((a.N + 8 * U - 1) / (8 * U)) * row_tiles(a, kStreamTokens);
     if (grid > 0x7fffffff)
         return hipErrorInvalidValue;
     waves = min(waves, (a.K + kSlot - 1) / kSlot);
-    hipLaunchKernelGGL((k_stream<U, AHEAD, GROUP, SB, ZERO, ENDS>), dim3((unsigned)grid), dim3(64 * waves),
+    hipLaunchKernelGGL((k_stream<U, GROUP, SB, ZERO, ENDS>), dim3((unsigned)grid), dim3(64 * waves),
                        waves * U * 512, s, a);
     return hipGetLastError();
 }
@@ -300,24 +287,25 @@ hipError_t stream_pick(const Args &a, hipStream_t s)
     // More rows a workgroup share one read of the tokens and one start, fewer
     // give the 256 CUs more workgroups: 8 rows up to two workgroups a CU, 32
     // from 16 times that (experts: of the tiles in the grid).  Measured, us
-    // with 8 / 16 / 32 rows, one token: 3.6 / 3.9 / 4.4 (2048 x 2048),
-    // 10.9 / 9.6 / 10.4 (10240 x 5120), 36 / 31.0 / 30.6 (51200 x 5120);
-    // 32 tokens through 128 experts of 1536 x 2048: - / 39.8 / 35.9.
+    // with 8 / 16 / 32 rows, one token: 4.9 / 5.1 / 5.7 (2048 x 2048),
+    // 12.6 / 11.0 / 11.7 (10240 x 5120), 36 / 32.8 / 31.3 (51200 x 5120).  Where K
+    // is long, reading the tokens again is what costs, and 32 rows share it: 8
+    // tokens on 5120 x 25600 28.6 against 36.1 us with 16 rows, one token 24.8 and
+    // 25.6; on 5120 x 8192 11.4 and 12.2, 11.0 both.
     // Waves: as many as K has slots while workgroups are few, one or two when
-    // they fill the GPU by themselves (the experts: 35.9 with two, 40.3 with
-    // four).  Where K is long and the tokens are several, reading them again is
-    // what costs, and 32 rows share it: 8 tokens on 5120 x 25600 27.7 against
-    // 36 us with 16 rows, on 5120 x 8192 10.4 and 11.5 (one token 10.2 and 9.8).
-    const int64_t units = (int64_t)((a.N + 7) / 8) * (a.experts ? row_tiles(a, kStreamTokens) : 1);
-    const bool tokens_cost = a.K >= 8192 && (a.experts ? a.rows / a.experts : a.M) > 2;
-    const int u = units >= 4096 ? 4 : units > 512 ? 2 : 1;
-    const int waves = (int)min(max((6144 * u + units - 1) / units, (int64_t)1), (int64_t)kStreamWaves);
-    if (u == 1)
-        return launch_stream_as<1, 1, GROUP, SB, ZERO, ENDS>(a, waves, s);
-    if (u == 2)
-        return tokens_cost ? launch_stream_as<4, 1, GROUP, SB, ZERO, ENDS>(a, kStreamWaves, s)
-                           : launch_stream_as<2, 1, GROUP, SB, ZERO, ENDS>(a, waves, s);
-    return launch_stream_as<4, 2, GROUP, SB, ZERO, ENDS>(a, waves, s);
+    // they fill the GPU by themselves (32 tokens through 128 experts of 2048 x
+    // 768: 25.7 with one, 30.3 with two, 33.9 with three); experts' workgroups
+    // without rows count half (one token: 8 of 129 tiles have any; 10.6 with two
+    // waves, 13.8 with one on 1536 x 2048).
+    const int64_t tiles = a.experts ? row_tiles(a, kStreamTokens) : 1, units = (int64_t)((a.N + 7) / 8) * tiles;
+    const int u = units >= 4096 || (a.K >= 8192 && units > 512) ? 4 : units > 512 ? 2 : 1;
+    const int64_t busy = a.experts ? (units + (int64_t)((a.N + 7) / 8) * min((int64_t)a.rows, tiles) + 1) / 2 : units;
+    const int waves = (int)min(max((6144 * u + busy - 1) / busy, (int64_t)1), (int64_t)kStreamWaves);
+    switch (u) {
+    case 1: return launch_stream_as<1, GROUP, SB, ZERO, ENDS>(a, waves, s);
+    case 2: return launch_stream_as<2, GROUP, SB, ZERO, ENDS>(a, waves, s);
+    default: return launch_stream_as<4, GROUP, SB, ZERO, ENDS>(a, waves, s);
+    }
 }
 
 template <int GROUP, int SB, bool ZERO>
