@@ -18,6 +18,7 @@
 
 #include "qlin_device.h"
 #include "qlin_dpp.h"
+#include "qlin_moe_scan.h"
 #include "qlinear.h"
 
 namespace qlin {
@@ -167,11 +168,7 @@ __global__ void __launch_bounds__(kSortThreads) k_moe_place(SortArgs a)
             for (int w = 0; w < kSortWaves; ++w) total[e] += hist[w * a.experts + e];
         sum += total[e];
     }
-    int scan = sum;
-    for (int d = 1; d < 64; d <<= 1) {
-        const int v = __shfl_up(scan, d);
-        scan += lane >= d ? v : 0;
-    }
+    const int scan = wave_scan(sum);
     if (lane == 63)
         wave_total[wave] = scan;
     __syncthreads();
@@ -369,11 +366,7 @@ __global__ void __launch_bounds__(kRowThreads) k_moe_dispatch(SortArgs s, RowArg
         const int each = (s.experts + kRowThreads - 1) / kRowThreads;
         int sum = 0;
         for (int e = tid * each; e < min((tid + 1) * each, s.experts); ++e) sum += hist[e];
-        int scan = sum;
-        for (int d = 1; d < 64; d <<= 1) {
-            const int v = __shfl_up(scan, d);
-            scan += lane >= d ? v : 0;
-        }
+        const int scan = wave_scan(sum);
         if (lane == 63)
             total[wave] = scan;
         __syncthreads();

@@ -21,6 +21,7 @@
 #include <stdint.h>
 
 #include "qlin_device.h"
+#include "qlin_moe_scan.h"
 #include "qlinear.h"
 
 namespace qlin {
@@ -77,21 +78,16 @@ __device__ inline bool enter_tile(Args &a, int y, int &m0)
         m0 = y * TILE;
         return m0 < a.M;
     }
+    // (offsets of the next 64 are on their way meanwhile; past the last expert the
+    // last offset twice, which is no rows)
     const int lane = threadIdx.x & 63;
+    int from = a.group_off[min(lane, a.experts)], to = a.group_off[min(lane + 1, a.experts)];
     for (int e0 = 0; e0 < a.experts; e0 += 64) {
-        const int e = e0 + lane;
-        int beg = 0, rows = 0;
-        if (e < a.experts) {
-            beg = min(max(a.group_off[e], 0), a.rows);
-            rows = min(max(min(a.group_off[e + 1], a.rows) - beg, 0), a.M);
-        }
-        const int tiles = (rows + TILE - 1) / TILE;
-        int scan = tiles;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const int v = __shfl_up(scan, d);
-            scan += lane >= d ? v : 0;
-        }
+        int beg = min(max(from, 0), a.rows);
+        const int rows = min(max(min(to, a.rows) - beg, 0), a.M);
+        from = a.group_off[min(e0 + 64 + lane, a.experts)];
+        to = a.group_off[min(e0 + 65 + lane, a.experts)];
+        const int tiles = (rows + TILE - 1) / TILE, scan = wave_scan(tiles);
         const int all = __builtin_amdgcn_readlane(scan, 63);
         if (y < all) {
             const int at = __builtin_ctzll(__ballot(scan > y));

@@ -64,7 +64,7 @@ def test_w4_matches_fp64(M, N, K, group):
 # to 256 weight rows, K whole and split,
 # stages of K that end inside a stage and that do not
 TILES = [
-    (5, 4500, 8192), (8, 4200, 8288), (3, 33000, 640), (9, 700, 640), (9, 700, 768), (40, 16400, 640), (40, 16400, 512), (20, 8200, 96), (20, 8200, 256),
+    (5, 4500, 8192), (8, 4200, 8288), (3, 33000, 640), (50, 200, 32), (9, 300, 64), (9, 700, 640), (9, 700, 768), (40, 16400, 640), (40, 16400, 512), (20, 8200, 96), (20, 8200, 256),
     (20, 3001, 1152), (20, 3001, 1280), (77, 16400, 640), (77, 16400, 512), (20, 16400, 96), (40, 16400, 256),
     (700, 100, 256), (1200, 1100, 384), (96, 3001, 2528), (64, 8200, 2048), (301, 20000, 96), (301, 20000, 160), (301, 20000, 256), (30, 700, 8352),
 ]
