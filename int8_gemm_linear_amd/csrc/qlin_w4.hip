@@ -150,9 +150,11 @@ namespace w4 {
 // The tile and the parts of K with the least estimated time.  A CU runs `at_once`
 // workgroups of a tile; with so many on every CU a stage takes `us` (`more` where
 // they come in several rounds), with fewer down to 0.4 of that, and starting and
-// ending a workgroup costs four stages.  Parts of K cost another launch and the
-// traffic of their sums.  Of all these tiles with 1 to 20 parts this choice takes
-// 2% longer than the best on average, 13% at most, on eight shapes from 2048 x 2048
+// ending a workgroup costs four stages.  Parts of K cost the traffic of their sums
+// and another launch: 1 us of the GPU's time, but 4 of a caller's who does not
+// replay graphs (59 tokens on 65 x 1280: 5.9 us in five parts, 6.3 in one, and 12.8
+// against 8.4 us a call).  Of all these tiles with 1 to 20 parts this choice takes
+// 3% longer on the GPU than the best on average, 13% at most, on eight shapes from 2048 x 2048
 // to 51200 x 5120 and 5120 x 25600 with 12 to 1000 tokens and groups of 64 and
 // 128.  12 tokens on 51200 x 5120: 39 us with rb = 2, 44 us with rb = 1; 32 on
 // 5120 x 25600: 32 us in ten parts, 251 us in one; 512 on 10240 x 5120: 80 us with
@@ -188,7 +190,7 @@ TilePick pick_tile(int64_t M, int64_t N, int64_t K, int64_t experts, int64_t row
             const double rest = std::ceil(each_cu * splits - whole * t.at_once - 1e-9);
             double us = (whole + (rest > 0 ? 0.4 + 0.6 * rest / t.at_once : 0)) * (each + 4) * (whole > 0 ? t.more : t.us);
             if (splits > 1)
-                us += 1.0 + splits * (double)M * N * 8 / 5e6;
+                us += 4.0 + splits * (double)M * N * 8 / 5e6;
             if (us < least) {
                 least = us;
                 best = TilePick{t.tb, t.rb, t.ks, splits};
