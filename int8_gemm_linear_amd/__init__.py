@@ -776,15 +776,20 @@ def _permute_args(x, T, scale, rows, out, out_scale):
             raise ValueError("out_scale without scale")
         sc = (None, 0, None)
     else:
-        rest = scale.shape[1:]
-        if scale.dim() not in (1, 2):
-            raise ValueError("scale must be [T] or [T, G]")
-        _flat(scale, torch.float32, (T, *rest), "scale", dev)
-        if out_scale is None:
-            out_scale = scale.new_empty((rows, *rest))
+        n = scale.dim()
+        if n == 1:
+            cols, one, each = 1, (T,), (rows,)
+        elif n == 2:
+            cols = scale.shape[1]
+            one, each = (T, cols), (rows, cols)
         else:
-            _flat(out_scale, torch.float32, (rows, *rest), "out_scale", dev)
-        sc = (scale.data_ptr(), rest[0] if rest else 1, out_scale.data_ptr())
+            raise ValueError("scale must be [T] or [T, G]")
+        _flat(scale, torch.float32, one, "scale", dev)
+        if out_scale is None:
+            out_scale = scale.new_empty(each)
+        else:
+            _flat(out_scale, torch.float32, each, "out_scale", dev)
+        sc = (scale.data_ptr(), cols, out_scale.data_ptr())
     return out, out_scale, rows, (K * es, x.data_ptr(), ldx * es), (out.data_ptr(), ldo * es), sc
 
 
