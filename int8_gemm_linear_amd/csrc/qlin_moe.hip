@@ -336,9 +336,10 @@ __global__ void __launch_bounds__(kRowThreads) k_moe_permute(RowArgs a)
 // own slots who comes before them (the ids fit LDS; a wave takes slots, its
 // lanes the ids), and then copies its tokens' rows; the last workgroup makes
 // the offsets.  Latency bounds it.  Top-8, 128 experts, 2 KB rows, this and the
-// two (or three) launches: 128 slots 5.0 and 9 us, 1024 7.5 and 9.4, and more
-// slots are counted faster by the sort (2048 in two launches 9.9 us).
-constexpr int kFusedSlots = 1024;
+// two launches: 128 slots 4.7 and 9 us, 1024 7.5 and 9.4, 2048 10.9 and 9.9, but
+// 10.8 against 13.0 for a caller who does not replay graphs; beyond, the sort
+// counts faster.
+constexpr int kFusedSlots = 2048;
 
 template <typename ID>
 __global__ void __launch_bounds__(kRowThreads) k_moe_dispatch(SortArgs s, RowArgs a)

@@ -29,7 +29,7 @@
 // The bytes bound it from below and the vector instructions come close behind:
 // 226 for 256 codes of 32 rows, half of which turn codes into bf16, keep the
 // vector units busy for 57% of the time.  One token on 51200 x 5120: 30 us, 4.5
-// TB/s; 32 tokens through 128 experts of 1536 x 2048: 35 to 42 us by what they hit.
+// TB/s; 32 tokens through 128 experts of 1536 x 2048: 35 to 42 us by the experts hit.
 #pragma once
 
 #include "qlin_w4.h"

@@ -71,6 +71,8 @@ DISPATCHES = [
     (16, 8, 128, 2048, torch.int8, 1), (17, 8, 60, 130, torch.float32, 1), (64, 2, 8, 768, torch.float8_e4m3fn, 6),
     (300, 4, 2048, 1027, torch.bfloat16, None), (1025, 8, 128, 384, torch.float8_e4m3fn, 3),
     (2000, 6, 16, 333, torch.float16, 2), (4, 2, 4, 40000, torch.int8, 300),
+    (256, 8, 128, 200, torch.int8, 1), (257, 8, 128, 200, torch.int8, 1), (2048, 1, 2000, 16, torch.bfloat16, None),
+    (2, 1024, 300, 64, torch.float32, None),
 ]
 
 
