@@ -289,6 +289,12 @@ __global__ void __launch_bounds__(64 * kTileWaves, 2) k_tile(Args a)
                 s = sums[par][at][q];
 #pragma unroll
                 for (int i = 0; i < PER; ++i) fetch(0, i);
+                // Where three waves share a SIMD, the one at its products goes
+                // before those that expand codes (1000 tokens on 5120 x 8192, groups
+                // of 64, 156 and so 151 us; with two waves, 2048 tokens on 10240 x
+                // 5120, 241 and so 248 us).
+                if (TB * RB < 16)
+                    __builtin_amdgcn_s_setprio(1);
 #pragma unroll
                 for (int t = 0; t <= TB; ++t) {
                     // What the stage asks of memory, and the next one's sums,
@@ -325,6 +331,8 @@ __global__ void __launch_bounds__(64 * kTileWaves, 2) k_tile(Args a)
                     }
                     __builtin_amdgcn_sched_barrier(0);
                 }
+                if (TB * RB < 16)
+                    __builtin_amdgcn_s_setprio(0);
             }
         }
         cur = next;
