@@ -50,8 +50,9 @@ struct Lane {
 
 // A slot's codes, scales, zero points and token operands, as loaded.  WHOLE: K
 // has 256 codes at least, and a slot that would pass its end is the last 256.
-template <int U, int GROUP, int SB, bool ZERO, bool WHOLE>
+template <int U, int GROUP, int SB, bool ZERO, int ENDS>
 struct Slot {
+    static constexpr bool WHOLE = ENDS != kShort;
     static constexpr int NG = 128 / GROUP;          // groups of a half
     static constexpr int SW = (NG * SB + 3) / 4;    // dwords of their scales
     static constexpr int SL = (U + 3) / 4;          // scale loads: 32 rows each
@@ -66,8 +67,12 @@ struct Slot {
             k0 = min(k0, a.K - kSlot);
 #pragma unroll
             for (int j = 0; j < 4; ++j) x[j] = ld16(o.xbase + 2 * k0 + 64 * j + o.x);
+            // (where rows are not whole lines, a line's other part is the next
+            // slot's or row's and worth keeping: 8 tokens on 40875 x 6272 41.8
+            // and so 39.0 us)
 #pragma unroll
-            for (int u = 0; u < U; ++u) w[u] = ld_nt(o.wbase + k0 / 2 + o.w[u]);
+            for (int u = 0; u < U; ++u)
+                w[u] = ENDS == kWhole ? ld_nt(o.wbase + k0 / 2 + o.w[u]) : ld16(o.wbase + k0 / 2 + o.w[u]);
             // Whole dwords, where a lane's own would be less, both halves' or
             // more: a narrower load's value is widened in an operation of its
             // own, which the compiler puts, with its wait, right behind it.
@@ -132,11 +137,11 @@ struct Slot {
 // An instruction takes 32 codes in a row, which keeps the token loads in whole
 // pieces of 64 bytes, whatever the group.
 template <int U, int GROUP, int SB, bool ZERO, int ENDS>
-__device__ inline void add_slot(v4f *total, Slot<U, GROUP, SB, ZERO, ENDS != kShort> &slot, int k0, const Args &a,
+__device__ inline void add_slot(v4f *total, Slot<U, GROUP, SB, ZERO, ENDS> &slot, int k0, const Args &a,
                                 int lane, uint32_t magic)
 {
     constexpr bool WHOLE = ENDS != kShort;
-    typedef Slot<U, GROUP, SB, ZERO, WHOLE> S;
+    typedef Slot<U, GROUP, SB, ZERO, ENDS> S;
     constexpr int PER = GROUP / 32;                 // matrix instructions of a group
     const v4i ones = {0x3f803f80, 0x3f803f80, 0x3f803f80, 0x3f803f80};
     const int n = lane & 15, q = lane >> 4;
@@ -239,7 +244,7 @@ __global__ void __launch_bounds__(64 * kStreamWaves) k_stream(Args a)
 
     const uint32_t magic = expand_magic(0x43004300u);
     const int stride = waves * kSlot;
-    Slot<U, GROUP, SB, ZERO, WHOLE> slot;
+    Slot<U, GROUP, SB, ZERO, ENDS> slot;
     slot.load(a, o, wave * kSlot, lane);
     for (int k0 = wave * kSlot; k0 < a.K; k0 += stride) {
         __builtin_amdgcn_sched_barrier(0);
