@@ -102,11 +102,13 @@ __device__ inline uint16_t bf16_bits(float f)
 // vmcnt(0) before every ds_read, which would also wait for the copies of
 // later pipeline stages.  Callers therefore wait for their own copies with
 // explicit, exactly counted s_waitcnt vmcnt(n) before reading the stage.
-// No register output: the copy writes only LDS.
+// No register output: the copy writes only LDS.  A load reads M0 one wait
+// state after its write at the earliest, which the hardware does not see to
+// and the compiler does not inside the string: hence the s_nop.
 __device__ inline void lds_dma16(const void *g, const void *lds)
 {
     const unsigned off = (unsigned)(size_t)lds;
-    asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off"
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off"
                  :
                  : "v"(g), "s"(__builtin_amdgcn_readfirstlane(off))
                  : "memory", "m0");
@@ -119,7 +121,7 @@ __device__ inline void lds_dma16(const void *g, const void *lds)
 __device__ inline void lds_dma16_nt(const void *g, const void *lds)
 {
     const unsigned off = (unsigned)(size_t)lds;
-    asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off nt"
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off nt"
                  :
                  : "v"(g), "s"(__builtin_amdgcn_readfirstlane(off))
                  : "memory", "m0");
@@ -131,7 +133,7 @@ __device__ inline void lds_dma16_nt(const void *g, const void *lds)
 __device__ inline void lds_dma4(const void *g, const void *lds)
 {
     const unsigned off = (unsigned)(size_t)lds;
-    asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dword %0, off"
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off"
                  :
                  : "v"(g), "s"(__builtin_amdgcn_readfirstlane(off))
                  : "memory", "m0");

@@ -181,7 +181,7 @@ __device__ inline void wait_loads()
 __device__ inline void lds_dma16_at(const uint8_t *base, uint32_t offset, const void *lds)
 {
     const unsigned to = (unsigned)(size_t)lds;
-    asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1"
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
                  :
                  : "v"(offset), "s"(base), "s"(__builtin_amdgcn_readfirstlane(to))
                  : "memory", "m0");
