@@ -22,6 +22,7 @@
 
 #include "qlin_device.h"
 #include "qlin_moe_scan.h"
+#include "qlin_w4_plan.h"
 #include "qlinear.h"
 
 namespace qlin {
@@ -83,8 +84,8 @@ __device__ inline bool enter_tile(Args &a, int y, int &m0)
     const int lane = threadIdx.x & 63;
     int from = a.group_off[min(lane, a.experts)], to = a.group_off[min(lane + 1, a.experts)];
     for (int e0 = 0; e0 < a.experts; e0 += 64) {
-        int beg = min(max(from, 0), a.rows);
-        const int rows = min(max(min(to, a.rows) - beg, 0), a.M);
+        int beg;
+        const int rows = expert_rows(from, to, a.rows, a.M, beg);
         from = a.group_off[min(e0 + 64 + lane, a.experts)];
         to = a.group_off[min(e0 + 65 + lane, a.experts)];
         const int tiles = (rows + TILE - 1) / TILE, scan = wave_scan(tiles);

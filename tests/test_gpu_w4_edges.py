@@ -1,0 +1,55 @@
+"""4-bit products on the GPU at the edges of what the header allows."""
+import sys
+
+import numpy as np
+import pytest
+import torch
+
+import int8_gemm_linear_amd as q
+from tests import reference64 as ref
+
+pytestmark = pytest.mark.gpu
+
+LOW, HIGH = -(1 << 31), (1 << 31) - 1
+
+
+def say(*a):
+    print("[gpu-w4-edges]", *a, flush=True)
+    sys.stdout.flush()
+
+
+def weights(lead, K, group, seed):
+    """(packed codes, codes, fp32 scales, zero points) on the GPU and the host."""
+    g = np.random.default_rng([seed, K, group, *lead])
+    codes = g.integers(0, 16, (*lead, K), dtype=np.uint8)
+    s = (0.002 + 0.01 * g.random((*lead, K // group))).astype(np.float32)
+    z = g.integers(0, 16, (*lead, K // group), dtype=np.uint8)
+    return codes, s, z
+
+
+def gpu(a):
+    return torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
+
+def tokens(M, K, seed):
+    return torch.randn((M, K), generator=torch.Generator().manual_seed(seed)).to(torch.bfloat16)
+
+
+@pytest.mark.parametrize("rows", [12, 120])
+def test_offsets_whose_differences_pass_32_bits_stay_inside_the_buffers(rows):
+    # few rows and many: both kernels.  The second expert's offsets fall by 2^31 and
+    # more, the third's rise by as much; x and y have rows behind those of the call
+    N, K, group, mid = 40, 256, 64, rows // 12
+    codes, s, z = weights((3, N), K, group, 1)
+    x = tokens(rows + 40, K, 2)
+    xd, b, sd, zd = x.cuda(), gpu(ref.pack4(codes)), gpu(s), gpu(z)
+    for off in ([0, mid, LOW, rows], [0, mid, LOW, HIGH], [mid, HIGH, LOW, HIGH]):
+        say("offsets", rows, off)
+        whole = torch.full((rows + 40, N), 3.0, dtype=torch.bfloat16, device="cuda")
+        q.grouped_w4_mm(xd[:rows], b, sd, torch.tensor(off, dtype=torch.int32, device="cuda"), 4 * rows, zd,
+                        out=whole[:rows])
+        torch.cuda.synchronize()
+        assert bool((whole[rows:] == 3.0).all())
+        # the third expert has all rows; those before `mid` (or behind) are the first's too
+        lo, hi = (mid, rows) if off[0] == 0 else (0, mid)
+        ref.w4_check(whole[lo:hi], ref.f64(x[lo:hi]), codes[2], ref.f64(s[2]), z[2], group, str(off))
