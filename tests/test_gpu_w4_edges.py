@@ -52,4 +52,4 @@ def test_offsets_whose_differences_pass_32_bits_stay_inside_the_buffers(rows):
         assert bool((whole[rows:] == 3.0).all())
         # the third expert has all rows; those before `mid` (or behind) are the first's too
         lo, hi = (mid, rows) if off[0] == 0 else (0, mid)
-        ref.w4_check(whole[lo:hi], ref.f64(x[lo:hi]), codes[2], ref.f64(s[2]), z[2], group, str(off))
+        ref.w4_check(whole[lo:hi], ref.f64(x[lo:hi]), codes[2], s[2], z[2], group, str(off))
