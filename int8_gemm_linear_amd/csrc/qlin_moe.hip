@@ -569,6 +569,25 @@ dim3 row_grid(const RowArgs &a)
     return dim3((unsigned)((a.tokens + per - 1) / per));
 }
 
+// Runs `launch` (grid, arguments) for all tokens, in parts of 2^31 threads at most:
+// a grid of 2^32 threads or more is taken modulo that, without an error.
+// `advance`: the arguments past so many tokens.
+constexpr int kRowBlocks = 1 << 23;
+
+template <typename Launch, typename Advance>
+hipError_t launch_rows(RowArgs a, Launch launch, Advance advance)
+{
+    const int most = (int)std::min<int64_t>((int64_t)kRowBlocks * (kRowThreads / a.lanes), kMaxSlots);
+    hipError_t e = hipSuccess;
+    for (int left = a.tokens; left > 0 && e == hipSuccess; left -= a.tokens) {
+        a.tokens = std::min(left, most);
+        launch(row_grid(a), a);
+        e = hipGetLastError();
+        advance(a, (int64_t)a.tokens);
+    }
+    return e;
+}
+
 qlin_status check_rows(int64_t tokens, int64_t topk, int64_t rows)
 {
     if (tokens < 0 || topk < 1 || topk > kMaxTopk || tokens > kMaxSlots / topk || rows < 0 || rows > kMaxSlots)
@@ -613,8 +632,13 @@ RowArgs permute_args(int64_t tokens, int64_t topk, int64_t rows, int64_t row_byt
 
 hipError_t launch_permute(const RowArgs &a, hipStream_t s)
 {
-    hipLaunchKernelGGL(k_moe_permute, row_grid(a), dim3(kRowThreads), 0, s, a);
-    return hipGetLastError();
+    return launch_rows(
+        a, [s](dim3 grid, const RowArgs &p) { hipLaunchKernelGGL(k_moe_permute, grid, dim3(kRowThreads), 0, s, p); },
+        [](RowArgs &p, int64_t tokens) {
+            p.x += tokens * p.ldx;
+            p.slot_row += tokens * p.topk;
+            p.scale += p.scale_cols ? tokens * p.scale_cols : 0;
+        });
 }
 
 // Bytes of an element, 0 for an unknown type.
@@ -656,13 +680,20 @@ qlin_status combine(qlin_row_type rt, int64_t tokens, int64_t topk, int64_t rows
     a.cols = (int)K;
     a.lanes = row_lanes(K * es);
     hipStream_t s = static_cast<hipStream_t>(stream);
-    const dim3 grid = row_grid(a), block(kRowThreads);
-    switch (rt) {
-    case QLIN_ROW_F32: hipLaunchKernelGGL((k_moe_combine<float>), grid, block, 0, s, a); break;
-    case QLIN_ROW_BF16: hipLaunchKernelGGL((k_moe_combine<uint16_t>), grid, block, 0, s, a); break;
-    case QLIN_ROW_F16: hipLaunchKernelGGL((k_moe_combine<__half>), grid, block, 0, s, a); break;
-    }
-    return hipGetLastError() == hipSuccess ? QLIN_OK : QLIN_ERR_HIP;
+    const auto launch = [rt, s](dim3 grid, const RowArgs &p) {
+        const dim3 block(kRowThreads);
+        switch (rt) {
+        case QLIN_ROW_F32: hipLaunchKernelGGL((k_moe_combine<float>), grid, block, 0, s, p); break;
+        case QLIN_ROW_BF16: hipLaunchKernelGGL((k_moe_combine<uint16_t>), grid, block, 0, s, p); break;
+        case QLIN_ROW_F16: hipLaunchKernelGGL((k_moe_combine<__half>), grid, block, 0, s, p); break;
+        }
+    };
+    const auto advance = [](RowArgs &p, int64_t tokens) {
+        p.slot_row += tokens * p.topk;
+        p.weights += p.weights ? tokens * p.topk : 0;
+        p.out += tokens * p.ldo;
+    };
+    return launch_rows(a, launch, advance) == hipSuccess ? QLIN_OK : QLIN_ERR_HIP;
 }
 
 }  // namespace
@@ -811,13 +842,21 @@ qlin_status qlin_moe_combine_backward(qlin_row_type rt, int64_t tokens, int64_t 
     a.cols = (int)K;
     a.lanes = std::max(row_lanes(K * es), 64);
     hipStream_t s = static_cast<hipStream_t>(stream);
-    const dim3 grid = row_grid(a), block(kRowThreads);
-    switch (rt) {
-    case QLIN_ROW_F32: hipLaunchKernelGGL((k_moe_combine_backward<float>), grid, block, 0, s, a); break;
-    case QLIN_ROW_BF16: hipLaunchKernelGGL((k_moe_combine_backward<uint16_t>), grid, block, 0, s, a); break;
-    case QLIN_ROW_F16: hipLaunchKernelGGL((k_moe_combine_backward<__half>), grid, block, 0, s, a); break;
-    }
-    return hipGetLastError() == hipSuccess ? QLIN_OK : QLIN_ERR_HIP;
+    const auto launch = [rt, s](dim3 grid, const RowArgs &p) {
+        const dim3 block(kRowThreads);
+        switch (rt) {
+        case QLIN_ROW_F32: hipLaunchKernelGGL((k_moe_combine_backward<float>), grid, block, 0, s, p); break;
+        case QLIN_ROW_BF16: hipLaunchKernelGGL((k_moe_combine_backward<uint16_t>), grid, block, 0, s, p); break;
+        case QLIN_ROW_F16: hipLaunchKernelGGL((k_moe_combine_backward<__half>), grid, block, 0, s, p); break;
+        }
+    };
+    const auto advance = [](RowArgs &p, int64_t tokens) {
+        p.x += tokens * p.ldx;
+        p.slot_row += tokens * p.topk;
+        p.weights += tokens * p.topk;
+        p.out_f += tokens * p.topk;
+    };
+    return launch_rows(a, launch, advance) == hipSuccess ? QLIN_OK : QLIN_ERR_HIP;
 }
 
 }  // extern "C"
