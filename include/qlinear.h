@@ -325,7 +325,9 @@ qlin_status qlin_silu_and_mul_per_block_quant(int64_t M, int64_t K, const uint16
  * 16-byte aligned, with any contents, not used by two calls that may overlap
  * in time (the parts of K where M x N alone is too little work for the GPU;
  * they are added in order, so results do not depend on timing).  Errors as for
- * qlin_scaled_mm (a group or scale type not listed: QLIN_ERR_BAD_ARGUMENT). */
+ * qlin_scaled_mm (a group or scale type not listed: QLIN_ERR_BAD_ARGUMENT; a
+ * product of more work than one launch takes: QLIN_ERR_BAD_SHAPE, never where
+ * M x N, with experts (rows + 64 groups) x N, is below 2^33). */
 typedef enum qlin_scale_type {
     QLIN_SCALE_F32 = 0,
     QLIN_SCALE_BF16 = 1,

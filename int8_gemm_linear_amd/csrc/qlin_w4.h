@@ -303,7 +303,11 @@ __device__ inline void store_value(const Args &a, int64_t m, int64_t n, float v)
 
 constexpr int kStreamTokens = 8;
 
-// Launchers, one unit per group length.
+// Threads of a launch: a grid of 2^32 or more is taken modulo that, without an error.
+constexpr int64_t kMostThreads = 0xffffffff;
+
+// Launchers, one unit per group length; hipErrorInvalidConfiguration, and nothing
+// launched, where the grid would have more threads.
 typedef hipError_t (*Launch)(const Args &a, hipStream_t s);
 hipError_t launch_stream_32(const Args &a, hipStream_t s);
 hipError_t launch_stream_64(const Args &a, hipStream_t s);

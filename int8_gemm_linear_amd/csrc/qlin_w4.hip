@@ -106,6 +106,11 @@ bool streams(const w4::Args &a)
     return a.rows <= few * a.experts;
 }
 
+qlin_status status_of(hipError_t e)
+{
+    return e == hipSuccess ? QLIN_OK : e == hipErrorInvalidConfiguration ? QLIN_ERR_BAD_SHAPE : QLIN_ERR_HIP;
+}
+
 qlin_status launch(w4::Args &a, void *ws, size_t ws_bytes, void *stream)
 {
     static const w4::Launch kStream[3] = {w4::launch_stream_32, w4::launch_stream_64, w4::launch_stream_128};
@@ -115,7 +120,7 @@ qlin_status launch(w4::Args &a, void *ws, size_t ws_bytes, void *stream)
     a.splits = 1;
     a.split_k = a.K;
     if (streams(a))
-        return kStream[which](a, s) == hipSuccess ? QLIN_OK : QLIN_ERR_HIP;
+        return status_of(kStream[which](a, s));
     const w4::TilePick p = w4::pick_tile(a.M, a.N, a.K, a.experts, a.rows);
     const size_t need = part_bytes(a.M, a.N, p.splits);
     if (need && (!ws || ws_bytes < need))
@@ -128,8 +133,9 @@ qlin_status launch(w4::Args &a, void *ws, size_t ws_bytes, void *stream)
     a.splits = p.splits;
     a.split_k = (stages + p.splits - 1) / p.splits * p.ks;
     a.part = static_cast<float *>(ws);
-    if (kTile[which](a, s) != hipSuccess)
-        return QLIN_ERR_HIP;
+    const qlin_status st = status_of(kTile[which](a, s));
+    if (st != QLIN_OK)
+        return st;
     if (a.splits > 1) {
         const int v = a.N % 4 == 0 ? 4 : 1;
         const dim3 grid((unsigned)(((int64_t)a.M * a.N / v + 255) / 256));
@@ -181,7 +187,8 @@ TilePick pick_tile(int64_t M, int64_t N, int64_t K, int64_t experts, int64_t row
             continue;
         const double tall = experts ? experts * std::max(std::min(1.0, mean), mean / high + 0.5) : (double)((M + high - 1) / high);
         const double each_cu = tall * ((N + 64 * t.rb - 1) / (64 * t.rb)) / 256;
-        const int most = experts ? 1 : (int)std::min<int64_t>(kMostParts, stages);
+        // (outputs that are too many for one launch of the sum of the parts are not split)
+        const int most = experts || M * N > w4::kMostThreads / 2 ? 1 : (int)std::min<int64_t>(kMostParts, stages);
         for (int splits = 1; splits <= most; ++splits) {
             const int64_t each = (stages + splits - 1) / splits;
             if ((stages + each - 1) / each != splits)

@@ -278,9 +278,9 @@ template <int U, int GROUP, int SB, bool ZERO, int ENDS>
 hipError_t launch_stream_as(const Args &a, int waves, hipStream_t s)
 {
     const int64_t grid = (int64_t)((a.N + 8 * U - 1) / (8 * U)) * row_tiles(a, kStreamTokens);
-    if (grid > 0x7fffffff)
-        return hipErrorInvalidValue;
     waves = min(waves, (a.K + kSlot - 1) / kSlot);
+    if (grid * 64 * waves > kMostThreads)
+        return hipErrorInvalidConfiguration;
     hipLaunchKernelGGL((k_stream<U, GROUP, SB, ZERO, ENDS>), dim3((unsigned)grid), dim3(64 * waves),
                        waves * U * 512, s, a);
     return hipGetLastError();

@@ -406,12 +406,12 @@ hipError_t launch_tile_as(Args a, hipStream_t s)
 {
     const int64_t tiles = row_tiles(a, 16 * TB);
     if (tiles > 0x7fffffff / 8)
-        return hipErrorInvalidValue;
+        return hipErrorInvalidConfiguration;
     a.tiles = (int)tiles;
     const Blocks bl = tile_blocks((a.N + 64 * RB - 1) / (64 * RB), a.tiles);
     const int64_t grid = bl.all * a.splits;
-    if (grid > 0x7fffffff)
-        return hipErrorInvalidValue;
+    if (grid * 64 * kTileWaves > kMostThreads)
+        return hipErrorInvalidConfiguration;
     hipLaunchKernelGGL((k_tile<TB, RB, KS, GROUP, SB, ZERO, ENDS>), dim3((unsigned)grid), dim3(64 * kTileWaves), 0, s, a);
     return hipGetLastError();
 }

@@ -47,3 +47,18 @@ def test_rows_of_any_offset_table_lie_inside_the_buffers(plan):
         lo, hi = (min(max(v, 0), rows) for v in (f, t))
         assert beg == lo and n == min(max(hi - lo, 0), most), (f, t, rows, most, beg, n)
         assert 0 <= beg and beg + n <= rows
+
+
+def test_products_of_more_threads_than_a_launch_takes_are_refused():
+    # a grid of 2^32 threads would be taken modulo that: nothing is launched here
+    shape, p = 2, 0x10000
+    lib = q.lib()
+    big = 1 << 24
+    assert lib.qlin_w4_mm(big, big, 32, 32, p, 32, p, 16, 0, p, None, p, big, None, 0, None) == shape
+    # experts of few rows (streamed) and of many (tiles)
+    for rows in (16, big):
+        assert lib.qlin_grouped_w4_mm(65535, p, rows, rows, big, 32, 32, p, 32, p, 16, 1 << 28, 0, p, None, p, big,
+                                      None) == shape, rows
+    # a K so long that parts would pay: not where their sum is more than one launch
+    assert lib.qlin_w4_workspace_size(1 << 17, 1 << 15, 1 << 20) == 0
+    assert lib.qlin_w4_workspace_size(32, 5120, 25600) > 0
