@@ -280,11 +280,13 @@ __device__ inline float exact_value(const Args &a, int64_t m, int64_t n)
                              ? reinterpret_cast<const float *>(a.scale)[at]
                              : scale_value<2>(reinterpret_cast<const uint16_t *>(a.scale)[at], a.st);
         const int z = a.zero ? a.zero[at] & 15 : 8;
+        double part = 0.0;          // scaled as a whole: an infinite scale times a zero in it is no NaN
         for (int k = g * group; k < (g + 1) * group; ++k) {
             const int q = (a.b[n * a.ldb + (k >> 1)] >> (4 * (k & 1))) & 15;
             const float x = __uint_as_float((uint32_t)a.x[m * a.ldx + k] << 16);
-            sum += s * (double)(q - z) * (double)x;
+            part += (double)(q - z) * (double)x;
         }
+        sum += s * part;
         if (sum != sum)
             break;                  // and nothing brings it back
     }

@@ -53,3 +53,20 @@ def test_offsets_whose_differences_pass_32_bits_stay_inside_the_buffers(rows):
         # the third expert has all rows; those before `mid` (or behind) are the first's too
         lo, hi = (mid, rows) if off[0] == 0 else (0, mid)
         ref.w4_check(whole[lo:hi], ref.f64(x[lo:hi]), codes[2], s[2], z[2], group, str(off))
+
+
+@pytest.mark.parametrize("M", [2, 40])
+def test_infinite_scales_multiply_their_groups_sum(M):
+    # the formula scales a group's sum, not its terms: an infinite scale gives an
+    # infinity of that sum's sign, also where some of the group's codes equal its zero point
+    N, K, group = 70, 512, 128
+    codes, s, z = weights((N,), K, group, 6)
+    codes[:, ::3] = np.repeat(z, group, axis=1)[:, ::3]
+    s[::2, 1] = np.inf
+    x = tokens(M, K, 7)
+    say("infinite scale", M)
+    y = ref.f64(q.w4_mm(x.cuda(), gpu(ref.pack4(codes)), gpu(s), gpu(z)))
+    sums = ((codes - np.repeat(z, group, axis=1).astype(np.float64))[None] * ref.f64(x)[:, None, :])
+    sums = sums.reshape(M, N, K // group, group).sum(axis=3)
+    assert np.array_equal(y[:, ::2], np.sign(sums[:, ::2, 1]) * np.inf)
+    ref.w4_check(torch.from_numpy(y[:, 1::2]), ref.f64(x), codes[1::2], s[1::2], z[1::2], group, "finite scales")
