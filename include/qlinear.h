@@ -320,7 +320,9 @@ qlin_status qlin_silu_and_mul_per_block_quant(int64_t M, int64_t K, const uint16
  * (bytes), ldy >= N, rows of X and B at most 2^25 bytes apart; X, B and Y
  * 16-byte aligned, b_scale 4-byte aligned.  An
  * infinity or NaN in X reaches the outputs that the formula gives it and no
- * other row.  The caller owns every buffer; the call is asynchronous on
+ * other row; outputs that are not finite in fp32 are computed a second time in
+ * fp64, which costs such a row many times an ordinary one (one infinity among
+ * 1000 tokens doubles the call; one in each makes it 100 times as long).  The caller owns every buffer; the call is asynchronous on
  * `stream` and allocates nothing.  workspace: qlin_w4_workspace_size bytes,
  * 16-byte aligned, with any contents, not used by two calls that may overlap
  * in time (the parts of K where M x N alone is too little work for the GPU;

@@ -13,7 +13,7 @@
 //
 // Where a row of X is not finite, or so large that 143 x overflows fp32, that
 // difference is NaN although the formula's value may not be: such outputs are
-// computed again from the formula in fp64 (exact_value), one by one.
+// computed again from the formula in fp64 (exact_value), a wave for each.
 #pragma once
 
 #include <hip/hip_fp16.h>
@@ -21,6 +21,7 @@
 #include <stdint.h>
 
 #include "qlin_device.h"
+#include "qlin_dpp.h"
 #include "qlin_moe_scan.h"
 #include "qlin_w4_plan.h"
 #include "qlinear.h"
@@ -269,38 +270,71 @@ __device__ inline int k_of(int j, int q)
                         : 32 * j + 8 * q;
 }
 
-// The formula's value in fp64, for an output whose fast value is not finite.
+// The formula's value in fp64, for an output whose fast value is not finite.  The
+// whole wave computes it, all lanes with the same m and n: a lane takes 32 codes
+// at a time, the lanes of a group add theirs, one of them scales the group's sum.
+// A row that has one costs its N walks over K: 1000 tokens with an infinity each
+// on 10240 x 5120 18 ms (one of them 0.28 ms, none 0.14 ms), one of 32 on 5120 x
+// 25600 3.6 ms.  (A lane by itself over all of K: 107, 1.5 and 15 ms.)
 __device__ inline float exact_value(const Args &a, int64_t m, int64_t n)
 {
-    const int group = a.K / a.G;
+    const int lane = threadIdx.x & 63, chunks = a.K / 32, per = chunks / a.G;
+    const uint8_t *b = a.b + n * a.ldb;
+    const uint8_t *x = reinterpret_cast<const uint8_t *>(a.x + m * a.ldx);
     double sum = 0.0;
-    for (int g = 0; g < a.G; ++g) {
-        const int64_t at = n * a.G + g;
-        const double s = a.st == QLIN_SCALE_F32
-                             ? reinterpret_cast<const float *>(a.scale)[at]
-                             : scale_value<2>(reinterpret_cast<const uint16_t *>(a.scale)[at], a.st);
+    for (int c0 = 0; c0 < chunks; c0 += 64) {
+        const int c = min(c0 + lane, chunks - 1);
+        const int64_t at = n * a.G + c / per;
+        const float s = a.st == QLIN_SCALE_F32
+                            ? reinterpret_cast<const float *>(a.scale)[at]
+                            : scale_value<2>(reinterpret_cast<const uint16_t *>(a.scale)[at], a.st);
         const int z = a.zero ? a.zero[at] & 15 : 8;
-        double part = 0.0;          // scaled as a whole: an infinite scale times a zero in it is no NaN
-        for (int k = g * group; k < (g + 1) * group; ++k) {
-            const int q = (a.b[n * a.ldb + (k >> 1)] >> (4 * (k & 1))) & 15;
-            const float x = __uint_as_float((uint32_t)a.x[m * a.ldx + k] << 16);
-            part += (double)(q - z) * (double)x;
+        double part = 0.0;
+#pragma unroll 1                                    // (registers: the callers' occupancy)
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t w = *reinterpret_cast<const uint32_t *>(b + 16 * (int64_t)c + 4 * i);
+            const v4i xs = ld16(x + 64 * (int64_t)c + 16 * i);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int q = (w >> (4 * k)) & 15;
+                const uint32_t pair = (uint32_t)xs[k / 2];
+                part = fma((double)(q - z), (double)__uint_as_float(k & 1 ? pair & 0xffff0000u : pair << 16), part);
+            }
         }
-        sum += s * part;
-        if (sum != sum)
-            break;                  // and nothing brings it back
+        if (per > 1)
+            part += dpp_partner(part, 0);
+        if (per > 2)
+            part += dpp_partner(part, 1);
+        if (c0 + lane < chunks && lane % per == 0)
+            sum = fma((double)s, part, sum);
+        if (__ballot(part != part || sum != sum))
+            return __uint_as_float(0x7fc00000u);        // nothing brings it back
     }
-    return (float)sum;
+    return (float)wave_sum(sum);
 }
 
 __device__ inline bool is_finite(float v) { return fabsf(v) <= 3.4028234663852886e38f; }
 
-// One output: rounded to bf16, or computed again where it is not finite.
-__device__ inline void store_value(const Args &a, int64_t m, int64_t n, float v)
+// v, or the exact value of output (m, n) where `again` holds, one lane's after
+// another: every lane of the wave calls.
+__device__ inline float recompute(const Args &a, bool again, int m, int n, float v)
 {
-    if (!is_finite(v))
-        v = exact_value(a, m, n);
-    a.y[m * a.ldy + n] = bf16_bits(v);
+    for (uint64_t left = __ballot(again); left; left &= left - 1) {
+        const int l = __builtin_ctzll(left);
+        const float e = exact_value(a, __builtin_amdgcn_readlane(m, l), __builtin_amdgcn_readlane(n, l));
+        if ((int)(threadIdx.x & 63) == l)
+            v = e;
+    }
+    return v;
+}
+
+// The output of a lane that has one (`there`): rounded to bf16, or computed again
+// where it is not finite.  Every lane of the wave calls.
+__device__ inline void store_value(const Args &a, bool there, int m, int n, float v)
+{
+    v = recompute(a, there && !is_finite(v), m, n, v);
+    if (there)
+        a.y[m * a.ldy + n] = bf16_bits(v);
 }
 
 constexpr int kStreamTokens = 8;

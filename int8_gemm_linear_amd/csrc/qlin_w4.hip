@@ -69,25 +69,24 @@ __global__ void __launch_bounds__(256) k_reduce(w4::Args a)
 {
     const int64_t all = (int64_t)a.M * a.N;
     const int64_t e = ((int64_t)blockIdx.x * 256 + threadIdx.x) * V;
-    if (e >= all)
-        return;
+    const bool there = e < all;                     // (V divides N: all of the V, or none)
     constexpr int kAtOnce = 4;
     float v[V] = {};
     for (int s = 0; s < a.splits; s += kAtOnce) {
         float p[kAtOnce][V];
 #pragma unroll
         for (int j = 0; j < kAtOnce; ++j)
-            if (s + j < a.splits)
+            if (there && s + j < a.splits)
                 __builtin_memcpy(p[j], a.part + (s + j) * all + e, 4 * V);
 #pragma unroll
         for (int j = 0; j < kAtOnce; ++j)
-            if (s + j < a.splits)
+            if (there && s + j < a.splits)
 #pragma unroll
                 for (int i = 0; i < V; ++i) v[i] += p[j][i];
     }
-    const int64_t m = e / a.N, n = e % a.N;
+    const int m = (int)(e / a.N), n = (int)(e % a.N);
 #pragma unroll
-    for (int i = 0; i < V; ++i) w4::store_value(a, m, n + i, v[i]);
+    for (int i = 0; i < V; ++i) w4::store_value(a, there, m, n + i, v[i]);
 }
 
 size_t part_bytes(int64_t M, int64_t N, int splits) { return splits > 1 ? (size_t)splits * M * N * sizeof(float) : 0; }

@@ -264,13 +264,13 @@ __global__ void __launch_bounds__(64 * kStreamWaves) k_stream(Args a)
                 part[((wave * 2 + (n >> 3)) * U + u) * 64 + (4 * (q & 1) + i) * 8 + (n & 7)] = total[u][i];
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < tokens * 8 * U; e += blockDim.x) {
+    for (int e = threadIdx.x; e - lane < tokens * 8 * U; e += blockDim.x) {     // whole waves: see store_value
         const int col = e % (8 * U), tok = e / (8 * U);               // rows fastest: stores side by side
-        if (n0 + col >= a.N)
-            continue;
+        const bool there = tok < tokens && n0 + col < a.N;
         float v = 0.0f;
-        for (int w = 0; w < 2 * waves; ++w) v += part[(w * U + (col >> 3)) * 64 + tok * 8 + (col & 7)];
-        store_value(a, m0 + tok, n0 + col, v);
+        if (there)
+            for (int w = 0; w < 2 * waves; ++w) v += part[(w * U + (col >> 3)) * 64 + tok * 8 + (col & 7)];
+        store_value(a, there, m0 + tok, n0 + col, v);
     }
 }
 

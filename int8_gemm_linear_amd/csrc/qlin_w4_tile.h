@@ -375,13 +375,15 @@ __global__ void __launch_bounds__(64 * kTileWaves, 2) k_tile(Args a)
                 mine[(16 * t + 4 * q + i) * ROW + 16 * r + n] = bf16_bits(total[r][t][i]);
                 fine = fine && is_finite(total[r][t][i]);
             }
-    if (!fine)
-        // rare: the lane looks its values over again, in a loop that costs no registers above
+    if (__ballot(!fine))
+        // rare: the lanes look their values over again, in a loop that costs no registers above
         for (int e = 0; e < 4 * TB * RB; ++e) {
             const int t = 16 * (e / (4 * RB)) + 4 * q + e / RB % 4, c = 16 * (e % RB) + n;
             uint16_t &v = mine[t * ROW + c];
-            if (m0 + t < a.M && n0 + c < a.N && (v & 0x7f80) == 0x7f80)
-                v = bf16_bits(exact_value(a, m0 + t, n0 + c));
+            const bool again = m0 + t < a.M && n0 + c < a.N && (v & 0x7f80) == 0x7f80;
+            const float f = recompute(a, again, m0 + t, n0 + c, 0.0f);
+            if (again)
+                v = bf16_bits(f);
         }
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
     __builtin_amdgcn_wave_barrier();

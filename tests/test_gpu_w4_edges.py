@@ -55,6 +55,40 @@ def test_offsets_whose_differences_pass_32_bits_stay_inside_the_buffers(rows):
         ref.w4_check(whole[lo:hi], ref.f64(x[lo:hi]), codes[2], s[2], z[2], group, str(off))
 
 
+@pytest.mark.parametrize("M,N,K,group", [(1, 700, 8192, 128), (8, 5120, 2528, 32), (30, 300, 25600, 64),
+                                         (200, 1030, 4160, 64), (700, 600, 1152, 128)])
+def test_infinities_and_nan_at_the_size_of_a_layer(M, N, K, group):
+    # every kernel and the sum of the parts: an infinity in each row (in half of them
+    # one of either sign as well), a NaN row and a row of values whose products pass
+    # fp32, against the formula in fp64 on the GPU
+    codes, s, z = weights((N,), K, group, 3)
+    x = tokens(M, K, 4)
+    r = torch.arange(M)
+    x[r, (r * 37) % K] = float("inf")
+    x[r[::2], (r[::2] * 37 + 5) % K] = float("-inf")
+    if M > 2:
+        x[1] = tokens(1, K, 5)[0] * 2.0 ** 124
+        x[2, K - 1] = float("nan")
+    say("infinities", M, N, K, group)
+    b, sd, zd = gpu(ref.pack4(codes)), gpu(s), gpu(z)
+    y = q.w4_mm(x.cuda(), b, sd, zd).double().cpu()
+    w = torch.from_numpy(ref.w4_weights(codes, s, z, group)).cuda()
+    want = torch.empty((M, N), dtype=torch.float64, device="cuda")
+    for m in range(M):                                  # elementwise: no product's own way with NaN
+        want[m] = (w * x[m].cuda().double()).sum(dim=1)
+    want = want.cpu()
+    assert torch.equal(torch.isnan(y), torch.isnan(want))
+    inf = torch.isinf(want)
+    assert torch.equal(y[inf], want[inf]) and bool(inf.any())
+    if M > 2:
+        # bf16 ends at (2 - 2^-7) 2^127; from half a step above, (2 - 2^-8) 2^127, a value
+        # rounds to an infinity (none of these lies within 2^-20 of that border)
+        past = (want[1].abs() >= (2 - 2.0 ** -8) * 2.0 ** 127).numpy()
+        assert np.array_equal(ref.f64(y[1])[past], np.sign(ref.f64(want[1])[past]) * np.inf)
+        ref.w4_check(y[1:2, torch.from_numpy(~past)], ref.f64(x[1:2]), codes[~past], s[~past], z[~past], group,
+                     "large values")
+
+
 @pytest.mark.parametrize("M", [2, 40])
 def test_infinite_scales_multiply_their_groups_sum(M):
     # the formula scales a group's sum, not its terms: an infinite scale gives an
