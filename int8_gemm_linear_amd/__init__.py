@@ -700,13 +700,14 @@ def grouped_w4_mm(x, b_q, b_scale, group_offsets, max_rows: int, b_zero=None, ou
     G, N, half = b_q.shape
     if half * 2 != K:
         raise ValueError("x is [rows,K] and b_q must be [G,N,K/2]")
+    apart, ldb, _ = b_q.stride()
+    apart, ldb = apart if G > 1 else 0, ldb if N > 1 else half       # a single one's stride says nothing
     group, st, zero = _w4_scales(b_scale, b_zero, (G, N), K, dev)
     _flat(group_offsets, torch.int32, (G + 1,), "group_offsets", dev)
     out, ldy = _rows_out(out, (rows, N), x)
     _call_on(dev, _lib().qlin_grouped_w4_mm,
              [G, group_offsets.data_ptr(), int(max_rows), rows, N, K, group, x.data_ptr(), ldx, b_q.data_ptr(),
-              b_q.stride(1), b_q.stride(0), st, b_scale.data_ptr(), zero, out.data_ptr(), ldy],
-             "qlin_grouped_w4_mm")
+              ldb, apart, st, b_scale.data_ptr(), zero, out.data_ptr(), ldy], "qlin_grouped_w4_mm")
     return out
 
 

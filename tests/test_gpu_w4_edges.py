@@ -104,3 +104,15 @@ def test_infinite_scales_multiply_their_groups_sum(M):
     sums = sums.reshape(M, N, K // group, group).sum(axis=3)
     assert np.array_equal(y[:, ::2], np.sign(sums[:, ::2, 1]) * np.inf)
     ref.w4_check(torch.from_numpy(y[:, 1::2]), ref.f64(x), codes[1::2], s[1::2], z[1::2], group, "finite scales")
+
+
+def test_strides_of_a_single_expert_or_row_are_not_read():
+    M, K, group = 20, 256, 64
+    x = tokens(M, K, 8).cuda()
+    for G, N, strides in ((1, 24, (7, K // 2, 1)), (3, 1, (K // 2, 7, 1)), (1, 1, (5, 3, 1))):
+        say("strides", G, N)
+        codes, s, z = weights((G, N), K, group, 9)
+        b, sd, zd = gpu(ref.pack4(codes)), gpu(s), gpu(z)
+        off = torch.tensor([0, *[M - G + 1 + g for g in range(G)]], dtype=torch.int32, device="cuda")
+        want = q.grouped_w4_mm(x, b, sd, off, M, zd)
+        assert torch.equal(q.grouped_w4_mm(x, b.as_strided((G, N, K // 2), strides), sd, off, M, zd), want)
