@@ -50,22 +50,8 @@ struct Args {
     float *part;                  // [splits][M][N] sums of the parts
 };
 
-// How K ends: with a whole stage (or slot); inside one, which then is the last one's
-// number of codes before the end, those that were had already against zeros; or
-// before one is full, where every load is held inside K by itself.  (K = 6304, 18
-// tokens, N = 40875, groups of 32: 135 us with every load held, so 81 us; a kernel
-// for the first two together costs whole stages 2%, and the streaming kernel with
-// fp32 scales 18%.)
-enum Ends { kWhole, kInside, kShort };
-
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 typedef uint32_t v2u __attribute__((ext_vector_type(2)));
-
-// Tiles of TILE rows that cover every expert's rows (or M): at most this many.
-inline int64_t row_tiles(const Args &a, int tile)
-{
-    return a.group_off ? a.rows / tile + a.experts : ((int64_t)a.M + tile - 1) / tile;
-}
 
 // The first row m0 of the workgroup's tile `y` among those; narrows the
 // arguments to its expert, whose rows are held inside the buffers whatever the
@@ -337,11 +323,6 @@ __device__ inline void store_value(const Args &a, bool there, int m, int n, floa
         a.y[m * a.ldy + n] = bf16_bits(v);
 }
 
-constexpr int kStreamTokens = 8;
-
-// Threads of a launch: a grid of 2^32 or more is taken modulo that, without an error.
-constexpr int64_t kMostThreads = 0xffffffff;
-
 // Launchers, one unit per group length; hipErrorInvalidConfiguration, and nothing
 // launched, where the grid would have more threads.
 typedef hipError_t (*Launch)(const Args &a, hipStream_t s);
@@ -351,15 +332,6 @@ hipError_t launch_stream_128(const Args &a, hipStream_t s);
 hipError_t launch_tile_32(const Args &a, hipStream_t s);
 hipError_t launch_tile_64(const Args &a, hipStream_t s);
 hipError_t launch_tile_128(const Args &a, hipStream_t s);
-
-// The tile kernel's tile, 16 tb tokens x 64 rb weight rows with ks codes of K
-// at a time, and the parts of K: for M tokens, or with experts for `rows` rows
-// of them (one part).
-struct TilePick {
-    int tb, rb, ks, splits;
-};
-constexpr TilePick kShortTile{4, 2, 128, 1};                // for K below a stage of any tile
-TilePick pick_tile(int64_t M, int64_t N, int64_t K, int64_t experts, int64_t rows);
 
 }  // namespace w4
 }  // namespace qlin

@@ -1,8 +1,5 @@
 // Entry points of the products with 4-bit weights: checks, and the choice of
 // the kernel.
-#include <algorithm>
-#include <cmath>
-
 #include "qlin_w4.h"
 
 namespace qlin {
@@ -91,20 +88,6 @@ __global__ void __launch_bounds__(256) k_reduce(w4::Args a)
 
 size_t part_bytes(int64_t M, int64_t N, int splits) { return splits > 1 ? (size_t)splits * M * N * sizeof(float) : 0; }
 
-// Whether the streaming kernel takes the call: up to 8 tokens (8 on 51200 x 5120
-// 36 us, where the smallest tiles take 40; 12 would have to be streamed twice); of
-// experts, which differ in their rows, up to 4 on average, or 8 where a tile of 64
-// weight rows each does not fill the CUs twice.  128 experts on 1536 x 2048
-// with 4 rows each 48 us against 49 us with tiles, with 6 rows 60 and 51 us;
-// 8 experts on 1536 x 4096 with 8 rows each 15 and 16 us.
-bool streams(const w4::Args &a)
-{
-    if (!a.experts)
-        return a.M <= w4::kStreamTokens;
-    const int64_t few = a.experts * (((int64_t)a.N + 63) / 64) <= 512 ? w4::kStreamTokens : w4::kStreamTokens / 2;
-    return a.rows <= few * a.experts;
-}
-
 qlin_status status_of(hipError_t e)
 {
     return e == hipSuccess ? QLIN_OK : e == hipErrorInvalidConfiguration ? QLIN_ERR_BAD_SHAPE : QLIN_ERR_HIP;
@@ -118,7 +101,7 @@ qlin_status launch(w4::Args &a, void *ws, size_t ws_bytes, void *stream)
     const int group = a.K / a.G, which = group == 128 ? 2 : group == 64 ? 1 : 0;
     a.splits = 1;
     a.split_k = a.K;
-    if (streams(a))
+    if (w4::streams(a.M, a.N, a.experts, a.rows))
         return status_of(kStream[which](a, s));
     const w4::TilePick p = w4::pick_tile(a.M, a.N, a.K, a.experts, a.rows);
     const size_t need = part_bytes(a.M, a.N, p.splits);
@@ -150,63 +133,6 @@ qlin_status launch(w4::Args &a, void *ws, size_t ws_bytes, void *stream)
 
 }  // namespace
 
-namespace w4 {
-
-// The tile and the parts of K with the least estimated time.  A CU runs `at_once`
-// workgroups of a tile; with so many on every CU a stage takes `us` (`more` where
-// they come in several rounds), with fewer down to 0.4 of that, and starting and
-// ending a workgroup costs four stages.  Parts of K cost the traffic of their sums
-// and another launch: 1 us of the GPU's time, but 4 of a caller's who does not
-// replay graphs (59 tokens on 65 x 1280: 5.9 us in five parts, 6.3 in one, and 12.8
-// against 8.4 us a call).  Of all these tiles with 1 to 20 parts this choice takes
-// 3% longer on the GPU than the best on average, 13% at most, on eight shapes from 2048 x 2048
-// to 51200 x 5120 and 5120 x 25600 with 12 to 1000 tokens and groups of 64 and
-// 128.  12 tokens on 51200 x 5120: 39 us with rb = 2, 44 us with rb = 1; 32 on
-// 5120 x 25600: 32 us in ten parts, 251 us in one; 512 on 10240 x 5120: 80 us with
-// tb, rb = 4, 2, 96 us with 4, 4; 2048: 267 and 247 us.
-// With experts, whose rows differ, no tile is higher than 1.5 times their mean
-// (25 rows each of 128 experts on 1536 x 2048: 88 us with tb = 2, 105 us with 4);
-// this choice is then 1% off the best on average, 8 to 128 experts with 2 to
-// 150 rows each.
-TilePick pick_tile(int64_t M, int64_t N, int64_t K, int64_t experts, int64_t rows)
-{
-    static const struct {
-        int tb, rb, ks, at_once;
-        double us, more;
-    } kTiles[] = {{1, 1, 256, 3, 1.3, 1.3}, {1, 2, 256, 2, 1.55, 1.55}, {2, 1, 256, 3, 1.7, 1.7},
-                  {2, 2, 256, 2, 2.0, 2.0}, {4, 2, 128, 3, 2.0, 2.1}, {4, 4, 128, 2, 2.9, 2.5}};
-    constexpr int kMostParts = 20;
-    TilePick best = kShortTile;
-    double least = 1e30;
-    for (const auto &t : kTiles) {
-        const int64_t high = 16 * t.tb, stages = (K + t.ks - 1) / t.ks;
-        // each expert that has rows has a tile, and its last one is half full on average
-        const double mean = experts ? (double)rows / experts : 0;
-        if ((t.tb > 1 && experts && high > 1.5 * mean && K >= 256) || t.ks > K)
-            continue;
-        const double tall = experts ? experts * std::max(std::min(1.0, mean), mean / high + 0.5) : (double)((M + high - 1) / high);
-        const double each_cu = tall * ((N + 64 * t.rb - 1) / (64 * t.rb)) / 256;
-        // (outputs that are too many for one launch of the sum of the parts are not split)
-        const int most = experts || M * N > w4::kMostThreads / 2 ? 1 : (int)std::min<int64_t>(kMostParts, stages);
-        for (int splits = 1; splits <= most; ++splits) {
-            const int64_t each = (stages + splits - 1) / splits;
-            if ((stages + each - 1) / each != splits)
-                continue;                                    // a part would be empty
-            const double whole = std::floor(each_cu * splits / t.at_once);
-            const double rest = std::ceil(each_cu * splits - whole * t.at_once - 1e-9);
-            double us = (whole + (rest > 0 ? 0.4 + 0.6 * rest / t.at_once : 0)) * (each + 4) * (whole > 0 ? t.more : t.us);
-            if (splits > 1)
-                us += 4.0 + splits * (double)M * N * 8 / 5e6;
-            if (us < least) {
-                least = us;
-                best = TilePick{t.tb, t.rb, t.ks, splits};
-            }
-        }
-    }
-    return best;
-}
-
-}  // namespace w4
 }  // namespace qlin
 
 using namespace qlin;

@@ -37,9 +37,6 @@
 namespace qlin {
 namespace w4 {
 
-constexpr int kSlot = 256;
-constexpr int kStreamWaves = 8;
-
 // Where a lane's loads go: bases of the workgroup's rows at code 0, and the
 // lane's offsets from them (bytes; of scales, elements).
 template <int U>
@@ -277,7 +274,7 @@ __global__ void __launch_bounds__(64 * kStreamWaves) k_stream(Args a)
 template <int U, int GROUP, int SB, bool ZERO, int ENDS>
 hipError_t launch_stream_as(const Args &a, int waves, hipStream_t s)
 {
-    const int64_t grid = (int64_t)((a.N + 8 * U - 1) / (8 * U)) * row_tiles(a, kStreamTokens);
+    const int64_t grid = (int64_t)((a.N + 8 * U - 1) / (8 * U)) * row_tiles(a.M, a.experts, a.rows, kStreamTokens);
     waves = min(waves, (a.K + kSlot - 1) / kSlot);
     if (grid * 64 * waves > kMostThreads)
         return hipErrorInvalidConfiguration;
@@ -289,37 +286,22 @@ hipError_t launch_stream_as(const Args &a, int waves, hipStream_t s)
 template <int GROUP, int SB, bool ZERO, int ENDS>
 hipError_t stream_pick(const Args &a, hipStream_t s)
 {
-    // More rows a workgroup share one read of the tokens and one start, fewer
-    // give the 256 CUs more workgroups: 8 rows up to two workgroups a CU, 32
-    // from 16 times that (experts: of the tiles in the grid).  Measured, us
-    // with 8 / 16 / 32 rows, one token: 4.9 / 5.1 / 5.7 (2048 x 2048),
-    // 12.6 / 11.0 / 11.7 (10240 x 5120), 36 / 32.8 / 31.3 (51200 x 5120).  Where K
-    // is long, reading the tokens again is what costs, and 32 rows share it: 8
-    // tokens on 5120 x 25600 28.6 against 36.1 us with 16 rows, one token 24.8 and
-    // 25.6; on 5120 x 8192 11.4 and 12.2, 11.0 both.
-    // Waves: as many as K has slots while workgroups are few, one or two when
-    // they fill the GPU by themselves (32 tokens through 128 experts of 2048 x
-    // 768: 25.7 with one, 30.3 with two, 33.9 with three); experts' workgroups
-    // without rows count half (one token: 8 of 129 tiles have any; 10.6 with two
-    // waves, 13.8 with one on 1536 x 2048).
-    const int64_t tiles = a.experts ? row_tiles(a, kStreamTokens) : 1, units = (int64_t)((a.N + 7) / 8) * tiles;
-    const int u = units >= 4096 || (a.K >= 8192 && units > 512) ? 4 : units > 512 ? 2 : 1;
-    const int64_t busy = a.experts ? (units + (int64_t)((a.N + 7) / 8) * min((int64_t)a.rows, tiles) + 1) / 2 : units;
-    const int waves = (int)min(max((6144 * u + busy - 1) / busy, (int64_t)1), (int64_t)kStreamWaves);
-    switch (u) {
-    case 1: return launch_stream_as<1, GROUP, SB, ZERO, ENDS>(a, waves, s);
-    case 2: return launch_stream_as<2, GROUP, SB, ZERO, ENDS>(a, waves, s);
-    default: return launch_stream_as<4, GROUP, SB, ZERO, ENDS>(a, waves, s);
+    const StreamPick p = pick_stream(a.N, a.K, a.experts, a.rows);
+    switch (p.u) {
+    case 1: return launch_stream_as<1, GROUP, SB, ZERO, ENDS>(a, p.waves, s);
+    case 2: return launch_stream_as<2, GROUP, SB, ZERO, ENDS>(a, p.waves, s);
+    default: return launch_stream_as<4, GROUP, SB, ZERO, ENDS>(a, p.waves, s);
     }
 }
 
 template <int GROUP, int SB, bool ZERO>
 hipError_t stream_ends(const Args &a, hipStream_t s)
 {
-    // (a dword of zero points needs four groups)
-    if (a.K < kSlot || a.G < 4)
-        return stream_pick<GROUP, SB, ZERO, kShort>(a, s);
-    return a.K % kSlot == 0 ? stream_pick<GROUP, SB, ZERO, kWhole>(a, s) : stream_pick<GROUP, SB, ZERO, kInside>(a, s);
+    switch (stream_end(a.K, a.G)) {
+    case kWhole: return stream_pick<GROUP, SB, ZERO, kWhole>(a, s);
+    case kInside: return stream_pick<GROUP, SB, ZERO, kInside>(a, s);
+    default: return stream_pick<GROUP, SB, ZERO, kShort>(a, s);
+    }
 }
 
 template <int GROUP>

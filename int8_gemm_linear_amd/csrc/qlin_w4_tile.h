@@ -406,7 +406,7 @@ __global__ void __launch_bounds__(64 * kTileWaves, 2) k_tile(Args a)
 template <int TB, int RB, int KS, int GROUP, int SB, bool ZERO, int ENDS>
 hipError_t launch_tile_as(Args a, hipStream_t s)
 {
-    const int64_t tiles = row_tiles(a, 16 * TB);
+    const int64_t tiles = row_tiles(a.M, a.experts, a.rows, 16 * TB);
     if (tiles > 0x7fffffff / 8)
         return hipErrorInvalidConfiguration;
     a.tiles = (int)tiles;
@@ -421,7 +421,7 @@ hipError_t launch_tile_as(Args a, hipStream_t s)
 template <int TB, int RB, int KS, int GROUP, int SB, bool ZERO>
 hipError_t tile_ends(const Args &a, hipStream_t s)
 {
-    if (a.K % KS == 0)
+    if (tile_end(a.K, KS) == kWhole)
         return launch_tile_as<TB, RB, KS, GROUP, SB, ZERO, kWhole>(a, s);
     return launch_tile_as<TB, RB, KS, GROUP, SB, ZERO, kInside>(a, s);
 }
