@@ -307,7 +307,12 @@ qlin_status qlin_silu_and_mul_per_block_quant(int64_t M, int64_t K, const uint16
  *   Y[m,n] = bf16( sum_g s[n,g] * sum_{k in group g} X[m,k] * (q[n,k] - z[n,g]) )
  * with q in 0..15, groups of `group` (32, 64 or 128) consecutive k starting at
  * k = 0, and z = 8 when b_zero is NULL.  The products are exact, the sums
- * fp32, the result is rounded once to bf16.
+ * fp32, the result is rounded once to bf16.  The sums are of x (128 + q) or
+ * x (143 + q - z), from which as many times the group's sum of x is taken
+ * away, so their rounding goes with |x| and not with |x (q - z)|: beside the
+ * rounding to bf16 an output is off by at most
+ *   2^-23 sum_k |s x| ((group + 4) (286 + q) + (2 K / group + 40) |q - z|),
+ * also where a large x meets q = z.
  *
  * X [M][ldx] bf16 bits.  B [N][ldb] bytes, two codes per byte: byte j of a row
  * holds k = 2j in its low and k = 2j + 1 in its high nibble.  b_scale
@@ -318,12 +323,13 @@ qlin_status qlin_silu_and_mul_per_block_quant(int64_t M, int64_t K, const uint16
  * Shapes: M >= 0, N >= 0 (0 is a no-op), 0 < K <= 2^20, K % group == 0.
  * ldx >= K with ldx % 8 == 0 (elements), ldb >= K/2 with ldb % 16 == 0
  * (bytes), ldy >= N, rows of X and B at most 2^25 bytes apart; X, B and Y
- * 16-byte aligned, b_scale 4-byte aligned.  An
- * infinity or NaN in X reaches the outputs that the formula gives it and no
- * other row; outputs that are not finite in fp32 are computed a second time in
- * fp64, which costs such a row many times an ordinary one (one infinity among
- * 1000 tokens doubles the call; one in each makes it 100 times as long).  The caller owns every buffer; the call is asynchronous on
- * `stream` and allocates nothing.  workspace: qlin_w4_workspace_size bytes,
+ * 16-byte aligned, b_scale 4-byte aligned.  An infinity or NaN in X reaches
+ * the outputs that the formula gives it and no other row; outputs that are not
+ * finite in fp32 are computed a second time in fp64, which such a row pays for:
+ * one infinity among 1000 tokens on 10240 x 5120 doubles the call, one in each,
+ * or one among 32 tokens on 5120 x 25600, makes it 70 to 130 times as long.
+ * The caller owns every buffer, and Y overlaps no other; the call is
+ * asynchronous on `stream` and allocates nothing.  workspace: qlin_w4_workspace_size bytes,
  * 16-byte aligned, with any contents, not used by two calls that may overlap
  * in time (the parts of K where M x N alone is too little work for the GPU;
  * they are added in order, so results do not depend on timing).  Errors as for
@@ -381,7 +387,7 @@ qlin_status qlin_grouped_w4_mm(int64_t groups, const int32_t *group_offsets, int
  *   moe_combine_backward   dY[slot_row[t,j]] = w[t,j] * dOut[t],
  *                          dW[t,j] = sum_k dOut[t,k] * Y[slot_row[t,j],k]
  *   moe_permute_backward   dX[t] = sum_j dOut[slot_row[t,j]]
- * Absent slots are skipped (their weight is not read) and get dW = 0; a token
+ * Absent slots are skipped (their weight is not used) and get dW = 0; a token
  * with no present slot gets a zero row.  Rows that belong to no slot are
  * neither read nor written.  Sums are fp32, over j in ascending order, and
  * are rounded once; results do not depend on timing.  dY may not overlap Y,

@@ -688,7 +688,8 @@ def grouped_w4_mm(x, b_q, b_scale, group_offsets, max_rows: int, b_zero=None, ou
     """w4_mm for each expert's rows: expert g computes rows group_offsets[g] ..
     group_offsets[g+1]-1 of x bf16 [rows,K] against b_q[g] uint8 [N, K/2] with
     b_scale[g] (and b_zero[g]) [N, K/group]; bf16 out [rows,N].  group_offsets
-    int32 [G+1] on the device; max_rows bounds any expert's row count."""
+    int32 [G+1] on the device; max_rows bounds any expert's row count, and an
+    expert's rows beyond it are not computed."""
     if x.dtype != torch.bfloat16:
         raise TypeError(f"x must be bfloat16, got {x.dtype}")
     if b_q.dtype != torch.uint8:
@@ -714,6 +715,7 @@ def grouped_w4_mm(x, b_q, b_scale, group_offsets, max_rows: int, b_zero=None, ou
 # ---------------------------------------------------------------------------
 # Routing of tokens to experts.  topk_ids [T, topk] holds each token's
 # experts; an id outside 0..experts-1 makes its slot absent.
+# The calls are no part of torch's autograd: the gradients are calls of their own.
 # ---------------------------------------------------------------------------
 _ROW_TYPE = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 
