@@ -42,11 +42,11 @@ inline int64_t row_tiles(int64_t M, int64_t experts, int64_t rows, int tile)
 }
 
 // Whether the streaming kernel takes the call: up to 8 tokens (8 on 51200 x 5120
-// 36 us, where the smallest tiles take 40; 12 would have to be streamed twice); of
+// 35 us, where tiles take 38 for 9; 12 would have to be streamed twice); of
 // experts, which differ in their rows, up to 4 on average, or 8 where a tile of 64
 // weight rows each does not fill the CUs twice.  128 experts on 1536 x 2048
-// with 4 rows each 48 us against 49 us with tiles, with 6 rows 60 and 51 us;
-// 8 experts on 1536 x 4096 with 8 rows each 15 and 16 us.
+// with 4 rows each 50 us against 51 us with tiles, with 6 rows 55 and 50 us;
+// 8 experts on 1536 x 4096 with 8 rows each 10 and 21 us.
 inline bool streams(int64_t M, int64_t N, int64_t experts, int64_t rows)
 {
     if (!experts)
@@ -64,16 +64,16 @@ struct StreamPick {
 // More rows a workgroup share one read of the tokens and one start, fewer
 // give the 256 CUs more workgroups: 8 rows up to two workgroups a CU, 32
 // from 16 times that (experts: of the tiles in the grid).  Measured, us
-// with 8 / 16 / 32 rows, one token: 4.9 / 5.1 / 5.7 (2048 x 2048),
-// 12.6 / 11.0 / 11.7 (10240 x 5120), 36 / 32.8 / 31.3 (51200 x 5120).  Where K
+// with 8 / 16 / 32 rows, one token: 3.6 / 3.8 / 4.5 (2048 x 2048),
+// 12.1 / 9.8 / 10.1 (10240 x 5120), 48 / 34.8 / 29.8 (51200 x 5120).  Where K
 // is long, reading the tokens again is what costs, and 32 rows share it: 8
-// tokens on 5120 x 25600 28.6 against 36.1 us with 16 rows, one token 24.8 and
-// 25.6; on 5120 x 8192 11.4 and 12.2, 11.0 both.
+// tokens on 5120 x 25600 24.5 against 32.2 us with 16 rows, one token 23.6 and
+// 22.8; on 5120 x 8192 10.8 and 12.3, 10.3 and 10.1.
 // Waves: as many as K has slots while workgroups are few, one or two when
 // they fill the GPU by themselves (32 tokens through 128 experts of 2048 x
-// 768: 25.7 with one, 30.3 with two, 33.9 with three); experts' workgroups
-// without rows count half (one token: 8 of 129 tiles have any; 10.6 with two
-// waves, 13.8 with one on 1536 x 2048).
+// 768: 22.4 with one, 25.1 with two, 26.7 with three); experts' workgroups
+// without rows count half (one token: 8 of 129 tiles have any; 12.1 with two
+// waves, 16.3 with one on 1536 x 2048).
 inline StreamPick pick_stream(int64_t N, int64_t K, int64_t experts, int64_t rows)
 {
     const int64_t tiles = experts ? row_tiles(0, experts, rows, kStreamTokens) : 1, units = (N + 7) / 8 * tiles;
@@ -102,17 +102,19 @@ constexpr TilePick kShortTile{4, 2, 128, 1};                // for K below a sta
 // they come in several rounds), with fewer down to 0.4 of that, and starting and
 // ending a workgroup costs four stages.  Parts of K cost the traffic of their sums
 // and another launch: 1 us of the GPU's time, but 4 of a caller's who does not
-// replay graphs (59 tokens on 65 x 1280: 5.9 us in five parts, 6.3 in one, and 12.8
-// against 8.4 us a call).  Of all these tiles with 1 to 20 parts this choice takes
-// 3% longer on the GPU than the best on average, 13% at most, on eight shapes from 2048 x 2048
-// to 51200 x 5120 and 5120 x 25600 with 12 to 1000 tokens and groups of 64 and
-// 128.  12 tokens on 51200 x 5120: 39 us with rb = 2, 44 us with rb = 1; 32 on
-// 5120 x 25600: 32 us in ten parts, 251 us in one; 512 on 10240 x 5120: 80 us with
-// tb, rb = 4, 2, 96 us with 4, 4; 2048: 267 and 247 us.
+// replay graphs (59 tokens on 65 x 1280: 5.8 us in five parts, 6.7 in one, and 14.0
+// against 9.5 us a call).  When it was fitted, of all these tiles with 1 to 20 parts
+// this choice took 3% longer on the GPU than the best on average, 13% at most, on
+// eight shapes from 2048 x 2048 to 51200 x 5120 and 5120 x 25600 with 12 to 1000
+// tokens and groups of 64 and 128.  12 tokens on 51200 x 5120: 40 us with rb = 2,
+// 43 us with rb = 1; 32 on 5120 x 25600 with groups of 64 and zero points: 35 us in
+// the twelve parts it picks (nine stages each, the last a single one), 37 in ten,
+// 41 in twenty, 168 in one; 512 on 10240 x 5120: 75 us with tb, rb = 4, 2, 85 us
+// with 4, 4; 2048: 263 and 234 us.
 // With experts, whose rows differ, no tile is higher than 1.5 times their mean
-// (25 rows each of 128 experts on 1536 x 2048: 88 us with tb = 2, 105 us with 4);
-// this choice is then 1% off the best on average, 8 to 128 experts with 2 to
-// 150 rows each.
+// (25 rows each of 128 experts on 1536 x 2048: 68 us as picked, 1, 2; 75 us with
+// 2, 2; 86 us with tb = 4); this choice was then 1% off the best on average, 8 to
+// 128 experts with 2 to 150 rows each.
 inline TilePick pick_tile(int64_t M, int64_t N, int64_t K, int64_t experts, int64_t rows)
 {
     static const struct {

@@ -23,13 +23,14 @@
 // take 160 to 210 registers, two or three waves: with groups of 128 the same time
 // on 51200 x 5120, with groups of 32 and for experts, most of whose workgroups have
 // nothing to do, 10 to 35% more; 27 tokens, top-8, 64 experts of 809 x 1216 23.0
-// against 18.0 us.)  The waves' sums meet in LDS and are added in wave order: no
+// against 18.0 us then, 14.0 now.)  The waves' sums meet in LDS and are added in wave order: no
 // second launch, no workspace, and the same bits every time.
 //
 // The bytes bound it from below and the vector instructions come close behind:
 // 226 for 256 codes of 32 rows, half of which turn codes into bf16, keep the
-// vector units busy for 57% of the time.  One token on 51200 x 5120: 30 us, 4.5
-// TB/s; 32 tokens through 128 experts of 1536 x 2048: 35 to 42 us by the experts hit.
+// vector units busy for 40% of the counted cycles, a third of which are the launch's
+// start and end.  One token on 51200 x 5120: 30 us, 4.5 TB/s; 32 tokens through 128
+// experts of 1536 x 2048: 35 to 43 us by the experts hit.
 #pragma once
 
 #include "qlin_w4.h"

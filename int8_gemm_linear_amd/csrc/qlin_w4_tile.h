@@ -13,13 +13,14 @@
 // Where M x N is too few tiles for the 256 CUs, K is split over workgroups
 // whose sums a second kernel adds in order.
 //
-// With many tokens the matrix instructions and the vector instructions that
-// expand codes and scale sums take about as long as each other, and two or three
-// waves on a SIMD overlap them: 1000 tokens on 10240 x 5120 138 us, 760 TFLOP/s;
-// 2048 tokens 238 us, 900 TFLOP/s.  With few, it is the time of a stage, from its
-// loads to its products, over the parts of K: 32 tokens on 5120 x 25600 with zero
-// points 35 us.  16 000 rows of 128 experts on 2048 x 768 115 us, 440 TFLOP/s: six
-// stages a tile, which starting and ending it outweigh.
+// With many tokens the vector units, which expand codes and scale sums, are busy for
+// 47% and the matrix cores for 40% of the time: a wave expands a group before its
+// products and scales after them, and the two or three waves of a SIMD overlap that
+// in part only.  1000 tokens on 10240 x 5120 134 us, 780 TFLOP/s; 2048 tokens 232 us,
+// 925 TFLOP/s.  With few, it is the time of a stage, from its loads to its products,
+// over the parts of K: 32 tokens on 5120 x 25600 with zero points 34 us.  16 000 rows
+// of 128 experts on 2048 x 768 109 us, 460 TFLOP/s: six stages a tile, which starting
+// and ending it outweigh.
 #pragma once
 
 #include "qlin_w4.h"
