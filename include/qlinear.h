@@ -435,6 +435,136 @@ qlin_status qlin_moe_permute_backward(qlin_row_type rt, int64_t tokens, int64_t 
                                       const int32_t *slot_row, void *dX, int64_t ldx,
                                       void *stream);
 
+/* Low-rank adapters of many requests beside a shared projection.  Token t has
+ * the adapter i = ids[t] (int32, or int64 with id_bits = 64; a value outside
+ * 0..adapters-1 is none), s_i = scale[i] (NULL: 1):
+ *   lora_mm           Y[t] = bf16( base[t] + s_i (X[t] A_i^T) B_i^T )
+ *   lora_mm_backward  u[t] = dY[t] B_i;  dX[t] = bf16( base[t] + s_i u[t] A_i ),
+ *                     dA_i = s_i sum_t u[t]^T X[t],
+ *                     dB_i = s_i sum_t dY[t]^T (X[t] A_i^T),  t over i's tokens
+ * `base` is the shared projection's output (of backward: the gradient that
+ * reached X through it); NULL counts as zeros.  A token without an adapter gets
+ * base[t] (zeros without base), an adapter without tokens dA = dB = 0.  Requests
+ * of several ranks share a call with their adapters' missing ranks as zeros.
+ *
+ * The products of bf16 values are exact, sums fp32.  X A^T (and u), fp32, go
+ * into the second product as their upper 16 bits and a bf16 rest, off by at
+ * most 2^-16 of each; into dA and dB whole.  Y and dX are rounded once, dA and
+ * dB are fp32.  No result depends on timing.
+ *
+ * X [tokens][ldx], dY [tokens][lddy], base, Y, dX: bf16 bits, row-major; A
+ * [adapters][rank][K] and B [adapters][N][rank] bf16 bits, contiguous, and so
+ * are dA and dB, fp32.  Strides in elements; every buffer aligned to its element.
+ *
+ * Shapes: 0 <= tokens <= 2^24, 0 < K <= 2^20, 0 <= N <= 2^20 (backward: 0 < N;
+ * 0 tokens or N is a no-op, but backward then writes dA = dB = 0), rank 8..128
+ * in steps of 8, 1 <= adapters <= 2048, adapters * max(rank, 64) * max(K, N) <
+ * 2^35.  Y may be `base` itself (the same address and stride), dX likewise; no
+ * other output may overlap another buffer.  workspace: the size below, 16-byte
+ * aligned, any contents, not used by two calls that may overlap in time.  The
+ * calls are asynchronous on `stream` and allocate nothing.  Errors as for
+ * qlin_scaled_mm. */
+size_t qlin_lora_workspace_size(int64_t tokens, int64_t K, int64_t N, int64_t rank, int64_t adapters);
+qlin_status qlin_lora_mm(int32_t id_bits, int64_t tokens, int64_t K, int64_t N, int64_t rank,
+                         int64_t adapters, const uint16_t *X, int64_t ldx, const uint16_t *A,
+                         const uint16_t *B, const void *ids, const float *scale,
+                         const uint16_t *base, int64_t ldb, uint16_t *Y, int64_t ldy,
+                         void *workspace, size_t workspace_bytes, void *stream);
+size_t qlin_lora_backward_workspace_size(int64_t tokens, int64_t K, int64_t N, int64_t rank,
+                                         int64_t adapters);
+qlin_status qlin_lora_mm_backward(int32_t id_bits, int64_t tokens, int64_t K, int64_t N,
+                                  int64_t rank, int64_t adapters, const uint16_t *dY, int64_t lddy,
+                                  const uint16_t *X, int64_t ldx, const uint16_t *A,
+                                  const uint16_t *B, const void *ids, const float *scale,
+                                  const uint16_t *base, int64_t ldb, uint16_t *dX, int64_t lddx,
+                                  float *dA, float *dB, void *workspace, size_t workspace_bytes,
+                                  void *stream);
+
+/* Log probabilities of one given token for each row of logits, with the row's
+ * entropy, the log of its sum of exponentials and its best alternatives:
+ *   lse[r] = ln sum_v exp(x[r,v]),  logprob[r] = x[r,target[r]] - lse[r],
+ *   entropy[r] = -sum_v p_v ln p_v  with  ln p_v = x[r,v] - lse[r],
+ *   top_id[r][j], top_logprob[r][j]: the `top` largest logits in order, equal
+ *   ones by their index, and their ln p.
+ * A target outside 0..V-1 (padding) gets logprob 0.  A logit of -inf is a
+ * banned token: p = 0.  A row of nothing but -inf has no distribution: lse and
+ * its log probabilities are -inf, its entropy is 0.  A NaN or +inf makes lse,
+ * entropy and the log probabilities of its row NaN; NaNs are no alternatives
+ * (top_id -1 where a row has fewer than `top` others).
+ *
+ * The gradient, from the forward call's lse and entropy:
+ *   dX[r,v] = g_r ([v = target[r]] - p_v) - h_r p_v (ln p_v + entropy[r]),
+ * g = dlogprob (0 for a target outside 0..V-1), h = dentropy (NULL: 0, and
+ * entropy is not read).  Rows with g = h = 0 and rows without a distribution
+ * get zeros whatever their logits hold.
+ *
+ * logits [rows][ld] of type rt; target [rows] int32, or int64 with id_bits =
+ * 64; outputs fp32 (top_id int32) and contiguous, dlogits [rows][ldo] of type
+ * rt, rounded once; it may be the logits themselves (the same address and
+ * stride), else nothing overlaps.  All sums are fp32, in an order that does not
+ * depend on timing.
+ *
+ * Shapes: 0 <= rows <= 2^23 (0 is a no-op), 0 < V <= 2^28, 0 <= top <= 64 and
+ * top <= V.  Every buffer is aligned to its element, the workspace
+ * (qlin_token_logprobs_workspace_size bytes, 0 for many rows) to 8 bytes; it
+ * has any contents and is not used by two calls that may overlap in time.  The
+ * calls are asynchronous on `stream` and allocate nothing.  Errors as for
+ * qlin_scaled_mm. */
+size_t qlin_token_logprobs_workspace_size(qlin_row_type rt, int64_t rows, int64_t V, int64_t top);
+qlin_status qlin_token_logprobs(qlin_row_type rt, int32_t id_bits, int64_t rows, int64_t V,
+                                int64_t top, const void *logits, int64_t ld, const void *target,
+                                float *logprob, float *entropy, float *lse, float *top_logprob,
+                                int32_t *top_id, void *workspace, size_t workspace_bytes,
+                                void *stream);
+qlin_status qlin_token_logprobs_backward(qlin_row_type rt, int32_t id_bits, int64_t rows, int64_t V,
+                                         const float *dlogprob, const float *dentropy,
+                                         const void *logits, int64_t ld, const void *target,
+                                         const float *lse, const float *entropy, void *dlogits,
+                                         int64_t ldo, void *stream);
+
+/* Embedding: Out[t,k] = scale * s[ids[t], k / 128] * table[ids[t], k], zeros
+ * where ids[t] is outside 0..vocab-1 (padding).  The table is plain, or codes
+ * with scales as the quantizers above give them: row_scale [vocab][scale_cols]
+ * with scale_cols 0 (none, row_scale NULL), 1 (a scale per row) or width / 128
+ * (one per 128 values); any table type goes with any of these and any output
+ * type ot.  Products are fp32, rounded once.
+ *
+ * Its gradient, dTable[v] = scale * sum_{t: ids[t] = v} dOut[t]: the positions
+ * are sorted by token and each token's rows added in fp32, in their order (in
+ * groups of 16 sorted positions), and rounded once; results do not depend on
+ * timing.  Every row of dTable is written, those of no position with zeros;
+ * with `accumulate` only rows with positions are, and their sum is added to
+ * what they hold.  dTable is of type ot: dOut's type rt, or fp32.
+ *
+ * ids [tokens] int32, or int64 with id_bits = 64.  table [vocab][ldt], Out
+ * [tokens][ldo], dOut [tokens][ldd], dTable [vocab][ldt]: strides in elements,
+ * every buffer aligned to its element.  No output overlaps another buffer.
+ *
+ * Shapes: 0 <= tokens < 2^30, 0 < vocab < 2^31, 0 < width <= 2^20; of the
+ * gradient tokens < 2^28, vocab < 2^22 and
+ * ceil(tokens / 16) * ceil(width / 1024) < 2^24.  workspace:
+ * the size below, 16-byte aligned, any contents, not used by two calls that may
+ * overlap in time.  The calls are asynchronous on `stream` and allocate
+ * nothing.  Errors as for qlin_scaled_mm. */
+typedef enum qlin_table_type {
+    QLIN_TABLE_F32 = 0,
+    QLIN_TABLE_BF16 = 1,
+    QLIN_TABLE_F16 = 2,
+    QLIN_TABLE_INT8 = 3,
+    QLIN_TABLE_E4M3 = 4
+} qlin_table_type;
+
+qlin_status qlin_embedding(qlin_table_type tt, qlin_row_type ot, int32_t id_bits, int64_t tokens,
+                           int64_t vocab, int64_t width, const void *ids, const void *table,
+                           int64_t ldt, const float *row_scale, int64_t scale_cols, float scale,
+                           void *Out, int64_t ldo, void *stream);
+size_t qlin_embedding_backward_workspace_size(int64_t tokens, int64_t vocab, int64_t width);
+qlin_status qlin_embedding_backward(qlin_row_type rt, qlin_row_type ot, int32_t id_bits,
+                                    int64_t tokens, int64_t vocab, int64_t width, const void *ids,
+                                    const void *dOut, int64_t ldd, float scale, int32_t accumulate,
+                                    void *dTable, int64_t ldt, void *workspace,
+                                    size_t workspace_bytes, void *stream);
+
 /* The config the table selects for a problem: the entry for (scaling, dt,
  * N, K) at the smallest tuned M >= M (else the largest tuned M); shapes not
  * in the table get the format's default for that M range. */

@@ -12,6 +12,9 @@ and the current stream.
     Y = w4_mm(x, b_q, b_scale, b_zero)                 # 4-bit weights, bf16 activations
     rows, scales, off, slot_row = moe_dispatch(x, topk_ids, experts, scale)
     Y = moe_combine(expert_rows, slot_row, weights)    # grouped products lie between the two
+    Y = lora_mm(x, a, b, adapter_ids, scale, base=Y)   # low-rank adapters of many requests
+    logprob, entropy, lse, top, top_id = token_logprobs(logits, target, top=5)
+    x = embedding(ids, table, row_scale)               # plain tables, or codes with scales
 
 ``a_q`` [M,K] and ``b_q`` [N,K] (torch.float8_e4m3fn or torch.int8, rows
 K-contiguous); fp32 scales ``a_scale`` [M] and ``b_scale`` [N], or for the
@@ -181,6 +184,26 @@ def _lib():
     lib.qlin_moe_combine_backward.restype = I
     lib.qlin_moe_permute_backward.argtypes = [I, I64, I64, I64, I64, P, I64, P, P, I64, P]
     lib.qlin_moe_permute_backward.restype = I
+    I32 = ctypes.c_int32
+    lib.qlin_lora_workspace_size.argtypes = lib.qlin_lora_backward_workspace_size.argtypes = [I64] * 5
+    lib.qlin_lora_workspace_size.restype = lib.qlin_lora_backward_workspace_size.restype = SZ
+    lib.qlin_lora_mm.argtypes = [I32, I64, I64, I64, I64, I64, P, I64, P, P, P, P, P, I64, P, I64, P, SZ, P]
+    lib.qlin_lora_mm.restype = I
+    lib.qlin_lora_mm_backward.argtypes = [I32, I64, I64, I64, I64, I64, P, I64, P, I64, P, P, P, P, P, I64, P, I64,
+                                          P, P, P, SZ, P]
+    lib.qlin_lora_mm_backward.restype = I
+    lib.qlin_token_logprobs_workspace_size.argtypes = [I, I64, I64, I64]
+    lib.qlin_token_logprobs_workspace_size.restype = SZ
+    lib.qlin_token_logprobs.argtypes = [I, I32, I64, I64, I64, P, I64, P, P, P, P, P, P, P, SZ, P]
+    lib.qlin_token_logprobs.restype = I
+    lib.qlin_token_logprobs_backward.argtypes = [I, I32, I64, I64, P, P, P, I64, P, P, P, P, I64, P]
+    lib.qlin_token_logprobs_backward.restype = I
+    lib.qlin_embedding.argtypes = [I, I, I32, I64, I64, I64, P, P, I64, P, I64, F, P, I64, P]
+    lib.qlin_embedding.restype = I
+    lib.qlin_embedding_backward_workspace_size.argtypes = [I64, I64, I64]
+    lib.qlin_embedding_backward_workspace_size.restype = SZ
+    lib.qlin_embedding_backward.argtypes = [I, I, I32, I64, I64, I64, P, P, I64, F, I32, P, I64, P, SZ, P]
+    lib.qlin_embedding_backward.restype = I
     _LIB = lib
     return lib
 
@@ -875,6 +898,236 @@ def moe_permute_backward(drows, slot_row, out=None):
     _call_on(dev, _lib().qlin_moe_permute_backward,
              (rt, T, topk, rows, K, drows.data_ptr(), ld, slot_row.data_ptr(), out.data_ptr(), ldo),
              "qlin_moe_permute_backward")
+    return out
+
+
+# ---------------------------------------------------------------------------
+# Low-rank adapters, log probabilities and the embedding.  The calls are no
+# part of torch's autograd: the gradients are calls of their own.
+# ---------------------------------------------------------------------------
+def _tokens(ids, T, device, name="ids"):
+    """The bits of a contiguous [T] tensor of int32 or int64 ids."""
+    bits = _ID_BITS.get(ids.dtype)
+    if bits is None:
+        raise TypeError(f"{name} must be int32 or int64, got {ids.dtype}")
+    if ids.dim() != 1 or ids.device != device or not ids.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous [T] tensor, on one device with the others")
+    if T is not None and ids.shape[0] != T:
+        raise ValueError(f"{name} has {ids.shape[0]} entries for {T} rows")
+    return bits
+
+
+_ID_BITS = {torch.int32: 32, torch.int64: 64}
+
+
+def _own_workspace(n, like):
+    """(address or None, the tensor that holds it): the call's own workspace, as in _sort_buffers."""
+    if not n:
+        return None, None
+    ws = like.new_empty(n, dtype=torch.uint8)
+    return ws.data_ptr(), ws
+
+
+def _adapters(x, a, b, ids, scale):
+    """Checks of the arguments that both adapter calls share: (bits, T, K, N, rank, adapters), x's row
+    stride and the scale's address."""
+    for t, name in ((x, "x"), (a, "a"), (b, "b")):
+        if t.dtype != torch.bfloat16:
+            raise TypeError(f"{name} must be bfloat16, got {t.dtype}")
+    dev = x.device
+    T, K, ldx = _matrix(x, "x", dev)
+    if a.dim() != 3 or b.dim() != 3:
+        raise ValueError("a must be [adapters, rank, K] and b [adapters, N, rank]")
+    L, R, cols = a.shape
+    N = b.shape[1]
+    if cols != K or b.shape[0] != L or b.shape[2] != R:
+        raise ValueError(f"x is [T,K], a must be [adapters, rank, K] and b [adapters, N, rank], got "
+                         f"{tuple(x.shape)}, {tuple(a.shape)} and {tuple(b.shape)}")
+    if a.device != dev or b.device != dev or not a.is_contiguous() or not b.is_contiguous():
+        raise ValueError("a and b must be contiguous, on one device with the others")
+    bits = _tokens(ids, T, dev)
+    if scale is not None:
+        _flat(scale, torch.float32, (L,), "scale", dev)
+    return (bits, T, K, N, R, L), ldx, None if scale is None else scale.data_ptr()
+
+
+def _base(base, shape, like):
+    """(address, row stride) of an optional bf16 tensor that an adapter's product is added to."""
+    if base is None:
+        return None, 0
+    if base.dtype != torch.bfloat16 or base.shape != shape:
+        raise ValueError(f"base must be a bfloat16 tensor of shape {tuple(shape)}")
+    return base.data_ptr(), _matrix(base, "base", like.device)[2]
+
+
+def lora_mm(x, a, b, ids, scale=None, base=None, out=None):
+    """Low-rank adapters of many requests beside a shared projection: bf16 [T,N],
+    out[t] = base[t] + scale[i] (x[t] a[i]^T) b[i]^T with i = ids[t], the adapter of
+    the token's request; a token whose id is outside 0..adapters-1 has none and gets
+    base[t].  x bf16 [T,K]; a bf16 [adapters, rank, K] and b bf16 [adapters, N, rank],
+    rank 8..128 in steps of 8 (adapters of a lower rank: zeros); ids int32 or int64
+    [T] in any order; scale float32 [adapters] (None: 1); base bf16 [T,N], the
+    projection's output (None: zeros), which may be `out`."""
+    dims, ldx, sc = _adapters(x, a, b, ids, scale)
+    T, N = dims[1], dims[3]
+    addr, ldb = _base(base, (T, N), x)
+    out, ldy = _rows_out(out, (T, N), x)
+    lib = _lib()
+    n = lib.qlin_lora_workspace_size(*dims[1:])
+    ws, held = _own_workspace(n, x)
+    _call_on(x.device, lib.qlin_lora_mm,
+             (*dims, x.data_ptr(), ldx, a.data_ptr(), b.data_ptr(), ids.data_ptr(), sc, addr, ldb, out.data_ptr(), ldy,
+              ws, n), "qlin_lora_mm")
+    return out
+
+
+def lora_mm_backward(dy, x, a, b, ids, scale=None, base=None, out=None):
+    """Gradients of lora_mm: (dx bf16 [T,K], da float32 [adapters, rank, K], db float32
+    [adapters, N, rank]) from dy bf16 [T,N] and the call's inputs.  `base` bf16 [T,K]
+    is the gradient that reached x through the shared projection (None: zeros); dx is
+    added to it, and may be written to it (out=base).  Adapters without tokens get
+    zeros."""
+    dims, ldx, sc = _adapters(x, a, b, ids, scale)
+    T, K, N, R, L = dims[1:]
+    if dy.dtype != torch.bfloat16:
+        raise TypeError(f"dy must be bfloat16, got {dy.dtype}")
+    rows, cols, lddy = _matrix(dy, "dy", x.device)
+    if rows != T or cols != N:
+        raise ValueError(f"dy has shape {(rows, cols)}, expected {(T, N)}")
+    addr, ldb = _base(base, (T, K), x)
+    out, lddx = _rows_out(out, (T, K), x)
+    da, db = a.new_empty(a.shape, dtype=torch.float32), b.new_empty(b.shape, dtype=torch.float32)
+    lib = _lib()
+    n = lib.qlin_lora_backward_workspace_size(*dims[1:])
+    ws, held = _own_workspace(n, x)
+    _call_on(x.device, lib.qlin_lora_mm_backward,
+             (*dims, dy.data_ptr(), lddy, x.data_ptr(), ldx, a.data_ptr(), b.data_ptr(), ids.data_ptr(), sc, addr, ldb,
+              out.data_ptr(), lddx, da.data_ptr(), db.data_ptr(), ws, n), "qlin_lora_mm_backward")
+    return out, da, db
+
+
+def token_logprobs(logits, target, top: int = 0):
+    """Log probability of one token for each row of logits [T,V] (float32, bfloat16 or
+    float16): (logprob, entropy, lse, top_logprob, top_id), float32 [T], [T], [T],
+    float32 and int32 [T, top].  target int32 or int64 [T]; outside 0..V-1 (padding)
+    logprob is 0.  lse is the log of the sum of exponentials, top_id the `top` (0..64)
+    largest logits in order, equal ones by index.  Logits of -inf are banned tokens; a
+    row of nothing else has log probabilities and lse -inf and entropy 0."""
+    rt, dev = _row_type(logits, "logits"), logits.device
+    T, V, ld = _matrix(logits, "logits", dev)
+    bits = _tokens(target, T, dev, "target")
+    top = int(top)
+    if not 0 <= top <= 64:
+        raise ValueError(f"top must be 0..64, got {top}")
+    one = logits.new_empty((3, T), dtype=torch.float32)
+    logprob, entropy, lse = one[0], one[1], one[2]
+    top_logprob = logits.new_empty((T, top), dtype=torch.float32)
+    top_id = logits.new_empty((T, top), dtype=torch.int32)
+    lib = _lib()
+    n = lib.qlin_token_logprobs_workspace_size(rt, T, V, top)
+    ws, held = _own_workspace(n, logits)
+    _call_on(dev, lib.qlin_token_logprobs,
+             (rt, bits, T, V, top, logits.data_ptr(), ld, target.data_ptr(), logprob.data_ptr(), entropy.data_ptr(),
+              lse.data_ptr(), top_logprob.data_ptr(), top_id.data_ptr(), ws, n), "qlin_token_logprobs")
+    return logprob, entropy, lse, top_logprob, top_id
+
+
+def token_logprobs_backward(dlogprob, logits, target, lse, entropy=None, dentropy=None, out=None):
+    """Gradient of token_logprobs with respect to the logits, of their type:
+    dlogprob[t] ([v = target[t]] - p_v) - dentropy[t] p_v (ln p_v + entropy[t]), from the
+    forward call's lse (and entropy, where dentropy is given); all float32 [T].  A row
+    whose gradients are both 0 gets zeros; targets outside 0..V-1 count as dlogprob 0.
+    `out` may be the logits themselves."""
+    rt, dev = _row_type(logits, "logits"), logits.device
+    T, V, ld = _matrix(logits, "logits", dev)
+    bits = _tokens(target, T, dev, "target")
+    _flat(dlogprob, torch.float32, (T,), "dlogprob", dev)
+    _flat(lse, torch.float32, (T,), "lse", dev)
+    h = e = None
+    if dentropy is not None:
+        if entropy is None:
+            raise ValueError("dentropy without entropy")
+        _flat(dentropy, torch.float32, (T,), "dentropy", dev)
+        _flat(entropy, torch.float32, (T,), "entropy", dev)
+        h, e = dentropy.data_ptr(), entropy.data_ptr()
+    out, ldo = _rows_out(out, (T, V), logits)
+    _call_on(dev, _lib().qlin_token_logprobs_backward,
+             (rt, bits, T, V, dlogprob.data_ptr(), h, logits.data_ptr(), ld, target.data_ptr(), lse.data_ptr(), e,
+              out.data_ptr(), ldo), "qlin_token_logprobs_backward")
+    return out
+
+
+_TABLE_TYPE = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2, torch.int8: 3, torch.float8_e4m3fn: 4}
+
+
+def embedding(ids, table, row_scale=None, scale: float = 1.0, dtype=None, out=None):
+    """Rows of an embedding table [V,H] by token: out[t] = scale * row_scale * table[ids[t]],
+    [T,H], zeros where ids[t] is outside 0..V-1 (padding).  ids int32 or int64 [T].  The
+    table is float32, bfloat16 or float16, or int8 or float8_e4m3fn codes; row_scale
+    float32 [V] or [V, H/128], a quantizer's (None: 1).  `dtype` (float32, bfloat16 or
+    float16) is out's: by default the table's, bfloat16 for codes."""
+    tt = _TABLE_TYPE.get(table.dtype)
+    if tt is None:
+        raise TypeError(f"table must be float32, bfloat16, float16, int8 or float8_e4m3fn, got {table.dtype}")
+    dev = table.device
+    V, H, ldt = _matrix(table, "table", dev)
+    bits = _tokens(ids, None, dev)
+    T = ids.shape[0]
+    cols, sc = 0, None
+    if row_scale is not None:
+        cols = 1 if row_scale.dim() == 1 else H // 128
+        if cols * 128 != H and row_scale.dim() != 1:
+            raise ValueError(f"row_scale must be [V], or [V, H/128] with H a multiple of 128, got "
+                             f"{tuple(row_scale.shape)} for H = {H}")
+        _flat(row_scale, torch.float32, (V,) if row_scale.dim() == 1 else (V, cols), "row_scale", dev)
+        sc = row_scale.data_ptr()
+    if out is not None:
+        dtype = out.dtype if dtype is None else dtype
+    elif dtype is None:
+        dtype = table.dtype if tt < 3 else torch.bfloat16
+    ot = _ROW_TYPE.get(dtype)
+    if ot is None:
+        raise TypeError(f"dtype must be float32, bfloat16 or float16, got {dtype}")
+    if out is None:
+        out, ldo = table.new_empty((T, H), dtype=dtype), H
+    elif out.dtype != dtype or out.shape != (T, H):
+        raise ValueError(f"out must be a {dtype} tensor of shape {(T, H)}")
+    else:
+        ldo = _matrix(out, "out", dev)[2]
+    _call_on(dev, _lib().qlin_embedding,
+             (tt, ot, bits, T, V, H, ids.data_ptr(), table.data_ptr(), ldt, sc, cols, float(scale), out.data_ptr(), ldo),
+             "qlin_embedding")
+    return out
+
+
+def embedding_backward(dout, ids, vocab: int, scale: float = 1.0, dtype=None, out=None, accumulate: bool = False):
+    """Gradient of embedding with respect to a plain table: dtable [V,H],
+    dtable[v] = scale * sum of dout[t] over the t with ids[t] = v, fp32 sums in the
+    order of t, zeros for rows of no token.  dout [T,H] float32, bfloat16 or float16;
+    `dtype` is dout's (the default) or float32.  With accumulate=True the sums are
+    added to what `out` holds, and rows of no token stay as they are."""
+    rt, dev = _row_type(dout, "dout"), dout.device
+    T, H, ldd = _matrix(dout, "dout", dev)
+    bits = _tokens(ids, T, dev)
+    vocab = int(vocab)
+    if accumulate and out is None:
+        raise ValueError("accumulate needs out")
+    if dtype is None:
+        dtype = dout.dtype if out is None else out.dtype
+    if dtype != dout.dtype and dtype != torch.float32:
+        raise TypeError(f"dtype must be dout's or float32, got {dtype}")
+    if out is None:
+        out, ldt = dout.new_empty((max(vocab, 0), H), dtype=dtype), H
+    elif out.dtype != dtype or out.shape != (vocab, H):
+        raise ValueError(f"out must be a {dtype} tensor of shape {(vocab, H)}")
+    else:
+        ldt = _matrix(out, "out", dev)[2]
+    lib = _lib()
+    n = lib.qlin_embedding_backward_workspace_size(T, vocab, H)
+    ws, held = _own_workspace(n, dout)
+    _call_on(dev, lib.qlin_embedding_backward,
+             (rt, _ROW_TYPE[dtype], bits, T, vocab, H, ids.data_ptr(), dout.data_ptr(), ldd, float(scale),
+              1 if accumulate else 0, out.data_ptr(), ldt, ws, n), "qlin_embedding_backward")
     return out
 
 

@@ -33,6 +33,9 @@ SOURCES = [
     "qlin_w4_tile_64.hip",
     "qlin_w4_tile_128.hip",
     "qlin_moe.hip",
+    "qlin_lora.hip",
+    "qlin_logprob.hip",
+    "qlin_embed.hip",
     "qlin_stream_fp8.hip",
     "qlin_stream_int8.hip",
     "qlin_stream_block.hip",

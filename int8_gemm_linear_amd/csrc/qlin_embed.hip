@@ -1,0 +1,603 @@
+// Rows of an embedding table by token, with scaling, and the table's gradient.
+//
+//   out[t] = c s[id_t, g(h)] table[id_t]             (zeros where there is no such row)
+//   dtable[v] = c sum_{t : id_t = v} dout[t]
+//
+// The gradient sorts the positions by token (a stable radix sort, so equal tokens
+// stay in order) and sums each token's run in that order: no atomics on values, and
+// results do not depend on timing.  A run that crosses the border between two
+// workgroups' shares of the sorted positions leaves a partial sum in each, which a
+// second kernel adds in order.  All of it moves bytes once; HBM bounds the long calls
+// and the launch the short ones.
+#include <algorithm>
+
+#include "qlin_dpp.h"
+#include "qlin_elem.h"
+#include "qlin_moe_scan.h"
+#include "qlinear.h"
+
+namespace qlin {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int64_t kMaxTokens = ((int64_t)1 << 30) - 1;
+constexpr int64_t kMaxVocab = ((int64_t)1 << 22) - 1;       // two digits of 11 bits, and one key for no token
+constexpr int64_t kMaxWidth = (int64_t)1 << 20;
+constexpr int64_t kMaxStride = (int64_t)1 << 31;
+
+bool aligned(const void *p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
+
+int elem_size(qlin_row_type rt)
+{
+    return rt == QLIN_ROW_F32 ? 4 : rt == QLIN_ROW_BF16 || rt == QLIN_ROW_F16 ? 2 : 0;
+}
+
+// Token `t`'s row, -1 for none.
+__device__ inline int row_of(const void *ids, int id_bits, int64_t t, int vocab)
+{
+    const int64_t id = id_bits == 64 ? static_cast<const int64_t *>(ids)[t] : static_cast<const int32_t *>(ids)[t];
+    return id >= 0 && id < vocab ? (int)id : -1;
+}
+
+// ---------------------------------------------------------------------------
+// Lookup
+// ---------------------------------------------------------------------------
+struct LookArgs {
+    const void *ids;
+    const uint8_t *table;
+    const float *scale;        // [vocab][scale_cols], or NULL
+    uint8_t *out;
+    int64_t ldt, ldo;          // bytes
+    int64_t tokens;
+    float factor;
+    int vocab, width, scale_cols, id_bits, lanes;
+};
+
+// Table elements as fp32: plain ones, int8 and e4m3 codes.
+template <typename T> struct Code : Elem<T> {};
+template <> struct Code<int8_t> {
+    static __device__ inline float get(int8_t v) { return (float)v; }
+};
+template <> struct Code<uint8_t> {             // e4m3
+    static __device__ inline float get(uint8_t v) { return __builtin_amdgcn_cvt_f32_fp8((int)v, 0); }
+};
+
+// A token belongs to `lanes` consecutive threads, each of which takes pieces of 16 bytes of the output.
+template <typename T, typename O>
+__global__ void __launch_bounds__(kThreads) k_embedding(LookArgs a)
+{
+    constexpr int E = 16 / sizeof(O);
+    const int64_t token = (int64_t)blockIdx.x * (kThreads / a.lanes) + threadIdx.x / a.lanes;
+    const int lane = threadIdx.x & (a.lanes - 1);
+    if (token >= a.tokens)
+        return;
+    const int row = row_of(a.ids, a.id_bits, token, a.vocab);
+    const T *x = reinterpret_cast<const T *>(a.table + (row < 0 ? 0 : row) * a.ldt);
+    O *out = reinterpret_cast<O *>(a.out + token * a.ldo);
+    const float *scale = a.scale ? a.scale + (int64_t)(row < 0 ? 0 : row) * a.scale_cols : nullptr;
+    for (int at = lane * E; at < a.width; at += a.lanes * E) {
+        const int n = min(E, a.width - at);
+        float v[E] = {};
+        if (row >= 0) {
+            T t[E] = {};
+            if (n == E)
+                __builtin_memcpy(t, x + at, sizeof(t));
+            else
+#pragma unroll
+                for (int i = 0; i < E; ++i)
+                    if (i < n)
+                        t[i] = x[at + i];
+            // (a piece of 8 lies within one group of 128)
+            const float s = !scale ? 1.0f : scale[a.scale_cols == 1 ? 0 : at >> 7];
+#pragma unroll
+            for (int i = 0; i < E; ++i) v[i] = Code<T>::get(t[i]) * s * a.factor;
+        }
+        if (n == E) {
+            const v4i o = value_piece<O>(v);
+            __builtin_memcpy(out + at, &o, 16);
+        } else {
+#pragma unroll
+            for (int i = 0; i < E; ++i)
+                if (i < n)
+                    out[at + i] = Elem<O>::put(v[i]);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Sort of positions by token: least significant digit first, a counting sort
+// a digit.  As pairs (key, position); the key of a position without a row is
+// the vocabulary's size, which comes last.
+// ---------------------------------------------------------------------------
+constexpr int kDigitBits = 11, kDigits = 1 << kDigitBits;
+constexpr int kSortWaves = 8, kSortThreads = 64 * kSortWaves;
+constexpr int64_t kSortOne = 4096;             // positions up to which one workgroup sorts alone
+constexpr int kSortBlock = 2048;               // positions of a workgroup otherwise, until
+constexpr int kSortMaxBlocks = 256;            // there would be more workgroups than this
+
+struct SortArgs {
+    const void *ids;           // the first digit's input, or NULL
+    const int2 *in;            // the later ones'
+    int2 *out;
+    int32_t *counts;           // [blocks][digits], or NULL for one workgroup
+    int n, per_block, vocab, id_bits;
+    int shift, digits;         // digit = (key >> shift) % digits, a power of two
+};
+
+__device__ inline int2 pair_at(const SortArgs &a, int i)
+{
+    if (!a.ids)
+        return a.in[i];
+    const int r = row_of(a.ids, a.id_bits, i, a.vocab);
+    return make_int2(r < 0 ? a.vocab : r, i);
+}
+
+// Positions per digit of each workgroup's range (integer atomics: their order does not matter).
+__global__ void __launch_bounds__(kSortThreads) k_sort_count(SortArgs a)
+{
+    __shared__ int32_t hist[kDigits];
+    for (int d = threadIdx.x; d < a.digits; d += kSortThreads) hist[d] = 0;
+    __syncthreads();
+    const int beg = (int)min((int64_t)blockIdx.x * a.per_block, (int64_t)a.n), end = min(beg + a.per_block, a.n);
+    for (int i = beg + threadIdx.x; i < end; i += kSortThreads)
+        atomicAdd(&hist[(pair_at(a, i).x >> a.shift) & (a.digits - 1)], 1);
+    __syncthreads();
+    for (int d = threadIdx.x; d < a.digits; d += kSortThreads)
+        a.counts[(int64_t)blockIdx.x * a.digits + d] = hist[d];
+}
+
+// A wave owns a contiguous part of the workgroup's range; a pair's place is the first place of its digit for
+// the wave, plus those of the wave before it, 64 at a time, plus the lower lanes with its digit.
+__global__ void __launch_bounds__(kSortThreads) k_sort_place(SortArgs a)
+{
+    __shared__ int32_t hist[kSortWaves * kDigits];
+    __shared__ int32_t total[kDigits], before[kDigits];
+    __shared__ int32_t wave_total[kSortWaves];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, mask = a.digits - 1;
+    const int part = a.per_block / kSortWaves;
+    const int beg = (int)min((int64_t)blockIdx.x * a.per_block + wave * part, (int64_t)a.n), end = min(beg + part, a.n);
+    for (int i = tid; i < kSortWaves * a.digits; i += kSortThreads) hist[i] = 0;
+    for (int i = tid; i < a.digits; i += kSortThreads) total[i] = before[i] = 0;
+    __syncthreads();
+    int32_t *mine = hist + wave * a.digits;
+    for (int i = beg + lane; i < end; i += 64) atomicAdd(&mine[(pair_at(a, i).x >> a.shift) & mask], 1);
+    if (a.counts) {
+        const int all = gridDim.x * a.digits, earlier = blockIdx.x * a.digits;
+#pragma unroll 4
+        for (int i = tid; i < all; i += kSortThreads) {
+            const int c = a.counts[i];
+            if (c) {
+                atomicAdd(&total[i & mask], c);
+                if (i < earlier)
+                    atomicAdd(&before[i & mask], c);
+            }
+        }
+    }
+    __syncthreads();
+    const int each = (a.digits + kSortThreads - 1) / kSortThreads;
+    const int d0 = min(tid * each, a.digits), d1 = min(d0 + each, a.digits);
+    int sum = 0;
+    for (int d = d0; d < d1; ++d) {
+        if (!a.counts)
+            for (int w = 0; w < kSortWaves; ++w) total[d] += hist[w * a.digits + d];
+        sum += total[d];
+    }
+    const int scan = wave_scan(sum);
+    if (lane == 63)
+        wave_total[wave] = scan;
+    __syncthreads();
+    int first = scan - sum;
+    for (int w = 0; w < wave; ++w) first += wave_total[w];
+    for (int d = d0; d < d1; ++d) {
+        int at = first + before[d];
+        for (int w = 0; w < kSortWaves; ++w) {
+            const int c = hist[w * a.digits + d];
+            hist[w * a.digits + d] = at;
+            at += c;
+        }
+        first += total[d];
+    }
+    __syncthreads();
+    const int bits = __ffs(a.digits) - 1;
+    for (int i = beg; i < end; i += 64) {
+        const bool there = i + lane < end;
+        const int2 p = there ? pair_at(a, i + lane) : make_int2(0, 0);
+        const int d = (p.x >> a.shift) & mask;
+        uint64_t same = __ballot(there);
+        same = there ? same : ~same;
+        for (int b = 0; b < bits; ++b) {
+            const uint64_t set = __ballot((d >> b) & 1);
+            same &= (d >> b) & 1 ? set : ~set;
+        }
+        const int lead = __ffsll((unsigned long long)same) - 1;
+        int at = 0;
+        if (there && lane == lead)
+            at = atomicAdd(&mine[d], __popcll(same));
+        at = __shfl(at, lead);
+        if (there)
+            a.out[at + __popcll(same & (((uint64_t)1 << lane) - 1))] = p;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Sums of the sorted positions' rows
+// ---------------------------------------------------------------------------
+constexpr int kChunk = 16;     // sorted positions of a workgroup
+
+struct SumArgs {
+    const int2 *pairs;         // sorted
+    const uint8_t *dout;
+    uint8_t *out;
+    float *part;               // [chunks][2][width]: the run that came in, the run that goes on
+    int64_t ldd, ldo;          // bytes
+    float factor;
+    int n, vocab, width, add;
+};
+
+// Zeros in `rows` rows of `width` elements, the last of them of `last`.
+template <typename O>
+__global__ void __launch_bounds__(kThreads) k_fill(uint8_t *out, int64_t ldo, int64_t rows, int width, int last)
+{
+    constexpr int E = 16 / sizeof(O);
+    for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
+        O *o = reinterpret_cast<O *>(out + row * ldo);
+        const int end = row == rows - 1 ? last : width;
+        for (int at = threadIdx.x * E; at < end; at += kThreads * E) {
+            if (at + E <= end) {
+                const v4i z{0, 0, 0, 0};
+                __builtin_memcpy(o + at, &z, 16);
+            } else {
+                for (int j = at; j < end; ++j) o[j] = Elem<O>::put(0.0f);
+            }
+        }
+    }
+}
+
+template <typename T>
+__device__ inline void load_values(float (&v)[4], const T *p, int n)
+{
+    if (n == 4) {
+        T t[4];
+        __builtin_memcpy(t, p, sizeof(t));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = Elem<T>::get(t[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = i < n ? Elem<T>::get(p[i]) : 0.0f;
+    }
+}
+
+// A token's sum to its row of the table (added to what it holds where the caller wants that).
+template <typename O>
+__device__ inline void store_row(const SumArgs &a, int row, int at, int n, const float (&sum)[4])
+{
+    O *o = reinterpret_cast<O *>(a.out + row * a.ldo) + at;
+    float v[4];
+    if (a.add)
+        load_values<O>(v, o, n);
+    O t[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) t[i] = Elem<O>::put(a.add ? fmaf(sum[i], a.factor, v[i]) : sum[i] * a.factor);
+    if (n == 4)
+        __builtin_memcpy(o, t, sizeof(t));
+    else
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < n)
+                o[i] = t[i];
+}
+
+// kChunk sorted positions and 4 kThreads columns a workgroup.
+template <typename T, typename O>
+__global__ void __launch_bounds__(kThreads) k_sum(SumArgs a)
+{
+    __shared__ int2 pair[kChunk + 2];          // with the neighbours on both sides
+    const int first = blockIdx.x * kChunk, count = min(kChunk, a.n - first);
+    if (threadIdx.x < kChunk + 2) {
+        const int i = first + (int)threadIdx.x - 1;
+        pair[threadIdx.x] = i >= 0 && i < a.n ? a.pairs[i] : make_int2(-1, 0);
+    }
+    __syncthreads();
+    const int at = (blockIdx.y * kThreads + threadIdx.x) * 4, n = min(4, a.width - at);
+    if (n <= 0)
+        return;
+    float sum[4] = {};
+    int began = 0;                             // where the run began
+    for (int j = 0; j < count; j += 4) {
+        float v[4][4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (j + u < count && pair[j + u + 1].x < a.vocab)
+                load_values<T>(v[u], reinterpret_cast<const T *>(a.dout + pair[j + u + 1].y * a.ldd) + at, n);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int p = j + u + 1, key = pair[p].x;
+            if (j + u >= count || key >= a.vocab)
+                continue;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sum[i] += v[u][i];
+            const bool ends = pair[p + 1].x != key;
+            if (!ends && j + u + 1 < count)
+                continue;
+            const bool came = began == 0 && pair[0].x == key;
+            if (ends && !came) {
+                store_row<O>(a, key, at, n, sum);
+            } else {
+                float *to = a.part + ((int64_t)blockIdx.x * 2 + (came ? 0 : 1)) * a.width + at;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (i < n)
+                        to[i] = sum[i];
+            }
+            began = j + u + 1;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sum[i] = 0.0f;
+        }
+    }
+}
+
+// The runs that cross chunks: the workgroup of the chunk where one begins adds its parts in order.
+template <typename O>
+__global__ void __launch_bounds__(kThreads) k_join(SumArgs a)
+{
+    const int last = (blockIdx.x + 1) * kChunk - 1;         // the chunk's last position
+    if (last + 1 >= a.n)
+        return;
+    const int key = a.pairs[last].x, before = blockIdx.x ? a.pairs[last - kChunk].x : -1;
+    if (key >= a.vocab || a.pairs[last + 1].x != key || before == key)
+        return;                                             // (a run that fills the chunk began in an earlier one)
+    // the chunks that begin with the token, counted 64 at a time
+    int parts = 0;
+    for (int more = 64; more == 64; parts += more) {
+        const int64_t i = last + 1 + (int64_t)(parts + (threadIdx.x & 63)) * kChunk;
+        more = __popcll(__ballot(i < a.n && a.pairs[i].x == key));
+    }
+    const int at = (blockIdx.y * kThreads + threadIdx.x) * 4, n = min(4, a.width - at);
+    if (n <= 0)
+        return;
+    float sum[4];
+    load_values<float>(sum, a.part + ((int64_t)blockIdx.x * 2 + 1) * a.width + at, n);
+    const float *p = a.part + (int64_t)(blockIdx.x + 1) * 2 * a.width + at;
+    for (int j = 0; j < parts; j += 4) {
+        float v[4][4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (j + u < parts)
+                load_values<float>(v[u], p + (int64_t)(j + u) * 2 * a.width, n);
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (j + u < parts)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) sum[i] += v[u][i];
+    }
+    store_row<O>(a, key, at, n, sum);
+}
+
+int sort_blocks(int64_t n)
+{
+    return n <= kSortOne ? 1 : (int)std::min((n + kSortBlock - 1) / kSortBlock, (int64_t)kSortMaxBlocks);
+}
+
+int64_t chunks(int64_t n) { return (n + kChunk - 1) / kChunk; }
+int64_t column_blocks(int64_t width) { return (width + 4 * kThreads - 1) / (4 * kThreads); }
+
+// A launch has fewer than 2^32 threads.
+bool sums_fit(int64_t n, int64_t width) { return chunks(n) * column_blocks(width) < (int64_t)1 << 24; }
+
+bool backward_shape(int64_t n, int64_t vocab, int64_t width)
+{
+    return n >= 0 && n <= kMaxTokens / 4 && vocab > 0 && vocab <= kMaxVocab && width > 0 && width <= kMaxWidth &&
+           sums_fit(n, width);
+}
+
+// Two buffers of pairs, the counts and the partial sums.
+struct Space {
+    size_t pairs, counts, part, bytes;
+};
+
+Space space(int64_t n, int64_t width)
+{
+    Space s;
+    s.pairs = ((size_t)n * sizeof(int2) + 15) / 16 * 16;
+    s.counts = sort_blocks(n) > 1 ? (size_t)sort_blocks(n) * kDigits * sizeof(int32_t) : 0;
+    s.part = (size_t)chunks(n) * 2 * width * sizeof(float);
+    s.bytes = 2 * s.pairs + s.counts + s.part;
+    return s;
+}
+
+// The sorted pairs lie in the returned buffer, a or b.
+hipError_t launch_sort(const void *ids, int32_t id_bits, int64_t n, int64_t vocab, int2 *a, int2 *b, int32_t *counts,
+                       hipStream_t s, int2 **sorted)
+{
+    int bits = 0;
+    while (((int64_t)1 << bits) <= vocab) ++bits;           // keys 0 .. vocab
+    const int passes = bits > kDigitBits ? 2 : 1, low = (bits + passes - 1) / passes;
+    const int blocks = sort_blocks(n);
+    int64_t per = (n + blocks - 1) / blocks;
+    per = (per + kSortThreads - 1) / kSortThreads * kSortThreads;
+    int2 *from = nullptr, *to = a;
+    for (int p = 0; p < passes; ++p) {
+        const int width = p == 0 ? low : bits - low;
+        SortArgs sa{p == 0 ? ids : nullptr, from, to, blocks > 1 ? counts : nullptr, (int)n, (int)per, (int)vocab,
+                    id_bits, p * low, 1 << width};
+        if (blocks > 1) {
+            hipLaunchKernelGGL(k_sort_count, dim3(blocks), dim3(kSortThreads), 0, s, sa);
+            const hipError_t e = hipGetLastError();
+            if (e != hipSuccess)
+                return e;
+        }
+        hipLaunchKernelGGL(k_sort_place, dim3(blocks), dim3(kSortThreads), 0, s, sa);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess)
+            return e;
+        from = to;
+        to = to == a ? b : a;
+    }
+    *sorted = from;
+    return hipSuccess;
+}
+
+template <typename T, typename O>
+hipError_t launch_sums(const SumArgs &a, hipStream_t s)
+{
+    const dim3 grid((unsigned)chunks(a.n), (unsigned)column_blocks(a.width));
+    hipLaunchKernelGGL((k_sum<T, O>), grid, dim3(kThreads), 0, s, a);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || grid.x == 1)
+        return e;
+    hipLaunchKernelGGL((k_join<O>), dim3(grid.x - 1, grid.y), dim3(kThreads), 0, s, a);
+    return hipGetLastError();
+}
+
+template <typename T>
+hipError_t launch_look(qlin_row_type ot, const LookArgs &a, dim3 grid, hipStream_t s)
+{
+    switch (ot) {
+    case QLIN_ROW_F32: hipLaunchKernelGGL((k_embedding<T, float>), grid, dim3(kThreads), 0, s, a); break;
+    case QLIN_ROW_BF16: hipLaunchKernelGGL((k_embedding<T, uint16_t>), grid, dim3(kThreads), 0, s, a); break;
+    case QLIN_ROW_F16: hipLaunchKernelGGL((k_embedding<T, __half>), grid, dim3(kThreads), 0, s, a); break;
+    }
+    return hipGetLastError();
+}
+
+int table_size(qlin_table_type tt)
+{
+    switch (tt) {
+    case QLIN_TABLE_F32: return 4;
+    case QLIN_TABLE_BF16:
+    case QLIN_TABLE_F16: return 2;
+    case QLIN_TABLE_INT8:
+    case QLIN_TABLE_E4M3: return 1;
+    }
+    return 0;
+}
+
+}  // namespace
+}  // namespace qlin
+
+using namespace qlin;
+
+extern "C" {
+
+qlin_status qlin_embedding(qlin_table_type tt, qlin_row_type ot, int32_t id_bits, int64_t tokens, int64_t vocab,
+                           int64_t width, const void *ids, const void *table, int64_t ldt, const float *row_scale,
+                           int64_t scale_cols, float scale, void *Out, int64_t ldo, void *stream)
+{
+    const int ts = table_size(tt), os = elem_size(ot);
+    if (!ts || !os || (id_bits != 32 && id_bits != 64))
+        return QLIN_ERR_BAD_ARGUMENT;
+    if (tokens < 0 || tokens > kMaxTokens || vocab <= 0 || vocab >= ((int64_t)1 << 31) || width <= 0 ||
+        width > kMaxWidth || (scale_cols != 0 && scale_cols != 1 && scale_cols * 128 != width))
+        return QLIN_ERR_BAD_SHAPE;
+    if (tokens == 0)
+        return QLIN_OK;
+    if (!ids || !table || !Out || (scale_cols > 0 && !row_scale))
+        return QLIN_ERR_NULL_POINTER;
+    if (ldt < width || ldo < width || ldt > kMaxStride || ldo > kMaxStride)
+        return QLIN_ERR_BAD_STRIDE;
+    if (!aligned(ids, id_bits / 8) || !aligned(table, ts) || !aligned(Out, os) || !aligned(row_scale, 4))
+        return QLIN_ERR_MISALIGNED;
+    LookArgs a{};
+    a.ids = ids;
+    a.table = static_cast<const uint8_t *>(table);
+    a.scale = scale_cols ? row_scale : nullptr;
+    a.out = static_cast<uint8_t *>(Out);
+    a.ldt = ldt * ts;
+    a.ldo = ldo * os;
+    a.factor = scale;
+    a.vocab = (int)vocab;
+    a.width = (int)width;
+    a.scale_cols = (int)scale_cols;
+    a.id_bits = id_bits;
+    a.lanes = 16;
+    while (a.lanes < kThreads && (int64_t)a.lanes * 16 < width * os) a.lanes *= 2;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    const int64_t per = kThreads / a.lanes, most = ((int64_t)1 << 23) * per;      // 2^31 threads a launch
+    hipError_t e = hipSuccess;
+    for (int64_t left = tokens; left > 0 && e == hipSuccess; left -= a.tokens) {
+        a.tokens = std::min(left, most);
+        const dim3 grid((unsigned)((a.tokens + per - 1) / per));
+        switch (tt) {
+        case QLIN_TABLE_F32: e = launch_look<float>(ot, a, grid, s); break;
+        case QLIN_TABLE_BF16: e = launch_look<uint16_t>(ot, a, grid, s); break;
+        case QLIN_TABLE_F16: e = launch_look<__half>(ot, a, grid, s); break;
+        case QLIN_TABLE_INT8: e = launch_look<int8_t>(ot, a, grid, s); break;
+        case QLIN_TABLE_E4M3: e = launch_look<uint8_t>(ot, a, grid, s); break;
+        }
+        a.ids = static_cast<const uint8_t *>(a.ids) + a.tokens * (id_bits / 8);
+        a.out += a.tokens * a.ldo;
+    }
+    return e == hipSuccess ? QLIN_OK : QLIN_ERR_HIP;
+}
+
+size_t qlin_embedding_backward_workspace_size(int64_t tokens, int64_t vocab, int64_t width)
+{
+    return tokens > 0 && backward_shape(tokens, vocab, width) ? space(tokens, width).bytes : 0;
+}
+
+qlin_status qlin_embedding_backward(qlin_row_type rt, qlin_row_type ot, int32_t id_bits, int64_t tokens,
+                                    int64_t vocab, int64_t width, const void *ids, const void *dOut, int64_t ldd,
+                                    float scale, int32_t accumulate, void *dTable, int64_t ldt, void *workspace,
+                                    size_t workspace_bytes, void *stream)
+{
+    const int es = elem_size(rt), os = elem_size(ot);
+    if (!es || !os || (ot != rt && ot != QLIN_ROW_F32) || (id_bits != 32 && id_bits != 64))
+        return QLIN_ERR_BAD_ARGUMENT;
+    if (!backward_shape(tokens, vocab, width))
+        return QLIN_ERR_BAD_SHAPE;
+    if (!dTable || (tokens > 0 && (!ids || !dOut)))
+        return QLIN_ERR_NULL_POINTER;
+    if (ldt < width || ldt > kMaxStride || (tokens > 0 && (ldd < width || ldd > kMaxStride)))
+        return QLIN_ERR_BAD_STRIDE;
+    if (!aligned(dTable, os) || !aligned(ids, id_bits / 8) || !aligned(dOut, es) || !aligned(workspace, 16))
+        return QLIN_ERR_MISALIGNED;
+    const size_t need = qlin_embedding_backward_workspace_size(tokens, vocab, width);
+    if (need && (!workspace || workspace_bytes < need))
+        return QLIN_ERR_WORKSPACE;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (!accumulate) {
+        // (rows without gaps are one long row)
+        const bool whole = ldt == width;
+        const int64_t all = vocab * width, row = whole ? 16384 : width, rows = (all + row - 1) / row;
+        const int last = (int)(whole ? all - (rows - 1) * row : width);
+        const dim3 grid((unsigned)std::min<int64_t>(rows, 1 << 20));
+        uint8_t *out = static_cast<uint8_t *>(dTable);
+        const int64_t apart = (whole ? row : ldt) * os;
+        if (os == 4)
+            hipLaunchKernelGGL((k_fill<float>), grid, dim3(kThreads), 0, s, out, apart, rows, (int)row, last);
+        else
+            hipLaunchKernelGGL((k_fill<uint16_t>), grid, dim3(kThreads), 0, s, out, apart, rows, (int)row, last);
+        if (hipGetLastError() != hipSuccess)
+            return QLIN_ERR_HIP;
+    }
+    if (tokens == 0)
+        return QLIN_OK;
+    const Space sp = space(tokens, width);
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    SumArgs a{};
+    int2 *sorted = nullptr;
+    if (launch_sort(ids, id_bits, tokens, vocab, reinterpret_cast<int2 *>(ws), reinterpret_cast<int2 *>(ws + sp.pairs),
+                    reinterpret_cast<int32_t *>(ws + 2 * sp.pairs), s, &sorted) != hipSuccess)
+        return QLIN_ERR_HIP;
+    a.pairs = sorted;
+    a.dout = static_cast<const uint8_t *>(dOut);
+    a.out = static_cast<uint8_t *>(dTable);
+    a.part = reinterpret_cast<float *>(ws + 2 * sp.pairs + sp.counts);
+    a.ldd = ldd * es;
+    a.ldo = ldt * os;
+    a.factor = scale;
+    a.n = (int)tokens;
+    a.vocab = (int)vocab;
+    a.width = (int)width;
+    a.add = accumulate != 0;
+    hipError_t e;
+    if (ot == QLIN_ROW_F32)
+        e = rt == QLIN_ROW_F32 ? launch_sums<float, float>(a, s)
+            : rt == QLIN_ROW_BF16 ? launch_sums<uint16_t, float>(a, s)
+                                  : launch_sums<__half, float>(a, s);
+    else
+        e = rt == QLIN_ROW_BF16 ? launch_sums<uint16_t, uint16_t>(a, s) : launch_sums<__half, __half>(a, s);
+    return e == hipSuccess ? QLIN_OK : QLIN_ERR_HIP;
+}
+
+}  // extern "C"

@@ -1,0 +1,523 @@
+// Log probabilities of given tokens, with the entropy of each row, its best
+// alternatives, and the gradient of both with respect to the logits.
+//
+// For a row x of V logits, m = max x, S = sum e^(x - m), W = sum e^(x - m) (x - m):
+//   lse = m + ln S,   log p_v = (x_v - m) - ln S,   H = ln S - W / S,
+//   dx_v = g ([v = target] - p_v) - h p_v (log p_v + H)
+// with g and h the gradients of the target's log p and of H.  One pass over the
+// logits keeps m, S, W and the best alternatives; a lane rescales its own S and W
+// when its maximum rises: from m to n, W becomes (W + S (m - n)) e^(m - n).
+//
+// x - m is taken before the product with log2 e, so that rows far from zero lose
+// nothing, and below -200 it counts as -200 where it is multiplied with e^(x - m),
+// which is 0 there: banned tokens (-inf, or a type's lowest value) add 0.
+#include <algorithm>
+#include <float.h>
+
+#include "qlin_dpp.h"
+#include "qlin_elem.h"
+#include "qlinear.h"
+
+namespace qlin {
+namespace {
+
+constexpr int kThreads = 256, kWaves = kThreads / 64;
+constexpr int kPieces = 4;                     // 16-byte pieces a thread takes at a time
+constexpr int kMaxTop = 64;                    // an alternative for each lane of a wave
+constexpr int kMaxParts = 64;                  // a part for each lane of the joining wave
+constexpr int64_t kMaxRows = (int64_t)1 << 23; // x parts: below 2^32 threads
+constexpr int64_t kMaxVocab = (int64_t)1 << 28;
+constexpr int64_t kMaxStride = (int64_t)1 << 31;
+constexpr float kLowest = -200.0f, kLog2e = 1.4426950408889634f;
+
+bool aligned(const void *p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
+
+__device__ inline float exp_of(float d) { return __builtin_amdgcn_exp2f(d * kLog2e); }
+
+// m, S and W of a part of a row (or of a lane's share of it).
+struct Stat {
+    float m, s, w;
+};
+
+__device__ inline void rescale(Stat &a, float m)
+{
+    const float r = fmaxf(a.m - m, kLowest), f = exp_of(r);
+    a.w = (a.w + a.s * r) * f;
+    a.s *= f;
+    a.m = m;
+}
+
+// An alternative as one number that orders by value, then by the lower index;
+// 0 is none, and so are NaNs.
+__device__ inline uint64_t key_of(float v, int at)
+{
+    const int b = __float_as_int(v + 0.0f);                  // -0 and +0 are equal
+    const uint32_t o = b < 0 ? ~(uint32_t)b : (uint32_t)b | 0x80000000u;
+    return v == v ? (uint64_t)o << 32 | (0xFFFFFFFFu - (uint32_t)at) : 0;
+}
+
+__device__ inline float key_value(uint64_t k)
+{
+    const uint32_t o = (uint32_t)(k >> 32);
+    return k == 0 ? __int_as_float(0x7FC00000) : __uint_as_float(o & 0x80000000u ? o & 0x7FFFFFFFu : ~o);
+}
+
+__device__ inline int key_index(uint64_t k) { return k == 0 ? -1 : (int)(0xFFFFFFFFu - (uint32_t)k); }
+
+__device__ inline uint64_t key_lane(uint64_t k, int lane)
+{
+    return (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(k >> 32), lane) << 32 |
+           (uint32_t)__builtin_amdgcn_readlane((int)k, lane);
+}
+
+__device__ inline uint64_t wave_max_key(uint64_t k)
+{
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+        const uint64_t o = (uint64_t)(uint32_t)dpp_partner((int)(k >> 32), s) << 32 | (uint32_t)dpp_partner((int)k, s);
+        k = o > k ? o : k;
+    }
+    const uint64_t a = key_lane(k, 0), b = key_lane(k, 16), c = key_lane(k, 32), d = key_lane(k, 48);
+    const uint64_t e = a > b ? a : b, f = c > d ? c : d;
+    return e > f ? e : f;
+}
+
+// A wave's best `top` keys so far, in order, one a lane.
+struct Best {
+    uint64_t mine = 0, last = 0;               // this lane's; that of lane top - 1
+    float bar = -INFINITY;                     // last's value: a greater one enters
+
+    // A key above `last` (the same in all lanes) goes to its place, the lower ones one lane on.
+    __device__ void insert(uint64_t k, int lane, int top)
+    {
+        const int at = __popcll(__ballot(mine > k));
+        const uint64_t up = (uint64_t)(uint32_t)__builtin_amdgcn_update_dpp(0, (int)(mine >> 32), 0x138, 0xF, 0xF, false) << 32 |
+                            (uint32_t)__builtin_amdgcn_update_dpp(0, (int)mine, 0x138, 0xF, 0xF, false);   // wave_shr:1
+        mine = lane < at ? mine : lane == at ? k : up;
+        last = key_lane(mine, top - 1);
+    }
+};
+
+struct Args {
+    const uint8_t *x;
+    int64_t ld, ldo;                           // bytes
+    const void *target;
+    float *logprob, *entropy, *lse, *top_v;
+    int32_t *top_id;
+    float *stat;                               // [rows][parts][4]: m, S, W, unused
+    uint64_t *list;                            // [rows][parts][top]
+    const float *g, *h, *lse_in, *entropy_in;  // gradient
+    uint8_t *out;
+    int V, top, parts, per, id_bits;
+};
+
+__device__ inline int target_of(const Args &a, int64_t row)
+{
+    const int64_t t = a.id_bits == 64 ? static_cast<const int64_t *>(a.target)[row] : static_cast<const int32_t *>(a.target)[row];
+    return t >= 0 && t < a.V ? (int)t : -1;
+}
+
+// The row's outputs from its statistics; the keys are in `best`.  A row that
+// holds no number above -inf has no distribution: log probabilities -inf, H = 0.
+template <typename T>
+__device__ inline void finish(const Args &a, int64_t row, Stat s, const uint64_t *best, int tid)
+{
+    const float ln = logf(s.s);
+    const bool none = s.s == 0.0f;
+    if (tid == 0) {
+        const int t = target_of(a, row);
+        float l = 0.0f;
+        if (t >= 0)
+            l = none ? -INFINITY : (Elem<T>::get(reinterpret_cast<const T *>(a.x + row * a.ld)[t]) - s.m) - ln;
+        a.logprob[row] = l;
+        a.entropy[row] = none ? 0.0f : ln - s.w / s.s;
+        a.lse[row] = none ? -INFINITY : s.m + ln;
+    }
+    if (tid < a.top) {
+        const uint64_t k = best[tid];
+        a.top_v[row * a.top + tid] = k == 0 ? key_value(k) : none ? -INFINITY : (key_value(k) - s.m) - ln;
+        a.top_id[row * a.top + tid] = key_index(k);
+    }
+}
+
+// The pieces of chunk c, values behind `end` as -inf.
+template <typename T>
+__device__ inline void load_chunk(v4i (&p)[kPieces], const T *x, int c, int end, int tid)
+{
+    constexpr int E = 16 / sizeof(T);
+    if (c + kThreads * E * kPieces <= end) {
+#pragma unroll
+        for (int u = 0; u < kPieces; ++u) p[u] = load_piece(x + c + (u * kThreads + tid) * E);
+        return;
+    }
+#pragma unroll
+    for (int u = 0; u < kPieces; ++u) {
+        const int at = c + (u * kThreads + tid) * E;
+        if (at + E <= end) {
+            p[u] = load_piece(x + at);
+        } else {
+            T t[E];
+#pragma unroll
+            for (int i = 0; i < E; ++i) t[i] = at + i < end ? x[at + i] : Elem<T>::put(-INFINITY);
+            __builtin_memcpy(&p[u], t, 16);
+        }
+    }
+}
+
+// A part of a row for each workgroup.
+template <typename T, bool TOP>
+__global__ void __launch_bounds__(kThreads) k_logprobs(Args a)
+{
+    constexpr int E = 16 / sizeof(T), kStep = kThreads * E * kPieces;
+    __shared__ uint64_t keys[TOP ? kWaves : 1][kMaxTop], merged[kMaxTop];
+    __shared__ Stat stats[kWaves];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int64_t row = blockIdx.x / a.parts;
+    const int part = blockIdx.x % a.parts, beg = part * a.per, end = min(beg + a.per, a.V);
+    const T *x = reinterpret_cast<const T *>(a.x + row * a.ld);
+    Stat s{-FLT_MAX, 0.0f, 0.0f};
+    Best best;
+    v4i next[kPieces];
+    load_chunk(next, x, beg, end, tid);
+    for (int c = beg; c < end; c += kStep) {
+        float v[kPieces][E], high[kPieces], most = -INFINITY;
+#pragma unroll
+        for (int u = 0; u < kPieces; ++u) {
+            piece_values<T>(v[u], next[u]);
+            high[u] = v[u][0];
+#pragma unroll
+            for (int i = 1; i < E; ++i) high[u] = fmaxf(high[u], v[u][i]);
+            most = fmaxf(most, high[u]);
+        }
+        if (c + kStep < end)
+            load_chunk(next, x, c + kStep, end, tid);
+        if (most > s.m)
+            rescale(s, most);
+#pragma unroll
+        for (int u = 0; u < kPieces; ++u)
+#pragma unroll
+            for (int i = 0; i < E; ++i) {
+                const float d = v[u][i] - s.m, e = exp_of(d);
+                s.s += e;
+                s.w = fmaf(e, fmaxf(d, kLowest), s.w);
+            }
+        if (TOP) {
+            // Of the first chunk, the top-th best of the lanes' maxima bounds what can enter; later, a value
+            // has to be greater than the last of the list, whose index is lower.
+            float bar = best.bar;
+            bool open = best.last == 0;
+            if (c == beg) {
+                int rank = 0;
+                for (int l = 0; l < 64; ++l) {
+                    const float o = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(most), l));
+                    rank += o > most || (o == most && l < lane) ? 1 : 0;
+                }
+                const uint64_t at = __ballot(rank == a.top - 1);
+                bar = at ? __int_as_float(__builtin_amdgcn_readlane(__float_as_int(most), __ffsll((unsigned long long)at) - 1))
+                         : -INFINITY;
+            }
+#pragma unroll
+            for (int u = 0; u < kPieces; ++u) {
+                if (!__ballot(high[u] > bar || (open && high[u] >= bar)))
+                    continue;
+                const int at = c + (u * kThreads + tid) * E;
+#pragma unroll
+                for (int i = 0; i < E; ++i) {
+                    const uint64_t k = at + i < end && v[u][i] >= bar ? key_of(v[u][i], at + i) : 0;
+                    uint64_t in = __ballot(k > best.last);
+                    while (in) {
+                        const uint64_t one = key_lane(k, __ffsll((unsigned long long)in) - 1);
+                        best.insert(one, lane, a.top);
+                        in &= in - 1;
+                        in &= __ballot(k > best.last);
+                    }
+                }
+            }
+            best.bar = best.last ? key_value(best.last) : -INFINITY;
+        }
+    }
+    // one statistic a wave, then one for all
+    const float m = wave_max(s.m);
+    rescale(s, m);
+    s.s = wave_sum(s.s);
+    s.w = wave_sum(s.w);
+    if (lane == 0)
+        stats[wave] = s;
+    if (TOP && lane < a.top) {
+        keys[wave][lane] = best.mine;
+        if (wave == 0)
+            merged[lane] = 0;
+    }
+    __syncthreads();
+    s = stats[0];
+    for (int w = 1; w < kWaves; ++w) s.m = fmaxf(s.m, stats[w].m);
+    {
+        Stat t = stats[0];
+        rescale(t, s.m);
+        s.s = t.s;
+        s.w = t.w;
+        for (int w = 1; w < kWaves; ++w) {
+            t = stats[w];
+            rescale(t, s.m);
+            s.s += t.s;
+            s.w += t.w;
+        }
+    }
+    if (TOP) {
+        if (tid < kWaves * a.top) {
+            const uint64_t k = keys[tid / a.top][tid % a.top];
+            int rank = 0;
+            for (int w = 0; w < kWaves; ++w)
+                for (int j = 0; j < a.top; ++j) rank += keys[w][j] > k ? 1 : 0;
+            if (k && rank < a.top)
+                merged[rank] = k;
+        }
+        __syncthreads();
+    }
+    if (a.parts == 1) {
+        finish<T>(a, row, s, merged, tid);
+        return;
+    }
+    const int64_t p = row * a.parts + part;
+    if (tid == 0) {
+        a.stat[4 * p] = s.m;
+        a.stat[4 * p + 1] = s.s;
+        a.stat[4 * p + 2] = s.w;
+    }
+    if (TOP && tid < a.top)
+        a.list[p * a.top + tid] = merged[tid];
+}
+
+// The parts of a row, one a lane; the alternatives are the best of the parts' heads, one after another.
+template <typename T>
+__global__ void __launch_bounds__(64) k_logprobs_join(Args a)
+{
+    __shared__ uint64_t merged[kMaxTop];
+    const int lane = threadIdx.x;
+    const int64_t row = blockIdx.x, p = row * a.parts + lane;
+    Stat s{-FLT_MAX, 0.0f, 0.0f};
+    if (lane < a.parts)
+        s = Stat{a.stat[4 * p], a.stat[4 * p + 1], a.stat[4 * p + 2]};
+    rescale(s, wave_max(s.m));
+    s.s = wave_sum(s.s);
+    s.w = wave_sum(s.w);
+    const uint64_t *list = a.list + p * a.top;
+    uint64_t head = lane < a.parts && a.top ? list[0] : 0;
+    int at = 0;
+    for (int j = 0; j < a.top; ++j) {
+        const uint64_t k = wave_max_key(head);
+        if (lane == 0)
+            merged[j] = k;
+        if (k && head == k)
+            head = ++at < a.top ? list[at] : 0;
+    }
+    __syncthreads();
+    finish<T>(a, row, s, merged, lane);
+}
+
+// The logits' gradient: a part of a row for each workgroup, read and written once.
+// A row with g = h = 0 (padding) gets zeros and is not read, one without a distribution zeros.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) k_logprobs_backward(Args a)
+{
+    constexpr int E = 16 / sizeof(T), kStep = kThreads * E * kPieces;
+    const int tid = threadIdx.x;
+    const int64_t row = blockIdx.x / a.parts;
+    const int part = blockIdx.x % a.parts, beg = part * a.per, end = min(beg + a.per, a.V);
+    const T *x = reinterpret_cast<const T *>(a.x + row * a.ld);
+    T *out = reinterpret_cast<T *>(a.out + row * a.ldo);
+    const int target = target_of(a, row);
+    const float lse = a.lse_in[row], g = target >= 0 ? a.g[row] : 0.0f, h = a.h ? a.h[row] : 0.0f,
+                entropy = a.h ? a.entropy_in[row] : 0.0f;
+    const bool zero = (g == 0.0f && h == 0.0f) || lse == -INFINITY;
+    for (int c = beg; c < end; c += kStep) {
+        v4i p[kPieces];
+        if (!zero)
+            load_chunk(p, x, c, end, tid);
+#pragma unroll
+        for (int u = 0; u < kPieces; ++u) {
+            const int at = c + (u * kThreads + tid) * E;
+            float v[E] = {};
+            if (!zero) {
+                piece_values<T>(v, p[u]);
+#pragma unroll
+                for (int i = 0; i < E; ++i) {
+                    const float z = v[i] - lse;
+                    v[i] = -exp_of(z) * fmaf(h, fmaxf(z, kLowest) + entropy, g);
+                    if (at + i == target)
+                        v[i] += g;
+                }
+            }
+            if (at + E <= end) {
+                const v4i o = value_piece<T>(v);
+                __builtin_memcpy(out + at, &o, 16);
+            } else {
+#pragma unroll
+                for (int i = 0; i < E; ++i)
+                    if (at + i < end)
+                        out[at + i] = Elem<T>::put(v[i]);
+            }
+        }
+    }
+}
+
+int elem_size(qlin_row_type rt)
+{
+    return rt == QLIN_ROW_F32 ? 4 : rt == QLIN_ROW_BF16 || rt == QLIN_ROW_F16 ? 2 : 0;
+}
+
+// Parts of a row: enough workgroups for the GPU where there are few rows, each of a chunk at least.
+int row_parts(int es, int64_t rows, int64_t V)
+{
+    const int64_t chunk = 16 / es * kThreads, most = std::min<int64_t>((V + chunk - 1) / chunk, kMaxParts);
+    return (int)std::max<int64_t>(1, std::min(most, 1024 / std::max<int64_t>(rows, 1)));
+}
+
+// Elements of each part, whole 16-byte pieces, and the parts that then have any.
+void divide(Args &a, int es, int parts)
+{
+    const int E = 16 / es, pieces = (a.V + E - 1) / E;
+    const int per = (pieces + parts - 1) / parts;
+    a.per = per * E;
+    a.parts = (pieces + per - 1) / per;
+}
+
+qlin_status check(qlin_row_type rt, int32_t id_bits, int64_t rows, int64_t V, const void *x, int64_t ld,
+                  const void *target)
+{
+    const int es = elem_size(rt);
+    if (!es || (id_bits != 32 && id_bits != 64))
+        return QLIN_ERR_BAD_ARGUMENT;
+    if (rows < 0 || rows > kMaxRows || V <= 0 || V > kMaxVocab)
+        return QLIN_ERR_BAD_SHAPE;
+    if (rows == 0)
+        return QLIN_OK;
+    if (!x || !target)
+        return QLIN_ERR_NULL_POINTER;
+    if (ld < V || ld > kMaxStride)
+        return QLIN_ERR_BAD_STRIDE;
+    if (!aligned(x, es) || !aligned(target, id_bits / 8))
+        return QLIN_ERR_MISALIGNED;
+    return QLIN_OK;
+}
+
+template <typename T>
+hipError_t launch_forward(const Args &a, int64_t rows, hipStream_t s)
+{
+    const dim3 grid((unsigned)(rows * a.parts));
+    if (a.top)
+        hipLaunchKernelGGL((k_logprobs<T, true>), grid, dim3(kThreads), 0, s, a);
+    else
+        hipLaunchKernelGGL((k_logprobs<T, false>), grid, dim3(kThreads), 0, s, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || a.parts == 1)
+        return e;
+    hipLaunchKernelGGL((k_logprobs_join<T>), dim3((unsigned)rows), dim3(64), 0, s, a);
+    return hipGetLastError();
+}
+
+template <typename T>
+hipError_t launch_backward(const Args &a, int64_t rows, hipStream_t s)
+{
+    hipLaunchKernelGGL((k_logprobs_backward<T>), dim3((unsigned)(rows * a.parts)), dim3(kThreads), 0, s, a);
+    return hipGetLastError();
+}
+
+}  // namespace
+}  // namespace qlin
+
+using namespace qlin;
+
+extern "C" {
+
+size_t qlin_token_logprobs_workspace_size(qlin_row_type rt, int64_t rows, int64_t V, int64_t top)
+{
+    const int es = elem_size(rt);
+    if (!es || rows <= 0 || rows > kMaxRows || V <= 0 || V > kMaxVocab || top < 0 || top > kMaxTop)
+        return 0;
+    const int parts = row_parts(es, rows, V);
+    return parts > 1 ? (size_t)rows * parts * (16 + 8 * top) : 0;
+}
+
+qlin_status qlin_token_logprobs(qlin_row_type rt, int32_t id_bits, int64_t rows, int64_t V, int64_t top,
+                                const void *logits, int64_t ld, const void *target, float *logprob,
+                                float *entropy, float *lse, float *top_logprob, int32_t *top_id,
+                                void *workspace, size_t workspace_bytes, void *stream)
+{
+    const qlin_status st = check(rt, id_bits, rows, V, logits, ld, target);
+    if (st != QLIN_OK)
+        return st;
+    if (top < 0 || top > kMaxTop || top > V)
+        return QLIN_ERR_BAD_SHAPE;
+    if (rows == 0)
+        return QLIN_OK;
+    if (!logprob || !entropy || !lse || (top > 0 && (!top_logprob || !top_id)))
+        return QLIN_ERR_NULL_POINTER;
+    if (!aligned(logprob, 4) || !aligned(entropy, 4) || !aligned(lse, 4) || !aligned(top_logprob, 4) ||
+        !aligned(top_id, 4) || !aligned(workspace, 8))
+        return QLIN_ERR_MISALIGNED;
+    const size_t need = qlin_token_logprobs_workspace_size(rt, rows, V, top);
+    if (need && (!workspace || workspace_bytes < need))
+        return QLIN_ERR_WORKSPACE;
+    const int es = elem_size(rt);
+    Args a{};
+    a.x = static_cast<const uint8_t *>(logits);
+    a.ld = ld * es;
+    a.target = target;
+    a.logprob = logprob;
+    a.entropy = entropy;
+    a.lse = lse;
+    a.top_v = top_logprob;
+    a.top_id = top_id;
+    a.V = (int)V;
+    a.top = (int)top;
+    a.id_bits = id_bits;
+    divide(a, es, row_parts(es, rows, V));
+    a.list = static_cast<uint64_t *>(workspace);
+    a.stat = reinterpret_cast<float *>(a.list + (size_t)rows * a.parts * top);
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    const hipError_t e = rt == QLIN_ROW_F32 ? launch_forward<float>(a, rows, s)
+                         : rt == QLIN_ROW_BF16 ? launch_forward<uint16_t>(a, rows, s)
+                                               : launch_forward<__half>(a, rows, s);
+    return e == hipSuccess ? QLIN_OK : QLIN_ERR_HIP;
+}
+
+qlin_status qlin_token_logprobs_backward(qlin_row_type rt, int32_t id_bits, int64_t rows, int64_t V,
+                                         const float *dlogprob, const float *dentropy, const void *logits,
+                                         int64_t ld, const void *target, const float *lse,
+                                         const float *entropy, void *dlogits, int64_t ldo, void *stream)
+{
+    const qlin_status st = check(rt, id_bits, rows, V, logits, ld, target);
+    if (st != QLIN_OK || rows == 0)
+        return st;
+    if (!dlogprob || !lse || !dlogits || (dentropy && !entropy))
+        return QLIN_ERR_NULL_POINTER;
+    if (ldo < V || ldo > kMaxStride)
+        return QLIN_ERR_BAD_STRIDE;
+    const int es = elem_size(rt);
+    if (!aligned(dlogits, es) || !aligned(dlogprob, 4) || !aligned(dentropy, 4) || !aligned(lse, 4) ||
+        !aligned(entropy, 4))
+        return QLIN_ERR_MISALIGNED;
+    Args a{};
+    a.x = static_cast<const uint8_t *>(logits);
+    a.out = static_cast<uint8_t *>(dlogits);
+    a.ld = ld * es;
+    a.ldo = ldo * es;
+    a.target = target;
+    a.g = dlogprob;
+    a.h = dentropy;
+    a.lse_in = lse;
+    a.entropy_in = entropy;
+    a.V = (int)V;
+    a.id_bits = id_bits;
+    // a chunk for each workgroup, as far as the rows leave a launch room for them
+    const int64_t chunk = 16 / es * kThreads * kPieces, most = (((int64_t)1 << 24) - 1) / rows;
+    divide(a, es, (int)std::max<int64_t>(1, std::min((V + chunk - 1) / chunk, most)));
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    const hipError_t e = rt == QLIN_ROW_F32 ? launch_backward<float>(a, rows, s)
+                         : rt == QLIN_ROW_BF16 ? launch_backward<uint16_t>(a, rows, s)
+                                               : launch_backward<__half>(a, rows, s);
+    return e == hipSuccess ? QLIN_OK : QLIN_ERR_HIP;
+}
+
+}  // extern "C"

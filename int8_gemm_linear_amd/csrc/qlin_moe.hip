@@ -10,7 +10,6 @@
 // is addressed by row[i]: permute scatters token rows to row[i], combine and
 // the gradients gather from it.  All of it moves bytes once; HBM bounds the
 // long calls and the launch the short ones.
-#include <hip/hip_fp16.h>
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -18,6 +17,7 @@
 
 #include "qlin_device.h"
 #include "qlin_dpp.h"
+#include "qlin_elem.h"
 #include "qlin_moe_scan.h"
 #include "qlinear.h"
 
@@ -408,20 +408,6 @@ __global__ void __launch_bounds__(kRowThreads) k_moe_dispatch(SortArgs s, RowArg
     if (token < a.tokens)
         copy_token(a, token, row + tid / a.lanes * a.topk, tid & (a.lanes - 1));
 }
-
-template <typename T> struct Elem;
-template <> struct Elem<float> {
-    static __device__ inline float get(float v) { return v; }
-    static __device__ inline float put(float v) { return v; }
-};
-template <> struct Elem<__half> {
-    static __device__ inline float get(__half v) { return __half2float(v); }
-    static __device__ inline __half put(float v) { return __float2half(v); }
-};
-template <> struct Elem<uint16_t> {                // bf16 bits
-    static __device__ inline float get(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
-    static __device__ inline uint16_t put(float v) { return bf16_bits(v); }
-};
 
 // Choices whose rows a thread loads together.
 constexpr int kChoices = 4;
