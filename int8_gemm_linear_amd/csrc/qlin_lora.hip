@@ -25,7 +25,6 @@ namespace {
 
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 
-constexpr int kThreads = 256, kWaves = kThreads / 64;
 constexpr int kMaxAdapters = 2048;
 constexpr int kMaxRank = 128;
 constexpr int64_t kMaxTokens = (int64_t)1 << 24;
@@ -71,15 +70,15 @@ __device__ inline int pack2(float lo, float hi)
 // ---------------------------------------------------------------------------
 // Plan: tokens by adapter, and the tiles of each.
 // ---------------------------------------------------------------------------
-constexpr int kPlanWaves = 16, kPlanThreads = 64 * kPlanWaves;
 constexpr int kBins = kMaxAdapters + 1;        // the last one in use: tokens without an adapter
 
 struct Plan {
     const void *ids;
     int32_t *order;            // [tokens]: the tokens by (adapter, token); those without one come last
-    int32_t *offsets;          // [adapters + 1]: the first place of each adapter
-    int4 *tiles;               // [max_tiles]: adapter (-1: none), first place, tokens (0: no tile)
-    int tokens, adapters, tile, max_tiles, id_bits;
+    int32_t *offsets;          // [adapters + 1]: the first place of each adapter (NULL: not wanted)
+    int4 *tiles;               // [max_tiles]: adapter (-1: none), first place, tokens (0: no tile), and the
+                               // tokens of the expand tile that begins here (0: none does)
+    int tokens, adapters, tile, wide, max_tiles, id_bits;
 };
 
 __device__ inline int bin_of(const Plan &p, int t)
@@ -88,7 +87,17 @@ __device__ inline int bin_of(const Plan &p, int t)
     return id >= 0 && id < p.adapters ? (int)id : p.adapters;
 }
 
-// One workgroup: a stable counting sort whose waves own contiguous parts of the tokens.
+// Tile j of an adapter with n tokens from place `first`.
+__device__ inline int4 tile_of(const Plan &p, int bin, int first, int n, int j)
+{
+    const int at = j * p.tile;
+    return make_int4(bin < p.adapters ? bin : -1, first + at, min(p.tile, n - at),
+                     at % p.wide == 0 ? min(p.wide, n - at) : 0);
+}
+
+// Many tokens: one workgroup sorts them (stably: its waves own contiguous parts) and writes all tiles.
+constexpr int kPlanWaves = 16, kPlanThreads = 64 * kPlanWaves;
+
 __global__ void __launch_bounds__(kPlanThreads) k_plan(Plan p)
 {
     __shared__ int32_t hist[kPlanWaves][kBins];
@@ -130,9 +139,9 @@ __global__ void __launch_bounds__(kPlanThreads) k_plan(Plan p)
             hist[w][b] = at;
             at += c;
         }
-        p.offsets[b] = first;                  // (that of the last bin: tokens with an adapter)
-        for (int t = first; t < at; t += p.tile)
-            p.tiles[tile++] = make_int4(b < p.adapters ? b : -1, t, min(p.tile, at - t), 0);
+        if (p.offsets)
+            p.offsets[b] = first;              // (that of the last bin: tokens with an adapter)
+        for (int j = 0; j * p.tile < at - first; ++j) p.tiles[tile++] = tile_of(p, b, first, at - first, j);
     }
     for (int t = all + tid; t < p.max_tiles; t += kPlanThreads) p.tiles[t] = make_int4(-1, 0, 0, 0);
     __syncthreads();
@@ -157,347 +166,524 @@ __global__ void __launch_bounds__(kPlanThreads) k_plan(Plan p)
     }
 }
 
-// ---------------------------------------------------------------------------
-// Shrink: part[split][place][r] = sum over the split's k of x[token,k] w[adapter,r,k].
-// Sixteen ranks by sixteen tokens a matrix product; waves share K in steps of 128.
-// ---------------------------------------------------------------------------
-constexpr int kStep = 128;
+// Few tokens: every workgroup of the shrink kernel finds its own tile, which takes it less time than a launch
+// of its own would take the call.  A wave owns a contiguous part of the tokens and keeps their bins.
+constexpr int kShrinkWaves = 8, kShrinkThreads = 64 * kShrinkWaves, kHold = 16;
+constexpr int kSelfTokens = kShrinkThreads * kHold;
 
-struct ShrinkArgs {
-    const uint16_t *x, *w;     // w [adapters][R][ldw]
-    const int32_t *order;
-    const int4 *tiles;
-    float *part;               // [splits][tokens][16 RB]
-    int64_t ldx, ldw;
-    int tokens, K, R, splits;
+struct PlanShare {
+    int32_t sums[2][kShrinkWaves];
+    int4 tile;
+    int32_t bin, skip;                         // the tile's bin and its tokens before the tile
+    int32_t token[64];
 };
 
-template <int TB, int RB>
-__global__ void __launch_bounds__(kThreads) k_shrink(ShrinkArgs a)
+// The tile `want`, its tokens in sh.token; `hist` [adapters + 1].  Called by all threads.
+__device__ inline int4 self_plan(const Plan &p, int want, int32_t *hist, PlanShare &sh)
 {
-    __shared__ v4f sums[kWaves - 1][TB * RB][64];
-    const int4 tile = a.tiles[blockIdx.x / a.splits];
-    const int split = blockIdx.x % a.splits;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, bins = p.adapters + 1;
+    const int turns = (p.tokens + kShrinkThreads - 1) / kShrinkThreads, beg = wave * turns * 64 + lane;
+    int held[kHold];
+#pragma unroll
+    for (int h = 0; h < kHold; ++h) held[h] = h < turns && beg + 64 * h < p.tokens ? bin_of(p, beg + 64 * h) : -1;
+    for (int b = tid; b < bins; b += kShrinkThreads) hist[b] = 0;
+    if (tid == 0) {
+        sh.tile = make_int4(-1, 0, 0, 0);
+        sh.bin = -1;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int h = 0; h < kHold; ++h) {
+        const uint64_t any = __ballot(held[h] >= 0);
+        if (!any)
+            continue;
+        const int lead = __ffsll((unsigned long long)any) - 1, b = __builtin_amdgcn_readlane(held[h], lead);
+        if (__ballot(held[h] == b) == any) {                // (one request's run: one addition for all)
+            if (lane == lead)
+                atomicAdd(&hist[b], __popcll(any));
+        } else if (held[h] >= 0) {
+            atomicAdd(&hist[held[h]], 1);
+        }
+    }
+    __syncthreads();
+    const int each = (bins + kShrinkThreads - 1) / kShrinkThreads;
+    const int b0 = min(tid * each, bins), b1 = min(b0 + each, bins);
+    int tokens = 0, tiles = 0;
+    for (int b = b0; b < b1; ++b) {
+        tokens += hist[b];
+        tiles += (hist[b] + p.tile - 1) / p.tile;
+    }
+    const int scan0 = wave_scan(tokens), scan1 = wave_scan(tiles);
+    if (lane == 63) {
+        sh.sums[0][wave] = scan0;
+        sh.sums[1][wave] = scan1;
+    }
+    __syncthreads();
+    int at = scan0 - tokens, tile = scan1 - tiles;
+    for (int w = 0; w < wave; ++w) {
+        at += sh.sums[0][w];
+        tile += sh.sums[1][w];
+    }
+    for (int b = b0; b < b1; ++b) {
+        const int n = hist[b], here = (n + p.tile - 1) / p.tile;
+        if (want >= tile && want < tile + here) {
+            sh.tile = tile_of(p, b, at, n, want - tile);
+            sh.bin = b;
+            sh.skip = (want - tile) * p.tile;
+        }
+        if (want == 0 && p.offsets)
+            p.offsets[b] = at;
+        at += n;
+        tile += here;
+    }
+    __syncthreads();
+    const int4 found = sh.tile;
+    const int bin = sh.bin, skip = sh.skip;
+    if (found.z == 0)
+        return found;
+    int before = 0;
+#pragma unroll
+    for (int h = 0; h < kHold; ++h) before += __popcll(__ballot(held[h] == bin));
+    if (lane == 0)
+        sh.sums[0][wave] = before;
+    __syncthreads();
+    int rank = -skip;
+    for (int w = 0; w < wave; ++w) rank += sh.sums[0][w];
+#pragma unroll
+    for (int h = 0; h < kHold; ++h) {
+        const uint64_t mine = __ballot(held[h] == bin);
+        const int r = rank + __popcll(mine & (((uint64_t)1 << lane) - 1));
+        if (held[h] == bin && r >= 0 && r < found.z)
+            sh.token[r] = beg + 64 * h;
+        rank += __popcll(mine);
+    }
+    __syncthreads();
+    return found;
+}
+
+// ---------------------------------------------------------------------------
+// Shrink: s v[place,r] with v = sum_k x[token,k] w[adapter,r,k], or, where the weights lie as [k][r], the
+// same from them (u).  Sixteen tokens by sixteen ranks a matrix product; a workgroup has a tile and all of
+// K, which its waves share in steps of 64 and add up in LDS.  Weights as [k][r] go through LDS, whose
+// transposing loads give a lane eight k of its rank.
+// ---------------------------------------------------------------------------
+constexpr int kStep = 64;
+
+struct ShrinkJob {
+    const uint16_t *x, *w;
+    uint16_t *rows;            // [tokens][2][Rp]: two pieces, or NULL
+    uint16_t *pieces;          // [3][Rp][places]: three pieces, or NULL
+    int64_t ldx;
+    int K;
+};
+
+struct ShrinkArgs {
+    ShrinkJob job[2];          // v; u
+    Plan plan;
+    const float *scale;
+    int64_t places;
+    int R, Rp, groups, self;   // groups of 16 RB ranks; self: the workgroups make the plan
+};
+
+template <int TB, int RB> constexpr int steps_at_once() { return TB * RB == 1 ? 4 : TB + RB <= 5 ? 2 : 1; }
+
+template <int TB>
+__device__ inline void load_steps(v4i (&x)[TB][2], const uint16_t *const (&px)[TB], int k, int K, int q)
+{
+    if (k + kStep <= K) {
+#pragma unroll
+        for (int t = 0; t < TB; ++t) {
+            x[t][0] = load8(px[t] + k);
+            x[t][1] = load8(px[t] + k + 32);
+        }
+    } else {
+        const int left = K - (k + 8 * q);
+#pragma unroll
+        for (int t = 0; t < TB; ++t) {
+            x[t][0] = load8(px[t] + k, left);
+            x[t][1] = load8(px[t] + k + 32, left - 32);
+        }
+    }
+}
+
+template <int TB, int RB, bool BACK>
+__global__ void __launch_bounds__(kShrinkThreads) k_shrink(ShrinkArgs a)
+{
+    // a wave's share: its steps' weights, then its sums
+    constexpr int kShare = BACK && TB < 2 ? 2 * RB * 64 : TB * RB * 64;            // 16-byte pieces
+    constexpr int kHist = (kBins + 3) / 4;
+    __shared__ v4i space[kShrinkWaves * kShare > kHist ? kShrinkWaves * kShare : kHist];
+    __shared__ PlanShare sh;
+    const int units = a.plan.max_tiles * a.groups;
+    const int second = BACK && (int)blockIdx.x >= units;
+    const ShrinkJob &job = a.job[second];
+    const int unit = (int)blockIdx.x - (second ? units : 0), index = unit / a.groups, group = unit % a.groups;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, i = lane & 15, q = lane >> 4;
+    int4 tile;
+    if (a.self) {
+        tile = self_plan(a.plan, index, reinterpret_cast<int32_t *>(space), sh);
+        if (group == 0 && !second) {
+            if (tid == 0)
+                a.plan.tiles[index] = tile;
+            if (tid < tile.z)
+                a.plan.order[tile.y + tid] = sh.token[tid];
+        }
+    } else {
+        tile = a.plan.tiles[index];
+        if (tid < tile.z)
+            sh.token[tid] = a.plan.order[tile.y + tid];
+        __syncthreads();
+    }
     if (tile.x < 0 || tile.z == 0)
         return;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = lane & 15, q = lane >> 4;
-    const uint16_t *px[TB], *pw[RB];
+    const uint16_t *px[TB];
 #pragma unroll
-    for (int t = 0; t < TB; ++t) px[t] = a.x + a.order[tile.y + min(16 * t + i, tile.z - 1)] * a.ldx + 8 * q;
-    // (ranks behind R take the last one's row: their sums are not read)
-#pragma unroll
-    for (int r = 0; r < RB; ++r) pw[r] = a.w + ((int64_t)tile.x * a.R + min(16 * r + i, a.R - 1)) * a.ldw + 8 * q;
+    for (int t = 0; t < TB; ++t) px[t] = job.x + sh.token[min(16 * t + i, tile.z - 1)] * job.ldx + 8 * q;
     v4f acc[TB][RB] = {};
-    const int steps = (a.K + kStep - 1) / kStep, per = (steps + a.splits - 1) / a.splits;
-    const int end = min((split + 1) * per, steps);
-    for (int s = split * per + wave; s < end; s += kWaves) {
-        const int k = s * kStep;
-        v4i x[TB][4], w[RB][4];
-        if (k + kStep <= a.K) {
+    const int steps = (job.K + kStep - 1) / kStep, r0 = 16 * RB * group;
+    if (!BACK || !second) {
+        constexpr int U = steps_at_once<TB, RB>();
+        const uint16_t *pw[RB];                // (ranks behind R take the last one's row: their sums are not read)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+        for (int r = 0; r < RB; ++r) pw[r] = job.w + ((int64_t)tile.x * a.R + min(r0 + 16 * r + i, a.R - 1)) * job.K + 8 * q;
+        for (int s = wave; s < steps; s += kShrinkWaves * U) {
+            v4i x[U][TB][2], w[U][RB][2];
 #pragma unroll
-                for (int t = 0; t < TB; ++t) x[t][j] = load8(px[t] + k + 32 * j);
-#pragma unroll
-                for (int r = 0; r < RB; ++r) w[r][j] = load8(pw[r] + k + 32 * j);
+            for (int u = 0; u < U; ++u) {
+                const int k = (s + kShrinkWaves * u) * kStep;
+                if (u > 0 && k >= job.K)
+                    break;
+                load_steps(x[u], px, k, job.K, q);
+                load_steps(w[u], pw, k, job.K, q);
             }
-        } else {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int left = a.K - (k + 32 * j + 8 * q);
+            for (int u = 0; u < U; ++u) {
+                if (u > 0 && (s + kShrinkWaves * u) * kStep >= job.K)
+                    break;
 #pragma unroll
-                for (int t = 0; t < TB; ++t) x[t][j] = load8(px[t] + k + 32 * j, left);
+                for (int h = 0; h < 2; ++h)
 #pragma unroll
-                for (int r = 0; r < RB; ++r) w[r][j] = load8(pw[r] + k + 32 * j, left);
+                    for (int t = 0; t < TB; ++t)
+#pragma unroll
+                        for (int r = 0; r < RB; ++r) acc[t][r] = mma(x[u][t][h], w[u][r][h], acc[t][r]);
             }
         }
+    } else {
+        // 64 rows of up to 2 RB chunks of 8 ranks a step, one row after another
+        const int chunks = min(2 * RB, a.R / 8 - r0 / 8);
+        const uint16_t *w = job.w + (int64_t)tile.x * job.K * a.R + r0;
+        uint16_t *mine = reinterpret_cast<uint16_t *>(space + wave * kShare);
+        int row[2 * RB], rank[2 * RB];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int h = 0; h < 2 * RB; ++h) {
+            row[h] = (lane + 64 * h) / chunks;
+            rank[h] = 8 * ((lane + 64 * h) % chunks);
+        }
+        v4i x[TB][2], b[2 * RB];
+        const auto load = [&](int s) {
+            load_steps(x, px, s * kStep, job.K, q);
 #pragma unroll
-            for (int t = 0; t < TB; ++t)
+            for (int h = 0; h < 2 * RB; ++h) {
+                b[h] = v4i{0, 0, 0, 0};
+                if (row[h] < kStep && s * kStep + row[h] < job.K)
+                    b[h] = load8(w + (int64_t)(s * kStep + row[h]) * a.R + rank[h]);
+            }
+        };
+        if (wave < steps)
+            load(wave);
+        for (int s = wave; s < steps; s += kShrinkWaves) {
+            v4i y[TB][2];
 #pragma unroll
-                for (int r = 0; r < RB; ++r) acc[t][r] = mma(x[t][j], w[r][j], acc[t][r]);
+            for (int t = 0; t < TB; ++t) {
+                y[t][0] = x[t][0];
+                y[t][1] = x[t][1];
+            }
+#pragma unroll
+            for (int h = 0; h < 2 * RB; ++h)
+                if (row[h] < kStep)
+                    *reinterpret_cast<v4i *>(mine + row[h] * (16 * RB) + rank[h]) = b[h];
+            if (s + kShrinkWaves < steps)
+                load(s + kShrinkWaves);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int r = 0; r < RB; ++r) {
+                    v4i f;
+#pragma unroll
+                    for (int g = 0; g < 2; ++g) {
+                        // sixteen lanes load four rows of sixteen ranks, and get a column each
+                        typedef short v4s __attribute__((ext_vector_type(4)));
+                        uint16_t *p = mine + (32 * h + 8 * q + 4 * g + (i >> 2)) * (16 * RB) + 16 * r + 4 * (i & 3);
+                        const v4s v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s *)p);
+                        const int2 d = __builtin_bit_cast(int2, v);
+                        f[2 * g] = d.x;
+                        f[2 * g + 1] = d.y;
+                    }
+#pragma unroll
+                    for (int t = 0; t < TB; ++t) acc[t][r] = mma(y[t][h], f, acc[t][r]);
+                }
+        }
     }
-    if (wave > 0)
-#pragma unroll
-        for (int t = 0; t < TB; ++t)
-#pragma unroll
-            for (int r = 0; r < RB; ++r) sums[wave - 1][t * RB + r][lane] = acc[t][r];
-    __syncthreads();
-    if (wave > 0)
-        return;
-    float *part = a.part + ((int64_t)split * a.tokens + tile.y) * (16 * RB);
+    __syncthreads();                           // (another wave may still read its weights where sums go)
+    v4f *sums = reinterpret_cast<v4f *>(space);
 #pragma unroll
     for (int t = 0; t < TB; ++t)
 #pragma unroll
-        for (int r = 0; r < RB; ++r) {
-            v4f v = acc[t][r];
-            for (int w = 0; w < kWaves - 1; ++w) v += sums[w][t * RB + r][lane];
+        for (int r = 0; r < RB; ++r) sums[(wave * TB * RB + t * RB + r) * 64 + lane] = acc[t][r];
+    __syncthreads();
+    const float s = a.scale ? a.scale[tile.x] : 1.0f;
+    for (int e = tid; e < TB * RB * 64; e += kShrinkThreads) {
+        v4f v = sums[e];
+        for (int w = 1; w < kShrinkWaves; ++w) v += sums[w * TB * RB * 64 + e];
+        const int block = e >> 6, rank = r0 + 16 * (block % RB) + (e & 15), at = 16 * (block / RB) + 4 * ((e >> 4) & 3);
+        const int n = tile.z - at;             // of the four places from there
+        if (n <= 0)
+            continue;
+        uint16_t o[3][4];
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
-                if (16 * t + 4 * q + c < tile.z)
-                    part[(16 * t + 4 * q + c) * (16 * RB) + 16 * r + i] = v[c];
+        for (int c = 0; c < 4; ++c) {
+            const float f = v[c] * s, h = cut(f), m = rest(f, h), mh = cut(m);
+            o[0][c] = bf16_bits(h);
+            o[1][c] = bf16_bits(mh);
+            o[2][c] = bf16_bits(rest(m, mh));
+            if (job.rows && c < n) {
+                uint16_t *p = job.rows + (int64_t)(tile.y + at + c) * 2 * a.Rp + rank;
+                p[0] = o[0][c];
+                p[a.Rp] = bf16_bits(m);
+            }
         }
+        if (BACK && job.pieces)
+#pragma unroll
+            for (int h = 0; h < 3; ++h) {
+                uint16_t *p = job.pieces + ((int64_t)h * a.Rp + rank) * a.places + tile.y + at;
+                if (n >= 4) {
+                    __builtin_memcpy(p, o[h], 8);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        if (c < n)
+                            p[c] = o[h][c];
+                }
+            }
+    }
 }
 
 // ---------------------------------------------------------------------------
-// Expand: out[token,n] = bf16(base[token,n] + s sum_r v[place,r] w[adapter,n,r]).
-// A wave takes 64 n at a time as four products of 16; a product's row 4 a + c is
-// n = 16 a + 4 j + c, so that a lane ends with 16 n in a row of its token.
+// Expand: out[token,n] = bf16(base[token,n] + sum_r (s v)[place,r] w[adapter,n,r]), or with the weights as
+// [adapter][r][n] (dx).  A wave takes 64 n at a time as four products of 16, dealt to them so that a lane ends
+// with twice eight n in a row of its token, and four lanes with 64 bytes of it.
 // ---------------------------------------------------------------------------
+constexpr int kThreads = 256, kWaves = kThreads / 64;
+
 struct ExpandArgs {
-    const float *part, *scale;
+    const uint16_t *rows;      // [tokens][2][Rp]: s v
     const int32_t *order;
     const int4 *tiles;
-    const uint16_t *w, *base;  // w [adapters][N][R]
+    const uint16_t *w, *base;
     uint16_t *out;
     int64_t ldb, ldo;
-    int tokens, N, R, Rp, splits, chunks;
+    int N, R, Rp, chunks;
 };
 
-// Ranks 8 c .. 8 c + 7 of a place: the splits' sums in order, times s.
-__device__ inline void load_ranks(float (&v)[8], const ExpandArgs &a, int place, int c, float s)
-{
-    const float *p = a.part + (int64_t)place * a.Rp + 8 * c;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = 0.0f;
-    for (int k = 0; k < a.splits; ++k, p += (int64_t)a.tokens * a.Rp) {
-        const v4f lo = *reinterpret_cast<const v4f *>(p), hi = *reinterpret_cast<const v4f *>(p + 4);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[i] += lo[i];
-            v[4 + i] += hi[i];
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] *= s;
-}
-
-// G groups of 32 ranks; PACK: at most 16 ranks, both pieces of v in one product.
-template <int TB, int G, bool PACK>
+// G groups of 32 ranks; PACK: at most 16 ranks, both pieces of v in one product; TR: weights [r][n].
+template <int TB, int G, bool PACK, bool TR>
 __global__ void __launch_bounds__(kThreads) k_expand(ExpandArgs a)
 {
     const int4 tile = a.tiles[blockIdx.x / a.chunks];
     const int chunk = blockIdx.x % a.chunks;
-    if (tile.z == 0)
+    if (tile.w == 0)
         return;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = lane & 15, q = lane >> 4;
     const int ranks = a.R / 8;                 // chunks of 8 ranks
     const bool live = tile.x >= 0;
     int64_t token[TB];
 #pragma unroll
-    for (int t = 0; t < TB; ++t) token[t] = a.order[tile.y + min(16 * t + i, tile.z - 1)];
+    for (int t = 0; t < TB; ++t) token[t] = a.order[tile.y + min(16 * t + i, tile.w - 1)];
     v4i hi[TB][G], lo[TB][PACK ? 1 : G];
     const uint16_t *w = a.w + (int64_t)(live ? tile.x : 0) * a.N * a.R;
-    if (live) {
-        const float s = a.scale ? a.scale[tile.x] : 1.0f;
+    if (live)
 #pragma unroll
-        for (int t = 0; t < TB; ++t)
+        for (int t = 0; t < TB; ++t) {
+            const uint16_t *v = a.rows + (int64_t)(tile.y + min(16 * t + i, tile.w - 1)) * 2 * a.Rp;
 #pragma unroll
             for (int g = 0; g < G; ++g) {
                 const int c = PACK ? q % ranks : 4 * g + q, piece = PACK ? q / ranks : 0;
-                float v[8] = {}, h[8], l[8];
+                hi[t][g] = v4i{0, 0, 0, 0};
                 if (c < ranks && piece < 2)
-                    load_ranks(v, a, tile.y + min(16 * t + i, tile.z - 1), c, s);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    h[e] = cut(v[e]);
-                    l[e] = rest(v[e], h[e]);
-                    if (PACK && piece == 1)
-                        h[e] = l[e];
-                }
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    hi[t][g][e] = pack2(h[2 * e], h[2 * e + 1]);
-                    if (!PACK)
-                        lo[t][g][e] = pack2(l[2 * e], l[2 * e + 1]);
-                }
-            }
-    }
-    const int blocks = (a.N + 63) / 64;
-    for (int b = chunk * kWaves + wave; b < blocks; b += a.chunks * kWaves) {
-        const int n0 = 64 * b;
-        v4i wv[4][G];
-        if (live) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int n = min(n0 + 16 * (i >> 2) + 4 * j + (i & 3), a.N - 1);
-#pragma unroll
-                for (int g = 0; g < G; ++g) {
-                    const int c = PACK ? q % ranks : 4 * g + q;
-                    wv[j][g] = v4i{0, 0, 0, 0};
-                    if (c < ranks && (!PACK || q < 2 * ranks))
-                        wv[j][g] = load8(w + (int64_t)n * a.R + 8 * c);
+                    hi[t][g] = load8(v + piece * a.Rp + 8 * c);
+                if (!PACK) {
+                    lo[t][PACK ? 0 : g] = v4i{0, 0, 0, 0};
+                    if (c < ranks)
+                        lo[t][PACK ? 0 : g] = load8(v + a.Rp + 8 * c);
                 }
             }
         }
-        const int at = n0 + 16 * q, left = a.N - at;
+    const int blocks = (a.N + 63) / 64;
+    for (int b = chunk * kWaves + wave; b < blocks; b += a.chunks * kWaves) {
+        const int n0 = 64 * b;
+        // this lane's outputs: n0 + 8 q .. + 7 and 32 behind
+        const int left = a.N - (n0 + 8 * q);
+        int o[TB][8];
+        if (a.base)
 #pragma unroll
-        for (int t = 0; t < TB; ++t) {
-            const bool mine = 16 * t + i < tile.z && left > 0;
-            int o[8] = {};
-            if (a.base && mine) {
-                const uint16_t *p = a.base + token[t] * a.ldb + at;
-                const v4i o0 = load8(p, left), o1 = load8(p + 8, left - 8);
+            for (int t = 0; t < TB; ++t) {
+                v4i o0{0, 0, 0, 0}, o1{0, 0, 0, 0};
+                if (16 * t + i < tile.w) {
+                    const uint16_t *p = a.base + token[t] * a.ldb + n0 + 8 * q;
+                    o0 = load8(p, left);
+                    o1 = load8(p + 32, left - 32);
+                }
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    o[e] = o0[e];
-                    o[4 + e] = o1[e];
+                    o[t][e] = o0[e];
+                    o[t][4 + e] = o1[e];
                 }
             }
-            v4f acc[4] = {};
-            if (live)
+        else
+#pragma unroll
+            for (int t = 0; t < TB; ++t)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) o[t][e] = 0;
+        v4i f[4][G];
+        if (live) {
+            if (TR) {
+                // rows of eight ranks, four n of each: the lane's row 4 a + c of product m is
+                // n = 32 (c / 2) + 8 a + 4 (c % 2) + m
+                const int n = n0 + 32 * ((i & 3) >> 1) + 8 * (i >> 2) + 4 * (i & 1), there = a.N - n;
+#pragma unroll
+                for (int g = 0; g < G; ++g) {
+                    const int c = PACK ? q % ranks : 4 * g + q;
+                    int2 r[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        r[j] = make_int2(0, 0);
+                        if (c < ranks && (!PACK || q < 2 * ranks)) {
+                            const uint16_t *p = w + (int64_t)(8 * c + j) * a.N + n;
+                            if (there >= 4) {
+                                __builtin_memcpy(&r[j], p, 8);
+                            } else {
+                                uint16_t e[4];
+#pragma unroll
+                                for (int m = 0; m < 4; ++m) e[m] = m < there ? p[m] : 0;
+                                __builtin_memcpy(&r[j], e, 8);
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int m = 0; m < 4; ++m)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            f[m][g][j] = (int)__builtin_amdgcn_perm(
+                                (uint32_t)(m < 2 ? r[2 * j + 1].x : r[2 * j + 1].y),
+                                (uint32_t)(m < 2 ? r[2 * j].x : r[2 * j].y), m % 2 ? 0x07060302u : 0x05040100u);
+                }
+            } else {
+                // rows of n: row 4 a + c of product j is n = 32 (j / 2) + 8 a + 4 (j % 2) + c
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int n = min(n0 + 32 * (j >> 1) + 8 * (i >> 2) + 4 * (j & 1) + (i & 3), a.N - 1);
+#pragma unroll
+                    for (int g = 0; g < G; ++g) {
+                        const int c = PACK ? q % ranks : 4 * g + q;
+                        f[j][g] = v4i{0, 0, 0, 0};
+                        if (c < ranks && (!PACK || q < 2 * ranks))
+                            f[j][g] = load8(w + (int64_t)n * a.R + 8 * c);
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int t = 0; t < TB; ++t) {
+            if (live) {
+                v4f acc[4] = {};
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
 #pragma unroll
                     for (int g = 0; g < G; ++g) {
-                        acc[j] = mma(wv[j][g], hi[t][g], acc[j]);
+                        acc[j] = mma(f[j][g], hi[t][g], acc[j]);
                         if (!PACK)
-                            acc[j] = mma(wv[j][g], lo[t][PACK ? 0 : g], acc[j]);
+                            acc[j] = mma(f[j][g], lo[t][PACK ? 0 : g], acc[j]);
                     }
-            if (!mine)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float d0 = TR ? acc[(2 * e) % 4][e / 2] : acc[e / 2][(2 * e) % 4];
+                    const float d1 = TR ? acc[(2 * e + 1) % 4][e / 2] : acc[e / 2][(2 * e + 1) % 4];
+                    const uint32_t d = (uint32_t)o[t][e];
+                    o[t][e] = pack2(__uint_as_float(d << 16) + d0, __uint_as_float(d & 0xFFFF0000u) + d1);
+                }
+            }
+            if (16 * t + i >= tile.w || left <= 0)
                 continue;
-            if (live || !a.base)
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-#pragma unroll
-                    for (int c = 0; c < 4; c += 2) {
-                        const uint32_t d = (uint32_t)o[2 * j + c / 2];
-                        o[2 * j + c / 2] = pack2(__uint_as_float(d << 16) + acc[j][c],
-                                                 __uint_as_float(d & 0xFFFF0000u) + acc[j][c + 1]);
-                    }
-            uint16_t *p = a.out + token[t] * a.ldo + at;
-            if (left >= 16) {
-                __builtin_memcpy(p, o, 32);
+            uint16_t *p = a.out + token[t] * a.ldo + n0 + 8 * q;
+            if (left >= 40) {
+                __builtin_memcpy(p, &o[t][0], 16);
+                __builtin_memcpy(p + 32, &o[t][4], 16);
             } else {
                 uint16_t v[16];
-                __builtin_memcpy(v, o, 32);
+                __builtin_memcpy(v, o[t], 32);
 #pragma unroll
-                for (int e = 0; e < 16; ++e)
+                for (int e = 0; e < 8; ++e) {
                     if (e < left)
                         p[e] = v[e];
-            }
-        }
-    }
-}
-
-// ---------------------------------------------------------------------------
-// Gradients
-// ---------------------------------------------------------------------------
-// out[l][q][p] = in[l][p][q] of the adapters that have tokens; columns P .. ldo - 1 are 0.
-struct TransposeArgs {
-    const uint16_t *in;
-    uint16_t *out;
-    const int32_t *offsets;
-    int64_t ldo;
-    int P, Q;
-};
-
-__global__ void __launch_bounds__(kThreads) k_transpose(TransposeArgs a)
-{
-    __shared__ uint16_t t[64][66];
-    const int l = blockIdx.z, q0 = blockIdx.x * 64, p0 = blockIdx.y * 64;
-    if (a.offsets[l] == a.offsets[l + 1])
-        return;
-    const uint16_t *in = a.in + (int64_t)l * a.P * a.Q;
-    uint16_t *out = a.out + (int64_t)l * a.Q * a.ldo;
-    const int x = threadIdx.x & 63, y = threadIdx.x >> 6;
-    for (int p = y; p < 64; p += 4) t[p][x] = p0 + p < a.P && q0 + x < a.Q ? in[(int64_t)(p0 + p) * a.Q + q0 + x] : 0;
-    __syncthreads();
-    for (int q = y; q < 64; q += 4)
-        if (q0 + q < a.Q && p0 + x < a.ldo)
-            out[(int64_t)(q0 + q) * a.ldo + p0 + x] = t[x][q];
-}
-
-// s v (or s u) as three bf16 pieces, places along the rows: pieces[3][16 RB][places].
-struct FactorArgs {
-    const float *part, *scale;
-    const int32_t *offsets;
-    uint16_t *pieces;
-    int64_t places;            // of a row, at least tokens
-    int tokens, adapters, Rp, splits;
-};
-
-__global__ void __launch_bounds__(kThreads) k_factors(FactorArgs a)
-{
-    __shared__ float t[16][65];
-    const int row0 = blockIdx.x * 64, r0 = blockIdx.y * 16, with = a.offsets[a.adapters];
-    for (int j = 0; j < 4; ++j) {
-        const int r = threadIdx.x & 15, row = row0 + 16 * j + (int)(threadIdx.x >> 4);
-        float v = 0.0f;
-        if (row < with) {
-            for (int k = 0; k < a.splits; ++k) v += a.part[((int64_t)k * a.tokens + row) * a.Rp + r0 + r];
-            if (a.scale) {
-                int lo = 0, hi = a.adapters;   // the adapter whose places hold the row
-                while (hi - lo > 1) {
-                    const int m = (lo + hi) / 2;
-                    if (a.offsets[m] <= row)
-                        lo = m;
-                    else
-                        hi = m;
+                    if (32 + e < left)
+                        p[32 + e] = v[8 + e];
                 }
-                v *= a.scale[lo];
             }
         }
-        t[r][row - row0] = v;
     }
-    __syncthreads();
-    const int r = threadIdx.x >> 4, c = 4 * (threadIdx.x & 15);
-    uint16_t o[3][4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float v = t[r][c + i], h = cut(v), m = rest(v, h), mh = cut(m);
-        o[0][i] = bf16_bits(h);
-        o[1][i] = bf16_bits(mh);
-        o[2][i] = bf16_bits(rest(m, mh));
-    }
-    // (rows of whole 64s: nothing lies behind them)
-#pragma unroll
-    for (int h = 0; h < 3; ++h)
-        __builtin_memcpy(a.pieces + ((int64_t)h * a.Rp + r0 + r) * a.places + row0 + c, o[h], 8);
 }
 
-// out[l][r][c] (or [l][c][r]) = sum over the adapter's places of f[r][place] z[token][c].  A wave takes 128
-// columns and 16 RB ranks, 32 places at a time: a lane loads 8 columns of 8 tokens and pairs them up for the
+// ---------------------------------------------------------------------------
+// Outer: out[l][r][c] (or [l][c][r]) = sum over the adapter's places of f[r][place] z[token][c].  A wave takes
+// 128 columns and 16 RB ranks, 32 places at a time: a lane loads 8 columns of 8 tokens and pairs them up for the
 // matrix cores, whose m-th product has the columns 8 i + m.  Waves and splits share the places.
-struct OuterArgs {
+// ---------------------------------------------------------------------------
+struct OuterJob {
     const uint16_t *z, *pieces;
-    const int32_t *order, *offsets;
     float *out;                // [splits] of the result
-    int64_t ldz, places, size; // size: elements of the result
-    int C, R, Rp, blocks, groups, splits;
+    int64_t ldz, size;         // size: elements of the result
+    int C, blocks, splits;
     int rank_last;             // the result is [l][c][r]
 };
 
+struct OuterArgs {
+    OuterJob job[2];
+    const int32_t *order, *offsets;
+    int64_t places;
+    int R, Rp, groups, first;  // workgroups of the first job
+};
+
 template <int RB>
-__global__ void __launch_bounds__(kThreads) k_outer(OuterArgs a)
+__global__ void __launch_bounds__(RB == 1 ? 1024 : 512) k_outer(OuterArgs a)
 {
-    __shared__ v4f sums[RB * 8][64];
-    int b = blockIdx.x;
-    const int split = b % a.splits;
-    b /= a.splits;
+    extern __shared__ v4f sums[];              // [waves / 2][RB * 8][64]
+    const int second = (int)blockIdx.x >= a.first;
+    const OuterJob &job = a.job[second];
+    int b = (int)blockIdx.x - (second ? a.first : 0);
+    const int split = b % job.splits;
+    b /= job.splits;
     const int group = b % a.groups;
     b /= a.groups;
-    const int c0 = b % a.blocks * 128, l = b / a.blocks;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = lane & 15, q = lane >> 4;
+    const int c0 = b % job.blocks * 128, l = b / job.blocks;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6, i = lane & 15, q = lane >> 4;
     const int beg = a.offsets[l], end = a.offsets[l + 1], r0 = group * 16 * RB;
-    const int left = a.C - (c0 + 8 * i);
-    const uint16_t *z = a.z + c0 + 8 * i;
+    const int left = job.C - (c0 + 8 * i);
+    const uint16_t *z = job.z + c0 + 8 * i;
     v4f acc[RB][8] = {};
-    for (int t = beg + 32 * (split * kWaves + wave); t < end; t += 32 * kWaves * a.splits) {
+    for (int t = beg + 32 * (split * waves + wave); t < end; t += 32 * waves * job.splits) {
         const int first = t + 8 * q, n = end - first;          // this lane's places
         v4i row[8], f[3][RB];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             row[j] = v4i{0, 0, 0, 0};
             if (j < n)
-                row[j] = load8(z + a.order[first + j] * a.ldz, left);
+                row[j] = load8(z + a.order[first + j] * job.ldz, left);
         }
 #pragma unroll
         for (int h = 0; h < 3; ++h)
 #pragma unroll
             for (int r = 0; r < RB; ++r)
-                f[h][r] = load8(a.pieces + ((int64_t)h * a.Rp + r0 + 16 * r + i) * a.places + first, n);
+                f[h][r] = load8(job.pieces + ((int64_t)h * a.Rp + r0 + 16 * r + i) * a.places + first, n);
 #pragma unroll
         for (int m = 0; m < 8; ++m) {
             v4i col;
@@ -511,37 +697,37 @@ __global__ void __launch_bounds__(kThreads) k_outer(OuterArgs a)
                 for (int r = 0; r < RB; ++r) acc[r][m] = mma(f[h][r], col, acc[r][m]);
         }
     }
-    for (int w = 1; w < kWaves; ++w) {
-        if (wave == w)
+    for (int half = waves / 2; half > 0; half /= 2) {
+        if (wave >= half && wave < 2 * half)
 #pragma unroll
             for (int r = 0; r < RB; ++r)
 #pragma unroll
-                for (int m = 0; m < 8; ++m) sums[r * 8 + m][lane] = acc[r][m];
+                for (int m = 0; m < 8; ++m) sums[((wave - half) * RB * 8 + r * 8 + m) * 64 + lane] = acc[r][m];
         __syncthreads();
-        if (wave == 0)
+        if (wave < half)
 #pragma unroll
             for (int r = 0; r < RB; ++r)
 #pragma unroll
-                for (int m = 0; m < 8; ++m) acc[r][m] += sums[r * 8 + m][lane];
+                for (int m = 0; m < 8; ++m) acc[r][m] += sums[(wave * RB * 8 + r * 8 + m) * 64 + lane];
         __syncthreads();
     }
     if (wave > 0)
         return;
-    float *out = a.out + split * a.size;
+    float *out = job.out + split * job.size;
 #pragma unroll
     for (int r = 0; r < RB; ++r) {
         const int rank = r0 + 16 * r + 4 * q;
         if (rank >= a.R)
             continue;
-        if (a.rank_last) {
+        if (job.rank_last) {
 #pragma unroll
             for (int m = 0; m < 8; ++m)
                 if (m < left)
-                    __builtin_memcpy(out + ((int64_t)l * a.C + c0 + 8 * i + m) * a.R + rank, &acc[r][m], 16);
+                    __builtin_memcpy(out + ((int64_t)l * job.C + c0 + 8 * i + m) * a.R + rank, &acc[r][m], 16);
         } else {
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                float *o = out + ((int64_t)l * a.R + rank + c) * a.C + c0 + 8 * i;
+                float *o = out + ((int64_t)l * a.R + rank + c) * job.C + c0 + 8 * i;
                 float v[8];
 #pragma unroll
                 for (int m = 0; m < 8; ++m) v[m] = acc[r][m][c];
@@ -574,32 +760,36 @@ __global__ void __launch_bounds__(kThreads) k_add_parts(float *out, const float 
 // ---------------------------------------------------------------------------
 struct Sizes {
     int64_t T, K, N, R, L;
-    int rb, tb, max_tiles;     // blocks of 16 ranks (1, 2, 4 or 8) and of 16 tokens of a tile
-    int64_t Rp;
+    int64_t Rp;                // ranks in whole blocks of 16: 1, 2, 4 or 8
+    int tb, rb, groups;        // shrink: blocks of tokens and ranks of a workgroup, groups of ranks
+    int wide;                  // expand: blocks of tokens
+    int max_tiles;
 };
 
 Sizes sizes(int64_t T, int64_t K, int64_t N, int64_t R, int64_t L)
 {
-    Sizes z{T, K, N, R, L, 1, 1, 0, 0};
-    while (16 * z.rb < R) z.rb *= 2;
-    z.Rp = 16 * z.rb;
-    // tiles as full as the adapters' mean number of tokens lets them be, at most 8 products of accumulators
+    Sizes z{T, K, N, R, L, 16, 1, 1, 1, 1, 0};
+    while (z.Rp < R) z.Rp *= 2;
     const int64_t mean = T / std::min(L, std::max<int64_t>(T, 1));
-    while (z.tb < 4 && z.tb * z.rb < 8 && mean > 16 * z.tb) z.tb *= 2;
+    // expand: as many tokens for each load of the weights as there are and registers hold
+    const int most = R <= 32 ? 4 : R <= 64 ? 2 : 1;
+    while (z.wide < most && mean > 16 * z.wide) z.wide *= 2;
+    // shrink: more tokens a workgroup only where there are workgroups for all CUs
+    while (z.tb < z.wide && T >= 16 * 2 * z.tb * 240) z.tb *= 2;
     z.max_tiles = (int)std::max<int64_t>(1, T / (16 * z.tb) + std::min(L + 1, T));
+    // and more ranks a workgroup likewise
+    const int blocks = (int)(z.Rp / 16);
+    while (z.rb < 4 && z.rb < blocks && z.rb * z.tb < 8 && (int64_t)z.max_tiles * (blocks / z.rb) > 512) z.rb *= 2;
+    z.groups = (int)((R + 16 * z.rb - 1) / (16 * z.rb));
     return z;
 }
 
-int shrink_splits(const Sizes &z, int64_t K)
-{
-    const int64_t steps = (K + kStep - 1) / kStep, most = (steps + kWaves - 1) / kWaves;
-    return (int)std::max<int64_t>(1, std::min<int64_t>({most, 32, 2048 / z.max_tiles}));
-}
+int outer_waves(const Sizes &z) { return z.T / z.L < 512 ? 4 : z.Rp > 16 ? 8 : 16; }
 
 int outer_splits(const Sizes &z, int64_t C)
 {
-    const int64_t wgs = z.L * ((C + 127) / 128) * (z.rb > 4 ? 2 : 1);
-    return (int)std::max<int64_t>(1, std::min<int64_t>({512 / wgs, z.T / 512, 16}));
+    const int64_t wgs = z.L * ((C + 127) / 128) * ((z.R + 31) / 32);
+    return (int)std::max<int64_t>(1, std::min<int64_t>({512 / wgs, z.T / (64 * outer_waves(z)), 16}));
 }
 
 // Consecutive pieces of the workspace, 256-byte aligned.
@@ -614,49 +804,34 @@ struct Layout {
     }
 };
 
-struct Forward {
+struct Space {
     int32_t *order, *offsets;
     int4 *tiles;
-    float *part;
+    uint16_t *rows;            // of s v (backward: s u) for expand
+    uint16_t *fv, *fu;         // backward: the pieces of s v and s u for outer
+    float *outer_a, *outer_b;  // and the parts of dA and dB
+    int64_t places;
     size_t bytes;
 };
 
-Forward forward_space(const Sizes &z, void *ws)
+Space space(const Sizes &z, void *ws, bool back)
 {
     Layout l{static_cast<uint8_t *>(ws)};
-    Forward f;
+    Space f{};
     f.order = l.take<int32_t>(z.T);
-    f.offsets = l.take<int32_t>(z.L + 1);
     f.tiles = l.take<int4>(z.max_tiles);
-    f.part = l.take<float>(shrink_splits(z, z.K) * z.T * z.Rp);
+    f.rows = l.take<uint16_t>(z.T * 2 * z.Rp);
+    if (back) {
+        f.offsets = l.take<int32_t>(z.L + 1);
+        f.places = (z.T + 7) / 8 * 8;
+        f.fv = l.take<uint16_t>(3 * z.Rp * f.places);
+        f.fu = l.take<uint16_t>(3 * z.Rp * f.places);
+        const int64_t sa = outer_splits(z, z.K), sb = outer_splits(z, z.N);
+        f.outer_a = l.take<float>(sa > 1 ? sa * z.L * z.R * z.K : 0);
+        f.outer_b = l.take<float>(sb > 1 ? sb * z.L * z.R * z.N : 0);
+    }
     f.bytes = l.bytes;
     return f;
-}
-
-struct Backward {
-    Forward f;                 // its part: v
-    float *u, *outer;
-    uint16_t *at, *bt, *fv, *fu;
-    int64_t ldbt, places;
-    size_t bytes;
-};
-
-Backward backward_space(const Sizes &z, void *ws)
-{
-    Backward b;
-    b.f = forward_space(z, ws);
-    Layout l{static_cast<uint8_t *>(ws), b.f.bytes};
-    b.u = l.take<float>(shrink_splits(z, z.N) * z.T * z.Rp);
-    b.ldbt = (z.N + 7) / 8 * 8;
-    b.at = l.take<uint16_t>(z.L * z.K * z.R);
-    b.bt = l.take<uint16_t>(z.L * z.R * b.ldbt);
-    b.places = (z.T + 63) / 64 * 64;
-    b.fv = l.take<uint16_t>(3 * z.Rp * b.places);
-    b.fu = l.take<uint16_t>(3 * z.Rp * b.places);
-    const int64_t sa = outer_splits(z, z.K), sb = outer_splits(z, z.N);
-    b.outer = l.take<float>(std::max(sa > 1 ? sa * z.L * z.R * z.K : 0, sb > 1 ? sb * z.L * z.R * z.N : 0));
-    b.bytes = l.bytes;
-    return b;
 }
 
 bool good_shape(int64_t T, int64_t K, int64_t N, int64_t R, int64_t L)
@@ -665,100 +840,96 @@ bool good_shape(int64_t T, int64_t K, int64_t N, int64_t R, int64_t L)
            R % 8 == 0 && L > 0 && L <= kMaxAdapters && L * std::max<int64_t>(R, 64) * std::max(K, N) < (int64_t)1 << 35;
 }
 
-hipError_t launch_plan(const Sizes &z, const Forward &f, const void *ids, int32_t id_bits, hipStream_t s)
+template <bool BACK>
+hipError_t launch_shrink(const Sizes &z, const ShrinkArgs &a, hipStream_t s)
 {
-    const Plan p{ids, f.order, f.offsets, f.tiles, (int)z.T, (int)z.L, 16 * z.tb, z.max_tiles, id_bits};
-    hipLaunchKernelGGL(k_plan, dim3(1), dim3(kPlanThreads), 0, s, p);
-    return hipGetLastError();
-}
-
-hipError_t launch_shrink(const Sizes &z, const Forward &f, const uint16_t *x, int64_t ldx, const uint16_t *w, int64_t ldw,
-                         int64_t K, float *part, hipStream_t s)
-{
-    const ShrinkArgs a{x, w, f.order, f.tiles, part, ldx, ldw, (int)z.T, (int)K, (int)z.R, shrink_splits(z, K)};
-    const dim3 grid((unsigned)(z.max_tiles * a.splits)), block(kThreads);
+    const dim3 grid((unsigned)(z.max_tiles * z.groups * (BACK ? 2 : 1))), block(kShrinkThreads);
     switch (z.rb * 8 + z.tb) {
-    case 8 + 1: hipLaunchKernelGGL((k_shrink<1, 1>), grid, block, 0, s, a); break;
-    case 8 + 2: hipLaunchKernelGGL((k_shrink<2, 1>), grid, block, 0, s, a); break;
-    case 8 + 4: hipLaunchKernelGGL((k_shrink<4, 1>), grid, block, 0, s, a); break;
-    case 16 + 1: hipLaunchKernelGGL((k_shrink<1, 2>), grid, block, 0, s, a); break;
-    case 16 + 2: hipLaunchKernelGGL((k_shrink<2, 2>), grid, block, 0, s, a); break;
-    case 16 + 4: hipLaunchKernelGGL((k_shrink<4, 2>), grid, block, 0, s, a); break;
-    case 32 + 1: hipLaunchKernelGGL((k_shrink<1, 4>), grid, block, 0, s, a); break;
-    case 32 + 2: hipLaunchKernelGGL((k_shrink<2, 4>), grid, block, 0, s, a); break;
-    default: hipLaunchKernelGGL((k_shrink<1, 8>), grid, block, 0, s, a); break;
+    case 8 + 1: hipLaunchKernelGGL((k_shrink<1, 1, BACK>), grid, block, 0, s, a); break;
+    case 8 + 2: hipLaunchKernelGGL((k_shrink<2, 1, BACK>), grid, block, 0, s, a); break;
+    case 8 + 4: hipLaunchKernelGGL((k_shrink<4, 1, BACK>), grid, block, 0, s, a); break;
+    case 16 + 1: hipLaunchKernelGGL((k_shrink<1, 2, BACK>), grid, block, 0, s, a); break;
+    case 16 + 2: hipLaunchKernelGGL((k_shrink<2, 2, BACK>), grid, block, 0, s, a); break;
+    case 16 + 4: hipLaunchKernelGGL((k_shrink<4, 2, BACK>), grid, block, 0, s, a); break;
+    case 32 + 1: hipLaunchKernelGGL((k_shrink<1, 4, BACK>), grid, block, 0, s, a); break;
+    default: hipLaunchKernelGGL((k_shrink<2, 4, BACK>), grid, block, 0, s, a); break;
     }
     return hipGetLastError();
 }
 
-template <int TB>
+// Fills in the plan, and makes it in a launch of its own where the tokens are too many for each workgroup.
+hipError_t make_plan(const Sizes &z, const Space &f, const void *ids, int32_t id_bits, ShrinkArgs &a, hipStream_t s)
+{
+    a.plan = Plan{ids, f.order, f.offsets, f.tiles, (int)z.T, (int)z.L, 16 * z.tb, 16 * z.wide, z.max_tiles, id_bits};
+    a.self = z.T > 0 && z.T <= kSelfTokens;
+    if (a.self)
+        return hipSuccess;
+    hipLaunchKernelGGL(k_plan, dim3(1), dim3(kPlanThreads), 0, s, a.plan);
+    return hipGetLastError();
+}
+
+template <int TB, bool TR>
 void expand_ranks(const ExpandArgs &a, dim3 grid, hipStream_t s)
 {
     const dim3 block(kThreads);
     if (a.R <= 16)
-        hipLaunchKernelGGL((k_expand<TB, 1, true>), grid, block, 0, s, a);
+        hipLaunchKernelGGL((k_expand<TB, 1, true, TR>), grid, block, 0, s, a);
     else if (a.R <= 32)
-        hipLaunchKernelGGL((k_expand<TB, 1, false>), grid, block, 0, s, a);
+        hipLaunchKernelGGL((k_expand<TB, 1, false, TR>), grid, block, 0, s, a);
     else if (TB < 4 && a.R <= 64)
-        hipLaunchKernelGGL((k_expand<TB < 4 ? TB : 1, 2, false>), grid, block, 0, s, a);
+        hipLaunchKernelGGL((k_expand<TB < 4 ? TB : 1, 2, false, TR>), grid, block, 0, s, a);
     else
-        hipLaunchKernelGGL((k_expand<1, 4, false>), grid, block, 0, s, a);
+        hipLaunchKernelGGL((k_expand<1, 4, false, TR>), grid, block, 0, s, a);
 }
 
-hipError_t launch_expand(const Sizes &z, const Forward &f, const float *part, int splits, const float *scale,
-                         const uint16_t *w, int64_t N, const uint16_t *base, int64_t ldb, uint16_t *out, int64_t ldo,
-                         hipStream_t s)
+template <bool TR>
+hipError_t launch_expand(const Sizes &z, const Space &f, const uint16_t *w, int64_t N, const uint16_t *base, int64_t ldb,
+                         uint16_t *out, int64_t ldo, hipStream_t s)
 {
     const int64_t blocks = (N + 63) / 64, full = (blocks + kWaves - 1) / kWaves;
-    const int chunks = (int)std::max<int64_t>(1, std::min<int64_t>(full, 4096 / z.max_tiles));
-    const ExpandArgs a{part, scale, f.order, f.tiles, w, base, out, ldb, ldo, (int)z.T, (int)N, (int)z.R, (int)z.Rp,
-                       splits, chunks};
+    const int64_t tiles = z.T / (16 * z.wide) + std::min(z.L + 1, z.T);
+    const int chunks = (int)std::max<int64_t>(1, std::min<int64_t>(full, 8192 / tiles));
+    const ExpandArgs a{f.rows, f.order, f.tiles, w, base, out, ldb, ldo, (int)N, (int)z.R, (int)z.Rp, chunks};
     const dim3 grid((unsigned)(z.max_tiles * chunks));
-    if (z.tb == 4)
-        expand_ranks<4>(a, grid, s);
-    else if (z.tb == 2)
-        expand_ranks<2>(a, grid, s);
+    if (z.wide == 4)
+        expand_ranks<4, TR>(a, grid, s);
+    else if (z.wide == 2)
+        expand_ranks<2, TR>(a, grid, s);
     else
-        expand_ranks<1>(a, grid, s);
+        expand_ranks<1, TR>(a, grid, s);
     return hipGetLastError();
 }
 
-hipError_t launch_outer(const Sizes &z, const Backward &b, const uint16_t *x, int64_t ldx, int64_t C,
-                        const uint16_t *pieces, bool rank_last, float *out, hipStream_t s)
+hipError_t launch_outer(const Sizes &z, const Space &f, const uint16_t *x, int64_t ldx, const uint16_t *dy, int64_t lddy,
+                        float *da, float *db, hipStream_t s)
 {
-    const int splits = outer_splits(z, C), rb = std::min(z.rb, 4);
-    OuterArgs a{x, pieces, b.f.order, b.f.offsets, splits > 1 ? b.outer : out, ldx, b.places, z.L * z.R * C, (int)C,
-                (int)z.R, (int)z.Rp, (int)((C + 127) / 128), z.rb / rb, splits, rank_last};
-    const dim3 grid((unsigned)(z.L * a.blocks * a.groups * splits)), block(kThreads);
+    const int sa = outer_splits(z, z.K), sb = outer_splits(z, z.N), waves = outer_waves(z), rb = z.Rp > 16 ? 2 : 1;
+    OuterArgs a{};
+    a.job[0] = OuterJob{x, f.fu, sa > 1 ? f.outer_a : da, ldx, z.L * z.R * z.K, (int)z.K, (int)((z.K + 127) / 128), sa, 0};
+    a.job[1] = OuterJob{dy, f.fv, sb > 1 ? f.outer_b : db, lddy, z.L * z.R * z.N, (int)z.N, (int)((z.N + 127) / 128), sb, 1};
+    a.order = f.order;
+    a.offsets = f.offsets;
+    a.places = f.places;
+    a.R = (int)z.R;
+    a.Rp = (int)z.Rp;
+    a.groups = (int)((z.R + 16 * rb - 1) / (16 * rb));
+    a.first = (int)(z.L * a.job[0].blocks * a.groups * sa);
+    const dim3 grid((unsigned)(a.first + z.L * a.job[1].blocks * a.groups * sb)), block(64 * waves);
+    const size_t lds = (size_t)waves / 2 * rb * 8 * 64 * sizeof(v4f);
     if (rb == 1)
-        hipLaunchKernelGGL((k_outer<1>), grid, block, 0, s, a);
-    else if (rb == 2)
-        hipLaunchKernelGGL((k_outer<2>), grid, block, 0, s, a);
+        hipLaunchKernelGGL((k_outer<1>), grid, block, lds, s, a);
     else
-        hipLaunchKernelGGL((k_outer<4>), grid, block, 0, s, a);
+        hipLaunchKernelGGL((k_outer<2>), grid, block, lds, s, a);
     hipError_t e = hipGetLastError();
-    if (e != hipSuccess || splits == 1)
-        return e;
-    hipLaunchKernelGGL(k_add_parts, dim3((unsigned)std::min<int64_t>((a.size + kThreads - 1) / kThreads, 4096)), block, 0,
-                       s, out, b.outer, a.size, splits);
-    return hipGetLastError();
-}
-
-hipError_t launch_transpose(const Sizes &z, const Forward &f, const uint16_t *in, int64_t P, int64_t Q, uint16_t *out,
-                            int64_t ldo, hipStream_t s)
-{
-    const TransposeArgs a{in, out, f.offsets, ldo, (int)P, (int)Q};
-    hipLaunchKernelGGL(k_transpose, dim3((unsigned)((Q + 63) / 64), (unsigned)((ldo + 63) / 64), (unsigned)z.L),
-                       dim3(kThreads), 0, s, a);
-    return hipGetLastError();
-}
-
-hipError_t launch_factors(const Sizes &z, const Backward &b, const float *part, int splits, const float *scale,
-                          uint16_t *pieces, hipStream_t s)
-{
-    const FactorArgs a{part, scale, b.f.offsets, pieces, b.places, (int)z.T, (int)z.L, (int)z.Rp, splits};
-    hipLaunchKernelGGL(k_factors, dim3((unsigned)(b.places / 64), (unsigned)z.rb), dim3(kThreads), 0, s, a);
-    return hipGetLastError();
+    for (int j = 0; j < 2 && e == hipSuccess; ++j) {
+        const OuterJob &o = a.job[j];
+        if (o.splits == 1)
+            continue;
+        hipLaunchKernelGGL(k_add_parts, dim3((unsigned)std::min<int64_t>((o.size + kThreads - 1) / kThreads, 4096)),
+                           dim3(kThreads), 0, s, j ? db : da, o.out, o.size, o.splits);
+        e = hipGetLastError();
+    }
+    return e;
 }
 
 }  // namespace
@@ -772,7 +943,7 @@ size_t qlin_lora_workspace_size(int64_t tokens, int64_t K, int64_t N, int64_t ra
 {
     if (!good_shape(tokens, K, N, rank, adapters) || tokens == 0)
         return 0;
-    return forward_space(sizes(tokens, K, N, rank, adapters), nullptr).bytes;
+    return space(sizes(tokens, K, N, rank, adapters), nullptr, false).bytes;
 }
 
 qlin_status qlin_lora_mm(int32_t id_bits, int64_t tokens, int64_t K, int64_t N, int64_t rank, int64_t adapters,
@@ -794,13 +965,18 @@ qlin_status qlin_lora_mm(int32_t id_bits, int64_t tokens, int64_t K, int64_t N, 
         !aligned(ids, id_bits / 8) || !aligned(scale, 4) || !aligned(workspace, 16))
         return QLIN_ERR_MISALIGNED;
     const Sizes z = sizes(tokens, K, N, rank, adapters);
-    const Forward f = forward_space(z, workspace);
+    const Space f = space(z, workspace, false);
     if (!workspace || workspace_bytes < f.bytes)
         return QLIN_ERR_WORKSPACE;
     hipStream_t s = static_cast<hipStream_t>(stream);
-    if (launch_plan(z, f, ids, id_bits, s) != hipSuccess ||
-        launch_shrink(z, f, X, ldx, A, K, K, f.part, s) != hipSuccess ||
-        launch_expand(z, f, f.part, shrink_splits(z, K), scale, B, N, base, ldb, Y, ldy, s) != hipSuccess)
+    ShrinkArgs a{};
+    a.job[0] = ShrinkJob{X, A, f.rows, nullptr, ldx, (int)K};
+    a.scale = scale;
+    a.R = (int)rank;
+    a.Rp = (int)z.Rp;
+    a.groups = z.groups;
+    if (make_plan(z, f, ids, id_bits, a, s) != hipSuccess || launch_shrink<false>(z, a, s) != hipSuccess ||
+        launch_expand<false>(z, f, B, N, base, ldb, Y, ldy, s) != hipSuccess)
         return QLIN_ERR_HIP;
     return QLIN_OK;
 }
@@ -809,7 +985,7 @@ size_t qlin_lora_backward_workspace_size(int64_t tokens, int64_t K, int64_t N, i
 {
     if (!good_shape(tokens, K, N, rank, adapters) || N == 0)
         return 0;
-    return backward_space(sizes(tokens, K, N, rank, adapters), nullptr).bytes;
+    return space(sizes(tokens, K, N, rank, adapters), nullptr, true).bytes;
 }
 
 qlin_status qlin_lora_mm_backward(int32_t id_bits, int64_t tokens, int64_t K, int64_t N, int64_t rank, int64_t adapters,
@@ -831,25 +1007,24 @@ qlin_status qlin_lora_mm_backward(int32_t id_bits, int64_t tokens, int64_t K, in
         !aligned(dA, 4) || !aligned(dB, 4) || !aligned(ids, id_bits / 8) || !aligned(scale, 4) || !aligned(workspace, 16))
         return QLIN_ERR_MISALIGNED;
     const Sizes z = sizes(tokens, K, N, rank, adapters);
-    const Backward b = backward_space(z, workspace);
-    if (!workspace || workspace_bytes < b.bytes)
+    const Space f = space(z, workspace, true);
+    if (!workspace || workspace_bytes < f.bytes)
         return QLIN_ERR_WORKSPACE;
     hipStream_t s = static_cast<hipStream_t>(stream);
-    if (launch_plan(z, b.f, ids, id_bits, s) != hipSuccess)
+    ShrinkArgs a{};
+    a.job[0] = ShrinkJob{X, A, nullptr, f.fv, ldx, (int)K};
+    a.job[1] = ShrinkJob{dY, B, f.rows, f.fu, lddy, (int)N};
+    a.scale = scale;
+    a.places = f.places;
+    a.R = (int)rank;
+    a.Rp = (int)z.Rp;
+    a.groups = z.groups;
+    if (make_plan(z, f, ids, id_bits, a, s) != hipSuccess)
         return QLIN_ERR_HIP;
-    if (tokens > 0) {
-        const int sv = shrink_splits(z, K), su = shrink_splits(z, N);
-        if (launch_transpose(z, b.f, A, rank, K, b.at, rank, s) != hipSuccess ||
-            launch_transpose(z, b.f, B, N, rank, b.bt, b.ldbt, s) != hipSuccess ||
-            launch_shrink(z, b.f, X, ldx, A, K, K, b.f.part, s) != hipSuccess ||
-            launch_shrink(z, b.f, dY, lddy, b.bt, b.ldbt, N, b.u, s) != hipSuccess ||
-            launch_factors(z, b, b.f.part, sv, scale, b.fv, s) != hipSuccess ||
-            launch_factors(z, b, b.u, su, scale, b.fu, s) != hipSuccess ||
-            launch_expand(z, b.f, b.u, su, scale, b.at, K, base, ldb, dX, lddx, s) != hipSuccess)
-            return QLIN_ERR_HIP;
-    }
-    if (launch_outer(z, b, X, ldx, K, b.fu, false, dA, s) != hipSuccess ||
-        launch_outer(z, b, dY, lddy, N, b.fv, true, dB, s) != hipSuccess)
+    if (tokens > 0 && (launch_shrink<true>(z, a, s) != hipSuccess ||
+                       launch_expand<true>(z, f, A, K, base, ldb, dX, lddx, s) != hipSuccess))
+        return QLIN_ERR_HIP;
+    if (launch_outer(z, f, X, ldx, dY, lddy, dA, dB, s) != hipSuccess)
         return QLIN_ERR_HIP;
     return QLIN_OK;
 }

@@ -65,6 +65,8 @@ SHAPES = [
     (333, 1032, 1001, 8, 3, None, 32), (257, 255, 300, 16, 1, [0], 32), (300, 256, 511, 32, 2, "runs", 64),
     (130, 384, 640, 64, 1, [0], 32), (1100, 200, 136, 16, 5, "runs", 32), (1500, 72, 264, 32, 300, None, 32),
     (2100, 520, 130, 8, 2, [0, -1], 32), (4001, 96, 120, 48, 6, "runs", 64), (600, 64, 200, 128, 3, None, 32),
+    (7700, 72, 40, 16, 2, "runs", 32), (8193, 40, 72, 40, 9, None, 64), (16000, 40, 72, 24, 3, None, 32),
+    (15500, 66, 48, 64, 1, [0], 32), (20000, 24, 16, 8, 2000, None, 32),
 ]
 
 
