@@ -58,6 +58,20 @@ __device__ inline v4i load8(const uint16_t *p, int n)
     return v;
 }
 
+__device__ inline void store8(uint16_t *p, v4i v, int n)
+{
+    if (n >= 8) {
+        __builtin_memcpy(p, &v, 16);
+        return;
+    }
+    uint16_t t[8];
+    __builtin_memcpy(t, &v, 16);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (i < n)
+            p[i] = t[i];
+}
+
 // The upper 16 bits of v as a float, and what is left of it (an infinity leaves nothing).
 __device__ inline float cut(float v) { return __uint_as_float(__float_as_uint(v) & 0xFFFF0000u); }
 __device__ inline float rest(float v, float c) { return fabsf(c) < INFINITY ? v - c : 0.0f; }
@@ -166,10 +180,45 @@ __global__ void __launch_bounds__(kPlanThreads) k_plan(Plan p)
     }
 }
 
-// Few tokens: every workgroup of the shrink kernel finds its own tile, which takes it less time than a launch
-// of its own would take the call.  A wave owns a contiguous part of the tokens and keeps their bins.
-constexpr int kShrinkWaves = 8, kShrinkThreads = 64 * kShrinkWaves, kHold = 16;
-constexpr int kSelfTokens = kShrinkThreads * kHold;
+// Up to 64 tokens: every wave of the shrink kernel finds its tile by itself, without LDS or a barrier.  `token`
+// becomes the token at the lane's place.
+constexpr int kWaveTokens = 64;
+
+__device__ inline int4 wave_plan(const Plan &p, int want, int &token)
+{
+    const int lane = threadIdx.x & 63;
+    const int bin = lane < p.tokens ? bin_of(p, lane) : kBins;
+    int place = 0;
+    for (int j = 0; j < p.tokens; ++j) {
+        const int o = __builtin_amdgcn_readlane(bin, j);
+        place += o < bin || (o == bin && j < lane) ? 1 : 0;
+    }
+    token = __builtin_amdgcn_ds_permute(4 * place, lane);
+    const int sorted = __builtin_amdgcn_ds_permute(4 * place, bin);
+    const int ahead = __shfl_up(sorted, 1);                 // (by all lanes)
+    const bool there = lane < p.tokens, starts = there && (lane == 0 || ahead != sorted);
+    const uint64_t firsts = __ballot(starts), low = ((uint64_t)2 << lane) - 1;
+    const int first = 63 - __clzll((long long)(firsts & low));
+    const uint64_t heads = __ballot(there && (lane - first) % p.tile == 0);
+    const uint64_t mine = __ballot(((heads >> lane) & 1) && __popcll(heads & (low >> 1)) == want);
+    if (want == 0 && p.offsets)
+        for (int b = threadIdx.x; b <= p.adapters; b += blockDim.x) {
+            int n = 0;
+            for (int j = 0; j < p.tokens; ++j) n += __builtin_amdgcn_readlane(bin, j) < b ? 1 : 0;
+            p.offsets[b] = n;
+        }
+    if (!mine)
+        return make_int4(-1, 0, 0, 0);
+    const int at = __ffsll((unsigned long long)mine) - 1, begin = __builtin_amdgcn_readlane(first, at);
+    const uint64_t later = firsts & ~(((uint64_t)2 << begin) - 1);
+    const int end = later ? __ffsll((unsigned long long)later) - 1 : p.tokens;
+    return tile_of(p, __builtin_amdgcn_readlane(sorted, at), begin, end - begin, (at - begin) / p.tile);
+}
+
+// Up to 8192: every workgroup of the shrink kernel finds its tile, which takes it less time than a launch of its
+// own would take the call.  A wave owns a contiguous part of the tokens and keeps their bins.
+constexpr int kShrinkWaves = 16, kHold = 16;
+constexpr int kSelfTokens = 64 * 8 * kHold;
 
 struct PlanShare {
     int32_t sums[2][kShrinkWaves];
@@ -181,12 +230,12 @@ struct PlanShare {
 // The tile `want`, its tokens in sh.token; `hist` [adapters + 1].  Called by all threads.
 __device__ inline int4 self_plan(const Plan &p, int want, int32_t *hist, PlanShare &sh)
 {
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, bins = p.adapters + 1;
-    const int turns = (p.tokens + kShrinkThreads - 1) / kShrinkThreads, beg = wave * turns * 64 + lane;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, threads = blockDim.x, bins = p.adapters + 1;
+    const int turns = (p.tokens + threads - 1) / threads, beg = wave * turns * 64 + lane;
     int held[kHold];
 #pragma unroll
     for (int h = 0; h < kHold; ++h) held[h] = h < turns && beg + 64 * h < p.tokens ? bin_of(p, beg + 64 * h) : -1;
-    for (int b = tid; b < bins; b += kShrinkThreads) hist[b] = 0;
+    for (int b = tid; b < bins; b += threads) hist[b] = 0;
     if (tid == 0) {
         sh.tile = make_int4(-1, 0, 0, 0);
         sh.bin = -1;
@@ -194,6 +243,8 @@ __device__ inline int4 self_plan(const Plan &p, int want, int32_t *hist, PlanSha
     __syncthreads();
 #pragma unroll
     for (int h = 0; h < kHold; ++h) {
+        if (h >= turns)
+            break;
         const uint64_t any = __ballot(held[h] >= 0);
         if (!any)
             continue;
@@ -206,7 +257,7 @@ __device__ inline int4 self_plan(const Plan &p, int want, int32_t *hist, PlanSha
         }
     }
     __syncthreads();
-    const int each = (bins + kShrinkThreads - 1) / kShrinkThreads;
+    const int each = (bins + threads - 1) / threads;
     const int b0 = min(tid * each, bins), b1 = min(b0 + each, bins);
     int tokens = 0, tiles = 0;
     for (int b = b0; b < b1; ++b) {
@@ -243,20 +294,27 @@ __device__ inline int4 self_plan(const Plan &p, int want, int32_t *hist, PlanSha
         return found;
     int before = 0;
 #pragma unroll
-    for (int h = 0; h < kHold; ++h) before += __popcll(__ballot(held[h] == bin));
+    for (int h = 0; h < kHold; ++h) {
+        if (h >= turns)
+            break;
+        before += __popcll(__ballot(held[h] == bin));
+    }
     if (lane == 0)
         sh.sums[0][wave] = before;
     __syncthreads();
     int rank = -skip;
     for (int w = 0; w < wave; ++w) rank += sh.sums[0][w];
+    if (rank < found.z && rank + before > 0)
 #pragma unroll
-    for (int h = 0; h < kHold; ++h) {
-        const uint64_t mine = __ballot(held[h] == bin);
-        const int r = rank + __popcll(mine & (((uint64_t)1 << lane) - 1));
-        if (held[h] == bin && r >= 0 && r < found.z)
-            sh.token[r] = beg + 64 * h;
-        rank += __popcll(mine);
-    }
+        for (int h = 0; h < kHold; ++h) {
+            if (h >= turns)
+                break;
+            const uint64_t mine = __ballot(held[h] == bin);
+            const int r = rank + __popcll(mine & (((uint64_t)1 << lane) - 1));
+            if (held[h] == bin && r >= 0 && r < found.z)
+                sh.token[r] = beg + 64 * h;
+            rank += __popcll(mine);
+        }
     __syncthreads();
     return found;
 }
@@ -272,7 +330,7 @@ constexpr int kStep = 64;
 struct ShrinkJob {
     const uint16_t *x, *w;
     uint16_t *rows;            // [tokens][2][Rp]: two pieces, or NULL
-    uint16_t *pieces;          // [3][Rp][places]: three pieces, or NULL
+    uint16_t *pieces;          // [place / 8][3][Rp][8]: three pieces, or NULL
     int64_t ldx;
     int K;
 };
@@ -281,98 +339,153 @@ struct ShrinkArgs {
     ShrinkJob job[2];          // v; u
     Plan plan;
     const float *scale;
-    int64_t places;
-    int R, Rp, groups, self;   // groups of 16 RB ranks; self: the workgroups make the plan
+    int R, Rp, groups, self;   // groups of 16 RB ranks; self: waves (1) or workgroups (2) make the plan
 };
 
-template <int TB, int RB> constexpr int steps_at_once() { return TB * RB == 1 ? 4 : TB + RB <= 5 ? 2 : 1; }
+// Waves of a workgroup at most (what registers allow), and steps whose loads a wave has in flight.
+template <int TB, int RB> constexpr int shrink_waves() { return TB * RB <= 2 ? 16 : 8; }
+template <int TB, int RB> constexpr int steps_at_once() { return TB * RB == 1 ? 5 : TB + RB <= 3 ? 3 : TB + RB <= 5 ? 2 : 1; }
 
-template <int TB>
-__device__ inline void load_steps(v4i (&x)[TB][2], const uint16_t *const (&px)[TB], int k, int K, int q)
+// A step's rows: eight lanes load 128 bytes of one, so that a load instruction touches eight lines (with a row
+// for each lane of sixteen, as the matrix cores want them, it touches 64: 32 tokens of 32 requests on K = 5120
+// took 12.4 us).  The wave's LDS brings them to the matrix cores' order; piece j of a row lies at j ^ row, which
+// keeps both directions free of bank conflicts.
+template <int B>
+__device__ inline void load_rows(v4i (&v)[B][2], const uint16_t *const (&p)[B][2], int k, int K)
 {
     if (k + kStep <= K) {
 #pragma unroll
-        for (int t = 0; t < TB; ++t) {
-            x[t][0] = load8(px[t] + k);
-            x[t][1] = load8(px[t] + k + 32);
+        for (int b = 0; b < B; ++b) {
+            v[b][0] = load8(p[b][0] + k);
+            v[b][1] = load8(p[b][1] + k);
         }
     } else {
-        const int left = K - (k + 8 * q);
+        const int left = K - (k + 8 * (threadIdx.x & 7));
 #pragma unroll
-        for (int t = 0; t < TB; ++t) {
-            x[t][0] = load8(px[t] + k, left);
-            x[t][1] = load8(px[t] + k + 32, left - 32);
+        for (int b = 0; b < B; ++b) {
+            v[b][0] = load8(p[b][0] + k, left);
+            v[b][1] = load8(p[b][1] + k, left);
         }
     }
 }
 
-template <int TB, int RB, bool BACK>
-__global__ void __launch_bounds__(kShrinkThreads) k_shrink(ShrinkArgs a)
+template <int B>
+__device__ inline void store_rows(v4i *lds, const v4i (&v)[B][2])
 {
-    // a wave's share: its steps' weights, then its sums
-    constexpr int kShare = BACK && TB < 2 ? 2 * RB * 64 : TB * RB * 64;            // 16-byte pieces
-    constexpr int kHist = (kBins + 3) / 4;
-    __shared__ v4i space[kShrinkWaves * kShare > kHist ? kShrinkWaves * kShare : kHist];
+    const int lane = threadIdx.x & 63, row = lane >> 3, at = 8 * row + ((lane & 7) ^ row);
+#pragma unroll
+    for (int b = 0; b < B; ++b) {
+        lds[128 * b + at] = v[b][0];
+        lds[128 * b + 64 + at] = v[b][1];
+    }
+}
+
+// Row l % 16 of block b, the half's eight k of the lane's quarter.
+__device__ inline v4i row_part(const v4i *lds, int b, int half)
+{
+    const int lane = threadIdx.x & 63, i = lane & 15;
+    return lds[128 * b + 8 * i + ((4 * half + (lane >> 4)) ^ (i & 7))];
+}
+
+// Where the pieces of adapter l's places begin, or of a tile of it (tiles have whole sixteens before them): at
+// eights, so that no two adapters share one, whatever their numbers of tokens.
+__host__ __device__ inline int64_t piece_place(int64_t place, int l) { return (place + 7) / 8 * 8 + 8 * (int64_t)l; }
+
+constexpr int shrink_share(int tb, int rb) { return tb * rb > 2 * (tb + rb) ? tb * rb * 64 : 2 * (tb + rb) * 64; }
+
+template <int TB, int RB, bool BACK>
+__global__ void __launch_bounds__((64 * shrink_waves<TB, RB>())) k_shrink(ShrinkArgs a)
+{
+    // a wave's share: a step's rows and weights, then its sums (16-byte pieces)
+    constexpr int kShare = shrink_share(TB, RB);
+    extern __shared__ v4i shared[];             // [waves][kShare], before that the plan's bins
     __shared__ PlanShare sh;
     const int units = a.plan.max_tiles * a.groups;
-    const int second = BACK && (int)blockIdx.x >= units;
+    // (the longer job's workgroups come first)
+    const int later = BACK && (int)blockIdx.x >= units, second = BACK && later != (a.job[1].K > a.job[0].K);
     const ShrinkJob &job = a.job[second];
-    const int unit = (int)blockIdx.x - (second ? units : 0), index = unit / a.groups, group = unit % a.groups;
+    const int unit = (int)blockIdx.x - (later ? units : 0), index = unit / a.groups, group = unit % a.groups;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, i = lane & 15, q = lane >> 4;
+    const int waves = blockDim.x >> 6;
     int4 tile;
-    if (a.self) {
-        tile = self_plan(a.plan, index, reinterpret_cast<int32_t *>(space), sh);
-        if (group == 0 && !second) {
-            if (tid == 0)
-                a.plan.tiles[index] = tile;
-            if (tid < tile.z)
-                a.plan.order[tile.y + tid] = sh.token[tid];
-        }
+    int token[TB];
+    if (a.self == 1) {
+        int sorted;
+        tile = wave_plan(a.plan, index, sorted);
+#pragma unroll
+        for (int t = 0; t < TB; ++t) token[t] = __shfl(sorted, tile.y + min(16 * t + i, tile.z - 1));
+        const int there = __shfl(sorted, (tile.y + lane) & 63);          // (by all lanes)
+        if (group == 0 && !second && wave == 0 && lane < tile.z)
+            a.plan.order[tile.y + lane] = there;
     } else {
-        tile = a.plan.tiles[index];
-        if (tid < tile.z)
-            sh.token[tid] = a.plan.order[tile.y + tid];
-        __syncthreads();
+        if (a.self) {
+            tile = self_plan(a.plan, index, reinterpret_cast<int32_t *>(shared), sh);
+            if (group == 0 && !second && tid < tile.z)
+                a.plan.order[tile.y + tid] = sh.token[tid];
+#pragma unroll
+            for (int t = 0; t < TB; ++t) token[t] = tile.z ? sh.token[min(16 * t + i, tile.z - 1)] : 0;
+        } else {
+            tile = a.plan.tiles[index];
+#pragma unroll
+            for (int t = 0; t < TB; ++t) token[t] = tile.z ? a.plan.order[tile.y + min(16 * t + i, tile.z - 1)] : 0;
+        }
     }
+    if (a.self && group == 0 && !second && tid == 0)
+        a.plan.tiles[index] = tile;
     if (tile.x < 0 || tile.z == 0)
         return;
-    const uint16_t *px[TB];
+    const uint16_t *px[TB][2];                 // rows l / 8 and 8 behind of each block
 #pragma unroll
-    for (int t = 0; t < TB; ++t) px[t] = job.x + sh.token[min(16 * t + i, tile.z - 1)] * job.ldx + 8 * q;
+    for (int t = 0; t < TB; ++t)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            px[t][h] = job.x + __shfl(token[t], 8 * h + (lane >> 3)) * job.ldx + 8 * (lane & 7);
     v4f acc[TB][RB] = {};
     const int steps = (job.K + kStep - 1) / kStep, r0 = 16 * RB * group;
+    v4i *const mine = shared + wave * kShare, *const weights = mine + TB * 128;
     if (!BACK || !second) {
         constexpr int U = steps_at_once<TB, RB>();
-        const uint16_t *pw[RB];                // (ranks behind R take the last one's row: their sums are not read)
+        const uint16_t *pw[RB][2];             // (ranks behind R take the last one's row: their sums are not read)
 #pragma unroll
-        for (int r = 0; r < RB; ++r) pw[r] = job.w + ((int64_t)tile.x * a.R + min(r0 + 16 * r + i, a.R - 1)) * job.K + 8 * q;
-        for (int s = wave; s < steps; s += kShrinkWaves * U) {
+        for (int r = 0; r < RB; ++r)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                pw[r][h] = job.w + ((int64_t)tile.x * a.R + min(r0 + 16 * r + 8 * h + (lane >> 3), a.R - 1)) * job.K +
+                           8 * (lane & 7);
+        for (int s = wave * U; s < steps; s += waves * U) {
             v4i x[U][TB][2], w[U][RB][2];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int k = (s + kShrinkWaves * u) * kStep;
-                if (u > 0 && k >= job.K)
+                if (u > 0 && s + u >= steps)
                     break;
-                load_steps(x[u], px, k, job.K, q);
-                load_steps(w[u], pw, k, job.K, q);
+                load_rows(x[u], px, (s + u) * kStep, job.K);
+                load_rows(w[u], pw, (s + u) * kStep, job.K);
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                if (u > 0 && (s + kShrinkWaves * u) * kStep >= job.K)
+                if (u > 0 && s + u >= steps)
                     break;
+                store_rows(mine, x[u]);
+                store_rows(weights, w[u]);
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
+                for (int h = 0; h < 2; ++h) {
+                    v4i f[RB];
 #pragma unroll
-                    for (int t = 0; t < TB; ++t)
+                    for (int r = 0; r < RB; ++r) f[r] = row_part(weights, r, h);
 #pragma unroll
-                        for (int r = 0; r < RB; ++r) acc[t][r] = mma(x[u][t][h], w[u][r][h], acc[t][r]);
+                    for (int t = 0; t < TB; ++t) {
+                        const v4i y = row_part(mine, t, h);
+#pragma unroll
+                        for (int r = 0; r < RB; ++r) acc[t][r] = mma(y, f[r], acc[t][r]);
+                    }
+                }
             }
         }
     } else {
         // 64 rows of up to 2 RB chunks of 8 ranks a step, one row after another
         const int chunks = min(2 * RB, a.R / 8 - r0 / 8);
         const uint16_t *w = job.w + (int64_t)tile.x * job.K * a.R + r0;
-        uint16_t *mine = reinterpret_cast<uint16_t *>(space + wave * kShare);
+        uint16_t *const wl = reinterpret_cast<uint16_t *>(weights);
         int row[2 * RB], rank[2 * RB];
 #pragma unroll
         for (int h = 0; h < 2 * RB; ++h) {
@@ -381,7 +494,7 @@ __global__ void __launch_bounds__(kShrinkThreads) k_shrink(ShrinkArgs a)
         }
         v4i x[TB][2], b[2 * RB];
         const auto load = [&](int s) {
-            load_steps(x, px, s * kStep, job.K, q);
+            load_rows(x, px, s * kStep, job.K);
 #pragma unroll
             for (int h = 0; h < 2 * RB; ++h) {
                 b[h] = v4i{0, 0, 0, 0};
@@ -391,58 +504,55 @@ __global__ void __launch_bounds__(kShrinkThreads) k_shrink(ShrinkArgs a)
         };
         if (wave < steps)
             load(wave);
-        for (int s = wave; s < steps; s += kShrinkWaves) {
-            v4i y[TB][2];
-#pragma unroll
-            for (int t = 0; t < TB; ++t) {
-                y[t][0] = x[t][0];
-                y[t][1] = x[t][1];
-            }
+        for (int s = wave; s < steps; s += waves) {
+            store_rows(mine, x);
 #pragma unroll
             for (int h = 0; h < 2 * RB; ++h)
                 if (row[h] < kStep)
-                    *reinterpret_cast<v4i *>(mine + row[h] * (16 * RB) + rank[h]) = b[h];
-            if (s + kShrinkWaves < steps)
-                load(s + kShrinkWaves);
+                    *reinterpret_cast<v4i *>(wl + row[h] * (16 * RB) + rank[h]) = b[h];
+            if (s + waves < steps)
+                load(s + waves);
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+            for (int h = 0; h < 2; ++h) {
+                v4i f[RB];
 #pragma unroll
-                for (int r = 0; r < RB; ++r) {
-                    v4i f;
+                for (int r = 0; r < RB; ++r)
 #pragma unroll
                     for (int g = 0; g < 2; ++g) {
                         // sixteen lanes load four rows of sixteen ranks, and get a column each
                         typedef short v4s __attribute__((ext_vector_type(4)));
-                        uint16_t *p = mine + (32 * h + 8 * q + 4 * g + (i >> 2)) * (16 * RB) + 16 * r + 4 * (i & 3);
+                        uint16_t *p = wl + (32 * h + 8 * q + 4 * g + (i >> 2)) * (16 * RB) + 16 * r + 4 * (i & 3);
                         const v4s v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s *)p);
                         const int2 d = __builtin_bit_cast(int2, v);
-                        f[2 * g] = d.x;
-                        f[2 * g + 1] = d.y;
+                        f[r][2 * g] = d.x;
+                        f[r][2 * g + 1] = d.y;
                     }
 #pragma unroll
-                    for (int t = 0; t < TB; ++t) acc[t][r] = mma(y[t][h], f, acc[t][r]);
+                for (int t = 0; t < TB; ++t) {
+                    const v4i y = row_part(mine, t, h);
+#pragma unroll
+                    for (int r = 0; r < RB; ++r) acc[t][r] = mma(y, f[r], acc[t][r]);
                 }
+            }
         }
     }
     __syncthreads();                           // (another wave may still read its weights where sums go)
-    v4f *sums = reinterpret_cast<v4f *>(space);
+    v4f *sums = reinterpret_cast<v4f *>(shared);
 #pragma unroll
     for (int t = 0; t < TB; ++t)
 #pragma unroll
         for (int r = 0; r < RB; ++r) sums[(wave * TB * RB + t * RB + r) * 64 + lane] = acc[t][r];
     __syncthreads();
     const float s = a.scale ? a.scale[tile.x] : 1.0f;
-    for (int e = tid; e < TB * RB * 64; e += kShrinkThreads) {
+    for (int e = tid; e < TB * RB * 64; e += (int)blockDim.x) {
         v4f v = sums[e];
-        for (int w = 1; w < kShrinkWaves; ++w) v += sums[w * TB * RB * 64 + e];
+        for (int w = 1; w < waves; ++w) v += sums[w * TB * RB * 64 + e];
         const int block = e >> 6, rank = r0 + 16 * (block % RB) + (e & 15), at = 16 * (block / RB) + 4 * ((e >> 4) & 3);
         const int n = tile.z - at;             // of the four places from there
-        if (n <= 0)
-            continue;
         uint16_t o[3][4];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-            const float f = v[c] * s, h = cut(f), m = rest(f, h), mh = cut(m);
+            const float f = c < n ? v[c] * s : 0.0f, h = cut(f), m = rest(f, h), mh = cut(m);
             o[0][c] = bf16_bits(h);
             o[1][c] = bf16_bits(mh);
             o[2][c] = bf16_bits(rest(m, mh));
@@ -452,28 +562,23 @@ __global__ void __launch_bounds__(kShrinkThreads) k_shrink(ShrinkArgs a)
                 p[a.Rp] = bf16_bits(m);
             }
         }
-        if (BACK && job.pieces)
+        if (BACK && job.pieces && (at & ~7) < tile.z) {     // (zeros fill the last eight)
+            const int64_t eight = piece_place(tile.y, tile.x) / 8 + at / 8;
 #pragma unroll
-            for (int h = 0; h < 3; ++h) {
-                uint16_t *p = job.pieces + ((int64_t)h * a.Rp + rank) * a.places + tile.y + at;
-                if (n >= 4) {
-                    __builtin_memcpy(p, o[h], 8);
-                } else {
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        if (c < n)
-                            p[c] = o[h][c];
-                }
-            }
+            for (int h = 0; h < 3; ++h)
+                __builtin_memcpy(job.pieces + ((eight * 3 + h) * a.Rp + rank) * 8 + (at & 4), o[h], 8);
+        }
     }
 }
 
 // ---------------------------------------------------------------------------
 // Expand: out[token,n] = bf16(base[token,n] + sum_r (s v)[place,r] w[adapter,n,r]), or with the weights as
-// [adapter][r][n] (dx).  A wave takes 64 n at a time as four products of 16, dealt to them so that a lane ends
-// with twice eight n in a row of its token, and four lanes with 64 bytes of it.
+// [adapter][r][n] (dx).  Two kernels: where an adapter has few tokens its weights are what is read, and a wave
+// takes them straight into registers; where it has many, base and out are, and the waves of a workgroup, 16
+// tokens each, share the weights in LDS.
 // ---------------------------------------------------------------------------
 constexpr int kThreads = 256, kWaves = kThreads / 64;
+constexpr int kWide = 16 * kWaves;             // tokens of a workgroup of the second kernel
 
 struct ExpandArgs {
     const uint16_t *rows;      // [tokens][2][Rp]: s v
@@ -485,9 +590,28 @@ struct ExpandArgs {
     int N, R, Rp, chunks;
 };
 
-// G groups of 32 ranks; PACK: at most 16 ranks, both pieces of v in one product; TR: weights [r][n].
-template <int TB, int G, bool PACK, bool TR>
-__global__ void __launch_bounds__(kThreads) k_expand(ExpandArgs a)
+// The pieces of s v as operands: chunk 4 g + q of 8 ranks; PACK (16 ranks at most): both pieces in one product.
+template <int G, bool PACK>
+__device__ inline void load_factors(v4i (&hi)[G], v4i (&lo)[G], const ExpandArgs &a, int place)
+{
+    const int q = (threadIdx.x & 63) >> 4, ranks = a.R / 8;
+    const uint16_t *v = a.rows + (int64_t)place * 2 * a.Rp;
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+        const int c = PACK ? q % ranks : 4 * g + q, piece = PACK ? q / ranks : 0;
+        hi[g] = lo[g] = v4i{0, 0, 0, 0};
+        if (c < ranks && piece < 2)
+            hi[g] = load8(v + piece * a.Rp + 8 * c);
+        if (!PACK && c < ranks)
+            lo[g] = load8(v + a.Rp + 8 * c);
+    }
+}
+
+// 64 n a wave at a time as four products of 16 n by 16 tokens, dealt to them so that a lane ends with twice eight n
+// in a row of its token, and four lanes with 64 bytes of it.  Weights' bytes bound it: 128 tokens of 24 adapters
+// of 64 ranks on N = 51200, 183 MB, 37 us, 5.0 TB/s.
+template <int G, bool PACK, bool TR>
+__global__ void __launch_bounds__(kThreads) k_expand_few(ExpandArgs a)
 {
     const int4 tile = a.tiles[blockIdx.x / a.chunks];
     const int chunk = blockIdx.x % a.chunks;
@@ -496,56 +620,24 @@ __global__ void __launch_bounds__(kThreads) k_expand(ExpandArgs a)
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = lane & 15, q = lane >> 4;
     const int ranks = a.R / 8;                 // chunks of 8 ranks
     const bool live = tile.x >= 0;
-    int64_t token[TB];
-#pragma unroll
-    for (int t = 0; t < TB; ++t) token[t] = a.order[tile.y + min(16 * t + i, tile.w - 1)];
-    v4i hi[TB][G], lo[TB][PACK ? 1 : G];
+    const int64_t token = a.order[tile.y + min(i, tile.w - 1)];
+    v4i hi[G], lo[G];
     const uint16_t *w = a.w + (int64_t)(live ? tile.x : 0) * a.N * a.R;
     if (live)
-#pragma unroll
-        for (int t = 0; t < TB; ++t) {
-            const uint16_t *v = a.rows + (int64_t)(tile.y + min(16 * t + i, tile.w - 1)) * 2 * a.Rp;
-#pragma unroll
-            for (int g = 0; g < G; ++g) {
-                const int c = PACK ? q % ranks : 4 * g + q, piece = PACK ? q / ranks : 0;
-                hi[t][g] = v4i{0, 0, 0, 0};
-                if (c < ranks && piece < 2)
-                    hi[t][g] = load8(v + piece * a.Rp + 8 * c);
-                if (!PACK) {
-                    lo[t][PACK ? 0 : g] = v4i{0, 0, 0, 0};
-                    if (c < ranks)
-                        lo[t][PACK ? 0 : g] = load8(v + a.Rp + 8 * c);
-                }
-            }
-        }
+        load_factors<G, PACK>(hi, lo, a, tile.y + min(i, tile.w - 1));
     const int blocks = (a.N + 63) / 64;
     for (int b = chunk * kWaves + wave; b < blocks; b += a.chunks * kWaves) {
         const int n0 = 64 * b;
         // this lane's outputs: n0 + 8 q .. + 7 and 32 behind
         const int left = a.N - (n0 + 8 * q);
-        int o[TB][8];
-        if (a.base)
-#pragma unroll
-            for (int t = 0; t < TB; ++t) {
-                v4i o0{0, 0, 0, 0}, o1{0, 0, 0, 0};
-                if (16 * t + i < tile.w) {
-                    const uint16_t *p = a.base + token[t] * a.ldb + n0 + 8 * q;
-                    o0 = load8(p, left);
-                    o1 = load8(p + 32, left - 32);
-                }
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    o[t][e] = o0[e];
-                    o[t][4 + e] = o1[e];
-                }
-            }
-        else
-#pragma unroll
-            for (int t = 0; t < TB; ++t)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) o[t][e] = 0;
-        v4i f[4][G];
+        v4i o[2] = {};
+        if (a.base && i < tile.w) {
+            const uint16_t *p = a.base + token * a.ldb + n0 + 8 * q;
+            o[0] = load8(p, left);
+            o[1] = load8(p + 32, left - 32);
+        }
         if (live) {
+            v4i f[4][G];
             if (TR) {
                 // rows of eight ranks, four n of each: the lane's row 4 a + c of product m is
                 // n = 32 (c / 2) + 8 a + 4 (c % 2) + m
@@ -591,45 +683,122 @@ __global__ void __launch_bounds__(kThreads) k_expand(ExpandArgs a)
                     }
                 }
             }
-        }
+            v4f acc[4] = {};
 #pragma unroll
-        for (int t = 0; t < TB; ++t) {
-            if (live) {
-                v4f acc[4] = {};
+            for (int j = 0; j < 4; ++j)
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-#pragma unroll
-                    for (int g = 0; g < G; ++g) {
-                        acc[j] = mma(f[j][g], hi[t][g], acc[j]);
-                        if (!PACK)
-                            acc[j] = mma(f[j][g], lo[t][PACK ? 0 : g], acc[j]);
-                    }
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float d0 = TR ? acc[(2 * e) % 4][e / 2] : acc[e / 2][(2 * e) % 4];
-                    const float d1 = TR ? acc[(2 * e + 1) % 4][e / 2] : acc[e / 2][(2 * e + 1) % 4];
-                    const uint32_t d = (uint32_t)o[t][e];
-                    o[t][e] = pack2(__uint_as_float(d << 16) + d0, __uint_as_float(d & 0xFFFF0000u) + d1);
+                for (int g = 0; g < G; ++g) {
+                    acc[j] = mma(f[j][g], hi[g], acc[j]);
+                    if (!PACK)
+                        acc[j] = mma(f[j][g], lo[g], acc[j]);
                 }
-            }
-            if (16 * t + i >= tile.w || left <= 0)
-                continue;
-            uint16_t *p = a.out + token[t] * a.ldo + n0 + 8 * q;
-            if (left >= 40) {
-                __builtin_memcpy(p, &o[t][0], 16);
-                __builtin_memcpy(p + 32, &o[t][4], 16);
-            } else {
-                uint16_t v[16];
-                __builtin_memcpy(v, o[t], 32);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    if (e < left)
-                        p[e] = v[e];
-                    if (32 + e < left)
-                        p[32 + e] = v[8 + e];
-                }
+            for (int e = 0; e < 8; ++e) {
+                const float d0 = TR ? acc[(2 * e) % 4][e / 2] : acc[e / 2][(2 * e) % 4];
+                const float d1 = TR ? acc[(2 * e + 1) % 4][e / 2] : acc[e / 2][(2 * e + 1) % 4];
+                const uint32_t d = (uint32_t)o[e / 4][e % 4];
+                o[e / 4][e % 4] = pack2(__uint_as_float(d << 16) + d0, __uint_as_float(d & 0xFFFF0000u) + d1);
             }
         }
+        if (i >= tile.w)
+            continue;
+        uint16_t *p = a.out + token * a.ldo + n0 + 8 * q;
+        store8(p, o[0], left);
+        store8(p + 32, o[1], left - 32);
+    }
+}
+
+// 128 n a workgroup at a time, 16 tokens a wave: eight products of 16 tokens by 16 n, the m-th with the n = 8 i + m,
+// so that a lane ends with eight n in a row of four tokens, and sixteen lanes with 256 bytes of one (64 bytes of
+// each token, as above, took 32 us where this takes 25: 4001 tokens on N = 5120, 32 ranks).
+template <int G, bool PACK, bool TR>
+__global__ void __launch_bounds__(kThreads) k_expand_many(ExpandArgs a)
+{
+    extern __shared__ v4i shared[];            // 128 n's weights
+    const int4 tile = a.tiles[blockIdx.x / a.chunks];
+    const int chunk = blockIdx.x % a.chunks;
+    if (tile.w == 0)
+        return;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, i = lane & 15, q = lane >> 4;
+    const int ranks = a.R / 8;                 // chunks of 8 ranks
+    const bool live = tile.x >= 0;
+    int token[4];                              // tokens 4 q + c of the wave's (-1: none)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        const int at = 16 * wave + 4 * q + c;
+        token[c] = at < tile.w ? a.order[tile.y + at] : -1;
+    }
+    v4i hi[G], lo[G];
+    const uint16_t *w = a.w + (int64_t)(live ? tile.x : 0) * a.N * a.R;
+    if (live)
+        load_factors<G, PACK>(hi, lo, a, tile.y + min(16 * wave + i, tile.w - 1));
+    const int blocks = (a.N + 127) / 128;
+    for (int b = chunk; b < blocks; b += a.chunks) {
+        const int n = 128 * b + 8 * i, left = a.N - n;      // this lane's n .. n + 7
+        v4i o[4] = {};
+        if (a.base)
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                if (token[c] >= 0)
+                    o[c] = load8(a.base + token[c] * a.ldb + n, left);
+        if (live) {
+            // [n][r]: row n's chunks in order, chunk p of all at p ^ (n / 8) % 8, so that the lanes of a product,
+            // whose rows are 8 apart, find theirs in different banks; [r][n]: rows of 256 bytes
+            __syncthreads();                   // (the block before this one has been read)
+            for (int p = tid; p < 128 * ranks; p += kThreads) {
+                if (TR) {
+                    const int r = p >> 4, at = 128 * b + 8 * (p & 15);
+                    shared[p] = load8(w + (int64_t)r * a.N + at, a.N - at);
+                } else {
+                    const int row = p / ranks;
+                    v4i v{0, 0, 0, 0};
+                    if (128 * b + row < a.N)
+                        v = load8(w + (int64_t)128 * b * a.R + 8 * p);
+                    shared[p ^ ((row >> 3) & 7)] = v;
+                }
+            }
+            __syncthreads();
+            v4f acc[8] = {};
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                const int c = PACK ? q % ranks : 4 * g + q;
+                const bool there = c < ranks && (!PACK || q < 2 * ranks);
+                v4i r[8], f[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    r[j] = v4i{0, 0, 0, 0};
+                    if (there)
+                        r[j] = TR ? shared[(8 * c + j) * 16 + i] : shared[((8 * i + j) * ranks + c) ^ (i & 7)];
+                }
+#pragma unroll
+                for (int m = 0; m < 8; ++m) {
+                    f[m] = r[m];
+                    if (TR)                    // eight ranks of eight n: a column for each product
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            f[m][j] = (int)__builtin_amdgcn_perm((uint32_t)r[2 * j + 1][m / 2], (uint32_t)r[2 * j][m / 2],
+                                                                 m % 2 ? 0x07060302u : 0x05040100u);
+                }
+#pragma unroll
+                for (int m = 0; m < 8; ++m) {
+                    acc[m] = mma(hi[g], f[m], acc[m]);
+                    if (!PACK)
+                        acc[m] = mma(lo[g], f[m], acc[m]);
+                }
+            }
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t d = (uint32_t)o[c][e];
+                    o[c][e] = pack2(__uint_as_float(d << 16) + acc[2 * e][c],
+                                    __uint_as_float(d & 0xFFFF0000u) + acc[2 * e + 1][c]);
+                }
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            if (token[c] >= 0)
+                store8(a.out + token[c] * a.ldo + n, o[c], left);
     }
 }
 
@@ -649,7 +818,6 @@ struct OuterJob {
 struct OuterArgs {
     OuterJob job[2];
     const int32_t *order, *offsets;
-    int64_t places;
     int R, Rp, groups, first;  // workgroups of the first job
 };
 
@@ -669,6 +837,9 @@ __global__ void __launch_bounds__(RB == 1 ? 1024 : 512) k_outer(OuterArgs a)
     const int beg = a.offsets[l], end = a.offsets[l + 1], r0 = group * 16 * RB;
     const int left = job.C - (c0 + 8 * i);
     const uint16_t *z = job.z + c0 + 8 * i;
+    // the pieces of eight places lie together: sixteen lanes load 256 bytes of them (ranks apart by all places
+    // fell on few channels of the L2: 85 us for the gradients of 8192 tokens of 5120 and 10240)
+    const uint16_t *pieces = job.pieces + (piece_place(beg, l) / 8 + q) * 24 * a.Rp + (r0 + i) * 8;
     v4f acc[RB][8] = {};
     for (int t = beg + 32 * (split * waves + wave); t < end; t += 32 * waves * job.splits) {
         const int first = t + 8 * q, n = end - first;          // this lane's places
@@ -683,7 +854,11 @@ __global__ void __launch_bounds__(RB == 1 ? 1024 : 512) k_outer(OuterArgs a)
         for (int h = 0; h < 3; ++h)
 #pragma unroll
             for (int r = 0; r < RB; ++r)
-                f[h][r] = load8(job.pieces + ((int64_t)h * a.Rp + r0 + 16 * r + i) * a.places + first, n);
+            {
+                f[h][r] = v4i{0, 0, 0, 0};
+                if (n > 0)
+                    f[h][r] = load8(pieces + (t - beg) * 3 * (int64_t)a.Rp + (h * a.Rp + 16 * r) * 8);
+            }
 #pragma unroll
         for (int m = 0; m < 8; ++m) {
             v4i col;
@@ -766,14 +941,16 @@ struct Sizes {
     int max_tiles;
 };
 
+// Tokens an adapter has on average from which base and out are more than the weights.
+constexpr int64_t kManyTokens = 16;
+
 Sizes sizes(int64_t T, int64_t K, int64_t N, int64_t R, int64_t L)
 {
     Sizes z{T, K, N, R, L, 16, 1, 1, 1, 1, 0};
     while (z.Rp < R) z.Rp *= 2;
     const int64_t mean = T / std::min(L, std::max<int64_t>(T, 1));
-    // expand: as many tokens for each load of the weights as there are and registers hold
-    const int most = R <= 32 ? 4 : R <= 64 ? 2 : 1;
-    while (z.wide < most && mean > 16 * z.wide) z.wide *= 2;
+    // expand: 16 tokens share a load of the weights, or 64 where adapters have so many
+    z.wide = mean >= kManyTokens ? kWide / 16 : 1;
     // shrink: more tokens a workgroup only where there are workgroups for all CUs
     while (z.tb < z.wide && T >= 16 * 2 * z.tb * 240) z.tb *= 2;
     z.max_tiles = (int)std::max<int64_t>(1, T / (16 * z.tb) + std::min(L + 1, T));
@@ -784,7 +961,7 @@ Sizes sizes(int64_t T, int64_t K, int64_t N, int64_t R, int64_t L)
     return z;
 }
 
-int outer_waves(const Sizes &z) { return z.T / z.L < 512 ? 4 : z.Rp > 16 ? 8 : 16; }
+int outer_waves(const Sizes &z) { return z.T / z.L < 512 ? 4 : 8; }
 
 int outer_splits(const Sizes &z, int64_t C)
 {
@@ -810,7 +987,6 @@ struct Space {
     uint16_t *rows;            // of s v (backward: s u) for expand
     uint16_t *fv, *fu;         // backward: the pieces of s v and s u for outer
     float *outer_a, *outer_b;  // and the parts of dA and dB
-    int64_t places;
     size_t bytes;
 };
 
@@ -823,9 +999,9 @@ Space space(const Sizes &z, void *ws, bool back)
     f.rows = l.take<uint16_t>(z.T * 2 * z.Rp);
     if (back) {
         f.offsets = l.take<int32_t>(z.L + 1);
-        f.places = (z.T + 7) / 8 * 8;
-        f.fv = l.take<uint16_t>(3 * z.Rp * f.places);
-        f.fu = l.take<uint16_t>(3 * z.Rp * f.places);
+        const int64_t places = piece_place(z.T, (int)z.L);
+        f.fv = l.take<uint16_t>(3 * z.Rp * places);
+        f.fu = l.take<uint16_t>(3 * z.Rp * places);
         const int64_t sa = outer_splits(z, z.K), sb = outer_splits(z, z.N);
         f.outer_a = l.take<float>(sa > 1 ? sa * z.L * z.R * z.K : 0);
         f.outer_b = l.take<float>(sb > 1 ? sb * z.L * z.R * z.N : 0);
@@ -843,16 +1019,18 @@ bool good_shape(int64_t T, int64_t K, int64_t N, int64_t R, int64_t L)
 template <bool BACK>
 hipError_t launch_shrink(const Sizes &z, const ShrinkArgs &a, hipStream_t s)
 {
-    const dim3 grid((unsigned)(z.max_tiles * z.groups * (BACK ? 2 : 1))), block(kShrinkThreads);
+    const int waves = z.tb * z.rb <= 2 && z.max_tiles * z.groups <= 128 ? 16 : 8;
+    const dim3 grid((unsigned)(z.max_tiles * z.groups * (BACK ? 2 : 1))), block(64 * waves);
+    const size_t lds = std::max(waves * shrink_share(z.tb, z.rb) * sizeof(v4i), (kBins + 3) / 4 * sizeof(v4i));
     switch (z.rb * 8 + z.tb) {
-    case 8 + 1: hipLaunchKernelGGL((k_shrink<1, 1, BACK>), grid, block, 0, s, a); break;
-    case 8 + 2: hipLaunchKernelGGL((k_shrink<2, 1, BACK>), grid, block, 0, s, a); break;
-    case 8 + 4: hipLaunchKernelGGL((k_shrink<4, 1, BACK>), grid, block, 0, s, a); break;
-    case 16 + 1: hipLaunchKernelGGL((k_shrink<1, 2, BACK>), grid, block, 0, s, a); break;
-    case 16 + 2: hipLaunchKernelGGL((k_shrink<2, 2, BACK>), grid, block, 0, s, a); break;
-    case 16 + 4: hipLaunchKernelGGL((k_shrink<4, 2, BACK>), grid, block, 0, s, a); break;
-    case 32 + 1: hipLaunchKernelGGL((k_shrink<1, 4, BACK>), grid, block, 0, s, a); break;
-    default: hipLaunchKernelGGL((k_shrink<2, 4, BACK>), grid, block, 0, s, a); break;
+    case 8 + 1: hipLaunchKernelGGL((k_shrink<1, 1, BACK>), grid, block, lds, s, a); break;
+    case 8 + 2: hipLaunchKernelGGL((k_shrink<2, 1, BACK>), grid, block, lds, s, a); break;
+    case 8 + 4: hipLaunchKernelGGL((k_shrink<4, 1, BACK>), grid, block, lds, s, a); break;
+    case 16 + 1: hipLaunchKernelGGL((k_shrink<1, 2, BACK>), grid, block, lds, s, a); break;
+    case 16 + 2: hipLaunchKernelGGL((k_shrink<2, 2, BACK>), grid, block, lds, s, a); break;
+    case 16 + 4: hipLaunchKernelGGL((k_shrink<4, 2, BACK>), grid, block, lds, s, a); break;
+    case 32 + 1: hipLaunchKernelGGL((k_shrink<1, 4, BACK>), grid, block, lds, s, a); break;
+    default: hipLaunchKernelGGL((k_shrink<2, 4, BACK>), grid, block, lds, s, a); break;
     }
     return hipGetLastError();
 }
@@ -861,42 +1039,39 @@ hipError_t launch_shrink(const Sizes &z, const ShrinkArgs &a, hipStream_t s)
 hipError_t make_plan(const Sizes &z, const Space &f, const void *ids, int32_t id_bits, ShrinkArgs &a, hipStream_t s)
 {
     a.plan = Plan{ids, f.order, f.offsets, f.tiles, (int)z.T, (int)z.L, 16 * z.tb, 16 * z.wide, z.max_tiles, id_bits};
-    a.self = z.T > 0 && z.T <= kSelfTokens;
+    a.self = z.T == 0 || z.T > kSelfTokens ? 0 : z.T <= kWaveTokens ? 1 : 2;
     if (a.self)
         return hipSuccess;
     hipLaunchKernelGGL(k_plan, dim3(1), dim3(kPlanThreads), 0, s, a.plan);
     return hipGetLastError();
 }
 
-template <int TB, bool TR>
-void expand_ranks(const ExpandArgs &a, dim3 grid, hipStream_t s)
+template <int G, bool PACK, bool TR>
+void expand_kernel(const Sizes &z, const ExpandArgs &a, dim3 grid, hipStream_t s)
 {
-    const dim3 block(kThreads);
-    if (a.R <= 16)
-        hipLaunchKernelGGL((k_expand<TB, 1, true, TR>), grid, block, 0, s, a);
-    else if (a.R <= 32)
-        hipLaunchKernelGGL((k_expand<TB, 1, false, TR>), grid, block, 0, s, a);
-    else if (TB < 4 && a.R <= 64)
-        hipLaunchKernelGGL((k_expand<TB < 4 ? TB : 1, 2, false, TR>), grid, block, 0, s, a);
+    if (z.wide > 1)
+        hipLaunchKernelGGL((k_expand_many<G, PACK, TR>), grid, dim3(kThreads), 128 * 2 * (size_t)z.R, s, a);
     else
-        hipLaunchKernelGGL((k_expand<1, 4, false, TR>), grid, block, 0, s, a);
+        hipLaunchKernelGGL((k_expand_few<G, PACK, TR>), grid, dim3(kThreads), 0, s, a);
 }
 
 template <bool TR>
 hipError_t launch_expand(const Sizes &z, const Space &f, const uint16_t *w, int64_t N, const uint16_t *base, int64_t ldb,
                          uint16_t *out, int64_t ldo, hipStream_t s)
 {
-    const int64_t blocks = (N + 63) / 64, full = (blocks + kWaves - 1) / kWaves;
+    const int64_t full = z.wide > 1 ? (N + 127) / 128 : (N + 64 * kWaves - 1) / (64 * kWaves);
     const int64_t tiles = z.T / (16 * z.wide) + std::min(z.L + 1, z.T);
     const int chunks = (int)std::max<int64_t>(1, std::min<int64_t>(full, 8192 / tiles));
     const ExpandArgs a{f.rows, f.order, f.tiles, w, base, out, ldb, ldo, (int)N, (int)z.R, (int)z.Rp, chunks};
     const dim3 grid((unsigned)(z.max_tiles * chunks));
-    if (z.wide == 4)
-        expand_ranks<4, TR>(a, grid, s);
-    else if (z.wide == 2)
-        expand_ranks<2, TR>(a, grid, s);
+    if (z.R <= 16)
+        expand_kernel<1, true, TR>(z, a, grid, s);
+    else if (z.R <= 32)
+        expand_kernel<1, false, TR>(z, a, grid, s);
+    else if (z.R <= 64)
+        expand_kernel<2, false, TR>(z, a, grid, s);
     else
-        expand_ranks<1, TR>(a, grid, s);
+        expand_kernel<4, false, TR>(z, a, grid, s);
     return hipGetLastError();
 }
 
@@ -909,7 +1084,6 @@ hipError_t launch_outer(const Sizes &z, const Space &f, const uint16_t *x, int64
     a.job[1] = OuterJob{dy, f.fv, sb > 1 ? f.outer_b : db, lddy, z.L * z.R * z.N, (int)z.N, (int)((z.N + 127) / 128), sb, 1};
     a.order = f.order;
     a.offsets = f.offsets;
-    a.places = f.places;
     a.R = (int)z.R;
     a.Rp = (int)z.Rp;
     a.groups = (int)((z.R + 16 * rb - 1) / (16 * rb));
@@ -1015,7 +1189,6 @@ qlin_status qlin_lora_mm_backward(int32_t id_bits, int64_t tokens, int64_t K, in
     a.job[0] = ShrinkJob{X, A, nullptr, f.fv, ldx, (int)K};
     a.job[1] = ShrinkJob{dY, B, f.rows, f.fu, lddy, (int)N};
     a.scale = scale;
-    a.places = f.places;
     a.R = (int)rank;
     a.Rp = (int)z.Rp;
     a.groups = z.groups;
