@@ -339,6 +339,8 @@ struct ShrinkArgs {
     ShrinkJob job[2];          // v; u
     Plan plan;
     const float *scale;
+    float *part;               // [splits][tokens][Rp]: sums of parts of K, for the expand kernel to add (or NULL)
+    int splits;
     int R, Rp, groups, self;   // groups of 16 RB ranks; self: waves (1) or workgroups (2) make the plan
 };
 
@@ -404,7 +406,10 @@ __global__ void __launch_bounds__((64 * shrink_waves<TB, RB>())) k_shrink(Shrink
     // (the longer job's workgroups come first)
     const int later = BACK && (int)blockIdx.x >= units, second = BACK && later != (a.job[1].K > a.job[0].K);
     const ShrinkJob &job = a.job[second];
-    const int unit = (int)blockIdx.x - (later ? units : 0), index = unit / a.groups, group = unit % a.groups;
+    const int split = BACK ? 0 : (int)blockIdx.x % a.splits;
+    const int unit = BACK ? (int)blockIdx.x - (later ? units : 0) : (int)blockIdx.x / a.splits;
+    const int index = unit / a.groups, group = unit % a.groups;
+    const bool publish = group == 0 && !second && split == 0;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, i = lane & 15, q = lane >> 4;
     const int waves = blockDim.x >> 6;
     int4 tile;
@@ -415,12 +420,12 @@ __global__ void __launch_bounds__((64 * shrink_waves<TB, RB>())) k_shrink(Shrink
 #pragma unroll
         for (int t = 0; t < TB; ++t) token[t] = __shfl(sorted, tile.y + min(16 * t + i, tile.z - 1));
         const int there = __shfl(sorted, (tile.y + lane) & 63);          // (by all lanes)
-        if (group == 0 && !second && wave == 0 && lane < tile.z)
+        if (publish && wave == 0 && lane < tile.z)
             a.plan.order[tile.y + lane] = there;
     } else {
         if (a.self) {
             tile = self_plan(a.plan, index, reinterpret_cast<int32_t *>(shared), sh);
-            if (group == 0 && !second && tid < tile.z)
+            if (publish && tid < tile.z)
                 a.plan.order[tile.y + tid] = sh.token[tid];
 #pragma unroll
             for (int t = 0; t < TB; ++t) token[t] = tile.z ? sh.token[min(16 * t + i, tile.z - 1)] : 0;
@@ -430,7 +435,7 @@ __global__ void __launch_bounds__((64 * shrink_waves<TB, RB>())) k_shrink(Shrink
             for (int t = 0; t < TB; ++t) token[t] = tile.z ? a.plan.order[tile.y + min(16 * t + i, tile.z - 1)] : 0;
         }
     }
-    if (a.self && group == 0 && !second && tid == 0)
+    if (a.self && publish && tid == 0)
         a.plan.tiles[index] = tile;
     if (tile.x < 0 || tile.z == 0)
         return;
@@ -452,18 +457,19 @@ __global__ void __launch_bounds__((64 * shrink_waves<TB, RB>())) k_shrink(Shrink
             for (int h = 0; h < 2; ++h)
                 pw[r][h] = job.w + ((int64_t)tile.x * a.R + min(r0 + 16 * r + 8 * h + (lane >> 3), a.R - 1)) * job.K +
                            8 * (lane & 7);
-        for (int s = wave * U; s < steps; s += waves * U) {
+        const int per = (steps + a.splits - 1) / a.splits, end = min((split + 1) * per, steps);
+        for (int s = split * per + wave; s < end; s += waves * U) {
             v4i x[U][TB][2], w[U][RB][2];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                if (u > 0 && s + u >= steps)
+                if (u > 0 && s + waves * u >= end)
                     break;
-                load_rows(x[u], px, (s + u) * kStep, job.K);
-                load_rows(w[u], pw, (s + u) * kStep, job.K);
+                load_rows(x[u], px, (s + waves * u) * kStep, job.K);
+                load_rows(w[u], pw, (s + waves * u) * kStep, job.K);
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                if (u > 0 && s + u >= steps)
+                if (u > 0 && s + waves * u >= end)
                     break;
                 store_rows(mine, x[u]);
                 store_rows(weights, w[u]);
@@ -549,6 +555,13 @@ __global__ void __launch_bounds__((64 * shrink_waves<TB, RB>())) k_shrink(Shrink
         for (int w = 1; w < waves; ++w) v += sums[w * TB * RB * 64 + e];
         const int block = e >> 6, rank = r0 + 16 * (block % RB) + (e & 15), at = 16 * (block / RB) + 4 * ((e >> 4) & 3);
         const int n = tile.z - at;             // of the four places from there
+        if (!BACK && a.part) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                if (c < n)
+                    a.part[((int64_t)split * a.plan.tokens + tile.y + at + c) * a.Rp + rank] = v[c];
+            continue;
+        }
         uint16_t o[3][4];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
@@ -582,6 +595,8 @@ constexpr int kWide = 16 * kWaves;             // tokens of a workgroup of the s
 
 struct ExpandArgs {
     const uint16_t *rows;      // [tokens][2][Rp]: s v
+    const float *part, *scale; // instead of rows: [splits][tokens][Rp], the parts of v, and s (or NULL)
+    int tokens, splits;
     const int32_t *order;
     const int4 *tiles;
     const uint16_t *w, *base;
@@ -607,6 +622,44 @@ __device__ inline void load_factors(v4i (&hi)[G], v4i (&lo)[G], const ExpandArgs
     }
 }
 
+// The same from the parts, four of them on their way at a time.
+template <int G, bool PACK>
+__device__ inline void add_factors(v4i (&hi)[G], v4i (&lo)[G], const ExpandArgs &a, int place, float s)
+{
+    const int q = (threadIdx.x & 63) >> 4, ranks = a.R / 8;
+    const int64_t apart = (int64_t)a.tokens * a.Rp;
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+        const int c = PACK ? q % ranks : 4 * g + q, piece = PACK ? q / ranks : 0;
+        hi[g] = lo[g] = v4i{0, 0, 0, 0};
+        if (c >= ranks || piece > 1)
+            continue;
+        const float *p = a.part + (int64_t)place * a.Rp + 8 * c;
+        v4f sum[2] = {};
+        for (int k = 0; k < a.splits; k += 4) {
+            v4f v[4][2] = {};
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (k + j < a.splits) {
+                    v[j][0] = *reinterpret_cast<const v4f *>(p + (k + j) * apart);
+                    v[j][1] = *reinterpret_cast<const v4f *>(p + (k + j) * apart + 4);
+                }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                sum[0] += v[j][0];
+                sum[1] += v[j][1];
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float v0 = sum[e / 2][2 * e % 4] * s, v1 = sum[e / 2][2 * e % 4 + 1] * s, h0 = cut(v0), h1 = cut(v1);
+            const int high = pack2(h0, h1), low = pack2(rest(v0, h0), rest(v1, h1));
+            hi[g][e] = PACK && piece == 1 ? low : high;
+            lo[g][e] = low;
+        }
+    }
+}
+
 // 64 n a wave at a time as four products of 16 n by 16 tokens, dealt to them so that a lane ends with twice eight n
 // in a row of its token, and four lanes with 64 bytes of it.  Weights' bytes bound it: 128 tokens of 24 adapters
 // of 64 ranks on N = 51200, 183 MB, 37 us, 5.0 TB/s.
@@ -623,8 +676,13 @@ __global__ void __launch_bounds__(kThreads) k_expand_few(ExpandArgs a)
     const int64_t token = a.order[tile.y + min(i, tile.w - 1)];
     v4i hi[G], lo[G];
     const uint16_t *w = a.w + (int64_t)(live ? tile.x : 0) * a.N * a.R;
-    if (live)
-        load_factors<G, PACK>(hi, lo, a, tile.y + min(i, tile.w - 1));
+    if (live) {
+        const int place = tile.y + min(i, tile.w - 1);
+        if (!TR && a.part)
+            add_factors<G, PACK>(hi, lo, a, place, a.scale ? a.scale[tile.x] : 1.0f);
+        else
+            load_factors<G, PACK>(hi, lo, a, place);
+    }
     const int blocks = (a.N + 63) / 64;
     for (int b = chunk * kWaves + wave; b < blocks; b += a.chunks * kWaves) {
         const int n0 = 64 * b;
@@ -939,14 +997,19 @@ struct Sizes {
     int tb, rb, groups;        // shrink: blocks of tokens and ranks of a workgroup, groups of ranks
     int wide;                  // expand: blocks of tokens
     int max_tiles;
+    int splits;                // shrink of the forward call: parts of K
 };
+
+// Parts of K that the expand kernel adds: 32 tokens of 28 adapters, K = 5120, N = 10240, both kernels: one part
+// 15.8 us, four 13.6, eight 14.5; 164 workgroups (24 adapters of 64 ranks, N = 51200): one 49.4, three 52.9.
+constexpr int64_t kMaxSplits = 4;
 
 // Tokens an adapter has on average from which base and out are more than the weights.
 constexpr int64_t kManyTokens = 16;
 
 Sizes sizes(int64_t T, int64_t K, int64_t N, int64_t R, int64_t L)
 {
-    Sizes z{T, K, N, R, L, 16, 1, 1, 1, 1, 0};
+    Sizes z{T, K, N, R, L, 16, 1, 1, 1, 1, 0, 1};
     while (z.Rp < R) z.Rp *= 2;
     const int64_t mean = T / std::min(L, std::max<int64_t>(T, 1));
     // expand: 16 tokens share a load of the weights, or 64 where adapters have so many
@@ -958,6 +1021,9 @@ Sizes sizes(int64_t T, int64_t K, int64_t N, int64_t R, int64_t L)
     const int blocks = (int)(z.Rp / 16);
     while (z.rb < 4 && z.rb < blocks && z.rb * z.tb < 8 && (int64_t)z.max_tiles * (blocks / z.rb) > 512) z.rb *= 2;
     z.groups = (int)((R + 16 * z.rb - 1) / (16 * z.rb));
+    // few workgroups: parts of K, a step for each wave at least (a CU alone loads some 50 GB/s)
+    if (z.wide == 1 && z.max_tiles * z.groups <= 128)
+        z.splits = (int)std::min<int64_t>((K + 8 * kStep - 1) / (8 * kStep), kMaxSplits);
     return z;
 }
 
@@ -985,6 +1051,7 @@ struct Space {
     int32_t *order, *offsets;
     int4 *tiles;
     uint16_t *rows;            // of s v (backward: s u) for expand
+    float *part;               // or the parts of v
     uint16_t *fv, *fu;         // backward: the pieces of s v and s u for outer
     float *outer_a, *outer_b;  // and the parts of dA and dB
     size_t bytes;
@@ -996,7 +1063,10 @@ Space space(const Sizes &z, void *ws, bool back)
     Space f{};
     f.order = l.take<int32_t>(z.T);
     f.tiles = l.take<int4>(z.max_tiles);
-    f.rows = l.take<uint16_t>(z.T * 2 * z.Rp);
+    if (back || z.splits == 1)
+        f.rows = l.take<uint16_t>(z.T * 2 * z.Rp);
+    else
+        f.part = l.take<float>(z.splits * z.T * z.Rp);
     if (back) {
         f.offsets = l.take<int32_t>(z.L + 1);
         const int64_t places = piece_place(z.T, (int)z.L);
@@ -1019,8 +1089,8 @@ bool good_shape(int64_t T, int64_t K, int64_t N, int64_t R, int64_t L)
 template <bool BACK>
 hipError_t launch_shrink(const Sizes &z, const ShrinkArgs &a, hipStream_t s)
 {
-    const int waves = z.tb * z.rb <= 2 && z.max_tiles * z.groups <= 128 ? 16 : 8;
-    const dim3 grid((unsigned)(z.max_tiles * z.groups * (BACK ? 2 : 1))), block(64 * waves);
+    const int waves = z.tb * z.rb <= 2 && z.max_tiles * z.groups <= 128 && a.splits == 1 ? 16 : 8;
+    const dim3 grid((unsigned)(z.max_tiles * z.groups * (BACK ? 2 : a.splits))), block(64 * waves);
     const size_t lds = std::max(waves * shrink_share(z.tb, z.rb) * sizeof(v4i), (kBins + 3) / 4 * sizeof(v4i));
     switch (z.rb * 8 + z.tb) {
     case 8 + 1: hipLaunchKernelGGL((k_shrink<1, 1, BACK>), grid, block, lds, s, a); break;
@@ -1056,13 +1126,13 @@ void expand_kernel(const Sizes &z, const ExpandArgs &a, dim3 grid, hipStream_t s
 }
 
 template <bool TR>
-hipError_t launch_expand(const Sizes &z, const Space &f, const uint16_t *w, int64_t N, const uint16_t *base, int64_t ldb,
+hipError_t launch_expand(const Sizes &z, const Space &f, const float *scale, const uint16_t *w, int64_t N, const uint16_t *base, int64_t ldb,
                          uint16_t *out, int64_t ldo, hipStream_t s)
 {
     const int64_t full = z.wide > 1 ? (N + 127) / 128 : (N + 64 * kWaves - 1) / (64 * kWaves);
     const int64_t tiles = z.T / (16 * z.wide) + std::min(z.L + 1, z.T);
-    const int chunks = (int)std::max<int64_t>(1, std::min<int64_t>(full, 8192 / tiles));
-    const ExpandArgs a{f.rows, f.order, f.tiles, w, base, out, ldb, ldo, (int)N, (int)z.R, (int)z.Rp, chunks};
+    const int chunks = (int)std::max<int64_t>(1, std::min<int64_t>(full, (z.wide > 1 ? 2048 : 8192) / tiles));
+    const ExpandArgs a{f.rows, f.part, scale, (int)z.T, z.splits, f.order, f.tiles, w, base, out, ldb, ldo, (int)N, (int)z.R, (int)z.Rp, chunks};
     const dim3 grid((unsigned)(z.max_tiles * chunks));
     if (z.R <= 16)
         expand_kernel<1, true, TR>(z, a, grid, s);
@@ -1145,12 +1215,14 @@ qlin_status qlin_lora_mm(int32_t id_bits, int64_t tokens, int64_t K, int64_t N, 
     hipStream_t s = static_cast<hipStream_t>(stream);
     ShrinkArgs a{};
     a.job[0] = ShrinkJob{X, A, f.rows, nullptr, ldx, (int)K};
+    a.part = f.part;
+    a.splits = z.splits;
     a.scale = scale;
     a.R = (int)rank;
     a.Rp = (int)z.Rp;
     a.groups = z.groups;
     if (make_plan(z, f, ids, id_bits, a, s) != hipSuccess || launch_shrink<false>(z, a, s) != hipSuccess ||
-        launch_expand<false>(z, f, B, N, base, ldb, Y, ldy, s) != hipSuccess)
+        launch_expand<false>(z, f, scale, B, N, base, ldb, Y, ldy, s) != hipSuccess)
         return QLIN_ERR_HIP;
     return QLIN_OK;
 }
@@ -1188,6 +1260,7 @@ qlin_status qlin_lora_mm_backward(int32_t id_bits, int64_t tokens, int64_t K, in
     ShrinkArgs a{};
     a.job[0] = ShrinkJob{X, A, nullptr, f.fv, ldx, (int)K};
     a.job[1] = ShrinkJob{dY, B, f.rows, f.fu, lddy, (int)N};
+    a.splits = 1;
     a.scale = scale;
     a.R = (int)rank;
     a.Rp = (int)z.Rp;
@@ -1195,7 +1268,7 @@ qlin_status qlin_lora_mm_backward(int32_t id_bits, int64_t tokens, int64_t K, in
     if (make_plan(z, f, ids, id_bits, a, s) != hipSuccess)
         return QLIN_ERR_HIP;
     if (tokens > 0 && (launch_shrink<true>(z, a, s) != hipSuccess ||
-                       launch_expand<true>(z, f, A, K, base, ldb, dX, lddx, s) != hipSuccess))
+                       launch_expand<true>(z, f, nullptr, A, K, base, ldb, dX, lddx, s) != hipSuccess))
         return QLIN_ERR_HIP;
     if (launch_outer(z, f, X, ldx, dY, lddy, dA, dB, s) != hipSuccess)
         return QLIN_ERR_HIP;
