@@ -912,35 +912,26 @@ def _tokens(ids, T, device, name="ids"):
         raise TypeError(f"{name} must be int32 or int64, got {ids.dtype}")
     if ids.dim() != 1 or ids.device != device or not ids.is_contiguous():
         raise ValueError(f"{name} must be a contiguous [T] tensor, on one device with the others")
-    if T is not None and ids.shape[0] != T:
-        raise ValueError(f"{name} has {ids.shape[0]} entries for {T} rows")
+    if T is not None and len(ids) != T:
+        raise ValueError(f"{name} has {len(ids)} entries for {T} rows")
     return bits
 
 
 _ID_BITS = {torch.int32: 32, torch.int64: 64}
 
 
-def _own_workspace(n, like):
-    """(address or None, the tensor that holds it): the call's own workspace, as in _sort_buffers."""
-    if not n:
-        return None, None
-    ws = like.new_empty(n, dtype=torch.uint8)
-    return ws.data_ptr(), ws
-
-
 def _adapters(x, a, b, ids, scale):
     """Checks of the arguments that both adapter calls share: (bits, T, K, N, rank, adapters), x's row
     stride and the scale's address."""
-    for t, name in ((x, "x"), (a, "a"), (b, "b")):
-        if t.dtype != torch.bfloat16:
-            raise TypeError(f"{name} must be bfloat16, got {t.dtype}")
+    if x.dtype != torch.bfloat16 or a.dtype != torch.bfloat16 or b.dtype != torch.bfloat16:
+        raise TypeError(f"x, a and b must be bfloat16, got {x.dtype}, {a.dtype} and {b.dtype}")
     dev = x.device
     T, K, ldx = _matrix(x, "x", dev)
     if a.dim() != 3 or b.dim() != 3:
         raise ValueError("a must be [adapters, rank, K] and b [adapters, N, rank]")
     L, R, cols = a.shape
-    N = b.shape[1]
-    if cols != K or b.shape[0] != L or b.shape[2] != R:
+    adapters, N, rank = b.shape
+    if cols != K or adapters != L or rank != R:
         raise ValueError(f"x is [T,K], a must be [adapters, rank, K] and b [adapters, N, rank], got "
                          f"{tuple(x.shape)}, {tuple(a.shape)} and {tuple(b.shape)}")
     if a.device != dev or b.device != dev or not a.is_contiguous() or not b.is_contiguous():
@@ -974,10 +965,10 @@ def lora_mm(x, a, b, ids, scale=None, base=None, out=None):
     out, ldy = _rows_out(out, (T, N), x)
     lib = _lib()
     n = lib.qlin_lora_workspace_size(*dims[1:])
-    ws, held = _own_workspace(n, x)
+    ws = x.new_empty(n, dtype=torch.uint8) if n else None               # the call's own: see _sort_buffers
     _call_on(x.device, lib.qlin_lora_mm,
              (*dims, x.data_ptr(), ldx, a.data_ptr(), b.data_ptr(), ids.data_ptr(), sc, addr, ldb, out.data_ptr(), ldy,
-              ws, n), "qlin_lora_mm")
+              None if ws is None else ws.data_ptr(), n), "qlin_lora_mm")
     return out
 
 
@@ -999,10 +990,11 @@ def lora_mm_backward(dy, x, a, b, ids, scale=None, base=None, out=None):
     da, db = a.new_empty(a.shape, dtype=torch.float32), b.new_empty(b.shape, dtype=torch.float32)
     lib = _lib()
     n = lib.qlin_lora_backward_workspace_size(*dims[1:])
-    ws, held = _own_workspace(n, x)
+    ws = x.new_empty(n, dtype=torch.uint8) if n else None
     _call_on(x.device, lib.qlin_lora_mm_backward,
              (*dims, dy.data_ptr(), lddy, x.data_ptr(), ldx, a.data_ptr(), b.data_ptr(), ids.data_ptr(), sc, addr, ldb,
-              out.data_ptr(), lddx, da.data_ptr(), db.data_ptr(), ws, n), "qlin_lora_mm_backward")
+              out.data_ptr(), lddx, da.data_ptr(), db.data_ptr(), None if ws is None else ws.data_ptr(), n),
+             "qlin_lora_mm_backward")
     return out, da, db
 
 
@@ -1019,16 +1011,18 @@ def token_logprobs(logits, target, top: int = 0):
     top = int(top)
     if not 0 <= top <= 64:
         raise ValueError(f"top must be 0..64, got {top}")
-    one = logits.new_empty((3, T), dtype=torch.float32)
-    logprob, entropy, lse = one[0], one[1], one[2]
-    top_logprob = logits.new_empty((T, top), dtype=torch.float32)
-    top_id = logits.new_empty((T, top), dtype=torch.int32)
+    # (one allocation and views of it: 2 us less than an allocation each)
+    logprob, entropy, lse, top_logprob, top_id = \
+        logits.new_empty((3 + 2 * top) * T, dtype=torch.float32).split_with_sizes([T, T, T, top * T, top * T])
+    top_logprob, top_id = top_logprob.view(T, top), top_id.view(torch.int32).view(T, top)
     lib = _lib()
     n = lib.qlin_token_logprobs_workspace_size(rt, T, V, top)
-    ws, held = _own_workspace(n, logits)
+    ws = logits.new_empty(n, dtype=torch.uint8) if n else None          # the call's own: see _sort_buffers
+    addr = logprob.data_ptr()
     _call_on(dev, lib.qlin_token_logprobs,
-             (rt, bits, T, V, top, logits.data_ptr(), ld, target.data_ptr(), logprob.data_ptr(), entropy.data_ptr(),
-              lse.data_ptr(), top_logprob.data_ptr(), top_id.data_ptr(), ws, n), "qlin_token_logprobs")
+             (rt, bits, T, V, top, logits.data_ptr(), ld, target.data_ptr(), addr, addr + 4 * T, addr + 8 * T,
+              addr + 12 * T, addr + 12 * T + 4 * T * top, None if ws is None else ws.data_ptr(), n),
+             "qlin_token_logprobs")
     return logprob, entropy, lse, top_logprob, top_id
 
 
@@ -1124,10 +1118,11 @@ def embedding_backward(dout, ids, vocab: int, scale: float = 1.0, dtype=None, ou
         ldt = _matrix(out, "out", dev)[2]
     lib = _lib()
     n = lib.qlin_embedding_backward_workspace_size(T, vocab, H)
-    ws, held = _own_workspace(n, dout)
+    ws = dout.new_empty(n, dtype=torch.uint8) if n else None
     _call_on(dev, lib.qlin_embedding_backward,
              (rt, _ROW_TYPE[dtype], bits, T, vocab, H, ids.data_ptr(), dout.data_ptr(), ldd, float(scale),
-              1 if accumulate else 0, out.data_ptr(), ldt, ws, n), "qlin_embedding_backward")
+              1 if accumulate else 0, out.data_ptr(), ldt, None if ws is None else ws.data_ptr(), n),
+             "qlin_embedding_backward")
     return out
 
 

@@ -25,6 +25,7 @@ constexpr int kThreads = 256, kWaves = kThreads / 64;
 constexpr int kPieces = 4;                     // 16-byte pieces a thread takes at a time
 constexpr int kMaxTop = 64;                    // an alternative for each lane of a wave
 constexpr int kMaxParts = 64;                  // a part for each lane of the joining wave
+constexpr int64_t kRowBlocks = 2048;           // workgroups that rows are divided into where they are fewer
 constexpr int64_t kMaxRows = (int64_t)1 << 23; // x parts: below 2^32 threads
 constexpr int64_t kMaxVocab = (int64_t)1 << 28;
 constexpr int64_t kMaxStride = (int64_t)1 << 31;
@@ -70,18 +71,6 @@ __device__ inline uint64_t key_lane(uint64_t k, int lane)
            (uint32_t)__builtin_amdgcn_readlane((int)k, lane);
 }
 
-__device__ inline uint64_t wave_max_key(uint64_t k)
-{
-#pragma unroll
-    for (int s = 0; s < 4; ++s) {
-        const uint64_t o = (uint64_t)(uint32_t)dpp_partner((int)(k >> 32), s) << 32 | (uint32_t)dpp_partner((int)k, s);
-        k = o > k ? o : k;
-    }
-    const uint64_t a = key_lane(k, 0), b = key_lane(k, 16), c = key_lane(k, 32), d = key_lane(k, 48);
-    const uint64_t e = a > b ? a : b, f = c > d ? c : d;
-    return e > f ? e : f;
-}
-
 // A wave's best `top` keys so far, in order, one a lane.
 struct Best {
     uint64_t mine = 0, last = 0;               // this lane's; that of lane top - 1
@@ -97,6 +86,21 @@ struct Best {
         last = key_lane(mine, top - 1);
     }
 };
+
+// A value that at least `top` lanes' v reach: the upper 16 bits, bit by bit, of the top-th greatest.
+__device__ inline float top_th(float v, int top)
+{
+    const int b = __float_as_int(v + 0.0f);
+    const uint32_t o = (b < 0 ? ~(uint32_t)b : (uint32_t)b | 0x80000000u) >> 16;
+    uint32_t t = 0;
+#pragma unroll
+    for (int i = 15; i >= 0; --i) {
+        const uint32_t more = t | 1u << i;
+        t = __popcll(__ballot(o >= more)) >= top ? more : t;
+    }
+    t <<= 16;
+    return t < 0x00800000u ? -INFINITY : __uint_as_float(t & 0x80000000u ? t & 0x7FFFFFFFu : ~t);
+}
 
 struct Args {
     const uint8_t *x;
@@ -117,19 +121,21 @@ __device__ inline int target_of(const Args &a, int64_t row)
     return t >= 0 && t < a.V ? (int)t : -1;
 }
 
+// The logit of the row's target, 0 for none: loaded first, used last.
+template <typename T>
+__device__ inline float target_logit(const Args &a, int64_t row, int target)
+{
+    return target >= 0 ? Elem<T>::get(reinterpret_cast<const T *>(a.x + row * a.ld)[target]) : 0.0f;
+}
+
 // The row's outputs from its statistics; the keys are in `best`.  A row that
 // holds no number above -inf has no distribution: log probabilities -inf, H = 0.
-template <typename T>
-__device__ inline void finish(const Args &a, int64_t row, Stat s, const uint64_t *best, int tid)
+__device__ inline void finish(const Args &a, int64_t row, Stat s, const uint64_t *best, int tid, int target, float x)
 {
     const float ln = logf(s.s);
     const bool none = s.s == 0.0f;
     if (tid == 0) {
-        const int t = target_of(a, row);
-        float l = 0.0f;
-        if (t >= 0)
-            l = none ? -INFINITY : (Elem<T>::get(reinterpret_cast<const T *>(a.x + row * a.ld)[t]) - s.m) - ln;
-        a.logprob[row] = l;
+        a.logprob[row] = target < 0 ? 0.0f : none ? -INFINITY : (x - s.m) - ln;
         a.entropy[row] = none ? 0.0f : ln - s.w / s.s;
         a.lse[row] = none ? -INFINITY : s.m + ln;
     }
@@ -175,14 +181,19 @@ __global__ void __launch_bounds__(kThreads) k_logprobs(Args a)
     const int64_t row = blockIdx.x / a.parts;
     const int part = blockIdx.x % a.parts, beg = part * a.per, end = min(beg + a.per, a.V);
     const T *x = reinterpret_cast<const T *>(a.x + row * a.ld);
+    const int target = a.parts == 1 ? target_of(a, row) : -1;
+    const float logit = target_logit<T>(a, row, target);
     Stat s{-FLT_MAX, 0.0f, 0.0f};
     Best best;
     v4i next[kPieces];
     load_chunk(next, x, beg, end, tid);
     for (int c = beg; c < end; c += kStep) {
         float v[kPieces][E], high[kPieces], most = -INFINITY;
+        const int pieces = min(kPieces, (end - c + kThreads * E - 1) / (kThreads * E));    // that hold anything
 #pragma unroll
         for (int u = 0; u < kPieces; ++u) {
+            if (u >= pieces)
+                break;
             piece_values<T>(v[u], next[u]);
             high[u] = v[u][0];
 #pragma unroll
@@ -194,30 +205,27 @@ __global__ void __launch_bounds__(kThreads) k_logprobs(Args a)
         if (most > s.m)
             rescale(s, most);
 #pragma unroll
-        for (int u = 0; u < kPieces; ++u)
+        for (int u = 0; u < kPieces; ++u) {
+            if (u >= pieces)
+                break;
 #pragma unroll
             for (int i = 0; i < E; ++i) {
                 const float d = v[u][i] - s.m, e = exp_of(d);
                 s.s += e;
                 s.w = fmaf(e, fmaxf(d, kLowest), s.w);
             }
+        }
         if (TOP) {
             // Of the first chunk, the top-th best of the lanes' maxima bounds what can enter; later, a value
             // has to be greater than the last of the list, whose index is lower.
             float bar = best.bar;
             bool open = best.last == 0;
-            if (c == beg) {
-                int rank = 0;
-                for (int l = 0; l < 64; ++l) {
-                    const float o = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(most), l));
-                    rank += o > most || (o == most && l < lane) ? 1 : 0;
-                }
-                const uint64_t at = __ballot(rank == a.top - 1);
-                bar = at ? __int_as_float(__builtin_amdgcn_readlane(__float_as_int(most), __ffsll((unsigned long long)at) - 1))
-                         : -INFINITY;
-            }
+            if (c == beg)
+                bar = top_th(most, a.top);
 #pragma unroll
             for (int u = 0; u < kPieces; ++u) {
+                if (u >= pieces)
+                    break;
                 if (!__ballot(high[u] > bar || (open && high[u] >= bar)))
                     continue;
                 const int at = c + (u * kThreads + tid) * E;
@@ -243,8 +251,8 @@ __global__ void __launch_bounds__(kThreads) k_logprobs(Args a)
     s.w = wave_sum(s.w);
     if (lane == 0)
         stats[wave] = s;
-    if (TOP && lane < a.top) {
-        keys[wave][lane] = best.mine;
+    if (TOP) {
+        keys[wave][lane] = lane < a.top ? best.mine : 0;
         if (wave == 0)
             merged[lane] = 0;
     }
@@ -267,15 +275,16 @@ __global__ void __launch_bounds__(kThreads) k_logprobs(Args a)
         if (tid < kWaves * a.top) {
             const uint64_t k = keys[tid / a.top][tid % a.top];
             int rank = 0;
-            for (int w = 0; w < kWaves; ++w)
-                for (int j = 0; j < a.top; ++j) rank += keys[w][j] > k ? 1 : 0;
+            for (int j = 0; j < a.top; j += 4)
+#pragma unroll
+                for (int e = 0; e < 4 * kWaves; ++e) rank += keys[e / 4][j + e % 4] > k ? 1 : 0;
             if (k && rank < a.top)
                 merged[rank] = k;
         }
         __syncthreads();
     }
     if (a.parts == 1) {
-        finish<T>(a, row, s, merged, tid);
+        finish(a, row, s, merged, tid, target, logit);
         return;
     }
     const int64_t p = row * a.parts + part;
@@ -288,31 +297,56 @@ __global__ void __launch_bounds__(kThreads) k_logprobs(Args a)
         a.list[p * a.top + tid] = merged[tid];
 }
 
-// The parts of a row, one a lane; the alternatives are the best of the parts' heads, one after another.
+// The parts of a row.  A value that `top` of the parts' best reach bounds what can be among the alternatives; what
+// reaches it is gathered and ranked.
 template <typename T>
-__global__ void __launch_bounds__(64) k_logprobs_join(Args a)
+__global__ void __launch_bounds__(kThreads) k_logprobs_join(Args a)
 {
-    __shared__ uint64_t merged[kMaxTop];
-    const int lane = threadIdx.x;
+    constexpr int kHold = 4;                   // keys a thread loads first
+    __shared__ uint64_t merged[kMaxTop], kept[kMaxParts * kMaxTop];
+    __shared__ int count;
+    const int tid = threadIdx.x, lane = tid & 63;
     const int64_t row = blockIdx.x, p = row * a.parts + lane;
+    const uint64_t *list = a.list + row * a.parts * a.top;
+    const int all = a.parts * a.top, target = target_of(a, row);
     Stat s{-FLT_MAX, 0.0f, 0.0f};
     if (lane < a.parts)
         s = Stat{a.stat[4 * p], a.stat[4 * p + 1], a.stat[4 * p + 2]};
+    const uint64_t head = a.top && lane < a.parts ? list[lane * a.top] : 0;
+    uint64_t mine[kHold];
+#pragma unroll
+    for (int h = 0; h < kHold; ++h) mine[h] = tid + h * kThreads < all ? list[tid + h * kThreads] : 0;
+    const float logit = target_logit<T>(a, row, target);
+    if (a.top) {
+        if (tid == 0)
+            count = 0;
+        if (tid < kMaxTop)
+            merged[tid] = 0;
+        __syncthreads();
+        const float bar = top_th(head ? key_value(head) : -INFINITY, a.top);
+        const auto keep = [&](uint64_t k) {
+            if (k && key_value(k) >= bar)
+                kept[atomicAdd(&count, 1)] = k;
+        };
+#pragma unroll
+        for (int h = 0; h < kHold; ++h) keep(mine[h]);
+        for (int e = tid + kHold * kThreads; e < all; e += kThreads) keep(list[e]);
+        __syncthreads();
+        const int n = count;
+        for (int e = tid; e < n; e += kThreads) {
+            const uint64_t k = kept[e];
+            int rank = 0;
+#pragma unroll 8
+            for (int l = 0; l < n; ++l) rank += kept[l] > k ? 1 : 0;
+            if (rank < a.top)
+                merged[rank] = k;
+        }
+        __syncthreads();
+    }
     rescale(s, wave_max(s.m));
     s.s = wave_sum(s.s);
     s.w = wave_sum(s.w);
-    const uint64_t *list = a.list + p * a.top;
-    uint64_t head = lane < a.parts && a.top ? list[0] : 0;
-    int at = 0;
-    for (int j = 0; j < a.top; ++j) {
-        const uint64_t k = wave_max_key(head);
-        if (lane == 0)
-            merged[j] = k;
-        if (k && head == k)
-            head = ++at < a.top ? list[at] : 0;
-    }
-    __syncthreads();
-    finish<T>(a, row, s, merged, lane);
+    finish(a, row, s, merged, tid, target, logit);
 }
 
 // The logits' gradient: a part of a row for each workgroup, read and written once.
@@ -366,20 +400,24 @@ int elem_size(qlin_row_type rt)
     return rt == QLIN_ROW_F32 ? 4 : rt == QLIN_ROW_BF16 || rt == QLIN_ROW_F16 ? 2 : 0;
 }
 
-// Parts of a row: enough workgroups for the GPU where there are few rows, each of a chunk at least.
+// Parts of a row: enough workgroups for the GPU where there are few rows, each of whole pieces a thread, and of
+// whole turns of kPieces where it has several.
 int row_parts(int es, int64_t rows, int64_t V)
 {
-    const int64_t chunk = 16 / es * kThreads, most = std::min<int64_t>((V + chunk - 1) / chunk, kMaxParts);
-    return (int)std::max<int64_t>(1, std::min(most, 1024 / std::max<int64_t>(rows, 1)));
+    const int64_t chunk = 16 / es * kThreads, pieces = (V + chunk - 1) / chunk;
+    const int64_t want = std::max<int64_t>(1, std::min<int64_t>(kRowBlocks / std::max<int64_t>(rows, 1), kMaxParts));
+    int64_t per = (pieces + want - 1) / want;
+    if (per > kPieces)
+        per = (per + kPieces - 1) / kPieces * kPieces;
+    return (int)((pieces + per - 1) / per);
 }
 
-// Elements of each part, whole 16-byte pieces, and the parts that then have any.
-void divide(Args &a, int es, int parts)
+// Elements of each part, whole pieces of a workgroup's threads, and the parts that then have any.
+void divide(Args &a, int es, int64_t parts)
 {
-    const int E = 16 / es, pieces = (a.V + E - 1) / E;
-    const int per = (pieces + parts - 1) / parts;
-    a.per = per * E;
-    a.parts = (pieces + per - 1) / per;
+    const int64_t chunk = 16 / es * kThreads, pieces = (a.V + chunk - 1) / chunk, per = (pieces + parts - 1) / parts;
+    a.per = (int)std::min<int64_t>(per * chunk, a.V);
+    a.parts = (int)((pieces + per - 1) / per);
 }
 
 qlin_status check(qlin_row_type rt, int32_t id_bits, int64_t rows, int64_t V, const void *x, int64_t ld,
@@ -412,7 +450,7 @@ hipError_t launch_forward(const Args &a, int64_t rows, hipStream_t s)
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.parts == 1)
         return e;
-    hipLaunchKernelGGL((k_logprobs_join<T>), dim3((unsigned)rows), dim3(64), 0, s, a);
+    hipLaunchKernelGGL((k_logprobs_join<T>), dim3((unsigned)rows), dim3(kThreads), 0, s, a);
     return hipGetLastError();
 }
 
@@ -512,7 +550,7 @@ qlin_status qlin_token_logprobs_backward(qlin_row_type rt, int32_t id_bits, int6
     a.id_bits = id_bits;
     // a chunk for each workgroup, as far as the rows leave a launch room for them
     const int64_t chunk = 16 / es * kThreads * kPieces, most = (((int64_t)1 << 24) - 1) / rows;
-    divide(a, es, (int)std::max<int64_t>(1, std::min((V + chunk - 1) / chunk, most)));
+    divide(a, es, std::max<int64_t>(1, std::min((V + chunk - 1) / chunk, most)));
     hipStream_t s = static_cast<hipStream_t>(stream);
     const hipError_t e = rt == QLIN_ROW_F32 ? launch_backward<float>(a, rows, s)
                          : rt == QLIN_ROW_BF16 ? launch_backward<uint16_t>(a, rows, s)
