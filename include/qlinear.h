@@ -530,9 +530,9 @@ qlin_status qlin_token_logprobs_backward(qlin_row_type rt, int32_t id_bits, int6
  * type ot.  Products are fp32, rounded once.
  *
  * Its gradient, dTable[v] = scale * sum_{t: ids[t] = v} dOut[t]: the positions
- * are sorted by token and each token's rows added in fp32, in their order (in
- * groups of 16 sorted positions), and rounded once; results do not depend on
- * timing.  Every row of dTable is written, those of no position with zeros;
+ * are sorted by token and each token's rows added in fp32 (sixteen sorted
+ * positions in order, then those sums in four shares) and rounded once; results
+ * do not depend on timing.  Every row of dTable is written, those of no position with zeros;
  * with `accumulate` only rows with positions are, and their sum is added to
  * what they hold.  dTable is of type ot: dOut's type rt, or fp32.
  *
@@ -542,7 +542,7 @@ qlin_status qlin_token_logprobs_backward(qlin_row_type rt, int32_t id_bits, int6
  *
  * Shapes: 0 <= tokens < 2^30, 0 < vocab < 2^31, 0 < width <= 2^20; of the
  * gradient tokens < 2^28, vocab < 2^22 and
- * ceil(tokens / 16) * ceil(width / 1024) < 2^24.  workspace:
+ * ceil(tokens / 16) * ceil(width / 256) < 2^24.  workspace:
  * the size below, 16-byte aligned, any contents, not used by two calls that may
  * overlap in time.  The calls are asynchronous on `stream` and allocate
  * nothing.  Errors as for qlin_scaled_mm. */

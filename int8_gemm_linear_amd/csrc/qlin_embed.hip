@@ -105,22 +105,48 @@ __global__ void __launch_bounds__(kThreads) k_embedding(LookArgs a)
 }
 
 // ---------------------------------------------------------------------------
-// Sort of positions by token: least significant digit first, a counting sort
-// a digit.  As pairs (key, position); the key of a position without a row is
-// the vocabulary's size, which comes last.
+// Sort of positions by token: least significant digit first, a counting sort a digit.  As pairs (key, position);
+// the key of a position without a row is the vocabulary's size, which comes last.  Its launches are short and
+// leave most of the GPU idle: the table's zeros are written beside them, a share in each.
 // ---------------------------------------------------------------------------
-constexpr int kDigitBits = 11, kDigits = 1 << kDigitBits;
+constexpr int kDigitBits = 11;
 constexpr int kSortWaves = 8, kSortThreads = 64 * kSortWaves;
-constexpr int64_t kSortOne = 4096;             // positions up to which one workgroup sorts alone
+constexpr int kSortOne = 4096;                 // positions up to which one workgroup sorts alone
 constexpr int kSortBlock = 2048;               // positions of a workgroup otherwise, until
 constexpr int kSortMaxBlocks = 256;            // there would be more workgroups than this
+
+// Zeros in rows `from` .. `to` - 1 of `width` elements, the last of all (`rows` - 1) of `last`; in workgroups behind
+// the `skip` that have other work.
+struct FillArgs {
+    uint8_t *out;
+    int64_t ldo, rows, from, to;               // ldo in bytes
+    int width, last, size, skip;               // size: bytes of an element
+};
+
+__device__ inline void fill(const FillArgs &f)
+{
+    for (int64_t row = f.from + blockIdx.x - f.skip; row < f.to; row += gridDim.x - f.skip) {
+        uint8_t *o = f.out + row * f.ldo;
+        const int64_t end = (int64_t)(row == f.rows - 1 ? f.last : f.width) * f.size;
+        for (int64_t at = threadIdx.x * 16; at < end; at += blockDim.x * 16) {
+            if (at + 16 <= end) {
+                const v4i z{0, 0, 0, 0};
+                __builtin_memcpy(o + at, &z, 16);
+            } else {
+                for (int64_t j = at; j < end; j += 2) *reinterpret_cast<uint16_t *>(o + j) = 0;
+            }
+        }
+    }
+}
+
+__global__ void __launch_bounds__(kSortThreads) k_fill(FillArgs f) { fill(f); }
 
 struct SortArgs {
     const void *ids;           // the first digit's input, or NULL
     const int2 *in;            // the later ones'
     int2 *out;
     int32_t *counts;           // [blocks][digits], or NULL for one workgroup
-    int n, per_block, vocab, id_bits;
+    int n, per_block, blocks, vocab, id_bits;
     int shift, digits;         // digit = (key >> shift) % digits, a power of two
 };
 
@@ -133,12 +159,17 @@ __device__ inline int2 pair_at(const SortArgs &a, int i)
 }
 
 // Positions per digit of each workgroup's range (integer atomics: their order does not matter).
-__global__ void __launch_bounds__(kSortThreads) k_sort_count(SortArgs a)
+__global__ void __launch_bounds__(kSortThreads) k_sort_count(SortArgs a, FillArgs f)
 {
-    __shared__ int32_t hist[kDigits];
+    extern __shared__ int32_t hist[];
+    if ((int)blockIdx.x >= a.blocks) {
+        fill(f);
+        return;
+    }
     for (int d = threadIdx.x; d < a.digits; d += kSortThreads) hist[d] = 0;
     __syncthreads();
     const int beg = (int)min((int64_t)blockIdx.x * a.per_block, (int64_t)a.n), end = min(beg + a.per_block, a.n);
+#pragma unroll 4
     for (int i = beg + threadIdx.x; i < end; i += kSortThreads)
         atomicAdd(&hist[(pair_at(a, i).x >> a.shift) & (a.digits - 1)], 1);
     __syncthreads();
@@ -146,23 +177,27 @@ __global__ void __launch_bounds__(kSortThreads) k_sort_count(SortArgs a)
         a.counts[(int64_t)blockIdx.x * a.digits + d] = hist[d];
 }
 
-// A wave owns a contiguous part of the workgroup's range; a pair's place is the first place of its digit for
-// the wave, plus those of the wave before it, 64 at a time, plus the lower lanes with its digit.
-__global__ void __launch_bounds__(kSortThreads) k_sort_place(SortArgs a)
+// LDS of `digits`: [waves][digits], twice [digits].
+constexpr size_t place_lds(int digits) { return (size_t)(kSortWaves + 2) * digits * sizeof(int32_t); }
+
+// One digit: get(i) is pair i, put(place, pair) takes it.  A wave owns a contiguous part of the workgroup's range; a
+// pair's place is the first place of its digit for the wave, plus those of the wave before it, 64 at a time, plus the
+// lower lanes with its digit.
+template <typename Get, typename Put>
+__device__ inline void place(const SortArgs &a, int shift, int digits, int32_t *hist, Get get, Put put)
 {
-    __shared__ int32_t hist[kSortWaves * kDigits];
-    __shared__ int32_t total[kDigits], before[kDigits];
     __shared__ int32_t wave_total[kSortWaves];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, mask = a.digits - 1;
+    int32_t *total = hist + kSortWaves * digits, *before = total + digits;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, mask = digits - 1;
     const int part = a.per_block / kSortWaves;
     const int beg = (int)min((int64_t)blockIdx.x * a.per_block + wave * part, (int64_t)a.n), end = min(beg + part, a.n);
-    for (int i = tid; i < kSortWaves * a.digits; i += kSortThreads) hist[i] = 0;
-    for (int i = tid; i < a.digits; i += kSortThreads) total[i] = before[i] = 0;
+    for (int i = tid; i < (kSortWaves + 2) * digits; i += kSortThreads) hist[i] = 0;
     __syncthreads();
-    int32_t *mine = hist + wave * a.digits;
-    for (int i = beg + lane; i < end; i += 64) atomicAdd(&mine[(pair_at(a, i).x >> a.shift) & mask], 1);
+    int32_t *mine = hist + wave * digits;
+#pragma unroll 4
+    for (int i = beg + lane; i < end; i += 64) atomicAdd(&mine[(get(i).x >> shift) & mask], 1);
     if (a.counts) {
-        const int all = gridDim.x * a.digits, earlier = blockIdx.x * a.digits;
+        const int all = a.blocks * digits, earlier = blockIdx.x * digits;
 #pragma unroll 4
         for (int i = tid; i < all; i += kSortThreads) {
             const int c = a.counts[i];
@@ -174,12 +209,12 @@ __global__ void __launch_bounds__(kSortThreads) k_sort_place(SortArgs a)
         }
     }
     __syncthreads();
-    const int each = (a.digits + kSortThreads - 1) / kSortThreads;
-    const int d0 = min(tid * each, a.digits), d1 = min(d0 + each, a.digits);
+    const int each = (digits + kSortThreads - 1) / kSortThreads;
+    const int d0 = min(tid * each, digits), d1 = min(d0 + each, digits);
     int sum = 0;
     for (int d = d0; d < d1; ++d) {
         if (!a.counts)
-            for (int w = 0; w < kSortWaves; ++w) total[d] += hist[w * a.digits + d];
+            for (int w = 0; w < kSortWaves; ++w) total[d] += hist[w * digits + d];
         sum += total[d];
     }
     const int scan = wave_scan(sum);
@@ -191,18 +226,18 @@ __global__ void __launch_bounds__(kSortThreads) k_sort_place(SortArgs a)
     for (int d = d0; d < d1; ++d) {
         int at = first + before[d];
         for (int w = 0; w < kSortWaves; ++w) {
-            const int c = hist[w * a.digits + d];
-            hist[w * a.digits + d] = at;
+            const int c = hist[w * digits + d];
+            hist[w * digits + d] = at;
             at += c;
         }
         first += total[d];
     }
     __syncthreads();
-    const int bits = __ffs(a.digits) - 1;
+    const int bits = __ffs(digits) - 1;
     for (int i = beg; i < end; i += 64) {
         const bool there = i + lane < end;
-        const int2 p = there ? pair_at(a, i + lane) : make_int2(0, 0);
-        const int d = (p.x >> a.shift) & mask;
+        const int2 p = there ? get(i + lane) : make_int2(0, 0);
+        const int d = (p.x >> shift) & mask;
         uint64_t same = __ballot(there);
         same = there ? same : ~same;
         for (int b = 0; b < bits; ++b) {
@@ -215,14 +250,43 @@ __global__ void __launch_bounds__(kSortThreads) k_sort_place(SortArgs a)
             at = atomicAdd(&mine[d], __popcll(same));
         at = __shfl(at, lead);
         if (there)
-            a.out[at + __popcll(same & (((uint64_t)1 << lane) - 1))] = p;
+            put(at + __popcll(same & (((uint64_t)1 << lane) - 1)), p);
     }
+}
+
+__global__ void __launch_bounds__(kSortThreads) k_sort_place(SortArgs a, FillArgs f)
+{
+    extern __shared__ int32_t hist[];
+    if ((int)blockIdx.x >= a.blocks) {
+        fill(f);
+        return;
+    }
+    place(a, a.shift, a.digits, hist, [&](int i) { return pair_at(a, i); }, [&](int at, int2 p) { a.out[at] = p; });
+}
+
+// Few positions: both digits (of `low` bits, and the others) in one launch, the pairs in LDS between them.
+__global__ void __launch_bounds__(kSortThreads) k_sort_one(SortArgs a, int high, FillArgs f)
+{
+    extern __shared__ int32_t hist[];
+    __shared__ int2 pairs[kSortOne];
+    if (blockIdx.x > 0) {
+        fill(f);
+        return;
+    }
+    if (high == 1) {
+        place(a, 0, a.digits, hist, [&](int i) { return pair_at(a, i); }, [&](int at, int2 p) { a.out[at] = p; });
+        return;
+    }
+    place(a, 0, a.digits, hist, [&](int i) { return pair_at(a, i); }, [&](int at, int2 p) { pairs[at] = p; });
+    __syncthreads();
+    place(a, a.shift, high, hist, [&](int i) { return pairs[i]; }, [&](int at, int2 p) { a.out[at] = p; });
 }
 
 // ---------------------------------------------------------------------------
 // Sums of the sorted positions' rows
 // ---------------------------------------------------------------------------
 constexpr int kChunk = 16;     // sorted positions of a workgroup
+constexpr int kAtOnce = 8;     // of them whose rows are on their way together
 
 struct SumArgs {
     const int2 *pairs;         // sorted
@@ -234,63 +298,54 @@ struct SumArgs {
     int n, vocab, width, add;
 };
 
-// Zeros in `rows` rows of `width` elements, the last of them of `last`.
-template <typename O>
-__global__ void __launch_bounds__(kThreads) k_fill(uint8_t *out, int64_t ldo, int64_t rows, int width, int last)
+// The n first of E elements as fp32, the others 0.
+template <typename T, int E>
+__device__ inline void load_values(float (&v)[E], const T *p, int n)
 {
-    constexpr int E = 16 / sizeof(O);
-    for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
-        O *o = reinterpret_cast<O *>(out + row * ldo);
-        const int end = row == rows - 1 ? last : width;
-        for (int at = threadIdx.x * E; at < end; at += kThreads * E) {
-            if (at + E <= end) {
-                const v4i z{0, 0, 0, 0};
-                __builtin_memcpy(o + at, &z, 16);
-            } else {
-                for (int j = at; j < end; ++j) o[j] = Elem<O>::put(0.0f);
-            }
-        }
-    }
-}
-
-template <typename T>
-__device__ inline void load_values(float (&v)[4], const T *p, int n)
-{
-    if (n == 4) {
-        T t[4];
+    T t[E];
+    if (n == E) {
         __builtin_memcpy(t, p, sizeof(t));
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = Elem<T>::get(t[i]);
     } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = i < n ? Elem<T>::get(p[i]) : 0.0f;
+        for (int i = 0; i < E; ++i) t[i] = i < n ? p[i] : Elem<T>::put(0.0f);
     }
+#pragma unroll
+    for (int i = 0; i < E; ++i) v[i] = Elem<T>::get(t[i]);
+}
+
+template <typename T, int E>
+__device__ inline void store_values(T *p, const float (&v)[E], int n)
+{
+    T t[E];
+#pragma unroll
+    for (int i = 0; i < E; ++i) t[i] = Elem<T>::put(v[i]);
+    if (n == E)
+        __builtin_memcpy(p, t, sizeof(t));
+    else
+#pragma unroll
+        for (int i = 0; i < E; ++i)
+            if (i < n)
+                p[i] = t[i];
 }
 
 // A token's sum to its row of the table (added to what it holds where the caller wants that).
-template <typename O>
-__device__ inline void store_row(const SumArgs &a, int row, int at, int n, const float (&sum)[4])
+template <typename O, int E>
+__device__ inline void store_row(const SumArgs &a, int row, int at, int n, const float (&sum)[E])
 {
     O *o = reinterpret_cast<O *>(a.out + row * a.ldo) + at;
-    float v[4];
+    float v[E] = {};
     if (a.add)
-        load_values<O>(v, o, n);
-    O t[4];
+        load_values<O, E>(v, o, n);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) t[i] = Elem<O>::put(a.add ? fmaf(sum[i], a.factor, v[i]) : sum[i] * a.factor);
-    if (n == 4)
-        __builtin_memcpy(o, t, sizeof(t));
-    else
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (i < n)
-                o[i] = t[i];
+    for (int i = 0; i < E; ++i) v[i] = a.add ? fmaf(sum[i], a.factor, v[i]) : sum[i] * a.factor;
+    store_values<O, E>(o, v, n);
 }
 
-// kChunk sorted positions and 4 kThreads columns a workgroup.
+// kChunk sorted positions and 16 bytes of a row for each thread a workgroup.
 template <typename T, typename O>
 __global__ void __launch_bounds__(kThreads) k_sum(SumArgs a)
 {
+    constexpr int E = 16 / sizeof(T);
     __shared__ int2 pair[kChunk + 2];          // with the neighbours on both sides
     const int first = blockIdx.x * kChunk, count = min(kChunk, a.n - first);
     if (threadIdx.x < kChunk + 2) {
@@ -298,79 +353,100 @@ __global__ void __launch_bounds__(kThreads) k_sum(SumArgs a)
         pair[threadIdx.x] = i >= 0 && i < a.n ? a.pairs[i] : make_int2(-1, 0);
     }
     __syncthreads();
-    const int at = (blockIdx.y * kThreads + threadIdx.x) * 4, n = min(4, a.width - at);
+    const int at = (blockIdx.y * kThreads + threadIdx.x) * E, n = min(E, a.width - at);
     if (n <= 0)
         return;
-    float sum[4] = {};
+    float sum[E] = {};
     int began = 0;                             // where the run began
-    for (int j = 0; j < count; j += 4) {
-        float v[4][4];
+#pragma unroll 1
+    for (int j = 0; j < count; j += kAtOnce) {
+        v4i t[kAtOnce];                        // (as they come: values taken out here would wait for each load)
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
-            if (j + u < count && pair[j + u + 1].x < a.vocab)
-                load_values<T>(v[u], reinterpret_cast<const T *>(a.dout + pair[j + u + 1].y * a.ldd) + at, n);
+        for (int u = 0; u < kAtOnce; ++u) {
+            t[u] = v4i{0, 0, 0, 0};
+            if (j + u < count && pair[j + u + 1].x < a.vocab) {
+                const T *p = reinterpret_cast<const T *>(a.dout + pair[j + u + 1].y * a.ldd) + at;
+                if (n == E) {
+                    t[u] = load_piece(p);
+                } else {
+                    T e[E];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const int p = j + u + 1, key = pair[p].x;
-            if (j + u >= count || key >= a.vocab)
+                    for (int i = 0; i < E; ++i) e[i] = i < n ? p[i] : Elem<T>::put(0.0f);
+                    __builtin_memcpy(&t[u], e, 16);
+                }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u) {
+            const int p = j + u + 1, key = j + u < count ? pair[p].x : a.vocab;
+            if (key >= a.vocab)
                 continue;
+            float v[E];
+            piece_values<T>(v, t[u]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) sum[i] += v[u][i];
+            for (int i = 0; i < E; ++i) sum[i] += v[i];
             const bool ends = pair[p + 1].x != key;
             if (!ends && j + u + 1 < count)
                 continue;
             const bool came = began == 0 && pair[0].x == key;
-            if (ends && !came) {
-                store_row<O>(a, key, at, n, sum);
-            } else {
-                float *to = a.part + ((int64_t)blockIdx.x * 2 + (came ? 0 : 1)) * a.width + at;
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (i < n)
-                        to[i] = sum[i];
-            }
+            if (ends && !came)
+                store_row<O, E>(a, key, at, n, sum);
+            else
+                store_values<float, E>(a.part + ((int64_t)blockIdx.x * 2 + (came ? 0 : 1)) * a.width + at, sum, n);
             began = j + u + 1;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) sum[i] = 0.0f;
+            for (int i = 0; i < E; ++i) sum[i] = 0.0f;
         }
     }
 }
 
-// The runs that cross chunks: the workgroup of the chunk where one begins adds its parts in order.
+// The runs that cross chunks: the workgroup of the chunk where one begins adds its parts, each wave a share of them in
+// order (a token of 950 positions has 60), then the waves' sums in order.
+constexpr int kJoinWaves = 4, kJoinWidth = 256;
+
 template <typename O>
-__global__ void __launch_bounds__(kThreads) k_join(SumArgs a)
+__global__ void __launch_bounds__(64 * kJoinWaves) k_join(SumArgs a)
 {
+    __shared__ float sums[kJoinWaves][kJoinWidth];
     const int last = (blockIdx.x + 1) * kChunk - 1;         // the chunk's last position
     if (last + 1 >= a.n)
         return;
-    const int key = a.pairs[last].x, before = blockIdx.x ? a.pairs[last - kChunk].x : -1;
-    if (key >= a.vocab || a.pairs[last + 1].x != key || before == key)
+    const int key = a.pairs[last].x, next = a.pairs[last + 1].x, before = blockIdx.x ? a.pairs[last - kChunk].x : -1;
+    if (key >= a.vocab || next != key || before == key)
         return;                                             // (a run that fills the chunk began in an earlier one)
     // the chunks that begin with the token, counted 64 at a time
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     int parts = 0;
     for (int more = 64; more == 64; parts += more) {
-        const int64_t i = last + 1 + (int64_t)(parts + (threadIdx.x & 63)) * kChunk;
+        const int64_t i = last + 1 + (int64_t)(parts + lane) * kChunk;
         more = __popcll(__ballot(i < a.n && a.pairs[i].x == key));
     }
-    const int at = (blockIdx.y * kThreads + threadIdx.x) * 4, n = min(4, a.width - at);
-    if (n <= 0)
+    const int at = blockIdx.y * kJoinWidth + lane * 4, n = min(4, a.width - at);
+    // part 0 is the run's beginning in this chunk, part p its piece in the p-th chunk behind
+    const int share = (parts + kJoinWaves) / kJoinWaves, end = min((wave + 1) * share, parts + 1);
+    float sum[4] = {};
+    if (n > 0)
+        for (int j = wave * share; j < end; j += 8) {
+            float v[8][4];
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                if (j + u < end)
+                    load_values<float, 4>(v[u], a.part + ((int64_t)(blockIdx.x + j + u) * 2 + (j + u == 0 ? 1 : 0)) * a.width + at, n);
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                if (j + u < end)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) sum[i] += v[u][i];
+        }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sums[wave][4 * lane + i] = sum[i];
+    __syncthreads();
+    if (wave > 0 || n <= 0)
         return;
-    float sum[4];
-    load_values<float>(sum, a.part + ((int64_t)blockIdx.x * 2 + 1) * a.width + at, n);
-    const float *p = a.part + (int64_t)(blockIdx.x + 1) * 2 * a.width + at;
-    for (int j = 0; j < parts; j += 4) {
-        float v[4][4];
+    for (int w = 1; w < kJoinWaves; ++w)
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
-            if (j + u < parts)
-                load_values<float>(v[u], p + (int64_t)(j + u) * 2 * a.width, n);
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-            if (j + u < parts)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) sum[i] += v[u][i];
-    }
-    store_row<O>(a, key, at, n, sum);
+        for (int i = 0; i < 4; ++i) sum[i] += sums[w][4 * lane + i];
+    store_row<O, 4>(a, key, at, n, sum);
 }
 
 int sort_blocks(int64_t n)
@@ -379,7 +455,7 @@ int sort_blocks(int64_t n)
 }
 
 int64_t chunks(int64_t n) { return (n + kChunk - 1) / kChunk; }
-int64_t column_blocks(int64_t width) { return (width + 4 * kThreads - 1) / (4 * kThreads); }
+int64_t column_blocks(int64_t width) { return (width + 255) / 256; }           // of the join, the most
 
 // A launch has fewer than 2^32 threads.
 bool sums_fit(int64_t n, int64_t width) { return chunks(n) * column_blocks(width) < (int64_t)1 << 24; }
@@ -390,62 +466,99 @@ bool backward_shape(int64_t n, int64_t vocab, int64_t width)
            sums_fit(n, width);
 }
 
+// Digits of the sort: passes of `low` bits and the others.
+struct Digits {
+    int passes, low, bits;
+};
+
+Digits digits_of(int64_t vocab)
+{
+    Digits d{1, 0, 0};
+    while (((int64_t)1 << d.bits) <= vocab) ++d.bits;       // keys 0 .. vocab
+    d.passes = d.bits > kDigitBits ? 2 : 1;
+    d.low = (d.bits + d.passes - 1) / d.passes;
+    return d;
+}
+
 // Two buffers of pairs, the counts and the partial sums.
 struct Space {
     size_t pairs, counts, part, bytes;
 };
 
-Space space(int64_t n, int64_t width)
+Space space(int64_t n, int64_t vocab, int64_t width)
 {
     Space s;
     s.pairs = ((size_t)n * sizeof(int2) + 15) / 16 * 16;
-    s.counts = sort_blocks(n) > 1 ? (size_t)sort_blocks(n) * kDigits * sizeof(int32_t) : 0;
+    s.counts = sort_blocks(n) > 1 ? ((size_t)sort_blocks(n) << digits_of(vocab).low) * sizeof(int32_t) : 0;
+    s.counts = (s.counts + 15) / 16 * 16;
     s.part = (size_t)chunks(n) * 2 * width * sizeof(float);
     s.bytes = 2 * s.pairs + s.counts + s.part;
     return s;
 }
 
-// The sorted pairs lie in the returned buffer, a or b.
-hipError_t launch_sort(const void *ids, int32_t id_bits, int64_t n, int64_t vocab, int2 *a, int2 *b, int32_t *counts,
-                       hipStream_t s, int2 **sorted)
+// Workgroups that write zeros beside `blocks` others, and their share of the rows.
+constexpr int kFillBlocks = 2048;
+
+FillArgs share_of(FillArgs f, int part, int parts, int blocks)
 {
-    int bits = 0;
-    while (((int64_t)1 << bits) <= vocab) ++bits;           // keys 0 .. vocab
-    const int passes = bits > kDigitBits ? 2 : 1, low = (bits + passes - 1) / passes;
+    f.from = f.rows * part / parts;
+    f.to = f.rows * (part + 1) / parts;
+    f.skip = blocks;
+    return f;
+}
+
+int fill_blocks(const FillArgs &f) { return (int)std::min<int64_t>(f.to - f.from, kFillBlocks); }
+
+// The sorted pairs lie in the returned buffer, a or b.  `f` is filled by the launches together (no rows: none).
+hipError_t launch_sort(const void *ids, int32_t id_bits, int64_t n, int64_t vocab, int2 *a, int2 *b, int32_t *counts,
+                       const FillArgs &f, hipStream_t s, int2 **sorted)
+{
+    const Digits d = digits_of(vocab);
     const int blocks = sort_blocks(n);
     int64_t per = (n + blocks - 1) / blocks;
     per = (per + kSortThreads - 1) / kSortThreads * kSortThreads;
-    int2 *from = nullptr, *to = a;
-    for (int p = 0; p < passes; ++p) {
-        const int width = p == 0 ? low : bits - low;
-        SortArgs sa{p == 0 ? ids : nullptr, from, to, blocks > 1 ? counts : nullptr, (int)n, (int)per, (int)vocab,
-                    id_bits, p * low, 1 << width};
-        if (blocks > 1) {
-            hipLaunchKernelGGL(k_sort_count, dim3(blocks), dim3(kSortThreads), 0, s, sa);
-            const hipError_t e = hipGetLastError();
-            if (e != hipSuccess)
-                return e;
-        }
-        hipLaunchKernelGGL(k_sort_place, dim3(blocks), dim3(kSortThreads), 0, s, sa);
-        const hipError_t e = hipGetLastError();
+    SortArgs sa{ids, nullptr, a, blocks > 1 ? counts : nullptr, (int)n, (int)per, blocks, (int)vocab, id_bits, 0, 1 << d.low};
+    *sorted = a;
+    if (blocks == 1) {
+        const FillArgs g = share_of(f, 0, 1, 1);
+        sa.shift = d.low;
+        hipLaunchKernelGGL(k_sort_one, dim3(1 + fill_blocks(g)), dim3(kSortThreads), place_lds(1 << d.low), s, sa,
+                           1 << (d.bits - d.low), g);
+        return hipGetLastError();
+    }
+    for (int p = 0; p < d.passes; ++p) {
+        FillArgs g = share_of(f, 2 * p, 2 * d.passes, blocks);
+        hipLaunchKernelGGL(k_sort_count, dim3(blocks + fill_blocks(g)), dim3(kSortThreads), sa.digits * sizeof(int32_t), s,
+                           sa, g);
+        hipError_t e = hipGetLastError();
         if (e != hipSuccess)
             return e;
-        from = to;
-        to = to == a ? b : a;
+        g = share_of(f, 2 * p + 1, 2 * d.passes, blocks);
+        hipLaunchKernelGGL(k_sort_place, dim3(blocks + fill_blocks(g)), dim3(kSortThreads), place_lds(sa.digits), s, sa, g);
+        e = hipGetLastError();
+        if (e != hipSuccess)
+            return e;
+        *sorted = sa.out;
+        sa.ids = nullptr;
+        sa.in = sa.out;
+        sa.out = b;
+        sa.shift = d.low;
+        sa.digits = 1 << (d.bits - d.low);
     }
-    *sorted = from;
     return hipSuccess;
 }
 
 template <typename T, typename O>
 hipError_t launch_sums(const SumArgs &a, hipStream_t s)
 {
-    const dim3 grid((unsigned)chunks(a.n), (unsigned)column_blocks(a.width));
+    constexpr int kCols = 16 / sizeof(T) * kThreads;
+    const dim3 grid((unsigned)chunks(a.n), (unsigned)((a.width + kCols - 1) / kCols));
     hipLaunchKernelGGL((k_sum<T, O>), grid, dim3(kThreads), 0, s, a);
-    hipError_t e = hipGetLastError();
+    const hipError_t e = hipGetLastError();
     if (e != hipSuccess || grid.x == 1)
         return e;
-    hipLaunchKernelGGL((k_join<O>), dim3(grid.x - 1, grid.y), dim3(kThreads), 0, s, a);
+    hipLaunchKernelGGL((k_join<O>), dim3(grid.x - 1, (unsigned)((a.width + kJoinWidth - 1) / kJoinWidth)),
+                       dim3(64 * kJoinWaves), 0, s, a);
     return hipGetLastError();
 }
 
@@ -532,7 +645,7 @@ qlin_status qlin_embedding(qlin_table_type tt, qlin_row_type ot, int32_t id_bits
 
 size_t qlin_embedding_backward_workspace_size(int64_t tokens, int64_t vocab, int64_t width)
 {
-    return tokens > 0 && backward_shape(tokens, vocab, width) ? space(tokens, width).bytes : 0;
+    return tokens > 0 && backward_shape(tokens, vocab, width) ? space(tokens, vocab, width).bytes : 0;
 }
 
 qlin_status qlin_embedding_backward(qlin_row_type rt, qlin_row_type ot, int32_t id_bits, int64_t tokens,
@@ -555,29 +668,31 @@ qlin_status qlin_embedding_backward(qlin_row_type rt, qlin_row_type ot, int32_t 
     if (need && (!workspace || workspace_bytes < need))
         return QLIN_ERR_WORKSPACE;
     hipStream_t s = static_cast<hipStream_t>(stream);
+    FillArgs f{};
     if (!accumulate) {
-        // (rows without gaps are one long row)
+        // (rows without gaps are as rows of 16384)
         const bool whole = ldt == width;
-        const int64_t all = vocab * width, row = whole ? 16384 : width, rows = (all + row - 1) / row;
-        const int last = (int)(whole ? all - (rows - 1) * row : width);
-        const dim3 grid((unsigned)std::min<int64_t>(rows, 1 << 20));
-        uint8_t *out = static_cast<uint8_t *>(dTable);
-        const int64_t apart = (whole ? row : ldt) * os;
-        if (os == 4)
-            hipLaunchKernelGGL((k_fill<float>), grid, dim3(kThreads), 0, s, out, apart, rows, (int)row, last);
-        else
-            hipLaunchKernelGGL((k_fill<uint16_t>), grid, dim3(kThreads), 0, s, out, apart, rows, (int)row, last);
-        if (hipGetLastError() != hipSuccess)
-            return QLIN_ERR_HIP;
+        const int64_t all = vocab * width, row = whole ? 16384 : width;
+        f.out = static_cast<uint8_t *>(dTable);
+        f.ldo = (whole ? row : ldt) * os;
+        f.rows = (all + row - 1) / row;
+        f.width = (int)row;
+        f.last = (int)(all - (f.rows - 1) * row);
+        f.size = os;
     }
-    if (tokens == 0)
-        return QLIN_OK;
-    const Space sp = space(tokens, width);
+    if (tokens == 0) {
+        if (accumulate)
+            return QLIN_OK;
+        const FillArgs g = share_of(f, 0, 1, 0);
+        hipLaunchKernelGGL(k_fill, dim3(fill_blocks(g)), dim3(kSortThreads), 0, s, g);
+        return hipGetLastError() == hipSuccess ? QLIN_OK : QLIN_ERR_HIP;
+    }
+    const Space sp = space(tokens, vocab, width);
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     SumArgs a{};
     int2 *sorted = nullptr;
     if (launch_sort(ids, id_bits, tokens, vocab, reinterpret_cast<int2 *>(ws), reinterpret_cast<int2 *>(ws + sp.pairs),
-                    reinterpret_cast<int32_t *>(ws + 2 * sp.pairs), s, &sorted) != hipSuccess)
+                    reinterpret_cast<int32_t *>(ws + 2 * sp.pairs), f, s, &sorted) != hipSuccess)
         return QLIN_ERR_HIP;
     a.pairs = sorted;
     a.dout = static_cast<const uint8_t *>(dOut);
