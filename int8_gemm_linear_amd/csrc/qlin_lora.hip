@@ -216,31 +216,21 @@ __device__ inline int4 wave_plan(const Plan &p, int want, int &token)
 }
 
 // Up to 8192: every workgroup of the shrink kernel finds its tile, which takes it less time than a launch of its
-// own would take the call.  A wave owns a contiguous part of the tokens and keeps their bins.
-constexpr int kShrinkWaves = 16, kHold = 16;
+// own would take the call.  A wave owns a contiguous part of the tokens, keeps their bins and counts them for itself;
+// then each wave walks the bins, 64 at a time.
+constexpr int kHold = 16;
 constexpr int kSelfTokens = 64 * 8 * kHold;
 
-struct PlanShare {
-    int32_t sums[2][kShrinkWaves];
-    int4 tile;
-    int32_t bin, skip;                         // the tile's bin and its tokens before the tile
-    int32_t token[64];
-};
-
-// The tile `want`, its tokens in sh.token; `hist` [adapters + 1].  Called by all threads.
-__device__ inline int4 self_plan(const Plan &p, int want, int32_t *hist, PlanShare &sh)
+// The tile `want`; its tokens in `token` (LDS); `hist` [waves][adapters + 1] (LDS).  Called by all threads.
+__device__ inline int4 self_plan(const Plan &p, int want, int32_t *hist, int32_t *token)
 {
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, threads = blockDim.x, bins = p.adapters + 1;
-    const int turns = (p.tokens + threads - 1) / threads, beg = wave * turns * 64 + lane;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6, bins = p.adapters + 1;
+    const int turns = (p.tokens + (int)blockDim.x - 1) / (int)blockDim.x, beg = wave * turns * 64 + lane;
     int held[kHold];
 #pragma unroll
     for (int h = 0; h < kHold; ++h) held[h] = h < turns && beg + 64 * h < p.tokens ? bin_of(p, beg + 64 * h) : -1;
-    for (int b = tid; b < bins; b += threads) hist[b] = 0;
-    if (tid == 0) {
-        sh.tile = make_int4(-1, 0, 0, 0);
-        sh.bin = -1;
-    }
-    __syncthreads();
+    int32_t *mine = hist + wave * bins;
+    for (int b = lane; b < bins; b += 64) mine[b] = 0;
 #pragma unroll
     for (int h = 0; h < kHold; ++h) {
         if (h >= turns)
@@ -251,69 +241,47 @@ __device__ inline int4 self_plan(const Plan &p, int want, int32_t *hist, PlanSha
         const int lead = __ffsll((unsigned long long)any) - 1, b = __builtin_amdgcn_readlane(held[h], lead);
         if (__ballot(held[h] == b) == any) {                // (one request's run: one addition for all)
             if (lane == lead)
-                atomicAdd(&hist[b], __popcll(any));
+                atomicAdd(&mine[b], __popcll(any));
         } else if (held[h] >= 0) {
-            atomicAdd(&hist[held[h]], 1);
+            atomicAdd(&mine[held[h]], 1);
         }
     }
     __syncthreads();
-    const int each = (bins + threads - 1) / threads;
-    const int b0 = min(tid * each, bins), b1 = min(b0 + each, bins);
-    int tokens = 0, tiles = 0;
-    for (int b = b0; b < b1; ++b) {
-        tokens += hist[b];
-        tiles += (hist[b] + p.tile - 1) / p.tile;
-    }
-    const int scan0 = wave_scan(tokens), scan1 = wave_scan(tiles);
-    if (lane == 63) {
-        sh.sums[0][wave] = scan0;
-        sh.sums[1][wave] = scan1;
-    }
-    __syncthreads();
-    int at = scan0 - tokens, tile = scan1 - tiles;
-    for (int w = 0; w < wave; ++w) {
-        at += sh.sums[0][w];
-        tile += sh.sums[1][w];
-    }
-    for (int b = b0; b < b1; ++b) {
-        const int n = hist[b], here = (n + p.tile - 1) / p.tile;
-        if (want >= tile && want < tile + here) {
-            sh.tile = tile_of(p, b, at, n, want - tile);
-            sh.bin = b;
-            sh.skip = (want - tile) * p.tile;
+    int4 found = make_int4(-1, 0, 0, 0);
+    int bin = -1, skip = 0;
+    const bool offsets = want == 0 && wave == 0 && p.offsets;
+    for (int b0 = 0, at0 = 0, tile0 = 0; b0 < bins && (offsets || bin < 0); b0 += 64) {
+        int n = 0;
+        if (b0 + lane < bins)
+            for (int w = 0; w < waves; ++w) n += hist[w * bins + b0 + lane];
+        const int tiles = (n + p.tile - 1) / p.tile, at = at0 + wave_scan(n) - n, tile = tile0 + wave_scan(tiles) - tiles;
+        if (offsets && b0 + lane < bins)
+            p.offsets[b0 + lane] = at;
+        const uint64_t here = __ballot(want >= tile && want < tile + tiles);
+        if (here) {
+            const int l = __ffsll((unsigned long long)here) - 1, j = want - __builtin_amdgcn_readlane(tile, l);
+            bin = b0 + l;
+            skip = j * p.tile;
+            found = tile_of(p, bin, __builtin_amdgcn_readlane(at, l), __builtin_amdgcn_readlane(n, l), j);
         }
-        if (want == 0 && p.offsets)
-            p.offsets[b] = at;
-        at += n;
-        tile += here;
+        at0 = __builtin_amdgcn_readlane(at + n, 63);
+        tile0 = __builtin_amdgcn_readlane(tile + tiles, 63);
     }
-    __syncthreads();
-    const int4 found = sh.tile;
-    const int bin = sh.bin, skip = sh.skip;
-    if (found.z == 0)
-        return found;
-    int before = 0;
-#pragma unroll
-    for (int h = 0; h < kHold; ++h) {
-        if (h >= turns)
-            break;
-        before += __popcll(__ballot(held[h] == bin));
-    }
-    if (lane == 0)
-        sh.sums[0][wave] = before;
-    __syncthreads();
+    if (bin < 0)
+        return found;                          // (in all waves)
     int rank = -skip;
-    for (int w = 0; w < wave; ++w) rank += sh.sums[0][w];
-    if (rank < found.z && rank + before > 0)
+    for (int w = 0; w < wave; ++w) rank += hist[w * bins + bin];
+    const int here = hist[wave * bins + bin];
+    if (rank < found.z && rank + here > 0)
 #pragma unroll
         for (int h = 0; h < kHold; ++h) {
             if (h >= turns)
                 break;
-            const uint64_t mine = __ballot(held[h] == bin);
-            const int r = rank + __popcll(mine & (((uint64_t)1 << lane) - 1));
+            const uint64_t same = __ballot(held[h] == bin);
+            const int r = rank + __popcll(same & (((uint64_t)1 << lane) - 1));
             if (held[h] == bin && r >= 0 && r < found.z)
-                sh.token[r] = beg + 64 * h;
-            rank += __popcll(mine);
+                token[r] = beg + 64 * h;
+            rank += __popcll(same);
         }
     __syncthreads();
     return found;
@@ -401,7 +369,7 @@ __global__ void __launch_bounds__((64 * shrink_waves<TB, RB>())) k_shrink(Shrink
     // a wave's share: a step's rows and weights, then its sums (16-byte pieces)
     constexpr int kShare = shrink_share(TB, RB);
     extern __shared__ v4i shared[];             // [waves][kShare], before that the plan's bins
-    __shared__ PlanShare sh;
+    __shared__ int32_t tokens[64];
     const int units = a.plan.max_tiles * a.groups;
     // (the longer job's workgroups come first)
     const int later = BACK && (int)blockIdx.x >= units, second = BACK && later != (a.job[1].K > a.job[0].K);
@@ -424,11 +392,11 @@ __global__ void __launch_bounds__((64 * shrink_waves<TB, RB>())) k_shrink(Shrink
             a.plan.order[tile.y + lane] = there;
     } else {
         if (a.self) {
-            tile = self_plan(a.plan, index, reinterpret_cast<int32_t *>(shared), sh);
+            tile = self_plan(a.plan, index, reinterpret_cast<int32_t *>(shared), tokens);
             if (publish && tid < tile.z)
-                a.plan.order[tile.y + tid] = sh.token[tid];
+                a.plan.order[tile.y + tid] = tokens[tid];
 #pragma unroll
-            for (int t = 0; t < TB; ++t) token[t] = tile.z ? sh.token[min(16 * t + i, tile.z - 1)] : 0;
+            for (int t = 0; t < TB; ++t) token[t] = tile.z ? tokens[min(16 * t + i, tile.z - 1)] : 0;
         } else {
             tile = a.plan.tiles[index];
 #pragma unroll
@@ -1091,7 +1059,8 @@ hipError_t launch_shrink(const Sizes &z, const ShrinkArgs &a, hipStream_t s)
 {
     const int waves = z.tb * z.rb <= 2 && z.max_tiles * z.groups <= 128 && a.splits == 1 ? 16 : 8;
     const dim3 grid((unsigned)(z.max_tiles * z.groups * (BACK ? 2 : a.splits))), block(64 * waves);
-    const size_t lds = std::max(waves * shrink_share(z.tb, z.rb) * sizeof(v4i), (kBins + 3) / 4 * sizeof(v4i));
+    const size_t lds = std::max(waves * shrink_share(z.tb, z.rb) * sizeof(v4i),
+                                a.self == 2 ? waves * (z.L + 1) * sizeof(int32_t) : 0);
     switch (z.rb * 8 + z.tb) {
     case 8 + 1: hipLaunchKernelGGL((k_shrink<1, 1, BACK>), grid, block, lds, s, a); break;
     case 8 + 2: hipLaunchKernelGGL((k_shrink<2, 1, BACK>), grid, block, lds, s, a); break;
