@@ -25,7 +25,9 @@ constexpr int kThreads = 256, kWaves = kThreads / 64;
 constexpr int kPieces = 4;                     // 16-byte pieces a thread takes at a time
 constexpr int kMaxTop = 64;                    // an alternative for each lane of a wave
 constexpr int kMaxParts = 64;                  // a part for each lane of the joining wave
-constexpr int64_t kRowBlocks = 2048;           // workgroups that rows are divided into where they are fewer
+// Workgroups that fewer rows are divided into: five run on a CU at once (48 rows of 100003, 5 alternatives: 13.9 us,
+// with 2048 workgroups 15.4; 512 rows of 131072, 20 alternatives 50.6 and 56).
+constexpr int64_t kRowBlocks = 1280;
 constexpr int64_t kMaxRows = (int64_t)1 << 23; // x parts: below 2^32 threads
 constexpr int64_t kMaxVocab = (int64_t)1 << 28;
 constexpr int64_t kMaxStride = (int64_t)1 << 31;
@@ -177,6 +179,10 @@ __global__ void __launch_bounds__(kThreads) k_logprobs(Args a)
     constexpr int E = 16 / sizeof(T), kStep = kThreads * E * kPieces;
     __shared__ uint64_t keys[TOP ? kWaves : 1][kMaxTop], merged[kMaxTop];
     __shared__ Stat stats[kWaves];
+    // For each wave a value that a quarter of `top` of its logits reach: the least of them bounds what can be among
+    // the alternatives (2047 rows of 131072, 20 alternatives: 122 us, with each wave's own list alone 146)
+    __shared__ float reached[kWaves];
+    const int quarter = (a.top + kWaves - 1) / kWaves;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int64_t row = blockIdx.x / a.parts;
     const int part = blockIdx.x % a.parts, beg = part * a.per, end = min(beg + a.per, a.V);
@@ -216,32 +222,46 @@ __global__ void __launch_bounds__(kThreads) k_logprobs(Args a)
             }
         }
         if (TOP) {
-            // Of the first chunk, the top-th best of the lanes' maxima bounds what can enter; later, a value
-            // has to be greater than the last of the list, whose index is lower.
-            float bar = best.bar;
-            bool open = best.last == 0;
-            if (c == beg)
-                bar = top_th(most, a.top);
+            // Of the first chunk, the lanes' maxima give the bound; later, a value also has to be greater than the
+            // last of the wave's list, whose index is lower.
+            if (c == beg) {
+                const float r = top_th(most, quarter);
+                if (lane == 0)
+                    reached[wave] = r;
+                __syncthreads();
+            }
+            float bound = INFINITY;
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) bound = fminf(bound, const_cast<volatile float *>(reached)[w]);
+            const float bar = best.bar;
+            const bool open = best.last == 0;
+            bool entered = false;
 #pragma unroll
             for (int u = 0; u < kPieces; ++u) {
                 if (u >= pieces)
                     break;
-                if (!__ballot(high[u] > bar || (open && high[u] >= bar)))
+                if (!__ballot(high[u] >= bound && (open || high[u] > bar)))
                     continue;
                 const int at = c + (u * kThreads + tid) * E;
 #pragma unroll
                 for (int i = 0; i < E; ++i) {
-                    const uint64_t k = at + i < end && v[u][i] >= bar ? key_of(v[u][i], at + i) : 0;
+                    const uint64_t k = at + i < end && v[u][i] >= bound ? key_of(v[u][i], at + i) : 0;
                     uint64_t in = __ballot(k > best.last);
                     while (in) {
                         const uint64_t one = key_lane(k, __ffsll((unsigned long long)in) - 1);
                         best.insert(one, lane, a.top);
+                        entered = true;
                         in &= in - 1;
                         in &= __ballot(k > best.last);
                     }
                 }
             }
-            best.bar = best.last ? key_value(best.last) : -INFINITY;
+            if (entered) {
+                best.bar = best.last ? key_value(best.last) : -INFINITY;
+                const uint64_t k = key_lane(best.mine, quarter - 1);
+                if (k && lane == 0)
+                    const_cast<volatile float *>(reached)[wave] = fmaxf(key_value(k), reached[wave]);
+            }
         }
     }
     // one statistic a wave, then one for all

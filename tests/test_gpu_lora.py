@@ -67,6 +67,9 @@ SHAPES = [
     (2100, 520, 130, 8, 2, [0, -1], 32), (4001, 96, 120, 48, 6, "runs", 64), (600, 64, 200, 128, 3, None, 32),
     (7700, 72, 40, 16, 2, "runs", 32), (8193, 40, 72, 40, 9, None, 64), (16000, 40, 72, 24, 3, None, 32),
     (15500, 66, 48, 64, 1, [0], 32), (20000, 24, 16, 8, 2000, None, 32),
+    # K and N in parts that a launch of their own adds
+    (2100, 1100, 600, 24, 2, None, 32), (3000, 2600, 520, 72, 40, None, 64), (9000, 640, 1300, 16, 3, "runs", 32),
+    (2049, 520, 4100, 40, 1, [0, -1], 32),
 ]
 
 
