@@ -72,9 +72,13 @@ __device__ inline void store8(uint16_t *p, v4i v, int n)
             p[i] = t[i];
 }
 
-// The upper 16 bits of v as a float, and what is left of it (an infinity leaves nothing).
+// The upper 16 bits of v as a float, and what is left of it.  Where nothing is left, 2^-40 of v stands for it: with
+// zero, an infinity among the weights would come out as NaN.  All pieces of v have its sign.
 __device__ inline float cut(float v) { return __uint_as_float(__float_as_uint(v) & 0xFFFF0000u); }
-__device__ inline float rest(float v, float c) { return fabsf(c) < INFINITY ? v - c : 0.0f; }
+__device__ inline float rest(float v, float c)
+{
+    return fabsf(c) < INFINITY && v != c ? v - c : c * 0x1p-40f;
+}
 
 __device__ inline int pack2(float lo, float hi)
 {
@@ -109,8 +113,30 @@ __device__ inline int4 tile_of(const Plan &p, int bin, int first, int n, int j)
                      at % p.wide == 0 ? min(p.wide, n - at) : 0);
 }
 
-// Many tokens: one workgroup sorts them (stably: its waves own contiguous parts) and writes all tiles.
-constexpr int kPlanWaves = 16, kPlanThreads = 64 * kPlanWaves;
+// Adds the wave's bins (-1: none) to its counts; where all are one request's, with one addition.
+__device__ inline void count_bins(int32_t *hist, int bin, int lane)
+{
+    const uint64_t any = __ballot(bin >= 0);
+    if (!any)
+        return;
+    const int lead = __ffsll((unsigned long long)any) - 1, b = __builtin_amdgcn_readlane(bin, lead);
+    if (__ballot(bin == b) == any) {
+        if (lane == lead)
+            atomicAdd(&hist[b], __popcll(any));
+    } else if (bin >= 0) {
+        atomicAdd(&hist[bin], 1);
+    }
+}
+
+// Many tokens: one workgroup sorts them (stably: its waves own contiguous parts) and writes all tiles.  Latency bounds
+// it, hence the loads kAtOnce at a time.
+constexpr int kPlanWaves = 16, kPlanThreads = 64 * kPlanWaves, kAtOnce = 8;
+
+__device__ inline void load_bins(int (&bin)[kAtOnce], const Plan &p, int t, int end)
+{
+#pragma unroll
+    for (int h = 0; h < kAtOnce; ++h) bin[h] = t + 64 * h < end ? bin_of(p, t + 64 * h) : -1;
+}
 
 __global__ void __launch_bounds__(kPlanThreads) k_plan(Plan p)
 {
@@ -122,7 +148,12 @@ __global__ void __launch_bounds__(kPlanThreads) k_plan(Plan p)
     for (int w = 0; w < kPlanWaves; ++w)
         for (int b = tid; b < bins; b += kPlanThreads) hist[w][b] = 0;
     __syncthreads();
-    for (int t = beg + lane; t < end; t += 64) atomicAdd(&hist[wave][bin_of(p, t)], 1);
+    for (int t = beg; t < end; t += 64 * kAtOnce) {
+        int bin[kAtOnce];
+        load_bins(bin, p, t + lane, end);
+#pragma unroll
+        for (int h = 0; h < kAtOnce; ++h) count_bins(hist[wave], bin[h], lane);
+    }
     __syncthreads();
     // a thread takes `each` consecutive adapters: their tokens and tiles before it
     const int each = (bins + kPlanThreads - 1) / kPlanThreads;
@@ -161,22 +192,26 @@ __global__ void __launch_bounds__(kPlanThreads) k_plan(Plan p)
     __syncthreads();
     int bits = 0;
     while ((1 << bits) < bins) ++bits;
-    for (int t = beg; t < end; t += 64) {
-        const bool there = t + lane < end;
-        const int b = there ? bin_of(p, t + lane) : 0;
-        uint64_t same = __ballot(there);
-        same = there ? same : ~same;
-        for (int i = 0; i < bits; ++i) {
-            const uint64_t set = __ballot((b >> i) & 1);
-            same &= (b >> i) & 1 ? set : ~set;
+    for (int t = beg; t < end; t += 64 * kAtOnce) {
+        int bin[kAtOnce];
+        load_bins(bin, p, t + lane, end);
+#pragma unroll
+        for (int h = 0; h < kAtOnce; ++h) {
+            const bool there = bin[h] >= 0;
+            uint64_t same = __ballot(there);
+            same = there ? same : ~same;
+            for (int i = 0; i < bits; ++i) {
+                const uint64_t set = __ballot((bin[h] >> i) & 1);
+                same &= (bin[h] >> i) & 1 ? set : ~set;
+            }
+            const int lead = __ffsll((unsigned long long)same) - 1;
+            int to = 0;
+            if (there && lane == lead)
+                to = atomicAdd(&hist[wave][bin[h]], __popcll(same));
+            to = __shfl(to, lead);
+            if (there)
+                p.order[to + __popcll(same & (((uint64_t)1 << lane) - 1))] = t + 64 * h + lane;
         }
-        const int lead = __ffsll((unsigned long long)same) - 1;
-        int to = 0;
-        if (there && lane == lead)
-            to = atomicAdd(&hist[wave][b], __popcll(same));
-        to = __shfl(to, lead);
-        if (there)
-            p.order[to + __popcll(same & (((uint64_t)1 << lane) - 1))] = t + lane;
     }
 }
 
@@ -235,16 +270,7 @@ __device__ inline int4 self_plan(const Plan &p, int want, int32_t *hist, int32_t
     for (int h = 0; h < kHold; ++h) {
         if (h >= turns)
             break;
-        const uint64_t any = __ballot(held[h] >= 0);
-        if (!any)
-            continue;
-        const int lead = __ffsll((unsigned long long)any) - 1, b = __builtin_amdgcn_readlane(held[h], lead);
-        if (__ballot(held[h] == b) == any) {                // (one request's run: one addition for all)
-            if (lane == lead)
-                atomicAdd(&mine[b], __popcll(any));
-        } else if (held[h] >= 0) {
-            atomicAdd(&mine[held[h]], 1);
-        }
+        count_bins(mine, held[h], lane);
     }
     __syncthreads();
     int4 found = make_int4(-1, 0, 0, 0);
@@ -1051,7 +1077,7 @@ Space space(const Sizes &z, void *ws, bool back)
 bool good_shape(int64_t T, int64_t K, int64_t N, int64_t R, int64_t L)
 {
     return T >= 0 && T <= kMaxTokens && K > 0 && K <= kMaxWidth && N >= 0 && N <= kMaxWidth && R > 0 && R <= kMaxRank &&
-           R % 8 == 0 && L > 0 && L <= kMaxAdapters && L * std::max<int64_t>(R, 64) * std::max(K, N) < (int64_t)1 << 35;
+           R % 8 == 0 && L > 0 && L <= kMaxAdapters && L * std::max<int64_t>(R, 64) * std::max(K, N) < (int64_t)1 << 33;
 }
 
 template <bool BACK>

@@ -182,6 +182,35 @@ def test_infinity_of_one_row_of_b():
     assert np.array_equal(f64(got[:, 33]), np.sign(v) * np.inf)
 
 
+@pytest.mark.parametrize("R", [8, 16, 40])
+def test_infinities_beside_short_values(R):
+    """v and u of few bits leave nothing for their lower pieces: an infinity that meets them stays one."""
+    L, T, K, N = 1, 20, 24, 40
+    x = torch.zeros((T, K), dtype=torch.bfloat16, device=DEV)
+    x[:, 0] = 1.0
+    a = torch.zeros((L, R, K), dtype=torch.bfloat16, device=DEV)
+    a[0, 0, 0] = 0.5
+    b = torch.zeros((L, N, R), dtype=torch.bfloat16, device=DEV)
+    b[0, :, 0] = 1.0
+    ids = torch.zeros(T, dtype=torch.int64, device=DEV)
+    b[0, 7, 0] = float("inf")
+    y = q.lora_mm(x, a, b, ids)
+    assert (y[:, 7] == float("inf")).all() and (y[:, :7] == 0.5).all() and (y[:, 8:] == 0.5).all()
+    b[0, 7, 0] = 1.0
+    dy = torch.zeros((T, N), dtype=torch.bfloat16, device=DEV)
+    dy[:, 3] = 2.0
+    dy[4, 9] = float("-inf")
+    x[5, 11] = float("inf")
+    a[0, 0, 11] = 1.0
+    dx, da, db = q.lora_mm_backward(dy, x, a, b, ids)
+    # token 4: u = -inf at rank 0, and NaN (-inf times b's 0) at the others; token 5: v = inf, u = 2
+    assert da[0, 0, 0] == float("-inf") and da[0, 0, 11].isnan() and dx[0, 0] == 1.0 and dx[4, 0].isnan()
+    assert db[0, 3, 0] == float("inf") and db[0, 9, 0].isnan() and db[0, 20, 0].isnan()
+    x[5, 11], dy[4, 9], x[6, 1] = 0.0, 0.0, float("inf")
+    dx, da, db = q.lora_mm_backward(dy, x, a, b, ids)
+    assert da[0, 0, 1] == float("inf") and da[0, 0, 0] == 2.0 * T
+
+
 def test_no_tokens():
     d = make(1, 64, 48, 16, 3, 17)
     e = {k: v[:0] if k in ("x", "ids", "base", "dy", "dbase") else v for k, v in d.items()}
