@@ -13,7 +13,7 @@
 
 #include "qlin_dpp.h"
 #include "qlin_elem.h"
-#include "qlin_moe_scan.h"
+#include "qlin_sort.h"
 #include "qlinear.h"
 
 namespace qlin {
@@ -110,10 +110,7 @@ __global__ void __launch_bounds__(kThreads) k_embedding(LookArgs a)
 // leave most of the GPU idle: the table's zeros are written beside them, a share in each.
 // ---------------------------------------------------------------------------
 constexpr int kDigitBits = 11;
-constexpr int kSortWaves = 8, kSortThreads = 64 * kSortWaves;
 constexpr int kSortOne = 4096;                 // positions up to which one workgroup sorts alone
-constexpr int kSortBlock = 2048;               // positions of a workgroup otherwise, until
-constexpr int kSortMaxBlocks = 256;            // there would be more workgroups than this
 
 // Zeros in rows `from` .. `to` - 1 of `width` elements, the last of all (`rows` - 1) of `last`; in workgroups behind
 // the `skip` that have other work.
@@ -150,6 +147,8 @@ struct SortArgs {
     int shift, digits;         // digit = (key >> shift) % digits, a power of two
 };
 
+__device__ inline SortRange range_of(const SortArgs &a) { return SortRange{a.n, a.per_block, a.blocks, a.counts}; }
+
 __device__ inline int2 pair_at(const SortArgs &a, int i)
 {
     if (!a.ids)
@@ -166,92 +165,7 @@ __global__ void __launch_bounds__(kSortThreads) k_sort_count(SortArgs a, FillArg
         fill(f);
         return;
     }
-    for (int d = threadIdx.x; d < a.digits; d += kSortThreads) hist[d] = 0;
-    __syncthreads();
-    const int beg = (int)min((int64_t)blockIdx.x * a.per_block, (int64_t)a.n), end = min(beg + a.per_block, a.n);
-#pragma unroll 4
-    for (int i = beg + threadIdx.x; i < end; i += kSortThreads)
-        atomicAdd(&hist[(pair_at(a, i).x >> a.shift) & (a.digits - 1)], 1);
-    __syncthreads();
-    for (int d = threadIdx.x; d < a.digits; d += kSortThreads)
-        a.counts[(int64_t)blockIdx.x * a.digits + d] = hist[d];
-}
-
-// LDS of `digits`: [waves][digits], twice [digits].
-constexpr size_t place_lds(int digits) { return (size_t)(kSortWaves + 2) * digits * sizeof(int32_t); }
-
-// One digit: get(i) is pair i, put(place, pair) takes it.  A wave owns a contiguous part of the workgroup's range; a
-// pair's place is the first place of its digit for the wave, plus those of the wave before it, 64 at a time, plus the
-// lower lanes with its digit.
-template <typename Get, typename Put>
-__device__ inline void place(const SortArgs &a, int shift, int digits, int32_t *hist, Get get, Put put)
-{
-    __shared__ int32_t wave_total[kSortWaves];
-    int32_t *total = hist + kSortWaves * digits, *before = total + digits;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, mask = digits - 1;
-    const int part = a.per_block / kSortWaves;
-    const int beg = (int)min((int64_t)blockIdx.x * a.per_block + wave * part, (int64_t)a.n), end = min(beg + part, a.n);
-    for (int i = tid; i < (kSortWaves + 2) * digits; i += kSortThreads) hist[i] = 0;
-    __syncthreads();
-    int32_t *mine = hist + wave * digits;
-#pragma unroll 4
-    for (int i = beg + lane; i < end; i += 64) atomicAdd(&mine[(get(i).x >> shift) & mask], 1);
-    if (a.counts) {
-        const int all = a.blocks * digits, earlier = blockIdx.x * digits;
-#pragma unroll 4
-        for (int i = tid; i < all; i += kSortThreads) {
-            const int c = a.counts[i];
-            if (c) {
-                atomicAdd(&total[i & mask], c);
-                if (i < earlier)
-                    atomicAdd(&before[i & mask], c);
-            }
-        }
-    }
-    __syncthreads();
-    const int each = (digits + kSortThreads - 1) / kSortThreads;
-    const int d0 = min(tid * each, digits), d1 = min(d0 + each, digits);
-    int sum = 0;
-    for (int d = d0; d < d1; ++d) {
-        if (!a.counts)
-            for (int w = 0; w < kSortWaves; ++w) total[d] += hist[w * digits + d];
-        sum += total[d];
-    }
-    const int scan = wave_scan(sum);
-    if (lane == 63)
-        wave_total[wave] = scan;
-    __syncthreads();
-    int first = scan - sum;
-    for (int w = 0; w < wave; ++w) first += wave_total[w];
-    for (int d = d0; d < d1; ++d) {
-        int at = first + before[d];
-        for (int w = 0; w < kSortWaves; ++w) {
-            const int c = hist[w * digits + d];
-            hist[w * digits + d] = at;
-            at += c;
-        }
-        first += total[d];
-    }
-    __syncthreads();
-    const int bits = __ffs(digits) - 1;
-    for (int i = beg; i < end; i += 64) {
-        const bool there = i + lane < end;
-        const int2 p = there ? get(i + lane) : make_int2(0, 0);
-        const int d = (p.x >> shift) & mask;
-        uint64_t same = __ballot(there);
-        same = there ? same : ~same;
-        for (int b = 0; b < bits; ++b) {
-            const uint64_t set = __ballot((d >> b) & 1);
-            same &= (d >> b) & 1 ? set : ~set;
-        }
-        const int lead = __ffsll((unsigned long long)same) - 1;
-        int at = 0;
-        if (there && lane == lead)
-            at = atomicAdd(&mine[d], __popcll(same));
-        at = __shfl(at, lead);
-        if (there)
-            put(at + __popcll(same & (((uint64_t)1 << lane) - 1)), p);
-    }
+    count(range_of(a), a.shift, a.digits, hist, [&](int i) { return pair_at(a, i).x; });
 }
 
 __global__ void __launch_bounds__(kSortThreads) k_sort_place(SortArgs a, FillArgs f)
@@ -261,7 +175,7 @@ __global__ void __launch_bounds__(kSortThreads) k_sort_place(SortArgs a, FillArg
         fill(f);
         return;
     }
-    place(a, a.shift, a.digits, hist, [&](int i) { return pair_at(a, i); }, [&](int at, int2 p) { a.out[at] = p; });
+    place(range_of(a), a.shift, a.digits, hist, [&](int i) { return pair_at(a, i); }, [&](int at, int2 p) { a.out[at] = p; });
 }
 
 // Few positions: both digits (of `low` bits, and the others) in one launch, the pairs in LDS between them.
@@ -274,12 +188,12 @@ __global__ void __launch_bounds__(kSortThreads) k_sort_one(SortArgs a, int high,
         return;
     }
     if (high == 1) {
-        place(a, 0, a.digits, hist, [&](int i) { return pair_at(a, i); }, [&](int at, int2 p) { a.out[at] = p; });
+        place(range_of(a), 0, a.digits, hist, [&](int i) { return pair_at(a, i); }, [&](int at, int2 p) { a.out[at] = p; });
         return;
     }
-    place(a, 0, a.digits, hist, [&](int i) { return pair_at(a, i); }, [&](int at, int2 p) { pairs[at] = p; });
+    place(range_of(a), 0, a.digits, hist, [&](int i) { return pair_at(a, i); }, [&](int at, int2 p) { pairs[at] = p; });
     __syncthreads();
-    place(a, a.shift, high, hist, [&](int i) { return pairs[i]; }, [&](int at, int2 p) { a.out[at] = p; });
+    place(range_of(a), a.shift, high, hist, [&](int i) { return pairs[i]; }, [&](int at, int2 p) { a.out[at] = p; });
 }
 
 // ---------------------------------------------------------------------------
@@ -449,10 +363,7 @@ __global__ void __launch_bounds__(64 * kJoinWaves) k_join(SumArgs a)
     store_row<O, 4>(a, key, at, n, sum);
 }
 
-int sort_blocks(int64_t n)
-{
-    return n <= kSortOne ? 1 : (int)std::min((n + kSortBlock - 1) / kSortBlock, (int64_t)kSortMaxBlocks);
-}
+int sort_blocks(int64_t n) { return n <= kSortOne ? 1 : sort_parts(n); }
 
 int64_t chunks(int64_t n) { return (n + kChunk - 1) / kChunk; }
 int64_t column_blocks(int64_t width) { return (width + 255) / 256; }           // of the join, the most
@@ -515,9 +426,8 @@ hipError_t launch_sort(const void *ids, int32_t id_bits, int64_t n, int64_t voca
 {
     const Digits d = digits_of(vocab);
     const int blocks = sort_blocks(n);
-    int64_t per = (n + blocks - 1) / blocks;
-    per = (per + kSortThreads - 1) / kSortThreads * kSortThreads;
-    SortArgs sa{ids, nullptr, a, blocks > 1 ? counts : nullptr, (int)n, (int)per, blocks, (int)vocab, id_bits, 0, 1 << d.low};
+    const int per = sort_share(n, blocks);
+    SortArgs sa{ids, nullptr, a, blocks > 1 ? counts : nullptr, (int)n, per, blocks, (int)vocab, id_bits, 0, 1 << d.low};
     *sorted = a;
     if (blocks == 1) {
         const FillArgs g = share_of(f, 0, 1, 1);

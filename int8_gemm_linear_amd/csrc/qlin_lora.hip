@@ -17,7 +17,7 @@
 #include <algorithm>
 
 #include "qlin_device.h"
-#include "qlin_moe_scan.h"
+#include "qlin_sort.h"
 #include "qlinear.h"
 
 namespace qlin {
@@ -25,7 +25,7 @@ namespace {
 
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 
-constexpr int kMaxAdapters = 2048;
+constexpr int kMaxAdapters = 2047;
 constexpr int kMaxRank = 128;
 constexpr int64_t kMaxTokens = (int64_t)1 << 24;
 constexpr int64_t kMaxWidth = (int64_t)1 << 20;
@@ -128,91 +128,42 @@ __device__ inline void count_bins(int32_t *hist, int bin, int lane)
     }
 }
 
-// Many tokens: one workgroup sorts them (stably: its waves own contiguous parts) and writes all tiles.  Latency bounds
-// it, hence the loads kAtOnce at a time.
-constexpr int kPlanWaves = 16, kPlanThreads = 64 * kPlanWaves, kAtOnce = 8;
+// Many tokens: a counting sort over several workgroups, the last of which writes the tiles.
+struct ManyArgs {
+    Plan plan;
+    SortRange range;
+    int digits;                // a power of two above the number of adapters
+};
 
-__device__ inline void load_bins(int (&bin)[kAtOnce], const Plan &p, int t, int end)
+__global__ void __launch_bounds__(kSortThreads) k_plan_count(ManyArgs a)
 {
-#pragma unroll
-    for (int h = 0; h < kAtOnce; ++h) bin[h] = t + 64 * h < end ? bin_of(p, t + 64 * h) : -1;
+    extern __shared__ int32_t hist[];
+    count(a.range, 0, a.digits, hist, [&](int i) { return bin_of(a.plan, i); });
 }
 
-__global__ void __launch_bounds__(kPlanThreads) k_plan(Plan p)
+__global__ void __launch_bounds__(kSortThreads) k_plan_place(ManyArgs a)
 {
-    __shared__ int32_t hist[kPlanWaves][kBins];
-    __shared__ int32_t sums[2][kPlanWaves];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, bins = p.adapters + 1;
-    const int part = (p.tokens + kPlanThreads - 1) / kPlanThreads * 64;
-    const int beg = min(wave * part, p.tokens), end = min(beg + part, p.tokens);
-    for (int w = 0; w < kPlanWaves; ++w)
-        for (int b = tid; b < bins; b += kPlanThreads) hist[w][b] = 0;
-    __syncthreads();
-    for (int t = beg; t < end; t += 64 * kAtOnce) {
-        int bin[kAtOnce];
-        load_bins(bin, p, t + lane, end);
-#pragma unroll
-        for (int h = 0; h < kAtOnce; ++h) count_bins(hist[wave], bin[h], lane);
-    }
-    __syncthreads();
-    // a thread takes `each` consecutive adapters: their tokens and tiles before it
-    const int each = (bins + kPlanThreads - 1) / kPlanThreads;
-    const int b0 = min(tid * each, bins), b1 = min(b0 + each, bins);
-    int tokens = 0, tiles = 0;
-    for (int b = b0; b < b1; ++b) {
-        int n = 0;
-        for (int w = 0; w < kPlanWaves; ++w) n += hist[w][b];
-        tokens += n;
-        tiles += (n + p.tile - 1) / p.tile;
-    }
-    const int scan0 = wave_scan(tokens), scan1 = wave_scan(tiles);
-    if (lane == 63) {
-        sums[0][wave] = scan0;
-        sums[1][wave] = scan1;
-    }
-    __syncthreads();
-    int at = scan0 - tokens, tile = scan1 - tiles, all = 0;
-    for (int w = 0; w < kPlanWaves; ++w) {
-        at += w < wave ? sums[0][w] : 0;
-        tile += w < wave ? sums[1][w] : 0;
-        all += sums[1][w];
-    }
-    for (int b = b0; b < b1; ++b) {
-        const int first = at;
-        for (int w = 0; w < kPlanWaves; ++w) {
-            const int c = hist[w][b];
-            hist[w][b] = at;
-            at += c;
+    extern __shared__ int32_t hist[];
+    const Plan &p = a.plan;
+    place(a.range, 0, a.digits, hist, [&](int i) { return make_int2(bin_of(p, i), i); },
+          [&](int at, int2 t) { p.order[at] = t.y; });
+    if (blockIdx.x != gridDim.x - 1)
+        return;
+    const int32_t *total = hist + kSortWaves * a.digits;
+    const int lane = threadIdx.x & 63;
+    int at0 = 0, tile0 = 0;
+    for (int b0 = 0; b0 <= p.adapters; b0 += 64) {          // (by each wave, which takes its share of the tiles)
+        const int b = b0 + lane, n = b <= p.adapters ? total[b] : 0, tiles = (n + p.tile - 1) / p.tile;
+        const int at = at0 + wave_scan(n) - n, tile = tile0 + wave_scan(tiles) - tiles;
+        if (b <= p.adapters) {
+            if (p.offsets && threadIdx.x < 64)
+                p.offsets[b] = at;             // (that of the last bin: tokens with an adapter)
+            for (int j = threadIdx.x >> 6; j < tiles; j += kSortWaves) p.tiles[tile + j] = tile_of(p, b, at, n, j);
         }
-        if (p.offsets)
-            p.offsets[b] = first;              // (that of the last bin: tokens with an adapter)
-        for (int j = 0; j * p.tile < at - first; ++j) p.tiles[tile++] = tile_of(p, b, first, at - first, j);
+        at0 = __builtin_amdgcn_readlane(at + n, 63);
+        tile0 = __builtin_amdgcn_readlane(tile + tiles, 63);
     }
-    for (int t = all + tid; t < p.max_tiles; t += kPlanThreads) p.tiles[t] = make_int4(-1, 0, 0, 0);
-    __syncthreads();
-    int bits = 0;
-    while ((1 << bits) < bins) ++bits;
-    for (int t = beg; t < end; t += 64 * kAtOnce) {
-        int bin[kAtOnce];
-        load_bins(bin, p, t + lane, end);
-#pragma unroll
-        for (int h = 0; h < kAtOnce; ++h) {
-            const bool there = bin[h] >= 0;
-            uint64_t same = __ballot(there);
-            same = there ? same : ~same;
-            for (int i = 0; i < bits; ++i) {
-                const uint64_t set = __ballot((bin[h] >> i) & 1);
-                same &= (bin[h] >> i) & 1 ? set : ~set;
-            }
-            const int lead = __ffsll((unsigned long long)same) - 1;
-            int to = 0;
-            if (there && lane == lead)
-                to = atomicAdd(&hist[wave][bin[h]], __popcll(same));
-            to = __shfl(to, lead);
-            if (there)
-                p.order[to + __popcll(same & (((uint64_t)1 << lane) - 1))] = t + 64 * h + lane;
-        }
-    }
+    for (int t = tile0 + (int)threadIdx.x; t < p.max_tiles; t += kSortThreads) p.tiles[t] = make_int4(-1, 0, 0, 0);
 }
 
 // Up to 64 tokens: every wave of the shrink kernel finds its tile by itself, without LDS or a barrier.  `token`
@@ -1042,7 +993,7 @@ struct Layout {
 };
 
 struct Space {
-    int32_t *order, *offsets;
+    int32_t *order, *offsets, *counts;
     int4 *tiles;
     uint16_t *rows;            // of s v (backward: s u) for expand
     float *part;               // or the parts of v
@@ -1051,12 +1002,20 @@ struct Space {
     size_t bytes;
 };
 
+int plan_digits(int64_t L)
+{
+    int d = 1;
+    while (d <= L) d *= 2;
+    return d;
+}
+
 Space space(const Sizes &z, void *ws, bool back)
 {
     Layout l{static_cast<uint8_t *>(ws)};
     Space f{};
     f.order = l.take<int32_t>(z.T);
     f.tiles = l.take<int4>(z.max_tiles);
+    f.counts = l.take<int32_t>(z.T > kSelfTokens ? (int64_t)sort_parts(z.T) * plan_digits(z.L) : 0);
     if (back || z.splits == 1)
         f.rows = l.take<uint16_t>(z.T * 2 * z.Rp);
     else
@@ -1107,7 +1066,16 @@ hipError_t make_plan(const Sizes &z, const Space &f, const void *ids, int32_t id
     a.self = z.T == 0 || z.T > kSelfTokens ? 0 : z.T <= kWaveTokens ? 1 : 2;
     if (a.self)
         return hipSuccess;
-    hipLaunchKernelGGL(k_plan, dim3(1), dim3(kPlanThreads), 0, s, a.plan);
+    const int blocks = std::max(1, sort_parts(z.T));
+    const ManyArgs m{a.plan, SortRange{(int)z.T, sort_share(z.T, blocks), blocks, z.T > kSelfTokens ? f.counts : nullptr},
+                     plan_digits(z.L)};
+    if (m.range.counts) {
+        hipLaunchKernelGGL(k_plan_count, dim3(blocks), dim3(kSortThreads), m.digits * sizeof(int32_t), s, m);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess)
+            return e;
+    }
+    hipLaunchKernelGGL(k_plan_place, dim3(blocks), dim3(kSortThreads), place_lds(m.digits), s, m);
     return hipGetLastError();
 }
 

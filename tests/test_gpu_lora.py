@@ -61,12 +61,12 @@ SHAPES = [
     (1, 64, 64, 8, 1, [0], 32), (1, 2048, 2048, 16, 8, None, 32), (1, 1, 1, 8, 1, [0], 64), (2, 3, 5, 16, 2, None, 32),
     (5, 127, 63, 24, 3, None, 64), (7, 128, 64, 32, 5, None, 32), (16, 129, 65, 40, 2, None, 32),
     (17, 511, 257, 64, 4, None, 32), (33, 513, 130, 72, 3, "runs", 32), (31, 640, 1001, 96, 2, None, 64),
-    (64, 1032, 77, 128, 3, "runs", 32), (65, 136, 4104, 8, 40, None, 32), (100, 5120, 48, 16, 2048, None, 64),
+    (64, 1032, 77, 128, 3, "runs", 32), (65, 136, 4104, 8, 40, None, 32), (100, 5120, 48, 16, 2047, None, 64),
     (333, 1032, 1001, 8, 3, None, 32), (257, 255, 300, 16, 1, [0], 32), (300, 256, 511, 32, 2, "runs", 64),
     (130, 384, 640, 64, 1, [0], 32), (1100, 200, 136, 16, 5, "runs", 32), (1500, 72, 264, 32, 300, None, 32),
     (2100, 520, 130, 8, 2, [0, -1], 32), (4001, 96, 120, 48, 6, "runs", 64), (600, 64, 200, 128, 3, None, 32),
     (7700, 72, 40, 16, 2, "runs", 32), (8193, 40, 72, 40, 9, None, 64), (16000, 40, 72, 24, 3, None, 32),
-    (15500, 66, 48, 64, 1, [0], 32), (20000, 24, 16, 8, 2000, None, 32),
+    (15500, 66, 48, 64, 1, [0], 32), (20000, 24, 16, 8, 2000, None, 32), (9001, 24, 16, 8, 2047, None, 64),
     # K and N in parts that a launch of their own adds
     (2100, 1100, 600, 24, 2, None, 32), (3000, 2600, 520, 72, 40, None, 64), (9000, 640, 1300, 16, 3, "runs", 32),
     (2049, 520, 4100, 40, 1, [0, -1], 32),

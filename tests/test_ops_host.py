@@ -34,8 +34,8 @@ def test_lora_refusals(call):
     assert call(K=0) == SHAPE and call(K=-8) == SHAPE and call(K=(1 << 20) + 1) == SHAPE
     assert call(N=-1) == SHAPE and call(N=(1 << 20) + 1) == SHAPE
     assert call(R=0) == SHAPE and call(R=4) == SHAPE and call(R=12) == SHAPE and call(R=136) == SHAPE
-    assert call(L=0) == SHAPE and call(L=2049) == SHAPE
-    assert call(L=2048, K=1 << 20) == SHAPE and call(L=512, R=128, N=1 << 19) == SHAPE
+    assert call(L=0) == SHAPE and call(L=2048) == SHAPE
+    assert call(L=2047, K=1 << 20) == SHAPE and call(L=512, R=128, N=1 << 19) == SHAPE
     assert call(x=None) == NULL and call(a=None) == NULL and call(b=None) == NULL and call(ids=None) == NULL
     assert call(ldx=63) == STRIDE and call(ldx=(1 << 31) + 1) == STRIDE
     assert call(ldb=0) == STRIDE and call(ldb=(1 << 31) + 1) == STRIDE
