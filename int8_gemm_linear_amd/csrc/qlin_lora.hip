@@ -808,7 +808,9 @@ __global__ void __launch_bounds__(kThreads) k_expand_many(ExpandArgs a)
 // ---------------------------------------------------------------------------
 // Outer: out[l][r][c] (or [l][c][r]) = sum over the adapter's places of f[r][place] z[token][c].  A wave takes
 // 128 columns and 16 RB ranks, 32 places at a time: a lane loads 8 columns of 8 tokens and pairs them up for the
-// matrix cores, whose m-th product has the columns 8 i + m.  Waves and splits share the places.
+// matrix cores, whose m-th product has the columns 8 i + m.  Waves and splits share the places.  Lines asked of the
+// L2 bound it, z's and the factors': 8192 tokens of 5120 and 10240, 16 ranks, 252 MB of z, 71 us; of 5120 and 5120,
+// 64 ranks 92 us (135 with 32 ranks at a time, which reads z twice).
 // ---------------------------------------------------------------------------
 struct OuterJob {
     const uint16_t *z, *pieces;
@@ -825,7 +827,7 @@ struct OuterArgs {
 };
 
 template <int RB>
-__global__ void __launch_bounds__(RB == 1 ? 1024 : 512) k_outer(OuterArgs a)
+__global__ void __launch_bounds__((RB == 1 ? 1024 : RB == 2 ? 512 : 256), (RB == 4 ? 2 : 1)) k_outer(OuterArgs a)
 {
     extern __shared__ v4f sums[];              // [waves / 2][RB * 8][64]
     const int second = (int)blockIdx.x >= a.first;
@@ -846,34 +848,35 @@ __global__ void __launch_bounds__(RB == 1 ? 1024 : 512) k_outer(OuterArgs a)
     v4f acc[RB][8] = {};
     for (int t = beg + 32 * (split * waves + wave); t < end; t += 32 * waves * job.splits) {
         const int first = t + 8 * q, n = end - first;          // this lane's places
-        v4i row[8], f[3][RB];
+        v4i row[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             row[j] = v4i{0, 0, 0, 0};
             if (j < n)
                 row[j] = load8(z + a.order[first + j] * job.ldz, left);
         }
+        v4i f[3][RB];
 #pragma unroll
         for (int h = 0; h < 3; ++h)
 #pragma unroll
-            for (int r = 0; r < RB; ++r)
-            {
+            for (int r = 0; r < RB; ++r) {
                 f[h][r] = v4i{0, 0, 0, 0};
                 if (n > 0)
                     f[h][r] = load8(pieces + (t - beg) * 3 * (int64_t)a.Rp + (h * a.Rp + 16 * r) * 8);
             }
+        v4i col[8];
 #pragma unroll
-        for (int m = 0; m < 8; ++m) {
-            v4i col;
+        for (int m = 0; m < 8; ++m)
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                col[j] = (int)__builtin_amdgcn_perm((uint32_t)row[2 * j + 1][m / 2], (uint32_t)row[2 * j][m / 2],
-                                                    m % 2 ? 0x07060302u : 0x05040100u);
+                col[m][j] = (int)__builtin_amdgcn_perm((uint32_t)row[2 * j + 1][m / 2], (uint32_t)row[2 * j][m / 2],
+                                                       m % 2 ? 0x07060302u : 0x05040100u);
 #pragma unroll
-            for (int h = 0; h < 3; ++h)
+        for (int h = 0; h < 3; ++h)
 #pragma unroll
-                for (int r = 0; r < RB; ++r) acc[r][m] = mma(f[h][r], col, acc[r][m]);
-        }
+            for (int r = 0; r < RB; ++r)
+#pragma unroll
+                for (int m = 0; m < 8; ++m) acc[r][m] = mma(f[h][r], col[m], acc[r][m]);
     }
     for (int half = waves / 2; half > 0; half /= 2) {
         if (wave >= half && wave < 2 * half)
@@ -972,11 +975,12 @@ Sizes sizes(int64_t T, int64_t K, int64_t N, int64_t R, int64_t L)
     return z;
 }
 
-int outer_waves(const Sizes &z) { return z.T / z.L < 512 ? 4 : 8; }
+// Waves of an outer workgroup: those of 64 ranks hold 250 registers.
+int outer_waves(const Sizes &z) { return z.T / z.L < 512 || z.Rp > 32 ? 4 : 8; }
 
 int outer_splits(const Sizes &z, int64_t C)
 {
-    const int64_t wgs = z.L * ((C + 127) / 128) * ((z.R + 31) / 32);
+    const int64_t wgs = z.L * ((C + 127) / 128) * ((z.R + 63) / 64);
     return (int)std::max<int64_t>(1, std::min<int64_t>({512 / wgs, z.T / (64 * outer_waves(z)), 16}));
 }
 
@@ -1111,7 +1115,7 @@ hipError_t launch_expand(const Sizes &z, const Space &f, const float *scale, con
 hipError_t launch_outer(const Sizes &z, const Space &f, const uint16_t *x, int64_t ldx, const uint16_t *dy, int64_t lddy,
                         float *da, float *db, hipStream_t s)
 {
-    const int sa = outer_splits(z, z.K), sb = outer_splits(z, z.N), waves = outer_waves(z), rb = z.Rp > 16 ? 2 : 1;
+    const int sa = outer_splits(z, z.K), sb = outer_splits(z, z.N), waves = outer_waves(z), rb = z.Rp > 32 ? 4 : z.Rp > 16 ? 2 : 1;
     OuterArgs a{};
     a.job[0] = OuterJob{x, f.fu, sa > 1 ? f.outer_a : da, ldx, z.L * z.R * z.K, (int)z.K, (int)((z.K + 127) / 128), sa, 0};
     a.job[1] = OuterJob{dy, f.fv, sb > 1 ? f.outer_b : db, lddy, z.L * z.R * z.N, (int)z.N, (int)((z.N + 127) / 128), sb, 1};
@@ -1125,8 +1129,10 @@ hipError_t launch_outer(const Sizes &z, const Space &f, const uint16_t *x, int64
     const size_t lds = (size_t)waves / 2 * rb * 8 * 64 * sizeof(v4f);
     if (rb == 1)
         hipLaunchKernelGGL((k_outer<1>), grid, block, lds, s, a);
-    else
+    else if (rb == 2)
         hipLaunchKernelGGL((k_outer<2>), grid, block, lds, s, a);
+    else
+        hipLaunchKernelGGL((k_outer<4>), grid, block, lds, s, a);
     hipError_t e = hipGetLastError();
     for (int j = 0; j < 2 && e == hipSuccess; ++j) {
         const OuterJob &o = a.job[j];
