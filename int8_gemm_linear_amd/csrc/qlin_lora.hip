@@ -128,7 +128,8 @@ __device__ inline void count_bins(int32_t *hist, int bin, int lane)
     }
 }
 
-// Many tokens: a counting sort over several workgroups, the last of which writes the tiles.
+// More than 8192 tokens: a counting sort over several workgroups, the last of which writes the tiles (65536 tokens:
+// 14 us).
 struct ManyArgs {
     Plan plan;
     SortRange range;
@@ -201,8 +202,7 @@ __device__ inline int4 wave_plan(const Plan &p, int want, int &token)
     return tile_of(p, __builtin_amdgcn_readlane(sorted, at), begin, end - begin, (at - begin) / p.tile);
 }
 
-// Up to 8192: every workgroup of the shrink kernel finds its tile, which takes it less time than a launch of its
-// own would take the call.  A wave owns a contiguous part of the tokens, keeps their bins and counts them for itself;
+// Up to 8192: every workgroup of the shrink kernel finds its tile (4 us for 4001 tokens; the two launches above take 14).  A wave owns a contiguous part of the tokens, keeps their bins and counts them for itself;
 // then each wave walks the bins, 64 at a time.
 constexpr int kHold = 16;
 constexpr int kSelfTokens = 64 * 8 * kHold;
@@ -269,6 +269,11 @@ __device__ inline int4 self_plan(const Plan &p, int want, int32_t *hist, int32_t
 // same from them (u).  Sixteen tokens by sixteen ranks a matrix product; a workgroup has a tile and all of
 // K, which its waves share in steps of 64 and add up in LDS.  Weights as [k][r] go through LDS, whose
 // transposing loads give a lane eight k of its rank.
+//
+// The lines of 128 bytes that a CU asks of the L2 bound it, about 160 a microsecond, the weights' of every tile
+// among them: 4001 tokens of 6 adapters of 32 ranks, K = 5120, 1.0 million lines, 21 us; u and v of 8192 tokens
+// of 5120 and 10240, 16 ranks, 3.0 million, 79 us.  Tiles of 64 tokens with K in parts, a launch that adds them,
+// need a tenth fewer lines and took 67 us for the latter, but 25 us more for the plan and the parts.
 // ---------------------------------------------------------------------------
 constexpr int kStep = 64;
 
@@ -289,13 +294,14 @@ struct ShrinkArgs {
     int R, Rp, groups, self;   // groups of 16 RB ranks; self: waves (1) or workgroups (2) make the plan
 };
 
-// Waves of a workgroup at most (what registers allow), and steps whose loads a wave has in flight.
-template <int TB, int RB> constexpr int shrink_waves() { return TB * RB <= 2 ? 16 : 8; }
+// Waves of a workgroup (16 took as long, four 43 us for 39: the gradients of 2048 tokens of an adapter of 16 ranks,
+// K = N = 2048), and steps whose loads a wave has in flight.
+constexpr int kShrinkWaves = 8;
 template <int TB, int RB> constexpr int steps_at_once() { return TB * RB == 1 ? 5 : TB + RB <= 3 ? 3 : TB + RB <= 5 ? 2 : 1; }
 
 // A step's rows: eight lanes load 128 bytes of one, so that a load instruction touches eight lines (with a row
-// for each lane of sixteen, as the matrix cores want them, it touches 64: 32 tokens of 32 requests on K = 5120
-// took 12.4 us).  The wave's LDS brings them to the matrix cores' order; piece j of a row lies at j ^ row, which
+// for each lane of sixteen, as the matrix cores want them, it touches 64: 32 tokens of 28 adapters on K = 5120
+// took 12.4 us, so 10.4).  The wave's LDS brings them to the matrix cores' order; piece j of a row lies at j ^ row, which
 // keeps both directions free of bank conflicts.
 template <int B>
 __device__ inline void load_rows(v4i (&v)[B][2], const uint16_t *const (&p)[B][2], int k, int K)
@@ -338,14 +344,14 @@ __device__ inline v4i row_part(const v4i *lds, int b, int half)
 // eights, so that no two adapters share one, whatever their numbers of tokens.
 __host__ __device__ inline int64_t piece_place(int64_t place, int l) { return (place + 7) / 8 * 8 + 8 * (int64_t)l; }
 
+// A wave's share of LDS: a step's rows and weights, then its sums (16-byte pieces).
 constexpr int shrink_share(int tb, int rb) { return tb * rb > 2 * (tb + rb) ? tb * rb * 64 : 2 * (tb + rb) * 64; }
 
 template <int TB, int RB, bool BACK>
-__global__ void __launch_bounds__((64 * shrink_waves<TB, RB>())) k_shrink(ShrinkArgs a)
+__global__ void __launch_bounds__(64 * kShrinkWaves) k_shrink(ShrinkArgs a)
 {
-    // a wave's share: a step's rows and weights, then its sums (16-byte pieces)
     constexpr int kShare = shrink_share(TB, RB);
-    extern __shared__ v4i shared[];             // [waves][kShare], before that the plan's bins
+    extern __shared__ v4i shared[];            // [waves][kShare], before that the plan's bins
     __shared__ int32_t tokens[64];
     const int units = a.plan.max_tiles * a.groups;
     // (the longer job's workgroups come first)
@@ -356,7 +362,7 @@ __global__ void __launch_bounds__((64 * shrink_waves<TB, RB>())) k_shrink(Shrink
     const int index = unit / a.groups, group = unit % a.groups;
     const bool publish = group == 0 && !second && split == 0;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, i = lane & 15, q = lane >> 4;
-    const int waves = blockDim.x >> 6;
+    constexpr int waves = kShrinkWaves;
     int4 tile;
     int token[TB];
     if (a.self == 1) {
@@ -495,7 +501,7 @@ __global__ void __launch_bounds__((64 * shrink_waves<TB, RB>())) k_shrink(Shrink
         for (int r = 0; r < RB; ++r) sums[(wave * TB * RB + t * RB + r) * 64 + lane] = acc[t][r];
     __syncthreads();
     const float s = a.scale ? a.scale[tile.x] : 1.0f;
-    for (int e = tid; e < TB * RB * 64; e += (int)blockDim.x) {
+    for (int e = tid; e < TB * RB * 64; e += 64 * waves) {
         v4f v = sums[e];
         for (int w = 1; w < waves; ++w) v += sums[w * TB * RB * 64 + e];
         const int block = e >> 6, rank = r0 + 16 * (block % RB) + (e & 15), at = 16 * (block / RB) + 4 * ((e >> 4) & 3);
@@ -733,8 +739,13 @@ __global__ void __launch_bounds__(kThreads) k_expand_many(ExpandArgs a)
     }
     v4i hi[G], lo[G];
     const uint16_t *w = a.w + (int64_t)(live ? tile.x : 0) * a.N * a.R;
-    if (live)
-        load_factors<G, PACK>(hi, lo, a, tile.y + min(16 * wave + i, tile.w - 1));
+    if (live) {
+        const int place = tile.y + min(16 * wave + i, tile.w - 1);
+        if (!TR && a.part)
+            add_factors<G, PACK>(hi, lo, a, place, a.scale ? a.scale[tile.x] : 1.0f);
+        else
+            load_factors<G, PACK>(hi, lo, a, place);
+    }
     const int blocks = (a.N + 127) / 128;
     for (int b = chunk; b < blocks; b += a.chunks) {
         const int n = 128 * b + 8 * i, left = a.N - n;      // this lane's n .. n + 7
@@ -809,8 +820,8 @@ __global__ void __launch_bounds__(kThreads) k_expand_many(ExpandArgs a)
 // Outer: out[l][r][c] (or [l][c][r]) = sum over the adapter's places of f[r][place] z[token][c].  A wave takes
 // 128 columns and 16 RB ranks, 32 places at a time: a lane loads 8 columns of 8 tokens and pairs them up for the
 // matrix cores, whose m-th product has the columns 8 i + m.  Waves and splits share the places.  Lines asked of the
-// L2 bound it, z's and the factors': 8192 tokens of 5120 and 10240, 16 ranks, 252 MB of z, 71 us; of 5120 and 5120,
-// 64 ranks 92 us (135 with 32 ranks at a time, which reads z twice).
+// L2 bound it, z's and the factors': 8192 tokens of 5120 and 10240, 16 ranks, 252 MB of z, 69 us (eight waves a
+// workgroup 71); of 5120 and 5120, 64 ranks 77 us (135 with 32 ranks at a time, which reads z twice).
 // ---------------------------------------------------------------------------
 struct OuterJob {
     const uint16_t *z, *pieces;
@@ -826,8 +837,10 @@ struct OuterArgs {
     int R, Rp, groups, first;  // workgroups of the first job
 };
 
+constexpr int kOuterWaves = 4;
+
 template <int RB>
-__global__ void __launch_bounds__((RB == 1 ? 1024 : RB == 2 ? 512 : 256), (RB == 4 ? 2 : 1)) k_outer(OuterArgs a)
+__global__ void __launch_bounds__(64 * kOuterWaves, 2) k_outer(OuterArgs a)
 {
     extern __shared__ v4f sums[];              // [waves / 2][RB * 8][64]
     const int second = (int)blockIdx.x >= a.first;
@@ -838,7 +851,8 @@ __global__ void __launch_bounds__((RB == 1 ? 1024 : RB == 2 ? 512 : 256), (RB ==
     const int group = b % a.groups;
     b /= a.groups;
     const int c0 = b % job.blocks * 128, l = b / job.blocks;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6, i = lane & 15, q = lane >> 4;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = lane & 15, q = lane >> 4;
+    constexpr int waves = kOuterWaves;
     const int beg = a.offsets[l], end = a.offsets[l + 1], r0 = group * 16 * RB;
     const int left = job.C - (c0 + 8 * i);
     const uint16_t *z = job.z + c0 + 8 * i;
@@ -952,36 +966,42 @@ struct Sizes {
 // 15.8 us, four 13.6, eight 14.5; 164 workgroups (24 adapters of 64 ranks, N = 51200): one 49.4, three 52.9.
 constexpr int64_t kMaxSplits = 4;
 
-// Tokens an adapter has on average from which base and out are more than the weights.
-constexpr int64_t kManyTokens = 16;
+// Tokens an adapter has on average from which 64 share a load of the expand kernel's weights, not 16: 32 adapters of
+// 16 ranks, K = N = 5120, 16 tokens each, both kernels: 19.0 us with 64 at a time, 15.7 with 16; 32 each 23.0 and 22.5;
+// 16 adapters, 64 each 21.3 and 21.7.
+constexpr int64_t kManyTokens = 64;
 
 Sizes sizes(int64_t T, int64_t K, int64_t N, int64_t R, int64_t L)
 {
     Sizes z{T, K, N, R, L, 16, 1, 1, 1, 1, 0, 1};
     while (z.Rp < R) z.Rp *= 2;
     const int64_t mean = T / std::min(L, std::max<int64_t>(T, 1));
-    // expand: 16 tokens share a load of the weights, or 64 where adapters have so many
     z.wide = mean >= kManyTokens ? kWide / 16 : 1;
-    // shrink: more tokens a workgroup only where there are workgroups for all CUs
+    // shrink: more tokens a workgroup only where there are workgroups for all CUs (8192 tokens of 8 adapters of 64
+    // ranks, K = N = 5120, both kernels: 16 at a time 136 us, 32 115; 65536 tokens of 8 adapters of 16 ranks, K = N =
+    // 2048: 16 at a time 270 us, 32 248, 64 235)
     while (z.tb < z.wide && T >= 16 * 2 * z.tb * 240) z.tb *= 2;
     z.max_tiles = (int)std::max<int64_t>(1, T / (16 * z.tb) + std::min(L + 1, T));
-    // and more ranks a workgroup likewise
-    const int blocks = (int)(z.Rp / 16);
-    while (z.rb < 4 && z.rb < blocks && z.rb * z.tb < 8 && (int64_t)z.max_tiles * (blocks / z.rb) > 512) z.rb *= 2;
+    // and 32 ranks a workgroup likewise (8192 tokens of 64 ranks: 16 at a time 136 us, 32 113, 64 115)
+    if (z.Rp > 16 && z.max_tiles * (z.Rp / 16) > 512)
+        z.rb = 2;
     z.groups = (int)((R + 16 * z.rb - 1) / (16 * z.rb));
-    // few workgroups: parts of K, a step for each wave at least (a CU alone loads some 50 GB/s)
-    if (z.wide == 1 && z.max_tiles * z.groups <= 128)
+    // few workgroups: parts of K, a step for each wave at least (a CU alone loads some 50 GB/s: 256 tokens of an
+    // adapter of 16 ranks, K = N = 5120, both kernels: one part 15.1 us, four 12.7)
+    if (z.max_tiles * z.groups <= 128)
         z.splits = (int)std::min<int64_t>((K + 8 * kStep - 1) / (8 * kStep), kMaxSplits);
     return z;
 }
 
-// Waves of an outer workgroup: those of 64 ranks hold 250 registers.
-int outer_waves(const Sizes &z) { return z.T / z.L < 512 || z.Rp > 32 ? 4 : 8; }
+int outer_blocks(const Sizes &z) { return z.Rp > 32 ? 4 : z.Rp > 16 ? 2 : 1; }
 
+// Splits of the places: both gradients' workgroups fill the CUs once, four to a CU with 16 ranks a workgroup and two with
+// more (8192 tokens of an adapter of 16 ranks, K = N = 5120: once 148 us, half of that 164; two of 64 ranks: once 231,
+// twice 246).
 int outer_splits(const Sizes &z, int64_t C)
 {
-    const int64_t wgs = z.L * ((C + 127) / 128) * ((z.R + 63) / 64);
-    return (int)std::max<int64_t>(1, std::min<int64_t>({512 / wgs, z.T / (64 * outer_waves(z)), 16}));
+    const int64_t wgs = z.L * ((C + 127) / 128) * ((z.R + 63) / 64), room = outer_blocks(z) == 1 ? 512 : 256;
+    return (int)std::max<int64_t>(1, std::min<int64_t>({room / wgs, z.T / (64 * kOuterWaves), 16}));
 }
 
 // Consecutive pieces of the workspace, 256-byte aligned.
@@ -1046,19 +1066,16 @@ bool good_shape(int64_t T, int64_t K, int64_t N, int64_t R, int64_t L)
 template <bool BACK>
 hipError_t launch_shrink(const Sizes &z, const ShrinkArgs &a, hipStream_t s)
 {
-    const int waves = z.tb * z.rb <= 2 && z.max_tiles * z.groups <= 128 && a.splits == 1 ? 16 : 8;
-    const dim3 grid((unsigned)(z.max_tiles * z.groups * (BACK ? 2 : a.splits))), block(64 * waves);
-    const size_t lds = std::max(waves * shrink_share(z.tb, z.rb) * sizeof(v4i),
-                                a.self == 2 ? waves * (z.L + 1) * sizeof(int32_t) : 0);
+    const dim3 grid((unsigned)(z.max_tiles * z.groups * (BACK ? 2 : a.splits))), block(64 * kShrinkWaves);
+    const size_t lds = std::max(kShrinkWaves * shrink_share(z.tb, z.rb) * sizeof(v4i),
+                                a.self == 2 ? kShrinkWaves * (z.L + 1) * sizeof(int32_t) : 0);
     switch (z.rb * 8 + z.tb) {
     case 8 + 1: hipLaunchKernelGGL((k_shrink<1, 1, BACK>), grid, block, lds, s, a); break;
     case 8 + 2: hipLaunchKernelGGL((k_shrink<2, 1, BACK>), grid, block, lds, s, a); break;
     case 8 + 4: hipLaunchKernelGGL((k_shrink<4, 1, BACK>), grid, block, lds, s, a); break;
     case 16 + 1: hipLaunchKernelGGL((k_shrink<1, 2, BACK>), grid, block, lds, s, a); break;
     case 16 + 2: hipLaunchKernelGGL((k_shrink<2, 2, BACK>), grid, block, lds, s, a); break;
-    case 16 + 4: hipLaunchKernelGGL((k_shrink<4, 2, BACK>), grid, block, lds, s, a); break;
-    case 32 + 1: hipLaunchKernelGGL((k_shrink<1, 4, BACK>), grid, block, lds, s, a); break;
-    default: hipLaunchKernelGGL((k_shrink<2, 4, BACK>), grid, block, lds, s, a); break;
+    default: hipLaunchKernelGGL((k_shrink<4, 2, BACK>), grid, block, lds, s, a); break;
     }
     return hipGetLastError();
 }
@@ -1115,7 +1132,7 @@ hipError_t launch_expand(const Sizes &z, const Space &f, const float *scale, con
 hipError_t launch_outer(const Sizes &z, const Space &f, const uint16_t *x, int64_t ldx, const uint16_t *dy, int64_t lddy,
                         float *da, float *db, hipStream_t s)
 {
-    const int sa = outer_splits(z, z.K), sb = outer_splits(z, z.N), waves = outer_waves(z), rb = z.Rp > 32 ? 4 : z.Rp > 16 ? 2 : 1;
+    const int sa = outer_splits(z, z.K), sb = outer_splits(z, z.N), rb = outer_blocks(z);
     OuterArgs a{};
     a.job[0] = OuterJob{x, f.fu, sa > 1 ? f.outer_a : da, ldx, z.L * z.R * z.K, (int)z.K, (int)((z.K + 127) / 128), sa, 0};
     a.job[1] = OuterJob{dy, f.fv, sb > 1 ? f.outer_b : db, lddy, z.L * z.R * z.N, (int)z.N, (int)((z.N + 127) / 128), sb, 1};
@@ -1125,8 +1142,8 @@ hipError_t launch_outer(const Sizes &z, const Space &f, const uint16_t *x, int64
     a.Rp = (int)z.Rp;
     a.groups = (int)((z.R + 16 * rb - 1) / (16 * rb));
     a.first = (int)(z.L * a.job[0].blocks * a.groups * sa);
-    const dim3 grid((unsigned)(a.first + z.L * a.job[1].blocks * a.groups * sb)), block(64 * waves);
-    const size_t lds = (size_t)waves / 2 * rb * 8 * 64 * sizeof(v4f);
+    const dim3 grid((unsigned)(a.first + z.L * a.job[1].blocks * a.groups * sb)), block(64 * kOuterWaves);
+    const size_t lds = (size_t)kOuterWaves / 2 * rb * 8 * 64 * sizeof(v4f);
     if (rb == 1)
         hipLaunchKernelGGL((k_outer<1>), grid, block, lds, s, a);
     else if (rb == 2)

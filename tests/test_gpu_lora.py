@@ -67,7 +67,10 @@ SHAPES = [
     (2100, 520, 130, 8, 2, [0, -1], 32), (4001, 96, 120, 48, 6, "runs", 64), (600, 64, 200, 128, 3, None, 32),
     (7700, 72, 40, 16, 2, "runs", 32), (8193, 40, 72, 40, 9, None, 64), (16000, 40, 72, 24, 3, None, 32),
     (15500, 66, 48, 64, 1, [0], 32), (20000, 24, 16, 8, 2000, None, 32), (9001, 24, 16, 8, 2047, None, 64),
-    # K and N in parts that a launch of their own adds
+    # many tokens an adapter: both sides of the rules on their number, K whole and in parts
+    (63, 600, 72, 16, 1, [0], 32), (64, 600, 72, 16, 1, [0], 64), (200, 1100, 130, 96, 2, None, 32),
+    (300, 2000, 264, 32, 1, [0, -1], 32), (511, 4100, 1001, 64, 4, "runs", 32), (1000, 2056, 72, 128, 7, None, 32),
+    (520, 70, 200, 40, 8, None, 32), (7700, 264, 136, 128, 2, "runs", 32),
     (2100, 1100, 600, 24, 2, None, 32), (3000, 2600, 520, 72, 40, None, 64), (9000, 640, 1300, 16, 3, "runs", 32),
     (2049, 520, 4100, 40, 1, [0, -1], 32),
 ]
