@@ -62,7 +62,8 @@ template <> struct Code<uint8_t> {             // e4m3
     static __device__ inline float get(uint8_t v) { return __builtin_amdgcn_cvt_f32_fp8((int)v, 0); }
 };
 
-// A token belongs to `lanes` consecutive threads, each of which takes pieces of 16 bytes of the output.
+// A token belongs to `lanes` consecutive threads, each of which takes pieces of 16 bytes of the output.  Bytes bound it:
+// 8192 rows of 5120 in bf16 28.9 us, 5.8 TB/s; 16 rows 3.8 us, which is a launch.
 template <typename T, typename O>
 __global__ void __launch_bounds__(kThreads) k_embedding(LookArgs a)
 {
@@ -107,7 +108,8 @@ __global__ void __launch_bounds__(kThreads) k_embedding(LookArgs a)
 // ---------------------------------------------------------------------------
 // Sort of positions by token: least significant digit first, a counting sort a digit.  As pairs (key, position);
 // the key of a position without a row is the vocabulary's size, which comes last.  Its launches are short and
-// leave most of the GPU idle: the table's zeros are written beside them, a share in each.
+// leave most of the GPU idle: the table's zeros are written beside them, a share in each (a table of 131072 rows of 2048
+// in bf16, 537 MB: 100 us for both, 78 for the zeros alone).
 // ---------------------------------------------------------------------------
 constexpr int kDigitBits = 11;
 constexpr int kSortOne = 4096;                 // positions up to which one workgroup sorts alone
@@ -255,7 +257,8 @@ __device__ inline void store_row(const SumArgs &a, int row, int at, int n, const
     store_values<O, E>(o, v, n);
 }
 
-// kChunk sorted positions and 16 bytes of a row for each thread a workgroup.
+// kChunk sorted positions and 16 bytes of a row for each thread a workgroup.  The rows are read in no order and bound it:
+// 16384 of 2048 in bf16, 67 MB, 37 us (16 of them at once took as long).
 template <typename T, typename O>
 __global__ void __launch_bounds__(kThreads) k_sum(SumArgs a)
 {

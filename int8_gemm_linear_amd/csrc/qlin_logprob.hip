@@ -22,13 +22,13 @@ namespace qlin {
 namespace {
 
 constexpr int kThreads = 256, kWaves = kThreads / 64;
-constexpr int kPieces = 4;                     // 16-byte pieces a thread takes at a time
+constexpr int kPieces = 4;                     // 16-byte pieces a thread takes at a time (two: 113 us where four take 105)
 constexpr int kMaxTop = 64;                    // an alternative for each lane of a wave
 constexpr int kMaxParts = 64;                  // a part for each lane of the joining wave
 // Workgroups that fewer rows are divided into: five run on a CU at once (48 rows of 100003, 5 alternatives: 13.9 us,
 // with 2048 workgroups 15.4; 512 rows of 131072, 20 alternatives 50.6 and 56).
 constexpr int64_t kRowBlocks = 1280;
-constexpr int64_t kMaxRows = (int64_t)1 << 23; // x parts: below 2^32 threads
+constexpr int64_t kMaxRows = (int64_t)1 << 23; // one part each: below 2^32 threads
 constexpr int64_t kMaxVocab = (int64_t)1 << 28;
 constexpr int64_t kMaxStride = (int64_t)1 << 31;
 constexpr float kLowest = -200.0f, kLog2e = 1.4426950408889634f;
@@ -172,7 +172,9 @@ __device__ inline void load_chunk(v4i (&p)[kPieces], const T *x, int c, int end,
     }
 }
 
-// A part of a row for each workgroup.
+// A part of a row for each workgroup, a chunk's loads on their way while the one before is added up.  The logits'
+// bytes bound it, with the exponentials close behind (the vector units are busy for three quarters of the time): 2047
+// rows of 131072 in bf16, 98 us, 5.5 TB/s, with one alternative 105 us.
 template <typename T, bool TOP>
 __global__ void __launch_bounds__(kThreads) k_logprobs(Args a)
 {
@@ -317,7 +319,8 @@ __global__ void __launch_bounds__(kThreads) k_logprobs(Args a)
         a.list[p * a.top + tid] = merged[tid];
 }
 
-// The parts of a row.  A value that `top` of the parts' best reach bounds what can be among the alternatives; what
+// The parts of a row, for the few rows of a decoding step (1 row of 131072, 20 alternatives: both kernels 10.4 us, most
+// of it their launches and two trips to memory).  A value that `top` of the parts' best reach bounds what can be among the alternatives; what
 // reaches it is gathered and ranked.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) k_logprobs_join(Args a)
@@ -369,7 +372,8 @@ __global__ void __launch_bounds__(kThreads) k_logprobs_join(Args a)
     finish(a, row, s, merged, tid, target, logit);
 }
 
-// The logits' gradient: a part of a row for each workgroup, read and written once.
+// The logits' gradient: a part of a row for each workgroup, read and written once, which bounds it (4096 rows of 100003
+// in bf16, 280 us, 5.8 TB/s).
 // A row with g = h = 0 (padding) gets zeros and is not read, one without a distribution zeros.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) k_logprobs_backward(Args a)
