@@ -340,6 +340,51 @@ __device__ inline v4i row_part(const v4i *lds, int b, int half)
     return lds[128 * b + 8 * i + ((4 * half + (lane >> 4)) ^ (i & 7))];
 }
 
+// Adds the steps first, first + kShrinkWaves, .. before `end` of 16 TB tokens and the ranks from r0 of weights [R][K].
+template <int TB, int RB>
+__device__ inline void add_steps(v4f (&acc)[TB][RB], const uint16_t *const (&px)[TB][2], const uint16_t *rows, int R, int r0,
+                                 int K, int first, int end, v4i *mine)
+{
+    constexpr int U = steps_at_once<TB, RB>(), waves = kShrinkWaves;
+    const int lane = threadIdx.x & 63;
+    v4i *const weights = mine + TB * 128;
+    const uint16_t *pw[RB][2];                 // (ranks behind R take the last one's row: their sums are not read)
+#pragma unroll
+    for (int r = 0; r < RB; ++r)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            pw[r][h] = rows + (int64_t)min(r0 + 16 * r + 8 * h + (lane >> 3), R - 1) * K + 8 * (lane & 7);
+    for (int s = first; s < end; s += waves * U) {
+        v4i x[U][TB][2], w[U][RB][2];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (u > 0 && s + waves * u >= end)
+                break;
+            load_rows(x[u], px, (s + waves * u) * kStep, K);
+            load_rows(w[u], pw, (s + waves * u) * kStep, K);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (u > 0 && s + waves * u >= end)
+                break;
+            store_rows(mine, x[u]);
+            store_rows(weights, w[u]);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                v4i f[RB];
+#pragma unroll
+                for (int r = 0; r < RB; ++r) f[r] = row_part(weights, r, h);
+#pragma unroll
+                for (int t = 0; t < TB; ++t) {
+                    const v4i y = row_part(mine, t, h);
+#pragma unroll
+                    for (int r = 0; r < RB; ++r) acc[t][r] = mma(y, f[r], acc[t][r]);
+                }
+            }
+        }
+    }
+}
+
 // Where the pieces of adapter l's places begin, or of a tile of it (tiles have whole sixteens before them): at
 // eights, so that no two adapters share one, whatever their numbers of tokens.
 __host__ __device__ inline int64_t piece_place(int64_t place, int l) { return (place + 7) / 8 * 8 + 8 * (int64_t)l; }
@@ -400,44 +445,8 @@ __global__ void __launch_bounds__(64 * kShrinkWaves) k_shrink(ShrinkArgs a)
     const int steps = (job.K + kStep - 1) / kStep, r0 = 16 * RB * group;
     v4i *const mine = shared + wave * kShare, *const weights = mine + TB * 128;
     if (!BACK || !second) {
-        constexpr int U = steps_at_once<TB, RB>();
-        const uint16_t *pw[RB][2];             // (ranks behind R take the last one's row: their sums are not read)
-#pragma unroll
-        for (int r = 0; r < RB; ++r)
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-                pw[r][h] = job.w + ((int64_t)tile.x * a.R + min(r0 + 16 * r + 8 * h + (lane >> 3), a.R - 1)) * job.K +
-                           8 * (lane & 7);
         const int per = (steps + a.splits - 1) / a.splits, end = min((split + 1) * per, steps);
-        for (int s = split * per + wave; s < end; s += waves * U) {
-            v4i x[U][TB][2], w[U][RB][2];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                if (u > 0 && s + waves * u >= end)
-                    break;
-                load_rows(x[u], px, (s + waves * u) * kStep, job.K);
-                load_rows(w[u], pw, (s + waves * u) * kStep, job.K);
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                if (u > 0 && s + waves * u >= end)
-                    break;
-                store_rows(mine, x[u]);
-                store_rows(weights, w[u]);
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    v4i f[RB];
-#pragma unroll
-                    for (int r = 0; r < RB; ++r) f[r] = row_part(weights, r, h);
-#pragma unroll
-                    for (int t = 0; t < TB; ++t) {
-                        const v4i y = row_part(mine, t, h);
-#pragma unroll
-                        for (int r = 0; r < RB; ++r) acc[t][r] = mma(y, f[r], acc[t][r]);
-                    }
-                }
-            }
-        }
+        add_steps(acc, px, job.w + (int64_t)tile.x * a.R * job.K, a.R, r0, job.K, split * per + wave, end, mine);
     } else {
         // 64 rows of up to 2 RB chunks of 8 ranks a step, one row after another
         const int chunks = min(2 * RB, a.R / 8 - r0 / 8);
@@ -573,6 +582,18 @@ __device__ inline void load_factors(v4i (&hi)[G], v4i (&lo)[G], const ExpandArgs
     }
 }
 
+// The pieces of s times eight sums (with `only`: the lower ones as both).
+__device__ inline void cut_factors(v4i &hi, v4i &lo, const v4f (&sum)[2], float s, bool only)
+{
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float v0 = sum[e / 2][2 * e % 4] * s, v1 = sum[e / 2][2 * e % 4 + 1] * s, h0 = cut(v0), h1 = cut(v1);
+        const int high = pack2(h0, h1), low = pack2(rest(v0, h0), rest(v1, h1));
+        hi[e] = only ? low : high;
+        lo[e] = low;
+    }
+}
+
 // The same from the parts, four of them on their way at a time.
 template <int G, bool PACK>
 __device__ inline void add_factors(v4i (&hi)[G], v4i (&lo)[G], const ExpandArgs &a, int place, float s)
@@ -601,19 +622,109 @@ __device__ inline void add_factors(v4i (&hi)[G], v4i (&lo)[G], const ExpandArgs 
                 sum[1] += v[j][1];
             }
         }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float v0 = sum[e / 2][2 * e % 4] * s, v1 = sum[e / 2][2 * e % 4 + 1] * s, h0 = cut(v0), h1 = cut(v1);
-            const int high = pack2(h0, h1), low = pack2(rest(v0, h0), rest(v1, h1));
-            hi[g][e] = PACK && piece == 1 ? low : high;
-            lo[g][e] = low;
-        }
+        cut_factors(hi[g], lo[g], sum, s, PACK && piece == 1);
     }
 }
 
-// 64 n a wave at a time as four products of 16 n by 16 tokens, dealt to them so that a lane ends with twice eight n
-// in a row of its token, and four lanes with 64 bytes of it.  Weights' bytes bound it: 128 tokens of 24 adapters
-// of 64 ranks on N = 51200, 183 MB, 37 us, 5.0 TB/s.
+// 64 n of a wave as four products of 16 n by 16 tokens, dealt to them so that a lane ends with twice eight n
+// in a row of its token, and four lanes with 64 bytes of it.
+template <int G, bool PACK, bool TR>
+struct Few {
+    v4i o[2], f[4][G];         // this lane's outputs, n0 + 8 q .. + 7 and 32 behind; operands of the products
+
+    // `w`: the adapter's weights, NULL for none; `row`: the lane's token, -1 for none
+    __device__ void load(const ExpandArgs &a, const uint16_t *w, int64_t row, int n0)
+    {
+        const int lane = threadIdx.x & 63, i = lane & 15, q = lane >> 4;
+        const int ranks = a.R / 8;             // chunks of 8 ranks
+        o[0] = o[1] = v4i{0, 0, 0, 0};
+        if (a.base && row >= 0) {
+            const uint16_t *p = a.base + row * a.ldb + n0 + 8 * q;
+            const int left = a.N - (n0 + 8 * q);
+            o[0] = load8(p, left);
+            o[1] = load8(p + 32, left - 32);
+        }
+        if (!w)
+            return;
+        if (TR) {
+            // rows of eight ranks, four n of each: the lane's row 4 a + c of product m is
+            // n = 32 (c / 2) + 8 a + 4 (c % 2) + m
+            const int n = n0 + 32 * ((i & 3) >> 1) + 8 * (i >> 2) + 4 * (i & 1), there = a.N - n;
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                const int c = PACK ? q % ranks : 4 * g + q;
+                int2 r[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    r[j] = make_int2(0, 0);
+                    if (c < ranks && (!PACK || q < 2 * ranks)) {
+                        const uint16_t *p = w + (int64_t)(8 * c + j) * a.N + n;
+                        if (there >= 4) {
+                            __builtin_memcpy(&r[j], p, 8);
+                        } else {
+                            uint16_t e[4];
+#pragma unroll
+                            for (int m = 0; m < 4; ++m) e[m] = m < there ? p[m] : 0;
+                            __builtin_memcpy(&r[j], e, 8);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int m = 0; m < 4; ++m)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        f[m][g][j] = (int)__builtin_amdgcn_perm(
+                            (uint32_t)(m < 2 ? r[2 * j + 1].x : r[2 * j + 1].y),
+                            (uint32_t)(m < 2 ? r[2 * j].x : r[2 * j].y), m % 2 ? 0x07060302u : 0x05040100u);
+            }
+        } else {
+            // rows of n: row 4 a + c of product j is n = 32 (j / 2) + 8 a + 4 (j % 2) + c
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int n = min(n0 + 32 * (j >> 1) + 8 * (i >> 2) + 4 * (j & 1) + (i & 3), a.N - 1);
+#pragma unroll
+                for (int g = 0; g < G; ++g) {
+                    const int c = PACK ? q % ranks : 4 * g + q;
+                    f[j][g] = v4i{0, 0, 0, 0};
+                    if (c < ranks && (!PACK || q < 2 * ranks))
+                        f[j][g] = load8(w + (int64_t)n * a.R + 8 * c);
+                }
+            }
+        }
+    }
+
+    __device__ void add(const v4i (&hi)[G], const v4i (&lo)[G])
+    {
+        v4f acc[4] = {};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                acc[j] = mma(f[j][g], hi[g], acc[j]);
+                if (!PACK)
+                    acc[j] = mma(f[j][g], lo[g], acc[j]);
+            }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float d0 = TR ? acc[(2 * e) % 4][e / 2] : acc[e / 2][(2 * e) % 4];
+            const float d1 = TR ? acc[(2 * e + 1) % 4][e / 2] : acc[e / 2][(2 * e + 1) % 4];
+            const uint32_t d = (uint32_t)o[e / 4][e % 4];
+            o[e / 4][e % 4] = pack2(__uint_as_float(d << 16) + d0, __uint_as_float(d & 0xFFFF0000u) + d1);
+        }
+    }
+
+    __device__ void store(const ExpandArgs &a, int64_t row, int n0) const
+    {
+        if (row < 0)
+            return;
+        const int q = (threadIdx.x & 63) >> 4, left = a.N - (n0 + 8 * q);
+        uint16_t *p = a.out + row * a.ldo + n0 + 8 * q;
+        store8(p, o[0], left);
+        store8(p + 32, o[1], left - 32);
+    }
+};
+
+// Weights' bytes bound it: 128 tokens of 24 adapters of 64 ranks on N = 51200, 183 MB, 37 us, 5.0 TB/s.
 template <int G, bool PACK, bool TR>
 __global__ void __launch_bounds__(kThreads) k_expand_few(ExpandArgs a)
 {
@@ -621,14 +732,13 @@ __global__ void __launch_bounds__(kThreads) k_expand_few(ExpandArgs a)
     const int chunk = blockIdx.x % a.chunks;
     if (tile.w == 0)
         return;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = lane & 15, q = lane >> 4;
-    const int ranks = a.R / 8;                 // chunks of 8 ranks
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = lane & 15;
     const bool live = tile.x >= 0;
-    const int64_t token = a.order[tile.y + min(i, tile.w - 1)];
+    const int place = tile.y + min(i, tile.w - 1);
+    const int64_t token = i < tile.w ? a.order[place] : -1;
     v4i hi[G], lo[G];
-    const uint16_t *w = a.w + (int64_t)(live ? tile.x : 0) * a.N * a.R;
+    const uint16_t *w = live ? a.w + (int64_t)tile.x * a.N * a.R : nullptr;
     if (live) {
-        const int place = tile.y + min(i, tile.w - 1);
         if (!TR && a.part)
             add_factors<G, PACK>(hi, lo, a, place, a.scale ? a.scale[tile.x] : 1.0f);
         else
@@ -636,85 +746,72 @@ __global__ void __launch_bounds__(kThreads) k_expand_few(ExpandArgs a)
     }
     const int blocks = (a.N + 63) / 64;
     for (int b = chunk * kWaves + wave; b < blocks; b += a.chunks * kWaves) {
-        const int n0 = 64 * b;
-        // this lane's outputs: n0 + 8 q .. + 7 and 32 behind
-        const int left = a.N - (n0 + 8 * q);
-        v4i o[2] = {};
-        if (a.base && i < tile.w) {
-            const uint16_t *p = a.base + token * a.ldb + n0 + 8 * q;
-            o[0] = load8(p, left);
-            o[1] = load8(p + 32, left - 32);
-        }
-        if (live) {
-            v4i f[4][G];
-            if (TR) {
-                // rows of eight ranks, four n of each: the lane's row 4 a + c of product m is
-                // n = 32 (c / 2) + 8 a + 4 (c % 2) + m
-                const int n = n0 + 32 * ((i & 3) >> 1) + 8 * (i >> 2) + 4 * (i & 1), there = a.N - n;
-#pragma unroll
-                for (int g = 0; g < G; ++g) {
-                    const int c = PACK ? q % ranks : 4 * g + q;
-                    int2 r[8];
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        r[j] = make_int2(0, 0);
-                        if (c < ranks && (!PACK || q < 2 * ranks)) {
-                            const uint16_t *p = w + (int64_t)(8 * c + j) * a.N + n;
-                            if (there >= 4) {
-                                __builtin_memcpy(&r[j], p, 8);
-                            } else {
-                                uint16_t e[4];
-#pragma unroll
-                                for (int m = 0; m < 4; ++m) e[m] = m < there ? p[m] : 0;
-                                __builtin_memcpy(&r[j], e, 8);
-                            }
-                        }
-                    }
-#pragma unroll
-                    for (int m = 0; m < 4; ++m)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            f[m][g][j] = (int)__builtin_amdgcn_perm(
-                                (uint32_t)(m < 2 ? r[2 * j + 1].x : r[2 * j + 1].y),
-                                (uint32_t)(m < 2 ? r[2 * j].x : r[2 * j].y), m % 2 ? 0x07060302u : 0x05040100u);
-                }
-            } else {
-                // rows of n: row 4 a + c of product j is n = 32 (j / 2) + 8 a + 4 (j % 2) + c
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int n = min(n0 + 32 * (j >> 1) + 8 * (i >> 2) + 4 * (j & 1) + (i & 3), a.N - 1);
-#pragma unroll
-                    for (int g = 0; g < G; ++g) {
-                        const int c = PACK ? q % ranks : 4 * g + q;
-                        f[j][g] = v4i{0, 0, 0, 0};
-                        if (c < ranks && (!PACK || q < 2 * ranks))
-                            f[j][g] = load8(w + (int64_t)n * a.R + 8 * c);
-                    }
-                }
-            }
-            v4f acc[4] = {};
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-                for (int g = 0; g < G; ++g) {
-                    acc[j] = mma(f[j][g], hi[g], acc[j]);
-                    if (!PACK)
-                        acc[j] = mma(f[j][g], lo[g], acc[j]);
-                }
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float d0 = TR ? acc[(2 * e) % 4][e / 2] : acc[e / 2][(2 * e) % 4];
-                const float d1 = TR ? acc[(2 * e + 1) % 4][e / 2] : acc[e / 2][(2 * e + 1) % 4];
-                const uint32_t d = (uint32_t)o[e / 4][e % 4];
-                o[e / 4][e % 4] = pack2(__uint_as_float(d << 16) + d0, __uint_as_float(d & 0xFFFF0000u) + d1);
-            }
-        }
-        if (i >= tile.w)
-            continue;
-        uint16_t *p = a.out + token * a.ldo + n0 + 8 * q;
-        store8(p, o[0], left);
-        store8(p + 32, o[1], left - 32);
+        Few<G, PACK, TR> n;
+        n.load(a, w, token, 64 * b);
+        if (live)
+            n.add(hi, lo);
+        n.store(a, token, 64 * b);
     }
+}
+
+// Few tokens of adapters that are small: both products in one launch, every workgroup with its own sums of all of K for
+// the tile whose 512 n it has.  A launch less is worth more than the reads of A by every workgroup while these are one a
+// CU at most: a token, 16 ranks, K = N = 2048 5.7 us, in two launches 7.4, and 3 us less of the calling thread's time.
+template <int RB>
+__global__ void __launch_bounds__(64 * kShrinkWaves) k_both(ShrinkArgs s, ExpandArgs a)
+{
+    constexpr bool PACK = RB == 1;
+    constexpr int kRow = 16 * RB + 4;          // a token's sums (a row's start falls on other banks than the last's)
+    extern __shared__ v4i shared[];            // [waves][shrink_share]
+    __shared__ __align__(16) float sums[16 * kRow];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = lane & 15, q = lane >> 4;
+    int sorted;
+    const int4 tile = wave_plan(s.plan, blockIdx.x / a.chunks, sorted);
+    const int there = __shfl(sorted, tile.y + min(i, max(tile.z, 1) - 1));
+    if (tile.z == 0)
+        return;
+    const bool live = tile.x >= 0;
+    const int64_t token = i < tile.z ? there : -1;
+    const uint16_t *w = live ? a.w + (int64_t)tile.x * a.N * a.R : nullptr;
+    const int n0 = 64 * (blockIdx.x % a.chunks * kShrinkWaves + wave);
+    Few<1, PACK, false> n;
+    if (n0 < a.N)
+        n.load(a, w, token, n0);               // (on its way meanwhile)
+    v4i hi[1], lo[1];
+    if (live) {
+        const ShrinkJob &job = s.job[0];
+        const uint16_t *px[1][2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) px[0][h] = job.x + __shfl(there, 8 * h + (lane >> 3)) * job.ldx + 8 * (lane & 7);
+        v4f acc[1][RB] = {};
+        add_steps(acc, px, job.w + (int64_t)tile.x * s.R * job.K, s.R, 0, job.K, wave, (job.K + kStep - 1) / kStep,
+                  shared + wave * shrink_share(1, RB));
+        __syncthreads();
+        v4f *parts = reinterpret_cast<v4f *>(shared);
+#pragma unroll
+        for (int r = 0; r < RB; ++r) parts[(wave * RB + r) * 64 + lane] = acc[0][r];
+        __syncthreads();
+        if (threadIdx.x < 64 * RB) {
+            v4f v = parts[threadIdx.x];
+#pragma unroll
+            for (int k = 1; k < kShrinkWaves; ++k) v += parts[k * RB * 64 + threadIdx.x];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) sums[(4 * q + c) * kRow + 16 * wave + i] = v[c];
+        }
+        __syncthreads();
+        const int ranks = a.R / 8, c = PACK ? q % ranks : q, piece = PACK ? q / ranks : 0;
+        hi[0] = lo[0] = v4i{0, 0, 0, 0};
+        if (c < ranks && piece < 2) {
+            const v4f *v = reinterpret_cast<const v4f *>(sums + i * kRow + 8 * c);
+            const v4f sum[2] = {v[0], v[1]};
+            cut_factors(hi[0], lo[0], sum, a.scale ? a.scale[tile.x] : 1.0f, PACK && piece == 1);
+        }
+    }
+    if (n0 >= a.N)
+        return;
+    if (live)
+        n.add(hi, lo);
+    n.store(a, token, n0);
 }
 
 // 128 n a workgroup at a time, 16 tokens a wave: eight products of 16 tokens by 16 n, the m-th with the n = 8 i + m,
@@ -1129,6 +1226,33 @@ hipError_t launch_expand(const Sizes &z, const Space &f, const float *scale, con
     return hipGetLastError();
 }
 
+// Workgroups of the kernel that has both products: 512 n of a tile each.
+int64_t both_chunks(int64_t N) { return (N + 64 * kShrinkWaves - 1) / (64 * kShrinkWaves); }
+
+// Whether it is taken (16 ranks, both kernels): K = 2048, 16 tokens of 12 adapters on N = 10240, some 240 workgroups, 8.7
+// us, in two launches 9.6; 32 of 28, 560 workgroups, 20.9 and 12.2; a token, K = N = 4096 7.6 and 7.6, 5120 8.8 and 8.0.
+bool one_launch(const Sizes &z)
+{
+    return z.T <= kWaveTokens && z.wide == 1 && z.Rp <= 32 && z.Rp * z.K <= 65536 && z.max_tiles * both_chunks(z.N) <= 320;   // (with tiles that stay empty)
+}
+
+hipError_t launch_both(const Sizes &z, const Space &f, const void *ids, int32_t id_bits, ShrinkArgs &a, const float *scale,
+                       const uint16_t *w, const uint16_t *base, int64_t ldb, uint16_t *out, int64_t ldo, hipStream_t s)
+{
+    const hipError_t p = make_plan(z, f, ids, id_bits, a, s);          // (no launch: every wave makes its own)
+    if (p != hipSuccess)
+        return p;
+    const int chunks = (int)both_chunks(z.N);
+    const ExpandArgs e{nullptr, nullptr, scale, (int)z.T, 1, nullptr, nullptr, w, base, out, ldb, ldo, (int)z.N, (int)z.R, (int)z.Rp, chunks};
+    const dim3 grid((unsigned)(z.max_tiles * chunks)), block(64 * kShrinkWaves);
+    const size_t lds = kShrinkWaves * shrink_share(1, (int)z.Rp / 16) * sizeof(v4i);
+    if (z.Rp == 16)
+        hipLaunchKernelGGL((k_both<1>), grid, block, lds, s, a, e);
+    else
+        hipLaunchKernelGGL((k_both<2>), grid, block, lds, s, a, e);
+    return hipGetLastError();
+}
+
 hipError_t launch_outer(const Sizes &z, const Space &f, const uint16_t *x, int64_t ldx, const uint16_t *dy, int64_t lddy,
                         float *da, float *db, hipStream_t s)
 {
@@ -1207,6 +1331,8 @@ qlin_status qlin_lora_mm(int32_t id_bits, int64_t tokens, int64_t K, int64_t N, 
     a.R = (int)rank;
     a.Rp = (int)z.Rp;
     a.groups = z.groups;
+    if (one_launch(z))
+        return launch_both(z, f, ids, id_bits, a, scale, B, base, ldb, Y, ldy, s) == hipSuccess ? QLIN_OK : QLIN_ERR_HIP;
     if (make_plan(z, f, ids, id_bits, a, s) != hipSuccess || launch_shrink<false>(z, a, s) != hipSuccess ||
         launch_expand<false>(z, f, scale, B, N, base, ldb, Y, ldy, s) != hipSuccess)
         return QLIN_ERR_HIP;

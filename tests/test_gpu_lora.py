@@ -67,6 +67,10 @@ SHAPES = [
     (2100, 520, 130, 8, 2, [0, -1], 32), (4001, 96, 120, 48, 6, "runs", 64), (600, 64, 200, 128, 3, None, 32),
     (7700, 72, 40, 16, 2, "runs", 32), (8193, 40, 72, 40, 9, None, 64), (16000, 40, 72, 24, 3, None, 32),
     (15500, 66, 48, 64, 1, [0], 32), (20000, 24, 16, 8, 2000, None, 32), (9001, 24, 16, 8, 2047, None, 64),
+    # few tokens and small adapters, and just beyond what one launch takes
+    (1, 4096, 512, 16, 3, [2], 32), (1, 4104, 513, 16, 3, [-1], 64), (3, 2048, 1001, 32, 2, [1, -1, 0], 32),
+    (64, 300, 700, 8, 70, None, 32), (63, 520, 1500, 24, 3, None, 64), (16, 65, 9000, 16, 12, None, 32),
+    (20, 1000, 40, 40, 5, None, 32), (64, 200, 2600, 32, 60, None, 64),
     # many tokens an adapter: both sides of the rules on their number, K whole and in parts
     (63, 600, 72, 16, 1, [0], 32), (64, 600, 72, 16, 1, [0], 64), (200, 1100, 130, 96, 2, None, 32),
     (300, 2000, 264, 32, 1, [0, -1], 32), (511, 4100, 1001, 64, 4, "runs", 32), (1000, 2056, 72, 128, 7, None, 32),
