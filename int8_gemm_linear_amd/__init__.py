@@ -1096,8 +1096,8 @@ def embedding(ids, table, row_scale=None, scale: float = 1.0, dtype=None, out=No
 
 def embedding_backward(dout, ids, vocab: int, scale: float = 1.0, dtype=None, out=None, accumulate: bool = False):
     """Gradient of embedding with respect to a plain table: dtable [V,H],
-    dtable[v] = scale * sum of dout[t] over the t with ids[t] = v, fp32 sums in the
-    order of t, zeros for rows of no token.  dout [T,H] float32, bfloat16 or float16;
+    dtable[v] = scale * sum of dout[t] over the t with ids[t] = v, fp32 sums in an
+    order that only ids decide, zeros for rows of no token.  dout [T,H] float32, bfloat16 or float16;
     `dtype` is dout's (the default) or float32.  With accumulate=True the sums are
     added to what `out` holds, and rows of no token stay as they are."""
     rt, dev = _row_type(dout, "dout"), dout.device
