@@ -1210,9 +1210,13 @@ template <bool TR>
 hipError_t launch_expand(const Sizes &z, const Space &f, const float *scale, const uint16_t *w, int64_t N, const uint16_t *base, int64_t ldb,
                          uint16_t *out, int64_t ldo, hipStream_t s)
 {
+    // Workgroups of a tile.  Many tokens: three blocks of 128 n each at most (65536 tokens, K = N = 2048, 16 ranks, both
+    // kernels: one block 186 us, three 187, four 203, eight 219; 8192 tokens, 5120 and 5120, 64 ranks: one 122, three 113),
+    // fewer where the tiles alone are too few
     const int64_t full = z.wide > 1 ? (N + 127) / 128 : (N + 64 * kWaves - 1) / (64 * kWaves);
-    const int64_t tiles = z.T / (16 * z.wide) + std::min(z.L + 1, z.T);
-    const int chunks = (int)std::max<int64_t>(1, std::min<int64_t>(full, (z.wide > 1 ? 2048 : 8192) / tiles));
+    const int64_t tiles = z.T / (16 * z.wide) + std::min(z.L + 1, z.T), least = z.wide > 1 ? (full + 2) / 3 : 1;
+    const int64_t want = std::max(least, std::min<int64_t>(full, (z.wide > 1 ? 2048 : 8192) / tiles));
+    const int chunks = (int)std::max<int64_t>(1, std::min<int64_t>(want, (((int64_t)1 << 24) - 1) / z.max_tiles));
     const ExpandArgs a{f.rows, f.part, scale, (int)z.T, z.splits, f.order, f.tiles, w, base, out, ldb, ldo, (int)N, (int)z.R, (int)z.Rp, chunks};
     const dim3 grid((unsigned)(z.max_tiles * chunks));
     if (z.R <= 16)
