@@ -96,7 +96,9 @@ struct Plan {
     int32_t *offsets;          // [adapters + 1]: the first place of each adapter (NULL: not wanted)
     int4 *tiles;               // [max_tiles]: adapter (-1: none), first place, tokens (0: no tile), and the
                                // tokens of the expand tile that begins here (0: none does)
-    int tokens, adapters, tile, wide, max_tiles, id_bits;
+    int4 *wides;               // [max_wides]: the tiles where an expand tile begins (NULL: not wanted); without it
+                               // the others' workgroups of the expand kernel, which have no work, cost it up to 3 us
+    int tokens, adapters, tile, wide, max_tiles, max_wides, id_bits;
 };
 
 __device__ inline int bin_of(const Plan &p, int t)
@@ -152,19 +154,28 @@ __global__ void __launch_bounds__(kSortThreads) k_plan_place(ManyArgs a)
         return;
     const int32_t *total = hist + kSortWaves * a.digits;
     const int lane = threadIdx.x & 63;
-    int at0 = 0, tile0 = 0;
+    int at0 = 0, tile0 = 0, wide0 = 0;
     for (int b0 = 0; b0 <= p.adapters; b0 += 64) {          // (by each wave, which takes its share of the tiles)
         const int b = b0 + lane, n = b <= p.adapters ? total[b] : 0, tiles = (n + p.tile - 1) / p.tile;
         const int at = at0 + wave_scan(n) - n, tile = tile0 + wave_scan(tiles) - tiles;
+        const int wides = (n + p.wide - 1) / p.wide, wide = wide0 + wave_scan(wides) - wides;
         if (b <= p.adapters) {
             if (p.offsets && threadIdx.x < 64)
                 p.offsets[b] = at;             // (that of the last bin: tokens with an adapter)
-            for (int j = threadIdx.x >> 6; j < tiles; j += kSortWaves) p.tiles[tile + j] = tile_of(p, b, at, n, j);
+            for (int j = threadIdx.x >> 6; j < tiles; j += kSortWaves) {
+                const int4 t = tile_of(p, b, at, n, j);
+                p.tiles[tile + j] = t;
+                if (p.wides && t.w)
+                    p.wides[wide + j * p.tile / p.wide] = t;
+            }
         }
         at0 = __builtin_amdgcn_readlane(at + n, 63);
         tile0 = __builtin_amdgcn_readlane(tile + tiles, 63);
+        wide0 = __builtin_amdgcn_readlane(wide + wides, 63);
     }
     for (int t = tile0 + (int)threadIdx.x; t < p.max_tiles; t += kSortThreads) p.tiles[t] = make_int4(-1, 0, 0, 0);
+    if (p.wides)
+        for (int t = wide0 + (int)threadIdx.x; t < p.max_wides; t += kSortThreads) p.wides[t] = make_int4(-1, 0, 0, 0);
 }
 
 // Up to 64 tokens: every wave of the shrink kernel finds its tile by itself, without LDS or a barrier.  `token`
@@ -207,8 +218,9 @@ __device__ inline int4 wave_plan(const Plan &p, int want, int &token)
 constexpr int kHold = 16;
 constexpr int kSelfTokens = 64 * 8 * kHold;
 
-// The tile `want`; its tokens in `token` (LDS); `hist` [waves][adapters + 1] (LDS).  Called by all threads.
-__device__ inline int4 self_plan(const Plan &p, int want, int32_t *hist, int32_t *token)
+// The tile `want`; its tokens in `token` (LDS); `hist` [waves][adapters + 1] (LDS).  Called by all threads.  With `publish`
+// it goes to the plan's lists.
+__device__ inline int4 self_plan(const Plan &p, int want, int32_t *hist, int32_t *token, bool publish)
 {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6, bins = p.adapters + 1;
     const int turns = (p.tokens + (int)blockDim.x - 1) / (int)blockDim.x, beg = wave * turns * 64 + lane;
@@ -225,13 +237,14 @@ __device__ inline int4 self_plan(const Plan &p, int want, int32_t *hist, int32_t
     }
     __syncthreads();
     int4 found = make_int4(-1, 0, 0, 0);
-    int bin = -1, skip = 0;
-    const bool offsets = want == 0 && wave == 0 && p.offsets;
-    for (int b0 = 0, at0 = 0, tile0 = 0; b0 < bins && (offsets || bin < 0); b0 += 64) {
+    int bin = -1, skip = 0, wide0 = 0, at_wide = 0;
+    const bool offsets = want == 0 && wave == 0 && p.offsets, all = offsets || (wave == 0 && publish && p.wides);
+    for (int b0 = 0, at0 = 0, tile0 = 0; b0 < bins && (all || bin < 0); b0 += 64) {
         int n = 0;
         if (b0 + lane < bins)
             for (int w = 0; w < waves; ++w) n += hist[w * bins + b0 + lane];
         const int tiles = (n + p.tile - 1) / p.tile, at = at0 + wave_scan(n) - n, tile = tile0 + wave_scan(tiles) - tiles;
+        const int wides = (n + p.wide - 1) / p.wide, wide = wide0 + wave_scan(wides) - wides;
         if (offsets && b0 + lane < bins)
             p.offsets[b0 + lane] = at;
         const uint64_t here = __ballot(want >= tile && want < tile + tiles);
@@ -240,9 +253,18 @@ __device__ inline int4 self_plan(const Plan &p, int want, int32_t *hist, int32_t
             bin = b0 + l;
             skip = j * p.tile;
             found = tile_of(p, bin, __builtin_amdgcn_readlane(at, l), __builtin_amdgcn_readlane(n, l), j);
+            at_wide = __builtin_amdgcn_readlane(wide, l) + skip / p.wide;
         }
         at0 = __builtin_amdgcn_readlane(at + n, 63);
         tile0 = __builtin_amdgcn_readlane(tile + tiles, 63);
+        wide0 = __builtin_amdgcn_readlane(wide + wides, 63);
+    }
+    if (publish && threadIdx.x == 0) {
+        p.tiles[want] = found;
+        if (p.wides && found.w)
+            p.wides[at_wide] = found;
+        if (p.wides && want >= wide0 && want < p.max_wides)
+            p.wides[want] = make_int4(-1, 0, 0, 0);
     }
     if (bin < 0)
         return found;                          // (in all waves)
@@ -418,9 +440,11 @@ __global__ void __launch_bounds__(64 * kShrinkWaves) k_shrink(ShrinkArgs a)
         const int there = __shfl(sorted, (tile.y + lane) & 63);          // (by all lanes)
         if (publish && wave == 0 && lane < tile.z)
             a.plan.order[tile.y + lane] = there;
+        if (publish && tid == 0)
+            a.plan.tiles[index] = tile;
     } else {
         if (a.self) {
-            tile = self_plan(a.plan, index, reinterpret_cast<int32_t *>(shared), tokens);
+            tile = self_plan(a.plan, index, reinterpret_cast<int32_t *>(shared), tokens, publish);
             if (publish && tid < tile.z)
                 a.plan.order[tile.y + tid] = tokens[tid];
 #pragma unroll
@@ -431,8 +455,6 @@ __global__ void __launch_bounds__(64 * kShrinkWaves) k_shrink(ShrinkArgs a)
             for (int t = 0; t < TB; ++t) token[t] = tile.z ? a.plan.order[tile.y + min(16 * t + i, tile.z - 1)] : 0;
         }
     }
-    if (a.self && publish && tid == 0)
-        a.plan.tiles[index] = tile;
     if (tile.x < 0 || tile.z == 0)
         return;
     const uint16_t *px[TB][2];                 // rows l / 8 and 8 behind of each block
@@ -1055,7 +1077,7 @@ struct Sizes {
     int64_t Rp;                // ranks in whole blocks of 16: 1, 2, 4 or 8
     int tb, rb, groups;        // shrink: blocks of tokens and ranks of a workgroup, groups of ranks
     int wide;                  // expand: blocks of tokens
-    int max_tiles;
+    int max_tiles, max_wides;  // the latter 0 where every tile begins an expand tile (or tokens are few)
     int splits;                // shrink of the forward call: parts of K
 };
 
@@ -1070,7 +1092,7 @@ constexpr int64_t kManyTokens = 64;
 
 Sizes sizes(int64_t T, int64_t K, int64_t N, int64_t R, int64_t L)
 {
-    Sizes z{T, K, N, R, L, 16, 1, 1, 1, 1, 0, 1};
+    Sizes z{T, K, N, R, L, 16, 1, 1, 1, 1, 0, 0, 1};
     while (z.Rp < R) z.Rp *= 2;
     const int64_t mean = T / std::min(L, std::max<int64_t>(T, 1));
     z.wide = mean >= kManyTokens ? kWide / 16 : 1;
@@ -1079,6 +1101,8 @@ Sizes sizes(int64_t T, int64_t K, int64_t N, int64_t R, int64_t L)
     // 2048: 16 at a time 270 us, 32 248, 64 235)
     while (z.tb < z.wide && T >= 16 * 2 * z.tb * 240) z.tb *= 2;
     z.max_tiles = (int)std::max<int64_t>(1, T / (16 * z.tb) + std::min(L + 1, T));
+    if (z.wide > z.tb && T > kWaveTokens)
+        z.max_wides = (int)(T / (16 * z.wide) + std::min(L + 1, T));
     // and 32 ranks a workgroup likewise (8192 tokens of 64 ranks: 16 at a time 136 us, 32 113, 64 115)
     if (z.Rp > 16 && z.max_tiles * (z.Rp / 16) > 512)
         z.rb = 2;
@@ -1115,7 +1139,7 @@ struct Layout {
 
 struct Space {
     int32_t *order, *offsets, *counts;
-    int4 *tiles;
+    int4 *tiles, *wides;
     uint16_t *rows;            // of s v (backward: s u) for expand
     float *part;               // or the parts of v
     uint16_t *fv, *fu;         // backward: the pieces of s v and s u for outer
@@ -1136,6 +1160,7 @@ Space space(const Sizes &z, void *ws, bool back)
     Space f{};
     f.order = l.take<int32_t>(z.T);
     f.tiles = l.take<int4>(z.max_tiles);
+    f.wides = z.max_wides ? l.take<int4>(z.max_wides) : nullptr;
     f.counts = l.take<int32_t>(z.T > kSelfTokens ? (int64_t)sort_parts(z.T) * plan_digits(z.L) : 0);
     if (back || z.splits == 1)
         f.rows = l.take<uint16_t>(z.T * 2 * z.Rp);
@@ -1180,7 +1205,7 @@ hipError_t launch_shrink(const Sizes &z, const ShrinkArgs &a, hipStream_t s)
 // Fills in the plan, and makes it in a launch of its own where the tokens are too many for each workgroup.
 hipError_t make_plan(const Sizes &z, const Space &f, const void *ids, int32_t id_bits, ShrinkArgs &a, hipStream_t s)
 {
-    a.plan = Plan{ids, f.order, f.offsets, f.tiles, (int)z.T, (int)z.L, 16 * z.tb, 16 * z.wide, z.max_tiles, id_bits};
+    a.plan = Plan{ids, f.order, f.offsets, f.tiles, f.wides, (int)z.T, (int)z.L, 16 * z.tb, 16 * z.wide, z.max_tiles, z.max_wides, id_bits};
     a.self = z.T == 0 || z.T > kSelfTokens ? 0 : z.T <= kWaveTokens ? 1 : 2;
     if (a.self)
         return hipSuccess;
@@ -1214,11 +1239,11 @@ hipError_t launch_expand(const Sizes &z, const Space &f, const float *scale, con
     // kernels: one block 186 us, three 187, four 203, eight 219; 8192 tokens, 5120 and 5120, 64 ranks: one 122, three 113),
     // fewer where the tiles alone are too few
     const int64_t full = z.wide > 1 ? (N + 127) / 128 : (N + 64 * kWaves - 1) / (64 * kWaves);
-    const int64_t tiles = z.T / (16 * z.wide) + std::min(z.L + 1, z.T), least = z.wide > 1 ? (full + 2) / 3 : 1;
+    const int64_t tiles = z.max_wides ? z.max_wides : z.max_tiles, least = z.wide > 1 ? (full + 2) / 3 : 1;
     const int64_t want = std::max(least, std::min<int64_t>(full, (z.wide > 1 ? 2048 : 8192) / tiles));
-    const int chunks = (int)std::max<int64_t>(1, std::min<int64_t>(want, (((int64_t)1 << 24) - 1) / z.max_tiles));
-    const ExpandArgs a{f.rows, f.part, scale, (int)z.T, z.splits, f.order, f.tiles, w, base, out, ldb, ldo, (int)N, (int)z.R, (int)z.Rp, chunks};
-    const dim3 grid((unsigned)(z.max_tiles * chunks));
+    const int chunks = (int)std::max<int64_t>(1, std::min<int64_t>(want, (((int64_t)1 << 24) - 1) / tiles));
+    const ExpandArgs a{f.rows, f.part, scale, (int)z.T, z.splits, f.order, f.wides ? f.wides : f.tiles, w, base, out, ldb, ldo, (int)N, (int)z.R, (int)z.Rp, chunks};
+    const dim3 grid((unsigned)(tiles * chunks));
     if (z.R <= 16)
         expand_kernel<1, true, TR>(z, a, grid, s);
     else if (z.R <= 32)

@@ -74,7 +74,8 @@ SHAPES = [
     # many tokens an adapter: both sides of the rules on their number, K whole and in parts
     (63, 600, 72, 16, 1, [0], 32), (64, 600, 72, 16, 1, [0], 64), (200, 1100, 130, 96, 2, None, 32),
     (300, 2000, 264, 32, 1, [0, -1], 32), (511, 4100, 1001, 64, 4, "runs", 32), (1000, 2056, 72, 128, 7, None, 32),
-    (520, 70, 200, 40, 8, None, 32), (7700, 264, 136, 128, 2, "runs", 32),
+    (520, 70, 200, 40, 8, None, 32), (8000, 40, 136, 16, 100, None, 32), (8192, 40, 72, 8, 128, "runs", 64),
+    (12000, 24, 264, 8, 150, None, 32), (9000, 40, 130, 24, 70, "runs", 32), (7700, 264, 136, 128, 2, "runs", 32),
     (2100, 1100, 600, 24, 2, None, 32), (3000, 2600, 520, 72, 40, None, 64), (9000, 640, 1300, 16, 3, "runs", 32),
     (2049, 520, 4100, 40, 1, [0, -1], 32),
 ]
