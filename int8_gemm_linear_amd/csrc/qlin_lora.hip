@@ -1063,14 +1063,28 @@ __global__ void __launch_bounds__(64 * kOuterWaves, 2) k_outer(OuterArgs a)
     }
 }
 
-// out = the splits' parts, added in order.
-__global__ void __launch_bounds__(kThreads) k_add_parts(float *out, const float *part, int64_t size, int splits)
+// out = the splits' parts, added in order, four elements a thread (whole numbers of four: ranks are).  Both gradients in one
+// launch: 2048 tokens of an adapter, 16 ranks, K = N = 2048, all kernels 37.8 us in two, 34.7 in one.
+struct AddArgs {
+    float *out[2];
+    const float *part[2];
+    int64_t size[2], first;    // elements; threads of the first gradient
+    int splits[2];
+};
+
+__global__ void __launch_bounds__(kThreads) k_add_parts(AddArgs a)
 {
-    const int64_t step = (int64_t)gridDim.x * kThreads;
-    for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < size; i += step) {
-        float v = 0.0f;
-        for (int k = 0; k < splits; ++k) v += part[k * size + i];
-        out[i] = v;
+    const int64_t step = (int64_t)gridDim.x * kThreads, all = a.first + a.size[1] / 4;
+    for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < all; i += step) {
+        const int j = i >= a.first;
+        const int64_t at = 4 * (j ? i - a.first : i);
+        v4f v = {};
+        for (int k = 0; k < a.splits[j]; ++k) {
+            v4f t;
+            __builtin_memcpy(&t, a.part[j] + k * a.size[j] + at, 16);
+            v += t;
+        }
+        __builtin_memcpy(a.out[j] + at, &v, 16);
     }
 }
 
@@ -1308,16 +1322,21 @@ hipError_t launch_outer(const Sizes &z, const Space &f, const uint16_t *x, int64
         hipLaunchKernelGGL((k_outer<2>), grid, block, lds, s, a);
     else
         hipLaunchKernelGGL((k_outer<4>), grid, block, lds, s, a);
-    hipError_t e = hipGetLastError();
-    for (int j = 0; j < 2 && e == hipSuccess; ++j) {
+    const hipError_t e = hipGetLastError();
+    AddArgs add{};
+    for (int j = 0; j < 2; ++j) {
         const OuterJob &o = a.job[j];
-        if (o.splits == 1)
-            continue;
-        hipLaunchKernelGGL(k_add_parts, dim3((unsigned)std::min<int64_t>((o.size + kThreads - 1) / kThreads, 4096)),
-                           dim3(kThreads), 0, s, j ? db : da, o.out, o.size, o.splits);
-        e = hipGetLastError();
+        add.out[j] = j ? db : da;
+        add.part[j] = o.out;
+        add.size[j] = o.splits > 1 ? o.size : 0;
+        add.splits[j] = o.splits;
     }
-    return e;
+    add.first = add.size[0] / 4;
+    const int64_t blocks = (add.first + add.size[1] / 4 + kThreads - 1) / kThreads;
+    if (e != hipSuccess || blocks == 0)
+        return e;
+    hipLaunchKernelGGL(k_add_parts, dim3((unsigned)std::min<int64_t>(blocks, 4096)), dim3(kThreads), 0, s, add);
+    return hipGetLastError();
 }
 
 }  // namespace
