@@ -1122,8 +1122,9 @@ Sizes sizes(int64_t T, int64_t K, int64_t N, int64_t R, int64_t L)
     z.max_tiles = (int)std::max<int64_t>(1, T / (16 * z.tb) + std::min(L + 1, T));
     if (z.wide > z.tb && T > kWaveTokens)
         z.max_wides = (int)(T / (16 * z.wide) + std::min(L + 1, T));
-    // and 32 ranks a workgroup likewise (8192 tokens of 64 ranks: 16 at a time 136 us, 32 113, 64 115)
-    if (z.Rp > 16 && z.max_tiles * (z.Rp / 16) > 512)
+    // and 32 ranks a workgroup likewise (64 ranks, K = N = 5120, both kernels: 8192 tokens of 8 adapters, 528 workgroups
+    // then, 113 us, 16 at a time 136; 1024 of 32, 194, 34 and 38; 256 of 64, 162, 28 and 26)
+    if (z.Rp > 16 && z.max_tiles * (z.Rp / 16) > 360)
         z.rb = 2;
     z.groups = (int)((R + 16 * z.rb - 1) / (16 * z.rb));
     // few workgroups: parts of K, a step for each wave at least (a CU alone loads some 50 GB/s: 256 tokens of an
