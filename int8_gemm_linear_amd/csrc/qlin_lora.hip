@@ -213,8 +213,9 @@ __device__ inline int4 wave_plan(const Plan &p, int want, int &token)
     return tile_of(p, __builtin_amdgcn_readlane(sorted, at), begin, end - begin, (at - begin) / p.tile);
 }
 
-// Up to 8192: every workgroup of the shrink kernel finds its tile (4 us for 4001 tokens; the two launches above take 14).  A wave owns a contiguous part of the tokens, keeps their bins and counts them for itself;
-// then each wave walks the bins, 64 at a time.
+// Up to 8192: every workgroup of the shrink kernel finds its tile (4 us for 4001 tokens; the two launches above take 14).
+// A wave owns a contiguous part of the tokens, keeps their bins and counts them for itself; then each wave walks the bins,
+// 64 at a time.
 constexpr int kHold = 16;
 constexpr int kSelfTokens = 64 * 8 * kHold;
 
@@ -1096,7 +1097,7 @@ struct Sizes {
     int64_t Rp;                // ranks in whole blocks of 16: 1, 2, 4 or 8
     int tb, rb, groups;        // shrink: blocks of tokens and ranks of a workgroup, groups of ranks
     int wide;                  // expand: blocks of tokens
-    int max_tiles, max_wides;  // the latter 0 where every tile begins an expand tile (or tokens are few)
+    int max_tiles, max_wides;  // the latter 0 where every tile begins an expand tile
     int splits;                // shrink of the forward call: parts of K
 };
 
@@ -1104,23 +1105,23 @@ struct Sizes {
 // 15.8 us, four 13.6, eight 14.5; 164 workgroups (24 adapters of 64 ranks, N = 51200): one 49.4, three 52.9.
 constexpr int64_t kMaxSplits = 4;
 
-// Tokens an adapter has on average from which 64 share a load of the expand kernel's weights, not 16: 32 adapters of
-// 16 ranks, K = N = 5120, 16 tokens each, both kernels: 19.0 us with 64 at a time, 15.7 with 16; 32 each 23.0 and 22.5;
-// 16 adapters, 64 each 21.3 and 21.7.
-constexpr int64_t kManyTokens = 64;
+// Tokens an adapter has on average from which 64 share a load of the expand kernel's weights, not 16 (K = N = 5120, 16
+// ranks, both kernels): 32 adapters of 16 tokens 17.4 us with 64 at a time, 15.9 with 16; of 32 tokens 21.3 and 22.9; 16
+// adapters of 64 tokens 20.4 and 22.0.  Up to kWaveTokens tokens never (64 of an adapter 12.8 and 12.4).
+constexpr int64_t kManyTokens = 32;
 
 Sizes sizes(int64_t T, int64_t K, int64_t N, int64_t R, int64_t L)
 {
     Sizes z{T, K, N, R, L, 16, 1, 1, 1, 1, 0, 0, 1};
     while (z.Rp < R) z.Rp *= 2;
     const int64_t mean = T / std::min(L, std::max<int64_t>(T, 1));
-    z.wide = mean >= kManyTokens ? kWide / 16 : 1;
+    z.wide = mean >= kManyTokens && T > kWaveTokens ? kWide / 16 : 1;
     // shrink: more tokens a workgroup only where there are workgroups for all CUs (8192 tokens of 8 adapters of 64
     // ranks, K = N = 5120, both kernels: 16 at a time 136 us, 32 115; 65536 tokens of 8 adapters of 16 ranks, K = N =
     // 2048: 16 at a time 270 us, 32 248, 64 235)
     while (z.tb < z.wide && T >= 16 * 2 * z.tb * 240) z.tb *= 2;
     z.max_tiles = (int)std::max<int64_t>(1, T / (16 * z.tb) + std::min(L + 1, T));
-    if (z.wide > z.tb && T > kWaveTokens)
+    if (z.wide > z.tb)
         z.max_wides = (int)(T / (16 * z.wide) + std::min(L + 1, T));
     // and 32 ranks a workgroup likewise (64 ranks, K = N = 5120, both kernels: 8192 tokens of 8 adapters, 528 workgroups
     // then, 113 us, 16 at a time 136; 1024 of 32, 194, 34 and 38; 256 of 64, 162, 28 and 26)

@@ -72,7 +72,8 @@ SHAPES = [
     (64, 300, 700, 8, 70, None, 32), (63, 520, 1500, 24, 3, None, 64), (16, 65, 9000, 16, 12, None, 32),
     (20, 1000, 40, 40, 5, None, 32), (64, 200, 2600, 32, 60, None, 64),
     # many tokens an adapter: both sides of the rules on their number, K whole and in parts
-    (63, 600, 72, 16, 1, [0], 32), (64, 600, 72, 16, 1, [0], 64), (200, 1100, 130, 96, 2, None, 32),
+    (63, 600, 72, 16, 1, [0], 32), (64, 600, 72, 16, 1, [0], 64), (65, 600, 72, 16, 2, None, 64), (95, 600, 136, 40, 3, None, 32),
+    (200, 1100, 130, 96, 2, None, 32),
     (300, 2000, 264, 32, 1, [0, -1], 32), (511, 4100, 1001, 64, 4, "runs", 32), (1000, 2056, 72, 128, 7, None, 32),
     (520, 70, 200, 40, 8, None, 32), (8000, 40, 136, 16, 100, None, 32), (8192, 40, 72, 8, 128, "runs", 64),
     (12000, 24, 264, 8, 150, None, 32), (9000, 40, 130, 24, 70, "runs", 32), (7700, 264, 136, 128, 2, "runs", 32),
