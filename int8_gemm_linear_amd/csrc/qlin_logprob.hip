@@ -173,7 +173,7 @@ __device__ inline void load_chunk(v4i (&p)[kPieces], const T *x, int c, int end,
 }
 
 // A part of a row for each workgroup, a chunk's loads on their way while the one before is added up.  The logits'
-// bytes bound it, with the exponentials close behind (the vector units are busy for three quarters of the time): 2047
+// bytes bound it, with the exponentials close behind (the vector units are busy for five sixths of the time): 2047
 // rows of 131072 in bf16, 98 us, 5.5 TB/s, with one alternative 105 us.
 template <typename T, bool TOP>
 __global__ void __launch_bounds__(kThreads) k_logprobs(Args a)
