@@ -459,8 +459,9 @@ qlin_status qlin_moe_permute_backward(qlin_row_type rt, int64_t tokens, int64_t 
  * Shapes: 0 <= tokens <= 2^24, 0 < K <= 2^20, 0 <= N <= 2^20 (backward: 0 < N;
  * 0 tokens or N is a no-op, but backward then writes dA = dB = 0), rank 8..128
  * in steps of 8, 1 <= adapters <= 2047, adapters * max(rank, 64) * max(K, N) <
- * 2^33.  Y may be `base` itself (the same address and stride), dX likewise; no
- * other output may overlap another buffer.  workspace: the size below, 16-byte
+ * 2^33.  Y may be `base` itself (the same address and stride), dX likewise; else
+ * no output overlaps another buffer, nor X or dY where those are `base` (the
+ * same address: QLIN_ERR_BAD_ARGUMENT).  workspace: the size below, 16-byte
  * aligned, any contents, not used by two calls that may overlap in time.  The
  * calls are asynchronous on `stream` and allocate nothing.  Errors as for
  * qlin_scaled_mm. */

@@ -1369,6 +1369,8 @@ qlin_status qlin_lora_mm(int32_t id_bits, int64_t tokens, int64_t K, int64_t N, 
         return QLIN_OK;
     if (!X || !A || !B || !ids || !Y)
         return QLIN_ERR_NULL_POINTER;
+    if (Y == X)                                // (other workgroups still read it)
+        return QLIN_ERR_BAD_ARGUMENT;
     if (ldx < K || ldx > kMaxStride || ldy < N || ldy > kMaxStride || (base && (ldb < N || ldb > kMaxStride)))
         return QLIN_ERR_BAD_STRIDE;
     if (!aligned(X, 2) || !aligned(A, 2) || !aligned(B, 2) || !aligned(base, 2) || !aligned(Y, 2) ||
@@ -1414,6 +1416,8 @@ qlin_status qlin_lora_mm_backward(int32_t id_bits, int64_t tokens, int64_t K, in
         return QLIN_ERR_BAD_SHAPE;
     if (!A || !B || !dA || !dB || (tokens > 0 && (!dY || !X || !ids || !dX)))
         return QLIN_ERR_NULL_POINTER;
+    if (tokens > 0 && (dX == X || dX == dY))
+        return QLIN_ERR_BAD_ARGUMENT;
     if (tokens > 0 && (ldx < K || ldx > kMaxStride || lddy < N || lddy > kMaxStride || lddx < K || lddx > kMaxStride ||
                        (base && (ldb < K || ldb > kMaxStride))))
         return QLIN_ERR_BAD_STRIDE;

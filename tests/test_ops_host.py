@@ -45,6 +45,12 @@ def test_lora_refusals(call):
     assert call(ws=None) == WS and call(n=0) == WS
 
 
+def test_lora_in_place():
+    """Only `base` may be written over: X and dY are still read when the first outputs are stored."""
+    assert lora(y=X, N=64) == ARG and lora(y=X, base=X, N=64) == ARG
+    assert lora_backward(dx=X) == ARG and lora_backward(dx=G, N=64) == ARG
+
+
 def test_lora_forward_only():
     assert lora(y=None) == NULL and lora(y=Y + 1) == ALIGN and lora(ldy=47) == STRIDE
     assert lora(T=0, x=None, ids=None, y=None, ws=None, n=0) == OK and lora(N=0, b=None, y=None, ws=None, n=0) == OK
