@@ -118,15 +118,16 @@ def test_tokens_without_an_adapter_and_adapters_without_tokens():
     assert torch.equal(y, d["base"]) and torch.equal(dx, d["dbase"]) and not da.any() and not db.any()
 
 
-def test_in_place_and_strides():
-    d = make(70, 200, 150, 16, 3, 12)
+@pytest.mark.parametrize("T", [30, 70, 700])       # one launch, and both forms of the second product
+def test_in_place_and_strides(T):
+    d = make(T, 200, 150, 16, 3, 12)
     want, back = forward(d), backward(d)
     wide = {k: torch.full((v.shape[0], v.shape[1] + 13), 7.0, dtype=v.dtype, device=DEV) for k, v in d.items()
             if v.dim() == 2}
     for k, w in wide.items():
         w[:, :d[k].shape[1]] = d[k]
     s = {**d, **{k: w[:, :d[k].shape[1]] for k, w in wide.items()}}
-    out = torch.full((70, 200), 3.0, dtype=torch.bfloat16, device=DEV)
+    out = torch.full((T, 200), 3.0, dtype=torch.bfloat16, device=DEV)
     forward(s, out=out[:, 17:167])
     assert torch.equal(out[:, 17:167], want) and (out[:, :17] == 3).all() and (out[:, 167:] == 3).all()
     assert torch.equal(forward(s, out=s["base"]), want) and torch.equal(s["base"], want)
@@ -136,8 +137,9 @@ def test_in_place_and_strides():
     assert torch.equal(s["dbase"], back[0]) and (wide["dbase"][:, 200:] == 7).all()
 
 
-def test_order_of_tokens_and_calls_do_not_matter():
-    d = make(500, 384, 320, 16, 7, 13)
+@pytest.mark.parametrize("T", [40, 500])
+def test_order_of_tokens_and_calls_do_not_matter(T):
+    d = make(T, 384, 320, 16, 7, 13)
     y, back = forward(d), backward(d)
     for _ in range(3):
         assert torch.equal(forward(d), y)
@@ -250,8 +252,9 @@ def test_refusals():
         q.lora_mm(d["x"], d["a"], d["b"], d["ids"].cpu())
 
 
-def test_own_stream():
-    d = make(200, 256, 320, 32, 4, 19)
+@pytest.mark.parametrize("T", [20, 200])
+def test_own_stream(T):
+    d = make(T, 256, 320, 32, 4, 19)
     want, back = forward(d), backward(d)
     torch.cuda.synchronize()
     s = torch.cuda.Stream()
