@@ -448,9 +448,8 @@ qlin_status qlin_moe_permute_backward(qlin_row_type rt, int64_t tokens, int64_t 
  * of several ranks share a call with their adapters' missing ranks as zeros.
  *
  * The products of bf16 values are exact, sums fp32.  X A^T (and u), fp32, go
- * into the second product as their upper 16 bits and a bf16 rest, off by at
- * most 2^-16 of each; into dA and dB whole.  Y and dX are rounded once, dA and
- * dB are fp32.  No result depends on timing.
+ * into the second product and into dA and dB with all of their bits.  Y and dX
+ * are rounded once, dA and dB are fp32.  No result depends on timing.
  *
  * X [tokens][ldx], dY [tokens][lddy], base, Y, dX: bf16 bits, row-major; A
  * [adapters][rank][K] and B [adapters][N][rank] bf16 bits, contiguous, and so

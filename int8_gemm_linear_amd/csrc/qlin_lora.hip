@@ -10,10 +10,11 @@
 //   shrink   a long K against few ranks: v, or u from B transposed
 //   expand   few ranks against a long N: y, or dx from A transposed
 //   outer    sums over an adapter's tokens: dA and dB
-// v and u stay fp32 between them.  A matrix core takes them as bf16 pieces: the upper 16
-// bits (cut, so that nothing overflows), then the rest.  Two pieces hold 16 bits of the
-// mantissa, far below the final rounding to bf16 of y and dx; dA and dB, which are fp32,
-// take three, which is all of it.
+// v and u stay fp32 between them.  A matrix core takes them as three bf16 pieces, which
+// are all of their 24 bits: the upper 16 bits (cut, so that nothing overflows), of the
+// rest the upper 16 bits, and what is left.
+// Two pieces, 16 bits, would do for y and dx but where base and product cancel, and cost
+// less: 8192 tokens of 8 adapters of 64 ranks, K = N = 5120, 113 us for 117.
 #include <algorithm>
 
 #include "qlin_device.h"
@@ -72,12 +73,24 @@ __device__ inline void store8(uint16_t *p, v4i v, int n)
             p[i] = t[i];
 }
 
-// The upper 16 bits of v as a float, and what is left of it.  Where nothing is left, 2^-40 of v stands for it: with
-// zero, an infinity among the weights would come out as NaN.  All pieces of v have its sign.
+// The upper 16 bits of v as a float, and what is left of it.  Where nothing is left, 2^-40 of the number that is taken
+// apart stands for it: with zero, an infinity among the weights would come out as NaN (as it does with a number below
+// 2^-86, whose 2^-40 are no bf16 number any more).  All pieces of a number have its sign.
 __device__ inline float cut(float v) { return __uint_as_float(__float_as_uint(v) & 0xFFFF0000u); }
-__device__ inline float rest(float v, float c)
+__device__ inline float rest(float v, float c, float whole)
 {
-    return fabsf(c) < INFINITY && v != c ? v - c : c * 0x1p-40f;
+    return fabsf(c) < INFINITY && v != c ? v - c : whole * 0x1p-40f;
+}
+
+constexpr int kPieces = 3;
+
+// The pieces of v, each a bf16 number.
+__device__ inline void pieces_of(float (&p)[kPieces], float v)
+{
+    p[0] = cut(v);
+    const float r = rest(v, p[0], v);
+    p[1] = cut(r);
+    p[2] = rest(r, p[1], v);
 }
 
 __device__ inline int pack2(float lo, float hi)
@@ -302,8 +315,8 @@ constexpr int kStep = 64;
 
 struct ShrinkJob {
     const uint16_t *x, *w;
-    uint16_t *rows;            // [tokens][2][Rp]: two pieces, or NULL
-    uint16_t *pieces;          // [place / 8][3][Rp][8]: three pieces, or NULL
+    uint16_t *rows;            // [tokens][3][Rp]: the pieces, for expand, or NULL
+    uint16_t *pieces;          // [place / 8][3][Rp][8]: the pieces, for outer, or NULL
     int64_t ldx;
     int K;
 };
@@ -545,24 +558,23 @@ __global__ void __launch_bounds__(64 * kShrinkWaves) k_shrink(ShrinkArgs a)
                     a.part[((int64_t)split * a.plan.tokens + tile.y + at + c) * a.Rp + rank] = v[c];
             continue;
         }
-        uint16_t o[3][4];
+        uint16_t o[kPieces][4];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-            const float f = c < n ? v[c] * s : 0.0f, h = cut(f), m = rest(f, h), mh = cut(m);
-            o[0][c] = bf16_bits(h);
-            o[1][c] = bf16_bits(mh);
-            o[2][c] = bf16_bits(rest(m, mh));
-            if (job.rows && c < n) {
-                uint16_t *p = job.rows + (int64_t)(tile.y + at + c) * 2 * a.Rp + rank;
-                p[0] = o[0][c];
-                p[a.Rp] = bf16_bits(m);
+            float f[kPieces];
+            pieces_of(f, c < n ? v[c] * s : 0.0f);
+#pragma unroll
+            for (int h = 0; h < kPieces; ++h) {
+                o[h][c] = bf16_bits(f[h]);
+                if (job.rows && c < n)
+                    job.rows[((int64_t)(tile.y + at + c) * kPieces + h) * a.Rp + rank] = o[h][c];
             }
         }
         if (BACK && job.pieces && (at & ~7) < tile.z) {     // (zeros fill the last eight)
             const int64_t eight = piece_place(tile.y, tile.x) / 8 + at / 8;
 #pragma unroll
-            for (int h = 0; h < 3; ++h)
-                __builtin_memcpy(job.pieces + ((eight * 3 + h) * a.Rp + rank) * 8 + (at & 4), o[h], 8);
+            for (int h = 0; h < kPieces; ++h)
+                __builtin_memcpy(job.pieces + ((eight * kPieces + h) * a.Rp + rank) * 8 + (at & 4), o[h], 8);
         }
     }
 }
@@ -577,7 +589,7 @@ constexpr int kThreads = 256, kWaves = kThreads / 64;
 constexpr int kWide = 16 * kWaves;             // tokens of a workgroup of the second kernel
 
 struct ExpandArgs {
-    const uint16_t *rows;      // [tokens][2][Rp]: s v
+    const uint16_t *rows;      // [tokens][3][Rp]: s v
     const float *part, *scale; // instead of rows: [splits][tokens][Rp], the parts of v, and s (or NULL)
     int tokens, splits;
     const int32_t *order;
@@ -588,46 +600,50 @@ struct ExpandArgs {
     int N, R, Rp, chunks;
 };
 
-// The pieces of s v as operands: chunk 4 g + q of 8 ranks; PACK (16 ranks at most): both pieces in one product.
-template <int G, bool PACK>
-__device__ inline void load_factors(v4i (&hi)[G], v4i (&lo)[G], const ExpandArgs &a, int place)
+// The pieces of s v as operands: chunk 4 g + q of 8 ranks.
+template <int G>
+__device__ inline void load_factors(v4i (&f)[kPieces][G], const ExpandArgs &a, int place)
 {
     const int q = (threadIdx.x & 63) >> 4, ranks = a.R / 8;
-    const uint16_t *v = a.rows + (int64_t)place * 2 * a.Rp;
+    const uint16_t *v = a.rows + (int64_t)place * kPieces * a.Rp;
 #pragma unroll
     for (int g = 0; g < G; ++g) {
-        const int c = PACK ? q % ranks : 4 * g + q, piece = PACK ? q / ranks : 0;
-        hi[g] = lo[g] = v4i{0, 0, 0, 0};
-        if (c < ranks && piece < 2)
-            hi[g] = load8(v + piece * a.Rp + 8 * c);
-        if (!PACK && c < ranks)
-            lo[g] = load8(v + a.Rp + 8 * c);
+        const int c = 4 * g + q;
+#pragma unroll
+        for (int h = 0; h < kPieces; ++h) {
+            f[h][g] = v4i{0, 0, 0, 0};
+            if (c < ranks)
+                f[h][g] = load8(v + h * a.Rp + 8 * c);
+        }
     }
 }
 
-// The pieces of s times eight sums (with `only`: the lower ones as both).
-__device__ inline void cut_factors(v4i &hi, v4i &lo, const v4f (&sum)[2], float s, bool only)
+// The pieces of s times eight sums.
+template <int G>
+__device__ inline void cut_factors(v4i (&f)[kPieces][G], int g, const v4f (&sum)[2], float s)
 {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        const float v0 = sum[e / 2][2 * e % 4] * s, v1 = sum[e / 2][2 * e % 4 + 1] * s, h0 = cut(v0), h1 = cut(v1);
-        const int high = pack2(h0, h1), low = pack2(rest(v0, h0), rest(v1, h1));
-        hi[e] = only ? low : high;
-        lo[e] = low;
+        float p0[kPieces], p1[kPieces];
+        pieces_of(p0, sum[e / 2][2 * e % 4] * s);
+        pieces_of(p1, sum[e / 2][2 * e % 4 + 1] * s);
+#pragma unroll
+        for (int h = 0; h < kPieces; ++h) f[h][g][e] = pack2(p0[h], p1[h]);
     }
 }
 
 // The same from the parts, four of them on their way at a time.
-template <int G, bool PACK>
-__device__ inline void add_factors(v4i (&hi)[G], v4i (&lo)[G], const ExpandArgs &a, int place, float s)
+template <int G>
+__device__ inline void add_factors(v4i (&f)[kPieces][G], const ExpandArgs &a, int place, float s)
 {
     const int q = (threadIdx.x & 63) >> 4, ranks = a.R / 8;
     const int64_t apart = (int64_t)a.tokens * a.Rp;
 #pragma unroll
     for (int g = 0; g < G; ++g) {
-        const int c = PACK ? q % ranks : 4 * g + q, piece = PACK ? q / ranks : 0;
-        hi[g] = lo[g] = v4i{0, 0, 0, 0};
-        if (c >= ranks || piece > 1)
+        const int c = 4 * g + q;
+#pragma unroll
+        for (int h = 0; h < kPieces; ++h) f[h][g] = v4i{0, 0, 0, 0};
+        if (c >= ranks)
             continue;
         const float *p = a.part + (int64_t)place * a.Rp + 8 * c;
         v4f sum[2] = {};
@@ -645,13 +661,13 @@ __device__ inline void add_factors(v4i (&hi)[G], v4i (&lo)[G], const ExpandArgs 
                 sum[1] += v[j][1];
             }
         }
-        cut_factors(hi[g], lo[g], sum, s, PACK && piece == 1);
+        cut_factors(f, g, sum, s);
     }
 }
 
 // 64 n of a wave as four products of 16 n by 16 tokens, dealt to them so that a lane ends with twice eight n
 // in a row of its token, and four lanes with 64 bytes of it.
-template <int G, bool PACK, bool TR>
+template <int G, bool TR>
 struct Few {
     v4i o[2], f[4][G];         // this lane's outputs, n0 + 8 q .. + 7 and 32 behind; operands of the products
 
@@ -675,12 +691,12 @@ struct Few {
             const int n = n0 + 32 * ((i & 3) >> 1) + 8 * (i >> 2) + 4 * (i & 1), there = a.N - n;
 #pragma unroll
             for (int g = 0; g < G; ++g) {
-                const int c = PACK ? q % ranks : 4 * g + q;
+                const int c = 4 * g + q;
                 int2 r[8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     r[j] = make_int2(0, 0);
-                    if (c < ranks && (!PACK || q < 2 * ranks)) {
+                    if (c < ranks) {
                         const uint16_t *p = w + (int64_t)(8 * c + j) * a.N + n;
                         if (there >= 4) {
                             __builtin_memcpy(&r[j], p, 8);
@@ -707,26 +723,24 @@ struct Few {
                 const int n = min(n0 + 32 * (j >> 1) + 8 * (i >> 2) + 4 * (j & 1) + (i & 3), a.N - 1);
 #pragma unroll
                 for (int g = 0; g < G; ++g) {
-                    const int c = PACK ? q % ranks : 4 * g + q;
+                    const int c = 4 * g + q;
                     f[j][g] = v4i{0, 0, 0, 0};
-                    if (c < ranks && (!PACK || q < 2 * ranks))
+                    if (c < ranks)
                         f[j][g] = load8(w + (int64_t)n * a.R + 8 * c);
                 }
             }
         }
     }
 
-    __device__ void add(const v4i (&hi)[G], const v4i (&lo)[G])
+    __device__ void add(const v4i (&v)[kPieces][G])
     {
         v4f acc[4] = {};
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
-            for (int g = 0; g < G; ++g) {
-                acc[j] = mma(f[j][g], hi[g], acc[j]);
-                if (!PACK)
-                    acc[j] = mma(f[j][g], lo[g], acc[j]);
-            }
+            for (int g = 0; g < G; ++g)
+#pragma unroll
+                for (int h = 0; h < kPieces; ++h) acc[j] = mma(f[j][g], v[h][g], acc[j]);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             const float d0 = TR ? acc[(2 * e) % 4][e / 2] : acc[e / 2][(2 * e) % 4];
@@ -748,7 +762,7 @@ struct Few {
 };
 
 // Weights' bytes bound it: 128 tokens of 24 adapters of 64 ranks on N = 51200, 183 MB, 37 us, 5.0 TB/s.
-template <int G, bool PACK, bool TR>
+template <int G, bool TR>
 __global__ void __launch_bounds__(kThreads) k_expand_few(ExpandArgs a)
 {
     const int4 tile = a.tiles[blockIdx.x / a.chunks];
@@ -759,20 +773,20 @@ __global__ void __launch_bounds__(kThreads) k_expand_few(ExpandArgs a)
     const bool live = tile.x >= 0;
     const int place = tile.y + min(i, tile.w - 1);
     const int64_t token = i < tile.w ? a.order[place] : -1;
-    v4i hi[G], lo[G];
+    v4i v[kPieces][G];
     const uint16_t *w = live ? a.w + (int64_t)tile.x * a.N * a.R : nullptr;
     if (live) {
         if (!TR && a.part)
-            add_factors<G, PACK>(hi, lo, a, place, a.scale ? a.scale[tile.x] : 1.0f);
+            add_factors(v, a, place, a.scale ? a.scale[tile.x] : 1.0f);
         else
-            load_factors<G, PACK>(hi, lo, a, place);
+            load_factors(v, a, place);
     }
     const int blocks = (a.N + 63) / 64;
     for (int b = chunk * kWaves + wave; b < blocks; b += a.chunks * kWaves) {
-        Few<G, PACK, TR> n;
+        Few<G, TR> n;
         n.load(a, w, token, 64 * b);
         if (live)
-            n.add(hi, lo);
+            n.add(v);
         n.store(a, token, 64 * b);
     }
 }
@@ -783,7 +797,6 @@ __global__ void __launch_bounds__(kThreads) k_expand_few(ExpandArgs a)
 template <int RB>
 __global__ void __launch_bounds__(64 * kShrinkWaves) k_both(ShrinkArgs s, ExpandArgs a)
 {
-    constexpr bool PACK = RB == 1;
     constexpr int kRow = 16 * RB + 4;          // a token's sums (a row's start falls on other banks than the last's)
     extern __shared__ v4i shared[];            // [waves][shrink_share]
     __shared__ __align__(16) float sums[16 * kRow];
@@ -797,10 +810,10 @@ __global__ void __launch_bounds__(64 * kShrinkWaves) k_both(ShrinkArgs s, Expand
     const int64_t token = i < tile.z ? there : -1;
     const uint16_t *w = live ? a.w + (int64_t)tile.x * a.N * a.R : nullptr;
     const int n0 = 64 * (blockIdx.x % a.chunks * kShrinkWaves + wave);
-    Few<1, PACK, false> n;
+    Few<1, false> n;
     if (n0 < a.N)
         n.load(a, w, token, n0);               // (on its way meanwhile)
-    v4i hi[1], lo[1];
+    v4i v[kPieces][1] = {};
     if (live) {
         const ShrinkJob &job = s.job[0];
         const uint16_t *px[1][2];
@@ -815,25 +828,23 @@ __global__ void __launch_bounds__(64 * kShrinkWaves) k_both(ShrinkArgs s, Expand
         for (int r = 0; r < RB; ++r) parts[(wave * RB + r) * 64 + lane] = acc[0][r];
         __syncthreads();
         if (threadIdx.x < 64 * RB) {
-            v4f v = parts[threadIdx.x];
+            v4f t = parts[threadIdx.x];
 #pragma unroll
-            for (int k = 1; k < kShrinkWaves; ++k) v += parts[k * RB * 64 + threadIdx.x];
+            for (int k = 1; k < kShrinkWaves; ++k) t += parts[k * RB * 64 + threadIdx.x];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) sums[(4 * q + c) * kRow + 16 * wave + i] = v[c];
+            for (int c = 0; c < 4; ++c) sums[(4 * q + c) * kRow + 16 * wave + i] = t[c];
         }
         __syncthreads();
-        const int ranks = a.R / 8, c = PACK ? q % ranks : q, piece = PACK ? q / ranks : 0;
-        hi[0] = lo[0] = v4i{0, 0, 0, 0};
-        if (c < ranks && piece < 2) {
-            const v4f *v = reinterpret_cast<const v4f *>(sums + i * kRow + 8 * c);
-            const v4f sum[2] = {v[0], v[1]};
-            cut_factors(hi[0], lo[0], sum, a.scale ? a.scale[tile.x] : 1.0f, PACK && piece == 1);
+        if (q < a.R / 8) {
+            const v4f *p = reinterpret_cast<const v4f *>(sums + i * kRow + 8 * q);
+            const v4f sum[2] = {p[0], p[1]};
+            cut_factors(v, 0, sum, a.scale ? a.scale[tile.x] : 1.0f);
         }
     }
     if (n0 >= a.N)
         return;
     if (live)
-        n.add(hi, lo);
+        n.add(v);
     n.store(a, token, n0);
 }
 
@@ -841,7 +852,7 @@ __global__ void __launch_bounds__(64 * kShrinkWaves) k_both(ShrinkArgs s, Expand
 // so that a lane ends with eight n in a row of four tokens, and sixteen lanes with 256 bytes of one (64 bytes of
 // each token, as above, took 32 us where this took 25: 4001 tokens on N = 5120, 32 ranks; 22 with the plan's list of
 // tiles, base and out at 3.8 TB/s).
-template <int G, bool PACK, bool TR>
+template <int G, bool TR>
 __global__ void __launch_bounds__(kThreads) k_expand_many(ExpandArgs a)
 {
     extern __shared__ v4i shared[];            // 128 n's weights
@@ -858,14 +869,14 @@ __global__ void __launch_bounds__(kThreads) k_expand_many(ExpandArgs a)
         const int at = 16 * wave + 4 * q + c;
         token[c] = at < tile.w ? a.order[tile.y + at] : -1;
     }
-    v4i hi[G], lo[G];
+    v4i v[kPieces][G];
     const uint16_t *w = a.w + (int64_t)(live ? tile.x : 0) * a.N * a.R;
     if (live) {
         const int place = tile.y + min(16 * wave + i, tile.w - 1);
         if (!TR && a.part)
-            add_factors<G, PACK>(hi, lo, a, place, a.scale ? a.scale[tile.x] : 1.0f);
+            add_factors(v, a, place, a.scale ? a.scale[tile.x] : 1.0f);
         else
-            load_factors<G, PACK>(hi, lo, a, place);
+            load_factors(v, a, place);
     }
     const int blocks = (a.N + 127) / 128;
     for (int b = chunk; b < blocks; b += a.chunks) {
@@ -896,8 +907,8 @@ __global__ void __launch_bounds__(kThreads) k_expand_many(ExpandArgs a)
             v4f acc[8] = {};
 #pragma unroll
             for (int g = 0; g < G; ++g) {
-                const int c = PACK ? q % ranks : 4 * g + q;
-                const bool there = c < ranks && (!PACK || q < 2 * ranks);
+                const int c = 4 * g + q;
+                const bool there = c < ranks;
                 v4i r[8], f[8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
@@ -915,11 +926,9 @@ __global__ void __launch_bounds__(kThreads) k_expand_many(ExpandArgs a)
                                                                  m % 2 ? 0x07060302u : 0x05040100u);
                 }
 #pragma unroll
-                for (int m = 0; m < 8; ++m) {
-                    acc[m] = mma(hi[g], f[m], acc[m]);
-                    if (!PACK)
-                        acc[m] = mma(lo[g], f[m], acc[m]);
-                }
+                for (int m = 0; m < 8; ++m)
+#pragma unroll
+                    for (int h = 0; h < kPieces; ++h) acc[m] = mma(v[h][g], f[m], acc[m]);
             }
 #pragma unroll
             for (int c = 0; c < 4; ++c)
@@ -1185,14 +1194,14 @@ Space space(const Sizes &z, void *ws, bool back)
     f.wides = z.max_wides ? l.take<int4>(z.max_wides) : nullptr;
     f.counts = l.take<int32_t>(z.T > kSelfTokens ? (int64_t)sort_parts(z.T) * plan_digits(z.L) : 0);
     if (back || z.splits == 1)
-        f.rows = l.take<uint16_t>(z.T * 2 * z.Rp);
+        f.rows = l.take<uint16_t>(z.T * kPieces * z.Rp);
     else
         f.part = l.take<float>(z.splits * z.T * z.Rp);
     if (back) {
         f.offsets = l.take<int32_t>(z.L + 1);
         const int64_t places = piece_place(z.T, (int)z.L);
-        f.fv = l.take<uint16_t>(3 * z.Rp * places);
-        f.fu = l.take<uint16_t>(3 * z.Rp * places);
+        f.fv = l.take<uint16_t>(kPieces * z.Rp * places);
+        f.fu = l.take<uint16_t>(kPieces * z.Rp * places);
         const int64_t sa = outer_splits(z, z.K), sb = outer_splits(z, z.N);
         f.outer_a = l.take<float>(sa > 1 ? sa * z.L * z.R * z.K : 0);
         f.outer_b = l.take<float>(sb > 1 ? sb * z.L * z.R * z.N : 0);
@@ -1244,13 +1253,13 @@ hipError_t make_plan(const Sizes &z, const Space &f, const void *ids, int32_t id
     return hipGetLastError();
 }
 
-template <int G, bool PACK, bool TR>
+template <int G, bool TR>
 void expand_kernel(const Sizes &z, const ExpandArgs &a, dim3 grid, hipStream_t s)
 {
     if (z.wide > 1)
-        hipLaunchKernelGGL((k_expand_many<G, PACK, TR>), grid, dim3(kThreads), 128 * 2 * (size_t)z.R, s, a);
+        hipLaunchKernelGGL((k_expand_many<G, TR>), grid, dim3(kThreads), 128 * 2 * (size_t)z.R, s, a);
     else
-        hipLaunchKernelGGL((k_expand_few<G, PACK, TR>), grid, dim3(kThreads), 0, s, a);
+        hipLaunchKernelGGL((k_expand_few<G, TR>), grid, dim3(kThreads), 0, s, a);
 }
 
 template <bool TR>
@@ -1266,14 +1275,12 @@ hipError_t launch_expand(const Sizes &z, const Space &f, const float *scale, con
     const int chunks = (int)std::max<int64_t>(1, std::min<int64_t>(want, (((int64_t)1 << 24) - 1) / tiles));
     const ExpandArgs a{f.rows, f.part, scale, (int)z.T, z.splits, f.order, f.wides ? f.wides : f.tiles, w, base, out, ldb, ldo, (int)N, (int)z.R, (int)z.Rp, chunks};
     const dim3 grid((unsigned)(tiles * chunks));
-    if (z.R <= 16)
-        expand_kernel<1, true, TR>(z, a, grid, s);
-    else if (z.R <= 32)
-        expand_kernel<1, false, TR>(z, a, grid, s);
+    if (z.R <= 32)
+        expand_kernel<1, TR>(z, a, grid, s);
     else if (z.R <= 64)
-        expand_kernel<2, false, TR>(z, a, grid, s);
+        expand_kernel<2, TR>(z, a, grid, s);
     else
-        expand_kernel<4, false, TR>(z, a, grid, s);
+        expand_kernel<4, TR>(z, a, grid, s);
     return hipGetLastError();
 }
 
