@@ -212,6 +212,8 @@ __global__ void __launch_bounds__(kThreads) k_logprobs(Args a)
             load_chunk(next, x, c + kStep, end, tid);
         if (most > s.m)
             rescale(s, most);
+        // (a turn's terms join the others as one sum: each by itself, next to a term of 1, those below 2^-24 were lost)
+        float turn_s = 0.0f, turn_w = 0.0f;
 #pragma unroll
         for (int u = 0; u < kPieces; ++u) {
             if (u >= pieces)
@@ -219,10 +221,12 @@ __global__ void __launch_bounds__(kThreads) k_logprobs(Args a)
 #pragma unroll
             for (int i = 0; i < E; ++i) {
                 const float d = v[u][i] - s.m, e = exp_of(d);
-                s.s += e;
-                s.w = fmaf(e, fmaxf(d, kLowest), s.w);
+                turn_s += e;
+                turn_w = fmaf(e, fmaxf(d, kLowest), turn_w);
             }
         }
+        s.s += turn_s;
+        s.w += turn_w;
         if (TOP) {
             // Of the first chunk, the lanes' maxima give the bound; later, a value also has to be greater than the
             // last of the wave's list, whose index is lower.
