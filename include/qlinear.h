@@ -495,8 +495,10 @@ qlin_status qlin_lora_mm_backward(int32_t id_bits, int64_t tokens, int64_t K, in
  * The gradient, from the forward call's lse and entropy:
  *   dX[r,v] = g_r ([v = target[r]] - p_v) - h_r p_v (ln p_v + entropy[r]),
  * g = dlogprob (0 for a target outside 0..V-1), h = dentropy (NULL: 0, and
- * entropy is not read).  Rows with g = h = 0 and rows without a distribution
- * get zeros whatever their logits hold.
+ * entropy is not read).  p_v = exp(x[r,v] - lse[r]) is as exact as lse, which is
+ * fp32: rows far from zero get p off by |lse| 2^-24 relatively (at logits near
+ * 3e4 by 2^-9), rows that were shifted towards zero first do not.  Rows with
+ * g = h = 0 and rows without a distribution get zeros whatever their logits hold.
  *
  * logits [rows][ld] of type rt; target [rows] int32, or int64 with id_bits =
  * 64; outputs fp32 (top_id int32) and contiguous, dlogits [rows][ldo] of type

@@ -9,8 +9,10 @@
 // when its maximum rises: from m to n, W becomes (W + S (m - n)) e^(m - n).
 //
 // x - m is taken before the product with log2 e, so that rows far from zero lose
-// nothing, and below -200 it counts as -200 where it is multiplied with e^(x - m),
-// which is 0 there: banned tokens (-inf, or a type's lowest value) add 0.
+// nothing in p and H (lse itself is rounded to fp32), and below -200 it counts as
+// -200 where it is multiplied with e^(x - m), which is 0 there: banned tokens (-inf,
+// or a type's lowest value) add 0.  The gradient has only the rounded lse to take p
+// from, so its p are off by |lse| 2^-24 relatively.
 #include <algorithm>
 #include <float.h>
 

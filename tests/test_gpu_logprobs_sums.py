@@ -1,4 +1,4 @@
-"""How the log probabilities add up long rows, on the GPU against the definition."""
+"""How exact the log probabilities are, on the GPU against the definition: sums of long rows, rows far from zero."""
 import math
 
 import numpy as np
@@ -6,7 +6,8 @@ import pytest
 import torch
 
 import int8_gemm_linear_amd as q
-from tests.reference64 import close, f64
+from tests import reference_ops as ref
+from tests.reference64 import HALF, close, f64
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
@@ -38,3 +39,29 @@ def test_many_small_terms_beside_a_large_one(T, V, dtype):
     D = -W / S
     more = D * (2 * 2.0 ** -24 * n + (2 * abs(small) + 5) * 2.0 ** -23 + 2 * 2.0 ** -24) + 2.0 ** -24 * (want + D)
     close(f64(entropy), (want + D) * one, (tol + more) * one, "entropy")
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("shift", [0.0, -800.0, 1e4, -3e4])
+def test_gradient_of_rows_far_from_zero(shift, dtype):
+    """Against lse and entropy of 64 bits.  The kernels' lse is off by its own bound and half a step, |lse| 2^-24; p by
+    as much relatively, and ln p + H by that and the entropy's error beside it."""
+    T, V = 20, 3001
+    g = torch.Generator().manual_seed(int(abs(shift)) + 1)
+    x = (2.5 * torch.randn((T, V), generator=g) + shift).to(dtype)
+    target = torch.randint(-1, V, (T,), generator=g)
+    dl, dh = torch.randn(T, generator=g), 0.3 * torch.randn(T, generator=g)
+    dev = x.to(DEV), target.to(DEV)
+    _, entropy, lse, _, _ = q.token_logprobs(*dev)
+    got = q.token_logprobs_backward(dl.to(DEV), *dev, lse, entropy=entropy, dentropy=dh.to(DEV))
+    _, entropy, lse, _, top = ref.logprobs(f64(x), target.numpy(), 1)
+    want, tol = ref.logprobs_backward(f64(dl), f64(x), target.numpy(), lse, entropy, f64(dh))
+    _, de, dlse, _ = (b[:, None] if b.ndim == 1 else b for b in ref.logprobs_bounds(f64(x), target.numpy(), top))
+    dlse = dlse + 2.0 ** -24 * np.abs(lse[:, None])
+    z = f64(x) - lse[:, None]
+    p = np.exp(z)
+    h = np.abs(f64(dh))[:, None]
+    there = ((target.numpy() >= 0) * np.abs(f64(dl)))[:, None]
+    # p (g + h (z + H)): p's error times the bracket, and p times the bracket's (1.01: products of errors)
+    tol = tol + 1.01 * p * (dlse * (there + h * np.abs(z + entropy[:, None])) + h * (dlse + de))
+    close(f64(got), want, ref.rounded(want, tol, HALF[dtype]), f"{shift}")
