@@ -39,8 +39,9 @@ COPY_BYTES = 256 << 20          # the calibration copy of bench.py --copy-calib
 COPY_TAG = "bitwise_not"        # its kernel is torch's elementwise bitwise_not
 
 
-# sources that no counted workload runs: the 4-bit products and the token routing
-OTHER_SOURCES = ("qlin_w4", "qlin_moe")
+# sources that no counted workload runs: the 4-bit products, the token routing, the adapters, the log
+# probabilities, the embedding, and the headers that only these include
+OTHER_SOURCES = ("qlin_w4", "qlin_moe", "qlin_lora", "qlin_logprob", "qlin_embed", "qlin_sort", "qlin_elem")
 
 
 def fingerprint(table_path: str | None = None) -> str:

@@ -84,3 +84,27 @@ def test_producer_bytes_count_every_operand_once():
         "quant_per_token", "quant_per_group128", "rms_norm_dynamic_per_token_quant",
         "rms_norm_per_block_quant", "silu_and_mul_dynamic_per_token_quant",
         "silu_and_mul_per_block_quant"}
+
+
+def test_committed_traffic_records_are_of_this_tree():
+    # a new source that no counted workload runs leaves the records in use;
+    # a change of the counted kernels or of the table means counting anew
+    for workload in ("all_32b_decode", "int8_1p7b_decode"):
+        traffic, src = bench.load_traffic(workload, None)
+        assert traffic is not None and traffic > 0, (workload, src)
+
+
+def test_fingerprint_is_over_the_sources_the_counted_kernels_include():
+    # nothing that the 8-bit kernels, their dispatcher or the producers include is left out
+    import re
+    from int8_gemm_linear_amd import build, profsum
+    csrc = build.CSRC
+    seen, todo = set(), [s for s in build.SOURCES if not s.startswith(profsum.OTHER_SOURCES)]
+    while todo:
+        f = todo.pop()
+        if f in seen or not os.path.exists(os.path.join(csrc, f)):
+            continue
+        seen.add(f)
+        with open(os.path.join(csrc, f)) as h:
+            todo += re.findall(r'#include "([^"]+)"', h.read())
+    assert seen == {f for f in os.listdir(csrc) if not f.startswith(profsum.OTHER_SOURCES)}
