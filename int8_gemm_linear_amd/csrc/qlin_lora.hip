@@ -213,10 +213,12 @@ __device__ inline int4 wave_plan(const Plan &p, int want, int &token)
     const uint64_t heads = __ballot(there && (lane - first) % p.tile == 0);
     const uint64_t mine = __ballot(((heads >> lane) & 1) && __popcll(heads & (low >> 1)) == want);
     if (want == 0 && p.offsets)
-        for (int b = threadIdx.x; b <= p.adapters; b += blockDim.x) {
+        for (int b0 = 0; b0 <= p.adapters; b0 += blockDim.x) {         // (by all lanes: other lanes' bins are read)
+            const int b = b0 + threadIdx.x;
             int n = 0;
             for (int j = 0; j < p.tokens; ++j) n += __builtin_amdgcn_readlane(bin, j) < b ? 1 : 0;
-            p.offsets[b] = n;
+            if (b <= p.adapters)
+                p.offsets[b] = n;
         }
     if (!mine)
         return make_int4(-1, 0, 0, 0);
