@@ -378,6 +378,15 @@ __device__ inline v4i row_part(const v4i *lds, int b, int half)
     return lds[128 * b + 8 * i + ((4 * half + (lane >> 4)) ^ (i & 7))];
 }
 
+// Between a wave's stores into LDS and its lanes' loads of what others stored, and back: the LDS takes a wave's accesses
+// in order, so that this only keeps the compiler from changing it.
+__device__ inline void wave_sync()
+{
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // Adds the steps first, first + kShrinkWaves, .. before `end` of 16 TB tokens and the ranks from r0 of weights [R][K].
 template <int TB, int RB>
 __device__ inline void add_steps(v4f (&acc)[TB][RB], const uint16_t *const (&px)[TB][2], const uint16_t *rows, int R, int r0,
@@ -405,8 +414,10 @@ __device__ inline void add_steps(v4f (&acc)[TB][RB], const uint16_t *const (&px)
         for (int u = 0; u < U; ++u) {
             if (u > 0 && s + waves * u >= end)
                 break;
+            wave_sync();                       // (the step before has been read)
             store_rows(mine, x[u]);
             store_rows(weights, w[u]);
+            wave_sync();
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 v4i f[RB];
@@ -509,11 +520,13 @@ __global__ void __launch_bounds__(64 * kShrinkWaves) k_shrink(ShrinkArgs a)
         if (wave < steps)
             load(wave);
         for (int s = wave; s < steps; s += waves) {
+            wave_sync();                       // (the step before has been read)
             store_rows(mine, x);
 #pragma unroll
             for (int h = 0; h < 2 * RB; ++h)
                 if (row[h] < kStep)
                     *reinterpret_cast<v4i *>(wl + row[h] * (16 * RB) + rank[h]) = b[h];
+            wave_sync();
             if (s + waves < steps)
                 load(s + waves);
 #pragma unroll
