@@ -459,11 +459,12 @@ qlin_status qlin_moe_permute_backward(qlin_row_type rt, int64_t tokens, int64_t 
  * 0 tokens or N is a no-op, but backward then writes dA = dB = 0), rank 8..128
  * in steps of 8, 1 <= adapters <= 2047, adapters * max(rank, 64) * max(K, N) <
  * 2^33.  Y may be `base` itself (the same address and stride), dX likewise; else
- * no output overlaps another buffer, nor X or dY where those are `base` (the
- * same address: QLIN_ERR_BAD_ARGUMENT).  workspace: the size below, 16-byte
- * aligned, any contents, not used by two calls that may overlap in time.  The
- * calls are asynchronous on `stream` and allocate nothing.  Errors as for
- * qlin_scaled_mm. */
+ * no output and no workspace overlaps another buffer, nor X or dY where those
+ * are `base`: QLIN_ERR_BAD_ARGUMENT, but for rows of two different strides, both
+ * with gaps, which are not looked through (columns of one buffer, side by side,
+ * do not overlap).  workspace: the size below, 16-byte aligned, any contents,
+ * not used by two calls that may overlap in time.  The calls are asynchronous on
+ * `stream` and allocate nothing.  Errors as for qlin_scaled_mm. */
 size_t qlin_lora_workspace_size(int64_t tokens, int64_t K, int64_t N, int64_t rank, int64_t adapters);
 qlin_status qlin_lora_mm(int32_t id_bits, int64_t tokens, int64_t K, int64_t N, int64_t rank,
                          int64_t adapters, const uint16_t *X, int64_t ldx, const uint16_t *A,
@@ -503,7 +504,7 @@ qlin_status qlin_lora_mm_backward(int32_t id_bits, int64_t tokens, int64_t K, in
  * logits [rows][ld] of type rt; target [rows] int32, or int64 with id_bits =
  * 64; outputs fp32 (top_id int32) and contiguous, dlogits [rows][ldo] of type
  * rt, rounded once; it may be the logits themselves (the same address and
- * stride), else nothing overlaps.  All sums are fp32, in an order that does not
+ * stride), else no output overlaps another buffer (refused as above).  All sums are fp32, in an order that does not
  * depend on timing.
  *
  * Shapes: 0 <= rows <= 2^23 (0 is a no-op), 0 < V <= 2^28, 0 <= top <= 64 and
@@ -540,7 +541,8 @@ qlin_status qlin_token_logprobs_backward(qlin_row_type rt, int32_t id_bits, int6
  *
  * ids [tokens] int32, or int64 with id_bits = 64.  table [vocab][ldt], Out
  * [tokens][ldo], dOut [tokens][ldd], dTable [vocab][ldt]: strides in elements,
- * every buffer aligned to its element.  No output overlaps another buffer.
+ * every buffer aligned to its element.  No output overlaps another buffer
+ * (refused as above).
  *
  * Shapes: 0 <= tokens < 2^30, 0 < vocab < 2^31, 0 < width <= 2^20; of the
  * gradient tokens < 2^28, vocab < 2^22 and

@@ -13,6 +13,7 @@
 
 #include "qlin_dpp.h"
 #include "qlin_elem.h"
+#include "qlin_overlap.h"
 #include "qlin_sort.h"
 #include "qlinear.h"
 
@@ -523,6 +524,10 @@ qlin_status qlin_embedding(qlin_table_type tt, qlin_row_type ot, int32_t id_bits
         return QLIN_ERR_BAD_STRIDE;
     if (!aligned(ids, id_bits / 8) || !aligned(table, ts) || !aligned(Out, os) || !aligned(row_scale, 4))
         return QLIN_ERR_MISALIGNED;
+    if (overlaps({Region{Out, tokens, width * os, ldo * os}},
+                 {Region{table, vocab, width * ts, ldt * ts}, flat(ids, tokens * (id_bits / 8)),
+                  flat(row_scale, 4 * vocab * scale_cols)}))
+        return QLIN_ERR_BAD_ARGUMENT;
     LookArgs a{};
     a.ids = ids;
     a.table = static_cast<const uint8_t *>(table);
@@ -580,6 +585,9 @@ qlin_status qlin_embedding_backward(qlin_row_type rt, qlin_row_type ot, int32_t 
     const size_t need = qlin_embedding_backward_workspace_size(tokens, vocab, width);
     if (need && (!workspace || workspace_bytes < need))
         return QLIN_ERR_WORKSPACE;
+    if (overlaps({Region{dTable, vocab, width * os, ldt * os}, flat(workspace, need)},
+                 {Region{dOut, tokens, width * es, ldd * es}, flat(ids, tokens * (id_bits / 8))}))
+        return QLIN_ERR_BAD_ARGUMENT;
     hipStream_t s = static_cast<hipStream_t>(stream);
     FillArgs f{};
     if (!accumulate) {

@@ -18,6 +18,7 @@
 
 #include "qlin_dpp.h"
 #include "qlin_elem.h"
+#include "qlin_overlap.h"
 #include "qlinear.h"
 
 namespace qlin {
@@ -531,6 +532,10 @@ qlin_status qlin_token_logprobs(qlin_row_type rt, int32_t id_bits, int64_t rows,
     if (need && (!workspace || workspace_bytes < need))
         return QLIN_ERR_WORKSPACE;
     const int es = elem_size(rt);
+    if (overlaps({flat(logprob, 4 * rows), flat(entropy, 4 * rows), flat(lse, 4 * rows), flat(top_logprob, 4 * rows * top),
+                  flat(top_id, 4 * rows * top), flat(workspace, need)},
+                 {Region{logits, rows, V * es, ld * es}, flat(target, rows * (id_bits / 8))}))
+        return QLIN_ERR_BAD_ARGUMENT;
     Args a{};
     a.x = static_cast<const uint8_t *>(logits);
     a.ld = ld * es;
@@ -569,6 +574,10 @@ qlin_status qlin_token_logprobs_backward(qlin_row_type rt, int32_t id_bits, int6
     if (!aligned(dlogits, es) || !aligned(dlogprob, 4) || !aligned(dentropy, 4) || !aligned(lse, 4) ||
         !aligned(entropy, 4))
         return QLIN_ERR_MISALIGNED;
+    const Region x{logits, rows, V * es, ld * es}, dx{dlogits, rows, V * es, ldo * es};
+    if (overlaps({dx}, {same(dx, x) ? Region{} : x, flat(target, rows * (id_bits / 8)), flat(dlogprob, 4 * rows),
+                        flat(dentropy, 4 * rows), flat(lse, 4 * rows), flat(dentropy ? entropy : nullptr, 4 * rows)}))
+        return QLIN_ERR_BAD_ARGUMENT;
     Args a{};
     a.x = static_cast<const uint8_t *>(logits);
     a.out = static_cast<uint8_t *>(dlogits);

@@ -18,6 +18,7 @@
 #include <algorithm>
 
 #include "qlin_device.h"
+#include "qlin_overlap.h"
 #include "qlin_sort.h"
 #include "qlinear.h"
 
@@ -1231,6 +1232,8 @@ bool good_shape(int64_t T, int64_t K, int64_t N, int64_t R, int64_t L)
            R % 8 == 0 && L > 0 && L <= kMaxAdapters && L * std::max<int64_t>(R, 64) * std::max(K, N) < (int64_t)1 << 33;
 }
 
+Region rows_of(const uint16_t *p, int64_t rows, int64_t width, int64_t ld) { return Region{p, rows, 2 * width, 2 * ld}; }
+
 template <bool BACK>
 hipError_t launch_shrink(const Sizes &z, const ShrinkArgs &a, hipStream_t s)
 {
@@ -1391,8 +1394,6 @@ qlin_status qlin_lora_mm(int32_t id_bits, int64_t tokens, int64_t K, int64_t N, 
         return QLIN_OK;
     if (!X || !A || !B || !ids || !Y)
         return QLIN_ERR_NULL_POINTER;
-    if (Y == X)                                // (other workgroups still read it)
-        return QLIN_ERR_BAD_ARGUMENT;
     if (ldx < K || ldx > kMaxStride || ldy < N || ldy > kMaxStride || (base && (ldb < N || ldb > kMaxStride)))
         return QLIN_ERR_BAD_STRIDE;
     if (!aligned(X, 2) || !aligned(A, 2) || !aligned(B, 2) || !aligned(base, 2) || !aligned(Y, 2) ||
@@ -1402,6 +1403,11 @@ qlin_status qlin_lora_mm(int32_t id_bits, int64_t tokens, int64_t K, int64_t N, 
     const Space f = space(z, workspace, false);
     if (!workspace || workspace_bytes < f.bytes)
         return QLIN_ERR_WORKSPACE;
+    const Region x = rows_of(X, tokens, K, ldx), y = rows_of(Y, tokens, N, ldy), add = rows_of(base, tokens, N, ldb),
+                 fa = flat(A, 2 * adapters * rank * K), fb = flat(B, 2 * adapters * N * rank),
+                 id = flat(ids, tokens * (id_bits / 8)), sc = flat(scale, 4 * adapters);
+    if (overlaps({y, flat(workspace, f.bytes)}, {x, fa, fb, id, sc, same(y, add) ? Region{} : add}))
+        return QLIN_ERR_BAD_ARGUMENT;
     hipStream_t s = static_cast<hipStream_t>(stream);
     ShrinkArgs a{};
     a.job[0] = ShrinkJob{X, A, f.rows, nullptr, ldx, (int)K};
@@ -1438,8 +1444,6 @@ qlin_status qlin_lora_mm_backward(int32_t id_bits, int64_t tokens, int64_t K, in
         return QLIN_ERR_BAD_SHAPE;
     if (!A || !B || !dA || !dB || (tokens > 0 && (!dY || !X || !ids || !dX)))
         return QLIN_ERR_NULL_POINTER;
-    if (tokens > 0 && (dX == X || dX == dY))
-        return QLIN_ERR_BAD_ARGUMENT;
     if (tokens > 0 && (ldx < K || ldx > kMaxStride || lddy < N || lddy > kMaxStride || lddx < K || lddx > kMaxStride ||
                        (base && (ldb < K || ldb > kMaxStride))))
         return QLIN_ERR_BAD_STRIDE;
@@ -1450,6 +1454,13 @@ qlin_status qlin_lora_mm_backward(int32_t id_bits, int64_t tokens, int64_t K, in
     const Space f = space(z, workspace, true);
     if (!workspace || workspace_bytes < f.bytes)
         return QLIN_ERR_WORKSPACE;
+    const Region x = rows_of(X, tokens, K, ldx), dy = rows_of(dY, tokens, N, lddy), dx = rows_of(dX, tokens, K, lddx),
+                 add = rows_of(base, tokens, K, ldb), fa = flat(A, 2 * adapters * rank * K),
+                 fb = flat(B, 2 * adapters * N * rank), id = flat(ids, tokens * (id_bits / 8)), sc = flat(scale, 4 * adapters);
+    const bool in_place = tokens > 0 && same(dx, add);
+    if (overlaps({dx, flat(dA, 4 * adapters * rank * K), flat(dB, 4 * adapters * N * rank), flat(workspace, f.bytes)},
+                 {x, dy, fa, fb, id, sc, in_place ? Region{} : add}))
+        return QLIN_ERR_BAD_ARGUMENT;
     hipStream_t s = static_cast<hipStream_t>(stream);
     ShrinkArgs a{};
     a.job[0] = ShrinkJob{X, A, nullptr, f.fv, ldx, (int)K};

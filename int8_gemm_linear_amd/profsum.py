@@ -41,7 +41,8 @@ COPY_TAG = "bitwise_not"        # its kernel is torch's elementwise bitwise_not
 
 # sources that no counted workload runs: the 4-bit products, the token routing, the adapters, the log
 # probabilities, the embedding, and the headers that only these include
-OTHER_SOURCES = ("qlin_w4", "qlin_moe", "qlin_lora", "qlin_logprob", "qlin_embed", "qlin_sort", "qlin_elem")
+OTHER_SOURCES = ("qlin_w4", "qlin_moe", "qlin_lora", "qlin_logprob", "qlin_embed", "qlin_sort", "qlin_elem",
+                 "qlin_overlap")
 
 
 def fingerprint(table_path: str | None = None) -> str:
