@@ -442,8 +442,10 @@ qlin_status qlin_moe_permute_backward(qlin_row_type rt, int64_t tokens, int64_t 
  *   lora_mm_backward  u[t] = dY[t] B_i;  dX[t] = bf16( base[t] + s_i u[t] A_i ),
  *                     dA_i = s_i sum_t u[t]^T X[t],
  *                     dB_i = s_i sum_t dY[t]^T (X[t] A_i^T),  t over i's tokens
- * `base` is the shared projection's output (of backward: the gradient that
- * reached X through it); NULL counts as zeros.  A token without an adapter gets
+ * `base` is the shared projection's output; of backward the gradient that
+ * reached X through it, dY times its weights, which no call here computes for a
+ * quantized product: without it dX is the adapters' share alone.  NULL counts as
+ * zeros.  A token without an adapter gets
  * base[t] (zeros without base), an adapter without tokens dA = dB = 0.  Requests
  * of several ranks share a call with their adapters' missing ranks as zeros.
  *

@@ -975,7 +975,8 @@ def lora_mm(x, a, b, ids, scale=None, base=None, out=None):
 def lora_mm_backward(dy, x, a, b, ids, scale=None, base=None, out=None):
     """Gradients of lora_mm: (dx bf16 [T,K], da float32 [adapters, rank, K], db float32
     [adapters, N, rank]) from dy bf16 [T,N] and the call's inputs.  `base` bf16 [T,K]
-    is the gradient that reached x through the shared projection (None: zeros); dx is
+    is the gradient that reached x through the shared projection, dy times its weights, which
+    the caller computes (None: zeros, and dx is the adapters' share alone); dx is
     added to it, and may be written to it (out=base).  Adapters without tokens get
     zeros."""
     dims, ldx, sc = _adapters(x, a, b, ids, scale)
