@@ -6,9 +6,9 @@
 // The gradient sorts the positions by token (a stable radix sort, so equal tokens
 // stay in order) and sums each token's run in that order: no atomics on values, and
 // results do not depend on timing.  A run that crosses the border between two
-// workgroups' shares of the sorted positions leaves a partial sum in each, which a
-// second kernel adds in order.  All of it moves bytes once; HBM bounds the long calls
-// and the launch the short ones.
+// workgroups' shares of the sorted positions leaves a partial sum in each; a second
+// kernel adds them in four shares, each in order, and the shares in order.  All of it
+// moves bytes once; HBM bounds the long calls and the launch the short ones.
 #include <algorithm>
 
 #include "qlin_dpp.h"
