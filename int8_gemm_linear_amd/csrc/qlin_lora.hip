@@ -14,7 +14,7 @@
 // are all of their 24 bits: the upper 16 bits (cut, so that nothing overflows), of the
 // rest the upper 16 bits, and what is left.
 // Two pieces, 16 bits, would do for y and dx but where base and product cancel, and cost
-// less: 8192 tokens of 8 adapters of 64 ranks, K = N = 5120, 113 us for 117.
+// less: 8192 tokens of 8 adapters of 64 ranks, K = N = 5120, 113 us for 116.
 #include <algorithm>
 
 #include "qlin_device.h"
@@ -74,24 +74,29 @@ __device__ inline void store8(uint16_t *p, v4i v, int n)
             p[i] = t[i];
 }
 
-// The upper 16 bits of v as a float, and what is left of it.  Where nothing is left, 2^-40 of the number that is taken
-// apart stands for it: with zero, an infinity among the weights would come out as NaN (as it does with a number below
-// 2^-86, whose 2^-40 are no bf16 number any more).  All pieces of a number have its sign.
-__device__ inline float cut(float v) { return __uint_as_float(__float_as_uint(v) & 0xFFFF0000u); }
-__device__ inline float rest(float v, float c, float whole)
-{
-    return fabsf(c) < INFINITY && v != c ? v - c : whole * 0x1p-40f;
-}
-
 constexpr int kPieces = 3;
 
-// The pieces of v, each a bf16 number.
+// The pieces of v as the upper halves of floats (the last one has eight bits left, too).  Where nothing is left of v, and
+// for an infinity, 2^-40 of v stands for the rest: with zero, an infinity among the weights would come out as NaN (as it
+// does with a v below 2^-86, whose 2^-40 are no bf16 number any more).  All pieces have v's sign.
 __device__ inline void pieces_of(float (&p)[kPieces], float v)
 {
-    p[0] = cut(v);
-    const float r = rest(v, p[0], v);
-    p[1] = cut(r);
-    p[2] = rest(r, p[1], v);
+    const float least = v * 0x1p-40f;
+    float r = v;
+#pragma unroll
+    for (int h = 0; h < kPieces - 1; ++h) {
+        p[h] = __uint_as_float(__float_as_uint(r) & 0xFFFF0000u);
+        r -= p[h];
+        r = __builtin_amdgcn_classf(r, 0x63) ? least : r;    // NaN or zero
+    }
+    p[kPieces - 1] = r;
+}
+
+__device__ inline uint16_t upper_half(float v) { return (uint16_t)(__float_as_uint(v) >> 16); }
+
+__device__ inline int upper_halves(float lo, float hi)
+{
+    return (int)__builtin_amdgcn_perm(__float_as_uint(hi), __float_as_uint(lo), 0x07060302u);
 }
 
 __device__ inline int pack2(float lo, float hi)
@@ -318,8 +323,8 @@ constexpr int kStep = 64;
 
 struct ShrinkJob {
     const uint16_t *x, *w;
-    uint16_t *rows;            // [tokens][3][Rp]: the pieces, for expand, or NULL
-    uint16_t *pieces;          // [place / 8][3][Rp][8]: the pieces, for outer, or NULL
+    float *sums;               // [splits][tokens][Rp]: sums of parts of K, without s, for expand (or NULL)
+    uint16_t *pieces;          // [place / 8][3][Rp][8]: the pieces, for outer (or NULL)
     int64_t ldx;
     int K;
 };
@@ -328,8 +333,7 @@ struct ShrinkArgs {
     ShrinkJob job[2];          // v; u
     Plan plan;
     const float *scale;
-    float *part;               // [splits][tokens][Rp]: sums of parts of K, for the expand kernel to add (or NULL)
-    int splits;
+    int splits;                // parts of K (backward: 1)
     int R, Rp, groups, self;   // groups of 16 RB ranks; self: waves (1) or workgroups (2) make the plan
 };
 
@@ -567,26 +571,20 @@ __global__ void __launch_bounds__(64 * kShrinkWaves) k_shrink(ShrinkArgs a)
         for (int w = 1; w < waves; ++w) v += sums[w * TB * RB * 64 + e];
         const int block = e >> 6, rank = r0 + 16 * (block % RB) + (e & 15), at = 16 * (block / RB) + 4 * ((e >> 4) & 3);
         const int n = tile.z - at;             // of the four places from there
-        if (!BACK && a.part) {
+        if (!BACK || job.sums)
 #pragma unroll
             for (int c = 0; c < 4; ++c)
                 if (c < n)
-                    a.part[((int64_t)split * a.plan.tokens + tile.y + at + c) * a.Rp + rank] = v[c];
-            continue;
-        }
-        uint16_t o[kPieces][4];
+                    job.sums[((int64_t)split * a.plan.tokens + tile.y + at + c) * a.Rp + rank] = v[c];
+        if (BACK && (at & ~7) < tile.z) {      // (zeros fill the last eight)
+            uint16_t o[kPieces][4];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            float f[kPieces];
-            pieces_of(f, c < n ? v[c] * s : 0.0f);
+            for (int c = 0; c < 4; ++c) {
+                float f[kPieces];
+                pieces_of(f, c < n ? v[c] * s : 0.0f);
 #pragma unroll
-            for (int h = 0; h < kPieces; ++h) {
-                o[h][c] = bf16_bits(f[h]);
-                if (job.rows && c < n)
-                    job.rows[((int64_t)(tile.y + at + c) * kPieces + h) * a.Rp + rank] = o[h][c];
+                for (int h = 0; h < kPieces; ++h) o[h][c] = upper_half(f[h]);
             }
-        }
-        if (BACK && job.pieces && (at & ~7) < tile.z) {     // (zeros fill the last eight)
             const int64_t eight = piece_place(tile.y, tile.x) / 8 + at / 8;
 #pragma unroll
             for (int h = 0; h < kPieces; ++h)
@@ -605,8 +603,8 @@ constexpr int kThreads = 256, kWaves = kThreads / 64;
 constexpr int kWide = 16 * kWaves;             // tokens of a workgroup of the second kernel
 
 struct ExpandArgs {
-    const uint16_t *rows;      // [tokens][3][Rp]: s v
-    const float *part, *scale; // instead of rows: [splits][tokens][Rp], the parts of v, and s (or NULL)
+    const float *sums;         // [splits][tokens][Rp]: the parts of v
+    const float *scale;        // s, or NULL
     int tokens, splits;
     const int32_t *order;
     const int4 *tiles;
@@ -615,24 +613,6 @@ struct ExpandArgs {
     int64_t ldb, ldo;
     int N, R, Rp, chunks;
 };
-
-// The pieces of s v as operands: chunk 4 g + q of 8 ranks.
-template <int G>
-__device__ inline void load_factors(v4i (&f)[kPieces][G], const ExpandArgs &a, int place)
-{
-    const int q = (threadIdx.x & 63) >> 4, ranks = a.R / 8;
-    const uint16_t *v = a.rows + (int64_t)place * kPieces * a.Rp;
-#pragma unroll
-    for (int g = 0; g < G; ++g) {
-        const int c = 4 * g + q;
-#pragma unroll
-        for (int h = 0; h < kPieces; ++h) {
-            f[h][g] = v4i{0, 0, 0, 0};
-            if (c < ranks)
-                f[h][g] = load8(v + h * a.Rp + 8 * c);
-        }
-    }
-}
 
 // The pieces of s times eight sums.
 template <int G>
@@ -644,13 +624,14 @@ __device__ inline void cut_factors(v4i (&f)[kPieces][G], int g, const v4f (&sum)
         pieces_of(p0, sum[e / 2][2 * e % 4] * s);
         pieces_of(p1, sum[e / 2][2 * e % 4 + 1] * s);
 #pragma unroll
-        for (int h = 0; h < kPieces; ++h) f[h][g][e] = pack2(p0[h], p1[h]);
+        for (int h = 0; h < kPieces; ++h) f[h][g][e] = upper_halves(p0[h], p1[h]);
     }
 }
 
-// The same from the parts, four of them on their way at a time.
+// The pieces of s v as operands, chunk 4 g + q of 8 ranks, from the parts of v, four of them on their way at a time.  (Cut
+// here and not by shrink: two bytes fewer a rank and token to write and to read.)
 template <int G>
-__device__ inline void add_factors(v4i (&f)[kPieces][G], const ExpandArgs &a, int place, float s)
+__device__ inline void load_factors(v4i (&f)[kPieces][G], const ExpandArgs &a, int place, float s)
 {
     const int q = (threadIdx.x & 63) >> 4, ranks = a.R / 8;
     const int64_t apart = (int64_t)a.tokens * a.Rp;
@@ -661,7 +642,7 @@ __device__ inline void add_factors(v4i (&f)[kPieces][G], const ExpandArgs &a, in
         for (int h = 0; h < kPieces; ++h) f[h][g] = v4i{0, 0, 0, 0};
         if (c >= ranks)
             continue;
-        const float *p = a.part + (int64_t)place * a.Rp + 8 * c;
+        const float *p = a.sums + (int64_t)place * a.Rp + 8 * c;
         v4f sum[2] = {};
         for (int k = 0; k < a.splits; k += 4) {
             v4f v[4][2] = {};
@@ -791,12 +772,8 @@ __global__ void __launch_bounds__(kThreads) k_expand_few(ExpandArgs a)
     const int64_t token = i < tile.w ? a.order[place] : -1;
     v4i v[kPieces][G];
     const uint16_t *w = live ? a.w + (int64_t)tile.x * a.N * a.R : nullptr;
-    if (live) {
-        if (!TR && a.part)
-            add_factors(v, a, place, a.scale ? a.scale[tile.x] : 1.0f);
-        else
-            load_factors(v, a, place);
-    }
+    if (live)
+        load_factors(v, a, place, a.scale ? a.scale[tile.x] : 1.0f);
     const int blocks = (a.N + 63) / 64;
     for (int b = chunk * kWaves + wave; b < blocks; b += a.chunks * kWaves) {
         Few<G, TR> n;
@@ -889,10 +866,7 @@ __global__ void __launch_bounds__(kThreads) k_expand_many(ExpandArgs a)
     const uint16_t *w = a.w + (int64_t)(live ? tile.x : 0) * a.N * a.R;
     if (live) {
         const int place = tile.y + min(16 * wave + i, tile.w - 1);
-        if (!TR && a.part)
-            add_factors(v, a, place, a.scale ? a.scale[tile.x] : 1.0f);
-        else
-            load_factors(v, a, place);
+        load_factors(v, a, place, a.scale ? a.scale[tile.x] : 1.0f);
     }
     const int blocks = (a.N + 127) / 128;
     for (int b = chunk; b < blocks; b += a.chunks) {
@@ -1187,8 +1161,7 @@ struct Layout {
 struct Space {
     int32_t *order, *offsets, *counts;
     int4 *tiles, *wides;
-    uint16_t *rows;            // of s v (backward: s u) for expand
-    float *part;               // or the parts of v
+    float *sums;               // the parts of v (backward: u) for expand
     uint16_t *fv, *fu;         // backward: the pieces of s v and s u for outer
     float *outer_a, *outer_b;  // and the parts of dA and dB
     size_t bytes;
@@ -1209,10 +1182,7 @@ Space space(const Sizes &z, void *ws, bool back)
     f.tiles = l.take<int4>(z.max_tiles);
     f.wides = z.max_wides ? l.take<int4>(z.max_wides) : nullptr;
     f.counts = l.take<int32_t>(z.T > kSelfTokens ? (int64_t)sort_parts(z.T) * plan_digits(z.L) : 0);
-    if (back || z.splits == 1)
-        f.rows = l.take<uint16_t>(z.T * kPieces * z.Rp);
-    else
-        f.part = l.take<float>(z.splits * z.T * z.Rp);
+    f.sums = l.take<float>((back ? 1 : z.splits) * z.T * z.Rp);
     if (back) {
         f.offsets = l.take<int32_t>(z.L + 1);
         const int64_t places = piece_place(z.T, (int)z.L);
@@ -1291,7 +1261,7 @@ hipError_t launch_expand(const Sizes &z, const Space &f, const float *scale, con
     const int64_t tiles = z.max_wides ? z.max_wides : z.max_tiles, least = z.wide > 1 ? (full + 2) / 3 : 1;
     const int64_t want = std::max(least, std::min<int64_t>(full, (z.wide > 1 ? 2048 : 8192) / tiles));
     const int chunks = (int)std::max<int64_t>(1, std::min<int64_t>(want, (((int64_t)1 << 24) - 1) / tiles));
-    const ExpandArgs a{f.rows, f.part, scale, (int)z.T, z.splits, f.order, f.wides ? f.wides : f.tiles, w, base, out, ldb, ldo, (int)N, (int)z.R, (int)z.Rp, chunks};
+    const ExpandArgs a{f.sums, scale, (int)z.T, TR ? 1 : z.splits, f.order, f.wides ? f.wides : f.tiles, w, base, out, ldb, ldo, (int)N, (int)z.R, (int)z.Rp, chunks};
     const dim3 grid((unsigned)(tiles * chunks));
     if (z.R <= 32)
         expand_kernel<1, TR>(z, a, grid, s);
@@ -1319,7 +1289,7 @@ hipError_t launch_both(const Sizes &z, const Space &f, const void *ids, int32_t 
     if (p != hipSuccess)
         return p;
     const int chunks = (int)both_chunks(z.N);
-    const ExpandArgs e{nullptr, nullptr, scale, (int)z.T, 1, nullptr, nullptr, w, base, out, ldb, ldo, (int)z.N, (int)z.R, (int)z.Rp, chunks};
+    const ExpandArgs e{nullptr, scale, (int)z.T, 1, nullptr, nullptr, w, base, out, ldb, ldo, (int)z.N, (int)z.R, (int)z.Rp, chunks};
     const dim3 grid((unsigned)(z.max_tiles * chunks)), block(64 * kShrinkWaves);
     const size_t lds = kShrinkWaves * shrink_share(1, (int)z.Rp / 16) * sizeof(v4i);
     if (z.Rp == 16)
@@ -1410,8 +1380,7 @@ qlin_status qlin_lora_mm(int32_t id_bits, int64_t tokens, int64_t K, int64_t N, 
         return QLIN_ERR_BAD_ARGUMENT;
     hipStream_t s = static_cast<hipStream_t>(stream);
     ShrinkArgs a{};
-    a.job[0] = ShrinkJob{X, A, f.rows, nullptr, ldx, (int)K};
-    a.part = f.part;
+    a.job[0] = ShrinkJob{X, A, f.sums, nullptr, ldx, (int)K};
     a.splits = z.splits;
     a.scale = scale;
     a.R = (int)rank;
@@ -1464,7 +1433,7 @@ qlin_status qlin_lora_mm_backward(int32_t id_bits, int64_t tokens, int64_t K, in
     hipStream_t s = static_cast<hipStream_t>(stream);
     ShrinkArgs a{};
     a.job[0] = ShrinkJob{X, A, nullptr, f.fv, ldx, (int)K};
-    a.job[1] = ShrinkJob{dY, B, f.rows, f.fu, lddy, (int)N};
+    a.job[1] = ShrinkJob{dY, B, f.sums, f.fu, lddy, (int)N};
     a.splits = 1;
     a.scale = scale;
     a.R = (int)rank;
@@ -1473,7 +1442,7 @@ qlin_status qlin_lora_mm_backward(int32_t id_bits, int64_t tokens, int64_t K, in
     if (make_plan(z, f, ids, id_bits, a, s) != hipSuccess)
         return QLIN_ERR_HIP;
     if (tokens > 0 && (launch_shrink<true>(z, a, s) != hipSuccess ||
-                       launch_expand<true>(z, f, nullptr, A, K, base, ldb, dX, lddx, s) != hipSuccess))
+                       launch_expand<true>(z, f, scale, A, K, base, ldb, dX, lddx, s) != hipSuccess))
         return QLIN_ERR_HIP;
     if (launch_outer(z, f, X, ldx, dY, lddy, dA, dB, s) != hipSuccess)
         return QLIN_ERR_HIP;
