@@ -1105,10 +1105,11 @@ struct Sizes {
 // 15.8 us, four 13.6, eight 14.5; 164 workgroups (24 adapters of 64 ranks, N = 51200): one 49.4, three 52.9.
 constexpr int64_t kMaxSplits = 4;
 
-// Tokens an adapter has on average from which 64 share a load of the expand kernel's weights, not 16 (K = N = 5120, 16
-// ranks, both kernels): 32 adapters of 16 tokens 17.4 us with 64 at a time, 15.9 with 16; of 32 tokens 21.3 and 22.9; 16
-// adapters of 64 tokens 20.4 and 22.0.  Up to kWaveTokens tokens never (64 of an adapter 12.8 and 12.4).
-constexpr int64_t kManyTokens = 32;
+// Tokens an adapter has on average from which 64 share a load of the expand kernel's weights, not 16 (both kernels): 32
+// adapters of 16 ranks, K = N = 5120, of 32 tokens 22.8 us with 64 at a time, 22.4 with 16; 16 adapters of 64 tokens 19.8 and
+// 21.8; 32 adapters of 48 tokens, K = N = 2048, 16 ranks 17.8 and 17.5, 64 ranks 23.6 and 25.0.  Up to kWaveTokens tokens never
+// (64 of an adapter 12.8 and 12.2).
+constexpr int64_t kManyTokens = 40;
 
 Sizes sizes(int64_t T, int64_t K, int64_t N, int64_t R, int64_t L)
 {
