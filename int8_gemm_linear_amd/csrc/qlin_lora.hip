@@ -315,9 +315,10 @@ __device__ inline int4 self_plan(const Plan &p, int want, int32_t *hist, int32_t
 // transposing loads give a lane eight k of its rank.
 //
 // The lines of 128 bytes that a CU asks of the L2 bound it, about 160 a microsecond, the weights' of every tile
-// among them: 4001 tokens of 6 adapters of 32 ranks, K = 5120, 1.0 million lines, 21 us; u and v of 8192 tokens
-// of 5120 and 10240, 16 ranks, 3.0 million, 79 us.  Tiles of 64 tokens with K in parts, a launch that adds them,
-// need a tenth fewer lines and took 67 us for the latter, but 25 us more for the plan and the parts.
+// among them: u and v of 8192 tokens of 5120 and 10240, 16 ranks, 3.0 million, 79 us (140 a CU and microsecond); 4001
+// tokens of 6 adapters of 32 ranks, K = 5120, 1.0 million lines, 21 us (122: a workgroup a CU, and nothing covers its
+// plan, 4 us, and its sums).  Tiles of 64 tokens with K in parts, a launch that adds them, need a tenth fewer lines
+// and took 67 us for the former, but 25 us more for the plan and the parts.
 // ---------------------------------------------------------------------------
 constexpr int kStep = 64;
 
@@ -337,7 +338,7 @@ struct ShrinkArgs {
     int R, Rp, groups, self;   // groups of 16 RB ranks; self: waves (1) or workgroups (2) make the plan
 };
 
-// Waves of a workgroup (16 took as long, four 43 us for 39: the gradients of 2048 tokens of an adapter of 16 ranks,
+// Waves of a workgroup (16 took as long, four 39 us for 35: the gradients of 2048 tokens of an adapter of 16 ranks,
 // K = N = 2048), and steps whose loads a wave has in flight.
 constexpr int kShrinkWaves = 8;
 template <int TB, int RB> constexpr int steps_at_once() { return TB * RB == 1 ? 5 : TB + RB <= 3 ? 3 : TB + RB <= 5 ? 2 : 1; }
@@ -758,7 +759,8 @@ struct Few {
     }
 };
 
-// Weights' bytes bound it: 128 tokens of 24 adapters of 64 ranks on N = 51200, 183 MB, 37 us, 5.0 TB/s.
+// Weights' bytes bound it: 128 tokens of 24 adapters of 64 ranks on N = 51200, 183 MB, 41 us, 4.5 TB/s (with two pieces of
+// v, cut by shrink, 37 us; two or four blocks a workgroup, and weights loaded ahead of v, took as long or longer).
 template <int G, bool TR>
 __global__ void __launch_bounds__(kThreads) k_expand_few(ExpandArgs a)
 {
@@ -786,7 +788,7 @@ __global__ void __launch_bounds__(kThreads) k_expand_few(ExpandArgs a)
 
 // Few tokens of adapters that are small: both products in one launch, every workgroup with its own sums of all of K for
 // the tile whose 512 n it has.  A launch less is worth more than the reads of A by every workgroup while these are one a
-// CU at most: a token, 16 ranks, K = N = 2048 5.7 us, in two launches 7.4, and 3 us less of the calling thread's time.
+// CU at most: a token, 16 ranks, K = N = 2048 5.5 us, in two launches 7.3, and 3 us less of the calling thread's time.
 template <int RB>
 __global__ void __launch_bounds__(64 * kShrinkWaves) k_both(ShrinkArgs s, ExpandArgs a)
 {
@@ -843,8 +845,9 @@ __global__ void __launch_bounds__(64 * kShrinkWaves) k_both(ShrinkArgs s, Expand
 
 // 128 n a workgroup at a time, 16 tokens a wave: eight products of 16 tokens by 16 n, the m-th with the n = 8 i + m,
 // so that a lane ends with eight n in a row of four tokens, and sixteen lanes with 256 bytes of one (64 bytes of
-// each token, as above, took 32 us where this took 25: 4001 tokens on N = 5120, 32 ranks; 22 with the plan's list of
-// tiles, base and out at 3.8 TB/s).
+// each token, as above, took 32 us where this took 25: 4001 tokens on N = 5120, 32 ranks; 23 with the plan's list of
+// tiles and three pieces of v, base and out at 3.6 TB/s: a workgroup's loads of order, v, weights and base wait for
+// each other).
 template <int G, bool TR>
 __global__ void __launch_bounds__(kThreads) k_expand_many(ExpandArgs a)
 {
@@ -973,8 +976,8 @@ __global__ void __launch_bounds__(64 * kOuterWaves, 2) k_outer(OuterArgs a)
     const int c0 = b % job.blocks * 128, l = b / job.blocks;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = lane & 15, q = lane >> 4;
     const int beg = a.offsets[l], end = a.offsets[l + 1], r0 = group * 16 * RB;
-    // few places: one wave, and no sums of others (1024 tokens of 64 adapters of 16 ranks, K = N = 4096, all kernels: 41 us,
-    // four waves 49; with 96 places too 4096 tokens of 51 adapters 92, four waves 87)
+    // few places: one wave, and no sums of others (1024 tokens of 64 adapters of 16 ranks, K = N = 4096, all kernels: 43 us,
+    // four waves 50; with 96 places too 4096 tokens of 51 adapters 89, four waves 88)
     const bool alone = end - beg <= kOuterAlone;
     const int waves = alone ? 1 : kOuterWaves;
     if (alone && wave > 0)
@@ -1065,7 +1068,7 @@ __global__ void __launch_bounds__(64 * kOuterWaves, 2) k_outer(OuterArgs a)
 }
 
 // out = the splits' parts, added in order, four elements a thread (whole numbers of four: ranks are).  Both gradients in one
-// launch: 2048 tokens of an adapter, 16 ranks, K = N = 2048, all kernels 37.8 us in two, 34.7 in one.
+// launch: 2048 tokens of an adapter, 16 ranks, K = N = 2048, all kernels 35 us, in two launches 38.
 struct AddArgs {
     float *out[2];
     const float *part[2];
@@ -1102,7 +1105,7 @@ struct Sizes {
 };
 
 // Parts of K that the expand kernel adds: 32 tokens of 28 adapters, K = 5120, N = 10240, both kernels: one part
-// 15.8 us, four 13.6, eight 14.5; 164 workgroups (24 adapters of 64 ranks, N = 51200): one 49.4, three 52.9.
+// 16.3 us, four 13.4, eight 14.6; 164 workgroups (24 adapters of 64 ranks, N = 51200): one 52.9, three 54.6.
 constexpr int64_t kMaxSplits = 4;
 
 // Tokens an adapter has on average from which 64 share a load of the expand kernel's weights, not 16 (both kernels): 32
@@ -1117,20 +1120,20 @@ Sizes sizes(int64_t T, int64_t K, int64_t N, int64_t R, int64_t L)
     while (z.Rp < R) z.Rp *= 2;
     const int64_t mean = T / std::min(L, std::max<int64_t>(T, 1));
     z.wide = mean >= kManyTokens && T > kWaveTokens ? kWide / 16 : 1;
-    // shrink: more tokens a workgroup only where there are workgroups for all CUs (8192 tokens of 8 adapters of 64
-    // ranks, K = N = 5120, both kernels: 16 at a time 136 us, 32 115; 65536 tokens of 8 adapters of 16 ranks, K = N =
-    // 2048: 16 at a time 270 us, 32 248, 64 235)
+    // shrink: more tokens a workgroup only where there are workgroups for all CUs (both kernels: 8192 tokens of 8
+    // adapters of 64 ranks, K = N = 5120, 16 at a time 131 us, 32 116; 131072 of 2 adapters of 16 ranks, K = N = 1024,
+    // 16 at a time 274, 32 218, 64 199; 65536 of 64 adapters, K = N = 2048, 189, 187 and 195)
     while (z.tb < z.wide && T >= 16 * 2 * z.tb * 240) z.tb *= 2;
     z.max_tiles = (int)std::max<int64_t>(1, T / (16 * z.tb) + std::min(L + 1, T));
     if (z.wide > z.tb)
         z.max_wides = (int)(T / (16 * z.wide) + std::min(L + 1, T));
     // and 32 ranks a workgroup likewise (64 ranks, K = N = 5120, both kernels: 8192 tokens of 8 adapters, 528 workgroups
-    // then, 113 us, 16 at a time 136; 1024 of 32, 194, 34 and 38; 256 of 64, 162, 28 and 26)
+    // then, 116 us, 16 at a time 138; 1024 of 32, 194, 36 and 40; 256 of 64, 162, 29 and 27)
     if (z.Rp > 16 && z.max_tiles * (z.Rp / 16) > 360)
         z.rb = 2;
     z.groups = (int)((R + 16 * z.rb - 1) / (16 * z.rb));
     // few workgroups: parts of K, a step for each wave at least (a CU alone loads some 50 GB/s: 256 tokens of an
-    // adapter of 16 ranks, K = N = 5120, both kernels: one part 15.1 us, four 12.7)
+    // adapter of 16 ranks, K = N = 5120, both kernels: one part 15.2 us, four 12.1)
     if (z.max_tiles * z.groups <= 128)
         z.splits = (int)std::min<int64_t>((K + 8 * kStep - 1) / (8 * kStep), kMaxSplits);
     return z;
@@ -1139,8 +1142,8 @@ Sizes sizes(int64_t T, int64_t K, int64_t N, int64_t R, int64_t L)
 int outer_blocks(const Sizes &z) { return z.Rp > 32 ? 4 : z.Rp > 16 ? 2 : 1; }
 
 // Splits of the places: both gradients' workgroups fill the CUs once, four to a CU with 16 ranks a workgroup and two with
-// more (8192 tokens of an adapter of 16 ranks, K = N = 5120: once 148 us, half of that 164; two of 64 ranks: once 231,
-// twice 246).
+// more (8192 tokens of an adapter of 16 ranks, K = N = 5120: once 144 us, half of that 161; two of 64 ranks: once 232,
+// twice 247).
 int outer_splits(const Sizes &z, int64_t C)
 {
     const int64_t wgs = z.L * ((C + 127) / 128) * ((z.R + 63) / 64), room = outer_blocks(z) == 1 ? 512 : 256;
@@ -1256,7 +1259,7 @@ hipError_t launch_expand(const Sizes &z, const Space &f, const float *scale, con
                          uint16_t *out, int64_t ldo, hipStream_t s)
 {
     // Workgroups of a tile.  Many tokens: three blocks of 128 n each at most (65536 tokens, K = N = 2048, 16 ranks, both
-    // kernels: one block 186 us, three 187, four 203, eight 219; 8192 tokens, 5120 and 5120, 64 ranks: one 122, three 113),
+    // kernels: one block 193 us, three 187, four 202, eight 221; 8192 tokens, 5120 and 5120, 64 ranks: one 118, three 116),
     // fewer where the tiles alone are too few
     const int64_t full = z.wide > 1 ? (N + 127) / 128 : (N + 64 * kWaves - 1) / (64 * kWaves);
     const int64_t tiles = z.max_wides ? z.max_wides : z.max_tiles, least = z.wide > 1 ? (full + 2) / 3 : 1;
@@ -1276,8 +1279,8 @@ hipError_t launch_expand(const Sizes &z, const Space &f, const float *scale, con
 // Workgroups of the kernel that has both products: 512 n of a tile each.
 int64_t both_chunks(int64_t N) { return (N + 64 * kShrinkWaves - 1) / (64 * kShrinkWaves); }
 
-// Whether it is taken (16 ranks, both kernels): K = 2048, 16 tokens of 12 adapters on N = 10240, some 240 workgroups, 8.7
-// us, in two launches 9.6; 32 of 28, 560 workgroups, 20.9 and 12.2; a token, K = N = 4096 7.6 and 7.6, 5120 8.8 and 8.0.
+// Whether it is taken (16 ranks, both kernels): K = 2048, 16 tokens of 12 adapters on N = 10240, some 240 workgroups, 8.5
+// us, in two launches 9.6; 32 of 28, 560 workgroups, 19.8 and 12.2; a token, K = N = 4096 7.5 and 7.5, 5120 8.5 and 7.9.
 bool one_launch(const Sizes &z)
 {
     return z.T <= kWaveTokens && z.wide == 1 && z.Rp <= 32 && z.Rp * z.K <= 65536 && z.max_tiles * both_chunks(z.N) <= 320;   // (with tiles that stay empty)
